@@ -164,6 +164,35 @@ int mla_decode_paged_fp8(const mla_dims_t* dims, const mla_opts_t* opts, const v
                          const float* q_scale, void* out, float* lse_out, void* workspace,
                          size_t workspace_bytes, void* stream);
 
+/* How a latent cache stores its rows [c_kv (L) ; k_rope (R)].  The rope part is bf16
+ * and comes last in every format.
+ *   BF16   L bf16 values
+ *   E4M3   L e4m3 codes; c_kv = code * kv_scales[row]      (mla_decode_paged_fp8)
+ *   E2M1   L/2 bytes of e2m1 codes, two a byte, the lower nibble first; L/32 bytes
+ *          of e8m0 scales, 2^(byte - 127), one per 32 values, 255 = NaN (the element
+ *          and scale types of the OCP Microscaling formats); zeros up to a multiple
+ *          of 16 bytes; c_kv = code * scale               (mla_decode_paged_fp4)
+ * Bytes a row at (L, R) = (512, 64): 1152, 640 (and a 4-byte scale), 400. */
+typedef enum {
+  MLA_CACHE_BF16 = 0,
+  MLA_CACHE_E4M3 = 1,
+  MLA_CACHE_E2M1 = 2
+} mla_cache_format_t;
+
+/* 4-bit latent cache: mla_decode_paged over rows in MLA_CACHE_E2M1 format.
+ *   kv_pool_fp4   bytes [num_pages, ps, row], row = 400 at (L, R) = (512, 64)
+ * Other arguments, shapes, masks, workspace and errors as mla_decode_paged (bf16
+ * weights).  The attention's products take f16 operands: the cached codes times scales
+ * from 2^-23 to 2^13 exactly, the absorbed query and the rope parts rounded to f16 (their
+ * magnitudes stay below 65520; below 2^-14 they keep a 2^-25 absolute precision).  A
+ * finite magnitude above f16's range becomes an infinity, which makes the queries that
+ * use it NaN, and is recorded: MLA_ERR_DEVICE_CHECK in debug mode.  Query tokens are walked one at a time (MLA_FLAG_FOLD_PAIRS does not apply). */
+int mla_decode_paged_fp4(const mla_dims_t* dims, const mla_opts_t* opts, const void* q,
+                         const uint32_t* input_row_offsets, int32_t batch, int32_t total_q,
+                         const void* kv_pool_fp4, const int32_t* block_table, int32_t block_table_stride,
+                         const uint32_t* cache_lens, const void* w_uk, const void* w_uv, void* out,
+                         float* lse_out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Sparse top-k decode (decode page: sparse_mla, d_indices, indices_stride,
  * topk_lengths; indexer page: -1 marks an unused slot).
  *   kv_pool        bf16 [num_pages, ps, L+R]
@@ -216,6 +245,90 @@ int mla_branch_prologue(const mla_dims_t* dims, void* q, const uint32_t* input_r
                         const uint32_t* cache_lens, const void* freqs_cis, int32_t max_seq_len,
                         const void* kv_norm_gamma, float epsilon, uint32_t flags, void* workspace,
                         size_t workspace_bytes, void* stream);
+
+/* Append to the paged cache.  Token t of request b at pos = cache_lens[b] - qlen + i
+ * brings its new latent row [c (L) ; r (R)] (the down projection's output); the row
+ * at position pos of request b becomes, in the cache's format,
+ *   c_kv   = bf16( c / sqrt(mean(c^2) + epsilon) * kv_norm_gamma )
+ *   k_rope = bf16( r turned by freqs_cis[pos] )
+ * and, if q is given, q_out is q with its rope part turned the same way: what a cache
+ * write followed by mla_branch_prologue computes, bit for bit, in one pass and for
+ * every cache format.  Coded formats store the codes of the bf16 c_kv divided by a
+ * power of two, nearest, ties to even:
+ *   E4M3  kv_scales[row] = the least 2^e with max|c_kv| <= 448 * 2^e
+ *   E2M1  per 32 values, the least 2^e with max|c_kv| <= 7 * 2^e (values above
+ *         6 * 2^e become 6 * 2^e)
+ * (1 where all are zero).  A row (E4M3) or group of 32 (E2M1) that holds a NaN or an
+ * infinity reads back as NaN throughout.
+ *   kv_new         bf16 [T, kv_new_stride], the first L + R of each row are used;
+ *                  kv_new_stride in elements, >= L + R, a multiple of 8
+ *   q, q_out       bf16 [T, H, N+R]; q_out == q turns in place; both NULL: no queries
+ *                  (num_heads and qk_nope are then ignored); they may not overlap otherwise
+ *   kv_pool        the cache, rows of the format
+ *   kv_scales      float [num_pages, ps] for E4M3, else NULL
+ *   rows_out       bf16 [T, L+R] or NULL: the values that the written rows stand for
+ *   freqs_cis      bf16 [max_seq_len, R], kv_norm_gamma bf16 [L], epsilon >= 0,
+ *   flags, workspace   as mla_branch_prologue
+ * kv_new, q, q_out, kv_pool, rows_out, freqs_cis and kv_norm_gamma are 16-byte
+ * aligned.  L is a multiple of 32 up to 512, R a multiple of 8 up to 128, N of 8.
+ * Tokens t >= input_row_offsets[B] are padding: nothing is written for them.
+ * A token whose position is outside [0, max_seq_len) or the block table, or whose page
+ * id is outside [0, num_pages), is skipped whole (its row, q_out and rows_out keep
+ * what they held) and recorded: MLA_ERR_DEVICE_CHECK in debug mode.  Two tokens that
+ * the block table sends to one row leave either's. */
+int mla_cache_append(const mla_dims_t* dims, int32_t cache_format, const void* kv_new, int64_t kv_new_stride,
+                     const uint32_t* input_row_offsets, int32_t batch, int32_t total_q, const void* q, void* q_out,
+                     void* kv_pool, float* kv_scales, void* rows_out, const int32_t* block_table,
+                     int32_t block_table_stride, const uint32_t* cache_lens, const void* freqs_cis,
+                     int32_t max_seq_len, const void* kv_norm_gamma, float epsilon, uint32_t flags, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Prefill: the decode's attention for many query tokens per request, in the expanded
+ * form (generic_flare_mla_prefill_kv_cache_ragged page), over the paged latent cache that
+ * mla_cache_append fills.  Per head, every visible cached row becomes a key
+ * [c_kv . w_uk ; k_rope] and a value w_uv . c_kv once, and the query tokens attend those:
+ * the values of mla_decode_paged for the same arguments, to rounding, at
+ * 2 H (N + R + V) operations per (query, key) pair instead of 2 H (2 L + R), plus
+ * 2 H L (N + V) per row.  At (N, R, L, V) = (128, 64, 512, 128) that is less from about
+ * 170 query tokens per request; for fewer the decode is the faster call.
+ *   dims         H <= 128; N, R, V multiples of 8, N and V <= 128, R <= 64; L a multiple
+ *                of 64 up to 512; any page size
+ *   opts         mask, window; scale finite; num_splits: ranges that each query block's
+ *                keys are cut into and joined from (0: one, more only while the call's
+ *                query blocks leave SMs idle; at most 256); flags 0 or
+ *                MLA_FLAG_DEBUG_CHECKS
+ *   q, out       bf16 [T, H, N+R], [T, H, V]; q already turned (rope part)
+ *   total_keys   host-side bound on the cached tokens of the requests that have query
+ *                tokens, >= their sum; it sizes the workspace.  A request that does not
+ *                fit gets NaN outputs and is recorded (MLA_ERR_DEVICE_CHECK in debug mode).
+ *   workspace    mla_prefill_workspace_size() bytes, 16-byte aligned.  The size has room
+ *                for the keys and values of as many heads as 4 GiB hold (at least one);
+ *                with less, down to one head's, the call takes more passes, with more,
+ *                fewer.
+ * Other arguments, masks, aliasing and errors as mla_decode_paged, with these points:
+ * tokens at or past input_row_offsets[B] keep what out and lse_out held; a cached row with
+ * a NaN or an infinity in its latent part makes NaN of the queries that see it and of no
+ * other.
+ * The fp8 call takes the cache and weights of mla_decode_paged_fp8, the fp4 call the cache
+ * of mla_decode_paged_fp4 and bf16 weights. */
+int mla_prefill_workspace_size(const mla_dims_t* dims, const mla_opts_t* opts, int32_t cache_format, int32_t batch,
+                               int32_t total_q, int64_t total_keys, size_t* bytes);
+int mla_prefill_paged(const mla_dims_t* dims, const mla_opts_t* opts, const void* q,
+                      const uint32_t* input_row_offsets, int32_t batch, int32_t total_q, const void* kv_pool,
+                      const int32_t* block_table, int32_t block_table_stride, const uint32_t* cache_lens,
+                      int64_t total_keys, const void* w_uk, const void* w_uv, void* out, float* lse_out,
+                      void* workspace, size_t workspace_bytes, void* stream);
+int mla_prefill_paged_fp8(const mla_dims_t* dims, const mla_opts_t* opts, const void* q,
+                          const uint32_t* input_row_offsets, int32_t batch, int32_t total_q, const void* kv_pool_fp8,
+                          const float* kv_scales, const int32_t* block_table, int32_t block_table_stride,
+                          const uint32_t* cache_lens, int64_t total_keys, const void* w_uk_fp8,
+                          const float* w_uk_scale, const void* w_uv_fp8, const float* w_uv_scale, void* out,
+                          float* lse_out, void* workspace, size_t workspace_bytes, void* stream);
+int mla_prefill_paged_fp4(const mla_dims_t* dims, const mla_opts_t* opts, const void* q,
+                          const uint32_t* input_row_offsets, int32_t batch, int32_t total_q, const void* kv_pool_fp4,
+                          const int32_t* block_table, int32_t block_table_stride, const uint32_t* cache_lens,
+                          int64_t total_keys, const void* w_uk, const void* w_uv, void* out, float* lse_out,
+                          void* workspace, size_t workspace_bytes, void* stream);
 
 /* FP8 indexer (mla_indexer_ragged_float8_paged page: the FP8 product of the query
  * with the key cache, with the query's per-head scales q_s and the key scales at

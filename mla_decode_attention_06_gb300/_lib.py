@@ -25,10 +25,15 @@ MLA_FLAG_DEBUG_CHECKS = 1
 MLA_FLAG_KERNEL_TIMING = 2
 MLA_FLAG_FOLD_PAIRS = 4
 MLA_FLAG_PER_TOKEN = 8
+MLA_CACHE_BF16 = 0
+MLA_CACHE_E4M3 = 1
+MLA_CACHE_E2M1 = 2
 KERNEL_NAMES = ("absorb_w_uk", "decode_splitkv", "w_uv")
 
 EXPORTED = ("mla_decode_workspace_size", "mla_decode_paged", "mla_decode_paged_fp8",
-            "mla_decode_sparse", "mla_decode_kernel_times", "mla_branch_prologue",
+            "mla_decode_paged_fp4", "mla_decode_sparse", "mla_decode_kernel_times", "mla_branch_prologue",
+            "mla_cache_append", "mla_prefill_workspace_size", "mla_prefill_paged", "mla_prefill_paged_fp8",
+            "mla_prefill_paged_fp4",
             "mla_indexer_workspace_size", "mla_indexer_fp8",
             "mla_debug_wait_selftest",
             "mla_status_string")
@@ -55,6 +60,23 @@ _SIGS = {
                              c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p,
                              c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
                              c_void_p],
+    "mla_decode_paged_fp4": [_P(MlaDims), _P(MlaOpts), c_void_p, c_void_p, c_int32, c_int32, c_void_p,
+                             c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                             c_void_p, c_size_t, c_void_p],
+    "mla_cache_append": [_P(MlaDims), c_int32, c_void_p, ctypes.c_int64, c_void_p, c_int32, c_int32, c_void_p,
+                         c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32,
+                         c_void_p, c_float, c_uint32, c_void_p, c_size_t, c_void_p],
+    "mla_prefill_workspace_size": [_P(MlaDims), _P(MlaOpts), c_int32, c_int32, c_int32, ctypes.c_int64,
+                                   _P(c_size_t)],
+    "mla_prefill_paged": [_P(MlaDims), _P(MlaOpts), c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p,
+                          c_int32, c_void_p, ctypes.c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                          c_size_t, c_void_p],
+    "mla_prefill_paged_fp8": [_P(MlaDims), _P(MlaOpts), c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p,
+                              c_void_p, c_int32, c_void_p, ctypes.c_int64, c_void_p, c_void_p, c_void_p, c_void_p,
+                              c_void_p, c_void_p, c_void_p, c_size_t, c_void_p],
+    "mla_prefill_paged_fp4": [_P(MlaDims), _P(MlaOpts), c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p,
+                              c_int32, c_void_p, ctypes.c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                              c_size_t, c_void_p],
     "mla_decode_sparse": [_P(MlaDims), _P(MlaOpts), c_void_p, c_void_p, c_int32, c_int32, c_void_p,
                           c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                           c_void_p, c_size_t, c_void_p],

@@ -3,10 +3,12 @@
 // Nothing here allocates or synchronises unless MLA_FLAG_DEBUG_CHECKS is set.
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 
 #include "mla_kernels.cuh"
 #include "mla_plan.cuh"
+#include "mla_prefill.cuh"
 
 using namespace mla;
 
@@ -72,8 +74,8 @@ int check_dims(const mla_dims_t* d) {
 // either the caller asks for pairs or, by default, the call is sparse (its
 // gathered loads bound the main loop; a dense call's tile period is set by the
 // score contraction, which pairs do not shrink).
-bool use_fold(const mla_dims_t* d, const mla_opts_t* o, int batch, int total_q, bool fp8_cache, bool sparse) {
-  if (total_q < 2 * batch || !decode_fold_supported(*d, fp8_cache)) return false;
+bool use_fold(const mla_dims_t* d, const mla_opts_t* o, int batch, int total_q, KVFmt fmt, bool sparse) {
+  if (total_q < 2 * batch || !decode_fold_supported(*d, fmt)) return false;
   if (o->flags & MLA_FLAG_FOLD_PAIRS) return true;
   if (o->flags & MLA_FLAG_PER_TOKEN) return false;
   return sparse;
@@ -82,8 +84,8 @@ bool use_fold(const mla_dims_t* d, const mla_opts_t* o, int batch, int total_q, 
 // The partition count: the caller's, else as many partitions as the device runs at
 // once for the instance the call uses (`d` given), or, for sizing the workspace, the
 // SM count over the CTAs per partition, which is never below that.
-int resolve_splits(const mla_opts_t* o, bool fold, int* K, const mla_dims_t* d = nullptr, bool fp8 = false,
-                   bool sparse = false) {
+int resolve_splits(const mla_opts_t* o, bool fold, int* K, const mla_dims_t* d = nullptr,
+                   KVFmt fmt = KVFmt::kBF16, bool sparse = false) {
   if (o->num_splits < 0 || o->num_splits > kMaxSplits) return MLA_ERR_INVALID_ARG;
   if (o->num_splits > 0) {
     *K = o->num_splits;
@@ -94,7 +96,7 @@ int resolve_splits(const mla_opts_t* o, bool fold, int* K, const mla_dims_t* d =
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MLA_ERR_CUDA;
   const int per = fold ? 4 : 2;   // CTAs per partition (one for narrow latents, which stay at sms / 2)
   const int bound = sms / per > 0 ? sms / per : 1;
-  int n = d ? decode_default_partitions(*d, fold, fp8, sparse) : 0;
+  int n = d ? decode_default_partitions(*d, fold, fmt, sparse) : 0;
   *K = n > 0 && n <= bound ? n : bound;
   return MLA_OK;
 }
@@ -159,9 +161,9 @@ int run(const CallCommon& c) {
       !aligned16(c.out) || !aligned16(c.ws))
     return MLA_ERR_INVALID_ARG;
   const bool sparse = c.ks.indices != nullptr;
-  const bool fold = use_fold(c.d, c.o, c.B, c.T, c.kv_fmt == KVFmt::kE4M3, sparse);
+  const bool fold = use_fold(c.d, c.o, c.B, c.T, c.kv_fmt, sparse);
   int K = 0;
-  if ((st = resolve_splits(c.o, fold, &K, c.d, c.kv_fmt == KVFmt::kE4M3, sparse))) return st;
+  if ((st = resolve_splits(c.o, fold, &K, c.d, c.kv_fmt, sparse))) return st;
   const WorkspaceLayout lay = workspace_layout(*c.d, c.T, K, fold ? 2 : 1);
   if (c.ws_bytes < lay.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
 
@@ -208,6 +210,11 @@ int run(const CallCommon& c) {
   pin.H = c.d->num_heads;
   pin.L = c.d->kv_lora_rank;
   pin.fold = fold;
+  // the e2m1 absorb checks its results beside the plan, so the plan must not clear the status
+  pin.keep_status = c.kv_fmt == KVFmt::kE2M1;
+  if (pin.keep_status && (c.o->flags & MLA_FLAG_DEBUG_CHECKS) &&
+      cudaMemsetAsync(hdr, 0, sizeof(PlanHeader), c.stream) != cudaSuccess)
+    return MLA_ERR_CUDA;
 
   EventSet* timer = nullptr;
   if (c.o->flags & MLA_FLAG_KERNEL_TIMING) {
@@ -222,7 +229,8 @@ int run(const CallCommon& c) {
   cudaError_t e = mark(0);
   if (e == cudaSuccess)
     e = launch_absorb_tc(*c.d, c.T, static_cast<const __nv_bfloat16*>(c.q), c.w_fmt, c.w_uk, c.w_uk_scale,
-                         reinterpret_cast<__nv_bfloat16*>(ws + lay.q_full), hdr, pin, c.stream);
+                         reinterpret_cast<__nv_bfloat16*>(ws + lay.q_full), hdr, pin, c.kv_fmt == KVFmt::kE2M1,
+                         c.stream);
   if (e == cudaSuccess) e = mark(1);
   if (e == cudaSuccess && c.T > 0) e = launch_decode_tc(a, c.stream);
   if (e == cudaSuccess) e = mark(2);
@@ -248,10 +256,10 @@ int mla_decode_workspace_size(const mla_dims_t* dims, const mla_opts_t* opts, in
   if (st) return st;
   if (!opts || !bytes || batch < 1 || total_q < 0) return MLA_ERR_INVALID_ARG;
   // one size for both walks, whether or not opts asks for folded pairs; the bf16
-  // shapes' size also covers an e4m3 cache (whose calls never fold)
+  // shapes' size also covers e4m3 and e2m1 caches (whose calls never fold)
   mla_opts_t both = *opts;
   both.flags |= MLA_FLAG_FOLD_PAIRS;
-  const bool fold = use_fold(dims, &both, batch, total_q, false, false);
+  const bool fold = use_fold(dims, &both, batch, total_q, KVFmt::kBF16, false);
   int K = 0;
   if ((st = resolve_splits(opts, fold, &K))) return st;
   const size_t a = workspace_layout(*dims, total_q, K, fold ? 2 : 1).total;
@@ -318,6 +326,34 @@ int mla_decode_paged_fp8(const mla_dims_t* dims, const mla_opts_t* opts, const v
   c.w_uv = w_uv_fp8;
   c.w_uk_scale = w_uk_scale;
   c.w_uv_scale = w_uv_scale;
+  c.out = out;
+  c.lse_out = lse_out;
+  c.ws = workspace;
+  c.ws_bytes = workspace_bytes;
+  c.stream = static_cast<cudaStream_t>(stream);
+  return run(c);
+}
+
+int mla_decode_paged_fp4(const mla_dims_t* dims, const mla_opts_t* opts, const void* q,
+                         const uint32_t* input_row_offsets, int32_t batch, int32_t total_q,
+                         const void* kv_pool_fp4, const int32_t* block_table, int32_t block_table_stride,
+                         const uint32_t* cache_lens, const void* w_uk, const void* w_uv, void* out,
+                         float* lse_out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dims || !block_table || !cache_lens || block_table_stride < 1) return MLA_ERR_INVALID_ARG;
+  CallCommon c{};
+  c.d = dims;
+  c.o = opts;
+  c.q = q;
+  c.offsets = input_row_offsets;
+  c.B = batch;
+  c.T = total_q;
+  c.ks = KeySource{block_table, block_table_stride, cache_lens, nullptr, 0, nullptr, dims->page_size,
+                   dims->num_pages};
+  c.kv_fmt = KVFmt::kE2M1;
+  c.kv_pool = kv_pool_fp4;
+  c.w_fmt = WFmt::kBF16;
+  c.w_uk = w_uk;
+  c.w_uv = w_uv;
   c.out = out;
   c.lse_out = lse_out;
   c.ws = workspace;
@@ -409,6 +445,173 @@ int mla_branch_prologue(const mla_dims_t* dims, void* q, const uint32_t* input_r
   }
   if (flags & MLA_FLAG_DEBUG_CHECKS) return device_status(hdr, s);
   return MLA_OK;
+}
+
+int mla_cache_append(const mla_dims_t* dims, int32_t cache_format, const void* kv_new, int64_t kv_new_stride,
+                     const uint32_t* input_row_offsets, int32_t batch, int32_t total_q, const void* q, void* q_out,
+                     void* kv_pool, float* kv_scales, void* rows_out, const int32_t* block_table,
+                     int32_t block_table_stride, const uint32_t* cache_lens, const void* freqs_cis,
+                     int32_t max_seq_len, const void* kv_norm_gamma, float epsilon, uint32_t flags, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (!dims || (q && (dims->num_heads < 1 || dims->qk_nope < 0)) || dims->qk_rope < 1 || dims->kv_lora_rank < 1 ||
+      dims->page_size < 1 || dims->num_pages < 1)
+    return MLA_ERR_INVALID_ARG;
+  if (cache_format < MLA_CACHE_BF16 || cache_format > MLA_CACHE_E2M1) return MLA_ERR_INVALID_ARG;
+  if (dims->kv_lora_rank % 32 != 0 || dims->kv_lora_rank > 512 || dims->qk_rope % 8 != 0 || dims->qk_rope > 128 ||
+      (q && dims->qk_nope % 8 != 0))
+    return MLA_ERR_UNSUPPORTED;
+  if ((int64_t)dims->num_pages * dims->page_size > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if (batch < 1 || total_q < 0 || block_table_stride < 1 || max_seq_len < 1) return MLA_ERR_INVALID_ARG;
+  if (kv_new_stride < dims->kv_lora_rank + dims->qk_rope || kv_new_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
+  if ((!kv_new && total_q > 0) || !input_row_offsets || !kv_pool || !block_table || !cache_lens || !freqs_cis ||
+      !kv_norm_gamma || !workspace)
+    return MLA_ERR_INVALID_ARG;
+  if ((cache_format == MLA_CACHE_E4M3) != (kv_scales != nullptr) || (q != nullptr) != (q_out != nullptr))
+    return MLA_ERR_INVALID_ARG;
+  for (const void* p : {kv_new, q, static_cast<const void*>(q_out), static_cast<const void*>(kv_pool),
+                        static_cast<const void*>(rows_out), freqs_cis, kv_norm_gamma})
+    if (!aligned16(p)) return MLA_ERR_INVALID_ARG;
+  if (!(epsilon >= 0.f) || (flags & ~MLA_FLAG_DEBUG_CHECKS)) return MLA_ERR_INVALID_ARG;
+  if (workspace_bytes < sizeof(PlanHeader) || !aligned16(workspace)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  PlanHeader* hdr = static_cast<PlanHeader*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // the status word is read back only in debug mode, so only then is it cleared first
+  if ((flags & MLA_FLAG_DEBUG_CHECKS) && cudaMemsetAsync(hdr, 0, sizeof(PlanHeader), s) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  const cudaError_t e = launch_append(*dims, cache_format, kv_new, kv_new_stride, input_row_offsets, batch, total_q, q,
+                                      q_out, kv_pool, kv_scales, rows_out, block_table, block_table_stride, cache_lens,
+                                      freqs_cis, max_seq_len, kv_norm_gamma, epsilon, hdr, s);
+  if (e != cudaSuccess) {
+    std::fprintf(stderr, "mla_cache_append: %s\n", cudaGetErrorString(e));
+    return MLA_ERR_CUDA;
+  }
+  if (flags & MLA_FLAG_DEBUG_CHECKS) return device_status(hdr, s);
+  return MLA_OK;
+}
+
+namespace {
+// K and V boxes of a pass: all heads if they fit this, else as many as do.
+constexpr size_t kPrefillPassBytes = size_t(4) << 30;
+
+int check_prefill(const mla_dims_t* d, const mla_opts_t* o, int batch, int total_q, int64_t total_keys) {
+  if (!d || !o) return MLA_ERR_INVALID_ARG;
+  if (d->num_heads < 1 || d->qk_nope < 1 || d->qk_rope < 1 || d->kv_lora_rank < 1 || d->v_head < 1 ||
+      d->page_size < 1 || d->num_pages < 1 || batch < 1 || total_q < 0 || total_keys < 0)
+    return MLA_ERR_INVALID_ARG;
+  const int st = check_opts(o);
+  if (st) return st;
+  if ((o->flags & ~MLA_FLAG_DEBUG_CHECKS) || o->num_splits < 0 || !(o->scale - o->scale == 0.f))
+    return MLA_ERR_INVALID_ARG;
+  if (d->num_heads > kMaxHeads || !prefill_supported(*d)) return MLA_ERR_UNSUPPORTED;
+  if ((int64_t)d->num_pages * d->page_size > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  // key tiles, query blocks and grids are counted in 32 bits
+  if (total_keys > (int64_t(1) << 28) || total_q > (1 << 28) || batch > (1 << 20) || o->num_splits > 256)
+    return MLA_ERR_UNSUPPORTED;
+  const PrefillLayout l = prefill_layout(*d, batch, total_q, total_keys, 1, false);
+  if (l.max_items * d->num_heads * (o->num_splits > 0 ? o->num_splits : 1) > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
+int prefill_resolve_splits(const mla_dims_t* d, const mla_opts_t* o, int batch, int total_q, int64_t total_keys,
+                           int* splits) {
+  *splits = o->num_splits;
+  if (*splits > 0) return MLA_OK;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  *splits = prefill_splits(*d, batch, total_q, total_keys, sms);
+  return MLA_OK;
+}
+
+struct PrefillArgs {
+  int fmt;
+  const mla_opts_t* o;
+  int64_t total_keys;
+  size_t ws_bytes;
+  void* stream;
+};
+
+int run_prefill(PrefillCall& c, const PrefillArgs& p) {
+  int st = check_prefill(&c.d, p.o, c.B, c.T, p.total_keys);
+  if (st) return st;
+  if (c.bt_stride < 1 || !c.offsets || !c.pool || !c.block_table || !c.cache_lens || !c.w_uk || !c.w_uv || !c.ws)
+    return MLA_ERR_INVALID_ARG;
+  if (c.T > 0 && (!c.q || !c.out)) return MLA_ERR_INVALID_ARG;
+  for (const void* x : {c.q, c.pool, c.w_uk, c.w_uv, static_cast<const void*>(c.out), static_cast<const void*>(c.ws)})
+    if (!aligned16(x)) return MLA_ERR_INVALID_ARG;
+  int splits = 1;
+  if ((st = prefill_resolve_splits(&c.d, p.o, c.B, c.T, p.total_keys, &splits))) return st;
+  const PrefillLayout lay = prefill_layout(c.d, c.B, c.T, p.total_keys, splits, c.w_uk_scale != nullptr);
+  if (p.ws_bytes < lay.kv + lay.head_bytes) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  const size_t fit = (p.ws_bytes - lay.kv) / lay.head_bytes;
+  // passes of equal size: the last one is not left with a few heads
+  const int H = c.d.num_heads, passes = fit >= (size_t)H ? 1 : (int)((H + fit - 1) / fit);
+  const int heads = (H + passes - 1) / passes;
+  c.fmt = p.fmt;
+  c.mask = p.o->mask;
+  c.window = p.o->window;
+  c.scale = p.o->scale;
+  cudaStream_t s = static_cast<cudaStream_t>(p.stream);
+  const cudaError_t e = launch_prefill(c, lay, heads, splits, s);
+  if (e != cudaSuccess) {
+    std::fprintf(stderr, "mla_prefill: %s\n", cudaGetErrorString(e));
+    return MLA_ERR_CUDA;
+  }
+  if ((p.o->flags & MLA_FLAG_DEBUG_CHECKS) && c.T > 0)
+    return device_status(reinterpret_cast<const PlanHeader*>(static_cast<char*>(c.ws) + lay.header), s);
+  return MLA_OK;
+}
+}  // namespace
+
+int mla_prefill_workspace_size(const mla_dims_t* dims, const mla_opts_t* opts, int32_t cache_format, int32_t batch,
+                               int32_t total_q, int64_t total_keys, size_t* bytes) {
+  int st = check_prefill(dims, opts, batch, total_q, total_keys);
+  if (st) return st;
+  if (!bytes || cache_format < MLA_CACHE_BF16 || cache_format > MLA_CACHE_E2M1) return MLA_ERR_INVALID_ARG;
+  int splits = 1;
+  if ((st = prefill_resolve_splits(dims, opts, batch, total_q, total_keys, &splits))) return st;
+  const PrefillLayout l = prefill_layout(*dims, batch, total_q, total_keys, splits, cache_format == MLA_CACHE_E4M3);
+  size_t heads = kPrefillPassBytes / l.head_bytes;
+  if (heads < 1) heads = 1;
+  if (heads > (size_t)dims->num_heads) heads = dims->num_heads;
+  *bytes = l.kv + heads * l.head_bytes;
+  return MLA_OK;
+}
+
+int mla_prefill_paged(const mla_dims_t* dims, const mla_opts_t* opts, const void* q,
+                      const uint32_t* input_row_offsets, int32_t batch, int32_t total_q, const void* kv_pool,
+                      const int32_t* block_table, int32_t block_table_stride, const uint32_t* cache_lens,
+                      int64_t total_keys, const void* w_uk, const void* w_uv, void* out, float* lse_out,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dims) return MLA_ERR_INVALID_ARG;
+  PrefillCall c{*dims,  0,    batch,      total_q, 0,       0,    block_table_stride, 0.f,       q, input_row_offsets,
+                kv_pool, nullptr, block_table, cache_lens, w_uk, w_uv, nullptr, nullptr, out, lse_out, workspace};
+  return run_prefill(c, PrefillArgs{MLA_CACHE_BF16, opts, total_keys, workspace_bytes, stream});
+}
+
+int mla_prefill_paged_fp8(const mla_dims_t* dims, const mla_opts_t* opts, const void* q,
+                          const uint32_t* input_row_offsets, int32_t batch, int32_t total_q, const void* kv_pool_fp8,
+                          const float* kv_scales, const int32_t* block_table, int32_t block_table_stride,
+                          const uint32_t* cache_lens, int64_t total_keys, const void* w_uk_fp8,
+                          const float* w_uk_scale, const void* w_uv_fp8, const float* w_uv_scale, void* out,
+                          float* lse_out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dims || !kv_scales || !w_uk_scale || !w_uv_scale) return MLA_ERR_INVALID_ARG;
+  PrefillCall c{*dims, 0, batch, total_q, 0, 0, block_table_stride, 0.f, q, input_row_offsets,
+                kv_pool_fp8, kv_scales, block_table, cache_lens, w_uk_fp8, w_uv_fp8, w_uk_scale, w_uv_scale, out,
+                lse_out, workspace};
+  return run_prefill(c, PrefillArgs{MLA_CACHE_E4M3, opts, total_keys, workspace_bytes, stream});
+}
+
+int mla_prefill_paged_fp4(const mla_dims_t* dims, const mla_opts_t* opts, const void* q,
+                          const uint32_t* input_row_offsets, int32_t batch, int32_t total_q, const void* kv_pool_fp4,
+                          const int32_t* block_table, int32_t block_table_stride, const uint32_t* cache_lens,
+                          int64_t total_keys, const void* w_uk, const void* w_uv, void* out, float* lse_out,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dims) return MLA_ERR_INVALID_ARG;
+  PrefillCall c{*dims, 0, batch, total_q, 0, 0, block_table_stride, 0.f, q, input_row_offsets,
+                kv_pool_fp4, nullptr, block_table, cache_lens, w_uk, w_uv, nullptr, nullptr, out, lse_out, workspace};
+  return run_prefill(c, PrefillArgs{MLA_CACHE_E2M1, opts, total_keys, workspace_bytes, stream});
 }
 
 namespace {

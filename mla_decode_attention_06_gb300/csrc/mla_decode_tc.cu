@@ -38,10 +38,11 @@
 //               domain, writes P (bf16 pairs) back into TMEM where the P . C
 //               MMA takes it as its A operand, rescales O only when the running
 //               max grows by more than 2^8, and writes the segment's output.
-//   warps 6-9   (e4m3 cache) widen the tile's codes x row scale into bf16.
+//   warps 6-9   (e4m3, e2m1 cache) widen the tile's codes x scale into bf16.
 //   last warp   P . C issuer (one thread), so a ready P never waits behind a QK.
 // Every wait is bounded in time; a timeout sets a status bit and the kernel
 // unwinds without hanging.
+#include <cuda_fp4.h>
 #include <math_constants.h>
 
 #include <mutex>
@@ -62,6 +63,7 @@ enum LoadMode : int {
   kLoadFp8 = 1,     // e4m3 pool through the page table: TMA bytes (multicast), widened by converter warps
   kLoadSparse = 2,  // bf16 pool rows named by an index list, TMA gather4: each CTA gathers half
                     // of a tile's boxes and multicasts them to both CTAs of the cluster
+  kLoadFp4 = 3,     // e2m1 pool through the page table: TMA bytes (multicast), widened like e4m3
 };
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: rescale O when the max grows by > 2^8
 // The producer reads the page-table entries of the tile this many ahead of the one it
@@ -71,7 +73,7 @@ constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
 struct Smem {   // control block after the stage ring
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
-  uint64_t kv_conv[kMaxStages];  // e4m3 rows widened (kLoadFp8)
+  uint64_t kv_conv[kMaxStages];  // coded rows widened (kLoadFp8, kLoadFp4)
   uint64_t kv_conv_a[kMaxStages];  // ... their first raw box (latent [0, RW)), when NRH > 1
   uint64_t row_mask[kMaxStages];
   uint64_t q_full, q_empty;
@@ -113,9 +115,16 @@ struct Cfg {
   static constexpr int kTmemCols = (kQCol + QT / 2) <= 256 ? 256 : 512;
   static constexpr int RW = L < 256 ? L : 256;      // e4m3 bytes per raw box row
   static constexpr int NRH = L / RW;                // raw boxes per cached row
+  static constexpr bool kCoded = kMode == kLoadFp8 || kMode == kLoadFp4;   // rows are widened by converter warps
+  // the instruction descriptor's operand types, bf16 or (e2m1) f16: flips bits 7 and 10
+  static constexpr uint32_t kOperands = kMode == kLoadFp4 ? (1u << 7) | (1u << 10) : 0u;
+  // e2m1: bytes of a row before its rope part (codes, a scale byte per 32 of them, zeros up
+  // to 16); a multiple of 16 that is an odd number of 16-byte pieces at both widths, so
+  // eight neighbouring rows start in eight different bank groups
+  static constexpr int kRow4 = (L / 2 + L / 32 + 15) / 16 * 16;
   static constexpr int kRawOff = NLB >= 8 ? 4 * kBox : 0;   // codes land where the last latent boxes go
-  static constexpr int kConvThreads = 64 * NRH;                // warps 6.. (kLoadFp8): one per row and raw box
-  static constexpr int kPvWarp = kMode == kLoadFp8 ? 6 + kConvThreads / 32 : 6;   // the P . C issuer
+  static constexpr int kConvThreads = 64 * NRH;                // warps 6.. (kCoded): one per row and raw box
+  static constexpr int kPvWarp = kCoded ? 6 + kConvThreads / 32 : 6;   // the P . C issuer
   static constexpr int kThreads = 32 * (kPvWarp + 1);
   static constexpr int kRegionBytes = kQBytes + kStages * kStageBytes;   // query buffer + stage ring
   static constexpr int kMrgHalf = (LC / 2) * kMaxHeads * 4;               // merge: one half partial slice
@@ -125,13 +134,14 @@ struct Cfg {
   static_assert(kQCol + QT / 2 <= 512, "TMEM columns");
   static_assert(kStgBytes + 2 * kMrgHalf <= kRegionBytes, "merge buffers in the idle region");
   static_assert(kMode != kLoadFp8 || NRH % CL == 0, "raw boxes split over the cluster");
-  static_assert(kMode != kLoadFp8 || NRH == 1 || QT == RW, "raw box 0 is the QK's TMEM-operand part");
+  static_assert(!kCoded || NRH == 1 || QT == RW, "the first widening pass is the QK's TMEM-operand part");
+  static_assert(kRawOff + 64 * kRow4 <= NLB * kBox, "e2m1 rows below the rope box");
   static_assert(QT / 64 <= NQS + 1, "the query staging fits the query buffer");
   static_assert(kSmem <= 232448, "shared memory");
 };
 
 struct Maps {
-  CUtensorMap kv_lat;    // bf16 latent boxes (dense: page rows, sparse: 1 row) / e4m3 bytes (kLoadFp8)
+  CUtensorMap kv_lat;    // bf16 latent boxes (dense: page rows, sparse: 1 row) / code bytes (kCoded)
   CUtensorMap kv_rope;   // bf16 rope box
   CUtensorMap q;         // absorbed queries [T * 128, L + R], 64-column boxes
 };
@@ -240,6 +250,40 @@ __device__ __forceinline__ uint32_t e4m3x2_scaled_bf16x2(uint16_t two, float sca
       : "=f"(x), "=f"(y)
       : "f"(f.x), "f"(f.y), "f"(scale));
   const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Two e2m1 codes (a byte, low nibble first) times a scale, as an f16 pair.
+__device__ __forceinline__ uint32_t e2m1x2_scaled_f16x2(uint32_t byte, __half2 scale) {
+  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1);
+  const __half2 v = __hmul2(__half2(h), scale);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A scale byte (2^(b - 127), 255 = NaN) as an f16 pair: zero below 2^-24, infinity above 2^15.
+__device__ __forceinline__ __half2 e8m0_f16x2(uint32_t b) {
+  const int e = (int)b - 127;
+  uint32_t h = (uint32_t)(e + 15) << 10;
+  if (e < -14) h = e < -24 ? 0u : 1u << (e + 24);
+  if (e > 15) h = b == 255u ? 0x7E00u : 0x7C00u;
+  h |= h << 16;
+  return *reinterpret_cast<const __half2*>(&h);
+}
+
+// A bf16 pair as an f16 pair.
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v) {
+  const __half2 h = __floats2half2_rn(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two probabilities as the MMA's operand pair: f16 over an e2m1 cache, else bf16.
+template <int MODE>
+__device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
+  if (MODE == kLoadFp4) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
@@ -509,8 +553,9 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
   const int H = a.d.num_heads;
   const int KQ = L + a.d.qk_rope;
   const int lat_x0 = (int)rank * LC;
-  // cache rope columns: they start at L in a bf16 row, at byte L (bf16 column L / 2) in an e4m3 row
-  const int rope_x0 = MODE == kLoadFp8 ? L / 2 : L;
+  // cache rope columns: they start at L in a bf16 row, at byte L (bf16 column L / 2) in an
+  // e4m3 row, at byte kRow4 in an e2m1 row
+  const int rope_x0 = MODE == kLoadFp8 ? L / 2 : MODE == kLoadFp4 ? C::kRow4 / 2 : L;
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
@@ -561,7 +606,9 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
 
   const int g0 = a.bounds[k], g1 = a.bounds[k + 1];
   const int ps = a.ks.page_size;
-  const int rows_per_load = ps < kTileKeys ? ps : kTileKeys;
+  // e2m1 rows are one box wide, so the CTAs of a cluster share a tile's loads by rows
+  constexpr int kMaxLoadRows = MODE == kLoadFp4 ? kTileKeys / 2 : kTileKeys;
+  const int rows_per_load = ps < kMaxLoadRows ? ps : kMaxLoadRows;
 
   if (warp == 0) {
     // ------------------------------------------------------------- producer
@@ -644,7 +691,9 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
           const uint64_t pm = (mask >> (p * rows_per_load)) & lmask;
           if (!pm) continue;
           const int y = load_row(it, p, pm, pg);
-          if (lane < kOwn) {
+          if (MODE == kLoadFp4) {
+            if (lane < 2 && p % CL == (int)crank) tma_prefetch_2d(lane ? &maps.kv_rope : &maps.kv_lat, lane ? rope_x0 : 0, y);
+          } else if (lane < kOwn) {
             if (MODE == kLoadFp8) tma_prefetch_2d(&maps.kv_lat, ((int)crank * kOwn + lane) * C::RW, y);
             else tma_prefetch_2d(&maps.kv_lat, 64 * ((int)crank * kOwn + lane), y);
           } else if (lane == kOwn && crank == 0) {
@@ -697,14 +746,14 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         // tile two ahead after issuing this one's loads instead.
         int raw[2], raw2[2];
         fetch(it, raw);
-        const bool pf = MODE == kLoadDense && it + kPrefetchAhead < ie;
+        const bool pf = (MODE == kLoadDense || MODE == kLoadFp4) && it + kPrefetchAhead < ie;
         if (pf) fetch(it + kPrefetchAhead, raw2);
         bool v[2], v2[2];
         int rid[2], pg[2], rid2[2], pg2[2];
-        if (MODE != kLoadDense) finish(it, raw, v, rid, pg);
+        if (MODE == kLoadFp8 || MODE == kLoadSparse) finish(it, raw, v, rid, pg);
         // stage s is free in both CTAs once both have committed their P . C of its last tile
         if (c >= S && !wwait(&cs->kv_empty[s], ((c / S) & 1) ^ 1, cs, hdr)) return;
-        if (MODE == kLoadDense) finish(it, raw, v, rid, pg);
+        if (MODE == kLoadDense || MODE == kLoadFp4) finish(it, raw, v, rid, pg);
         if (pf) finish(it + kPrefetchAhead, raw2, v2, rid2, pg2);
         if (MODE == kLoadSparse) {
           cs->rowid[s][lane] = rid[0];
@@ -749,7 +798,8 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
           // pages of this tile that hold at least one live row; both CTAs count the
           // same bytes, most of which the other CTAs' multicasts deliver (an e4m3 row's
           // 4-byte scale each CTA copies for itself)
-          const uint32_t row_bytes = (MODE == kLoadFp8 ? L + 4 : C::NLB * 128) + 128;
+          const uint32_t row_bytes =
+              (MODE == kLoadFp8 ? L + 4 : MODE == kLoadFp4 ? C::kRow4 : C::NLB * 128) + 128;
           uint32_t live_rows = 0;
           for (int p = 0; p < nloads; ++p)
             if ((mask >> (p * rows_per_load)) & lmask) live_rows += rows_per_load;
@@ -764,7 +814,12 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
             const int r0 = p * rows_per_load;
             const int y = load_row(it, p, pm, pg);
             // one box per lane: this CTA's share of the latent (or raw e4m3) boxes, then the rope box (rank 0)
-            if (lane < kOwn) {
+            if (MODE == kLoadFp4) {
+              if (p % CL == (int)crank && lane == 0)
+                load_box(st + C::kRawOff + r0 * C::kRow4, &maps.kv_lat, &cs->kv_full[s], 0, y);
+              else if (p % CL == (int)crank && lane == 1)
+                load_box(st_rope + r0 * 128, &maps.kv_rope, &cs->kv_full[s], rope_x0, y);
+            } else if (lane < kOwn) {
               if (MODE == kLoadFp8) {
                 const int h = (int)crank * kOwn + lane;
                 load_box(st + C::kRawOff + h * 64 * C::RW + r0 * C::RW, &maps.kv_lat, &cs->kv_full[s], h * C::RW, y);
@@ -824,7 +879,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
     // QK of tile c as soon as its rows have landed.  The S buffer of tile c held
     // P of tile c - 2, which the P . C warp reads: wait for that MMA to complete.
     // The MMA queue is shallow, so the 36 MMAs are issued back to back.
-    const uint32_t idesc_qk = idesc_bf16_f32(128, 64, false, false);
+    const uint32_t idesc_qk = idesc_bf16_f32(128, 64, false, false) ^ C::kOperands;
     // K-major operand descriptors of the query boxes and of stage 0; the start
     // address field is advanced by (byte offset >> 4) for every other operand
     const uint64_t dq0 = smem_desc(smem_u32(sQ), 16, 1024, kLayoutSw128);
@@ -843,11 +898,11 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         const int s = cq % S, b = cq & 1;
         const uint32_t par = (cq / S) & 1;
         if (cq >= 2 && !wwait(&cs->pv_done[b], ((cq - 2) >> 1) & 1, cs, hdr)) return;
-        if (!wwait(MODE != kLoadFp8 ? &cs->kv_full[s] : C::NRH > 1 ? &cs->kv_conv_a[s] : &cs->kv_conv[s], par, cs,
+        if (!wwait(!C::kCoded ? &cs->kv_full[s] : C::NRH > 1 ? &cs->kv_conv_a[s] : &cs->kv_conv[s], par, cs,
                    hdr))
           return;
         const uint64_t mask = cs->row_mask[s];
-        if (MODE != kLoadFp8 && mask != ~0ull) {
+        if (!C::kCoded && mask != ~0ull) {
           // Rows outside the key range may hold anything (NaN included).  Their
           // scores are dropped by the row mask, not by value, so only this CTA's
           // P . C boxes need them zeroed (P = 0 times NaN would poison O): one
@@ -887,7 +942,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
           tc_fence_after();
           q_smem = true;
         }
-        if (MODE == kLoadFp8 && C::NRH > 1) {
+        if (C::kCoded && C::NRH > 1) {
           // the rest of the tile's latent columns and the dead rows' rope zeros
           __syncwarp();
           if (!wwait(&cs->kv_conv[s], par, cs, hdr)) return;
@@ -918,7 +973,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
     // O += P . C for tile c as soon as its P is in TMEM (and, for a segment's
     // first tile, the previous segment's O has been read); the commit frees the
     // stage in both CTAs of the cluster.
-    const uint32_t idesc_pv = idesc_bf16_f32(128, LC, false, true);
+    const uint32_t idesc_pv = idesc_bf16_f32(128, LC, false, true) ^ C::kOperands;
     const uint64_t dv0 = smem_desc(smem_u32(sStage) + (lat_x0 / 64) * C::kBox, C::kBox, 1024, kLayoutSw128);
     int cp = 0;
     for_each_segment(a, k, g0, g1, [&](int si, int t, const TokenPlan& tp, int ia, int ie, bool, int) {
@@ -1020,6 +1075,98 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         mbar_arrive(&cs->kv_conv[s]);
       }
     });
+  } else if (MODE == kLoadFp4 && warp >= 6) {
+    // ------------------------------------------------------------- e2m1 converters
+    // Tile row crow is widened by NRH threads, pass p taking its codes of latent
+    // [p RW, (p + 1) RW), thread hh the hh-th RW / NRH of them: groups of 32 codes
+    // (16 bytes) under one scale byte.  The operands are f16: a code times 2^e is exact
+    // for e in [-23, 13] (one conversion and one packed multiply per pair; bf16 has no
+    // conversion from e2m1 and would take six operations), and the absorbed query and P
+    // lose 2^-12 instead of 2^-9.  The rope part is bf16 and is converted with the last
+    // pass.  A magnitude that f16 does not reach becomes an infinity and is reported.
+    // The last pass overwrites the codes, so it waits until every thread has read its own.
+    const int ci = tid - 192, crow = ci & 63, hh = ci >> 6;
+    constexpr int kGroups = C::RW / C::NRH / 32;   // groups per thread and pass
+    constexpr int kRopeChunks = 8 / C::NRH;        // 16-byte chunks of the rope row per thread
+    int c = 0;
+    bool out_of_range = false;
+    for_each_segment(a, k, g0, g1, [&](int si, int t, const TokenPlan& tp, int ia, int ie, bool, int) {
+      for (int it = ia; it < ie; ++it, ++c) {
+        if (waborted(cs)) return;
+        const int s = c % S;
+        if (!wwait(&cs->kv_full[s], (c / S) & 1, cs, hdr)) return;
+        uint8_t* st = sStage + s * C::kStageBytes;
+        const bool live = (cs->row_mask[s] >> crow) & 1ull;
+        const uint8_t* src = st + C::kRawOff + crow * C::kRow4;
+#pragma unroll 1
+        for (int p = 0; p < C::NRH; ++p) {
+          const int grp0 = p * (C::RW / 32) + hh * kGroups;
+          uint4 raw[kGroups];
+          uint32_t sb = 0;   // kGroups <= 4 scale bytes
+#pragma unroll
+          for (int q = 0; q < kGroups; ++q) raw[q] = *reinterpret_cast<const uint4*>(src + (grp0 + q) * 16);
+          if (kGroups == 4) {
+            sb = *reinterpret_cast<const uint32_t*>(src + L / 2 + grp0);
+          } else {
+#pragma unroll
+            for (int q = 0; q < kGroups; ++q) sb |= (uint32_t)src[L / 2 + grp0 + q] << (8 * q);
+          }
+          if (p == C::NRH - 1) {
+            mbar_arrive(&cs->conv_sync);
+            if (!wwait(&cs->conv_sync, c & 1, cs, hdr)) return;
+          }
+          auto put = [&](int q, auto&& value) {   // group q's 32 columns: four 16-byte slots of the swizzled row
+            const int col = (grp0 + q) * 32;
+            uint8_t* box = st + (col >> 6) * C::kBox + crow * 128;
+            const int ch = (col & 63) >> 3;
+            const uint32_t w[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(box + (((ch + i) ^ (crow & 7)) << 4)) =
+                  make_uint4(value(w[i] & 0xFFu), value((w[i] >> 8) & 0xFFu), value((w[i] >> 16) & 0xFFu),
+                             value(w[i] >> 24));
+          };
+          if (live) {
+#pragma unroll
+            for (int q = 0; q < kGroups; ++q) {
+              const uint32_t b = (sb >> (8 * q)) & 0xFFu;
+              out_of_range |= b > 140u && b != 255u;   // 6 * 2^14 is past f16
+              const __half2 sc = e8m0_f16x2(b);
+              put(q, [&](uint32_t byte) { return e2m1x2_scaled_f16x2(byte, sc); });
+            }
+          } else {
+            // a dead row (only in a token's ragged tiles) becomes zeros
+#pragma unroll
+            for (int q = 0; q < kGroups; ++q) put(q, [](uint32_t) { return 0u; });
+          }
+          if (C::NRH > 1 && p == 0) {
+            // latent [0, RW) is in place: the QK's TMEM-operand part may start
+            fence_proxy_async_smem();
+            mbar_arrive(&cs->kv_conv_a[s]);
+          }
+        }
+        uint8_t* rr = st + C::NLB * C::kBox + crow * 128;
+#pragma unroll
+        for (int i = 0; i < kRopeChunks; ++i) {
+          uint4* x = reinterpret_cast<uint4*>(rr + (((hh * kRopeChunks + i) ^ (crow & 7)) << 4));
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (live) {
+            v = *x;
+            // 0x4780: 65536 as bf16, the first that rounds to infinity
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              out_of_range |= ((w[e] & 0x7FFFu) >= 0x4780u && (w[e] & 0x7FFFu) < 0x7F80u) ||
+                              ((w[e] >> 16 & 0x7FFFu) >= 0x4780u && (w[e] >> 16 & 0x7FFFu) < 0x7F80u);
+            v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+          }
+          *x = v;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&cs->kv_conv[s]);
+      }
+    });
+    if (out_of_range) atomicOr(&hdr->status, kDeviceCheckFailed);
   } else {
     // ------------------------------------------------------------- softmax
     const int q = warp & 3;
@@ -1168,7 +1315,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
             const float p0 = ex2(fmaf(sv[2 * j], sl2, neg_m));
             const float p1 = ex2(fmaf(sv[2 * j + 1], sl2, neg_m));
             ps4[j & 3] += p0 + p1;
-            pk[j] = pack_bf16(p0, p1);
+            pk[j] = pack_p<MODE>(p0, p1);
           }
         } else {
 #pragma unroll
@@ -1178,7 +1325,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
             p0 = ((mask >> (2 * j)) & 1ull) ? p0 : 0.f;
             p1 = ((mask >> (2 * j + 1)) & 1ull) ? p1 : 0.f;
             ps4[j & 3] += p0 + p1;
-            pk[j] = pack_bf16(p0, p1);
+            pk[j] = pack_p<MODE>(p0, p1);
           }
         }
         l += (ps4[0] + ps4[1]) + (ps4[2] + ps4[3]);
@@ -1331,7 +1478,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         // columns are idle; no partial of this token is in TMEM
         // (a time-out inside has set the abort flag; the threads go on to the teardown)
         bool merged = true;
-        if constexpr (MODE == kLoadFp8) {
+        if constexpr (C::kCoded) {
           if (row < H) merge_split_token(a, pend_t, pend_tp, kf, kl, slot_kf, rank, row, lat_x0, LC, C::NSLOT, tslot);
         } else {
           merged = merge_in_tmem<LC>(a, cs, pend_t, pend_tp, -1, kf, kl, slot_kf, rank, row, lat_x0, trow,
@@ -1469,7 +1616,8 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
   using C = Cfg<LC, CL, MODE>;
   constexpr CUtensorMapDataType kBF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int L = a.d.kv_lora_rank, R = a.d.qk_rope, KQ = L + R, ps = a.d.page_size;
-  const uint32_t rows = MODE == kLoadSparse ? 1u : (uint32_t)(ps < kTileKeys ? ps : kTileKeys);
+  constexpr int kMaxLoadRows = MODE == kLoadFp4 ? kTileKeys / 2 : kTileKeys;
+  const uint32_t rows = MODE == kLoadSparse ? 1u : (uint32_t)(ps < kMaxLoadRows ? ps : kMaxLoadRows);
   const uint64_t pool_rows = (uint64_t)a.d.num_pages * ps;
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return cudaErrorInvalidDevice;
@@ -1490,6 +1638,12 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
     if (MODE == kLoadFp8) {
       const uint64_t rb = (uint64_t)L + 2 * R;   // bytes per cached row
       ok = encode_2d(&maps.kv_lat, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.kv_pool, rb, pool_rows, rb, C::RW, rows,
+                     CU_TENSOR_MAP_SWIZZLE_NONE) &&
+           encode_2d(&maps.kv_rope, kBF16, a.kv_pool, rb / 2, pool_rows, rb, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B);
+    } else if (MODE == kLoadFp4) {
+      // code and scale bytes as 16-bit elements (a box is at most 256 elements wide)
+      const uint64_t rb = C::kRow4 + 2ull * R;
+      ok = encode_2d(&maps.kv_lat, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.kv_pool, rb / 2, pool_rows, rb, C::kRow4 / 2, rows,
                      CU_TENSOR_MAP_SWIZZLE_NONE) &&
            encode_2d(&maps.kv_rope, kBF16, a.kv_pool, rb / 2, pool_rows, rb, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B);
     } else {
@@ -1561,7 +1715,7 @@ int max_active_clusters() {
 template <int MODE>
 cudaError_t launch_mode(const DecodeArgs& a, cudaStream_t s) {
   if (a.d.kv_lora_rank == 512) {
-    if constexpr (MODE != kLoadFp8) {
+    if constexpr (MODE == kLoadDense || MODE == kLoadSparse) {
       if (a.fold) return launch<256, 4, MODE>(a, s);
     }
     return launch<256, 2, MODE>(a, s);
@@ -1574,23 +1728,25 @@ cudaError_t launch_mode(const DecodeArgs& a, cudaStream_t s) {
 // Shapes with a tensor-core instance: (L, R) = (512, 64) on a 2-CTA cluster,
 // and L = 64 with R <= 32 on one CTA; qk_nope and v_head multiples of 8, v_head <= 512;
 // dense pages of 8..64 tokens or a multiple of 64.
-int decode_default_partitions(const mla_dims_t& d, bool fold, bool fp8_cache, bool sparse) {
+int decode_default_partitions(const mla_dims_t& d, bool fold, KVFmt fmt, bool sparse) {
   if (d.kv_lora_rank != 512) {
     if (sparse) return tc::max_active_clusters<64, 1, tc::kLoadSparse>();
-    if (fp8_cache) return tc::max_active_clusters<64, 1, tc::kLoadFp8>();
+    if (fmt == KVFmt::kE4M3) return tc::max_active_clusters<64, 1, tc::kLoadFp8>();
+    if (fmt == KVFmt::kE2M1) return tc::max_active_clusters<64, 1, tc::kLoadFp4>();
     return tc::max_active_clusters<64, 1, tc::kLoadDense>();
   }
-  if (fold && !fp8_cache) {
+  if (fold && fmt == KVFmt::kBF16) {
     if (sparse) return tc::max_active_clusters<256, 4, tc::kLoadSparse>();
     return tc::max_active_clusters<256, 4, tc::kLoadDense>();
   }
   if (sparse) return tc::max_active_clusters<256, 2, tc::kLoadSparse>();
-  if (fp8_cache) return tc::max_active_clusters<256, 2, tc::kLoadFp8>();
+  if (fmt == KVFmt::kE2M1) return tc::max_active_clusters<256, 2, tc::kLoadFp4>();
+  if (fmt == KVFmt::kE4M3) return tc::max_active_clusters<256, 2, tc::kLoadFp8>();
   return tc::max_active_clusters<256, 2, tc::kLoadDense>();
 }
 
-bool decode_fold_supported(const mla_dims_t& d, bool fp8_cache) {
-  return d.kv_lora_rank == 512 && d.qk_rope == 64 && !fp8_cache;
+bool decode_fold_supported(const mla_dims_t& d, KVFmt fmt) {
+  return d.kv_lora_rank == 512 && d.qk_rope == 64 && fmt == KVFmt::kBF16;
 }
 
 bool decode_tc_supported(const mla_dims_t& d) {
@@ -1613,6 +1769,7 @@ cudaError_t launch_wait_selftest(PlanHeader* hdr, uint64_t limit_ns, cudaStream_
 cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t s) {
   if (a.ks.indices) return tc::launch_mode<tc::kLoadSparse>(a, s);
   if (a.kv_fmt == KVFmt::kE4M3) return tc::launch_mode<tc::kLoadFp8>(a, s);
+  if (a.kv_fmt == KVFmt::kE2M1) return tc::launch_mode<tc::kLoadFp4>(a, s);
   return tc::launch_mode<tc::kLoadDense>(a, s);
 }
 

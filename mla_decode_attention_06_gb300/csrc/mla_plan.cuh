@@ -24,6 +24,7 @@ struct PlanInputs {
   float* lse_ws;             // [T, H]:    -inf for tokens without keys
   int H, L;
   bool fold;                 // pair consecutive tokens of a request (they share tiles)
+  bool keep_status;          // blocks beside the plan report too: the host clears the status word
 };
 
 // Key range [lo, hi) of the query at position pos of request b with cache_len len.
@@ -42,7 +43,7 @@ __device__ __forceinline__ void plan_block(const PlanInputs& in) {
   const int tid = threadIdx.x, nthr = blockDim.x;
   if (tid == 0) {
     any_bad = 0;
-    atomicExch(&in.hdr->status, 0);   // the plan runs first in every call
+    if (!in.keep_status) atomicExch(&in.hdr->status, 0);   // the plan runs first in every call
     in.hdr->pad[0] = 0;               // time-out record
     in.hdr->pad[1] = 0;
   }

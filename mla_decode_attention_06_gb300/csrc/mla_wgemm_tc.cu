@@ -59,6 +59,7 @@ struct Args {
   const float* wscale; // e4m3 block scales [H, ceil(M/128), ceil(K/128)]
   // absorb
   __nv_bfloat16* q_full; int KQ, L, R, N; const __nv_bfloat16* q;
+  bool half;           // q_full holds f16 (the operands of the e2m1 decode); what f16 does not reach is reported
   // W_uv
   __nv_bfloat16* out; int V; const float* lse_ws; float* lse_out;
   PlanHeader* hdr;
@@ -84,6 +85,25 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint16_t two) {
   const float2 f = __half22float2(__half2(h));
   return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(f.x)) |
          ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(f.y)) << 16);
+}
+
+// The bits of v rounded to f16, in the 16-bit type of the staging tile.
+__device__ __forceinline__ __nv_bfloat16 f16_in_bf16(float v) {
+  return __ushort_as_bfloat16(__half_as_ushort(__float2half_rn(v)));
+}
+// Eight bf16 values as f16; finite ones that become infinite are reported.
+__device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v, PlanHeader* hdr) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool over = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x = __uint_as_float(w[i] << 16), y = __uint_as_float(w[i] & 0xFFFF0000u);
+    over |= (fabsf(x) >= 65520.f && fabsf(x) < CUDART_INF_F) || (fabsf(y) >= 65520.f && fabsf(y) < CUDART_INF_F);
+    const __half2 h = __floats2half2_rn(x, y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  if (over) atomicOr(&hdr->status, kDeviceCheckFailed);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <bool kFp8>
@@ -209,8 +229,10 @@ __global__ void __launch_bounds__(kThreads, 1) wgemm_kernel(const __grid_constan
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         const int i = i0 + j * stride, t = t0 + i / cpr;
-        if (i < TN * cpr && t < a.T)
+        if (i < TN * cpr && t < a.T) {
+          if (a.half) v[j] = bf16x8_to_f16x8(v[j], a.hdr);
           reinterpret_cast<uint4*>(a.q_full + ((size_t)t * kMaxHeads + h) * a.KQ + a.L)[i % cpr] = v[j];
+        }
       }
     }
     if (h == 0 && a.H < kMaxHeads) {
@@ -311,7 +333,14 @@ __global__ void __launch_bounds__(kThreads, 1) wgemm_kernel(const __grid_constan
       }
 #pragma unroll
       for (int q = 0; q < 32; ++q)
-        if (j0 + q < TN) stg[((size_t)i * TN + j0 + q) * 128 + row] = __float2bfloat16_rn(v[q]);
+        if (j0 + q < TN) stg[((size_t)i * TN + j0 + q) * 128 + row] = a.half ? f16_in_bf16(v[q]) : __float2bfloat16_rn(v[q]);
+      if (a.half) {
+        // columns past the last token hold zeros
+        bool over = false;
+#pragma unroll
+        for (int q = 0; q < 32; ++q) over |= fabsf(v[q]) >= 65520.f && fabsf(v[q]) < CUDART_INF_F;
+        if (over) atomicOr(&a.hdr->status, kDeviceCheckFailed);
+      }
     }
   }
   __syncthreads();
@@ -465,9 +494,10 @@ cudaError_t launch(const Args& a0, WFmt wf, const void* w, const void* x, int Kx
 
 cudaError_t launch_absorb_tc(const mla_dims_t& d, int T, const __nv_bfloat16* q, WFmt wf, const void* w_uk,
                              const float* w_uk_scale, __nv_bfloat16* q_full, PlanHeader* hdr,
-                             const PlanInputs& plan, cudaStream_t s) {
+                             const PlanInputs& plan, bool half, cudaStream_t s) {
   wg::Args a{};
   a.mode = 0;
+  a.half = half;
   a.H = d.num_heads;
   a.T = T;
   a.M = d.kv_lora_rank;

@@ -1,0 +1,207 @@
+"""GPU: mla_decode_paged_fp4 (e2m1 latent cache) against the fp64 oracle on the values that its
+rows stand for.
+
+Tolerances, as relative 2-norms over the output.  A rounding to t bits is off by at most
+u = eps / 2 of the value and u / sqrt(3) rms at worst (a value at the low end of its binade):
+2.3e-3 for bf16, 2.8e-4 for f16.  The codes times their scales are exact in f16.  The latent
+output and the output are rounded to bf16, independently: sqrt(2) * 2.3e-3 = 3.2e-3; P, the
+absorbed query and the rope part are rounded to f16, the last two with the spread of the scores
+(about 2) as their factor: 2.8e-4 * sqrt(1 + 2 * 4) = 8e-4.  Together at most 4.0e-3.  The
+log-sum-exp moves by the scores' error: two roundings of at most 2^-11 of scores up to 8: 8e-3.
+The bf16 decode of the same values has 2.3e-3 * sqrt(3 + 4) = 6.1e-3 of its own.
+"""
+TOL, TOL_LSE, TOL_BF16 = 4.0e-3, 8e-3, 6.1e-3
+
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+import latent_ref as ref
+import oracle
+from workloads import mla as W
+from workloads.run import device_inputs, run_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from mla_decode_attention_06_gb300 import build
+    build.build()
+    return torch.device("cuda:0")
+
+
+def coded(p):
+    """A bf16 problem -> (the same with its rows rounded to e2m1 values, their row bytes)."""
+    live = ~np.isnan(ref.bf16_values(p.rows_bf16)).any(1)
+    rows = np.full((len(live), -(-(p.L // 2 + p.L // 32) // 16) * 16 + 2 * p.R), 0xFF, np.uint8)   # dead rows: NaN
+    rows[live], _ = ref.encode(p.rows_bf16[live, :p.L], p.rows_bf16[live, p.L:], ref.E2M1)
+    values = p.rows_bf16.copy()
+    values[live] = ref.bf16_bits(ref.decode(rows[live], None, ref.E2M1, p.L, p.R))
+    return dataclasses.replace(p, rows_bf16=values), rows
+
+
+def run_fp4(p, rows, d, **kw):
+    import mla_decode_attention_06_gb300 as M
+    pool = torch.full((p.pool_rows, rows.shape[1]), 0xFF, dtype=torch.uint8, device=d["q"].device)
+    pool[torch.from_numpy(p.rows_phys).to(pool.device)] = torch.from_numpy(rows).to(pool.device)
+    lse = torch.empty(p.T, p.H, device=pool.device)
+    kw = dict(dict(debug=True), **kw)
+    return M.mla_decode_paged_fp4(d["q"], d["offsets"], pool, d["block_table"], d["cache_lens"], d["w_uk"], d["w_uv"],
+                                  page_size=p.ps, scale=p.scale, mask=p.mask, window=p.window, lse_out=lse, **kw)
+
+
+def check(p, dev, num_splits=0, oracle_too=True):
+    p, rows = coded(p)
+    d = device_inputs(p, dev)
+    out, lse = run_fp4(p, rows, d, num_splits=num_splits)
+    want, want_lse = run_gpu(p, d, num_splits=num_splits, debug=True, fold_pairs=False)
+    assert (out.float() - want.float()).norm() <= (TOL + TOL_BF16) * want.float().norm()
+    if oracle_too:
+        o, l = oracle.decode(p)
+        g = out.float().cpu().numpy().astype(np.float64)
+        assert np.isfinite(g).all()
+        rel = np.linalg.norm(g - o) / np.linalg.norm(o)
+        assert rel <= TOL, rel
+        fin = np.isfinite(l)
+        lg = lse.cpu().numpy()
+        assert np.array_equal(np.isfinite(lg), fin) and np.abs(lg[fin] - l[fin]).max() <= TOL_LSE
+    return out
+
+
+def wide(seed, lens, **kw):
+    return W.make_dense("fp4", seed, **dict(dict(W.DSV3, ps=64, cache_lens=lens, rms_norm=True,
+                                                num_pages=sum(-(-n // 8) for n in lens) + 5), **kw))
+
+
+def narrow(seed, lens, **kw):
+    return W.make_dense("fp4n", seed, **dict(dict(H=4, N=32, R=16, L=64, V=32, ps=16, cache_lens=lens,
+                                                 num_pages=sum(-(-n // 8) for n in lens) + 5), **kw))
+
+
+@pytest.mark.parametrize("num_splits", [0, 1, 5])
+@pytest.mark.parametrize("make", [wide, narrow])
+def test_ragged(dev, make, num_splits):
+    check(make(31, (1, 63, 64, 65, 200, 777)), dev, num_splits)
+
+
+@pytest.mark.parametrize("ps", [8, 16, 32, 64, 128])
+@pytest.mark.parametrize("make", [wide, narrow])
+def test_page_sizes(dev, make, ps):
+    check(make(32, (5, 130, 301), ps=ps), dev)
+
+
+@pytest.mark.parametrize("mask,window", [(W.MASK_NULL, 0), (W.MASK_SLIDING_WINDOW_CAUSAL, 1),
+                                         (W.MASK_SLIDING_WINDOW_CAUSAL, 100)])
+def test_masks_and_several_tokens(dev, mask, window):
+    check(wide(33, (3, 150, 400), qlens=(3, 2, 1), mask=mask, window=window), dev, 3)
+
+
+@pytest.mark.parametrize("heads", [1, 17, 127])
+def test_heads(dev, heads):
+    check(wide(34, (70, 400), H=heads), dev)
+
+
+def test_scales_of_every_size(dev):
+    # groups from 2^-23 to 2^13 beside each other: every scale whose products f16 holds exactly
+    p = wide(35, (90, 300))
+    r = np.random.default_rng(5)
+    v = ref.bf16_values(p.rows_bf16)
+    v[:, :p.L] *= np.exp2(np.repeat(r.integers(-22, 13, (len(v), p.L // 32)), 32, 1))
+    p = dataclasses.replace(p, rows_bf16=np.where(np.isnan(v), np.uint16(0xFFFF), ref.bf16_bits(np.nan_to_num(v))), scale=1e-5)
+    check(p, dev, 2)
+
+
+@pytest.mark.parametrize("what", ["scale", "rope", "query", "absorbed"])
+def test_magnitudes_past_f16_are_reported(dev, what):
+    # the products take f16 operands: what they cannot hold makes NaN, never a quiet wrong value
+    import mla_decode_attention_06_gb300 as M
+    p, rows = coded(narrow(41, (40, 50)))
+    d = device_inputs(p, dev)
+    if what == "scale":
+        hit = int(np.flatnonzero(p.rows_phys == int(p.block_table[0, 1]) * p.ps + 3)[0])
+        rows[hit, p.L // 2] = 141
+        rows[hit, :16] = 0x77                                # 6 * 2^14
+    elif what == "rope":
+        hit = int(np.flatnonzero(p.rows_phys == int(p.block_table[0, 1]) * p.ps + 3)[0])
+        rows[hit, -2 * p.R:][:2] = np.array([0x4780], np.uint16).view(np.uint8)   # 65536
+    elif what == "query":
+        d["q"][0, 1, p.N + 3] = 65536.0
+    else:
+        d["w_uk"][1] *= 2.0 ** 20
+    with pytest.raises(M.MlaError) as e:
+        run_fp4(p, rows, d)
+    assert e.value.code == 5
+    out, _ = run_fp4(p, rows, d, debug=False)
+    if what == "rope":
+        # a score of +inf makes NaN; one of -inf drops its key, as 65536 times that query would
+        up = d["q"][0, :, p.N].float() > 0
+        assert torch.isnan(out[0][up].float()).all() and torch.isfinite(out[0][~up].float()).all()
+    else:
+        bad = {"scale": out[0], "query": out[0, 1], "absorbed": out[:, 1]}[what]
+        assert torch.isnan(bad.float()).all()
+    assert torch.isfinite(out[1, 0].float()).all()
+
+
+def test_infinite_and_nan_scales_in_dead_rows(dev):
+    # rows behind a request's end may hold any bytes
+    p, rows = coded(narrow(42, (20, 33)))
+    want, _ = run_fp4(p, rows, device_inputs(p, dev))
+    for byte in (0x00, 0x7F, 0xFE):
+        other = rows.copy()
+        other[np.isnan(ref.bf16_values(p.rows_bf16)).any(1)] = byte
+        out, _ = run_fp4(p, other, device_inputs(p, dev))
+        assert torch.equal(out, want)
+
+
+def test_many_requests(dev):
+    lens = tuple(int(n) for n in np.random.default_rng(6).integers(1, 400, 90))
+    check(wide(36, lens), dev, oracle_too=False)
+
+
+def test_empty_rows_and_nan_garbage(dev):
+    # a request with fewer cached than query tokens is reported and gives 0 and -inf; dead rows
+    # of every page are NaN codes
+    import mla_decode_attention_06_gb300 as M
+    p, rows = coded(narrow(37, (20, 33)))
+    d = device_inputs(p, dev)
+    d["cache_lens"][1] = 0
+    with pytest.raises(M.MlaError) as e:
+        run_fp4(p, rows, d)
+    assert e.value.code == 5
+    out, lse = run_fp4(p, rows, d, debug=False)
+    assert (out[1] == 0).all() and torch.isneginf(lse[1]).all()
+    assert torch.isfinite(out.float()).all() and torch.isfinite(lse[0]).all()
+
+
+def test_nan_scale_reaches_the_output(dev):
+    p, rows = coded(narrow(38, (40, 50)))
+    hit = int(np.flatnonzero(p.rows_phys == int(p.block_table[0, 1]) * p.ps + 3)[0])
+    rows[hit, p.L // 2] = 0xFF
+    out, _ = run_fp4(p, rows, device_inputs(p, dev))
+    assert torch.isnan(out[0].float()).all() and torch.isfinite(out[1].float()).all()
+
+
+def test_bad_page_is_reported(dev):
+    import mla_decode_attention_06_gb300 as M
+    p, rows = coded(narrow(39, (40, 50)))
+    d = device_inputs(p, dev)
+    d["block_table"][1, 0] = p.num_pages
+    with pytest.raises(M.MlaError) as e:
+        run_fp4(p, rows, d)
+    assert e.value.code == 5
+
+
+def test_own_stream_without_workspace(dev):
+    p, rows = coded(wide(40, (200, 90)))
+    d = device_inputs(p, dev)
+    want, _ = run_fp4(p, rows, d)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    out, _ = run_fp4(p, rows, d, stream=s, debug=False)
+    s.synchronize()
+    assert torch.equal(out, want)
