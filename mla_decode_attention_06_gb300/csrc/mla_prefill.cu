@@ -468,6 +468,12 @@ __device__ __forceinline__ bool all_of_128(int id, bool v) {
       : "memory");
   return r != 0;
 }
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r)::"memory");
+  return r != 0;
+}
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
@@ -553,23 +559,26 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
         mbar_wait(&cs->full[j % kExpStages], (j / kExpStages) & 1, kWaitLimitNs);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t type = in_f16 ? kBf16Operands : 0u;
-      const uint32_t id_k = idesc_bf16_f32(128, 64 * a.nbk, false, true) ^ type;
-      const uint32_t id_v = idesc_bf16_f32(128, 64 * a.nbv, false, false) ^ type;
-      int c = 0, it = 0;
-      bool ok = true;
-      for (long long w = blockIdx.x; w < total && ok; w += gridDim.x, ++it) {
-        const uint32_t acc = tmem + 256 * (it & 1);
-        if (it >= 2 && !(ok = wait(&cs->acc_empty[it & 1], ((it >> 1) & 1) ^ 1, &cs->ctl, hdr))) break;
-        for (int kb = 0; kb < nkb; ++kb, ++c) {
-          const int s = c % kExpStages;
-          if (!(ok = wait(&cs->full[s], (c / kExpStages) & 1, &cs->ctl, hdr))) break;
-          tc_fence_after();
-          const uint32_t st = smem_u32(sm + s * kExpStageBytes);
-          const uint64_t da = smem_desc(st, 16, 1024, kLayoutSw128);
-          const uint64_t dk = smem_desc(st + kBox, kBox / 2, 1024, kLayoutSw128);
-          const uint64_t dv = smem_desc(st + 2 * kBox, 16, 1024, kLayoutSw128);
+    // The whole warp walks the loop and one lane issues: the descriptors then are warp-uniform
+    // values (in a single-lane loop each instruction first has to move them there).
+    const uint32_t type = in_f16 ? kBf16Operands : 0u;
+    const uint32_t id_k = idesc_bf16_f32(128, 64 * a.nbk, false, true) ^ type;
+    const uint32_t id_v = idesc_bf16_f32(128, 64 * a.nbv, false, false) ^ type;
+    const uint32_t base = smem_u32(sm);
+    int c = 0, it = 0;
+    bool ok = true;
+    for (long long w = blockIdx.x; w < total && ok; w += gridDim.x, ++it) {
+      const uint32_t acc = tmem + 256 * (it & 1);
+      if (it >= 2 && !(ok = wwait(&cs->acc_empty[it & 1], ((it >> 1) & 1) ^ 1, &cs->ctl, hdr))) break;
+      for (int kb = 0; kb < nkb; ++kb, ++c) {
+        const int s = c % kExpStages;
+        if (!(ok = wwait(&cs->full[s], (c / kExpStages) & 1, &cs->ctl, hdr))) break;
+        tc_fence_after();
+        const uint32_t st = base + s * kExpStageBytes;
+        const uint64_t da = smem_desc(st, 16, 1024, kLayoutSw128);
+        const uint64_t dk = smem_desc(st + kBox, kBox / 2, 1024, kLayoutSw128);
+        const uint64_t dv = smem_desc(st + 2 * kBox, 16, 1024, kLayoutSw128);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             mma_ss(acc, da + 2 * kk, dk + (uint64_t)((kk * 2048) >> 4), id_k, kb > 0 || kk > 0);
@@ -577,8 +586,10 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
           }
           mma_commit(&cs->empty[s]);
         }
-        if (ok) mma_commit(&cs->acc_full[it & 1]);
+        __syncwarp();
       }
+      if (ok && elect_one()) mma_commit(&cs->acc_full[it & 1]);
+      __syncwarp();
     }
     __syncwarp();
   } else {
@@ -648,10 +659,14 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
 // pairs over S) and O of A and B: all 512 columns.  One thread issues, per key tile,
 //   P.V of A (tile j), Q.K of A (j + 1), P.V of B (j), Q.K of B (j + 1)
 // so while the softmax warps of one sub-block work, the tensor core has the other's two
-// products.  Boxes of K (with the rope box) and V stream through an eight-box ring.
+// products.  K (with the rope box) and V stream through a ring of eight boxes, in which key
+// tile j has the five places from 5 j on (three for K, two for V): K of tile j lies where V
+// of tile j - 2 was, V of tile j where K of tile j - 1 was, so each needs one barrier to wait
+// for and the issuing thread one wait and one signal per product (a barrier per box cost it
+// as much time as the products: 1,586 us against 1,1xx at 16,384 tokens x 16 heads).
 // Warp 0 loads, warp 1 issues, warps 2-5 and 6-9 are the softmax of A and B: thread =
 // query token = TMEM lane.
-constexpr int kSlots = 8;
+constexpr int kSlots = 8, kSlotsPerTile = 5, kVSlot = 3;   // ring boxes; places of a key tile, its V from
 constexpr int kAttThreads = 320;
 constexpr float kRescaleThreshold = 8.0f;   // log2: O is rescaled when a row's maximum grows by more than 2^8
 
@@ -663,7 +678,7 @@ struct Block {
   int j0[2], j1[2], js, je;   // key tiles of each sub-block, and of both
 };
 struct AttSmem {
-  uint64_t full[kSlots], empty[kSlots], q_full, q_ready[2], s_full[2], p_full[2], o_full[2];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full, q_ready[2], s_full[2], p_full[2], o_full[2];
   Ctl ctl;
   Block blk;
 };
@@ -754,12 +769,12 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
   for (long long at = blockIdx.x; at < nblocks; at += gridDim.x) {
   if ((int)(at / a.splits % a.max_items) >= nitems) continue;
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&cs->full[i], 1);
-      mbar_init(&cs->empty[i], 1);
-    }
     mbar_init(&cs->q_full, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&cs->k_full[i], 1);
+      mbar_init(&cs->k_empty[i], 1);
+      mbar_init(&cs->v_full[i], 1);
+      mbar_init(&cs->v_empty[i], 1);
       mbar_init(&cs->q_ready[i], 128);
       mbar_init(&cs->s_full[i], 1);
       mbar_init(&cs->p_full[i], 128);
@@ -774,7 +789,6 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
   const uint32_t tmem = cs->ctl.tmem_base;
   const Block& blk = cs->blk;
 
-  const int per = a.nbq + a.nbv;   // boxes per key tile
   if (warp == 0) {
     const int js = blk.js, je = blk.je, nsub = blk.nsub, t0 = blk.q.q0 + blk.r0, h = blk.h, tile0 = blk.q.tile0;
     if (lane == 0 && je > js) {
@@ -786,99 +800,118 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
           if (i < a.nbk) tma_load_3d(dst, &maps.qn, &cs->q_full, 64 * i, a.h0 + h, t);
           else tma_load_3d(dst, &maps.qr, &cs->q_full, 0, a.h0 + h, t);
         }
-      int c = 0;
       bool ok = true;
-      const uint8_t* kv = a.kv + ((size_t)h * a.cap_tiles + tile0) * (a.nbk + a.nbv) * kBox;
-      for (int j = js; j < je && ok; ++j)
-        for (int i = 0; i < per; ++i, ++c) {
-          const int s = c % kSlots;
-          if (c >= kSlots && !(ok = wait(&cs->empty[s], ((c / kSlots) & 1) ^ 1, &cs->ctl, hdr))) break;
-          const uint8_t* src = i == a.nbk ? a.rope + (size_t)(tile0 + j) * kBox
-                                          : kv + ((size_t)j * (a.nbk + a.nbv) + (i < a.nbk ? i : i - 1)) * kBox;
-          mbar_arrive_expect_tx(&cs->full[s], kBox);
-          bulk_copy_g2s(ring + s * kBox, src, kBox, &cs->full[s]);
+      const int nb = a.nbk + a.nbv;
+      const uint8_t* kv = a.kv + ((size_t)h * a.cap_tiles + tile0) * nb * kBox;
+      auto place = [&](int n, int i) { return ring + ((kSlotsPerTile * n + i) % kSlots) * kBox; };
+      int n = 0;   // key tiles loaded
+      for (int j = js; j < je && ok; ++j, ++n) {
+        const int b = n & 1;
+        const uint8_t* src = kv + (size_t)j * nb * kBox;
+        if (n >= 2 && !(ok = wait(&cs->v_empty[b], ((n - 2) >> 1) & 1, &cs->ctl, hdr))) break;
+        mbar_arrive_expect_tx(&cs->k_full[b], (uint32_t)(a.nbq * kBox));
+        for (int i = 0; i < a.nbk; ++i) bulk_copy_g2s(place(n, i), src + (size_t)i * kBox, kBox, &cs->k_full[b]);
+        bulk_copy_g2s(place(n, a.nbk), a.rope + (size_t)(tile0 + j) * kBox, kBox, &cs->k_full[b]);
+        if (n >= 1 && !(ok = wait(&cs->k_empty[b ^ 1], ((n - 1) >> 1) & 1, &cs->ctl, hdr))) {
+          mbar_wait(&cs->k_full[b], (n >> 1) & 1, kWaitLimitNs);
+          break;
         }
-      for (int j = c > kSlots ? c - kSlots : 0; j < c; ++j)   // nothing in flight when the CTA leaves
-        mbar_wait(&cs->full[j % kSlots], (j / kSlots) & 1, kWaitLimitNs);
+        mbar_arrive_expect_tx(&cs->v_full[b], (uint32_t)(a.nbv * kBox));
+        for (int i = 0; i < a.nbv; ++i)
+          bulk_copy_g2s(place(n, kVSlot + i), src + (size_t)(a.nbk + i) * kBox, kBox, &cs->v_full[b]);
+      }
+      for (int i = n > 2 ? n - 2 : 0; i < n; ++i) {   // nothing in flight when the CTA leaves
+        mbar_wait(&cs->k_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
+        mbar_wait(&cs->v_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
+      }
       mbar_wait(&cs->q_full, 0, kWaitLimitNs);
     }
     __syncwarp();
   } else if (warp == 1) {
     const int js = blk.js, je = blk.je;
-    const int j0[2] = {blk.j0[0], blk.j0[1]}, j1[2] = {blk.j1[0], blk.j1[1]};
-    if (lane == 0 && je > js) {
+    const int ja0 = blk.j0[0], ja1 = blk.j1[0], jb0 = blk.j0[1], jb1 = blk.j1[1];
+    if (je > js) {
+      // the whole warp walks the loop, one lane issues (as in the expansion)
       const uint32_t type = kHalf ? kBf16Operands : 0u;
       const uint32_t id_s = idesc_bf16_f32(128, 128, false, false) ^ type;
       const uint32_t id_o = idesc_bf16_f32(128, 64 * a.nbv, false, true) ^ type;
       const uint32_t id_o1 = idesc_bf16_f32(128, 64, false, true) ^ type;
-      const uint32_t base_q = smem_u32(sQ), base_r = smem_u32(ring);
-      auto steps = [&](int i) {   // 16-column steps of query box i that hold anything
-        const int n = i < a.nbk ? a.d.qk_nope - 64 * i : a.d.qk_rope;
-        return min(4, (n + 15) / 16);
-      };
-      auto qk = [&](int s, int c) {   // S of sub-block s = Q K^T, K in ring boxes from count c on
-        for (int i = 0; i < a.nbq; ++i) {
-          if (!wait(&cs->full[(c + i) % kSlots], ((c + i) / kSlots) & 1, &cs->ctl, hdr)) return false;
-          if (i == 0) tc_fence_after();
-          const uint64_t dq = smem_desc(base_q + (s * a.nbq + i) * kBox, 16, 1024, kLayoutSw128);
-          const uint64_t dk = smem_desc(base_r + ((c + i) % kSlots) * kBox, 16, 1024, kLayoutSw128);
-          const int n = steps(i);
-          for (int kk = 0; kk < n; ++kk) mma_ss(tmem + 128 * s, dq + 2 * kk, dk + 2 * kk, id_s, i > 0 || kk > 0);
+      const uint64_t dq0 = smem_desc(smem_u32(sQ), 16, 1024, kLayoutSw128);
+      const uint64_t dk0 = smem_desc(smem_u32(ring), 16, 1024, kLayoutSw128);
+      const uint64_t dv0 = smem_desc(smem_u32(ring), kBox, 1024, kLayoutSw128);
+      constexpr uint64_t kBoxStep = kBox >> 4;
+      const int nbq = a.nbq, nbv = a.nbv;
+      // S of sub-block s = Q K^T for the n-th key tile; `first`: K is waited for
+      auto qk = [&](int s, int n, bool first) {
+        if (first) {
+          if (!wwait(&cs->k_full[n & 1], (n >> 1) & 1, &cs->ctl, hdr)) return false;
+          tc_fence_after();
         }
-        mma_commit(&cs->s_full[s]);
+        if (elect_one()) {
+          for (int i = 0; i < nbq; ++i) {
+            // columns past the row's end are zero on both sides
+            const uint64_t dq = dq0 + (s * nbq + i) * kBoxStep, dk = dk0 + ((kSlotsPerTile * n + i) % kSlots) * kBoxStep;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mma_ss(tmem + 128 * s, dq + 2 * kk, dk + 2 * kk, id_s, i > 0 || kk > 0);
+          }
+          mma_commit(&cs->s_full[s]);
+        }
+        __syncwarp();
         return true;
       };
-      auto pv = [&](int s, int c, bool add) {   // O of sub-block s (+)= P V
-        for (int i = 0; i < a.nbv; ++i)
-          if (!wait(&cs->full[(c + i) % kSlots], ((c + i) / kSlots) & 1, &cs->ctl, hdr)) return false;
+      // O of sub-block s (+)= P V for the n-th key tile, once the softmax has left P (its np-th)
+      auto pv = [&](int s, int n, int np, bool first, bool last) {
+        if (first && !wwait(&cs->v_full[n & 1], (n >> 1) & 1, &cs->ctl, hdr)) return false;
+        if (!wwait(&cs->p_full[s], np & 1, &cs->ctl, hdr)) return false;
         tc_fence_after();
         const uint32_t o = tmem + 256 + 128 * s, p = tmem + 128 * s;
-        const int s0 = c % kSlots;
-        if (a.nbv == 1 || s0 + 1 < kSlots) {
-          const uint64_t dv = smem_desc(base_r + s0 * kBox, kBox, 1024, kLayoutSw128);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(o, p + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4), id_o, add || kk > 0);
-        } else {   // the two boxes lie at the ring's end and start: one product for each
-          for (int i = 0; i < 2; ++i) {
-            const uint64_t dv = smem_desc(base_r + ((c + i) % kSlots) * kBox, kBox, 1024, kLayoutSw128);
+        const int s0 = (kSlotsPerTile * n + kVSlot) % kSlots;
+        const uint64_t dv = dv0 + s0 * kBoxStep;
+        if (elect_one()) {
+          if (nbv == 1 || s0 + 1 < kSlots) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_ts(o + 64 * i, p + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4), id_o1, add || kk > 0);
+              mma_ts(o, p + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4), id_o, np > 0 || kk > 0);
+          } else {   // the two boxes lie at the ring's end and start: one product for each
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) mma_ts(o, p + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4), id_o1, np > 0 || kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts(o + 64, p + 8 * kk, dv0 + (uint64_t)((kk * 2048) >> 4), id_o1, np > 0 || kk > 0);
           }
+          if (last) mma_commit(&cs->o_full[s]);
         }
+        __syncwarp();
         return true;
       };
-      bool ok = true;
-      int np[2] = {0, 0};   // P tiles taken
-      auto release = [&](int c, int n) {
-        for (int i = 0; i < n; ++i) mma_commit(&cs->empty[(c + i) % kSlots]);
+      auto release = [&](uint64_t* bar) {
+        if (elect_one()) mma_commit(bar);
+        __syncwarp();
       };
-      for (int s = 0; s < 2 && ok; ++s)
-        if (j1[s] > j0[s]) {
-          ok = wait(&cs->q_ready[s], 0, &cs->ctl, hdr);
-          if (ok && js == j0[s]) ok = qk(s, 0);
-        }
-      if (ok) release(0, a.nbq);
-      for (int j = js; j < je && ok; ++j) {
-        const int c = (j - js) * per;
-        for (int s = 0; s < 2 && ok; ++s) {
-          if (j >= j0[s] && j < j1[s]) {
-            ok = wait(&cs->p_full[s], np[s] & 1, &cs->ctl, hdr);
-            ok = ok && pv(s, c + a.nbq, np[s] > 0);
-            ++np[s];
-            if (ok && j + 1 == j1[s]) mma_commit(&cs->o_full[s]);
-          }
-          if (s == 1 && ok) release(c + a.nbq, a.nbv);
-          if (ok && j + 1 >= j0[s] && j + 1 < j1[s]) ok = qk(s, c + per);
-          if (s == 1 && ok && j + 1 < je) release(c + per, a.nbq);
-        }
+      bool ok = true;
+      int np0 = 0, np1 = 0;   // P tiles taken
+      const bool a_on = ja1 > ja0, b_on = jb1 > jb0;
+      if (a_on) ok = wwait(&cs->q_ready[0], 0, &cs->ctl, hdr);
+      if (ok && b_on) ok = wwait(&cs->q_ready[1], 0, &cs->ctl, hdr);
+      const bool a_first = a_on && js == ja0;
+      if (ok && a_first) ok = qk(0, 0, true);
+      if (ok && b_on && js == jb0) ok = qk(1, 0, !a_first);
+      if (ok) release(&cs->k_empty[0]);
+      int n = 0;
+      for (int j = js; j < je && ok; ++j, ++n) {
+        // a sub-block's last tile leaves the other alone with the tensor core
+        const bool a_now = j >= ja0 && j < ja1, b_now = j >= jb0 && j < jb1;
+        const bool a_next = j + 1 >= ja0 && j + 1 < ja1, b_next = j + 1 >= jb0 && j + 1 < jb1;
+        if (a_now) ok = pv(0, n, np0++, true, j + 1 == ja1);
+        if (ok && a_next) ok = qk(0, n + 1, true);
+        if (ok && b_now) ok = pv(1, n, np1++, !a_now, j + 1 == jb1);
+        if (ok) release(&cs->v_empty[n & 1]);
+        if (ok && b_next) ok = qk(1, n + 1, !a_next);
+        if (ok && j + 1 < je) release(&cs->k_empty[(n + 1) & 1]);
       }
       // the last signal has arrived before the barriers go away
-      const int last = (je - js) * per - 1;
-      if (ok) wait(&cs->empty[last % kSlots], (last / kSlots) & 1, &cs->ctl, hdr);
+      if (ok) wwait(&cs->v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, &cs->ctl, hdr);
     }
-    __syncwarp();
   } else {
     const int s = warp >= 6 ? 1 : 0;
     const int quad = warp & 3, row = 32 * quad + lane;
