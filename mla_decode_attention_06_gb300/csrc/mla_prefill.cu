@@ -664,10 +664,12 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
 // of tile j - 2 was, V of tile j where K of tile j - 1 was, so each needs one barrier to wait
 // for and the issuing thread one wait and one signal per product (a barrier per box cost it
 // as much time as the products: 1,586 us against 1,1xx at 16,384 tokens x 16 heads).
-// Warp 0 loads, warp 1 issues, warps 2-5 and 6-9 are the softmax of A and B: thread =
-// query token = TMEM lane.
+// Warp 0 loads, warp 1 issues, warps 4-7 and 8-11 are the softmax of A and B: thread =
+// query token = TMEM lane.  A softmax thread holds a row of 128 scores: the 168 registers
+// that 384 threads get at launch are split 104 / 200 between the warpgroups (384 x 168 =
+// 128 x 104 + 256 x 200).
 constexpr int kSlots = 8, kSlotsPerTile = 5, kVSlot = 3;   // ring boxes; places of a key tile, its V from
-constexpr int kAttThreads = 320;
+constexpr int kAttThreads = 384;
 constexpr float kRescaleThreshold = 8.0f;   // log2: O is rescaled when a row's maximum grows by more than 2^8
 
 // What a CTA works on: kept in shared memory, read where it is used (the softmax threads
@@ -789,6 +791,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
   const uint32_t tmem = cs->ctl.tmem_base;
   const Block& blk = cs->blk;
 
+  if (kHalf && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == 0) {
     const int js = blk.js, je = blk.je, nsub = blk.nsub, t0 = blk.q.q0 + blk.r0, h = blk.h, tile0 = blk.q.tile0;
     if (lane == 0 && je > js) {
@@ -912,8 +915,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
       // the last signal has arrived before the barriers go away
       if (ok) wwait(&cs->v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, &cs->ctl, hdr);
     }
-  } else {
-    const int s = warp >= 6 ? 1 : 0;
+  } else if (warp >= 4) {
+    if (kHalf) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");   // once: this instance has one block a CTA
+    const int s = warp >= 8 ? 1 : 0;
     const int quad = warp & 3, row = 32 * quad + lane;
     const uint32_t trow = tmem + ((uint32_t)(32 * quad) << 16), ts = trow + 128 * s, to = trow + 256 + 128 * s;
     const int ja = blk.j0[s], jb = blk.j1[s];
