@@ -656,15 +656,16 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
 
 // One CTA: 256 query tokens of a request (two sub-blocks A and B of 128) for one head,
 // over a range of its key tiles.  TMEM holds S of A and B (128 columns each, P as bf16
-// pairs over S) and O of A and B: all 512 columns.  One thread issues, per key tile,
-//   P.V of A (tile j), Q.K of A (j + 1), P.V of B (j), Q.K of B (j + 1)
-// so while the softmax warps of one sub-block work, the tensor core has the other's two
-// products.  K (with the rope box) and V stream through a ring of eight boxes, in which key
-// tile j has the five places from 5 j on (three for K, two for V): K of tile j lies where V
-// of tile j - 2 was, V of tile j where K of tile j - 1 was, so each needs one barrier to wait
-// for and the issuing thread one wait and one signal per product (a barrier per box cost it
-// as much time as the products: 1,586 us against 1,1xx at 16,384 tokens x 16 heads).
-// Warp 0 loads, warp 1 issues, warps 4-7 and 8-11 are the softmax of A and B: thread =
+// pairs over S) and O of A and B: all 512 columns.  Per sub-block and key tile the tensor
+// core does P.V of tile j, then Q.K of tile j + 1 into the same S; while the softmax warps
+// of one sub-block work, it has the other's two products.  Each sub-block has an issuing
+// warp of its own: the tensor core's queue is a few instructions deep, so a single one left
+// it idle during each of its waits (150 cycles even for a barrier that has completed, eight
+// a tile; 1,184 us against %s us at 16,384 tokens x 16 heads).
+// K (with the rope box) and V stream through a ring of eight boxes, in which key tile j has
+// the five places from 5 j on (three for K, two for V): K of tile j lies where V of tile
+// j - 2 was, V of tile j where K of tile j - 1 was, so each waits for one barrier.
+// Warp 0 loads, warps 1 and 2 issue, warps 4-7 and 8-11 are the softmax of A and B: thread =
 // query token = TMEM lane.  A softmax thread holds a row of 128 scores: the 168 registers
 // that 384 threads get at launch are split 104 / 200 between the warpgroups (384 x 168 =
 // 128 x 104 + 256 x 200).
@@ -774,9 +775,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     mbar_init(&cs->q_full, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&cs->k_full[i], 1);
-      mbar_init(&cs->k_empty[i], 1);
       mbar_init(&cs->v_full[i], 1);
-      mbar_init(&cs->v_empty[i], 1);
       mbar_init(&cs->q_ready[i], 128);
       mbar_init(&cs->s_full[i], 1);
       mbar_init(&cs->p_full[i], 128);
@@ -784,7 +783,16 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     }
     fence_mbar_init();
   }
-  if (tid == 64) set_block(a, at, cs->blk);
+  if (tid == 64) {
+    set_block(a, at, cs->blk);
+    // a tile's places are free once every sub-block that has key tiles is done with it
+    const int users = (cs->blk.j1[0] > cs->blk.j0[0]) + (cs->blk.j1[1] > cs->blk.j0[1]);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&cs->k_empty[i], max(users, 1));
+      mbar_init(&cs->v_empty[i], max(users, 1));
+    }
+    fence_mbar_init();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -830,87 +838,76 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
       mbar_wait(&cs->q_full, 0, kWaitLimitNs);
     }
     __syncwarp();
-  } else if (warp == 1) {
-    const int js = blk.js, je = blk.je;
-    const int ja0 = blk.j0[0], ja1 = blk.j1[0], jb0 = blk.j0[1], jb1 = blk.j1[1];
-    if (je > js) {
-      // the whole warp walks the loop, one lane issues (as in the expansion)
+  } else if (warp == 1 || warp == 2) {
+    // One sub-block's products.  The whole warp walks the loop, one lane issues (as in the
+    // expansion).  For a key tile that this sub-block does not use it only passes the data on.
+    const int s = warp - 1, js = blk.js, je = blk.je, ja = blk.j0[s], jb = blk.j1[s];
+    if (jb > ja) {
       const uint32_t type = kHalf ? kBf16Operands : 0u;
       const uint32_t id_s = idesc_bf16_f32(128, 128, false, false) ^ type;
       const uint32_t id_o = idesc_bf16_f32(128, 64 * a.nbv, false, true) ^ type;
       const uint32_t id_o1 = idesc_bf16_f32(128, 64, false, true) ^ type;
-      const uint64_t dq0 = smem_desc(smem_u32(sQ), 16, 1024, kLayoutSw128);
+      const uint64_t dq0 = smem_desc(smem_u32(sQ) + s * a.nbq * kBox, 16, 1024, kLayoutSw128);
       const uint64_t dk0 = smem_desc(smem_u32(ring), 16, 1024, kLayoutSw128);
       const uint64_t dv0 = smem_desc(smem_u32(ring), kBox, 1024, kLayoutSw128);
       constexpr uint64_t kBoxStep = kBox >> 4;
       const int nbq = a.nbq, nbv = a.nbv;
-      // S of sub-block s = Q K^T for the n-th key tile; `first`: K is waited for
-      auto qk = [&](int s, int n, bool first) {
-        if (first) {
-          if (!wwait(&cs->k_full[n & 1], (n >> 1) & 1, &cs->ctl, hdr)) return false;
-          tc_fence_after();
-        }
+      const uint32_t ts = tmem + 128 * s, to = tmem + 256 + 128 * s;
+      // S = Q K^T of the n-th key tile
+      auto qk = [&](int n, bool use) {
+        if (!wwait(&cs->k_full[n & 1], (n >> 1) & 1, &cs->ctl, hdr)) return false;
+        tc_fence_after();
         if (elect_one()) {
-          for (int i = 0; i < nbq; ++i) {
-            // columns past the row's end are zero on both sides
-            const uint64_t dq = dq0 + (s * nbq + i) * kBoxStep, dk = dk0 + ((kSlotsPerTile * n + i) % kSlots) * kBoxStep;
+          if (use) {
+            for (int i = 0; i < nbq; ++i) {
+              // columns past the row's end are zero on both sides
+              const uint64_t dq = dq0 + i * kBoxStep, dk = dk0 + ((kSlotsPerTile * n + i) % kSlots) * kBoxStep;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mma_ss(tmem + 128 * s, dq + 2 * kk, dk + 2 * kk, id_s, i > 0 || kk > 0);
+              for (int kk = 0; kk < 4; ++kk) mma_ss(ts, dq + 2 * kk, dk + 2 * kk, id_s, i > 0 || kk > 0);
+            }
+            mma_commit(&cs->s_full[s]);
+            mma_commit(&cs->k_empty[n & 1]);
+          } else {
+            mbar_arrive(&cs->k_empty[n & 1]);
           }
-          mma_commit(&cs->s_full[s]);
         }
         __syncwarp();
         return true;
       };
-      // O of sub-block s (+)= P V for the n-th key tile, once the softmax has left P (its np-th)
-      auto pv = [&](int s, int n, int np, bool first, bool last) {
-        if (first && !wwait(&cs->v_full[n & 1], (n >> 1) & 1, &cs->ctl, hdr)) return false;
-        if (!wwait(&cs->p_full[s], np & 1, &cs->ctl, hdr)) return false;
+      bool ok = wwait(&cs->q_ready[s], 0, &cs->ctl, hdr);
+      ok = ok && qk(0, js == ja);
+      int n = 0, np = 0;   // key tiles passed, P tiles taken
+      for (int j = js; j < je && ok; ++j, ++n) {
+        // O (+)= P V of the n-th key tile
+        const bool use = j >= ja && j < jb;
+        if (!(ok = wwait(&cs->v_full[n & 1], (n >> 1) & 1, &cs->ctl, hdr))) break;
+        if (use && !(ok = wwait(&cs->p_full[s], np & 1, &cs->ctl, hdr))) break;
         tc_fence_after();
-        const uint32_t o = tmem + 256 + 128 * s, p = tmem + 128 * s;
         const int s0 = (kSlotsPerTile * n + kVSlot) % kSlots;
         const uint64_t dv = dv0 + s0 * kBoxStep;
         if (elect_one()) {
-          if (nbv == 1 || s0 + 1 < kSlots) {
+          if (use) {
+            if (nbv == 1 || s0 + 1 < kSlots) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ts(o, p + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4), id_o, np > 0 || kk > 0);
-          } else {   // the two boxes lie at the ring's end and start: one product for each
+              for (int kk = 0; kk < 8; ++kk)
+                mma_ts(to, ts + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4), id_o, np > 0 || kk > 0);
+            } else {   // the two boxes lie at the ring's end and start: one product for each
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) mma_ts(o, p + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4), id_o1, np > 0 || kk > 0);
+              for (int kk = 0; kk < 8; ++kk)
+                mma_ts(to, ts + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4), id_o1, np > 0 || kk > 0);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ts(o + 64, p + 8 * kk, dv0 + (uint64_t)((kk * 2048) >> 4), id_o1, np > 0 || kk > 0);
+              for (int kk = 0; kk < 8; ++kk)
+                mma_ts(to + 64, ts + 8 * kk, dv0 + (uint64_t)((kk * 2048) >> 4), id_o1, np > 0 || kk > 0);
+            }
+            if (j + 1 == jb) mma_commit(&cs->o_full[s]);
+            mma_commit(&cs->v_empty[n & 1]);
+          } else {
+            mbar_arrive(&cs->v_empty[n & 1]);
           }
-          if (last) mma_commit(&cs->o_full[s]);
         }
         __syncwarp();
-        return true;
-      };
-      auto release = [&](uint64_t* bar) {
-        if (elect_one()) mma_commit(bar);
-        __syncwarp();
-      };
-      bool ok = true;
-      int np0 = 0, np1 = 0;   // P tiles taken
-      const bool a_on = ja1 > ja0, b_on = jb1 > jb0;
-      if (a_on) ok = wwait(&cs->q_ready[0], 0, &cs->ctl, hdr);
-      if (ok && b_on) ok = wwait(&cs->q_ready[1], 0, &cs->ctl, hdr);
-      const bool a_first = a_on && js == ja0;
-      if (ok && a_first) ok = qk(0, 0, true);
-      if (ok && b_on && js == jb0) ok = qk(1, 0, !a_first);
-      if (ok) release(&cs->k_empty[0]);
-      int n = 0;
-      for (int j = js; j < je && ok; ++j, ++n) {
-        // a sub-block's last tile leaves the other alone with the tensor core
-        const bool a_now = j >= ja0 && j < ja1, b_now = j >= jb0 && j < jb1;
-        const bool a_next = j + 1 >= ja0 && j + 1 < ja1, b_next = j + 1 >= jb0 && j + 1 < jb1;
-        if (a_now) ok = pv(0, n, np0++, true, j + 1 == ja1);
-        if (ok && a_next) ok = qk(0, n + 1, true);
-        if (ok && b_now) ok = pv(1, n, np1++, !a_now, j + 1 == jb1);
-        if (ok) release(&cs->v_empty[n & 1]);
-        if (ok && b_next) ok = qk(1, n + 1, !a_next);
-        if (ok && j + 1 < je) release(&cs->k_empty[(n + 1) & 1]);
+        np += use;
+        if (j + 1 < je) ok = qk(n + 1, j + 1 >= ja && j + 1 < jb);
       }
       // the last signal has arrived before the barriers go away
       if (ok) wwait(&cs->v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, &cs->ctl, hdr);
