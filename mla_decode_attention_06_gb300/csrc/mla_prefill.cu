@@ -661,15 +661,22 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
 // of one sub-block work, it has the other's two products.  Each sub-block has an issuing
 // warp of its own: the tensor core's queue is a few instructions deep, so a single one left
 // it idle during each of its waits (150 cycles even for a barrier that has completed, eight
-// a tile; 1,184 us against %s us at 16,384 tokens x 16 heads).
-// K (with the rope box) and V stream through a ring of eight boxes, in which key tile j has
-// the five places from 5 j on (three for K, two for V): K of tile j lies where V of tile
-// j - 2 was, V of tile j where K of tile j - 1 was, so each waits for one barrier.
+// a tile).  The two take turns: left alone they fall into step, both sub-blocks in their
+// softmax at once and then both at the tensor core.
+// K (its first box K0 and the others K12, the last of them the rope) and V stream through
+// eight places of a box: two for K0 and three pairs.  K12 of tile n lies in pair n % 3, V of
+// tile n in the pair that K12 of tile n - 1 left, K0 in place n % 2.  So V(n + 1) and
+// K0(n + 2) load when Q.K(n) is done, K12(n + 2) when P.V(n) is: the ten boxes of two tiles do
+// not fit beside the queries, and these are the ones needed last.
 // Warp 0 loads, warps 1 and 2 issue, warps 4-7 and 8-11 are the softmax of A and B: thread =
 // query token = TMEM lane.  A softmax thread holds a row of 128 scores: the 168 registers
 // that 384 threads get at launch are split 104 / 200 between the warpgroups (384 x 168 =
 // 128 x 104 + 256 x 200).
-constexpr int kSlots = 8, kSlotsPerTile = 5, kVSlot = 3;   // ring boxes; places of a key tile, its V from
+constexpr int kSlots = 8;
+// First byte of a place: K0 of tile n, K12 of tile n, V of tile n.
+__device__ __forceinline__ uint32_t place_k0(int n) { return (6 + (n & 1)) * kBox; }
+__device__ __forceinline__ uint32_t place_k12(int n) { return n % 3 * 2 * kBox; }
+__device__ __forceinline__ uint32_t place_v(int n) { return (n + 2) % 3 * 2 * kBox; }
 constexpr int kAttThreads = 384;
 constexpr float kRescaleThreshold = 8.0f;   // log2: O is rescaled when a row's maximum grows by more than 2^8
 
@@ -681,7 +688,7 @@ struct Block {
   int j0[2], j1[2], js, je;   // key tiles of each sub-block, and of both
 };
 struct AttSmem {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full, q_ready[2], s_full[2], p_full[2], o_full[2];
+  uint64_t k0_full[2], k12_full[2], k_empty[2], v_full[2], v_empty[2], turn[2], q_full, q_ready[2], s_full[2], p_full[2], o_full[2];
   Ctl ctl;
   Block blk;
 };
@@ -774,8 +781,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
   if (tid == 0) {
     mbar_init(&cs->q_full, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&cs->k_full[i], 1);
+      mbar_init(&cs->k0_full[i], 1);
+      mbar_init(&cs->k12_full[i], 1);
       mbar_init(&cs->v_full[i], 1);
+      mbar_init(&cs->turn[i], 1);
       mbar_init(&cs->q_ready[i], 128);
       mbar_init(&cs->s_full[i], 1);
       mbar_init(&cs->p_full[i], 128);
@@ -811,29 +820,48 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
           if (i < a.nbk) tma_load_3d(dst, &maps.qn, &cs->q_full, 64 * i, a.h0 + h, t);
           else tma_load_3d(dst, &maps.qr, &cs->q_full, 0, a.h0 + h, t);
         }
-      bool ok = true;
-      const int nb = a.nbk + a.nbv;
-      const uint8_t* kv = a.kv + ((size_t)h * a.cap_tiles + tile0) * nb * kBox;
-      auto place = [&](int n, int i) { return ring + ((kSlotsPerTile * n + i) % kSlots) * kBox; };
-      int n = 0;   // key tiles loaded
-      for (int j = js; j < je && ok; ++j, ++n) {
-        const int b = n & 1;
-        const uint8_t* src = kv + (size_t)j * nb * kBox;
-        if (n >= 2 && !(ok = wait(&cs->v_empty[b], ((n - 2) >> 1) & 1, &cs->ctl, hdr))) break;
-        mbar_arrive_expect_tx(&cs->k_full[b], (uint32_t)(a.nbq * kBox));
-        for (int i = 0; i < a.nbk; ++i) bulk_copy_g2s(place(n, i), src + (size_t)i * kBox, kBox, &cs->k_full[b]);
-        bulk_copy_g2s(place(n, a.nbk), a.rope + (size_t)(tile0 + j) * kBox, kBox, &cs->k_full[b]);
-        if (n >= 1 && !(ok = wait(&cs->k_empty[b ^ 1], ((n - 1) >> 1) & 1, &cs->ctl, hdr))) {
-          mbar_wait(&cs->k_full[b], (n >> 1) & 1, kWaitLimitNs);
+      const int nb = a.nbk + a.nbv, tiles = je - js;
+      const uint8_t* kv = a.kv + (((size_t)h * a.cap_tiles + tile0 + js) * nb) * kBox;
+      const uint8_t* rope = a.rope + (size_t)(tile0 + js) * kBox;
+      auto load_k0 = [&](int n) {
+        if (n >= tiles) return;
+        mbar_arrive_expect_tx(&cs->k0_full[n & 1], kBox);
+        bulk_copy_g2s(ring + place_k0(n), kv + (size_t)n * nb * kBox, kBox, &cs->k0_full[n & 1]);
+      };
+      auto load_k12 = [&](int n) {
+        if (n >= tiles) return;
+        mbar_arrive_expect_tx(&cs->k12_full[n & 1], (uint32_t)(a.nbk * kBox));
+        if (a.nbk > 1) bulk_copy_g2s(ring + place_k12(n), kv + ((size_t)n * nb + 1) * kBox, kBox, &cs->k12_full[n & 1]);
+        bulk_copy_g2s(ring + place_k12(n) + (a.nbk - 1) * kBox, rope + (size_t)n * kBox, kBox, &cs->k12_full[n & 1]);
+      };
+      auto load_v = [&](int n) {
+        if (n >= tiles) return;
+        mbar_arrive_expect_tx(&cs->v_full[n & 1], (uint32_t)(a.nbv * kBox));
+        bulk_copy_g2s(ring + place_v(n), kv + ((size_t)n * nb + a.nbk) * kBox, (uint32_t)(a.nbv * kBox), &cs->v_full[n & 1]);
+      };
+      load_k0(0);
+      load_k12(0);
+      load_v(0);
+      load_k0(1);
+      load_k12(1);
+      int n = 0;
+      for (; n + 1 < tiles; ++n) {
+        if (!wait(&cs->k_empty[n & 1], (n >> 1) & 1, &cs->ctl, hdr)) break;
+        load_v(n + 1);
+        load_k0(n + 2);
+        if (n + 2 < tiles && !wait(&cs->v_empty[n & 1], (n >> 1) & 1, &cs->ctl, hdr)) {
+          ++n;
           break;
         }
-        mbar_arrive_expect_tx(&cs->v_full[b], (uint32_t)(a.nbv * kBox));
-        for (int i = 0; i < a.nbv; ++i)
-          bulk_copy_g2s(place(n, kVSlot + i), src + (size_t)(a.nbk + i) * kBox, kBox, &cs->v_full[b]);
+        load_k12(n + 2);
       }
-      for (int i = n > 2 ? n - 2 : 0; i < n; ++i) {   // nothing in flight when the CTA leaves
-        mbar_wait(&cs->k_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
-        mbar_wait(&cs->v_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
+      // nothing in flight when the CTA leaves: the last loads of each kind (V up to tile n, K0
+      // up to n + 1, K12 up to n + 1, or n after a wait that ran out between them)
+      for (int i = n > 1 ? n - 1 : 0; i < tiles && i <= n + 1; ++i) {
+        mbar_wait(&cs->k0_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
+        if (i <= n || !*reinterpret_cast<volatile int*>(&cs->ctl.abort))
+          mbar_wait(&cs->k12_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
+        if (i <= n) mbar_wait(&cs->v_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
       }
       mbar_wait(&cs->q_full, 0, kWaitLimitNs);
     }
@@ -846,69 +874,65 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
       const uint32_t type = kHalf ? kBf16Operands : 0u;
       const uint32_t id_s = idesc_bf16_f32(128, 128, false, false) ^ type;
       const uint32_t id_o = idesc_bf16_f32(128, 64 * a.nbv, false, true) ^ type;
-      const uint32_t id_o1 = idesc_bf16_f32(128, 64, false, true) ^ type;
       const uint64_t dq0 = smem_desc(smem_u32(sQ) + s * a.nbq * kBox, 16, 1024, kLayoutSw128);
-      const uint64_t dk0 = smem_desc(smem_u32(ring), 16, 1024, kLayoutSw128);
+      const uint64_t dr0 = smem_desc(smem_u32(ring), 16, 1024, kLayoutSw128);
       const uint64_t dv0 = smem_desc(smem_u32(ring), kBox, 1024, kLayoutSw128);
       constexpr uint64_t kBoxStep = kBox >> 4;
-      const int nbq = a.nbq, nbv = a.nbv;
+      const int nbq = a.nbq;
       const uint32_t ts = tmem + 128 * s, to = tmem + 256 + 128 * s;
-      // S = Q K^T of the n-th key tile
-      auto qk = [&](int n, bool use) {
-        if (!wwait(&cs->k_full[n & 1], (n >> 1) & 1, &cs->ctl, hdr)) return false;
+      const bool both = blk.j1[s ^ 1] > blk.j0[s ^ 1];
+      bool ok = wwait(&cs->q_ready[s], 0, &cs->ctl, hdr);
+      int np = 0;   // P tiles taken
+      // Group n: O (+)= P V of key tile n - 1, then S = Q K^T of key tile n
+      int n = 0;
+      for (int j = js; j <= je && ok; ++j, ++n) {
+        const bool use_v = j > js && j - 1 >= ja && j - 1 < jb, use_k = j >= ja && j < jb;
+        const int v = n - 1;
+        if (j < je && !(ok = wwait(&cs->k0_full[n & 1], (n >> 1) & 1, &cs->ctl, hdr))) break;
+        if (j > js && !(ok = wwait(&cs->v_full[v & 1], (v >> 1) & 1, &cs->ctl, hdr))) break;
+        if (use_v && !(ok = wwait(&cs->p_full[s], np & 1, &cs->ctl, hdr))) break;
+        // the sub-blocks take turns
+        if (both && (s == 1 || n > 0) && !(ok = wwait(&cs->turn[s], (s == 1 ? n : n - 1) & 1, &cs->ctl, hdr))) break;
+        tc_fence_after();
+        const uint64_t dv = dv0 + (place_v(v + 3) >> 4), dk0 = dr0 + (place_k0(n) >> 4), dk12 = dr0 + (place_k12(n) >> 4);
+        if (elect_one()) {
+          if (use_v) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts(to, ts + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4), id_o, np > 0 || kk > 0);
+            if (j == jb) mma_commit(&cs->o_full[s]);
+            mma_commit(&cs->v_empty[v & 1]);
+          } else if (j > js) {
+            mbar_arrive(&cs->v_empty[v & 1]);
+          }
+          // columns past a row's end are zero on both sides
+          if (use_k) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mma_ss(ts, dq0 + 2 * kk, dk0 + 2 * kk, id_s, kk > 0);
+          }
+        }
+        __syncwarp();
+        if (j < je && !(ok = wwait(&cs->k12_full[n & 1], (n >> 1) & 1, &cs->ctl, hdr))) break;
         tc_fence_after();
         if (elect_one()) {
-          if (use) {
-            for (int i = 0; i < nbq; ++i) {
-              // columns past the row's end are zero on both sides
-              const uint64_t dq = dq0 + i * kBoxStep, dk = dk0 + ((kSlotsPerTile * n + i) % kSlots) * kBoxStep;
+          for (int i = 1; i < nbq && use_k; ++i) {
+            const uint64_t dq = dq0 + i * kBoxStep, dk = dk12 + (i - 1) * kBoxStep;
+            if (i == nbq - 1 && both) mbar_arrive(&cs->turn[s ^ 1]);   // its wait passes under the last box
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) mma_ss(ts, dq + 2 * kk, dk + 2 * kk, id_s, i > 0 || kk > 0);
-            }
+            for (int kk = 0; kk < 4; ++kk) mma_ss(ts, dq + 2 * kk, dk + 2 * kk, id_s, 1u);
+          }
+          if (use_k) {
             mma_commit(&cs->s_full[s]);
             mma_commit(&cs->k_empty[n & 1]);
           } else {
-            mbar_arrive(&cs->k_empty[n & 1]);
+            if (both) mbar_arrive(&cs->turn[s ^ 1]);
+            if (j < je) mbar_arrive(&cs->k_empty[n & 1]);
           }
         }
         __syncwarp();
-        return true;
-      };
-      bool ok = wwait(&cs->q_ready[s], 0, &cs->ctl, hdr);
-      ok = ok && qk(0, js == ja);
-      int n = 0, np = 0;   // key tiles passed, P tiles taken
-      for (int j = js; j < je && ok; ++j, ++n) {
-        // O (+)= P V of the n-th key tile
-        const bool use = j >= ja && j < jb;
-        if (!(ok = wwait(&cs->v_full[n & 1], (n >> 1) & 1, &cs->ctl, hdr))) break;
-        if (use && !(ok = wwait(&cs->p_full[s], np & 1, &cs->ctl, hdr))) break;
-        tc_fence_after();
-        const int s0 = (kSlotsPerTile * n + kVSlot) % kSlots;
-        const uint64_t dv = dv0 + s0 * kBoxStep;
-        if (elect_one()) {
-          if (use) {
-            if (nbv == 1 || s0 + 1 < kSlots) {
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                mma_ts(to, ts + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4), id_o, np > 0 || kk > 0);
-            } else {   // the two boxes lie at the ring's end and start: one product for each
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                mma_ts(to, ts + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4), id_o1, np > 0 || kk > 0);
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                mma_ts(to + 64, ts + 8 * kk, dv0 + (uint64_t)((kk * 2048) >> 4), id_o1, np > 0 || kk > 0);
-            }
-            if (j + 1 == jb) mma_commit(&cs->o_full[s]);
-            mma_commit(&cs->v_empty[n & 1]);
-          } else {
-            mbar_arrive(&cs->v_empty[n & 1]);
-          }
-        }
-        __syncwarp();
-        np += use;
-        if (j + 1 < je) ok = qk(n + 1, j + 1 >= ja && j + 1 < jb);
+        np += use_v;
       }
+      --n;   // key tiles passed
       // the last signal has arrived before the barriers go away
       if (ok) wwait(&cs->v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, &cs->ctl, hdr);
     }
