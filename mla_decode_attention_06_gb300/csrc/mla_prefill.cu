@@ -856,11 +856,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         load_k12(n + 2);
       }
       // nothing in flight when the CTA leaves: the last loads of each kind (V up to tile n, K0
-      // up to n + 1, K12 up to n + 1, or n after a wait that ran out between them)
+      // and K12 up to n + 1; after a wait that ran out, one of them may only run out too)
       for (int i = n > 1 ? n - 1 : 0; i < tiles && i <= n + 1; ++i) {
         mbar_wait(&cs->k0_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
-        if (i <= n || !*reinterpret_cast<volatile int*>(&cs->ctl.abort))
-          mbar_wait(&cs->k12_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
+        mbar_wait(&cs->k12_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
         if (i <= n) mbar_wait(&cs->v_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
       }
       mbar_wait(&cs->q_full, 0, kWaitLimitNs);
