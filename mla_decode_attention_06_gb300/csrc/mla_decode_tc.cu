@@ -38,7 +38,7 @@
 //               domain, writes P (bf16 pairs) back into TMEM where the P . C
 //               MMA takes it as its A operand, rescales O only when the running
 //               max grows by more than 2^8, and writes the segment's output.
-//   warps 6-9   (e4m3, e2m1 cache) widen the tile's codes x scale into bf16.
+//   warps 6-9   (e4m3 cache; 8-11 over an e2m1 cache, see Cfg) widen the tile's codes x scale into bf16.
 //   last warp   P . C issuer (one thread), so a ready P never waits behind a QK.
 // Every wait is bounded in time; a timeout sets a status bit and the kernel
 // unwinds without hanging.
@@ -119,13 +119,19 @@ struct Cfg {
   // the instruction descriptor's operand types, bf16 or (e2m1) f16: flips bits 7 and 10
   static constexpr uint32_t kOperands = kMode == kLoadFp4 ? (1u << 7) | (1u << 10) : 0u;
   // e2m1: bytes of a row before its rope part (codes, a scale byte per 32 of them, zeros up
-  // to 16); a multiple of 16 that is an odd number of 16-byte pieces at both widths, so
+  // to 16).  With the rope part a row is an odd number of 16-byte pieces at (512, 64), so
   // eight neighbouring rows start in eight different bank groups
   static constexpr int kRow4 = (L / 2 + L / 32 + 15) / 16 * 16;
   static constexpr int kRawOff = NLB >= 8 ? 4 * kBox : 0;   // codes land where the last latent boxes go
   static constexpr int kConvThreads = 64 * NRH;                // warps 6.. (kCoded): one per row and raw box
-  static constexpr int kPvWarp = kCoded ? 6 + kConvThreads / 32 : 6;   // the P . C issuer
-  static constexpr int kThreads = 32 * (kPvWarp + 1);
+  // The e2m1 instance lays its warps out by warpgroup (0 load, 1 QK, 2 P . C, 3 rope | 4-7
+  // softmax | 8.. converters) so that the softmax's get the registers that the first four do
+  // not need: 104 / 232 / 168 of 168 each.  Spilled, a row of scores goes to L2, since shared
+  // memory leaves the L1 cache 20 KB.
+  static constexpr bool kGrouped = kMode == kLoadFp4;
+  static constexpr int kConvWarp = kGrouped ? 8 : 6;
+  static constexpr int kPvWarp = kGrouped ? 2 : (kCoded ? 6 + kConvThreads / 32 : 6);   // the P . C issuer
+  static constexpr int kThreads = kGrouped ? 256 + kConvThreads : 32 * (kPvWarp + 1);
   static constexpr int kRegionBytes = kQBytes + kStages * kStageBytes;   // query buffer + stage ring
   static constexpr int kMrgHalf = (LC / 2) * kMaxHeads * 4;               // merge: one half partial slice
   static constexpr int kStgBytes = kMaxHeads * (LC * 2 + 16);             // merge: staged output rows
@@ -135,7 +141,8 @@ struct Cfg {
   static_assert(kStgBytes + 2 * kMrgHalf <= kRegionBytes, "merge buffers in the idle region");
   static_assert(kMode != kLoadFp8 || NRH % CL == 0, "raw boxes split over the cluster");
   static_assert(!kCoded || NRH == 1 || QT == RW, "the first widening pass is the QK's TMEM-operand part");
-  static_assert(kRawOff + 64 * kRow4 <= NLB * kBox, "e2m1 rows below the rope box");
+  static constexpr int kMaxRope = L < 256 ? 32 : 64;
+  static_assert(kRawOff + 64 * (kRow4 + 2 * kMaxRope) <= NLB * kBox, "e2m1 rows below the rope box");
   static_assert(QT / 64 <= NQS + 1, "the query staging fits the query buffer");
   static_assert(kSmem <= 232448, "shared memory");
 };
@@ -258,6 +265,21 @@ __device__ __forceinline__ uint32_t e2m1x2_scaled_f16x2(uint32_t byte, __half2 s
   const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1);
   const __half2 v = __hmul2(__half2(h), scale);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Eight e2m1 codes as four f16 pairs, times the power of two in the tables: the f16 values of
+// the eight magnitudes differ in their high bytes only, so one byte permute looks up four of
+// them (t0, t1 hold the high bytes, an exponent added to each), two operations set four signs
+// and one permute per pair widens.  (The conversion instruction takes 19 cycles a pair here,
+// and a multiply.)
+__device__ __forceinline__ uint4 e2m1x8_f16(uint32_t w, uint32_t t0, uint32_t t1) {
+  const uint32_t m = w & 0x77777777u;
+  uint32_t a = __byte_perm(t0, t1, m), b = __byte_perm(t0, t1, m >> 16);
+  const uint32_t u = __byte_perm(w, 0u, 0x1100u), v = __byte_perm(w, 0u, 0x3322u);
+  a |= ((u << 4) & 0x00800080u) | (u & 0x80008000u);
+  b |= ((v << 4) & 0x00800080u) | (v & 0x80008000u);
+  return make_uint4(__byte_perm(a, 0u, 0x1404u), __byte_perm(a, 0u, 0x3424u), __byte_perm(b, 0u, 0x1404u),
+                    __byte_perm(b, 0u, 0x3424u));
 }
 
 // A scale byte (2^(b - 127), 255 = NaN) as an f16 pair: zero below 2^-24, infinity above 2^15.
@@ -529,6 +551,19 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// (x, y) * a + b and (x, y) + (a, b), both halves in one instruction.
+__device__ __forceinline__ void fma_pair(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 v, s, t;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 t, {%3, %3};\n\t"
+      "fma.rn.f32x2 v, v, s, t;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\tadd.rn.f32x2 v, v, s;\n\t"
+      "mov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
 
 template <int LC, int CL, int MODE>
 __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
@@ -554,14 +589,15 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
   const int KQ = L + a.d.qk_rope;
   const int lat_x0 = (int)rank * LC;
   // cache rope columns: they start at L in a bf16 row, at byte L (bf16 column L / 2) in an
-  // e4m3 row, at byte kRow4 in an e2m1 row
-  const int rope_x0 = MODE == kLoadFp8 ? L / 2 : MODE == kLoadFp4 ? C::kRow4 / 2 : L;
+  // e4m3 row (an e2m1 row is copied whole)
+  const int rope_x0 = MODE == kLoadFp8 ? L / 2 : L;
+  const int row4 = C::kRow4 + 2 * a.d.qk_rope;   // bytes of an e2m1 row
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&cs->kv_full[s], 1);
       mbar_init(&cs->kv_empty[s], CL);   // one tcgen05.commit from each CTA of the cluster
-      mbar_init(&cs->kv_conv[s], C::kConvThreads);
+      mbar_init(&cs->kv_conv[s], C::kConvThreads + (C::kGrouped ? 32 : 0));   // ... and the rope warp
       mbar_init(&cs->kv_conv_a[s], C::kConvThreads);
     }
     mbar_init(&cs->q_full, 1 + 128);     // producer (TMA bytes) + every softmax thread (TMEM part)
@@ -574,7 +610,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
       mbar_init(&cs->pv_done[b], 1);
     }
     mbar_init(&cs->o_free, 128);
-    mbar_init(&cs->conv_sync, C::kConvThreads);
+    mbar_init(&cs->conv_sync, C::kConvThreads + (C::kGrouped ? 32 : 0));
     mbar_init(&cs->fix_bar, 128);
     mbar_init(&cs->fix_done, 1);
     for (int i = 0; i < 2; ++i) {
@@ -590,8 +626,10 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
     tmem_relinquish();
   }
   if (warp == 0 && lane == 0) {
-    prefetch_tensormap(&maps.kv_lat);
-    prefetch_tensormap(&maps.kv_rope);
+    if (MODE != kLoadFp4) {
+      prefetch_tensormap(&maps.kv_lat);
+      prefetch_tensormap(&maps.kv_rope);
+    }
     prefetch_tensormap(&maps.q);
   }
   tc_fence_before();
@@ -606,10 +644,11 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
 
   const int g0 = a.bounds[k], g1 = a.bounds[k + 1];
   const int ps = a.ks.page_size;
-  // e2m1 rows are one box wide, so the CTAs of a cluster share a tile's loads by rows
+  // e2m1 rows lie one behind the other, so the CTAs of a cluster share a tile by rows
   constexpr int kMaxLoadRows = MODE == kLoadFp4 ? kTileKeys / 2 : kTileKeys;
   const int rows_per_load = ps < kMaxLoadRows ? ps : kMaxLoadRows;
 
+  if (C::kGrouped && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == 0) {
     // ------------------------------------------------------------- producer
     auto load_box = [&](void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
@@ -692,7 +731,8 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
           if (!pm) continue;
           const int y = load_row(it, p, pm, pg);
           if (MODE == kLoadFp4) {
-            if (lane < 2 && p % CL == (int)crank) tma_prefetch_2d(lane ? &maps.kv_rope : &maps.kv_lat, lane ? rope_x0 : 0, y);
+            if (lane == 0 && p % CL == (int)crank)
+              bulk_prefetch_l2(static_cast<const uint8_t*>(a.kv_pool) + (size_t)y * row4, (uint32_t)(rows_per_load * row4));
           } else if (lane < kOwn) {
             if (MODE == kLoadFp8) tma_prefetch_2d(&maps.kv_lat, ((int)crank * kOwn + lane) * C::RW, y);
             else tma_prefetch_2d(&maps.kv_lat, 64 * ((int)crank * kOwn + lane), y);
@@ -799,7 +839,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
           // same bytes, most of which the other CTAs' multicasts deliver (an e4m3 row's
           // 4-byte scale each CTA copies for itself)
           const uint32_t row_bytes =
-              (MODE == kLoadFp8 ? L + 4 : MODE == kLoadFp4 ? C::kRow4 : C::NLB * 128) + 128;
+              MODE == kLoadFp4 ? (uint32_t)row4 : (MODE == kLoadFp8 ? L + 4 : C::NLB * 128) + 128;
           uint32_t live_rows = 0;
           for (int p = 0; p < nloads; ++p)
             if ((mask >> (p * rows_per_load)) & lmask) live_rows += rows_per_load;
@@ -815,10 +855,14 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
             const int y = load_row(it, p, pm, pg);
             // one box per lane: this CTA's share of the latent (or raw e4m3) boxes, then the rope box (rank 0)
             if (MODE == kLoadFp4) {
-              if (p % CL == (int)crank && lane == 0)
-                load_box(st + C::kRawOff + r0 * C::kRow4, &maps.kv_lat, &cs->kv_full[s], 0, y);
-              else if (p % CL == (int)crank && lane == 1)
-                load_box(st_rope + r0 * 128, &maps.kv_rope, &cs->kv_full[s], rope_x0, y);
+              if (p % CL == (int)crank && lane == 0) {
+                const uint8_t* rows = static_cast<const uint8_t*>(a.kv_pool) + (size_t)y * row4;
+                if (CL >= 2)
+                  bulk_copy_g2s_mc(st + C::kRawOff + r0 * row4, rows, (uint32_t)(rows_per_load * row4), &cs->kv_full[s],
+                                   (uint16_t)C::kMcMask);
+                else
+                  bulk_copy_g2s(st + C::kRawOff + r0 * row4, rows, (uint32_t)(rows_per_load * row4), &cs->kv_full[s]);
+              }
             } else if (lane < kOwn) {
               if (MODE == kLoadFp8) {
                 const int h = (int)crank * kOwn + lane;
@@ -1075,19 +1119,55 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         mbar_arrive(&cs->kv_conv[s]);
       }
     });
-  } else if (MODE == kLoadFp4 && warp >= 6) {
+  } else if (MODE == kLoadFp4 && warp == 3) {
+    // ------------------------------------------------------------- rope of e2m1 rows
+    // Two rows a lane, bf16 -> f16, into the tile's rope box (zeros past qk_rope and in dead rows).
+    __half2 top = __float2half2_rn(0.f);   // largest magnitude so far, NaN aside
+    int c = 0;
+    for_each_segment(a, k, g0, g1, [&](int si, int t, const TokenPlan& tp, int ia, int ie, bool, int) {
+      for (int it = ia; it < ie; ++it, ++c) {
+        if (waborted(cs)) return;
+        const int s = c % S;
+        if (!wwait(&cs->kv_full[s], (c / S) & 1, cs, hdr)) return;
+        uint8_t* st = sStage + s * C::kStageBytes;
+        const uint64_t mask = cs->row_mask[s];
+#pragma unroll 1
+        for (int r = lane; r < 64; r += 32) {
+          const uint8_t* src = st + C::kRawOff + r * row4 + C::kRow4;
+          uint8_t* dst = st + C::NLB * C::kBox + r * 128;
+          const int nch = (mask >> r) & 1ull ? a.d.qk_rope / 8 : 0;
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (ch < nch) v = *reinterpret_cast<const uint4*>(src + 16 * ch);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              w[e] = bf16x2_to_f16x2(w[e]);
+              top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&w[e])));
+            }
+            *reinterpret_cast<uint4*>(dst + ((ch ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        mbar_arrive(&cs->conv_sync);   // the rows may be overwritten
+        fence_proxy_async_smem();
+        mbar_arrive(&cs->kv_conv[s]);
+      }
+    });
+    const float2 big = __half22float2(top);
+    if (isinf(big.x) || isinf(big.y)) atomicOr(&hdr->status, kDeviceCheckFailed);
+  } else if (MODE == kLoadFp4 && warp >= C::kConvWarp) {
     // ------------------------------------------------------------- e2m1 converters
     // Tile row crow is widened by NRH threads, pass p taking its codes of latent
     // [p RW, (p + 1) RW), thread hh the hh-th RW / NRH of them: groups of 32 codes
     // (16 bytes) under one scale byte.  The operands are f16: a code times 2^e is exact
-    // for e in [-23, 13] (one conversion and one packed multiply per pair; bf16 has no
-    // conversion from e2m1 and would take six operations), and the absorbed query and P
-    // lose 2^-12 instead of 2^-9.  The rope part is bf16 and is converted with the last
-    // pass.  A magnitude that f16 does not reach becomes an infinity and is reported.
-    // The last pass overwrites the codes, so it waits until every thread has read its own.
-    const int ci = tid - 192, crow = ci & 63, hh = ci >> 6;
+    // for e in [-23, 13], and the absorbed query and P lose 2^-12 instead of 2^-9.  The
+    // scale goes into the lookup tables of e2m1x8_f16 where all products are normal
+    // numbers (|e| <= 13).  The rope part is converted by a warp of its own.  A
+    // magnitude that f16 does not reach becomes an infinity and is reported.  The last pass
+    // overwrites the rows, so it waits until every thread has read its part.
+    const int ci = tid - 32 * C::kConvWarp, crow = ci & 63, hh = ci >> 6;
     constexpr int kGroups = C::RW / C::NRH / 32;   // groups per thread and pass
-    constexpr int kRopeChunks = 8 / C::NRH;        // 16-byte chunks of the rope row per thread
     int c = 0;
     bool out_of_range = false;
     for_each_segment(a, k, g0, g1, [&](int si, int t, const TokenPlan& tp, int ia, int ie, bool, int) {
@@ -1097,12 +1177,16 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         if (!wwait(&cs->kv_full[s], (c / S) & 1, cs, hdr)) return;
         uint8_t* st = sStage + s * C::kStageBytes;
         const bool live = (cs->row_mask[s] >> crow) & 1ull;
-        const uint8_t* src = st + C::kRawOff + crow * C::kRow4;
+        const uint8_t* src = st + C::kRawOff + crow * row4;
 #pragma unroll 1
         for (int p = 0; p < C::NRH; ++p) {
           const int grp0 = p * (C::RW / 32) + hh * kGroups;
-          uint4 raw[kGroups];
-          uint32_t sb = 0;   // kGroups <= 4 scale bytes
+          // the loop over groups stays rolled, the next group moving up in registers: five roles
+          // of warps run different code on each SM, and unrolled it does not stay in the
+          // instruction cache (ncu: 36 % of the fetches missed)
+          static_assert(kGroups <= 4, "groups and scale bytes of a pass in registers");
+          uint4 raw[4] = {};
+          uint32_t sb = 0;
 #pragma unroll
           for (int q = 0; q < kGroups; ++q) raw[q] = *reinterpret_cast<const uint4*>(src + (grp0 + q) * 16);
           if (kGroups == 4) {
@@ -1115,60 +1199,46 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
             mbar_arrive(&cs->conv_sync);
             if (!wwait(&cs->conv_sync, c & 1, cs, hdr)) return;
           }
-          auto put = [&](int q, auto&& value) {   // group q's 32 columns: four 16-byte slots of the swizzled row
+#pragma unroll 1
+          for (int q = 0; q < kGroups; ++q) {
+            // group q's 32 columns: four 16-byte slots of the swizzled row
             const int col = (grp0 + q) * 32;
             uint8_t* box = st + (col >> 6) * C::kBox + crow * 128;
             const int ch = (col & 63) >> 3;
-            const uint32_t w[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
+            const int e = (int)(sb & 0xFFu) - 127;
+            uint4 o[4] = {};   // a dead row (only in a token's ragged tiles) becomes zeros
+            if (live) {
+              const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+              if (e >= -13 && e <= 13) {
+                const uint32_t t0 = 0x3E3C3800u + (uint32_t)e * 0x04040400u, t1 = 0x46444240u + (uint32_t)e * 0x04040404u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4*>(box + (((ch + i) ^ (crow & 7)) << 4)) =
-                  make_uint4(value(w[i] & 0xFFu), value((w[i] >> 8) & 0xFFu), value((w[i] >> 16) & 0xFFu),
-                             value(w[i] >> 24));
-          };
-          if (live) {
+                for (int i = 0; i < 4; ++i) o[i] = e2m1x8_f16(w[i], t0, t1);
+              } else {
+                out_of_range |= e > 13 && e < 128;   // 6 * 2^14 is past f16
+                const __half2 sc = e8m0_f16x2((uint32_t)(e + 127));
 #pragma unroll
-            for (int q = 0; q < kGroups; ++q) {
-              const uint32_t b = (sb >> (8 * q)) & 0xFFu;
-              out_of_range |= b > 140u && b != 255u;   // 6 * 2^14 is past f16
-              const __half2 sc = e8m0_f16x2(b);
-              put(q, [&](uint32_t byte) { return e2m1x2_scaled_f16x2(byte, sc); });
+                for (int i = 0; i < 4; ++i)
+                  o[i] = make_uint4(e2m1x2_scaled_f16x2(w[i] & 0xFFu, sc), e2m1x2_scaled_f16x2((w[i] >> 8) & 0xFFu, sc),
+                                    e2m1x2_scaled_f16x2((w[i] >> 16) & 0xFFu, sc), e2m1x2_scaled_f16x2(w[i] >> 24, sc));
+              }
             }
-          } else {
-            // a dead row (only in a token's ragged tiles) becomes zeros
 #pragma unroll
-            for (int q = 0; q < kGroups; ++q) put(q, [](uint32_t) { return 0u; });
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(box + (((ch + i) ^ (crow & 7)) << 4)) = o[i];
+            raw[0] = raw[1];
+            raw[1] = raw[2];
+            raw[2] = raw[3];
+            sb >>= 8;
           }
-          if (C::NRH > 1 && p == 0) {
-            // latent [0, RW) is in place: the QK's TMEM-operand part may start
-            fence_proxy_async_smem();
-            mbar_arrive(&cs->kv_conv_a[s]);
-          }
+          fence_proxy_async_smem();
+          // after all but the last pass: latent [0, RW) is in place, the QK's TMEM-operand part may start
+          mbar_arrive(C::NRH > 1 && p == 0 ? &cs->kv_conv_a[s] : &cs->kv_conv[s]);
         }
-        uint8_t* rr = st + C::NLB * C::kBox + crow * 128;
-#pragma unroll
-        for (int i = 0; i < kRopeChunks; ++i) {
-          uint4* x = reinterpret_cast<uint4*>(rr + (((hh * kRopeChunks + i) ^ (crow & 7)) << 4));
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (live) {
-            v = *x;
-            // 0x4780: 65536 as bf16, the first that rounds to infinity
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              out_of_range |= ((w[e] & 0x7FFFu) >= 0x4780u && (w[e] & 0x7FFFu) < 0x7F80u) ||
-                              ((w[e] >> 16 & 0x7FFFu) >= 0x4780u && (w[e] >> 16 & 0x7FFFu) < 0x7F80u);
-            v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
-          }
-          *x = v;
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&cs->kv_conv[s]);
       }
     });
     if (out_of_range) atomicOr(&hdr->status, kDeviceCheckFailed);
-  } else {
+  } else if (!C::kGrouped || warp >= 4) {
     // ------------------------------------------------------------- softmax
+    if (C::kGrouped) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int q = warp & 3;
     const int row = 32 * q + lane;
     const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16);
@@ -1246,6 +1316,69 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         float sv[64];
 #pragma unroll
         for (int j = 0; j < 64; ++j) sv[j] = __uint_as_float(sr[j]);
+        if constexpr (MODE == kLoadFp4) {
+          // The same softmax in as few instructions (pairs where the hardware has them, one path
+          // for whole and ragged tiles): this instance's code is bound by the instruction cache.
+          const bool up = sl2 > 0.f;   // else the scores are scaled here, so that the max is a max
+          const float f = up ? sl2 : 1.f;
+          if (!up) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j) sv[j] *= sl2;
+          }
+          if (mask != ~0ull) {
+            const uint32_t mw[2] = {(uint32_t)mask, (uint32_t)(mask >> 32)};
+#pragma unroll
+            for (int j = 0; j < 64; ++j) sv[j] = (mw[j >> 5] >> (j & 31)) & 1u ? sv[j] : -CUDART_INF_F;
+          }
+          float r4[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+          for (int j = 4; j < 60; j += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r4[i] = fmaxf(fmaxf(r4[i], sv[j + i]), sv[j + 4 + i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r4[i] = fmaxf(r4[i], sv[60 + i]);
+          const float mx = fmaxf(fmaxf(r4[0], r4[1]), fmaxf(r4[2], r4[3])) * f;
+          const bool want = m != -CUDART_INF_F && mx > m + kRescaleThreshold;
+          if (__any_sync(0xffffffffu, want)) {
+            const float alpha = want ? ex2(m - mx) : 1.f;
+            if (!wwait(&cs->pv_done[(c - 1) & 1], ((c - 1) >> 1) & 1, cs, hdr)) return;
+            tc_fence_after();
+#pragma unroll 1
+            for (int col = 0; col < LC; col += 16) {
+              uint32_t r[16];
+              tmem_ld16(trow + col, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+              tmem_st16(trow + col, r);
+            }
+            tmem_st_wait();
+            if (want) {
+              l *= alpha;
+              m = mx;
+            }
+          }
+          if (m == -CUDART_INF_F) m = mx;
+          const float neg = m == -CUDART_INF_F ? 0.f : -m;
+          uint32_t pk[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            fma_pair(sv[2 * j], sv[2 * j + 1], f, neg);
+            sv[2 * j] = ex2(sv[2 * j]);
+            sv[2 * j + 1] = ex2(sv[2 * j + 1]);
+            pk[j] = pack_p<MODE>(sv[2 * j], sv[2 * j + 1]);
+          }
+          tmem_st32(trow + C::kSCol + 64 * b, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&cs->p_full[b]);
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) add_pair(l0, l1, sv[2 * j], sv[2 * j + 1]);
+          l += l0 + l1;
+          last_c = c;
+          continue;
+        }
         // row max of the scaled scores (log2 domain); dead keys do not count.
         // Eight independent chains, then a tree, keep the dependency depth short;
         // full tiles (the common case) skip the mask tests.
@@ -1616,8 +1749,7 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
   using C = Cfg<LC, CL, MODE>;
   constexpr CUtensorMapDataType kBF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int L = a.d.kv_lora_rank, R = a.d.qk_rope, KQ = L + R, ps = a.d.page_size;
-  constexpr int kMaxLoadRows = MODE == kLoadFp4 ? kTileKeys / 2 : kTileKeys;
-  const uint32_t rows = MODE == kLoadSparse ? 1u : (uint32_t)(ps < kMaxLoadRows ? ps : kMaxLoadRows);
+  const uint32_t rows = MODE == kLoadSparse ? 1u : (uint32_t)(ps < kTileKeys ? ps : kTileKeys);
   const uint64_t pool_rows = (uint64_t)a.d.num_pages * ps;
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return cudaErrorInvalidDevice;
@@ -1626,7 +1758,7 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
   static bool cache_valid = false;
   static MapKey cache_key;
   static Maps cache_maps;
-  Maps maps;
+  Maps maps = {};
   bool hit;
   {
     std::lock_guard<std::mutex> lock(cache_mu);
@@ -1641,11 +1773,7 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
                      CU_TENSOR_MAP_SWIZZLE_NONE) &&
            encode_2d(&maps.kv_rope, kBF16, a.kv_pool, rb / 2, pool_rows, rb, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B);
     } else if (MODE == kLoadFp4) {
-      // code and scale bytes as 16-bit elements (a box is at most 256 elements wide)
-      const uint64_t rb = C::kRow4 + 2ull * R;
-      ok = encode_2d(&maps.kv_lat, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.kv_pool, rb / 2, pool_rows, rb, C::kRow4 / 2, rows,
-                     CU_TENSOR_MAP_SWIZZLE_NONE) &&
-           encode_2d(&maps.kv_rope, kBF16, a.kv_pool, rb / 2, pool_rows, rb, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B);
+      ok = true;   // rows are copied whole, without a map
     } else {
       ok = encode_2d(&maps.kv_lat, kBF16, a.kv_pool, KQ, pool_rows, (uint64_t)KQ * 2, 64, rows,
                      CU_TENSOR_MAP_SWIZZLE_128B);

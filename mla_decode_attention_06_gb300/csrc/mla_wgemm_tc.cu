@@ -235,12 +235,14 @@ __global__ void __launch_bounds__(kThreads, 1) wgemm_kernel(const __grid_constan
         }
       }
     }
-    if (h == 0 && a.H < kMaxHeads) {
-      const int per = (kMaxHeads - a.H) * a.KQ;
-      for (int i = first; i < TN * per; i += stride) {
-        const int t = t0 + i / per;
-        if (t < a.T) a.q_full[((size_t)t * kMaxHeads + a.H) * a.KQ + i % per] = __float2bfloat16_rn(0.f);
-      }
+    // rows of absent heads: zeros, each head's blocks a share (16-byte pieces; KQ is a multiple of 8)
+    const int r0 = a.H + (int)((long long)(kMaxHeads - a.H) * h / a.H);
+    const int r1 = a.H + (int)((long long)(kMaxHeads - a.H) * (h + 1) / a.H);
+    const int per = (r1 - r0) * a.KQ / 8;
+    for (int i = first; i < TN * per; i += stride) {
+      const int t = t0 + i / per;
+      if (t < a.T)
+        reinterpret_cast<uint4*>(a.q_full + ((size_t)t * kMaxHeads + r0) * a.KQ)[i % per] = make_uint4(0, 0, 0, 0);
     }
   };
   bool ok = true;

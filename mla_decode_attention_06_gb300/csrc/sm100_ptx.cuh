@@ -190,6 +190,17 @@ __device__ __forceinline__ void bulk_copy_g2s(void* dst, const void* src, uint32
                : "memory");
 }
 
+// The same copy delivered to every CTA of the cluster named in `cta_mask`, at the same
+// shared-memory offset; each CTA's mbarrier at the offset of `bar` counts the bytes.
+__device__ __forceinline__ void bulk_copy_g2s_mc(void* dst, const void* src, uint32_t bytes, uint64_t* bar,
+                                                 uint16_t cta_mask) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar)), "h"(cta_mask)
+      : "memory");
+}
+
 // Contiguous shared -> global copy of `bytes` (multiple of 16, both addresses
 // 16-byte aligned) on the bulk-copy engine, tracked by the issuing thread's
 // bulk groups (bulk_commit / bulk_wait_all).
