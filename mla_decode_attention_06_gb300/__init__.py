@@ -43,6 +43,9 @@ def library_path() -> str:
 def _ptr(t: Optional[torch.Tensor], name: str, dtypes=None, device=None):
     if t is None:
         return None
+    if isinstance(t, torch.Tensor) and (dtypes is None or t.dtype in dtypes) and t.is_cuda and \
+            t.is_contiguous() and (device is None or t.device == device):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -180,6 +183,19 @@ def _buffer(shape, dtype, device, stream):
     return t
 
 
+_status = {}
+
+
+def _unread_status(device):
+    """The status word of calls that nobody reads it of: kernels only set bits in it."""
+    t = _status.get(device)
+    if t is None:
+        if torch.cuda.is_current_stream_capturing():
+            return _buffer(256, torch.uint8, device, None)   # the graph's own memory, not kept
+        t = _status[device] = torch.zeros(256, dtype=torch.uint8, device=device)
+    return t
+
+
 def _call(name, device, *args):
     """One library call with `device` current (the library launches on the current device)."""
     fn = getattr(_lib.load(), name)
@@ -256,7 +272,7 @@ def mla_cache_append(kv_new, input_row_offsets, kv_pool, block_table, cache_lens
         raise ValueError("kv_scales must hold one value per cache row")
     B, offsets, table, table_stride, lens = _tables(input_row_offsets, block_table, cache_lens, dev)
     if workspace is None:
-        workspace = _buffer(256, torch.uint8, dev, stream)
+        workspace = _buffer(256, torch.uint8, dev, stream) if debug else _unread_status(dev)
     _call("mla_cache_append", dev, ctypes.byref(dims), int(cache_format), kv_new.data_ptr(), new_stride, offsets,
           B, T, _ptr(q, "q", _BF16, dev), _ptr(q_out, "q_out", _BF16, dev), _ptr(kv_pool, "kv_pool", None, dev),
           _ptr(kv_scales, "kv_scales", (torch.float32,), dev), _ptr(rows_out, "rows_out", _BF16, dev), table,

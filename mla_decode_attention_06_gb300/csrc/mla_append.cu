@@ -16,11 +16,15 @@
 // Arithmetic.  The codes follow the last bit of y, so y is the correctly rounded
 // value: squares of bf16 are exact in fp32 and are summed as an unevaluated pair
 // hi + lo (Knuth's TwoSum); 1 / sqrt is taken once per row in fp64 and split into two
-// floats; c * gamma is exact in fp32, its product with the pair is exact to ~2^-46
-// (an fma gives the low part), and the pair is rounded to bf16 once.  That leaves one
-// fp64 root per row on the narrow fp64 pipe.  Rows and products outside the range in
-// which these steps neither overflow nor underflow take fp64 throughout.  Results
-// equal mla_branch_prologue's bit for bit (bf16 rows, queries).
+// floats; c * gamma is exact in fp32.  What is left is one fma, of an exact product and a
+// small or exact term, and it is rounded to odd: of its value rounded down and rounded up
+// the one whose last bit is set (the two are equal if it is exact).  Rounding that to
+// bf16 rounds the exact value, since no odd fp32 number lies on a bf16 boundary.  The
+// same goes for the rotations.  (With TwoSum and a rounding of the pair in integers, four
+// times the operations, 8,483 prompt tokens took 262 us, twice the time of their bytes.)
+// Rows and products outside the range in which these steps neither overflow nor
+// underflow take fp64 throughout.  Results equal mla_branch_prologue's bit for bit (bf16
+// rows, queries; a NaN is a NaN).
 //
 // Layout.  A warp takes a row (16 consecutive values a lane: two lanes hold one group
 // of 32); a block of 256 threads takes 16 KB of a token's queries, 16 bytes a thread
@@ -71,33 +75,29 @@ __device__ __forceinline__ void two_sum(float a, float b, float& hi, float& lo) 
   lo = __fadd_rn(__fsub_rn(a, __fsub_rn(hi, z)), __fsub_rn(b, z));
 }
 
-// bf16 bits of hi + lo (|lo| at most half an fp32 ulp of hi), nearest, ties to even.
-__device__ __forceinline__ uint32_t round_pair(float hi, float lo) {
-  const uint32_t u = __float_as_uint(hi), mag = u & 0x7FFFFFFFu;
-  if (mag > 0x7F800000u) return 0x7FC0u;
-  const uint32_t rem = mag & 0xFFFFu, base = mag >> 16;
-  const float away = (u >> 31) ? -lo : lo;
-  const bool up = rem > 0x8000u || (rem == 0x8000u && (away > 0.f || (away == 0.f && (base & 1u))));
-  return ((u >> 16) & 0x8000u) | (base + (up ? 1u : 0u));
+// a * b + c rounded to odd.
+__device__ __forceinline__ float fma_odd(float a, float b, float c) {
+  const float down = __fmaf_rd(a, b, c), up = __fmaf_ru(a, b, c);
+  return __float_as_uint(down) & 1u ? down : up;
 }
 
-// bf16 bits of a double, rounded once: through fp32 rounded to odd (truncated, the
-// last bit set if anything was dropped), which the second rounding cannot mistake
-// for a halfway point.
-__device__ __forceinline__ uint32_t round_double(double x) {
-  float f = __double2float_rz(x);
-  if (isfinite(f) && (double)f != x) f = __uint_as_float(__float_as_uint(f) | 1u);
-  return round_pair(f, 0.f);
+// Two floats as a bf16 pair, the first in the low half; nearest, ties to even.
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// The pair (x0, x1) of `x` turned by (cos, sin) of `f`, as a bf16 pair: the four
-// products are exact in fp32, their sums exact pairs.
+// A double as a float rounded to odd (truncated, the last bit set if anything was dropped).
+__device__ __forceinline__ float double_odd(double x) {
+  const float f = __double2float_rz(x);
+  return isfinite(f) && (double)f != x ? __uint_as_float(__float_as_uint(f) | 1u) : f;
+}
+
+// The pair (x0, x1) of `x` turned by (cos, sin) of `f`, as a bf16 pair (products of bf16 values
+// are exact in fp32).
 __device__ __forceinline__ uint32_t turn(uint32_t x, uint32_t f) {
   const float x0 = lo_f(x), x1 = hi_f(x), c = lo_f(f), s = hi_f(f);
-  float h0, l0, h1, l1;
-  two_sum(__fmul_rn(x0, c), -__fmul_rn(x1, s), h0, l0);
-  two_sum(__fmul_rn(x0, s), __fmul_rn(x1, c), h1, l1);
-  return round_pair(h0, l0) | (round_pair(h1, l1) << 16);
+  return pack(fma_odd(x0, c, -__fmul_rn(x1, s)), fma_odd(x0, s, __fmul_rn(x1, c)));
 }
 
 struct Place {
@@ -199,22 +199,16 @@ __device__ __forceinline__ void new_row(const Args& a, int t, int lane) {
   const double inv = rsqrt(sum / (double)a.L + a.eps);
   const float ih = (float)inv, il = (float)(inv - (double)ih);
 
-  auto scaled = [&](float v, float gm) -> uint32_t {
-    const float m = __fmul_rn(v, gm);
-    const float am = fabsf(m);
-    if (am >= 0x1p-40f && am <= 0x1p60f && ih >= 0x1p-60f && ih <= 0x1p60f) {
-      const float h = __fmul_rn(m, ih);
-      float hi, lo;
-      two_sum(h, __fmaf_rn(m, il, __fmaf_rn(m, ih, -h)), hi, lo);
-      return round_pair(hi, lo);
-    }
-    return round_double((double)v * inv * (double)gm);
+  auto scaled = [&](float v, float gm) {   // v * inv * gm rounded to odd
+    const float m = __fmul_rn(v, gm), am = fabsf(m);
+    if (am >= 0x1p-40f && am <= 0x1p60f && ih >= 0x1p-60f && ih <= 0x1p60f) return fma_odd(m, ih, __fmul_rn(m, il));
+    return double_odd((double)v * inv * (double)gm);
   };
   uint32_t y[8];
   uint32_t amax = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    y[i] = have ? scaled(lo_f(x[i]), lo_f(g[i])) | (scaled(hi_f(x[i]), hi_f(g[i])) << 16) : 0u;
+    y[i] = have ? pack(scaled(lo_f(x[i]), lo_f(g[i])), scaled(hi_f(x[i]), hi_f(g[i]))) : 0u;
     amax = max(amax, max(y[i] & 0x7FFFu, (y[i] >> 16) & 0x7FFFu));
   }
 
