@@ -26,10 +26,11 @@
 // 128B-swizzled shared memory.  TMEM: O (256) | S, two 64-column buffers |
 // Q latent (128).  Narrow latents (64) run the same code on one CTA.
 //
-// Warp roles (224 threads; 352 with the converter warps of an e4m3 cache):
+// Warp roles (224 threads; 352 with the converter warps of an e4m3 cache; for the e2m1
+// cache's 512 see Cfg::kGrouped):
 //   warp 0      TMA producer: the query's shared-memory part once per segment,
 //               cache tiles through the page table into a kStages-deep ring,
-//               and an L2 prefetch of the tile two ahead.
+//               and (not e2m1) an L2 prefetch of the tile two ahead.
 //   warp 1      TMEM owner and QK issuer (one thread); its other lanes zero
 //               cache rows outside the key range before the MMAs read them
 //               (0 * NaN would poison P . C).
@@ -38,7 +39,7 @@
 //               domain, writes P (bf16 pairs) back into TMEM where the P . C
 //               MMA takes it as its A operand, rescales O only when the running
 //               max grows by more than 2^8, and writes the segment's output.
-//   warps 6-9   (e4m3 cache; 8-11 over an e2m1 cache, see Cfg) widen the tile's codes x scale into bf16.
+//   warps 6-9   (e4m3 cache) widen the tile's codes x scale into bf16.
 //   last warp   P . C issuer (one thread), so a ready P never waits behind a QK.
 // Every wait is bounded in time; a timeout sets a status bit and the kernel
 // unwinds without hanging.
@@ -63,7 +64,7 @@ enum LoadMode : int {
   kLoadFp8 = 1,     // e4m3 pool through the page table: TMA bytes (multicast), widened by converter warps
   kLoadSparse = 2,  // bf16 pool rows named by an index list, TMA gather4: each CTA gathers half
                     // of a tile's boxes and multicasts them to both CTAs of the cluster
-  kLoadFp4 = 3,     // e2m1 pool through the page table: TMA bytes (multicast), widened like e4m3
+  kLoadFp4 = 3,     // e2m1 pool through the page table: whole rows by bulk copies, widened into f16
 };
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: rescale O when the max grows by > 2^8
 // The producer reads the page-table entries of the tile this many ahead of the one it
@@ -123,6 +124,14 @@ struct Cfg {
   // eight neighbouring rows start in eight different bank groups
   static constexpr int kRow4 = (L / 2 + L / 32 + 15) / 16 * 16;
   static constexpr int kRawOff = NLB >= 8 ? 4 * kBox : 0;   // codes land where the last latent boxes go
+  // The e2m1 pair: each CTA loads the whole tile for itself, into the latent half that only the
+  // QK reads, as soon as that product is done with the tile before; the load passes under the
+  // softmax and the P . C, which needs the other half.  400 bytes a key are too few for a
+  // multicast, which waits for both CTAs, to gain: 64 requests of 1,024 to 8,192 tokens 228
+  // us with one, 208 us without.  Nor is an L2 prefetch worth its instructions here (244 us
+  // with it, 216 us without: the roles' code together is more than the SM's instruction cache
+  // holds, and what the producer runs costs the other warps' fetches).
+  static constexpr bool kEarly = kMode == kLoadFp4 && CL == 2;
   static constexpr int kConvThreads = 64 * NRH;                // warps 6.. (kCoded): one per row and raw box
   // The e2m1 instance lays its warps out by warpgroup (0 load, 1 QK, 2 P . C, 3 rope | 4-7
   // softmax | 8.. converters) so that the softmax's get the registers that the first four do
@@ -592,11 +601,13 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
   // e4m3 row (an e2m1 row is copied whole)
   const int rope_x0 = MODE == kLoadFp8 ? L / 2 : L;
   const int row4 = C::kRow4 + 2 * a.d.qk_rope;   // bytes of an e2m1 row
+  // where e2m1 rows land: the boxes of the other CTA's latent half
+  const int raw_off = C::kEarly ? (crank == 0 ? C::NLB / 2 : 0) * C::kBox : C::kRawOff;
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&cs->kv_full[s], 1);
-      mbar_init(&cs->kv_empty[s], CL);   // one tcgen05.commit from each CTA of the cluster
+      mbar_init(&cs->kv_empty[s], C::kEarly ? 1 : CL);   // one tcgen05.commit from each CTA of the cluster
       mbar_init(&cs->kv_conv[s], C::kConvThreads + (C::kGrouped ? 32 : 0));   // ... and the rope warp
       mbar_init(&cs->kv_conv_a[s], C::kConvThreads);
     }
@@ -644,9 +655,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
 
   const int g0 = a.bounds[k], g1 = a.bounds[k + 1];
   const int ps = a.ks.page_size;
-  // e2m1 rows lie one behind the other, so the CTAs of a cluster share a tile by rows
-  constexpr int kMaxLoadRows = MODE == kLoadFp4 ? kTileKeys / 2 : kTileKeys;
-  const int rows_per_load = ps < kMaxLoadRows ? ps : kMaxLoadRows;
+  const int rows_per_load = ps < kTileKeys ? ps : kTileKeys;
 
   if (C::kGrouped && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == 0) {
@@ -723,17 +732,14 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
       // L2 prefetch of this CTA's boxes of tile `it` (paged modes): its load, issued
       // when a stage frees up, then reads L2 instead of waiting on HBM
       auto prefetch_from = [&](int it, const bool (&v)[2], const int (&pg)[2]) {
-        if (MODE == kLoadSparse || it >= ie) return;
+        if (MODE == kLoadSparse || MODE == kLoadFp4 || it >= ie) return;
         const uint64_t mask = (uint64_t)__ballot_sync(0xffffffffu, v[0]) |
                               ((uint64_t)__ballot_sync(0xffffffffu, v[1]) << 32);
         for (int p = 0; p < nloads; ++p) {
           const uint64_t pm = (mask >> (p * rows_per_load)) & lmask;
           if (!pm) continue;
           const int y = load_row(it, p, pm, pg);
-          if (MODE == kLoadFp4) {
-            if (lane == 0 && p % CL == (int)crank)
-              bulk_prefetch_l2(static_cast<const uint8_t*>(a.kv_pool) + (size_t)y * row4, (uint32_t)(rows_per_load * row4));
-          } else if (lane < kOwn) {
+          if (lane < kOwn) {
             if (MODE == kLoadFp8) tma_prefetch_2d(&maps.kv_lat, ((int)crank * kOwn + lane) * C::RW, y);
             else tma_prefetch_2d(&maps.kv_lat, 64 * ((int)crank * kOwn + lane), y);
           } else if (lane == kOwn && crank == 0) {
@@ -786,13 +792,14 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         // tile two ahead after issuing this one's loads instead.
         int raw[2], raw2[2];
         fetch(it, raw);
-        const bool pf = (MODE == kLoadDense || MODE == kLoadFp4) && it + kPrefetchAhead < ie;
+        const bool pf = MODE == kLoadDense && it + kPrefetchAhead < ie;
         if (pf) fetch(it + kPrefetchAhead, raw2);
         bool v[2], v2[2];
         int rid[2], pg[2], rid2[2], pg2[2];
         if (MODE == kLoadFp8 || MODE == kLoadSparse) finish(it, raw, v, rid, pg);
         // stage s is free in both CTAs once both have committed their P . C of its last tile
-        if (c >= S && !wwait(&cs->kv_empty[s], ((c / S) & 1) ^ 1, cs, hdr)) return;
+        // (kEarly: the half that the rows go to is free once the QK of its last tile is done)
+        if (c >= S && !wwait(C::kEarly ? &cs->s_full[c & 1] : &cs->kv_empty[s], ((c / S) & 1) ^ 1, cs, hdr)) return;
         if (MODE == kLoadDense || MODE == kLoadFp4) finish(it, raw, v, rid, pg);
         if (pf) finish(it + kPrefetchAhead, raw2, v2, rid2, pg2);
         if (MODE == kLoadSparse) {
@@ -844,7 +851,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
           for (int p = 0; p < nloads; ++p)
             if ((mask >> (p * rows_per_load)) & lmask) live_rows += rows_per_load;
           if (lane == 0) {
-            cs->row_mask[s] = mask;
+            cs->row_mask[C::kEarly ? c & 3 : s] = mask;
             mbar_arrive_expect_tx(&cs->kv_full[s], live_rows * row_bytes);
           }
           __syncwarp();
@@ -855,14 +862,9 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
             const int y = load_row(it, p, pm, pg);
             // one box per lane: this CTA's share of the latent (or raw e4m3) boxes, then the rope box (rank 0)
             if (MODE == kLoadFp4) {
-              if (p % CL == (int)crank && lane == 0) {
-                const uint8_t* rows = static_cast<const uint8_t*>(a.kv_pool) + (size_t)y * row4;
-                if (CL >= 2)
-                  bulk_copy_g2s_mc(st + C::kRawOff + r0 * row4, rows, (uint32_t)(rows_per_load * row4), &cs->kv_full[s],
-                                   (uint16_t)C::kMcMask);
-                else
-                  bulk_copy_g2s(st + C::kRawOff + r0 * row4, rows, (uint32_t)(rows_per_load * row4), &cs->kv_full[s]);
-              }
+              if (lane == 0)
+                bulk_copy_g2s(st + raw_off + r0 * row4, static_cast<const uint8_t*>(a.kv_pool) + (size_t)y * row4,
+                              (uint32_t)(rows_per_load * row4), &cs->kv_full[s]);
             } else if (lane < kOwn) {
               if (MODE == kLoadFp8) {
                 const int h = (int)crank * kOwn + lane;
@@ -915,7 +917,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
       for (int j = c - S; j < c; ++j) {
         if (j < 0) continue;
         mbar_wait(&cs->kv_full[j % S], (j / S) & 1, kWaitLimitNs);
-        if (CL >= 2) mbar_wait(&cs->kv_empty[j % S], (j / S) & 1, kWaitLimitNs);
+        if (CL >= 2) mbar_wait(&cs->kv_empty[j % S], (j / S) & 1, kWaitLimitNs);   // (kEarly: its own)
       }
     }
   } else if (warp == 1) {
@@ -945,7 +947,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         if (!wwait(!C::kCoded ? &cs->kv_full[s] : C::NRH > 1 ? &cs->kv_conv_a[s] : &cs->kv_conv[s], par, cs,
                    hdr))
           return;
-        const uint64_t mask = cs->row_mask[s];
+        const uint64_t mask = C::kCoded ? ~0ull : cs->row_mask[s];
         if (!C::kCoded && mask != ~0ull) {
           // Rows outside the key range may hold anything (NaN included).  Their
           // scores are dropped by the row mask, not by value, so only this CTA's
@@ -966,11 +968,17 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         tc_fence_after();
         const uint64_t dk = dk0 + (uint64_t)((s * C::kStageBytes) >> 4);
         const uint32_t sd = tmem + C::kSCol + 64 * b;
+        // One elected lane issues: behind elect.sync the compiler knows that one thread runs
+        // the loop, behind lane == 0 it does not (64 e2m1 requests of 1,024 to 8,192 tokens:
+        // 208 -> 195 us).
+        // kEarly, CTA 1: its own latent half, the first that is widened, is the shared-memory
+        // part of the query; that goes first there, then the TMEM part, then the rope
+        const bool smem_first = C::kEarly && crank == 1;
         // latent [0, QT): A = query in TMEM; then latent [QT, L) and the rope
         // (64 columns; past qk_rope both sides read the TMA zero fill) with A =
         // query boxes in shared memory.  The MMA queue is shallow, so the issue
         // runs back to back; the box loops stay rolled to keep the code small.
-        if (lane == 0) {
+        if (!smem_first && elect_one()) {
 #pragma unroll 1
           for (int j = 0; j < C::QT / 64; ++j) {
             const uint64_t dkj = dk + (uint64_t)((j * C::kBox) >> 4);
@@ -986,15 +994,35 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
           tc_fence_after();
           q_smem = true;
         }
+        if (smem_first && elect_one()) {
+#pragma unroll 1
+          for (int i = 0; i < C::NQS; ++i) {
+            const uint64_t dqi = dq0 + (uint64_t)((i * C::kQBox) >> 4);
+            const uint64_t dki = dk + (uint64_t)(((C::QT / 64 + i) * C::kBox) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ss(sd, dqi + (uint64_t)((kk * 32) >> 4), dki + (uint64_t)((kk * 32) >> 4), idesc_qk,
+                     (i > 0 || kk > 0) ? 1u : 0u);
+          }
+        }
         if (C::kCoded && C::NRH > 1) {
           // the rest of the tile's latent columns and the dead rows' rope zeros
           __syncwarp();
           if (!wwait(&cs->kv_conv[s], par, cs, hdr)) return;
           tc_fence_after();
         }
-        if (lane == 0) {
+        if (smem_first && elect_one()) {
 #pragma unroll 1
-          for (int i = 0; i <= C::NQS; ++i) {
+          for (int j = 0; j < C::QT / 64; ++j) {
+            const uint64_t dkj = dk + (uint64_t)((j * C::kBox) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts(sd, tmem + C::kQCol + 8 * (4 * j + kk), dkj + (uint64_t)((kk * 32) >> 4), idesc_qk, 1u);
+          }
+        }
+        if (elect_one()) {
+#pragma unroll 1
+          for (int i = smem_first ? C::NQS : 0; i <= C::NQS; ++i) {
             // box i of the query buffer pairs with cache box QT / 64 + i (the rope box after the latent ones)
             const uint64_t dqi = dq0 + (uint64_t)((i * C::kQBox) >> 4);
             const uint64_t dki = dk + (uint64_t)(((C::QT / 64 + i) * C::kBox) >> 4);
@@ -1027,14 +1055,14 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         if (!wwait(&cs->p_full[b], (cp >> 1) & 1, cs, hdr)) return;
         if (it == ia && si > 0 && !wwait(&cs->o_free, (si - 1) & 1, cs, hdr)) return;
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           // B = this CTA's latent boxes of the stage, keys along K (MN-major)
           const uint64_t dv = dv0 + (uint64_t)(((cp % S) * C::kStageBytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_ts(tmem, tmem + C::kSCol + 64 * b + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4), idesc_pv,
                    (it == ia && kk == 0) ? 0u : 1u);
-          if (CL >= 2) mma_commit_mc(&cs->kv_empty[cp % S], (uint16_t)C::kMcMask);
+          if (CL >= 2 && !C::kEarly) mma_commit_mc(&cs->kv_empty[cp % S], (uint16_t)C::kMcMask);
           else mma_commit(&cs->kv_empty[cp % S]);
           mma_commit(&cs->pv_done[b]);
         }
@@ -1130,13 +1158,13 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         const int s = c % S;
         if (!wwait(&cs->kv_full[s], (c / S) & 1, cs, hdr)) return;
         uint8_t* st = sStage + s * C::kStageBytes;
-        const uint64_t mask = cs->row_mask[s];
+        const uint64_t mask = cs->row_mask[C::kEarly ? c & 3 : s];
 #pragma unroll 1
         for (int r = lane; r < 64; r += 32) {
-          const uint8_t* src = st + C::kRawOff + r * row4 + C::kRow4;
+          const uint8_t* src = st + raw_off + r * row4 + C::kRow4;
           uint8_t* dst = st + C::NLB * C::kBox + r * 128;
           const int nch = (mask >> r) & 1ull ? a.d.qk_rope / 8 : 0;
-#pragma unroll
+#pragma unroll 1
           for (int ch = 0; ch < 8; ++ch) {
             uint4 v = make_uint4(0, 0, 0, 0);
             if (ch < nch) v = *reinterpret_cast<const uint4*>(src + 16 * ch);
@@ -1158,8 +1186,8 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
     if (isinf(big.x) || isinf(big.y)) atomicOr(&hdr->status, kDeviceCheckFailed);
   } else if (MODE == kLoadFp4 && warp >= C::kConvWarp) {
     // ------------------------------------------------------------- e2m1 converters
-    // Tile row crow is widened by NRH threads, pass p taking its codes of latent
-    // [p RW, (p + 1) RW), thread hh the hh-th RW / NRH of them: groups of 32 codes
+    // Tile row crow is widened by NRH threads, pass p taking its codes of one
+    // latent half, thread hh the hh-th RW / NRH of them: groups of 32 codes
     // (16 bytes) under one scale byte.  The operands are f16: a code times 2^e is exact
     // for e in [-23, 13], and the absorbed query and P lose 2^-12 instead of 2^-9.  The
     // scale goes into the lookup tables of e2m1x8_f16 where all products are normal
@@ -1176,11 +1204,14 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         const int s = c % S;
         if (!wwait(&cs->kv_full[s], (c / S) & 1, cs, hdr)) return;
         uint8_t* st = sStage + s * C::kStageBytes;
-        const bool live = (cs->row_mask[s] >> crow) & 1ull;
-        const uint8_t* src = st + C::kRawOff + crow * row4;
+        const bool live = (cs->row_mask[C::kEarly ? c & 3 : s] >> crow) & 1ull;
+        const uint8_t* src = st + raw_off + crow * row4;
+        // the first pass overwrites what the P . C of the stage's last tile reads
+        if (C::kEarly && c >= S && !wwait(&cs->kv_empty[s], ((c / S) & 1) ^ 1, cs, hdr)) return;
 #pragma unroll 1
         for (int p = 0; p < C::NRH; ++p) {
-          const int grp0 = p * (C::RW / 32) + hh * kGroups;
+          // this CTA's own latent half first, then the one that the rows lie in
+          const int grp0 = (C::kEarly ? p ^ (int)rank : p) * (C::RW / 32) + hh * kGroups;
           // the loop over groups stays rolled, the next group moving up in registers: five roles
           // of warps run different code on each SM, and unrolled it does not stay in the
           // instruction cache (ncu: 36 % of the fetches missed)
@@ -1230,7 +1261,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
             sb >>= 8;
           }
           fence_proxy_async_smem();
-          // after all but the last pass: latent [0, RW) is in place, the QK's TMEM-operand part may start
+          // after all but the last pass: one latent half is in place, the QK's part of it may start
           mbar_arrive(C::NRH > 1 && p == 0 ? &cs->kv_conv_a[s] : &cs->kv_conv[s]);
         }
       }
@@ -1296,8 +1327,11 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
       for (int it = ia; it < ie; ++it, ++c) {
         if (waborted(cs)) return;
         const int s = c % S, b = c & 1;
-        if (!wwait(&cs->kv_full[s], (c / S) & 1, cs, hdr)) return;   // row mask visibility
-        uint64_t mask = cs->row_mask[s];
+        // row mask visibility (kEarly: the next tile's rows may land before this one's scores are
+        // read, so its barrier is not waited for here; the mask comes with the scores)
+        uint64_t* mask_bar = C::kEarly ? &cs->s_full[b] : &cs->kv_full[s];
+        if (!wwait(mask_bar, C::kEarly ? (c >> 1) & 1 : (c / S) & 1, cs, hdr)) return;
+        uint64_t mask = cs->row_mask[C::kEarly ? c & 3 : s];
         if (own_mask) {
           // keys of the tile outside this token's own range do not count
           const int key0 = (tp.tile_first + it) * kTileKeys;
@@ -1306,7 +1340,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
           const uint64_t below = a1 >= 64 ? ~0ull : (a1 <= 0 ? 0ull : (1ull << a1) - 1);
           mask &= above & below;
         }
-        if (!wwait(&cs->s_full[b], (c >> 1) & 1, cs, hdr)) return;
+        if (!C::kEarly && !wwait(&cs->s_full[b], (c >> 1) & 1, cs, hdr)) return;
         tc_fence_after();
         // S row (64 fp32) for this thread's head; both halves of the load in flight at once
         uint32_t sr[64];
