@@ -27,7 +27,7 @@
 // Q latent (128).  Narrow latents (64) run the same code on one CTA.
 //
 // Warp roles (224 threads; 352 with the converter warps of an e4m3 cache; for the e2m1
-// cache's 512 see Cfg::kGrouped):
+// cache's 384 see Cfg::kGrouped):
 //   warp 0      TMA producer: the query's shared-memory part once per segment,
 //               cache tiles through the page table into a kStages-deep ring,
 //               and (not e2m1) an L2 prefetch of the tile two ahead.
@@ -132,7 +132,8 @@ struct Cfg {
   // with it, 216 us without: the roles' code together is more than the SM's instruction cache
   // holds, and what the producer runs costs the other warps' fetches).
   static constexpr bool kEarly = kMode == kLoadFp4 && CL == 2;
-  static constexpr int kConvThreads = 64 * NRH;                // warps 6.. (kCoded): one per row and raw box
+  static constexpr int kConvPer = kMode == kLoadFp4 && kCluster == 2 ? 2 * NRH : NRH;
+  static constexpr int kConvThreads = 64 * kConvPer;                // warps 6.. (kCoded): one per row and raw box
   // The e2m1 instance lays its warps out by warpgroup (0 load, 1 QK, 2 P . C, 3 rope | 4-7
   // softmax | 8.. converters) so that the softmax's get the registers that the first four do
   // not need: 104 / 232 / 168 of 168 each.  Spilled, a row of scores goes to L2, since shared
@@ -606,9 +607,9 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&cs->kv_full[s], 1);
-      mbar_init(&cs->kv_empty[s], C::kEarly ? 1 : CL);   // one tcgen05.commit from each CTA of the cluster
-      mbar_init(&cs->kv_conv[s], C::kConvThreads + (C::kGrouped ? 32 : 0));   // ... and the rope warp
+      mbar_init(&cs->kv_full[s], C::kEarly ? 2 : 1);
+      mbar_init(&cs->kv_empty[s], CL);   // one tcgen05.commit from each CTA of the cluster
+      mbar_init(&cs->kv_conv[s], C::kConvThreads);
       mbar_init(&cs->kv_conv_a[s], C::kConvThreads);
     }
     mbar_init(&cs->q_full, 1 + 128);     // producer (TMA bytes) + every softmax thread (TMEM part)
@@ -621,7 +622,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
       mbar_init(&cs->pv_done[b], 1);
     }
     mbar_init(&cs->o_free, 128);
-    mbar_init(&cs->conv_sync, C::kConvThreads + (C::kGrouped ? 32 : 0));
+    mbar_init(&cs->conv_sync, C::kConvThreads);
     mbar_init(&cs->fix_bar, 128);
     mbar_init(&cs->fix_done, 1);
     for (int i = 0; i < 2; ++i) {
@@ -657,7 +658,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
   const int ps = a.ks.page_size;
   const int rows_per_load = ps < kTileKeys ? ps : kTileKeys;
 
-  if (C::kGrouped && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  if (C::kGrouped && warp < 4) { if (C::kConvThreads == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;"); }
   if (warp == 0) {
     // ------------------------------------------------------------- producer
     auto load_box = [&](void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
@@ -732,7 +733,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
       // L2 prefetch of this CTA's boxes of tile `it` (paged modes): its load, issued
       // when a stage frees up, then reads L2 instead of waiting on HBM
       auto prefetch_from = [&](int it, const bool (&v)[2], const int (&pg)[2]) {
-        if (MODE == kLoadSparse || MODE == kLoadFp4 || it >= ie) return;
+        if (MODE == kLoadSparse || it >= ie) return;
         const uint64_t mask = (uint64_t)__ballot_sync(0xffffffffu, v[0]) |
                               ((uint64_t)__ballot_sync(0xffffffffu, v[1]) << 32);
         for (int p = 0; p < nloads; ++p) {
@@ -755,11 +756,60 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         }
         __syncwarp();
       };
+      // e2m1: lane p's page of the coming tile (load p of it) and of the two after it, read
+      // three tiles ahead: with the page table's latency and the page arithmetic in between,
+      // a load went out 1,300 cycles after its place was free, of 4,000 a tile.
+      int pages[3];
+      auto page_of = [&](int it) {
+        const int key = (tp.tile_first + it) * kTileKeys + lane * rows_per_load;
+        const bool reads = it < ie && lane < nloads && key < tp.hi && key + rows_per_load > tp.lo;
+        return reads ? a.ks.block_table[(size_t)tp.b * a.ks.bt_stride + key / ps] : -1;
+      };
+      if (MODE == kLoadFp4) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) pages[i] = page_of(ia + i);
+      }
+      auto load_coded = [&](int it) -> bool {   // one tile of e2m1 rows, lane p issuing load p
+        const int s = c % S;
+        const int key0 = (tp.tile_first + it) * kTileKeys, key = key0 + lane * rows_per_load;
+        const bool wanted = lane < nloads && key < tp.hi && key + rows_per_load > tp.lo;
+        const bool ok = wanted && pages[0] >= 0 && pages[0] < a.ks.num_pages;
+        const uint32_t all = __ballot_sync(0xffffffffu, ok);
+        // live rows: the tile's part of the key range, less the loads of pages that do not exist
+        const int a0 = tp.lo - key0, a1 = tp.hi - key0;
+        uint64_t mask = (a0 <= 0 ? ~0ull : a0 >= 64 ? 0ull : ~0ull << a0) & (a1 >= 64 ? ~0ull : a1 <= 0 ? 0ull : (1ull << a1) - 1);
+        for (uint32_t b = __ballot_sync(0xffffffffu, wanted && !ok); b; b &= b - 1) {
+          mask &= ~(lmask << ((__ffs((int)b) - 1) * rows_per_load));
+          bad = true;
+        }
+        const int row = key % ps;   // the page's
+        const uint8_t* src = static_cast<const uint8_t*>(a.kv_pool) + ((size_t)(ok ? pages[0] : 0) * ps + row) * row4;
+        const uint32_t bytes = (uint32_t)(rows_per_load * row4);
+        uint8_t* dst = sStage + s * C::kStageBytes + raw_off + lane * bytes;
+        // the place is free once the QK (kEarly) or the P . C of the stage's last tile is done
+        if (c >= S && !wwait(C::kEarly ? &cs->s_full[c & 1] : &cs->kv_empty[s], ((c / S) & 1) ^ 1, cs, hdr)) return false;
+        if (lane == 0) {
+          cs->row_mask[C::kEarly ? c & 3 : s] = mask;
+          mbar_arrive_expect_tx(&cs->kv_full[s], (uint32_t)__popc(all) * bytes);
+          // kEarly: the barrier's other arrival comes from the P . C of the stage's last tile
+          if (C::kEarly && c < S) mbar_arrive(&cs->kv_full[s]);
+        }
+        __syncwarp();
+        if (ok) bulk_copy_g2s(dst, src, bytes, &cs->kv_full[s]);
+        // into L2, for both CTAs: this lane's load of the tile two ahead (one of them asks for it)
+        const int key2 = key + 2 * kTileKeys;
+        if (pages[2] >= 0 && pages[2] < a.ks.num_pages && ((it ^ (int)crank) & (CL - 1)) == 0)
+          bulk_prefetch_l2(static_cast<const uint8_t*>(a.kv_pool) + ((size_t)pages[2] * ps + key2 % ps) * row4, bytes);
+        pages[0] = pages[1];
+        pages[1] = pages[2];
+        pages[2] = page_of(it + 3);
+        return true;
+      };
       // the partition's first query goes out before any page-table read: the
       // first QK waits on it, not on the cache
       const bool qa_sent = si == 0;
       if (qa_sent) issue_qa();
-      if (si > 0 && MODE != kLoadSparse && ia + 1 < ie) {
+      if (si > 0 && MODE != kLoadSparse && MODE != kLoadFp4 && ia + 1 < ie) {
         // a later segment waits for a free stage first: bring its second tile
         // into L2 meanwhile
         bool v1[2];
@@ -786,106 +836,104 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
             bulk_prefetch_l2(a.part_lse + (size_t)(kk * 2 * NS + tslot) * 2 * Hh, (uint32_t)(2 * Hh * 4));
           }
         }
-        // global reads of this tile and (bf16 pool) of the one two ahead, for its
-        // L2 prefetch, issued together before the wait for the stage so their
-        // latency overlaps it.  The e4m3 kernel, short of registers, reads the
-        // tile two ahead after issuing this one's loads instead.
-        int raw[2], raw2[2];
-        fetch(it, raw);
-        const bool pf = MODE == kLoadDense && it + kPrefetchAhead < ie;
-        if (pf) fetch(it + kPrefetchAhead, raw2);
-        bool v[2], v2[2];
-        int rid[2], pg[2], rid2[2], pg2[2];
-        if (MODE == kLoadFp8 || MODE == kLoadSparse) finish(it, raw, v, rid, pg);
-        // stage s is free in both CTAs once both have committed their P . C of its last tile
-        // (kEarly: the half that the rows go to is free once the QK of its last tile is done)
-        if (c >= S && !wwait(C::kEarly ? &cs->s_full[c & 1] : &cs->kv_empty[s], ((c / S) & 1) ^ 1, cs, hdr)) return;
-        if (MODE == kLoadDense || MODE == kLoadFp4) finish(it, raw, v, rid, pg);
-        if (pf) finish(it + kPrefetchAhead, raw2, v2, rid2, pg2);
-        if (MODE == kLoadSparse) {
-          cs->rowid[s][lane] = rid[0];
-          cs->rowid[s][lane + 32] = rid[1];
-        }
-        const uint64_t mask = (uint64_t)__ballot_sync(0xffffffffu, v[0]) |
-                              ((uint64_t)__ballot_sync(0xffffffffu, v[1]) << 32);
-        uint8_t* st = sStage + s * C::kStageBytes;
-        uint8_t* st_rope = st + C::NLB * C::kBox;
-        if (MODE == kLoadSparse) {
-          // every row is fetched (row 0 stands in for a dead slot; its P . C part is zeroed);
-          // each CTA gathers half of the boxes and multicasts them to both
-          if (lane == 0) {
-            cs->row_mask[s] = mask;
-            mbar_arrive_expect_tx(&cs->kv_full[s], 64 * (C::NLB + 1) * 128);
-          }
-          __syncwarp();
-          if (lane < 16) {
-            // this CTA's share of the boxes (both CTAs see the same rows), multicast
-            const int r0 = 4 * lane;
-            const int y0 = cs->rowid[s][r0], y1 = cs->rowid[s][r0 + 1];
-            const int y2 = cs->rowid[s][r0 + 2], y3 = cs->rowid[s][r0 + 3];
-            constexpr int kOwnBoxes = C::NLB / CL;
-#pragma unroll
-            for (int j = 0; j < kOwnBoxes; ++j) {
-              const int i = (int)crank * kOwnBoxes + j;
-              if (CL >= 2)
-                tma_gather4_mc(st + i * C::kBox + r0 * 128, &maps.kv_lat, &cs->kv_full[s], 64 * i, y0, y1, y2, y3,
-                               (uint16_t)C::kMcMask);
-              else
-                tma_gather4(st + i * C::kBox + r0 * 128, &maps.kv_lat, &cs->kv_full[s], 64 * i, y0, y1, y2, y3);
-            }
-            if (crank == 0) {
-              if (CL >= 2)
-                tma_gather4_mc(st_rope + r0 * 128, &maps.kv_rope, &cs->kv_full[s], rope_x0, y0, y1, y2, y3,
-                               (uint16_t)C::kMcMask);
-              else
-                tma_gather4(st_rope + r0 * 128, &maps.kv_rope, &cs->kv_full[s], rope_x0, y0, y1, y2, y3);
-            }
-          }
+        if constexpr (MODE == kLoadFp4) {
+          if (!load_coded(it)) return;
         } else {
-          // pages of this tile that hold at least one live row; both CTAs count the
-          // same bytes, most of which the other CTAs' multicasts deliver (an e4m3 row's
-          // 4-byte scale each CTA copies for itself)
-          const uint32_t row_bytes =
-              MODE == kLoadFp4 ? (uint32_t)row4 : (MODE == kLoadFp8 ? L + 4 : C::NLB * 128) + 128;
-          uint32_t live_rows = 0;
-          for (int p = 0; p < nloads; ++p)
-            if ((mask >> (p * rows_per_load)) & lmask) live_rows += rows_per_load;
-          if (lane == 0) {
-            cs->row_mask[C::kEarly ? c & 3 : s] = mask;
-            mbar_arrive_expect_tx(&cs->kv_full[s], live_rows * row_bytes);
+          // global reads of this tile and (bf16 pool) of the one two ahead, for its
+          // L2 prefetch, issued together before the wait for the stage so their
+          // latency overlaps it.  The e4m3 kernel, short of registers, reads the
+          // tile two ahead after issuing this one's loads instead.
+          int raw[2], raw2[2];
+          fetch(it, raw);
+          const bool pf = MODE == kLoadDense && it + kPrefetchAhead < ie;
+          if (pf) fetch(it + kPrefetchAhead, raw2);
+          bool v[2], v2[2];
+          int rid[2], pg[2], rid2[2], pg2[2];
+          if (MODE == kLoadFp8 || MODE == kLoadSparse) finish(it, raw, v, rid, pg);
+          // stage s is free in both CTAs once both have committed their P . C of its last tile
+          if (c >= S && !wwait(&cs->kv_empty[s], ((c / S) & 1) ^ 1, cs, hdr)) return;
+          if (MODE == kLoadDense) finish(it, raw, v, rid, pg);
+          if (pf) finish(it + kPrefetchAhead, raw2, v2, rid2, pg2);
+          if (MODE == kLoadSparse) {
+            cs->rowid[s][lane] = rid[0];
+            cs->rowid[s][lane + 32] = rid[1];
           }
-          __syncwarp();
-          for (int p = 0; p < nloads; ++p) {
-            const uint64_t pm = (mask >> (p * rows_per_load)) & lmask;
-            if (!pm) continue;
-            const int r0 = p * rows_per_load;
-            const int y = load_row(it, p, pm, pg);
-            // one box per lane: this CTA's share of the latent (or raw e4m3) boxes, then the rope box (rank 0)
-            if (MODE == kLoadFp4) {
-              if (lane == 0)
-                bulk_copy_g2s(st + raw_off + r0 * row4, static_cast<const uint8_t*>(a.kv_pool) + (size_t)y * row4,
-                              (uint32_t)(rows_per_load * row4), &cs->kv_full[s]);
-            } else if (lane < kOwn) {
-              if (MODE == kLoadFp8) {
-                const int h = (int)crank * kOwn + lane;
-                load_box(st + C::kRawOff + h * 64 * C::RW + r0 * C::RW, &maps.kv_lat, &cs->kv_full[s], h * C::RW, y);
-              } else {
-                const int i = (int)crank * kOwn + lane;
-                load_box(st + i * C::kBox + r0 * 128, &maps.kv_lat, &cs->kv_full[s], 64 * i, y);
-              }
-            } else if (lane == kOwn && crank == 0) {
-              load_box(st_rope + r0 * 128, &maps.kv_rope, &cs->kv_full[s], rope_x0, y);
-            } else if (MODE == kLoadFp8 && lane == kOwn + 1) {
-              // the load's row scales: rows y .. y + rows_per_load - 1 are consecutive
-              // (one page), y a multiple of 8, so the copy is 16-byte aligned
-              bulk_copy_g2s(&cs->rowid[s][r0], a.kv_scales + y, (uint32_t)rows_per_load * 4, &cs->kv_full[s]);
+          const uint64_t mask = (uint64_t)__ballot_sync(0xffffffffu, v[0]) |
+                                ((uint64_t)__ballot_sync(0xffffffffu, v[1]) << 32);
+          uint8_t* st = sStage + s * C::kStageBytes;
+          uint8_t* st_rope = st + C::NLB * C::kBox;
+          if (MODE == kLoadSparse) {
+            // every row is fetched (row 0 stands in for a dead slot; its P . C part is zeroed);
+            // each CTA gathers half of the boxes and multicasts them to both
+            if (lane == 0) {
+              cs->row_mask[s] = mask;
+              mbar_arrive_expect_tx(&cs->kv_full[s], 64 * (C::NLB + 1) * 128);
             }
-          }
-          if (pf) {
-            prefetch_from(it + kPrefetchAhead, v2, pg2);
-          } else if (MODE == kLoadFp8 && it + kPrefetchAhead < ie) {
-            lookup(it + kPrefetchAhead, v2, rid2, pg2);
-            prefetch_from(it + kPrefetchAhead, v2, pg2);
+            __syncwarp();
+            if (lane < 16) {
+              // this CTA's share of the boxes (both CTAs see the same rows), multicast
+              const int r0 = 4 * lane;
+              const int y0 = cs->rowid[s][r0], y1 = cs->rowid[s][r0 + 1];
+              const int y2 = cs->rowid[s][r0 + 2], y3 = cs->rowid[s][r0 + 3];
+              constexpr int kOwnBoxes = C::NLB / CL;
+#pragma unroll
+              for (int j = 0; j < kOwnBoxes; ++j) {
+                const int i = (int)crank * kOwnBoxes + j;
+                if (CL >= 2)
+                  tma_gather4_mc(st + i * C::kBox + r0 * 128, &maps.kv_lat, &cs->kv_full[s], 64 * i, y0, y1, y2, y3,
+                                 (uint16_t)C::kMcMask);
+                else
+                  tma_gather4(st + i * C::kBox + r0 * 128, &maps.kv_lat, &cs->kv_full[s], 64 * i, y0, y1, y2, y3);
+              }
+              if (crank == 0) {
+                if (CL >= 2)
+                  tma_gather4_mc(st_rope + r0 * 128, &maps.kv_rope, &cs->kv_full[s], rope_x0, y0, y1, y2, y3,
+                                 (uint16_t)C::kMcMask);
+                else
+                  tma_gather4(st_rope + r0 * 128, &maps.kv_rope, &cs->kv_full[s], rope_x0, y0, y1, y2, y3);
+              }
+            }
+          } else {
+            // pages of this tile that hold at least one live row; both CTAs count the
+            // same bytes, most of which the other CTAs' multicasts deliver (an e4m3 row's
+            // 4-byte scale each CTA copies for itself)
+            const uint32_t row_bytes = (MODE == kLoadFp8 ? L + 4 : C::NLB * 128) + 128;
+            uint32_t live_rows = 0;
+            for (int p = 0; p < nloads; ++p)
+              if ((mask >> (p * rows_per_load)) & lmask) live_rows += rows_per_load;
+            if (lane == 0) {
+              cs->row_mask[s] = mask;
+              mbar_arrive_expect_tx(&cs->kv_full[s], live_rows * row_bytes);
+            }
+            __syncwarp();
+            for (int p = 0; p < nloads; ++p) {
+              const uint64_t pm = (mask >> (p * rows_per_load)) & lmask;
+              if (!pm) continue;
+              const int r0 = p * rows_per_load;
+              const int y = load_row(it, p, pm, pg);
+              // one box per lane: this CTA's share of the latent (or raw e4m3) boxes, then the rope box (rank 0)
+              if (lane < kOwn) {
+                if (MODE == kLoadFp8) {
+                  const int h = (int)crank * kOwn + lane;
+                  load_box(st + C::kRawOff + h * 64 * C::RW + r0 * C::RW, &maps.kv_lat, &cs->kv_full[s], h * C::RW, y);
+                } else {
+                  const int i = (int)crank * kOwn + lane;
+                  load_box(st + i * C::kBox + r0 * 128, &maps.kv_lat, &cs->kv_full[s], 64 * i, y);
+                }
+              } else if (lane == kOwn && crank == 0) {
+                load_box(st_rope + r0 * 128, &maps.kv_rope, &cs->kv_full[s], rope_x0, y);
+              } else if (MODE == kLoadFp8 && lane == kOwn + 1) {
+                // the load's row scales: rows y .. y + rows_per_load - 1 are consecutive
+                // (one page), y a multiple of 8, so the copy is 16-byte aligned
+                bulk_copy_g2s(&cs->rowid[s][r0], a.kv_scales + y, (uint32_t)rows_per_load * 4, &cs->kv_full[s]);
+              }
+            }
+            if (pf) {
+              prefetch_from(it + kPrefetchAhead, v2, pg2);
+            } else if (MODE == kLoadFp8 && it + kPrefetchAhead < ie) {
+              lookup(it + kPrefetchAhead, v2, rid2, pg2);
+              prefetch_from(it + kPrefetchAhead, v2, pg2);
+            }
           }
         }
         __syncwarp();
@@ -917,7 +965,12 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
       for (int j = c - S; j < c; ++j) {
         if (j < 0) continue;
         mbar_wait(&cs->kv_full[j % S], (j / S) & 1, kWaitLimitNs);
-        if (CL >= 2) mbar_wait(&cs->kv_empty[j % S], (j / S) & 1, kWaitLimitNs);   // (kEarly: its own)
+        if (C::kEarly) {   // its P . C's commit has landed, with a last arrival in place of a load's
+          mbar_arrive(&cs->kv_full[j % S]);
+          mbar_wait(&cs->kv_full[j % S], ((j / S) & 1) ^ 1, kWaitLimitNs);
+        } else if (CL >= 2) {
+          mbar_wait(&cs->kv_empty[j % S], (j / S) & 1, kWaitLimitNs);
+        }
       }
     }
   } else if (warp == 1) {
@@ -1062,7 +1115,8 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
           for (int kk = 0; kk < 4; ++kk)
             mma_ts(tmem, tmem + C::kSCol + 64 * b + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4), idesc_pv,
                    (it == ia && kk == 0) ? 0u : 1u);
-          if (CL >= 2 && !C::kEarly) mma_commit_mc(&cs->kv_empty[cp % S], (uint16_t)C::kMcMask);
+          if (C::kEarly) mma_commit(&cs->kv_full[cp % S]);   // with the next rows' landing: they may be widened
+          else if (CL >= 2) mma_commit_mc(&cs->kv_empty[cp % S], (uint16_t)C::kMcMask);
           else mma_commit(&cs->kv_empty[cp % S]);
           mma_commit(&cs->pv_done[b]);
         }
@@ -1147,43 +1201,6 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         mbar_arrive(&cs->kv_conv[s]);
       }
     });
-  } else if (MODE == kLoadFp4 && warp == 3) {
-    // ------------------------------------------------------------- rope of e2m1 rows
-    // Two rows a lane, bf16 -> f16, into the tile's rope box (zeros past qk_rope and in dead rows).
-    __half2 top = __float2half2_rn(0.f);   // largest magnitude so far, NaN aside
-    int c = 0;
-    for_each_segment(a, k, g0, g1, [&](int si, int t, const TokenPlan& tp, int ia, int ie, bool, int) {
-      for (int it = ia; it < ie; ++it, ++c) {
-        if (waborted(cs)) return;
-        const int s = c % S;
-        if (!wwait(&cs->kv_full[s], (c / S) & 1, cs, hdr)) return;
-        uint8_t* st = sStage + s * C::kStageBytes;
-        const uint64_t mask = cs->row_mask[C::kEarly ? c & 3 : s];
-#pragma unroll 1
-        for (int r = lane; r < 64; r += 32) {
-          const uint8_t* src = st + raw_off + r * row4 + C::kRow4;
-          uint8_t* dst = st + C::NLB * C::kBox + r * 128;
-          const int nch = (mask >> r) & 1ull ? a.d.qk_rope / 8 : 0;
-#pragma unroll 1
-          for (int ch = 0; ch < 8; ++ch) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (ch < nch) v = *reinterpret_cast<const uint4*>(src + 16 * ch);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              w[e] = bf16x2_to_f16x2(w[e]);
-              top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&w[e])));
-            }
-            *reinterpret_cast<uint4*>(dst + ((ch ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-        mbar_arrive(&cs->conv_sync);   // the rows may be overwritten
-        fence_proxy_async_smem();
-        mbar_arrive(&cs->kv_conv[s]);
-      }
-    });
-    const float2 big = __half22float2(top);
-    if (isinf(big.x) || isinf(big.y)) atomicOr(&hdr->status, kDeviceCheckFailed);
   } else if (MODE == kLoadFp4 && warp >= C::kConvWarp) {
     // ------------------------------------------------------------- e2m1 converters
     // Tile row crow is widened by NRH threads, pass p taking its codes of one
@@ -1195,9 +1212,11 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
     // magnitude that f16 does not reach becomes an infinity and is reported.  The last pass
     // overwrites the rows, so it waits until every thread has read its part.
     const int ci = tid - 32 * C::kConvWarp, crow = ci & 63, hh = ci >> 6;
-    constexpr int kGroups = C::RW / C::NRH / 32;   // groups per thread and pass
+    if (C::kConvThreads == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    constexpr int kGroups = C::RW / C::kConvPer / 32;   // groups per thread and pass
     int c = 0;
     bool out_of_range = false;
+    __half2 top = __float2half2_rn(0.f);   // largest rope magnitude so far, NaN aside
     for_each_segment(a, k, g0, g1, [&](int si, int t, const TokenPlan& tp, int ia, int ie, bool, int) {
       for (int it = ia; it < ie; ++it, ++c) {
         if (waborted(cs)) return;
@@ -1206,8 +1225,6 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         uint8_t* st = sStage + s * C::kStageBytes;
         const bool live = (cs->row_mask[C::kEarly ? c & 3 : s] >> crow) & 1ull;
         const uint8_t* src = st + raw_off + crow * row4;
-        // the first pass overwrites what the P . C of the stage's last tile reads
-        if (C::kEarly && c >= S && !wwait(&cs->kv_empty[s], ((c / S) & 1) ^ 1, cs, hdr)) return;
 #pragma unroll 1
         for (int p = 0; p < C::NRH; ++p) {
           // this CTA's own latent half first, then the one that the rows lie in
@@ -1227,6 +1244,21 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
             for (int q = 0; q < kGroups; ++q) sb |= (uint32_t)src[L / 2 + grp0 + q] << (8 * q);
           }
           if (p == C::NRH - 1) {
+            // the row's rope part, bf16 -> f16, into its box (zeros past qk_rope and in a dead row)
+            const int nch = live ? a.d.qk_rope / 8 : 0;
+#pragma unroll 2
+            for (int ch = hh; ch < 8; ch += C::kConvPer) {
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (ch < nch) v = *reinterpret_cast<const uint4*>(src + C::kRow4 + 16 * ch);
+              uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                w[e] = bf16x2_to_f16x2(w[e]);
+                top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&w[e])));
+              }
+              *reinterpret_cast<uint4*>(st + C::NLB * C::kBox + crow * 128 + ((ch ^ (crow & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
             mbar_arrive(&cs->conv_sync);
             if (!wwait(&cs->conv_sync, c & 1, cs, hdr)) return;
           }
@@ -1266,10 +1298,11 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         }
       }
     });
-    if (out_of_range) atomicOr(&hdr->status, kDeviceCheckFailed);
+    const float2 big = __half22float2(top);
+    if (out_of_range || isinf(big.x) || isinf(big.y)) atomicOr(&hdr->status, kDeviceCheckFailed);
   } else if (!C::kGrouped || warp >= 4) {
     // ------------------------------------------------------------- softmax
-    if (C::kGrouped) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    if (C::kGrouped) { if (C::kConvThreads == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;"); else asm volatile("setmaxnreg.inc.sync.aligned.u32 232;"); }
     const int q = warp & 3;
     const int row = 32 * q + lane;
     const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16);
