@@ -27,7 +27,7 @@
 // Q latent (128).  Narrow latents (64) run the same code on one CTA.
 //
 // Warp roles (224 threads; 352 with the converter warps of an e4m3 cache; for the e2m1
-// cache's 384 see Cfg::kGrouped):
+// cache's 512 see Cfg::kGrouped):
 //   warp 0      TMA producer: the query's shared-memory part once per segment,
 //               cache tiles through the page table into a kStages-deep ring,
 //               and (not e2m1) an L2 prefetch of the tile two ahead.
@@ -128,16 +128,16 @@ struct Cfg {
   // QK reads, as soon as that product is done with the tile before; the load passes under the
   // softmax and the P . C, which needs the other half.  400 bytes a key are too few for a
   // multicast, which waits for both CTAs, to gain: 64 requests of 1,024 to 8,192 tokens 228
-  // us with one, 208 us without.  Nor is an L2 prefetch worth its instructions here (244 us
-  // with it, 216 us without: the roles' code together is more than the SM's instruction cache
-  // holds, and what the producer runs costs the other warps' fetches).
+  // us with one, 208 us without.
   static constexpr bool kEarly = kMode == kLoadFp4 && CL == 2;
+  // converter threads per cached row: one per raw box, twice as many for the e2m1 pair (64
+  // requests 194 -> 185 us)
   static constexpr int kConvPer = kMode == kLoadFp4 && kCluster == 2 ? 2 * NRH : NRH;
-  static constexpr int kConvThreads = 64 * kConvPer;                // warps 6.. (kCoded): one per row and raw box
-  // The e2m1 instance lays its warps out by warpgroup (0 load, 1 QK, 2 P . C, 3 rope | 4-7
-  // softmax | 8.. converters) so that the softmax's get the registers that the first four do
-  // not need: 104 / 232 / 168 of 168 each.  Spilled, a row of scores goes to L2, since shared
-  // memory leaves the L1 cache 20 KB.
+  static constexpr int kConvThreads = 64 * kConvPer;
+  // The e2m1 instance lays its warps out by warpgroup (0 load, 1 QK, 2 P . C | 4-7 softmax |
+  // 8.. converters) so that the softmax's get the registers that the others do not need: of a
+  // block of 512 x 128 88 / 232 / 96 / 96, of the narrow one's 320 x 168 104 / 232 / 168.
+  // Spilled, a row of scores goes to L2, since shared memory leaves the L1 cache 20 KB.
   static constexpr bool kGrouped = kMode == kLoadFp4;
   static constexpr int kConvWarp = kGrouped ? 8 : 6;
   static constexpr int kPvWarp = kGrouped ? 2 : (kCoded ? 6 + kConvThreads / 32 : 6);   // the P . C issuer
@@ -658,7 +658,10 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
   const int ps = a.ks.page_size;
   const int rows_per_load = ps < kTileKeys ? ps : kTileKeys;
 
-  if (C::kGrouped && warp < 4) { if (C::kConvThreads == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;"); }
+  if (C::kGrouped && warp < 4) {
+    if (C::kConvThreads == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  }
   if (warp == 0) {
     // ------------------------------------------------------------- producer
     auto load_box = [&](void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
@@ -1203,17 +1206,18 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
     });
   } else if (MODE == kLoadFp4 && warp >= C::kConvWarp) {
     // ------------------------------------------------------------- e2m1 converters
-    // Tile row crow is widened by NRH threads, pass p taking its codes of one
-    // latent half, thread hh the hh-th RW / NRH of them: groups of 32 codes
-    // (16 bytes) under one scale byte.  The operands are f16: a code times 2^e is exact
-    // for e in [-23, 13], and the absorbed query and P lose 2^-12 instead of 2^-9.  The
-    // scale goes into the lookup tables of e2m1x8_f16 where all products are normal
-    // numbers (|e| <= 13).  The rope part is converted by a warp of its own.  A
-    // magnitude that f16 does not reach becomes an infinity and is reported.  The last pass
-    // overwrites the rows, so it waits until every thread has read its part.
+    // Tile row crow is widened by kConvPer threads, pass p taking its codes of one latent half,
+    // thread hh the hh-th part of them: groups of 32 codes (16 bytes) under one scale byte.  The
+    // operands are f16: a code times 2^e is exact for e in [-23, 13], and the absorbed query and
+    // P lose 2^-12 instead of 2^-9.  The scale goes into the lookup tables of e2m1x8_f16 where
+    // all products are normal numbers (|e| <= 13).  A magnitude that f16 does not reach becomes
+    // an infinity and is reported.  The last pass overwrites the rows, so before it the threads
+    // convert the rope part and wait until every one of them has read its codes.  (A warp of its
+    // own for the rope part was the last to finish: 64 requests 185 us, 175 us so.)
     const int ci = tid - 32 * C::kConvWarp, crow = ci & 63, hh = ci >> 6;
     if (C::kConvThreads == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     constexpr int kGroups = C::RW / C::kConvPer / 32;   // groups per thread and pass
+    static_assert(MODE != kLoadFp4 || kGroups <= 4, "scale bytes of a pass in a register");
     int c = 0;
     bool out_of_range = false;
     __half2 top = __float2half2_rn(0.f);   // largest rope magnitude so far, NaN aside
@@ -1229,19 +1233,15 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         for (int p = 0; p < C::NRH; ++p) {
           // this CTA's own latent half first, then the one that the rows lie in
           const int grp0 = (C::kEarly ? p ^ (int)rank : p) * (C::RW / 32) + hh * kGroups;
-          // the loop over groups stays rolled, the next group moving up in registers: five roles
-          // of warps run different code on each SM, and unrolled it does not stay in the
-          // instruction cache (ncu: 36 % of the fetches missed)
-          static_assert(kGroups <= 4, "groups and scale bytes of a pass in registers");
-          uint4 raw[4] = {};
+          // the loop over groups stays rolled, the next group moving up in registers: the roles'
+          // code together does not stay in the instruction cache (ncu: 36 % of the fetches
+          // missed with it unrolled)
+          uint4 raw[kGroups];
           uint32_t sb = 0;
 #pragma unroll
-          for (int q = 0; q < kGroups; ++q) raw[q] = *reinterpret_cast<const uint4*>(src + (grp0 + q) * 16);
-          if (kGroups == 4) {
-            sb = *reinterpret_cast<const uint32_t*>(src + L / 2 + grp0);
-          } else {
-#pragma unroll
-            for (int q = 0; q < kGroups; ++q) sb |= (uint32_t)src[L / 2 + grp0 + q] << (8 * q);
+          for (int q = 0; q < kGroups; ++q) {
+            raw[q] = *reinterpret_cast<const uint4*>(src + (grp0 + q) * 16);
+            sb |= (uint32_t)src[L / 2 + grp0 + q] << (8 * q);
           }
           if (p == C::NRH - 1) {
             // the row's rope part, bf16 -> f16, into its box (zeros past qk_rope and in a dead row)
@@ -1287,9 +1287,8 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(box + (((ch + i) ^ (crow & 7)) << 4)) = o[i];
-            raw[0] = raw[1];
-            raw[1] = raw[2];
-            raw[2] = raw[3];
+#pragma unroll
+            for (int i = 0; i + 1 < kGroups; ++i) raw[i] = raw[i + 1];
             sb >>= 8;
           }
           fence_proxy_async_smem();
@@ -1302,7 +1301,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
     if (out_of_range || isinf(big.x) || isinf(big.y)) atomicOr(&hdr->status, kDeviceCheckFailed);
   } else if (!C::kGrouped || warp >= 4) {
     // ------------------------------------------------------------- softmax
-    if (C::kGrouped) { if (C::kConvThreads == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;"); else asm volatile("setmaxnreg.inc.sync.aligned.u32 232;"); }
+    if (C::kGrouped) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int q = warp & 3;
     const int row = 32 * q + lane;
     const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16);
