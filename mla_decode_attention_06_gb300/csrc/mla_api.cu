@@ -460,6 +460,8 @@ int mla_cache_append(const mla_dims_t* dims, int32_t cache_format, const void* k
   if (dims->kv_lora_rank % 32 != 0 || dims->kv_lora_rank > 512 || dims->qk_rope % 8 != 0 || dims->qk_rope > 128 ||
       (q && dims->qk_nope % 8 != 0))
     return MLA_ERR_UNSUPPORTED;
+  // a token's queries are counted in 32 bits
+  if (q && ((int64_t)dims->qk_nope + dims->qk_rope) * dims->num_heads > INT32_MAX) return MLA_ERR_UNSUPPORTED;
   if ((int64_t)dims->num_pages * dims->page_size > INT32_MAX) return MLA_ERR_UNSUPPORTED;
   if (batch < 1 || total_q < 0 || block_table_stride < 1 || max_seq_len < 1) return MLA_ERR_INVALID_ARG;
   if (kv_new_stride < dims->kv_lora_rank + dims->qk_rope || kv_new_stride % 8 != 0) return MLA_ERR_INVALID_ARG;

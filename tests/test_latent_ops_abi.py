@@ -58,6 +58,7 @@ def test_append_reports_unsupported_shapes(lib):
     for kw in (dict(kv_lora_rank=520), dict(kv_lora_rank=544), dict(kv_lora_rank=48), dict(qk_rope=60),
                dict(qk_rope=136), dict(qk_nope=100), dict(page_size=1 << 20, num_pages=1 << 12)):
         assert _append(lib, dims=_dims(**kw), stride=1024) == UNSUPPORTED, kw
+    assert _append(lib, dims=_dims(num_heads=1 << 24)) == UNSUPPORTED     # a token's queries pass 32 bits
     # without queries the head count and qk_nope are not looked at; the workspace is
     assert _append(lib, dims=_dims(num_heads=0, qk_nope=-1), q=None, q_out=None, ws_bytes=0) == TOO_SMALL
     assert _append(lib, ws=FAKE + 8) == TOO_SMALL
