@@ -77,7 +77,8 @@ struct Args {
   const int32_t* block_table;
   const uint8_t* pool;
   const float* scales;
-  PlanHeader* hdr;                 // total_tiles: key tiles; pad[2]: query blocks; pad[3]: f16 does not do
+  PlanHeader* hdr;                 // total_tiles: key tiles; pad[2]: query blocks; pad[3]: f16 does not do;
+                                   // pad[4]: blocks that the attention's CTAs took beyond their first
   Req* reqs;
   int2* items;                     // (request, query block)
   uint4* live;                     // per tile: live rows
@@ -530,6 +531,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
   const long long total = runs(a) ? (long long)tiles * a.hg : 0;
   const bool in_f16 = a.half && a.fmt == MLA_CACHE_E4M3;   // latents and weights
   PlanHeader* hdr = a.hdr;
+  if (blockIdx.x == 0 && tid == 0) hdr->pad[4] = 0;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -678,13 +680,16 @@ constexpr float kRescaleThreshold = 8.0f;   // log2: O is rescaled when a row's 
 // have no registers to keep it in).
 struct Block {
   Req q;
-  int r0, nsub, h, split;     // first query row, sub-blocks, head of the pass, key split
+  int r0, nsub, h, split;     // first query row, sub-blocks, head of the pass (-1: no more), key split
   int j0[2], j1[2], js, je;   // key tiles of each sub-block, and of both
 };
+constexpr int kBlocks = 4;      // blocks known ahead
+constexpr int kBlockUsers = 11; // warps that read a block: loads, two issuers, eight of the softmax
 struct AttSmem {
   uint64_t k0_full[2], k12_full[2], k_empty[2], v_full[2], v_empty[2], turn[2], q_full, q_ready[2], s_full[2], p_full[2], o_full[2];
+  uint64_t blk_full[kBlocks], blk_empty[kBlocks], want;
   Ctl ctl;
-  Block blk;
+  Block blk[kBlocks];
 };
 constexpr int kMaxQBoxes = 3;
 constexpr int kAttSmem = 1024 + 2 * kMaxQBoxes * kBox + kSlots * kBox + (int)sizeof(AttSmem);
@@ -714,8 +719,9 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
 // Bits [0, n) of a word.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
 
-__device__ __forceinline__ void set_block(const Args& a, long long at, Block& k) {
-  const int split = (int)(at % a.splits), item = (int)(at / a.splits % a.max_items);
+// Block `at`: split fastest, then query block, then head.
+__device__ __forceinline__ void set_block(const Args& a, int nitems, long long at, Block& k) {
+  const int split = (int)(at % a.splits), item = (int)(at / a.splits % nitems);
   const int2 it = a.items[item];
   const Req q = a.reqs[it.x];
   const int r0 = it.y * 2 * kTile, nsub = q.qlen > r0 + kTile ? 2 : 1;
@@ -737,7 +743,7 @@ __device__ __forceinline__ void set_block(const Args& a, long long at, Block& k)
   k.q = q;
   k.r0 = r0;
   k.nsub = nsub;
-  k.h = (int)(at / a.splits / a.max_items);
+  k.h = (int)(at / a.splits / nitems);
   k.split = split;
   for (int s = 0; s < 2; ++s) {
     k.j0[s] = j0[s];
@@ -760,39 +766,31 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
   griddep_wait();
   fence_proxy_async_global();
   if (!runs(a)) return;
-  // blocks: split fastest, then query block, then head.  The f16 sequence has a CTA for
-  // each, the other one strides over them.
   const int nitems = hdr->pad[2];
-  const long long nblocks = (long long)a.splits * a.max_items * a.hg;
-  if (kHalf && (int)(blockIdx.x / a.splits) % a.max_items >= nitems) return;
+  const long long nblocks = (long long)a.splits * nitems * a.hg;
   if (warp == 1) {
     tmem_alloc(&cs->ctl.tmem_base, 512);
     tmem_relinquish();
   }
-  if (tid == 0) cs->ctl.abort = 0;
-  for (long long at = blockIdx.x; at < nblocks; at += gridDim.x) {
-  if ((int)(at / a.splits % a.max_items) >= nitems) continue;
   if (tid == 0) {
+    cs->ctl.abort = 0;
     mbar_init(&cs->q_full, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&cs->k0_full[i], 1);
       mbar_init(&cs->k12_full[i], 1);
+      mbar_init(&cs->k_empty[i], 2);
       mbar_init(&cs->v_full[i], 1);
+      mbar_init(&cs->v_empty[i], 2);
       mbar_init(&cs->turn[i], 1);
       mbar_init(&cs->q_ready[i], 128);
       mbar_init(&cs->s_full[i], 1);
       mbar_init(&cs->p_full[i], 128);
       mbar_init(&cs->o_full[i], 1);
     }
-    fence_mbar_init();
-  }
-  if (tid == 64) {
-    set_block(a, at, cs->blk);
-    // a tile's places are free once every sub-block that has key tiles is done with it
-    const int users = (cs->blk.j1[0] > cs->blk.j0[0]) + (cs->blk.j1[1] > cs->blk.j0[1]);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&cs->k_empty[i], max(users, 1));
-      mbar_init(&cs->v_empty[i], max(users, 1));
+    mbar_init(&cs->want, 1);
+    for (int i = 0; i < kBlocks; ++i) {
+      mbar_init(&cs->blk_full[i], 1);
+      mbar_init(&cs->blk_empty[i], kBlockUsers);
     }
     fence_mbar_init();
   }
@@ -800,84 +798,149 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = cs->ctl.tmem_base;
-  const Block& blk = cs->blk;
+  // Block i of this CTA, for a warp that uses it; its place is given back by `done_with`.
+  auto block = [&](int i) { return wwait(&cs->blk_full[i % kBlocks], (i / kBlocks) & 1, &cs->ctl, hdr); };
+  auto done_with = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&cs->blk_empty[i % kBlocks]);
+  };
 
-  if (kHalf && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-  if (warp == 0) {
-    const int js = blk.js, je = blk.je, nsub = blk.nsub, t0 = blk.q.q0 + blk.r0, h = blk.h, tile0 = blk.q.tile0;
-    if (lane == 0 && je > js) {
-      mbar_arrive_expect_tx(&cs->q_full, (uint32_t)(2 * a.nbq * kBox));
-      for (int s = 0; s < 2; ++s)
-        for (int i = 0; i < a.nbq; ++i) {
-          uint8_t* dst = sQ + (s * a.nbq + i) * kBox;
-          const int t = t0 + (s < nsub ? s : 0) * kTile;   // a block of one sub-block loads it twice
-          if (i < a.nbk) tma_load_3d(dst, &maps.qn, &cs->q_full, 64 * i, a.h0 + h, t);
-          else tma_load_3d(dst, &maps.qr, &cs->q_full, 0, a.h0 + h, t);
-        }
-      const int nb = a.nbk + a.nbv, tiles = je - js;
-      const uint8_t* kv = a.kv + (((size_t)h * a.cap_tiles + tile0 + js) * nb) * kBox;
-      const uint8_t* rope = a.rope + (size_t)(tile0 + js) * kBox;
-      auto load_k0 = [&](int n) {
-        if (n >= tiles) return;
-        mbar_arrive_expect_tx(&cs->k0_full[n & 1], kBox);
-        bulk_copy_g2s(ring + place_k0(n), kv + (size_t)n * nb * kBox, kBox, &cs->k0_full[n & 1]);
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  if (warp == 3) {
+    // Which blocks: the first by the CTA's number, then whatever nobody took yet, one at a time
+    // and as late as the loads allow (with four taken ahead the last ones were spread badly:
+    // 16,384 tokens x 16 heads 1,159 us).
+    if (lane == 0) {
+      // A block may take any time: this wait ends with the producer's, which are bounded.
+      auto asked = [&](int i) {
+        while (!mbar_wait(&cs->want, (i - 1) & 1, kWaitLimitNs))
+          if (*reinterpret_cast<volatile int*>(&cs->ctl.abort)) return false;
+        return true;
       };
-      auto load_k12 = [&](int n) {
-        if (n >= tiles) return;
-        mbar_arrive_expect_tx(&cs->k12_full[n & 1], (uint32_t)(a.nbk * kBox));
-        if (a.nbk > 1) bulk_copy_g2s(ring + place_k12(n), kv + ((size_t)n * nb + 1) * kBox, kBox, &cs->k12_full[n & 1]);
-        bulk_copy_g2s(ring + place_k12(n) + (a.nbk - 1) * kBox, rope + (size_t)n * kBox, kBox, &cs->k12_full[n & 1]);
-      };
-      auto load_v = [&](int n) {
-        if (n >= tiles) return;
-        mbar_arrive_expect_tx(&cs->v_full[n & 1], (uint32_t)(a.nbv * kBox));
-        bulk_copy_g2s(ring + place_v(n), kv + ((size_t)n * nb + a.nbk) * kBox, (uint32_t)(a.nbv * kBox), &cs->v_full[n & 1]);
-      };
-      load_k0(0);
-      load_k12(0);
-      load_v(0);
-      load_k0(1);
-      load_k12(1);
-      int n = 0;
-      for (; n + 1 < tiles; ++n) {
-        if (!wait(&cs->k_empty[n & 1], (n >> 1) & 1, &cs->ctl, hdr)) break;
-        load_v(n + 1);
-        load_k0(n + 2);
-        if (n + 2 < tiles && !wait(&cs->v_empty[n & 1], (n >> 1) & 1, &cs->ctl, hdr)) {
-          ++n;
-          break;
-        }
-        load_k12(n + 2);
+      for (int i = 0;; ++i) {
+        if (i > 0 && !asked(i)) break;
+        if (i >= kBlocks && !wait(&cs->blk_empty[i % kBlocks], ((i / kBlocks) & 1) ^ 1, &cs->ctl, hdr)) break;
+        const long long at = i == 0 ? blockIdx.x : (long long)gridDim.x + atomicAdd(&hdr->pad[4], 1);
+        Block& k = cs->blk[i % kBlocks];
+        if (at < nblocks) set_block(a, nitems, at, k);
+        else k.h = -1;
+        mbar_arrive(&cs->blk_full[i % kBlocks]);
+        if (at >= nblocks) break;
       }
-      // nothing in flight when the CTA leaves: the last loads of each kind (V up to tile n, K0
-      // and K12 up to n + 1; after a wait that ran out, one of them may only run out too)
-      for (int i = n > 1 ? n - 1 : 0; i < tiles && i <= n + 1; ++i) {
-        mbar_wait(&cs->k0_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
-        mbar_wait(&cs->k12_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
-        if (i <= n) mbar_wait(&cs->v_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
+    }
+    __syncwarp();
+  } else if (warp == 0) {
+    if (lane == 0) {
+      // Key tiles are counted through the CTA's blocks.  Step n: V of tile n + 1, K of tile n + 2,
+      // and the queries of a block as its first tile becomes n + 1, when the block before has
+      // done its last Q.K.  A: the block of tile n + 1, B: the one after it, once it is known.
+      const int nb = a.nbk + a.nbv;
+      const uint8_t *kv_a = nullptr, *kv_b = nullptr, *rope_a = nullptr, *rope_b = nullptr;   // of its tile 0, were it the CTA's first
+      int end_a = 0, end_b = 0, t_b = 0, h_b = 0, two_b = 0;
+      bool have_b = false, stop = false, ok = true;
+      int nblk = 0, nq = 0, nk0 = 0, nk12 = 0, nv = 0;   // blocks read; loads of each kind
+      int nasked = 1;                                    // blocks asked for, the first by itself
+      auto ask = [&]() {
+        if (nasked > nblk) return;
+        mbar_arrive(&cs->want);
+        ++nasked;
+      };
+      auto next_block = [&]() {
+        for (; !have_b && !stop && ok; ++nblk) {
+          ask();
+          if (!(ok = wait(&cs->blk_full[nblk % kBlocks], (nblk / kBlocks) & 1, &cs->ctl, hdr))) return;
+          const Block& k = cs->blk[nblk % kBlocks];
+          if ((stop = k.h < 0)) return;
+          if (k.je > k.js) {
+            have_b = true;
+            h_b = k.h;
+            t_b = k.q.q0 + k.r0;
+            two_b = k.nsub > 1;
+            end_b = end_a + (k.je - k.js);
+            const long long first = (long long)k.q.tile0 + k.js;
+            kv_b = a.kv + ((long long)h_b * a.cap_tiles + first - end_a) * nb * kBox;
+            rope_b = a.rope + (first - end_a) * kBox;
+          }
+          mbar_arrive(&cs->blk_empty[nblk % kBlocks]);
+        }
+      };
+      for (int n = -2; ok; ++n) {
+        if (n >= 0 && !(ok = wait(&cs->k_empty[n & 1], (n >> 1) & 1, &cs->ctl, hdr))) break;
+        if (n >= -1) {
+          if (n + 1 == end_a) {
+            if (!have_b) break;   // no more
+            kv_a = kv_b;
+            rope_a = rope_b;
+            end_a = end_b;
+            have_b = false;
+            mbar_arrive_expect_tx(&cs->q_full, (uint32_t)(2 * a.nbq * kBox));
+            for (int s = 0; s < 2; ++s)
+              for (int i = 0; i < a.nbq; ++i) {
+                uint8_t* dst = sQ + (s * a.nbq + i) * kBox;
+                const int t = t_b + (s & two_b) * kTile;   // a block of one sub-block loads it twice
+                if (i < a.nbk) tma_load_3d(dst, &maps.qn, &cs->q_full, 64 * i, a.h0 + h_b, t);
+                else tma_load_3d(dst, &maps.qr, &cs->q_full, 0, a.h0 + h_b, t);
+              }
+            ++nq;
+          }
+          mbar_arrive_expect_tx(&cs->v_full[nv & 1], (uint32_t)(a.nbv * kBox));
+          bulk_copy_g2s(ring + place_v(nv), kv_a + ((long long)nv * nb + a.nbk) * kBox, (uint32_t)(a.nbv * kBox),
+                        &cs->v_full[nv & 1]);
+          ++nv;
+        }
+        if (n + 5 >= end_a && !have_b && !stop) ask();
+        const uint8_t *kv = kv_a, *rope = rope_a;
+        if (n + 2 >= end_a) {
+          next_block();
+          if (!have_b) continue;
+          kv = kv_b;
+          rope = rope_b;
+        }
+        mbar_arrive_expect_tx(&cs->k0_full[nk0 & 1], kBox);
+        bulk_copy_g2s(ring + place_k0(nk0), kv + (long long)nk0 * nb * kBox, kBox, &cs->k0_full[nk0 & 1]);
+        ++nk0;
+        if (n >= 0 && !(ok = wait(&cs->v_empty[n & 1], (n >> 1) & 1, &cs->ctl, hdr))) break;
+        mbar_arrive_expect_tx(&cs->k12_full[nk12 & 1], (uint32_t)(a.nbk * kBox));
+        if (a.nbk > 1)
+          bulk_copy_g2s(ring + place_k12(nk12), kv + ((long long)nk12 * nb + 1) * kBox, kBox, &cs->k12_full[nk12 & 1]);
+        bulk_copy_g2s(ring + place_k12(nk12) + (a.nbk - 1) * kBox, rope + (long long)nk12 * kBox, kBox,
+                      &cs->k12_full[nk12 & 1]);
+        ++nk12;
       }
-      mbar_wait(&cs->q_full, 0, kWaitLimitNs);
+      // nothing in flight when the CTA leaves: the last loads of each kind
+      for (int i = max(nk0 - 2, 0); i < nk0; ++i) mbar_wait(&cs->k0_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
+      for (int i = max(nk12 - 2, 0); i < nk12; ++i) mbar_wait(&cs->k12_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
+      for (int i = max(nv - 2, 0); i < nv; ++i) mbar_wait(&cs->v_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
+      if (nq > 0) mbar_wait(&cs->q_full, (nq - 1) & 1, kWaitLimitNs);
     }
     __syncwarp();
   } else if (warp == 1 || warp == 2) {
     // One sub-block's products.  The whole warp walks the loop, one lane issues (as in the
     // expansion).  For a key tile that this sub-block does not use it only passes the data on.
-    const int s = warp - 1, js = blk.js, je = blk.je, ja = blk.j0[s], jb = blk.j1[s];
-    if (jb > ja) {
-      const uint32_t type = kHalf ? kBf16Operands : 0u;
-      const uint32_t id_s = idesc_bf16_f32(128, 128, false, false) ^ type;
-      const uint32_t id_o = idesc_bf16_f32(128, 64 * a.nbv, false, true) ^ type;
-      const uint64_t dq0 = smem_desc(smem_u32(sQ) + s * a.nbq * kBox, 16, 1024, kLayoutSw128);
-      const uint64_t dr0 = smem_desc(smem_u32(ring), 16, 1024, kLayoutSw128);
-      const uint64_t dv0 = smem_desc(smem_u32(ring), kBox, 1024, kLayoutSw128);
-      constexpr uint64_t kBoxStep = kBox >> 4;
-      const int nbq = a.nbq;
-      const uint32_t ts = tmem + 128 * s, to = tmem + 256 + 128 * s;
-      const bool both = blk.j1[s ^ 1] > blk.j0[s ^ 1];
-      bool ok = wwait(&cs->q_ready[s], 0, &cs->ctl, hdr);
-      int np = 0;   // P tiles taken
+    const int s = warp - 1;
+    const uint32_t type = kHalf ? kBf16Operands : 0u;
+    const uint32_t id_s = idesc_bf16_f32(128, 128, false, false) ^ type;
+    const uint32_t id_o = idesc_bf16_f32(128, 64 * a.nbv, false, true) ^ type;
+    const uint64_t dq0 = smem_desc(smem_u32(sQ) + s * a.nbq * kBox, 16, 1024, kLayoutSw128);
+    const uint64_t dr0 = smem_desc(smem_u32(ring), 16, 1024, kLayoutSw128);
+    const uint64_t dv0 = smem_desc(smem_u32(ring), kBox, 1024, kLayoutSw128);
+    constexpr uint64_t kBoxStep = kBox >> 4;
+    const int nbq = a.nbq;
+    const uint32_t ts = tmem + 128 * s, to = tmem + 256 + 128 * s;
+    bool ok = true, waits_turn = s == 1;   // A begins
+    int n0 = 0, np = 0, nturn = 0;         // key tiles of the blocks before, P tiles and turns taken
+    for (int i = 0; ok; ++i) {
+      if (!(ok = block(i))) break;
+      const Block& blk = cs->blk[i % kBlocks];
+      if (blk.h < 0) break;
+      const int js = blk.js, je = blk.je, ja = blk.j0[s], jb = blk.j1[s];
+      const bool both = jb > ja && blk.j1[s ^ 1] > blk.j0[s ^ 1];
+      done_with(i);
+      if (je <= js) continue;
+      if (jb > ja && !(ok = wwait(&cs->q_ready[s], i & 1, &cs->ctl, hdr))) break;
+      bool add = false;   // O holds something
       // Group n: O (+)= P V of key tile n - 1, then S = Q K^T of key tile n
-      int n = 0;
+      int n = n0;
       for (int j = js; j <= je && ok; ++j, ++n) {
         const bool use_v = j > js && j - 1 >= ja && j - 1 < jb, use_k = j >= ja && j < jb;
         const int v = n - 1;
@@ -885,14 +948,17 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         if (j > js && !(ok = wwait(&cs->v_full[v & 1], (v >> 1) & 1, &cs->ctl, hdr))) break;
         if (use_v && !(ok = wwait(&cs->p_full[s], np & 1, &cs->ctl, hdr))) break;
         // the sub-blocks take turns
-        if (both && (s == 1 || n > 0) && !(ok = wwait(&cs->turn[s], (s == 1 ? n : n - 1) & 1, &cs->ctl, hdr))) break;
+        if (both) {
+          if (waits_turn && !(ok = wwait(&cs->turn[s], nturn++ & 1, &cs->ctl, hdr))) break;
+          waits_turn = true;
+        }
         tc_fence_after();
         const uint64_t dv = dv0 + (place_v(v + 3) >> 4), dk0 = dr0 + (place_k0(n) >> 4), dk12 = dr0 + (place_k12(n) >> 4);
         if (elect_one()) {
           if (use_v) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_ts(to, ts + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4), id_o, np > 0 || kk > 0);
+              mma_ts(to, ts + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4), id_o, add || kk > 0);
             if (j == jb) mma_commit(&cs->o_full[s]);
             mma_commit(&cs->v_empty[v & 1]);
           } else if (j > js) {
@@ -908,9 +974,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         if (j < je && !(ok = wwait(&cs->k12_full[n & 1], (n >> 1) & 1, &cs->ctl, hdr))) break;
         tc_fence_after();
         if (elect_one()) {
-          for (int i = 1; i < nbq && use_k; ++i) {
-            const uint64_t dq = dq0 + i * kBoxStep, dk = dk12 + (i - 1) * kBoxStep;
-            if (i == nbq - 1 && both) mbar_arrive(&cs->turn[s ^ 1]);   // its wait passes under the last box
+          for (int b = 1; b < nbq && use_k; ++b) {
+            const uint64_t dq = dq0 + b * kBoxStep, dk = dk12 + (b - 1) * kBoxStep;
+            if (b == nbq - 1 && both) mbar_arrive(&cs->turn[s ^ 1]);   // its wait passes under the last box
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) mma_ss(ts, dq + 2 * kk, dk + 2 * kk, id_s, 1u);
           }
@@ -923,17 +989,26 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
           }
         }
         __syncwarp();
-        np += use_v;
+        if (use_v) {
+          ++np;
+          add = true;
+        }
       }
-      --n;   // key tiles passed
-      // the last signal has arrived before the barriers go away
-      if (ok) wwait(&cs->v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, &cs->ctl, hdr);
+      n0 += je - js;
     }
+    // the last signals have arrived before the barriers go away
+    if (ok && n0 > 0) wwait(&cs->v_empty[(n0 - 1) & 1], ((n0 - 1) >> 1) & 1, &cs->ctl, hdr);
   } else if (warp >= 4) {
-    if (kHalf) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");   // once: this instance has one block a CTA
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int s = warp >= 8 ? 1 : 0;
     const int quad = warp & 3, row = 32 * quad + lane;
     const uint32_t trow = tmem + ((uint32_t)(32 * quad) << 16), ts = trow + 128 * s, to = trow + 256 + 128 * s;
+    uint32_t phase = 0;   // bit 0: of s_full, bit 1: of q_full, bit 2: of o_full
+    bool ok = true;
+    for (int at = 0; ok; ++at) {
+    if (!(ok = block(at))) break;
+    const Block& blk = cs->blk[at % kBlocks];
+    if (blk.h < 0) break;
     const int ja = blk.j0[s], jb = blk.j1[s];
     const bool live = jb > ja;
     // this row's keys [lo, hi); the sub-block's first and last row bound what needs no mask
@@ -946,11 +1021,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
       row_range(a, blk.q, min(r, last), unused, hi_first);
     }
     float sl2 = a.scale * 1.4426950408889634f;
-    bool ok = true;
     if (live) {
       // this thread's query row: bf16 -> f16, scaled to a largest magnitude in [2^10, 2^11);
       // a scale below zero turns its sign, a scale of zero its values to zero
-      ok = wwait(&cs->q_full, 0, &cs->ctl, hdr);
+      ok = wwait(&cs->q_full, (phase >> 1) & 1, &cs->ctl, hdr);
       if (ok && (kHalf || !(sl2 > 0.f))) {
         uint8_t* qr = sQ + s * a.nbq * kBox + row * 128;
         uint32_t top = 0;
@@ -979,15 +1053,16 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         sl2 = sl2 * __uint_as_float((uint32_t)(k / 2 + 127) << 23) * __uint_as_float((uint32_t)(k - k / 2 + 127) << 23);
         fence_proxy_async_smem();
       }
-      mbar_arrive(&cs->q_ready[s]);
     }
+    mbar_arrive(&cs->q_ready[s]);
+    if (blk.je > blk.js) phase ^= 2;
     float m = -CUDART_INF_F, l = 0.f;
-    int n = 0;
     const uint4* live_rows = a.live + blk.q.tile0;
     if (ok && s < blk.nsub) {
-      for (int j = ja; j < jb; ++j, ++n) {
+      for (int j = ja; j < jb; ++j) {
         const uint4 lv = __ldcg(live_rows + j);   // its latency passes in the wait
-        if (!(ok = wwait(&cs->s_full[s], n & 1, &cs->ctl, hdr))) break;
+        if (!(ok = wwait(&cs->s_full[s], phase & 1, &cs->ctl, hdr))) break;
+        phase ^= 1;
         tc_fence_after();
         float x[128];
         const int k0 = j * kTile;
@@ -1062,9 +1137,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         mbar_arrive(&cs->p_full[s]);
       }
       // epilogue
-      if (ok && live) ok = wwait(&cs->o_full[s], 0, &cs->ctl, hdr);
+      if (ok && live) ok = wwait(&cs->o_full[s], (phase >> 2) & 1, &cs->ctl, hdr);
+      if (live) phase ^= 4;
       tc_fence_after();
-      const volatile Block* vb = &cs->blk;   // read again: nothing of it was kept
+      const volatile Block* vb = &cs->blk[at % kBlocks];   // read again: nothing of it was kept
       const int r = vb->r0 + s * kTile + row;
       const bool mine = ok && r < vb->q.qlen, fits = vb->q.fits != 0;
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : CUDART_NAN_F);
@@ -1104,19 +1180,15 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         else if (a.lse_out) a.lse_out[th] = lse;
       }
     }
+    tc_fence_before();   // O is read
+    done_with(at);
+    }
   }
   tc_fence_before();
   __syncthreads();
-  if (gridDim.x < nblocks && tid == 0) {   // another block follows: its barriers start afresh
-    uint64_t* bar = reinterpret_cast<uint64_t*>(cs);
-    for (int i = 0; i < (int)(offsetof(AttSmem, ctl) / 8); ++i)
-      asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar + i)) : "memory");
-  }
-  }
-  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(cs->ctl.tmem_base, 512);
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -1332,9 +1404,8 @@ cudaError_t launch_prefill(const PrefillCall& c, const PrefillLayout& lay, int h
       const long long pairs = lay.cap_tiles * a.hg, blocks = lay.max_items * a.hg * splits;
       e = start(expand_kernel, (unsigned)std::min<long long>(pairs, sms), kExpThreads, kExpSmem, s, em, a);
       if (e == cudaSuccess)
-        e = a.half ? start(attend_kernel<true>, (unsigned)blocks, kAttThreads, kAttSmem, s, am, a)
-                   : start(attend_kernel<false>, (unsigned)std::min<long long>(blocks, sms), kAttThreads, kAttSmem, s, am,
-                           a);
+        e = start(a.half ? attend_kernel<true> : attend_kernel<false>, (unsigned)std::min<long long>(blocks, sms), kAttThreads,
+                  kAttSmem, s, am, a);
     }
   }
   if (e == cudaSuccess && splits > 1)
