@@ -927,7 +927,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     constexpr uint64_t kBoxStep = kBox >> 4;
     const int nbq = a.nbq;
     const uint32_t ts = tmem + 128 * s, to = tmem + 256 + 128 * s;
-    bool ok = true, waits_turn = s == 1;   // A begins
+    bool ok = true;
     int n0 = 0, np = 0, nturn = 0;         // key tiles of the blocks before, P tiles and turns taken
     for (int i = 0; ok; ++i) {
       if (!(ok = block(i))) break;
@@ -947,11 +947,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         if (j < je && !(ok = wwait(&cs->k0_full[n & 1], (n >> 1) & 1, &cs->ctl, hdr))) break;
         if (j > js && !(ok = wwait(&cs->v_full[v & 1], (v >> 1) & 1, &cs->ctl, hdr))) break;
         if (use_v && !(ok = wwait(&cs->p_full[s], np & 1, &cs->ctl, hdr))) break;
-        // the sub-blocks take turns
-        if (both) {
-          if (waits_turn && !(ok = wwait(&cs->turn[s], nturn++ & 1, &cs->ctl, hdr))) break;
-          waits_turn = true;
-        }
+        // the sub-blocks take turns, A first in each block
+        if (both && (s == 1 || j > js) && !(ok = wwait(&cs->turn[s], nturn++ & 1, &cs->ctl, hdr))) break;
         tc_fence_after();
         const uint64_t dv = dv0 + (place_v(v + 3) >> 4), dk0 = dr0 + (place_k0(n) >> 4), dk12 = dr0 + (place_k12(n) >> 4);
         if (elect_one()) {
@@ -984,7 +981,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
             mma_commit(&cs->s_full[s]);
             mma_commit(&cs->k_empty[n & 1]);
           } else {
-            if (both) mbar_arrive(&cs->turn[s ^ 1]);
+            if (both && (s == 0 || j < je)) mbar_arrive(&cs->turn[s ^ 1]);
             if (j < je) mbar_arrive(&cs->k_empty[n & 1]);
           }
         }
@@ -1027,15 +1024,16 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
       ok = wwait(&cs->q_full, (phase >> 1) & 1, &cs->ctl, hdr);
       if (ok && (kHalf || !(sl2 > 0.f))) {
         uint8_t* qr = sQ + s * a.nbq * kBox + row * 128;
-        uint32_t top = 0;
+        __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);   // a NaN does not count: its row is NaN anyhow
         for (int i = 0; i < a.nbq && kHalf; ++i)
 #pragma unroll
           for (int ch = 0; ch < 8; ++ch) {
             const uint4 v = *reinterpret_cast<const uint4*>(qr + i * kBox + ((ch ^ (row & 7)) << 4));
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+            for (int e = 0; e < 4; ++e) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
           }
+        const uint32_t tw = *reinterpret_cast<const uint32_t*>(&top2), top = max(tw & 0xFFFFu, tw >> 16);
         const int k = (top >= 0x7F80u || top == 0u ? 10 : max((int)(top >> 7) - 127, -110)) - 10;
         const float f = (sl2 > 0.f ? 1.f : (sl2 < 0.f ? -1.f : 0.f)) * __uint_as_float((uint32_t)(127 - k) << 23);
         auto put = [&](uint32_t v) {
