@@ -1026,7 +1026,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         uint8_t* qr = sQ + s * a.nbq * kBox + row * 128;
         __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);   // a NaN does not count: its row is NaN anyhow
         for (int i = 0; i < a.nbq && kHalf; ++i)
-#pragma unroll
+#pragma unroll 4
           for (int ch = 0; ch < 8; ++ch) {
             const uint4 v = *reinterpret_cast<const uint4*>(qr + i * kBox + ((ch ^ (row & 7)) << 4));
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -1040,7 +1040,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
           return kHalf ? pack_f16(lo_f(v) * f, hi_f(v) * f) : pack_bf16(lo_f(v) * f, hi_f(v) * f);
         };
         for (int i = 0; i < a.nbq; ++i)
-#pragma unroll
+#pragma unroll 4
           for (int ch = 0; ch < 8; ++ch) {
             uint4* p = reinterpret_cast<uint4*>(qr + i * kBox + ((ch ^ (row & 7)) << 4));
             const uint4 v = *p;
@@ -1146,8 +1146,12 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
       const size_t th = (size_t)(vb->q.q0 + r) * a.d.num_heads + a.h0 + vb->h;
       const size_t sp = (size_t)vb->split * a.T * a.d.num_heads;
       const int V = a.d.v_head;
+      // This code and the queries' conversion run once a block, from a cold instruction cache:
+      // few instructions and rolled loops (one prompt of 1,900 tokens 257 -> 245 us).
+      const bool some = live && fits && l != 0.f;
+      const float fill = fits ? 0.f : CUDART_NAN_F;
 #pragma unroll 1
-      for (int col = 0; col < 64 * a.nbv; col += 32) {
+      for (int col = 0; col < V; col += 32) {
         uint32_t o[32];
         if (live) {
           tmem_ld32(to + col, o);
@@ -1155,21 +1159,20 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         }
         if (!mine) continue;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          o[i] = __float_as_uint(!fits ? CUDART_NAN_F : (live && l != 0.f ? __uint_as_float(o[i]) * inv : 0.f));
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(some ? __uint_as_float(o[i]) * inv : fill);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (col + 8 * i >= V) break;
+        for (int i = 0; i < 32; i += 8) {
+          if (col + i >= V) break;
           if (a.splits == 1) {
-            *reinterpret_cast<uint4*>(a.out + th * V + col + 8 * i) =
-                make_uint4(pack_bf16(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
-                           pack_bf16(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3])),
-                           pack_bf16(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
-                           pack_bf16(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])));
+            *reinterpret_cast<uint4*>(a.out + th * V + col + i) =
+                make_uint4(pack_bf16(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
+                           pack_bf16(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3])),
+                           pack_bf16(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5])),
+                           pack_bf16(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7])));
           } else {
-            uint4* d = reinterpret_cast<uint4*>(a.part_o + (sp + th) * V + col + 8 * i);
-            d[0] = make_uint4(o[8 * i], o[8 * i + 1], o[8 * i + 2], o[8 * i + 3]);
-            d[1] = make_uint4(o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]);
+            uint4* d = reinterpret_cast<uint4*>(a.part_o + (sp + th) * V + col + i);
+            d[0] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            d[1] = make_uint4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
           }
         }
       }
