@@ -14,7 +14,8 @@
 //   gather   cache rows of any format -> bf16 tiles of 128 rows, and which rows are live.
 //   expand   K and V of a pass's heads: one GEMM tile (128 rows x (N | V) x L) per key
 //            tile and head, tcgen05, written as the attention's shared-memory images.
-//   attend   one CTA per query block, head and key split: flash attention on tcgen05.
+//   attend   one CTA per SM, taking (query block, head, key split) after (...): softmax on the
+//            fly between two tcgen05 products.
 //   combine  joins the key splits (only where a call has few query blocks).
 //
 // Every tile that passes between these kernels is stored as 128-byte-swizzled boxes of
@@ -650,24 +651,33 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
 
 // ------------------------------------------------------------------------------ attend
 
-// One CTA: 256 query tokens of a request (two sub-blocks A and B of 128) for one head,
-// over a range of its key tiles.  TMEM holds S of A and B (128 columns each, P as bf16
-// pairs over S) and O of A and B: all 512 columns.  Per sub-block and key tile the tensor
-// core does P.V of tile j, then Q.K of tile j + 1 into the same S; while the softmax warps
-// of one sub-block work, it has the other's two products.  Each sub-block has an issuing
-// warp of its own: the tensor core's queue is a few instructions deep, so a single one left
-// it idle during each of its waits (150 cycles even for a barrier that has completed, eight
-// a tile).  The two take turns: left alone they fall into step, both sub-blocks in their
-// softmax at once and then both at the tensor core.
+// A block: 256 query tokens of a request (two sub-blocks A and B of 128) for one head, over a
+// range of its key tiles.  TMEM holds S of A and B (128 columns each, P over S) and O of A and
+// B: all 512 columns.  Per sub-block and key tile the tensor core does P.V of tile j, then Q.K
+// of tile j + 1 into the same S; while the softmax warps of one sub-block work, it has the
+// other's two products.  Each sub-block has an issuing warp of its own: the tensor core's queue
+// is a few instructions deep, so a single one left it idle during each of its waits (150 cycles
+// even for a barrier that has completed, eight a tile).  The two take turns: left alone they
+// fall into step, both sub-blocks in their softmax at once and then both at the tensor core.
 // K (its first box K0 and the others K12, the last of them the rope) and V stream through
 // eight places of a box: two for K0 and three pairs.  K12 of tile n lies in pair n % 3, V of
 // tile n in the pair that K12 of tile n - 1 left, K0 in place n % 2.  So V(n + 1) and
 // K0(n + 2) load when Q.K(n) is done, K12(n + 2) when P.V(n) is: the ten boxes of two tiles do
 // not fit beside the queries, and these are the ones needed last.
-// Warp 0 loads, warps 1 and 2 issue, warps 4-7 and 8-11 are the softmax of A and B: thread =
-// query token = TMEM lane.  A softmax thread holds a row of 128 scores: the 168 registers
-// that 384 threads get at launch are split 104 / 200 between the warpgroups (384 x 168 =
-// 128 x 104 + 256 x 200).
+// A CTA stays on its SM and takes block after block, tiles counted through; a block's queries
+// load when the last Q.K of the block before is done, its first keys earlier.
+// Warp 0 loads, warps 1 and 2 issue, warp 3 names the blocks, warps 4-7 and 8-11 are the
+// softmax of A and B: thread = query token = TMEM lane.  A softmax thread holds a row of 128
+// scores: the 168 registers that 384 threads get at launch are split 104 / 200 between the
+// warpgroups (384 x 168 = 128 x 104 + 256 x 200).
+// Measured, 16,384 tokens x 16 heads: 2,230 us with one barrier a box, 1,184 with one a tile
+// and the register split, 1,125 with two issuers, 989 with turns and these places, 971 block
+// after block (1,480 TFLOP/s over the whole call; 3,260 cycles a step of 256 x 128, of which
+// the products take 96 %).  Prompts of 1,500 to 2,300 tokens, 128 heads: 718 -> 647 us with
+// the last; what is left there is a block's own start and end, about 13,000 cycles in which
+// the queries are converted and the rows of O leave by stores of 16 bytes a row (32-byte
+// stores, staging, and the next block's queries converted before this one's O is written were
+// all slower).
 constexpr int kSlots = 8;
 // First byte of a place: K0 of tile n, K12 of tile n, V of tile n.
 __device__ __forceinline__ uint32_t place_k0(int n) { return (6 + (n & 1)) * kBox; }
@@ -809,7 +819,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
   if (warp == 3) {
     // Which blocks: the first by the CTA's number, then whatever nobody took yet, one at a time
     // and as late as the loads allow (with four taken ahead the last ones were spread badly:
-    // 16,384 tokens x 16 heads 1,159 us).
+    // 16,384 tokens x 16 heads 1,159 instead of 978 us).
     if (lane == 0) {
       // A block may take any time: this wait ends with the producer's, which are bounded.
       auto asked = [&](int i) {
