@@ -671,9 +671,9 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
 // scores: the 168 registers that 384 threads get at launch are split 104 / 200 between the
 // warpgroups (384 x 168 = 128 x 104 + 256 x 200).
 // Measured, 16,384 tokens x 16 heads: 2,230 us with one barrier a box, 1,184 with one a tile
-// and the register split, 1,125 with two issuers, 989 with turns and these places, 971 block
-// after block (1,480 TFLOP/s over the whole call; 3,260 cycles a step of 256 x 128, of which
-// the products take 96 %).  Prompts of 1,500 to 2,300 tokens, 128 heads: 718 -> 647 us with
+// and the register split, 1,125 with two issuers, 989 with turns and these places, 983 block
+// after block (1,467 TFLOP/s over the whole call; 3,260 cycles a step of 256 x 128, of which
+// the products take 96 %).  Prompts of 1,500 to 2,300 tokens, 128 heads: 718 -> 651 us with
 // the last; what is left there is a block's own start and end, about 13,000 cycles in which
 // the queries are converted and the rows of O leave by stores of 16 bytes a row (32-byte
 // stores, staging, and the next block's queries converted before this one's O is written were
@@ -696,7 +696,7 @@ struct Block {
 constexpr int kBlocks = 4;      // blocks known ahead
 constexpr int kBlockUsers = 11; // warps that read a block: loads, two issuers, eight of the softmax
 struct AttSmem {
-  uint64_t k0_full[2], k12_full[2], k_empty[2], v_full[2], v_empty[2], turn[2], q_full, q_ready[2], s_full[2], p_full[2], o_full[2];
+  uint64_t k0_full[2], k12_full[2], k_empty[2], v_full[2], v_empty[2], turn[2][2], q_full, q_ready[2], s_full[2], p_full[2], o_full[2];
   uint64_t blk_full[kBlocks], blk_empty[kBlocks], want;
   Ctl ctl;
   Block blk[kBlocks];
@@ -791,7 +791,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
       mbar_init(&cs->k_empty[i], 2);
       mbar_init(&cs->v_full[i], 1);
       mbar_init(&cs->v_empty[i], 2);
-      mbar_init(&cs->turn[i], 1);
+      mbar_init(&cs->turn[i][0], 1);
+      mbar_init(&cs->turn[i][1], 1);
       mbar_init(&cs->q_ready[i], 128);
       mbar_init(&cs->s_full[i], 1);
       mbar_init(&cs->p_full[i], 128);
@@ -809,7 +810,17 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = cs->ctl.tmem_base;
   // Block i of this CTA, for a warp that uses it; its place is given back by `done_with`.
-  auto block = [&](int i) { return wwait(&cs->blk_full[i % kBlocks], (i / kBlocks) & 1, &cs->ctl, hdr); };
+  // A role that has nothing to do in a block waits it out: 2^28 keys take 4 seconds.
+  auto long_wait = [&](uint64_t* bar, uint32_t parity) {
+    for (int i = 0; i < 20; ++i) {
+      if (mbar_wait(bar, parity, kWaitLimitNs)) return true;
+      if (*reinterpret_cast<volatile int*>(&cs->ctl.abort)) return false;
+    }
+    return give_up(bar, &cs->ctl, hdr);
+  };
+  auto block = [&](int i) {
+    return __all_sync(0xffffffffu, long_wait(&cs->blk_full[i % kBlocks], (i / kBlocks) & 1));
+  };
   auto done_with = [&](int i) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&cs->blk_empty[i % kBlocks]);
@@ -821,14 +832,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     // and as late as the loads allow (with four taken ahead the last ones were spread badly:
     // 16,384 tokens x 16 heads 1,159 instead of 978 us).
     if (lane == 0) {
-      // A block may take any time: this wait ends with the producer's, which are bounded.
-      auto asked = [&](int i) {
-        while (!mbar_wait(&cs->want, (i - 1) & 1, kWaitLimitNs))
-          if (*reinterpret_cast<volatile int*>(&cs->ctl.abort)) return false;
-        return true;
-      };
       for (int i = 0;; ++i) {
-        if (i > 0 && !asked(i)) break;
+        if (i > 0 && !long_wait(&cs->want, (i - 1) & 1)) break;
         if (i >= kBlocks && !wait(&cs->blk_empty[i % kBlocks], ((i / kBlocks) & 1) ^ 1, &cs->ctl, hdr)) break;
         const long long at = i == 0 ? blockIdx.x : (long long)gridDim.x + atomicAdd(&hdr->pad[4], 1);
         Block& k = cs->blk[i % kBlocks];
@@ -938,7 +943,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     const int nbq = a.nbq;
     const uint32_t ts = tmem + 128 * s, to = tmem + 256 + 128 * s;
     bool ok = true;
-    int n0 = 0, np = 0, nturn = 0;         // key tiles of the blocks before, P tiles and turns taken
+    int n0 = 0, np = 0, nblk = 0;      // key tiles of the blocks before, P tiles taken, blocks with tiles
+    // A may be in the next block while B has its last turn of this one before it, so blocks
+    // alternate between two barriers each
+    int par = 0, nturn[2] = {0, 0};
     for (int i = 0; ok; ++i) {
       if (!(ok = block(i))) break;
       const Block& blk = cs->blk[i % kBlocks];
@@ -947,7 +955,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
       const bool both = jb > ja && blk.j1[s ^ 1] > blk.j0[s ^ 1];
       done_with(i);
       if (je <= js) continue;
-      if (jb > ja && !(ok = wwait(&cs->q_ready[s], i & 1, &cs->ctl, hdr))) break;
+      // waited for in every block with tiles, used or not: a barrier's parity tells one phase from
+      // the next only, so neither side may be two ahead
+      if (!(ok = wwait(&cs->q_ready[s], nblk++ & 1, &cs->ctl, hdr))) break;
       bool add = false;   // O holds something
       // Group n: O (+)= P V of key tile n - 1, then S = Q K^T of key tile n
       int n = n0;
@@ -958,7 +968,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         if (j > js && !(ok = wwait(&cs->v_full[v & 1], (v >> 1) & 1, &cs->ctl, hdr))) break;
         if (use_v && !(ok = wwait(&cs->p_full[s], np & 1, &cs->ctl, hdr))) break;
         // the sub-blocks take turns, A first in each block
-        if (both && (s == 1 || j > js) && !(ok = wwait(&cs->turn[s], nturn++ & 1, &cs->ctl, hdr))) break;
+        if (both && (s == 1 || j > js)) {
+          const int t = par ? nturn[1]++ : nturn[0]++;
+          if (!(ok = wwait(&cs->turn[s][par], t & 1, &cs->ctl, hdr))) break;
+        }
         tc_fence_after();
         const uint64_t dv = dv0 + (place_v(v + 3) >> 4), dk0 = dr0 + (place_k0(n) >> 4), dk12 = dr0 + (place_k12(n) >> 4);
         if (elect_one()) {
@@ -983,7 +996,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         if (elect_one()) {
           for (int b = 1; b < nbq && use_k; ++b) {
             const uint64_t dq = dq0 + b * kBoxStep, dk = dk12 + (b - 1) * kBoxStep;
-            if (b == nbq - 1 && both) mbar_arrive(&cs->turn[s ^ 1]);   // its wait passes under the last box
+            if (b == nbq - 1 && both) mbar_arrive(&cs->turn[s ^ 1][par]);   // its wait passes under the last box
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) mma_ss(ts, dq + 2 * kk, dk + 2 * kk, id_s, 1u);
           }
@@ -991,7 +1004,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
             mma_commit(&cs->s_full[s]);
             mma_commit(&cs->k_empty[n & 1]);
           } else {
-            if (both && (s == 0 || j < je)) mbar_arrive(&cs->turn[s ^ 1]);
+            if (both && (s == 0 || j < je)) mbar_arrive(&cs->turn[s ^ 1][par]);
             if (j < je) mbar_arrive(&cs->k_empty[n & 1]);
           }
         }
@@ -1002,6 +1015,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         }
       }
       n0 += je - js;
+      par ^= both;
     }
     // the last signals have arrived before the barriers go away
     if (ok && n0 > 0) wwait(&cs->v_empty[(n0 - 1) & 1], ((n0 - 1) >> 1) & 1, &cs->ctl, hdr);
@@ -1028,10 +1042,13 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
       row_range(a, blk.q, min(r, last), unused, hi_first);
     }
     float sl2 = a.scale * 1.4426950408889634f;
+    if (blk.je > blk.js) {   // waited for whether used or not, as q_ready is
+      ok = wwait(&cs->q_full, (phase >> 1) & 1, &cs->ctl, hdr);
+      phase ^= 2;
+    }
     if (live) {
       // this thread's query row: bf16 -> f16, scaled to a largest magnitude in [2^10, 2^11);
       // a scale below zero turns its sign, a scale of zero its values to zero
-      ok = wwait(&cs->q_full, (phase >> 1) & 1, &cs->ctl, hdr);
       if (ok && (kHalf || !(sl2 > 0.f))) {
         uint8_t* qr = sQ + s * a.nbq * kBox + row * 128;
         __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);   // a NaN does not count: its row is NaN anyhow
@@ -1062,8 +1079,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         fence_proxy_async_smem();
       }
     }
-    mbar_arrive(&cs->q_ready[s]);
-    if (blk.je > blk.js) phase ^= 2;
+    if (blk.je > blk.js) mbar_arrive(&cs->q_ready[s]);
     float m = -CUDART_INF_F, l = 0.f;
     const uint4* live_rows = a.live + blk.q.tile0;
     if (ok && s < blk.nsub) {

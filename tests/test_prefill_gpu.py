@@ -368,3 +368,22 @@ def test_captured_and_replayed(dev):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want_c)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_short_and_long_blocks_in_turn(dev, fmt):
+    # many times more blocks than SMs, of one and of two sub-blocks, with and without keys: what one
+    # of a block's roles skips must not let it run ahead into the next
+    c = Case(fmt, 20, **NARROW, H=96, ps=16, qlens=(1, 300, 129, 0, 128, 500, 3, 260, 17, 400, 64, 5), past=(0, 0, 40, 9, 0, 0, 0, 0, 200, 0, -10, 0),
+             pad=2)
+    out, lse = call(c, dev, debug=False)
+    compare(c, out, lse, "e4m3" if c.fmt == ref.E4M3 else "f16")
+    first = out.clone()
+    for _ in range(5):
+        again, _ = call(c, dev, debug=False)
+        assert torch.equal(again[:c.T], first[:c.T])
+
+
+def test_short_and_long_blocks_in_turn_over_wide_heads(dev):
+    c = Case("bf16", 21, **WIDE, H=64, ps=64, qlens=(1, 300, 129, 128, 420, 3, 260), past=(0,) * 7)
+    check(c, dev)
