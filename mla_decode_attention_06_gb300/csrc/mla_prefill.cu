@@ -671,10 +671,10 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
 // scores: the 168 registers that 384 threads get at launch are split 104 / 200 between the
 // warpgroups (384 x 168 = 128 x 104 + 256 x 200).
 // Measured, 16,384 tokens x 16 heads: 2,230 us with one barrier a box, 1,184 with one a tile
-// and the register split, 1,125 with two issuers, 989 with turns and these places, 983 block
-// after block (1,467 TFLOP/s over the whole call; 3,260 cycles a step of 256 x 128, of which
-// the products take 96 %).  Prompts of 1,500 to 2,300 tokens, 128 heads: 718 -> 651 us with
-// the last; what is left there is a block's own start and end, about 13,000 cycles in which
+// and the register split, 1,125 with two issuers, 989 with turns and these places, 978 block
+// after block, 895 with the blocks in a better order (1,610 TFLOP/s over the whole call; 3,260 cycles a step of 256 x 128, of which
+// the products take 96 %).  Prompts of 1,500 to 2,300 tokens, 128 heads: 718, 650 and 629 us with
+// the last three; what is left there is a block's own start and end, about 13,000 cycles in which
 // the queries are converted and the rows of O leave by stores of 16 bytes a row (32-byte
 // stores, staging, and the next block's queries converted before this one's O is written were
 // all slower).
@@ -693,6 +693,7 @@ struct Block {
   int r0, nsub, h, split;     // first query row, sub-blocks, head of the pass (-1: no more), key split
   int j0[2], j1[2], js, je;   // key tiles of each sub-block, and of both
 };
+constexpr long long kGroupBytes = 64ll << 20;   // half the L2
 constexpr int kBlocks = 4;      // blocks known ahead
 constexpr int kBlockUsers = 11; // warps that read a block: loads, two issuers, eight of the softmax
 struct AttSmem {
@@ -729,9 +730,15 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
 // Bits [0, n) of a word.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
 
-// Block `at`: split fastest, then query block, then head.
+// Block `at`: split fastest, then head, then query block (the longest first, so that the SMs
+// finish together), in groups of as many heads as keep their keys and values in half the L2
+// (16,384 tokens x 16 heads 978 us head by head, 895 so; 927 and 902 with 16 and 128 MB).
 __device__ __forceinline__ void set_block(const Args& a, int nitems, long long at, Block& k) {
-  const int split = (int)(at % a.splits), item = (int)(at / a.splits % nitems);
+  const long long head = (long long)max(a.hdr->total_tiles, 1) * (a.nbk + a.nbv) * kBox, i = at / a.splits;
+  const int group = (int)min((long long)a.hg, max(1ll, kGroupBytes / head));
+  const int h0 = (int)(i / ((long long)group * nitems)) * group, heads = min(group, a.hg - h0);
+  const long long in = i - (long long)h0 * nitems;
+  const int split = (int)(at % a.splits), item = (int)(in / heads);
   const int2 it = a.items[item];
   const Req q = a.reqs[it.x];
   const int r0 = it.y * 2 * kTile, nsub = q.qlen > r0 + kTile ? 2 : 1;
@@ -753,7 +760,7 @@ __device__ __forceinline__ void set_block(const Args& a, int nitems, long long a
   k.q = q;
   k.r0 = r0;
   k.nsub = nsub;
-  k.h = (int)(at / a.splits / nitems);
+  k.h = h0 + (int)(in % heads);
   k.split = split;
   for (int s = 0; s < 2; ++s) {
     k.j0[s] = j0[s];
