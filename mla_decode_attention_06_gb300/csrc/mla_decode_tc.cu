@@ -658,6 +658,11 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
   const int ps = a.ks.page_size;
   const int rows_per_load = ps < kTileKeys ? ps : kTileKeys;
 
+  // The issuing lane of a converged warp.  Behind elect.sync the compiler knows that one thread
+  // runs the MMA loops, behind lane == 0 it does not: 64 e2m1 requests of 1,024 to 8,192 tokens
+  // 208 -> 195 us, 128 e4m3 ones 736 -> 704 us.  Over bf16 it did not help (82 -> 86 us for 8
+  // requests of 4,096 keys).
+  auto issuer = [&]() { return C::kCoded ? elect_one() : lane == 0; };
   if (C::kGrouped && warp < 4) {
     if (C::kConvThreads == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
@@ -1024,9 +1029,6 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         tc_fence_after();
         const uint64_t dk = dk0 + (uint64_t)((s * C::kStageBytes) >> 4);
         const uint32_t sd = tmem + C::kSCol + 64 * b;
-        // One elected lane issues: behind elect.sync the compiler knows that one thread runs
-        // the loop, behind lane == 0 it does not (64 e2m1 requests of 1,024 to 8,192 tokens:
-        // 208 -> 195 us).
         // kEarly, CTA 1: its own latent half, the first that is widened, is the shared-memory
         // part of the query; that goes first there, then the TMEM part, then the rope
         const bool smem_first = C::kEarly && crank == 1;
@@ -1034,7 +1036,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         // (64 columns; past qk_rope both sides read the TMA zero fill) with A =
         // query boxes in shared memory.  The MMA queue is shallow, so the issue
         // runs back to back; the box loops stay rolled to keep the code small.
-        if (!smem_first && elect_one()) {
+        if (!smem_first && issuer()) {
 #pragma unroll 1
           for (int j = 0; j < C::QT / 64; ++j) {
             const uint64_t dkj = dk + (uint64_t)((j * C::kBox) >> 4);
@@ -1050,7 +1052,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
           tc_fence_after();
           q_smem = true;
         }
-        if (smem_first && elect_one()) {
+        if (smem_first && issuer()) {
 #pragma unroll 1
           for (int i = 0; i < C::NQS; ++i) {
             const uint64_t dqi = dq0 + (uint64_t)((i * C::kQBox) >> 4);
@@ -1067,7 +1069,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
           if (!wwait(&cs->kv_conv[s], par, cs, hdr)) return;
           tc_fence_after();
         }
-        if (smem_first && elect_one()) {
+        if (smem_first && issuer()) {
 #pragma unroll 1
           for (int j = 0; j < C::QT / 64; ++j) {
             const uint64_t dkj = dk + (uint64_t)((j * C::kBox) >> 4);
@@ -1076,7 +1078,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
               mma_ts(sd, tmem + C::kQCol + 8 * (4 * j + kk), dkj + (uint64_t)((kk * 32) >> 4), idesc_qk, 1u);
           }
         }
-        if (elect_one()) {
+        if (issuer()) {
 #pragma unroll 1
           for (int i = smem_first ? C::NQS : 0; i <= C::NQS; ++i) {
             // box i of the query buffer pairs with cache box QT / 64 + i (the rope box after the latent ones)
@@ -1111,7 +1113,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         if (!wwait(&cs->p_full[b], (cp >> 1) & 1, cs, hdr)) return;
         if (it == ia && si > 0 && !wwait(&cs->o_free, (si - 1) & 1, cs, hdr)) return;
         tc_fence_after();
-        if (elect_one()) {
+        if (issuer()) {
           // B = this CTA's latent boxes of the stage, keys along K (MN-major)
           const uint64_t dv = dv0 + (uint64_t)(((cp % S) * C::kStageBytes) >> 4);
 #pragma unroll

@@ -59,7 +59,6 @@ struct Args {
   const float* wscale; // e4m3 block scales [H, ceil(M/128), ceil(K/128)]
   // absorb
   __nv_bfloat16* q_full; int KQ, L, R, N; const __nv_bfloat16* q;
-  bool half;           // q_full holds f16 (the operands of the e2m1 decode); what f16 does not reach is reported
   // W_uv
   __nv_bfloat16* out; int V; const float* lse_ws; float* lse_out;
   PlanHeader* hdr;
@@ -106,7 +105,9 @@ __device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v, PlanHeader* hdr) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <bool kFp8>
+// kHalf: q_full holds f16 (the operands of the e2m1 decode); what f16 does not reach is reported.
+// An instance of its own: chosen at run time it cost the epilogue of every call 4 us of 14.
+template <bool kFp8, bool kHalf>
 __global__ void __launch_bounds__(kThreads, 1) wgemm_kernel(const __grid_constant__ Maps maps, const Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgemm_kernel(const __grid_constan
       for (int j = 0; j < kBatch; ++j) {
         const int i = i0 + j * stride, t = t0 + i / cpr;
         if (i < TN * cpr && t < a.T) {
-          if (a.half) v[j] = bf16x8_to_f16x8(v[j], a.hdr);
+          if (kHalf) v[j] = bf16x8_to_f16x8(v[j], a.hdr);
           reinterpret_cast<uint4*>(a.q_full + ((size_t)t * kMaxHeads + h) * a.KQ + a.L)[i % cpr] = v[j];
         }
       }
@@ -335,8 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1) wgemm_kernel(const __grid_constan
       }
 #pragma unroll
       for (int q = 0; q < 32; ++q)
-        if (j0 + q < TN) stg[((size_t)i * TN + j0 + q) * 128 + row] = a.half ? f16_in_bf16(v[q]) : __float2bfloat16_rn(v[q]);
-      if (a.half) {
+        if (j0 + q < TN) stg[((size_t)i * TN + j0 + q) * 128 + row] = kHalf ? f16_in_bf16(v[q]) : __float2bfloat16_rn(v[q]);
+      if (kHalf) {
         // columns past the last token hold zeros
         bool over = false;
 #pragma unroll
@@ -388,7 +389,7 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-cudaError_t launch(const Args& a0, WFmt wf, const void* w, const void* x, int Kx, cudaStream_t s) {
+cudaError_t launch(const Args& a0, WFmt wf, const void* w, const void* x, int Kx, bool half, cudaStream_t s) {
   Args a = a0;
   EncodeTiledFn fn = encode_fn();
   if (!fn || a.T == 0) return a.T == 0 ? cudaSuccess : cudaErrorInvalidValue;
@@ -440,8 +441,8 @@ cudaError_t launch(const Args& a0, WFmt wf, const void* w, const void* x, int Kx
   }
   if (!hit) {
   {
+      cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)a.H * a.M};
     const bool f8 = wf == WFmt::kE4M3;
-    cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)a.H * a.M};
     cuuint64_t strides[1] = {(cuuint64_t)a.K * (f8 ? 1 : 2)};
     cuuint32_t box[2] = {64, 128};
     cuuint32_t es[2] = {1, 1};
@@ -466,7 +467,6 @@ cudaError_t launch(const Args& a0, WFmt wf, const void* w, const void* x, int Kx
     cache_maps[a.mode] = maps;
     cache_valid[a.mode] = true;
   }
-  const bool f8 = wf == WFmt::kE4M3;
   const size_t ring_bytes = std::max((size_t)a.S * stage_smem, (size_t)a.MB * a.TN * 128 * 2);
   const size_t smem = 1024 + ring_bytes + (2 * kMaxStages + 2) * 8;
   if (smem > 232448) return cudaErrorInvalidValue;
@@ -481,14 +481,9 @@ cudaError_t launch(const Args& a0, WFmt wf, const void* w, const void* x, int Kx
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.mode == 1 ? 1 : 0;
-  cudaError_t e;
-  if (f8) {
-    e = ensure_smem_limit(reinterpret_cast<const void*>(wgemm_kernel<true>), (int)smem);
-    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, wgemm_kernel<true>, maps, a);
-  } else {
-    e = ensure_smem_limit(reinterpret_cast<const void*>(wgemm_kernel<false>), (int)smem);
-    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, wgemm_kernel<false>, maps, a);
-  }
+  auto kernel = wf == WFmt::kE4M3 ? wgemm_kernel<true, false> : half ? wgemm_kernel<false, true> : wgemm_kernel<false, false>;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, maps, a);
   return e;
 }
 
@@ -499,7 +494,6 @@ cudaError_t launch_absorb_tc(const mla_dims_t& d, int T, const __nv_bfloat16* q,
                              const PlanInputs& plan, bool half, cudaStream_t s) {
   wg::Args a{};
   a.mode = 0;
-  a.half = half;
   a.H = d.num_heads;
   a.T = T;
   a.M = d.kv_lora_rank;
@@ -513,7 +507,7 @@ cudaError_t launch_absorb_tc(const mla_dims_t& d, int T, const __nv_bfloat16* q,
   a.q = q;
   a.hdr = hdr;
   a.pin = plan;
-  return wg::launch(a, wf, w_uk, q, d.qk_nope + d.qk_rope, s);
+  return wg::launch(a, wf, w_uk, q, d.qk_nope + d.qk_rope, half, s);
 }
 
 cudaError_t launch_uv_tc(const mla_dims_t& d, int T, const __nv_bfloat16* o_lat, WFmt wf, const void* w_uv,
@@ -531,7 +525,7 @@ cudaError_t launch_uv_tc(const mla_dims_t& d, int T, const __nv_bfloat16* o_lat,
   a.lse_ws = lse_ws;
   a.lse_out = lse_out;
   a.hdr = hdr;
-  return wg::launch(a, wf, w_uv, o_lat, d.kv_lora_rank, s);
+  return wg::launch(a, wf, w_uv, o_lat, d.kv_lora_rank, false, s);
 }
 
 }  // namespace mla
