@@ -14,8 +14,8 @@
 //   gather   cache rows of any format -> bf16 tiles of 128 rows, and which rows are live.
 //   expand   K and V of a pass's heads: one GEMM tile (128 rows x (N | V) x L) per key
 //            tile and head, tcgen05, written as the attention's shared-memory images.
-//   attend   one CTA per SM, taking (query block, head, key split) after (...): softmax on the
-//            fly between two tcgen05 products.
+//   attend   one CTA per SM, taking one (query block, head, key split) after another: running
+//            softmax between two tcgen05 products.
 //   combine  joins the key splits (only where a call has few query blocks).
 //
 // Every tile that passes between these kernels is stored as 128-byte-swizzled boxes of
