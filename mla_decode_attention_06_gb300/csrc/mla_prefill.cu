@@ -93,10 +93,18 @@ struct Args {
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// After the wait on the previous kernel: does this sequence run?
+// Whole block, after the wait on the previous kernel: does this sequence run?  One thread reads
+// the flag for all: other blocks of the same launch may raise it meanwhile, and a block whose
+// warps disagree would wait for threads that have left.  Blocks may disagree: what a launch that
+// raises the flag writes is not used.
 __device__ __forceinline__ bool runs(const Args& a) {
-  const bool wide = *reinterpret_cast<const volatile int*>(&a.hdr->pad[3]) != 0;
-  return a.half ? !wide : wide;
+  __shared__ int go;
+  if (threadIdx.x == 0) {
+    const bool wide = *reinterpret_cast<const volatile int*>(&a.hdr->pad[3]) != 0;
+    go = a.half ? !wide : wide;
+  }
+  __syncthreads();
+  return go != 0;
 }
 // Whole warp: is the largest of the lanes' magnitudes (fp32 bits) one that f16 holds well:
 // zero, or within [2^-8, 2^15]?  The others then are off by at most 2^-17 of it.

@@ -387,3 +387,24 @@ def test_short_and_long_blocks_in_turn(dev, fmt):
 def test_short_and_long_blocks_in_turn_over_wide_heads(dev):
     c = Case("bf16", 21, **WIDE, H=64, ps=64, qlens=(1, 300, 129, 128, 420, 3, 260), past=(0,) * 7)
     check(c, dev)
+
+
+def test_blocks_that_start_late_beside_others_that_raise_the_flag(dev):
+    # one head past f16's range, most blocks of the expansion with a pair or two of their own, and
+    # another stream's products on the SMs, so that blocks start while others end: all warps of a
+    # block take the same decision, no wait runs out and the bits do not change
+    c = Case("bf16", 22, **NARROW, H=96, qlens=(130, 70), past=(200, 0))
+    c.w[1][40] = ref.bf16_bits(ref.bf16_values(c.w[1][40]) * 2.0 ** 30)
+    c.uv = ref.bf16_values(c.w[1])
+    first, lse = call(c, dev)
+    compare(c, first, lse, "bf16")
+    args = c.args(dev)
+    x = torch.randn(2048, 2048, device=dev, dtype=torch.bfloat16)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(s):
+            for _ in range(4):
+                torch.mm(x, x)
+        out, _ = call(c, dev, args)
+        assert torch.equal(out, first)
