@@ -841,7 +841,10 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
           for (int kk = k + 1 + lane; kk <= kl; kk += 32) {
             bulk_prefetch_l2(reinterpret_cast<const float4*>(a.part_o) + ((size_t)(kk * 2 * NS + tslot) * L4 + lat_x0 / 4) * Hh,
                              (uint32_t)(LC * Hh * 4));
-            bulk_prefetch_l2(a.part_lse + (size_t)(kk * 2 * NS + tslot) * 2 * Hh, (uint32_t)(2 * Hh * 4));
+            // 8 H bytes, widened to whole 16-byte pieces: with an odd H neither its start nor its
+            // size is one (the workspace goes on past part_lse's last slot)
+            const uint64_t ls = (uint64_t)(kk * 2 * NS + tslot) * 8 * Hh, lb = ls & ~15ull;
+            bulk_prefetch_l2(reinterpret_cast<const uint8_t*>(a.part_lse) + lb, (uint32_t)(((ls + 8 * Hh + 15) & ~15ull) - lb));
           }
         }
         if constexpr (MODE == kLoadFp4) {

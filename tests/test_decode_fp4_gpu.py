@@ -205,3 +205,11 @@ def test_own_stream_without_workspace(dev):
     out, _ = run_fp4(p, rows, d, stream=s, debug=False)
     s.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("heads", [1, 3, 127])
+@pytest.mark.parametrize("make", [wide, narrow])
+def test_odd_heads_over_split_keys(dev, make, heads):
+    # tokens that several partitions share, with rows of 8 H bytes that are no whole 16-byte
+    # pieces; the bf16 decode that `check` runs beside it reads the same rows
+    check(make(43, (700, 64, 900, 333), H=heads), dev, 9)
