@@ -353,16 +353,21 @@ __device__ __noinline__ void merge_split_token(const DecodeArgs& a, int t, const
   auto slot_of = [&](int k) { return (k == kf ? slot_kf : 0) * ns + ts; };
   auto lse_of = [&](int k) { return __ldcg(part_lse + ((size_t)(k * 2 * ns + slot_of(k)) * 2 + rank) * H + row); };
   float mx = -CUDART_INF_F;
-  for (int k = kf; k <= kl; ++k) mx = fmaxf(mx, lse_of(k));
+  bool nan = false;   // a partial that is NaN makes the row NaN (the maximum passes over it)
+  for (int k = kf; k <= kl; ++k) {
+    const float v = lse_of(k);
+    mx = fmaxf(mx, v);
+    nan |= v != v;
+  }
   float sum = 0.f;
   if (mx != -CUDART_INF_F)
     for (int k = kf; k <= kl; ++k) sum += __expf(lse_of(k) - mx);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = nan ? CUDART_NAN_F : (sum > 0.f ? 1.f / sum : 0.f);
   for (int col0 = 0; col0 < LC; col0 += 32) {
     float4 acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (mx != -CUDART_INF_F) {
+    if (mx != -CUDART_INF_F || nan) {
       for (int k = kf; k <= kl; ++k) {
         const float w = __expf(lse_of(k) - mx) * inv;
         const int c0 = (lat_x0 + col0) / 4;
@@ -384,7 +389,8 @@ __device__ __noinline__ void merge_split_token(const DecodeArgs& a, int t, const
       dst[i] = make_uint4(pack_bf16(acc[2 * i].x, acc[2 * i].y), pack_bf16(acc[2 * i].z, acc[2 * i].w),
                           pack_bf16(acc[2 * i + 1].x, acc[2 * i + 1].y), pack_bf16(acc[2 * i + 1].z, acc[2 * i + 1].w));
   }
-  if (rank == 0) a.lse_ws[(size_t)t * H + row] = mx != -CUDART_INF_F ? mx + __logf(sum) : -CUDART_INF_F;
+  if (rank == 0)
+    a.lse_ws[(size_t)t * H + row] = nan ? CUDART_NAN_F : (mx != -CUDART_INF_F ? mx + __logf(sum) : -CUDART_INF_F);
 }
 
 // Warp-uniform forms: every lane waits, then the warp votes, so lanes never
@@ -471,9 +477,17 @@ __device__ __noinline__ bool merge_in_tmem(const DecodeArgs& a, Smem* cs, int t,
     return kk == k ? lse_own : __ldcg(lse_ptr(kk));
   };
   float mx = -CUDART_INF_F;
+  bool nan = false;   // a partial that is NaN: its O is too, and so is what it is added to
 #pragma unroll
-  for (int j = 0; j < 8; ++j) mx = fmaxf(mx, lv0[j]);
-  for (int kk = kf + 8; kk <= kl; ++kk) mx = fmaxf(mx, lse_at(kk));
+  for (int j = 0; j < 8; ++j) {
+    mx = fmaxf(mx, lv0[j]);
+    nan |= lv0[j] != lv0[j];
+  }
+  for (int kk = kf + 8; kk <= kl; ++kk) {
+    const float v = lse_at(kk);
+    mx = fmaxf(mx, v);
+    nan |= v != v;
+  }
   float sum = 0.f;
   if (mx != -CUDART_INF_F) {
 #pragma unroll
@@ -549,7 +563,8 @@ __device__ __noinline__ bool merge_in_tmem(const DecodeArgs& a, Smem* cs, int t,
     fence_proxy_async_smem();
     bulk_copy_s2g(a.o_lat + ((size_t)t * H + row) * L + lat_x0, srow, LC * 2);
     bulk_commit();
-    if (rank == 0) a.lse_ws[(size_t)t * H + row] = mx != -CUDART_INF_F ? mx + __logf(sum) : -CUDART_INF_F;
+    if (rank == 0)
+      a.lse_ws[(size_t)t * H + row] = nan ? CUDART_NAN_F : (mx != -CUDART_INF_F ? mx + __logf(sum) : -CUDART_INF_F);
     bulk_wait_all();
   }
   return true;
@@ -1589,8 +1604,9 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         merger = cs->fix_last;
       }
       const int slot = (is_first_seg ? 0 : 1) * NS + tslot;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float lse = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+      // l = 0: no visible key; l NaN: a score was, and the row is, in its log-sum-exp too
+      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : CUDART_NAN_F);
+      const float lse = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : (l == 0.f ? -CUDART_INF_F : CUDART_NAN_F);
       const bool live = row < H && !shadow;
       if (!merger) {
 #pragma unroll 1

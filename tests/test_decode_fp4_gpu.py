@@ -213,3 +213,44 @@ def test_odd_heads_over_split_keys(dev, make, heads):
     # tokens that several partitions share, with rows of 8 H bytes that are no whole 16-byte
     # pieces; the bf16 decode that `check` runs beside it reads the same rows
     check(make(43, (700, 64, 900, 333), H=heads), dev, 9)
+
+
+def all_formats(p, dev, d, num_splits, **kw):
+    """Outputs of the bf16, e4m3 and e2m1 decode (a bf16 problem's shapes; e4m3 rows and weights
+    are its values over a power of two)."""
+    import mla_decode_attention_06_gb300 as M
+    lse = torch.empty(p.T, p.H, device=dev)
+    yield "bf16", run_gpu(p, d, num_splits=num_splits, fold_pairs=False)
+    _, rows = coded(p)
+    yield "e2m1", run_fp4(p, rows, d, num_splits=num_splits, debug=False)
+    e4 = torch.float8_e4m3fn
+    live = ~np.isnan(ref.bf16_values(p.rows_bf16)).any(1)
+    rows = np.zeros((len(live), p.L + 2 * p.R), np.uint8)
+    scales = np.ones(len(live), np.float32)
+    rows[live], scales[live] = ref.encode(p.rows_bf16[live, :p.L], p.rows_bf16[live, p.L:], ref.E4M3)
+    pool = torch.zeros((p.pool_rows, p.L + 2 * p.R), dtype=torch.uint8, device=dev)
+    row_scales = torch.zeros(p.pool_rows, device=dev)
+    at = torch.from_numpy(p.rows_phys).to(dev)
+    pool[at], row_scales[at] = torch.from_numpy(rows).to(dev), torch.from_numpy(scales).to(dev)
+    w = []
+    for x in (d["w_uk"], d["w_uv"]):
+        w += [x.to(e4), torch.ones(p.H, -(-x.shape[1] // 128), -(-x.shape[2] // 128), device=dev)]
+    yield "e4m3", M.mla_decode_paged_fp8(d["q"], d["offsets"], pool, row_scales, d["block_table"], d["cache_lens"], *w,
+                                         page_size=p.ps, scale=p.scale, mask=p.mask, window=p.window, lse_out=lse,
+                                         num_splits=num_splits)
+
+
+@pytest.mark.parametrize("num_splits", [1, 3, 7, 0])
+@pytest.mark.parametrize("make", [wide, narrow])
+def test_nan_rows_stay_nan_over_split_keys(dev, make, num_splits):
+    # every partial of a head is NaN, in tokens that end in a partition's first segment and in its
+    # last: whichever partition joins them, output and log-sum-exp are NaN, and no other head's bits move
+    p = make(44, (700, 64, 900, 333, 1200, 5))
+    d = device_inputs(p, dev)
+    clean = {k: (o.clone(), l.clone()) for k, (o, l) in all_formats(p, dev, d, num_splits)}
+    d["q"][:, 1, 3] = float("nan")
+    for k, (out, lse) in all_formats(p, dev, d, num_splits):
+        assert torch.isnan(out[:, 1].float()).all() and torch.isnan(lse[:, 1]).all(), k
+        others = [h for h in range(p.H) if h != 1]
+        assert torch.isfinite(clean[k][0].float()).all() and torch.isfinite(clean[k][1]).all(), k
+        assert torch.equal(out[:, others], clean[k][0][:, others]) and torch.equal(lse[:, others], clean[k][1][:, others]), k
