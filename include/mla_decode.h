@@ -182,11 +182,14 @@ typedef enum {
 /* 4-bit latent cache: mla_decode_paged over rows in MLA_CACHE_E2M1 format.
  *   kv_pool_fp4   bytes [num_pages, ps, row], row = 400 at (L, R) = (512, 64)
  * Other arguments, shapes, masks, workspace and errors as mla_decode_paged (bf16
- * weights).  The attention's products take f16 operands: the cached codes times scales
- * from 2^-23 to 2^13 exactly, the absorbed query and the rope parts rounded to f16 (their
- * magnitudes stay below 65520; below 2^-14 they keep a 2^-25 absolute precision).  A
- * finite magnitude above f16's range becomes an infinity, which makes the queries that
- * use it NaN, and is recorded: MLA_ERR_DEVICE_CHECK in debug mode.  Query tokens are walked one at a time (MLA_FLAG_FOLD_PAIRS does not apply). */
+ * weights).  The attention's products take f16 operands: the cached codes times their
+ * scales (exactly for scales from 2^-23 to 2^13), the absorbed query and the rope parts, each
+ * rounded to f16 (magnitudes stay below 65520; below 2^-14 they keep a 2^-25 absolute
+ * precision).  A finite value that f16 does not hold is recorded (MLA_ERR_DEVICE_CHECK in debug
+ * mode) and never used quietly: of the query it makes that head NaN, of a row's latent part
+ * every query that sees the row, of a row's rope part the heads whose score it does not
+ * lower, the others taking that key's score from the value itself.  Query tokens are walked
+ * one at a time (MLA_FLAG_FOLD_PAIRS does not apply). */
 int mla_decode_paged_fp4(const mla_dims_t* dims, const mla_opts_t* opts, const void* q,
                          const uint32_t* input_row_offsets, int32_t batch, int32_t total_q,
                          const void* kv_pool_fp4, const int32_t* block_table, int32_t block_table_stride,

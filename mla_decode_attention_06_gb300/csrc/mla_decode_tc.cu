@@ -90,6 +90,7 @@ struct Smem {   // control block after the stage ring
   alignas(16) int32_t rowid[kMaxStages][64];
   uint32_t tmem_base;
   int abort;
+  int over;       // e2m1: a rope value past f16's range came by
   int fix_last;   // this CTA merges the split token it just finished (it claimed it last)
 };
 
@@ -270,11 +271,19 @@ __device__ __forceinline__ uint32_t e4m3x2_scaled_bf16x2(uint16_t two, float sca
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// Two e2m1 codes (a byte, low nibble first) times a scale, as an f16 pair.
-__device__ __forceinline__ uint32_t e2m1x2_scaled_f16x2(uint32_t byte, __half2 scale) {
+// Two e2m1 codes (a byte, low nibble first) times two scales, as an f16 pair, rounded once at
+// most: the first product is exact.  What f16 does not hold becomes NaN (an infinity times zero,
+// added); `top` keeps the largest magnitude before that.
+__device__ __forceinline__ uint32_t e2m1x2_scaled_f16x2(uint32_t byte, __half2 s1, __half2 s2, __half2& top) {
   const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1);
-  const __half2 v = __hmul2(__half2(h), scale);
+  __half2 v = __hmul2(__hmul2(__half2(h), s1), s2);
+  top = __hmax2(top, __habs2(v));
+  v = __hfma2(v, __float2half2_rn(0.f), v);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Is one of the two non-negative numbers infinite?
+__device__ __forceinline__ bool any_inf(__half2 v) {
+  return ((*reinterpret_cast<const uint32_t*>(&v) + 0x04000400u) & 0x80008000u) != 0u;
 }
 
 // Eight e2m1 codes as four f16 pairs, times the power of two in the tables: the f16 values of
@@ -292,14 +301,10 @@ __device__ __forceinline__ uint4 e2m1x8_f16(uint32_t w, uint32_t t0, uint32_t t1
                     __byte_perm(b, 0u, 0x3424u));
 }
 
-// A scale byte (2^(b - 127), 255 = NaN) as an f16 pair: zero below 2^-24, infinity above 2^15.
-__device__ __forceinline__ __half2 e8m0_f16x2(uint32_t b) {
-  const int e = (int)b - 127;
-  uint32_t h = (uint32_t)(e + 15) << 10;
-  if (e < -14) h = e < -24 ? 0u : 1u << (e + 24);
-  if (e > 15) h = b == 255u ? 0x7E00u : 0x7C00u;
-  h |= h << 16;
-  return *reinterpret_cast<const __half2*>(&h);
+// 2^e as an f16 pair, e in [-24, 15].
+__device__ __forceinline__ __half2 pow2_f16x2(int e) {
+  const uint32_t h = e >= -14 ? (uint32_t)(e + 15) << 10 : 1u << (e + 24), hh = h | h << 16;
+  return *reinterpret_cast<const __half2*>(&hh);
 }
 
 // A bf16 pair as an f16 pair.
@@ -317,6 +322,31 @@ __device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
   }
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// The product of head `row`'s absorbed query (f16, as the tensor core has it) of token t with
+// the e2m1 cache row of request b's key, its rope part as the bf16 numbers that it holds, in 64
+// bits; `scale` multiplies it later.  -inf only where the row holds an infinity; NaN where fp32
+// does not hold the score.
+__device__ __forceinline__ float e2m1_score(const DecodeArgs& a, int b, int t, int row, int key, int row_bytes,
+                                            int rope_at, float scale) {
+  const int L = a.d.kv_lora_rank, R = a.d.qk_rope, ps = a.ks.page_size;
+  const int page = a.ks.block_table[(size_t)b * a.ks.bt_stride + key / ps];
+  const uint8_t* src = static_cast<const uint8_t*>(a.kv_pool) + ((size_t)page * ps + key % ps) * row_bytes;
+  const __half* q = reinterpret_cast<const __half*>(a.q_full) + ((size_t)t * kMaxHeads + row) * (L + R);
+  double s = 0.0;
+#pragma unroll 1
+  for (int l = 0; l < L; l += 2) {
+    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)src[l / 2], __NV_E2M1);
+    const float2 c = __half22float2(__half2(h));
+    const uint32_t e = src[L / 2 + l / 32];
+    const float sc = e == 255u ? CUDART_NAN_F : (e == 0u ? 0x1p-127f : __uint_as_float(e << 23));
+    s += (double)__half2float(q[l]) * (double)(c.x * sc) + (double)__half2float(q[l + 1]) * (double)(c.y * sc);
+  }
+#pragma unroll 1
+  for (int r = 0; r < R; ++r)
+    s += (double)__half2float(q[L + r]) * (double)__uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(src + rope_at)[r] << 16);
+  return fabs(s) < CUDART_INF && !(fabs(s) < 1e38 && fabs(s * (double)scale) < 1e38) ? CUDART_NAN_F : (float)s;
 }
 
 // Two floats rounded to a bf16 pair (low half = lo) in one conversion.
@@ -646,6 +676,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
     }
     mbar_init(&cs->bye, CL > 1 ? CL - 1 : 1);   // one arrival from every other CTA
     cs->abort = 0;
+    cs->over = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -1230,8 +1261,8 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
     // thread hh the hh-th part of them: groups of 32 codes (16 bytes) under one scale byte.  The
     // operands are f16: a code times 2^e is exact for e in [-23, 13], and the absorbed query and
     // P lose 2^-12 instead of 2^-9.  The scale goes into the lookup tables of e2m1x8_f16 where
-    // all products are normal numbers (|e| <= 13).  A magnitude that f16 does not reach becomes
-    // an infinity and is reported.  The last pass overwrites the rows, so before it the threads
+    // all products are normal numbers (|e| <= 13).  A latent value that f16 does not hold becomes
+    // NaN, a rope value an infinity (see the softmax), and both are reported.  The last pass overwrites the rows, so before it the threads
     // convert the rope part and wait until every one of them has read its codes.  (A warp of its
     // own for the rope part was the last to finish: 64 requests 185 us, 175 us so.)
     const int ci = tid - 32 * C::kConvWarp, crow = ci & 63, hh = ci >> 6;
@@ -1239,8 +1270,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
     constexpr int kGroups = C::RW / C::kConvPer / 32;   // groups per thread and pass
     static_assert(MODE != kLoadFp4 || kGroups <= 4, "scale bytes of a pass in a register");
     int c = 0;
-    bool out_of_range = false;
-    __half2 top = __float2half2_rn(0.f);   // largest rope magnitude so far, NaN aside
+    __half2 top = __float2half2_rn(0.f);   // largest magnitude so far of those that may pass f16, NaN aside
     for_each_segment(a, k, g0, g1, [&](int si, int t, const TokenPlan& tp, int ia, int ie, bool, int) {
       for (int it = ia; it < ie; ++it, ++c) {
         if (waborted(cs)) return;
@@ -1279,6 +1309,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
               *reinterpret_cast<uint4*>(st + C::NLB * C::kBox + crow * 128 + ((ch ^ (crow & 7)) << 4)) =
                   make_uint4(w[0], w[1], w[2], w[3]);
             }
+            if (any_inf(top)) *reinterpret_cast<volatile int*>(&cs->over) = 1;
             mbar_arrive(&cs->conv_sync);
             if (!wwait(&cs->conv_sync, c & 1, cs, hdr)) return;
           }
@@ -1297,12 +1328,15 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[i] = e2m1x8_f16(w[i], t0, t1);
               } else {
-                out_of_range |= e > 13 && e < 128;   // 6 * 2^14 is past f16
-                const __half2 sc = e8m0_f16x2((uint32_t)(e + 127));
+                // two factors, so that each is an f16 number and a code of zero stays zero
+                const int e1 = min(max(e, -14), 15), e2 = min(max(e - e1, -24), 15);
+                const __half2 s1 = e == 128 ? __float2half2_rn(CUDART_NAN_F) : pow2_f16x2(e1), s2 = pow2_f16x2(e2);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  o[i] = make_uint4(e2m1x2_scaled_f16x2(w[i] & 0xFFu, sc), e2m1x2_scaled_f16x2((w[i] >> 8) & 0xFFu, sc),
-                                    e2m1x2_scaled_f16x2((w[i] >> 16) & 0xFFu, sc), e2m1x2_scaled_f16x2(w[i] >> 24, sc));
+                  o[i] = make_uint4(e2m1x2_scaled_f16x2(w[i] & 0xFFu, s1, s2, top),
+                                    e2m1x2_scaled_f16x2((w[i] >> 8) & 0xFFu, s1, s2, top),
+                                    e2m1x2_scaled_f16x2((w[i] >> 16) & 0xFFu, s1, s2, top),
+                                    e2m1x2_scaled_f16x2(w[i] >> 24, s1, s2, top));
               }
             }
 #pragma unroll
@@ -1317,8 +1351,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         }
       }
     });
-    const float2 big = __half22float2(top);
-    if (out_of_range || isinf(big.x) || isinf(big.y)) atomicOr(&hdr->status, kDeviceCheckFailed);
+    if (any_inf(top)) atomicOr(&hdr->status, kDeviceCheckFailed);
   } else if (!C::kGrouped || warp >= 4) {
     // ------------------------------------------------------------- softmax
     if (C::kGrouped) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
@@ -1394,6 +1427,26 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         }
         if (!C::kEarly && !wwait(&cs->s_full[b], (c >> 1) & 1, cs, hdr)) return;
         tc_fence_after();
+        if constexpr (MODE == kLoadFp4) {
+          // A rope value past f16's range is an infinity in the product.  A score of +inf makes the
+          // row NaN.  One of -inf would drop its key, whatever the key's true score: it is computed
+          // anew from the cache row itself (rare, one key after the other).
+          if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&cs->over) != 0)) {
+#pragma unroll 1
+            for (int j = 0; j < 64; ++j) {
+              if (!((mask >> j) & 1ull)) continue;
+              uint32_t v;
+              tmem_ld1(trow + C::kSCol + 64 * b + j, v);
+              tmem_ld_wait();
+              const bool lost = row < H && __uint_as_float(v) * sl2 == -CUDART_INF_F;
+              if (!__any_sync(0xffffffffu, lost)) continue;
+              if (lost) v = __float_as_uint(e2m1_score(a, tp.b, t, row, (tp.tile_first + it) * kTileKeys + j, row4, C::kRow4, sl2));
+              __syncwarp();
+              tmem_st1(trow + C::kSCol + 64 * b + j, v);
+            }
+            tmem_st_wait();
+          }
+        }
         // S row (64 fp32) for this thread's head; both halves of the load in flight at once
         uint32_t sr[64];
         tmem_ld32(trow + C::kSCol + 64 * b, *reinterpret_cast<uint32_t(*)[32]>(sr));

@@ -86,11 +86,14 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint16_t two) {
          ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(f.y)) << 16);
 }
 
+// v as f16, NaN where f16 does not hold it: an infinite query value would make scores of -inf
+// that drop their keys quietly.
+__device__ __forceinline__ float f16_or_nan(float v) { return fabsf(v) < 65520.f ? v : CUDART_NAN_F; }
 // The bits of v rounded to f16, in the 16-bit type of the staging tile.
 __device__ __forceinline__ __nv_bfloat16 f16_in_bf16(float v) {
-  return __ushort_as_bfloat16(__half_as_ushort(__float2half_rn(v)));
+  return __ushort_as_bfloat16(__half_as_ushort(__float2half_rn(f16_or_nan(v))));
 }
-// Eight bf16 values as f16; finite ones that become infinite are reported.
+// Eight bf16 values as f16; finite ones that f16 does not hold are reported.
 __device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v, PlanHeader* hdr) {
   uint32_t w[4] = {v.x, v.y, v.z, v.w};
   bool over = false;
@@ -98,7 +101,7 @@ __device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v, PlanHeader* hdr) {
   for (int i = 0; i < 4; ++i) {
     const float x = __uint_as_float(w[i] << 16), y = __uint_as_float(w[i] & 0xFFFF0000u);
     over |= (fabsf(x) >= 65520.f && fabsf(x) < CUDART_INF_F) || (fabsf(y) >= 65520.f && fabsf(y) < CUDART_INF_F);
-    const __half2 h = __floats2half2_rn(x, y);
+    const __half2 h = __floats2half2_rn(f16_or_nan(x), f16_or_nan(y));
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   if (over) atomicOr(&hdr->status, kDeviceCheckFailed);

@@ -254,3 +254,102 @@ def test_nan_rows_stay_nan_over_split_keys(dev, make, num_splits):
         others = [h for h in range(p.H) if h != 1]
         assert torch.isfinite(clean[k][0].float()).all() and torch.isfinite(clean[k][1]).all(), k
         assert torch.equal(out[:, others], clean[k][0][:, others]) and torch.equal(lse[:, others], clean[k][1][:, others]), k
+
+
+def plain(p, rows, d):
+    """64-bit values of a call on these row bytes and device inputs."""
+    at = {int(r): i for i, r in enumerate(p.rows_phys)}
+    cached = []
+    for b, n in enumerate(p.cache_lens):
+        j = np.arange(int(n))
+        idx = [at[int(p.block_table[b, i // p.ps]) * p.ps + i % p.ps] for i in j]
+        cached.append(ref.decode(rows[idx], None, ref.E2M1, p.L, p.R))
+    v = lambda t: t.float().cpu().numpy().astype(np.float64)  # noqa: E731
+    return ref.attention(v(d["q"]), v(d["w_uk"]), v(d["w_uv"]), cached, [int(n) for n in p.cache_lens],
+                         d["offsets"].cpu().numpy(), p.scale, p.mask, p.window)
+
+
+def row_of(p, b, key):
+    return int(np.flatnonzero(p.rows_phys == int(p.block_table[b, key // p.ps]) * p.ps + key % p.ps)[0])
+
+
+@pytest.mark.parametrize("num_splits", [1, 6])
+@pytest.mark.parametrize("make", [wide, narrow])
+def test_a_rope_value_past_f16_drops_no_key(dev, make, num_splits):
+    # a head whose score the value lowers gives what the value itself gives (65536 and 2^100; with a
+    # large query the key falls out, with a small one it counts, with one visible key it is all
+    # there is), the others NaN, in the output and in the log-sum-exp; requests around it are whole
+    p = make(45, (1, 500, 130, 700, 64), qlens=(1, 2, 1, 1, 1), H=6)
+    p, rows = coded(p)
+    d = device_inputs(p, dev)
+    big = {0: 0, 1: 77, 3: 698}                     # request: key with a value past f16
+    for b, key in big.items():
+        rows[row_of(p, b, key), -2 * p.R:][:2] = np.array([0x7180 if b == 3 else 0x4780], np.uint16).view(np.uint8)
+    q = d["q"][..., p.N].float()
+    q[:, 0::3] = -q[:, 0::3].abs()
+    q[:, 1::3] = q[:, 1::3].abs() + 2.0 ** -6
+    q[:, 2::3] = -(2.0 ** -20)
+    d["q"][..., p.N] = q.to(torch.bfloat16)
+    want, want_lse = plain(p, rows, d)
+    out, lse = run_fp4(p, rows, d, debug=False, num_splits=num_splits)
+    g, gl = out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    request = np.repeat(np.arange(5), (1, 2, 1, 1, 1))
+    hit = np.isin(request, list(big))
+    raised = np.arange(p.H) % 3 == 1
+    for t in range(p.T):
+        nan = raised & hit[t]
+        assert np.array_equal(np.isnan(g[t]).all(1), nan) and np.array_equal(np.isnan(gl[t]), nan)
+        assert np.isfinite(g[t][~nan]).all()
+        err = np.linalg.norm(g[t][~nan] - want[t][~nan]) / np.linalg.norm(want[t][~nan])
+        assert err <= TOL, (t, err)
+        # scores of 2^16 |q| scale are compared relative to their size
+        diff = np.abs(gl[t][~nan] - want_lse[t][~nan])
+        assert (diff <= TOL_LSE + 2.0 ** -10 * np.abs(want_lse[t][~nan])).all(), t
+
+
+@pytest.mark.parametrize("make", [wide, narrow])
+def test_scales_at_the_ends_of_f16(dev, make):
+    # zeros under any scale are zeros; 0.5 .. 3 times 2^14, 0.5 .. 1.5 times 2^15 and 0.5 times 2^16
+    # are numbers that f16 holds; 1 times 2^16 and the scale 255 are NaN
+    import mla_decode_attention_06_gb300 as M
+    p, rows = coded(make(46, (90, 70), H=6))
+    p = dataclasses.replace(p, scale=2.0 ** -26)
+    hit = row_of(p, 0, 3)
+    g = p.L // 2
+    rows[hit, :32], rows[hit, g], rows[hit, g + 1] = 0, 0xFE, 141
+    rows[hit, 16:20] = [0x52, 0xA1, 0x35, 0x14]      # 1 3 | .5 -1 | 3 1.5 | 2 .5 times 2^14
+    d = device_inputs(p, dev)
+    want, want_lse = plain(p, rows, d)
+    out, lse = run_fp4(p, rows, d)
+    o = out.float().cpu().numpy()
+    assert np.linalg.norm(o - want) <= TOL * np.linalg.norm(want)
+    assert np.abs(lse.cpu().numpy() - want_lse).max() <= TOL_LSE
+    for byte, code in ((142, 0x31), (143, 0x10)):     # 0.5 1.5 | 0 0.5
+        rows[hit, 16:32], rows[hit, g + 1] = code, byte
+        want, _ = plain(p, rows, d)
+        o = run_fp4(p, rows, d)[0].float().cpu().numpy()
+        assert np.linalg.norm(o - want) <= TOL * np.linalg.norm(want)
+    rows[hit, 16] = 0x02
+    with pytest.raises(M.MlaError) as e:
+        run_fp4(p, rows, d)
+    assert e.value.code == 5
+    out, lse = run_fp4(p, rows, d, debug=False)
+    assert torch.isnan(out[0].float()).all() and torch.isnan(lse[0]).all() and torch.isfinite(out[1].float()).all()
+
+
+def test_queries_past_f16_are_nan_whatever_the_scores(dev):
+    # a query value past f16, in tokens with one visible key and over split keys: NaN, not 0 and -inf
+    import mla_decode_attention_06_gb300 as M
+    for sign in (1.0, -1.0):
+        p, rows = coded(wide(47, (1, 600, 64)))
+        d = device_inputs(p, dev)
+        d["q"][:, 3, p.N + 5] = sign * 65536.0
+        d["w_uk"][7] = sign * 2.0 ** 22
+        with pytest.raises(M.MlaError) as e:
+            run_fp4(p, rows, d, num_splits=4)
+        assert e.value.code == 5
+        out, lse = run_fp4(p, rows, d, debug=False, num_splits=4)
+        bad = [3, 7]
+        rest = [h for h in range(p.H) if h not in bad]
+        assert torch.isnan(out[:, bad].float()).all() and torch.isnan(lse[:, bad]).all()
+        assert torch.isfinite(out[:, rest].float()).all() and torch.isfinite(lse[:, rest]).all()
