@@ -67,6 +67,19 @@ def _opts(mask, window, scale, num_splits, debug, timing=False, fold_pairs=None)
                    num_splits=int(num_splits), flags=flags)
 
 
+def _buffer(shape, dtype, device, stream, returned=False):
+    """A buffer of one call.  It comes from the memory of the stream that the call runs on: what
+    another stream has given back may still be in use there.  One that is returned is not given to
+    that stream again before the current stream is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def mla_decode_workspace_size(dims: MlaDims, opts: MlaOpts, batch: int, total_q: int) -> int:
     n = ctypes.c_size_t(0)
     rc = _lib.load().mla_decode_workspace_size(ctypes.byref(dims), ctypes.byref(opts), batch,
@@ -77,7 +90,7 @@ def mla_decode_workspace_size(dims: MlaDims, opts: MlaOpts, batch: int, total_q:
 
 
 def _prepare(q, w_uk, w_uv, page_size, pool_bytes, row_bytes_fn, out, lse_out, workspace, opts,
-             batch):
+             batch, stream):
     T, H, NR = q.shape
     Hk, L, N = w_uk.shape
     Hv, V, Lv = w_uv.shape
@@ -91,10 +104,10 @@ def _prepare(q, w_uk, w_uv, page_size, pool_bytes, row_bytes_fn, out, lse_out, w
                    page_size=page_size, num_pages=pool_bytes // (page_size * row_bytes))
     dev = q.device
     if out is None:
-        out = torch.empty((T, H, V), dtype=torch.bfloat16, device=dev)
+        out = _buffer((T, H, V), torch.bfloat16, dev, stream, returned=True)
     need = mla_decode_workspace_size(dims, opts, batch, T)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        workspace = _buffer(max(need, 256), torch.uint8, dev, stream)
     return dims, out, workspace
 
 
@@ -119,7 +132,7 @@ def mla_decode_paged(q, input_row_offsets, kv_pool, block_table, cache_lens, w_u
     opts = _opts(mask, window, scale, num_splits, debug, timing, fold_pairs)
     dims, out, workspace = _prepare(q, w_uk, w_uv, page_size,
                                     kv_pool.numel() * kv_pool.element_size(),
-                                    lambda L, R: 2 * (L + R), out, lse_out, workspace, opts, B)
+                                    lambda L, R: 2 * (L + R), out, lse_out, workspace, opts, B, stream)
     i32 = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32,)
     rc = _lib.load().mla_decode_paged(
         ctypes.byref(dims), ctypes.byref(opts), _ptr(q, "q", (torch.bfloat16,), dev),
@@ -150,7 +163,7 @@ def mla_decode_paged_fp8(q, input_row_offsets, kv_pool_fp8, kv_scales, block_tab
     opts = _opts(mask, window, scale, num_splits, debug, timing, fold_pairs)
     dims, out, workspace = _prepare(q, w_uk_fp8, w_uv_fp8, page_size,
                                     kv_pool_fp8.numel() * kv_pool_fp8.element_size(),
-                                    lambda L, R: L + 2 * R, out, lse_out, workspace, opts, B)
+                                    lambda L, R: L + 2 * R, out, lse_out, workspace, opts, B, stream)
     i32 = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32,)
     f8 = (torch.uint8, torch.float8_e4m3fn)
     rc = _lib.load().mla_decode_paged_fp8(
@@ -174,25 +187,19 @@ _I32 = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32
 _BF16 = (torch.bfloat16,)
 
 
-def _buffer(shape, dtype, device, stream):
-    """A buffer for one call: one that runs on a stream of its own keeps it until that
-    stream is done with it."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 _status = {}
 
 
-def _unread_status(device):
-    """The status word of calls that nobody reads it of: kernels only set bits in it."""
-    t = _status.get(device)
+def _unread_status(device, stream):
+    """The status word of a stream's calls that nobody reads it of: kernels only set bits in it."""
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    key = (device, s.cuda_stream)
+    t = _status.get(key)
     if t is None:
-        if torch.cuda.is_current_stream_capturing():
-            return _buffer(256, torch.uint8, device, None)   # the graph's own memory, not kept
-        t = _status[device] = torch.zeros(256, dtype=torch.uint8, device=device)
+        with torch.cuda.stream(s):
+            if torch.cuda.is_current_stream_capturing():
+                return torch.empty(256, dtype=torch.uint8, device=device)   # the graph's own memory, not kept
+            t = _status[key] = torch.zeros(256, dtype=torch.uint8, device=device)
     return t
 
 
@@ -272,7 +279,7 @@ def mla_cache_append(kv_new, input_row_offsets, kv_pool, block_table, cache_lens
         raise ValueError("kv_scales must hold one value per cache row")
     B, offsets, table, table_stride, lens = _tables(input_row_offsets, block_table, cache_lens, dev)
     if workspace is None:
-        workspace = _buffer(256, torch.uint8, dev, stream) if debug else _unread_status(dev)
+        workspace = _buffer(256, torch.uint8, dev, stream) if debug else _unread_status(dev, stream)
     _call("mla_cache_append", dev, ctypes.byref(dims), int(cache_format), kv_new.data_ptr(), new_stride, offsets,
           B, T, _ptr(q, "q", _BF16, dev), _ptr(q_out, "q_out", _BF16, dev), _ptr(kv_pool, "kv_pool", None, dev),
           _ptr(kv_scales, "kv_scales", (torch.float32,), dev), _ptr(rows_out, "rows_out", _BF16, dev), table,
@@ -300,7 +307,7 @@ def mla_decode_paged_fp4(q, input_row_offsets, kv_pool_fp4, block_table, cache_l
     dims = MlaDims(num_heads=H, qk_nope=N, qk_rope=NR - N, kv_lora_rank=L, v_head=V, page_size=page_size,
                    num_pages=_pages(kv_pool_fp4, page_size, mla_cache_row_bytes(MLA_CACHE_E2M1, L, NR - N)))
     if out is None:
-        out = _buffer((T, H, V), torch.bfloat16, dev, stream)
+        out = _buffer((T, H, V), torch.bfloat16, dev, stream, returned=True)
     elif tuple(out.shape) != (T, H, V):
         raise ValueError("out must be [T, H, V]")
     if lse_out is not None and lse_out.numel() != T * H:
@@ -344,7 +351,7 @@ def _prefill(name, cache_format, q, input_row_offsets, cache, block_table, cache
     if len(cache) > 1 and cache[1].numel() != dims.num_pages * page_size:
         raise ValueError("kv_scales must hold one value per cache row")
     if out is None:
-        out = _buffer((T, H, V), torch.bfloat16, dev, stream)
+        out = _buffer((T, H, V), torch.bfloat16, dev, stream, returned=True)
     elif tuple(out.shape) != (T, H, V):
         raise ValueError("out must be [T, H, V]")
     if lse_out is not None and lse_out.numel() != T * H:
@@ -423,7 +430,7 @@ def mla_decode_sparse(q, input_row_offsets, kv_pool, d_indices, topk_lengths, w_
     opts = _opts(MLA_MASK_NULL, 0, scale, num_splits, debug, timing, fold_pairs)
     dims, out, workspace = _prepare(q, w_uk, w_uv, page_size,
                                     kv_pool.numel() * kv_pool.element_size(),
-                                    lambda L, R: 2 * (L + R), out, lse_out, workspace, opts, B)
+                                    lambda L, R: 2 * (L + R), out, lse_out, workspace, opts, B, stream)
     i32 = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32,)
     rc = _lib.load().mla_decode_sparse(
         ctypes.byref(dims), ctypes.byref(opts), _ptr(q, "q", (torch.bfloat16,), dev),
@@ -457,7 +464,7 @@ def mla_branch_prologue(q, input_row_offsets, kv_pool, block_table, cache_lens, 
     dims = MlaDims(num_heads=H, qk_nope=NR - R, qk_rope=R, kv_lora_rank=L, v_head=1,
                    page_size=page_size, num_pages=pool_bytes // (page_size * row_bytes))
     if workspace is None:
-        workspace = torch.empty(256, dtype=torch.uint8, device=dev)
+        workspace = _buffer(256, torch.uint8, dev, stream)
     i32 = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32,)
     rc = _lib.load().mla_branch_prologue(
         ctypes.byref(dims), _ptr(q, "q", (torch.bfloat16,), dev),
@@ -494,10 +501,10 @@ def mla_indexer_fp8(q, q_s, input_row_offsets, k_cache, k_scales, block_table, c
     if rc:
         raise MlaError("mla_indexer_workspace_size", rc)
     if workspace is None:
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        workspace = _buffer(need.value, torch.uint8, dev, stream)
     if out is None:
-        out = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    scores = torch.empty((T, top_k), dtype=torch.float64, device=dev) if with_scores else None
+        out = _buffer((T, top_k), torch.int32, dev, stream, returned=True)
+    scores = _buffer((T, top_k), torch.float64, dev, stream, returned=True) if with_scores else None
     i32 = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32,)
     f8 = (torch.uint8, torch.float8_e4m3fn)
     rc = lib.mla_indexer_fp8(

@@ -215,3 +215,57 @@ def test_calls_side_by_side(dev):
     torch.cuda.synchronize()
     for x, y in got:
         assert torch.equal(x, want[0]) and torch.equal(y, want[1])
+
+
+@pytest.mark.parametrize("op", ["prefill", "decode e2m1", "decode bf16", "decode sparse", "indexer"])
+def test_a_stream_of_its_own_leaves_freed_memory_alone(dev, op):
+    # memory that the current stream has given back but still reads, of the sizes that the call
+    # asks for: a call on another stream must not write there
+    import mla_decode_attention_06_gb300 as M
+    r = np.random.default_rng(50)
+    T, rows = 24, 24 * 128
+    t = lambda a, d=torch.int32: torch.from_numpy(np.ascontiguousarray(a)).to(dev, d)  # noqa: E731
+    offsets, table, lens = t(np.arange(T + 1)), t(np.arange(2 * T).reshape(T, 2)), t(np.full(T, 100))
+    rand = lambda *shape: t(r.standard_normal(shape), torch.bfloat16)  # noqa: E731
+    q, uk, uv = rand(T, H, N + R), rand(H, L, N) / N ** 0.5, rand(H, V, L) / L ** 0.5
+    pool = rand(rows, L + R)
+    dims = M.MlaDims(num_heads=H, qk_nope=N, qk_rope=R, kv_lora_rank=L, v_head=V, page_size=PS, num_pages=2 * T)
+    opts = M.MlaOpts(mask=1, window=0, scale=0.07, num_splits=0, flags=0)
+    size = M.mla_decode_workspace_size(dims, opts, T, T)
+    kw = dict(page_size=PS, scale=0.07)
+    if op == "prefill":
+        size = M.mla_prefill_workspace_size(dims, opts, 0, T, T, 100 * T)
+        call = lambda **k: M.mla_prefill_paged(q, offsets, pool, table, lens, uk, uv, total_keys=100 * T, **kw, **k)[0]  # noqa: E731
+    elif op == "decode e2m1":
+        pool4 = t(r.integers(0, 120, (rows, 400)), torch.uint8)
+        call = lambda **k: M.mla_decode_paged_fp4(q, offsets, pool4, table, lens, uk, uv, **kw, **k)[0]  # noqa: E731
+        pool4[:, 256:272] = 127
+        pool4[:, 272:] = pool.view(torch.uint8)[:, 2 * L:]
+    elif op == "decode bf16":
+        call = lambda **k: M.mla_decode_paged(q, offsets, pool, table, lens, uk, uv, **kw, **k)[0]  # noqa: E731
+    elif op == "decode sparse":
+        rows_of = t(r.integers(0, rows, (T, 64)))
+        call = lambda **k: M.mla_decode_sparse(q, offsets, pool, rows_of, None, uk, uv, **kw, **k)[0]  # noqa: E731
+    else:
+        codes = [t(r.integers(0, 120, s), torch.uint8) for s in ((T, 4, 64), (rows, 64))]
+        ones = [torch.ones(T, 4, device=dev), torch.ones(rows, device=dev)]
+        size = 0
+        call = lambda **k: M.mla_indexer_fp8(codes[0], ones[0], offsets, codes[1], ones[1], table, lens, page_size=PS,  # noqa: E731
+                                             top_k=32, **k)[0]
+    want = call().clone()
+    s = torch.cuda.Stream()
+    call(stream=s)                       # one-time set-up of the call
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = [torch.full_like(want, 3), torch.full((max(size, 1),), 7, dtype=torch.uint8, device=dev)]
+    seen = [torch.empty_like(x) for x in held]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)       # about 0.2 s
+    for a, b in zip(seen, held):
+        a.copy_(b)
+    del a, b, held
+    got = call(stream=s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert (seen[0] == 3).all() and (seen[1] == 7).all()
