@@ -20,10 +20,10 @@
 // small or exact term, and it is rounded to odd: of its value rounded down and rounded up
 // the one whose last bit is set (the two are equal if it is exact).  Rounding that to
 // bf16 rounds the exact value, since no odd fp32 number lies on a bf16 boundary.  The
-// same goes for the rotations.  (With TwoSum and a rounding of the pair in integers, four
+// same goes for the rotations, where the one product that is rounded on its own is exact.  (With TwoSum and a rounding of the pair in integers, four
 // times the operations, 8,483 prompt tokens took 262 us, twice the time of their bytes.)
 // Rows and products outside the range in which these steps neither overflow nor
-// underflow take fp64 throughout.  Results equal mla_branch_prologue's bit for bit (bf16
+// underflow take fp64 (a rotation's sum there is rounded to odd from an exact pair).  Results equal mla_branch_prologue's bit for bit (bf16
 // rows, queries; a NaN is a NaN).
 //
 // Layout.  A warp takes a row (16 consecutive values a lane: two lanes hold one group
@@ -93,11 +93,18 @@ __device__ __forceinline__ float double_odd(double x) {
   return isfinite(f) && (double)f != x ? __uint_as_float(__float_as_uint(f) | 1u) : f;
 }
 
+// `turn` for products that fp32 does not hold.
+__device__ __noinline__ uint32_t turn_wide(uint32_t x, uint32_t f) {
+  const double x0 = lo_f(x), x1 = hi_f(x), c = lo_f(f), s = hi_f(f);
+  return pack(double_odd(add_odd(x0 * c, -(x1 * s))), double_odd(add_odd(x0 * s, x1 * c)));
+}
 // The pair (x0, x1) of `x` turned by (cos, sin) of `f`, as a bf16 pair (products of bf16 values
-// are exact in fp32).
+// are exact in fp32's normal range).
 __device__ __forceinline__ uint32_t turn(uint32_t x, uint32_t f) {
   const float x0 = lo_f(x), x1 = hi_f(x), c = lo_f(f), s = hi_f(f);
-  return pack(fma_odd(x0, c, -__fmul_rn(x1, s)), fma_odd(x0, s, __fmul_rn(x1, c)));
+  const float p = __fmul_rn(x1, s), r = __fmul_rn(x1, c);
+  if (product_lost(p, x1, s) || product_lost(r, x1, c)) return turn_wide(x, f);
+  return pack(fma_odd(x0, c, -p), fma_odd(x0, s, r));
 }
 
 struct Place {

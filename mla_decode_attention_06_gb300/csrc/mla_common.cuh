@@ -95,6 +95,22 @@ __device__ __forceinline__ float bf16_to_f32(uint16_t b) {
   return __uint_as_float(((uint32_t)b) << 16);
 }
 
+// a + b rounded to odd in 53 bits: the exact sum, or of the two doubles around it the one whose
+// last bit is set.  Rounded again to fewer bits it gives the rounding of the exact sum.
+__device__ __forceinline__ double add_odd(double a, double b) {
+  const double hi = __dadd_rn(a, b), z = __dsub_rn(hi, a);
+  const double lo = __dadd_rn(__dsub_rn(a, __dsub_rn(hi, z)), __dsub_rn(b, z));   // Knuth's TwoSum
+  const long long u = __double_as_longlong(hi);
+  if (!isfinite(hi) || lo == 0.0 || (u & 1)) return hi;
+  return __longlong_as_double((lo > 0.0) == (hi > 0.0) ? u + 1 : u - 1);
+}
+// Is the fp32 product p of two bf16 values other than their exact product?  (It has 16 bits, so
+// only past the ends of fp32's normal range.)
+__device__ __forceinline__ bool product_lost(float p, float x, float y) {
+  const float m = fabsf(p);
+  return !(m >= 0x1p-126f && m < INFINITY) && x != 0.f && y != 0.f;
+}
+
 // OCP E4M3FN code -> float through the hardware fp8 -> half conversion (exact).
 __device__ __forceinline__ float e4m3_to_f32(uint8_t code) {
   __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3);

@@ -13,7 +13,8 @@
 // Every result is the bf16 (nearest, ties to even) of the expression's value:
 //   - rotations: the two products of bf16 values are exact in fp32 and their
 //     difference / sum is formed exactly as an fp32 pair (TwoSum), which is
-//     rounded to bf16 once, looking at the low part only at a halfway point; the
+//     rounded to bf16 once, looking at the low part only at a halfway point (products
+//     past fp32's normal range: the same in double precision); the
 //     result is the exactly rounded value of x0 c - x1 s (x0 s + x1 c), as a
 //     double-precision evaluation gives it;
 //   - RMSNorm: the mean square, 1 / sqrt(mean + eps) and the two products are
@@ -122,9 +123,15 @@ __device__ __forceinline__ void bf2(uint32_t v, float& lo, float& hi) {
 // (x0, x1) turned by (c, s), as bf16 bits: the products of bf16 values are
 // exact in fp32.
 __device__ __forceinline__ void rotate(float x0, float x1, float c, float s, uint16_t& y0, uint16_t& y1) {
+  const float p0 = __fmul_rn(x0, c), p1 = __fmul_rn(x1, s), p2 = __fmul_rn(x0, s), p3 = __fmul_rn(x1, c);
+  if (product_lost(p0, x0, c) || product_lost(p1, x1, s) || product_lost(p2, x0, s) || product_lost(p3, x1, c)) {
+    y0 = round_bf16(add_odd((double)x0 * c, -((double)x1 * s)));
+    y1 = round_bf16(add_odd((double)x0 * s, (double)x1 * c));
+    return;
+  }
   float h0, l0, h1, l1;
-  two_sum(__fmul_rn(x0, c), -__fmul_rn(x1, s), h0, l0);
-  two_sum(__fmul_rn(x0, s), __fmul_rn(x1, c), h1, l1);
+  two_sum(p0, -p1, h0, l0);
+  two_sum(p2, p3, h1, l1);
   y0 = round_bf16_pair(h0, l0);
   y1 = round_bf16_pair(h1, l1);
 }

@@ -6,6 +6,8 @@ rounded once to bf16, codes of the bf16 value over a power of two), so there is 
 pools, row scales, turned queries and returned rows are compared bitwise, rows that no token
 owns included.
 """
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -293,3 +295,59 @@ def test_captured_and_replayed(dev):
     pool, _, q_ref, _ = c.expected()
     assert np.array_equal(a["kv_pool"].cpu().numpy(), pool)
     assert np.array_equal(bits(a["q_out"]), q_ref)
+
+
+def exact_bf16(v):
+    """A Fraction's bf16 bits (nearest, ties to even); the sign of a zero is not asked."""
+    a = abs(v)
+    if a == 0:
+        return 0
+    e = max(a.numerator.bit_length() - a.denominator.bit_length(), -126)
+    while Fraction(2) ** e > a and e > -126:
+        e -= 1
+    n = round(a / Fraction(2) ** (e - 7))
+    mag = min((e + 1 + 127 << 7) if n >= 256 else ((e + 127 << 7) + n - 128 if n >= 128 else n), 0x7F80)
+    return mag | (0x8000 if v < 0 else 0)
+
+
+def test_rotations_past_the_normal_range(dev):
+    # products below 2^-126 and past 2^128, sums of either size: each result is the exact value
+    # rounded once, in the append and in the prologue
+    import mla_decode_attention_06_gb300 as M
+    r = np.random.default_rng(51)
+    c = Case(ref.BF16, 14, **NARROW, H=16, qlens=(12,), past=(0,))
+    wild = lambda shape, lo, hi: ref.bf16_bits(r.choice([-1, 1], shape) * (1 + r.integers(0, 128, shape) / 128) *  # noqa: E731
+                                               np.exp2(r.integers(lo, hi, shape)))
+    c.q[..., c.N:] = wild(c.q[..., c.N:].shape, -133, 128)
+    c.new[:, c.L:] = wild(c.new[:, c.L:].shape, -133, 128)
+    c.freqs = wild(c.freqs.shape, -60, 2)
+    # halfway between two bf16 values but for a product of 2^-150
+    tie = ref.bf16_bits(np.array([1.5 * 2.0 ** -100, 2.0 ** -130]))
+    c.q[0, :, c.N:c.N + 2] = c.new[0, c.L:c.L + 2] = tie
+    c.freqs[0, :2] = ref.bf16_bits(np.array([1 + 2.0 ** -7, 2.0 ** -20]))
+    c.q[1, :, c.N:c.N + 2] = c.new[1, c.L:c.L + 2] = tie
+    c.freqs[1, :2] = ref.bf16_bits(np.array([1 + 2.0 ** -7, -2.0 ** -20]))
+
+    def turned(x, pos):
+        v = np.vectorize(lambda b: Fraction(float(ref.bf16_values(b))), otypes=[object])
+        x, f = v(x), v(c.freqs[pos])
+        out = np.empty(x.shape, np.uint16)
+        for i in range(0, x.shape[-1], 2):
+            x0, x1, cos, sin = x[..., i], x[..., i + 1], f[i], f[i + 1]
+            out[..., i] = np.vectorize(exact_bf16, otypes=[np.uint16])(x0 * cos - x1 * sin)
+            out[..., i + 1] = np.vectorize(exact_bf16, otypes=[np.uint16])(x0 * sin + x1 * cos)
+        return out
+
+    _, q, rows = run(c, dev)
+    b = c.args(dev)
+    pool = b["kv_pool"].clone()
+    at = torch.from_numpy(c.row).to(dev)
+    pool[at] = b["kv_new"].view(torch.uint8).view(c.T, -1)
+    M.mla_branch_prologue(b["q"], b["input_row_offsets"], pool, b["block_table"], b["cache_lens"], b["freqs_cis"],
+                          b["kv_norm_gamma"], page_size=c.ps, kv_lora_rank=c.L, epsilon=c.eps)
+    pro_rows = pool[at].cpu().numpy().view(np.uint16)
+    no_sign = lambda x: np.where(x & 0x7FFF, x, 0)  # noqa: E731
+    for t in range(c.T):
+        want_q, want_r = turned(c.q[t, :, c.N:], t), turned(c.new[t, c.L:], t)
+        for got_q, got_r in ((bits(q)[t, :, c.N:], bits(rows)[t, c.L:]), (bits(b["q"])[t, :, c.N:], pro_rows[t, c.L:])):
+            assert np.array_equal(no_sign(got_q), no_sign(want_q)) and np.array_equal(no_sign(got_r), no_sign(want_r)), t
