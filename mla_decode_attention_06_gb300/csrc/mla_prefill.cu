@@ -29,10 +29,14 @@
 // Precision.  K, V and P are rounded once each; as bf16 (2^-9) the score's share of that,
 // amplified by the softmax, would be most of the error.  They are kept as f16 (2^-12, the
 // same tensor rate), which holds what such values are in practice but not what they could
-// be: the kernels that write them check every 32 x 64 patch (every row, for rope and e4m3
-// latents) for magnitudes above 2^15 and for patches with no magnitude above 2^-8, and
-// raise a flag.  A second sequence of the same kernels with bf16 throughout follows in
-// the stream and returns at once unless the flag is up.  Queries are converted by the
+// be: the kernels that write them check the largest magnitude of every row (64 columns of a K
+// or V row, a rope row, an e4m3 latent row, 256 neighbouring e4m3 weights) and raise a flag
+// where it is above 2^15 or, not being zero, below 2^-15.  At 2^-15 f16's step is 2^-24, so
+// each value is off by at most 2^-10 of its row's largest, half of what bf16 may be off by:
+// a row small beside its neighbours loses nothing that the second sequence would keep, and
+// heads or weights some thousand times smaller than usual stay in the first.  A second
+// sequence of the same kernels with bf16 throughout follows in the stream and returns at once
+// unless the flag is up.  Queries are converted by the
 // CTA that uses them, each row scaled by its own power of two; e4m3 latents and weights
 // become f16 before the expansion, bf16 and e2m1 ones enter it as the bf16 values they are.
 // Measured on uniform random cases: 1.7e-3 relative to 64 bits with f16, most of it the
@@ -106,11 +110,15 @@ __device__ __forceinline__ bool runs(const Args& a) {
   __syncthreads();
   return go != 0;
 }
-// Whole warp: is the largest of the lanes' magnitudes (fp32 bits) one that f16 holds well:
-// zero, or within [2^-8, 2^15]?  The others then are off by at most 2^-17 of it.
+// Is a row's largest magnitude (fp32 bits) one that f16 holds well: zero, or within
+// [2^-15, 2^15]?  Half a step of f16 then is at most 2^-10 of it.
+__device__ __forceinline__ bool f16_holds_row(uint32_t top) {
+  return top == 0u || (top >= 0x38000000u && top <= 0x47000000u);
+}
+// The same for a row that a whole warp holds, `top` the largest of a lane's values.
 __device__ __forceinline__ bool f16_holds(uint32_t top) {
   const bool over = __any_sync(0xffffffffu, top > 0x47000000u), some = __any_sync(0xffffffffu, top != 0u);
-  return !over && (__any_sync(0xffffffffu, top >= 0x3B800000u) || !some);
+  return !over && (__any_sync(0xffffffffu, top >= 0x38000000u) || !some);
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -637,7 +645,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
           }
           *reinterpret_cast<uint4*>(box + ((ch ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        if (!f16_holds(top)) wide = true;
+        wide |= !f16_holds_row(top);
         fence_proxy_async_smem();
         all_of_128(3, true);
         if (first) {
@@ -646,7 +654,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
         }
       }
     }
-    if (a.half && wide && lane == 0) atomicOr(&hdr->pad[3], 1);
+    if (a.half && __any_sync(0xffffffffu, wide) && lane == 0) atomicOr(&hdr->pad[3], 1);
     if (first) bulk_wait_all();
   }
   tc_fence_before();

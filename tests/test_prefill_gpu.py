@@ -408,3 +408,50 @@ def test_blocks_that_start_late_beside_others_that_raise_the_flag(dev):
                 torch.mm(x, x)
         out, _ = call(c, dev, args)
         assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("small", [2.0 ** -13, 2.0 ** -22])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_small_rows_beside_large_ones(dev, fmt, small):
+    # cached rows far smaller than their neighbours: a query that sees nothing else keeps its
+    # relative precision (that of the bf16 sequence at least), token by token
+    c = Case(fmt, 23, **WIDE, qlens=(150, 3), past=(0, 40))
+    for b, keys in ((0, range(5)), (1, range(3, 31))):
+        row = c.rows[b][list(keys)]
+        if fmt == "bf16":
+            v = ref.bf16_values(np.ascontiguousarray(c.pool[row, :2 * c.L]).view(np.uint16)) * small
+            c.pool[row, :2 * c.L] = ref.bf16_bits(v).view(np.uint8)
+        elif fmt == "e4m3":
+            c.scales[row] *= np.float32(small)
+        else:
+            c.pool[row, c.L // 2:c.L // 2 + c.L // 32] -= np.uint8(-np.log2(small))
+    out, lse = call(c, dev)
+    want, want_lse = c.expected()
+    g = out.float().cpu().numpy().astype(np.float64)
+    kind = "bf16 e4m3" if fmt == "e4m3" else "bf16"
+    for t in range(c.T):
+        assert np.linalg.norm(g[t] - want[t]) <= TOL[kind] * np.linalg.norm(want[t]), t
+    assert np.abs(lse.cpu().numpy() - want_lse).max() <= TOL_LSE[kind]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_weak_head_changes_no_other(dev, fmt):
+    # one head's weights 2048 times smaller: the other heads' bits stay, its own values keep the
+    # precision of the bf16 sequence at least
+    kw = dict(**WIDE, H=3, qlens=(140, 9), past=(3, 150))
+    want, want_lse = check(Case(fmt, 24, **kw), dev)
+    c = Case(fmt, 24, **kw)
+    for i, name in enumerate(("uk", "uv")):
+        if fmt == "e4m3":
+            c.w[i][1][1] *= np.float32(2.0 ** -11)
+        else:
+            c.w[i][1] = ref.bf16_bits(ref.bf16_values(c.w[i][1]) * 2.0 ** -11)
+        getattr(c, name)[1] *= 2.0 ** -11
+    out, lse = call(c, dev)
+    for h in (0, 2):
+        assert torch.equal(out[:, h], want[:, h]) and torch.equal(lse[:, h], want_lse[:, h])
+    ref_out, ref_lse = c.expected()
+    kind = "bf16 e4m3" if fmt == "e4m3" else "bf16"
+    g = out[:, 1].float().cpu().numpy()
+    assert np.linalg.norm(g - ref_out[:, 1]) <= TOL[kind] * np.linalg.norm(ref_out[:, 1])
+    assert np.abs(lse[:, 1].cpu().numpy() - ref_lse[:, 1]).max() <= TOL_LSE[kind]
