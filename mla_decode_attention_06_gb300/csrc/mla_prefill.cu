@@ -1376,7 +1376,7 @@ cudaError_t launch_prefill(const PrefillCall& c, const PrefillLayout& lay, int h
   a.B = c.B;
   a.T = c.T;
   a.mask = c.mask;
-  a.window = c.window;
+  a.window = std::min(c.window, 1 << 30);   // more than a call can hold keys; positions less a window stay in 32 bits
   a.scale = c.scale;
   a.bt_stride = c.bt_stride;
   a.cap_tiles = (int)lay.cap_tiles;

@@ -455,3 +455,12 @@ def test_a_weak_head_changes_no_other(dev, fmt):
     g = out[:, 1].float().cpu().numpy()
     assert np.linalg.norm(g - ref_out[:, 1]) <= TOL[kind] * np.linalg.norm(ref_out[:, 1])
     assert np.abs(lse[:, 1].cpu().numpy() - ref_lse[:, 1]).max() <= TOL_LSE[kind]
+
+
+def test_widest_window(dev):
+    # the largest window there is is no window, for query tokens before the first cached key too
+    for past in ((40, 5), (-3, -100)):
+        c = Case("bf16", 25, **NARROW, qlens=(20, 150), past=past, mask=2, window=2 ** 31 - 1)
+        out, lse = call(c, dev, debug=past[0] >= 0)
+        c.lens = c.lens.astype(np.int64)
+        compare(c, out, lse, "f16")
