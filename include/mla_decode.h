@@ -278,7 +278,8 @@ int mla_branch_prologue(const mla_dims_t* dims, void* q, const uint32_t* input_r
  * A token whose position is outside [0, max_seq_len) or the block table, or whose page
  * id is outside [0, num_pages), is skipped whole (its row, q_out and rows_out keep
  * what they held) and recorded: MLA_ERR_DEVICE_CHECK in debug mode.  Two tokens that
- * the block table sends to one row leave either's. */
+ * the block table sends to one row may leave parts of both in it (the same row, if they
+ * bring the same values). */
 int mla_cache_append(const mla_dims_t* dims, int32_t cache_format, const void* kv_new, int64_t kv_new_stride,
                      const uint32_t* input_row_offsets, int32_t batch, int32_t total_q, const void* q, void* q_out,
                      void* kv_pool, float* kv_scales, void* rows_out, const int32_t* block_table,

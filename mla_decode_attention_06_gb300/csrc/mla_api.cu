@@ -464,6 +464,7 @@ int mla_cache_append(const mla_dims_t* dims, int32_t cache_format, const void* k
   if (q && ((int64_t)dims->qk_nope + dims->qk_rope) * dims->num_heads > INT32_MAX) return MLA_ERR_UNSUPPORTED;
   if ((int64_t)dims->num_pages * dims->page_size > INT32_MAX) return MLA_ERR_UNSUPPORTED;
   if (batch < 1 || total_q < 0 || block_table_stride < 1 || max_seq_len < 1) return MLA_ERR_INVALID_ARG;
+  if (append_blocks(*dims, total_q, q != nullptr, q == q_out) > INT32_MAX) return MLA_ERR_UNSUPPORTED;
   if (kv_new_stride < dims->kv_lora_rank + dims->qk_rope || kv_new_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
   if ((!kv_new && total_q > 0) || !input_row_offsets || !kv_pool || !block_table || !cache_lens || !freqs_cis ||
       !kv_norm_gamma || !workspace)

@@ -364,6 +364,12 @@ long long cache_row_bytes(int fmt, int L, int R) {
   return (long long)((L / 2 + L / 32 + 15) / 16 * 16) + 2 * R;
 }
 
+long long append_blocks(const mla_dims_t& d, int T, bool queries, bool in_place) {
+  const long long pieces = (long long)d.num_heads * (in_place ? d.qk_rope : d.qk_nope + d.qk_rope) / 8;
+  return ((long long)T + app::kRowsPerBlock - 1) / app::kRowsPerBlock +
+         (queries ? T * ((pieces + app::kPieces - 1) / app::kPieces) : 0);
+}
+
 cudaError_t launch_append(const mla_dims_t& d, int fmt, const void* kv_new, long long new_stride,
                           const uint32_t* offsets, int B, int T, const void* q, void* q_out, void* pool,
                           float* scales, void* rows_out, const int32_t* block_table, int bt_stride,
@@ -397,11 +403,9 @@ cudaError_t launch_append(const mla_dims_t& d, int fmt, const void* kv_new, long
   a.freqs = static_cast<const __nv_bfloat16*>(freqs);
   a.gamma = static_cast<const __nv_bfloat16*>(gamma);
   a.hdr = hdr;
-  a.row_blocks = (T + app::kRowsPerBlock - 1) / app::kRowsPerBlock;
-  const long long pieces = (long long)a.H * (q == q_out ? a.R : a.N + a.R) / 8;
-  a.q_blocks = q ? (int)((pieces + app::kPieces - 1) / app::kPieces) : 0;
-  const long long blocks = a.row_blocks + (long long)T * a.q_blocks;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  const long long blocks = append_blocks(d, T, q != nullptr, q == q_out);
+  a.row_blocks = (int)append_blocks(d, T, false, false);
+  a.q_blocks = (int)((blocks - a.row_blocks) / T);
   app::append_kernel<<<(unsigned)blocks, app::kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }

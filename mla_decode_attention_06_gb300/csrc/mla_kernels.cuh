@@ -70,6 +70,8 @@ cudaError_t launch_prologue(const mla_dims_t& d, void* q, const uint32_t* offset
 
 // Bytes of a cache row in a MLA_CACHE_ format.
 long long cache_row_bytes(int fmt, int L, int R);
+// Blocks of the append's grid, at most 2^31 - 1.
+long long append_blocks(const mla_dims_t& d, int T, bool queries, bool in_place);
 // New latent rows into the paged cache (RMSNorm, RoPE, the format's codes) and the
 // queries' RoPE; q may be NULL.
 cudaError_t launch_append(const mla_dims_t& d, int fmt, const void* kv_new, long long new_stride,

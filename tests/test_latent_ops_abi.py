@@ -59,6 +59,8 @@ def test_append_reports_unsupported_shapes(lib):
                dict(qk_rope=136), dict(qk_nope=100), dict(page_size=1 << 20, num_pages=1 << 12)):
         assert _append(lib, dims=_dims(**kw), stride=1024) == UNSUPPORTED, kw
     assert _append(lib, dims=_dims(num_heads=1 << 24)) == UNSUPPORTED     # a token's queries pass 32 bits
+    assert _append(lib, T=1 << 30, q_out=FAKE + 16) == UNSUPPORTED        # more blocks than a grid has
+    assert _append(lib, T=1 << 30, ws_bytes=0, q=None, q_out=None) == TOO_SMALL
     # without queries the head count and qk_nope are not looked at; the workspace is
     assert _append(lib, dims=_dims(num_heads=0, qk_nope=-1), q=None, q_out=None, ws_bytes=0) == TOO_SMALL
     assert _append(lib, ws=FAKE + 8) == TOO_SMALL
