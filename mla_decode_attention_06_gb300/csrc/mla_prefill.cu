@@ -212,11 +212,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
   int tiles = 0, blocks = 0;
   for (int b = b0; b < b1; ++b) {
     const Req q = request(b);
-    tiles += min(q.ntiles, a.cap_tiles + 1);   // more than there is room for is no room, whatever the sum
+    // more than there is room for is no room, whatever the sum
+    tiles = min(tiles + min(q.ntiles, a.cap_tiles + 1), a.cap_tiles + 1);
     blocks += (q.qlen + 2 * kTile - 1) / (2 * kTile);
   }
   int total_tiles, total_items;
-  int tile = block_scan(min(tiles, a.cap_tiles + 1), sums, &total_tiles);
+  int tile = block_scan(tiles, sums, &total_tiles);
   int item = block_scan(blocks, sums, &total_items);
   for (int b = b0; b < b1; ++b) {
     Req q = request(b);
