@@ -192,11 +192,10 @@ _status = {}
 
 def _unread_status(device, stream):
     """The status word of a stream's calls that nobody reads it of: kernels only set bits in it."""
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    key = (device, s.cuda_stream)
+    key = (device.index, stream.cuda_stream)
     t = _status.get(key)
     if t is None:
-        with torch.cuda.stream(s):
+        with torch.cuda.stream(stream):
             if torch.cuda.is_current_stream_capturing():
                 return torch.empty(256, dtype=torch.uint8, device=device)   # the graph's own memory, not kept
             t = _status[key] = torch.zeros(256, dtype=torch.uint8, device=device)
@@ -278,15 +277,16 @@ def mla_cache_append(kv_new, input_row_offsets, kv_pool, block_table, cache_lens
     if kv_scales is not None and kv_scales.numel() != dims.num_pages * page_size:
         raise ValueError("kv_scales must hold one value per cache row")
     B, offsets, table, table_stride, lens = _tables(input_row_offsets, block_table, cache_lens, dev)
+    s = torch.cuda.current_stream(dev) if stream is None else stream
     if workspace is None:
-        workspace = _buffer(256, torch.uint8, dev, stream) if debug else _unread_status(dev, stream)
+        workspace = _buffer(256, torch.uint8, dev, stream) if debug else _unread_status(dev, s)
     _call("mla_cache_append", dev, ctypes.byref(dims), int(cache_format), kv_new.data_ptr(), new_stride, offsets,
           B, T, _ptr(q, "q", _BF16, dev), _ptr(q_out, "q_out", _BF16, dev), _ptr(kv_pool, "kv_pool", None, dev),
           _ptr(kv_scales, "kv_scales", (torch.float32,), dev), _ptr(rows_out, "rows_out", _BF16, dev), table,
           table_stride, lens, _ptr(freqs_cis, "freqs_cis", _BF16, dev), freqs_cis.shape[0],
           _ptr(kv_norm_gamma, "kv_norm_gamma", _BF16, dev), float(epsilon),
           MLA_FLAG_DEBUG_CHECKS if debug else 0, _ptr(workspace, "workspace", None, dev),
-          workspace.numel() * workspace.element_size(), _stream(stream, dev))
+          workspace.numel() * workspace.element_size(), ctypes.c_void_p(s.cuda_stream))
     return kv_pool, q_out
 
 

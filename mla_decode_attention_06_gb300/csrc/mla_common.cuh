@@ -104,12 +104,10 @@ __device__ __forceinline__ double add_odd(double a, double b) {
   if (!isfinite(hi) || lo == 0.0 || (u & 1)) return hi;
   return __longlong_as_double((lo > 0.0) == (hi > 0.0) ? u + 1 : u - 1);
 }
-// Is the fp32 product p of two bf16 values other than their exact product?  (It has 16 bits, so
-// only past the ends of fp32's normal range.)
-__device__ __forceinline__ bool product_lost(float p, float x, float y) {
-  const float m = fabsf(p);
-  return !(m >= 0x1p-126f && m < INFINITY) && x != 0.f && y != 0.f;
-}
+// Other than 0 if the fp32 product p of two bf16 values is not their exact product (which has 16
+// bits, so only past the ends of fp32's normal range): what p lost, rounded up, is +0 only if it
+// is nothing, however small.
+__device__ __forceinline__ uint32_t product_lost(float p, float x, float y) { return __float_as_uint(__fmaf_ru(x, y, -p)); }
 
 // OCP E4M3FN code -> float through the hardware fp8 -> half conversion (exact).
 __device__ __forceinline__ float e4m3_to_f32(uint8_t code) {

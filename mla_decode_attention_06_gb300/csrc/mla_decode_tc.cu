@@ -1427,11 +1427,18 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
         }
         if (!C::kEarly && !wwait(&cs->s_full[b], (c >> 1) & 1, cs, hdr)) return;
         tc_fence_after();
+        // S row (64 fp32) for this thread's head; both halves of the load in flight at once
+        uint32_t sr[64];
+        tmem_ld32(trow + C::kSCol + 64 * b, *reinterpret_cast<uint32_t(*)[32]>(sr));
+        tmem_ld32(trow + C::kSCol + 64 * b + 32, *reinterpret_cast<uint32_t(*)[32]>(sr + 32));
+        const int over = MODE == kLoadFp4 ? *reinterpret_cast<volatile int*>(&cs->over) : 0;
+        tmem_ld_wait();
         if constexpr (MODE == kLoadFp4) {
           // A rope value past f16's range is an infinity in the product.  A score of +inf makes the
           // row NaN.  One of -inf would drop its key, whatever the key's true score: it is computed
-          // anew from the cache row itself (rare, one key after the other).
-          if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&cs->over) != 0)) {
+          // anew from the cache row itself (rare, one key after the other; the flag's read passes
+          // under the load of S: before it, it cost 4 us of 164).
+          if (__any_sync(0xffffffffu, over != 0)) {
 #pragma unroll 1
             for (int j = 0; j < 64; ++j) {
               if (!((mask >> j) & 1ull)) continue;
@@ -1445,13 +1452,11 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
               tmem_st1(trow + C::kSCol + 64 * b + j, v);
             }
             tmem_st_wait();
+            tmem_ld32(trow + C::kSCol + 64 * b, *reinterpret_cast<uint32_t(*)[32]>(sr));
+            tmem_ld32(trow + C::kSCol + 64 * b + 32, *reinterpret_cast<uint32_t(*)[32]>(sr + 32));
+            tmem_ld_wait();
           }
         }
-        // S row (64 fp32) for this thread's head; both halves of the load in flight at once
-        uint32_t sr[64];
-        tmem_ld32(trow + C::kSCol + 64 * b, *reinterpret_cast<uint32_t(*)[32]>(sr));
-        tmem_ld32(trow + C::kSCol + 64 * b + 32, *reinterpret_cast<uint32_t(*)[32]>(sr + 32));
-        tmem_ld_wait();
         float sv[64];
 #pragma unroll
         for (int j = 0; j < 64; ++j) sv[j] = __uint_as_float(sr[j]);

@@ -124,7 +124,7 @@ __device__ __forceinline__ void bf2(uint32_t v, float& lo, float& hi) {
 // exact in fp32.
 __device__ __forceinline__ void rotate(float x0, float x1, float c, float s, uint16_t& y0, uint16_t& y1) {
   const float p0 = __fmul_rn(x0, c), p1 = __fmul_rn(x1, s), p2 = __fmul_rn(x0, s), p3 = __fmul_rn(x1, c);
-  if (product_lost(p0, x0, c) || product_lost(p1, x1, s) || product_lost(p2, x0, s) || product_lost(p3, x1, c)) {
+  if (product_lost(p0, x0, c) | product_lost(p1, x1, s) | product_lost(p2, x0, s) | product_lost(p3, x1, c)) {
     y0 = round_bf16(add_odd((double)x0 * c, -((double)x1 * s)));
     y1 = round_bf16(add_odd((double)x0 * s, (double)x1 * c));
     return;

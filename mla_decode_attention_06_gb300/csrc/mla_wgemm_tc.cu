@@ -86,25 +86,40 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint16_t two) {
          ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(f.y)) << 16);
 }
 
-// v as f16, NaN where f16 does not hold it: an infinite query value would make scores of -inf
-// that drop their keys quietly.
-__device__ __forceinline__ float f16_or_nan(float v) { return fabsf(v) < 65520.f ? v : CUDART_NAN_F; }
 // The bits of v rounded to f16, in the 16-bit type of the staging tile.
 __device__ __forceinline__ __nv_bfloat16 f16_in_bf16(float v) {
-  return __ushort_as_bfloat16(__half_as_ushort(__float2half_rn(f16_or_nan(v))));
+  return __ushort_as_bfloat16(__half_as_ushort(__float2half_rn(v)));
 }
-// Eight bf16 values as f16; finite ones that f16 does not hold are reported.
+// Infinities among two f16 values become NaN: an infinite query value would make scores of
+// -inf that drop their keys quietly.  (Where none is, values are not looked at one by one: that
+// cost a microsecond of 16.)
+__device__ __forceinline__ uint32_t inf_to_nan(uint32_t w) {
+  if ((w & 0x7FFFu) == 0x7C00u) w |= 0x0200u;
+  if ((w & 0x7FFF0000u) == 0x7C000000u) w |= 0x02000000u;
+  return w;
+}
+// Eight bf16 values as f16, NaN for what f16 does not hold; finite ones of those are reported.
 __device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v, PlanHeader* hdr) {
   uint32_t w[4] = {v.x, v.y, v.z, v.w};
   bool over = false;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float x = __uint_as_float(w[i] << 16), y = __uint_as_float(w[i] & 0xFFFF0000u);
-    over |= (fabsf(x) >= 65520.f && fabsf(x) < CUDART_INF_F) || (fabsf(y) >= 65520.f && fabsf(y) < CUDART_INF_F);
-    const __half2 h = __floats2half2_rn(f16_or_nan(x), f16_or_nan(y));
+    over |= fabsf(x) >= 65520.f || fabsf(y) >= 65520.f;
+    const __half2 h = __floats2half2_rn(x, y);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  if (over) atomicOr(&hdr->status, kDeviceCheckFailed);
+  if (over) {
+    const uint32_t b[4] = {v.x, v.y, v.z, v.w};
+    bool finite = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = fabsf(__uint_as_float(b[i] << 16)), y = fabsf(__uint_as_float(b[i] & 0xFFFF0000u));
+      finite |= (x >= 65520.f && x < CUDART_INF_F) || (y >= 65520.f && y < CUDART_INF_F);
+      w[i] = inf_to_nan(w[i]);
+    }
+    if (finite) atomicOr(&hdr->status, kDeviceCheckFailed);
+  }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -344,8 +359,18 @@ __global__ void __launch_bounds__(kThreads, 1) wgemm_kernel(const __grid_constan
         // columns past the last token hold zeros
         bool over = false;
 #pragma unroll
-        for (int q = 0; q < 32; ++q) over |= fabsf(v[q]) >= 65520.f && fabsf(v[q]) < CUDART_INF_F;
-        if (over) atomicOr(&a.hdr->status, kDeviceCheckFailed);
+        for (int q = 0; q < 32; ++q) over |= fabsf(v[q]) >= 65520.f;
+        if (over) {
+          bool finite = false;
+#pragma unroll
+          for (int q = 0; q < 32; ++q) finite |= fabsf(v[q]) >= 65520.f && fabsf(v[q]) < CUDART_INF_F;
+          if (finite) atomicOr(&a.hdr->status, kDeviceCheckFailed);
+#pragma unroll 1
+          for (int q = 0; j0 + q < TN && q < 32; ++q) {
+            __nv_bfloat16* p = stg + ((size_t)i * TN + j0 + q) * 128 + row;
+            *p = __ushort_as_bfloat16((unsigned short)inf_to_nan(__bfloat16_as_ushort(*p)));
+          }
+        }
       }
     }
   }
