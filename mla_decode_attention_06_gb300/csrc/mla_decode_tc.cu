@@ -383,12 +383,11 @@ __device__ __noinline__ void merge_split_token(const DecodeArgs& a, int t, const
   auto slot_of = [&](int k) { return (k == kf ? slot_kf : 0) * ns + ts; };
   auto lse_of = [&](int k) { return __ldcg(part_lse + ((size_t)(k * 2 * ns + slot_of(k)) * 2 + rank) * H + row); };
   float mx = -CUDART_INF_F;
-  bool nan = false;   // a partial that is NaN makes the row NaN (the maximum passes over it)
-  for (int k = kf; k <= kl; ++k) {
-    const float v = lse_of(k);
-    mx = fmaxf(mx, v);
-    nan |= v != v;
-  }
+  for (int k = kf; k <= kl; ++k) mx = fmaxf(mx, lse_of(k));
+  // a partial that is NaN makes the row NaN: by its weight, unless the maximum found no other
+  bool nan = false;
+  if (mx == -CUDART_INF_F)
+    for (int k = kf; k <= kl; ++k) nan |= isnan(lse_of(k));
   float sum = 0.f;
   if (mx != -CUDART_INF_F)
     for (int k = kf; k <= kl; ++k) sum += __expf(lse_of(k) - mx);
@@ -507,17 +506,9 @@ __device__ __noinline__ bool merge_in_tmem(const DecodeArgs& a, Smem* cs, int t,
     return kk == k ? lse_own : __ldcg(lse_ptr(kk));
   };
   float mx = -CUDART_INF_F;
-  bool nan = false;   // a partial that is NaN: its O is too, and so is what it is added to
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    mx = fmaxf(mx, lv0[j]);
-    nan |= lv0[j] != lv0[j];
-  }
-  for (int kk = kf + 8; kk <= kl; ++kk) {
-    const float v = lse_at(kk);
-    mx = fmaxf(mx, v);
-    nan |= v != v;
-  }
+  for (int j = 0; j < 8; ++j) mx = fmaxf(mx, lv0[j]);
+  for (int kk = kf + 8; kk <= kl; ++kk) mx = fmaxf(mx, lse_at(kk));
   float sum = 0.f;
   if (mx != -CUDART_INF_F) {
 #pragma unroll
@@ -593,8 +584,17 @@ __device__ __noinline__ bool merge_in_tmem(const DecodeArgs& a, Smem* cs, int t,
     fence_proxy_async_smem();
     bulk_copy_s2g(a.o_lat + ((size_t)t * H + row) * L + lat_x0, srow, LC * 2);
     bulk_commit();
-    if (rank == 0)
-      a.lse_ws[(size_t)t * H + row] = nan ? CUDART_NAN_F : (mx != -CUDART_INF_F ? mx + __logf(sum) : -CUDART_INF_F);
+    if (rank == 0) {
+      // a partial that is NaN has a NaN O, and its weight is NaN, so the row and `sum` are, unless
+      // the maximum found no other partial
+      float lse = mx + __logf(sum);
+      if (mx == -CUDART_INF_F) {
+        lse = mx;
+        for (int kk = kf; kk <= kl; ++kk)
+          if (isnan(kk == k ? lse_own : __ldcg(lse_ptr(kk)))) lse = CUDART_NAN_F;
+      }
+      a.lse_ws[(size_t)t * H + row] = lse;
+    }
     bulk_wait_all();
   }
   return true;
