@@ -18,7 +18,9 @@
 // same instructions on the same bits, hence the same S, the same online softmax
 // and the same P; each then applies P to its own half of the latent columns.
 // Nothing is exchanged between the two CTAs but the tiles and the "stage free"
-// signals (tcgen05.commit multicast to both CTAs' empty barriers).
+// signals (tcgen05.commit multicast to both CTAs' empty barriers).  Over an e2m1
+// cache each CTA loads the tiles for itself, and CTA 1 sums S in another order
+// (Cfg::kEarly); each normalises its own half of O by its own row sums.
 //
 // The absorbed query (576 columns per head) is split between TMEM and shared
 // memory: latent columns [0, 256) sit in TMEM as the A operand of
@@ -30,7 +32,7 @@
 // cache's 512 see Cfg::kGrouped):
 //   warp 0      TMA producer: the query's shared-memory part once per segment,
 //               cache tiles through the page table into a kStages-deep ring,
-//               and (not e2m1) an L2 prefetch of the tile two ahead.
+//               and an L2 prefetch of the tile two ahead.
 //   warp 1      TMEM owner and QK issuer (one thread); its other lanes zero
 //               cache rows outside the key range before the MMAs read them
 //               (0 * NaN would poison P . C).
@@ -600,26 +602,6 @@ __device__ __noinline__ bool merge_in_tmem(const DecodeArgs& a, Smem* cs, int t,
   return true;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// (x, y) * a + b and (x, y) + (a, b), both halves in one instruction.
-__device__ __forceinline__ void fma_pair(float& x, float& y, float a, float b) {
-  asm("{\n\t.reg .b64 v, s, t;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 t, {%3, %3};\n\t"
-      "fma.rn.f32x2 v, v, s, t;\n\tmov.b64 {%0, %1}, v;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b));
-}
-__device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
-  asm("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\tadd.rn.f32x2 v, v, s;\n\t"
-      "mov.b64 {%0, %1}, v;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b));
-}
-
 template <int LC, int CL, int MODE>
 __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
     decode_tc_kernel(const __grid_constant__ Maps maps, const DecodeArgs a) {
@@ -706,7 +688,7 @@ __global__ void __launch_bounds__(Cfg<LC, CL, MODE>::kThreads, 1)
 
   // The issuing lane of a converged warp.  Behind elect.sync the compiler knows that one thread
   // runs the MMA loops, behind lane == 0 it does not: 64 e2m1 requests of 1,024 to 8,192 tokens
-  // 208 -> 195 us, 128 e4m3 ones 736 -> 704 us.  Over bf16 it did not help (82 -> 86 us for 8
+  // 208 -> 195 us, 128 e4m3 ones 723 -> 686 us.  Over bf16 it did not help (82 -> 86 us for 8
   // requests of 4,096 keys).
   auto issuer = [&]() { return C::kCoded ? elect_one() : lane == 0; };
   if (C::kGrouped && warp < 4) {

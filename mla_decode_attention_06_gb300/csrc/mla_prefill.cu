@@ -36,7 +36,9 @@
 // a row small beside its neighbours loses nothing that the second sequence would keep, and
 // heads or weights some thousand times smaller than usual stay in the first.  A second
 // sequence of the same kernels with bf16 throughout follows in the stream and returns at once
-// unless the flag is up.  Queries are converted by the
+// unless the flag is up (measured, raised in the gather and in the expansion against not at all:
+// one prompt of 16,384 tokens x 16 heads 911 and 949 against 893 us, two chunks behind 7,600
+// e2m1 keys 620 and 874 against 617, seven short prompts 183 and 246 against 182).  Queries are converted by the
 // CTA that uses them, each row scaled by its own power of two; e4m3 latents and weights
 // become f16 before the expansion, bf16 and e2m1 ones enter it as the bf16 values they are.
 // Measured on uniform random cases: 1.7e-3 relative to 64 bits with f16, most of it the
@@ -689,9 +691,10 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
 // warpgroups (384 x 168 = 128 x 104 + 256 x 200).
 // Measured, 16,384 tokens x 16 heads: 2,230 us with one barrier a box, 1,184 with one a tile
 // and the register split, 1,125 with two issuers, 989 with turns and these places, 978 block
-// after block, 895 with the blocks in a better order (1,610 TFLOP/s over the whole call; 3,260 cycles a step of 256 x 128, of which
-// the products take 96 %).  Prompts of 1,500 to 2,300 tokens, 128 heads: 718, 650 and 629 us with
-// the last three; what is left there is a block's own start and end, about 13,000 cycles in which
+// after block, 895 with the blocks in a better order (1,610 TFLOP/s over the whole call; 3,260
+// cycles a step of 256 x 128, of which the products take 96 %).  Those are runs of some 20 calls;
+// in longer ones the power cap makes it 967 (1,490 TFLOP/s).  Prompts of 1,500 to 2,300 tokens,
+// 128 heads: 718, 690 and 648 us with the last three; what is left there is a block's own start and end, about 13,000 cycles in which
 // the queries are converted and the rows of O leave by stores of 16 bytes a row (32-byte
 // stores, staging, and the next block's queries converted before this one's O is written were
 // all slower).
@@ -727,23 +730,6 @@ struct AttMaps {
   CUtensorMap qn, qr;   // queries: [T, H, N] and [T, H, R] of rows of N + R, boxes 64 x 1 x 128
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ void fma2(float& x, float& y, float a, float b) {   // (x, y) * a + b
-  asm("{\n\t.reg .b64 v, s, t;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 t, {%3, %3};\n\t"
-      "fma.rn.f32x2 v, v, s, t;\n\tmov.b64 {%0, %1}, v;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b));
-}
-__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
-  asm("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\tadd.rn.f32x2 v, v, s;\n\t"
-      "mov.b64 {%0, %1}, v;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b));
-}
 // Bits [0, n) of a word.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
 
@@ -1166,14 +1152,14 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
             float* v = x + 32 * i + 2 * e;
-            fma2(v[0], v[1], sl2, neg);
-            fma2(v[2], v[3], sl2, neg);
+            fma_pair(v[0], v[1], sl2, neg);
+            fma_pair(v[2], v[3], sl2, neg);
             v[0] = ex2(v[0]);
             v[1] = ex2(v[1]);
             v[2] = ex2(v[2]);
             v[3] = ex2(v[3]);
-            add2(l0, l1, v[0], v[1]);
-            add2(l2, l3, v[2], v[3]);
+            add_pair(l0, l1, v[0], v[1]);
+            add_pair(l2, l3, v[2], v[3]);
             p[e] = kHalf ? pack_f16(v[0], v[1]) : pack_bf16(v[0], v[1]);
             p[e + 1] = kHalf ? pack_f16(v[2], v[3]) : pack_bf16(v[2], v[3]);
           }

@@ -469,8 +469,8 @@ cudaError_t launch(const Args& a0, WFmt wf, const void* w, const void* x, int Kx
   }
   if (!hit) {
   {
-      cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)a.H * a.M};
     const bool f8 = wf == WFmt::kE4M3;
+    cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)a.H * a.M};
     cuuint64_t strides[1] = {(cuuint64_t)a.K * (f8 ? 1 : 2)};
     cuuint32_t box[2] = {64, 128};
     cuuint32_t es[2] = {1, 1};
