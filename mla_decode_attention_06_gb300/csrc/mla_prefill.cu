@@ -30,15 +30,18 @@
 // amplified by the softmax, would be most of the error.  They are kept as f16 (2^-12, the
 // same tensor rate), which holds what such values are in practice but not what they could
 // be: the kernels that write them check the largest magnitude of every row (64 columns of a K
-// or V row, a rope row, an e4m3 latent row, 256 neighbouring e4m3 weights) and raise a flag
-// where it is above 2^15 or, not being zero, below 2^-15.  At 2^-15 f16's step is 2^-24, so
+// or V row, a rope row, an e4m3 latent row, 256 neighbouring e4m3 weights) and flag the request
+// (for weights the call) where it is above 2^15 or, not being zero, below 2^-15.  At 2^-15 f16's step is 2^-24, so
 // each value is off by at most 2^-10 of its row's largest, half of what bf16 may be off by:
 // a row small beside its neighbours loses nothing that the second sequence would keep, and
 // heads or weights some thousand times smaller than usual stay in the first.  A second
-// sequence of the same kernels with bf16 throughout follows in the stream and returns at once
-// unless the flag is up (measured, raised in the gather and in the expansion against not at all:
-// one prompt of 16,384 tokens x 16 heads 911 and 949 against 893 us, two chunks behind 7,600
-// e2m1 keys 620 and 874 against 617, seven short prompts 183 and 246 against 182).  Queries are converted by the
+// sequence of the same kernels with bf16 throughout follows in the stream: it takes the flagged
+// requests, the first leaves them, so a request's result does not depend on what it is batched
+// with; without flags it returns at once.  Measured, all requests flagged by the gather, all by the
+// expansion, the first one by the gather, none: two chunks behind 7,600 e2m1 keys 702, 928, 736 and
+// 619 us, seven short prompts 218, 275, 245 and 183, one prompt of 16,384 tokens x 16 heads 962, 986
+// and 894.  A flag is raised by one kernel and decides in later ones only: within a launch no two
+// threads see it differ.  Queries are converted by the
 // CTA that uses them, each row scaled by its own power of two; e4m3 latents and weights
 // become f16 before the expansion, bf16 and e2m1 ones enter it as the bf16 values they are.
 // Measured on uniform random cases: 1.7e-3 relative to 64 bits with f16, most of it the
@@ -69,7 +72,8 @@ struct Req {
   int32_t tile0, ntiles;
   int32_t item0;           // query blocks of the requests before
   int32_t fits;            // 0: no room in the workspace, its outputs are NaN
-  int32_t pad[3];
+  int32_t wide[2];         // f16 does not do, found by the gather, by the expansion
+  int32_t pad;
 };
 
 struct Args {
@@ -99,18 +103,32 @@ struct Args {
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// Whole block, after the wait on the previous kernel: does this sequence run?  One thread reads
-// the flag for all: other blocks of the same launch may raise it meanwhile, and a block whose
-// warps disagree would wait for threads that have left.  Blocks may disagree: what a launch that
-// raises the flag writes is not used.
-__device__ __forceinline__ bool runs(const Args& a) {
-  __shared__ int go;
-  if (threadIdx.x == 0) {
-    const bool wide = *reinterpret_cast<const volatile int*>(&a.hdr->pad[3]) != 0;
-    go = a.half ? !wide : wide;
+constexpr int kWeights = 1, kGathered = 2, kExpanded = 4;   // bits of hdr->pad[3]
+__device__ __forceinline__ int raised(const Args& a) { return *reinterpret_cast<const volatile int*>(&a.hdr->pad[3]); }
+__device__ __forceinline__ void raise(const Args& a, int bit, int b) {   // b: the request, -1 for weights
+  int* w = b < 0 ? &a.hdr->pad[3] : &a.reqs[b].wide[bit == kGathered ? 0 : 1];
+  if (__ldcg(w) & bit) return;   // by another thread (all of them at once took three times the call)
+  atomicOr(w, bit);
+  if (b >= 0) atomicOr(&a.hdr->pad[3], bit);
+}
+// After the wait on the previous kernel: does this sequence take any request?  (`flags`: one read
+// of the word.  What a kernel itself raises it does not look at: the first sequence raises flags,
+// the second does not.)
+__device__ __forceinline__ bool runs(const Args& a, int flags) { return a.half ? !(flags & kWeights) : flags != 0; }
+// Does it take request b, by the gather's flags and (`expanded`) the expansion's?
+__device__ __forceinline__ bool takes(const Args& a, int flags, int b, bool expanded) {
+  const bool wide = (flags & kWeights) || __ldcg(&a.reqs[b].wide[0]) != 0 || (expanded && __ldcg(&a.reqs[b].wide[1]) != 0);
+  return a.half ? !wide : wide;
+}
+// The request that holds a key tile: the last one with tile0 <= tile that has tiles.
+__device__ __forceinline__ int request_of(const Args& a, int tile) {
+  int lo = 0, hi = a.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.reqs[mid].tile0 <= tile) lo = mid; else hi = mid - 1;
   }
-  __syncthreads();
-  return go != 0;
+  while (lo > 0 && a.reqs[lo].ntiles == 0) --lo;
+  return lo;
 }
 // Is a row's largest magnitude (fp32 bits) one that f16 holds well: zero, or within
 // [2^-15, 2^15]?  Half a step of f16 then is at most 2^-10 of it.
@@ -291,17 +309,14 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const Args a) {
   __shared__ uint32_t word;
   griddep_launch();
   griddep_wait();
-  if (!runs(a)) return;
+  const int flags = raised(a);
+  if (!runs(a, flags)) return;
   const int tile = blockIdx.x / (kTile / kGatherRows), part = blockIdx.x % (kTile / kGatherRows);
   if (tile >= a.hdr->total_tiles) return;
   const bool lat_f16 = a.half && a.fmt == MLA_CACHE_E4M3;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int lo = 0, hi = a.B - 1;   // the last request with tile0 <= tile that has tiles
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.reqs[mid].tile0 <= tile) lo = mid; else hi = mid - 1;
-  }
-  while (lo > 0 && a.reqs[lo].ntiles == 0) --lo;
+  const int lo = request_of(a, tile);
+  if (!a.half && !takes(a, flags, lo, true)) return;
   const Req q = a.reqs[lo];
   if (threadIdx.x == 0) word = 0;
   __syncthreads();
@@ -406,7 +421,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const Args a) {
       if (odd && lane < R / 8) rw[e] = 0x7FFF7FFFu;   // NaN in either type
     }
     const bool rope_holds = f16_holds(rt);
-    if (a.half && lane == 0 && (!rope_holds || (lat_f16 && !odd && !lat_holds))) atomicOr(&a.hdr->pad[3], 1);
+    if (a.half && lane == 0 && (!rope_holds || (lat_f16 && !odd && !lat_holds))) raise(a, kGathered, lo);
     rp[i] = make_uint4(rw[0], rw[1], rw[2], rw[3]);
     if (have) {
       uint8_t* box = a.lat + ((size_t)tile * (L / 64) + (l0 >> 6)) * kBox + row * 128;
@@ -427,7 +442,7 @@ __global__ void __launch_bounds__(256) widen_weights_kernel(const Args a, const 
   const int nr = (rows + 127) / 128, nc = (cols + 127) / 128;
   griddep_launch();
   griddep_wait();
-  if (!runs(a)) return;
+  if (!a.half && !runs(a, raised(a))) return;
   bool wide = false;
   for (long long i0 = (long long)blockIdx.x * 256; i0 < n8; i0 += (long long)gridDim.x * 256) {
     const long long i = i0 + threadIdx.x;
@@ -451,7 +466,7 @@ __global__ void __launch_bounds__(256) widen_weights_kernel(const Args a, const 
     }
     if (!f16_holds(top)) wide = true;   // 256 neighbouring weights
   }
-  if (a.half && wide && (threadIdx.x & 31) == 0) atomicOr(&a.hdr->pad[3], 1);
+  if (a.half && wide && (threadIdx.x & 31) == 0) raise(a, kWeights, -1);
 }
 
 // ------------------------------------------------------------------------------ waits
@@ -548,7 +563,11 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
   griddep_wait();
   fence_proxy_async_global();
   const int L = a.d.kv_lora_rank, nkb = L / 64, tiles = a.hdr->total_tiles;
-  const long long total = runs(a) ? (long long)tiles * a.hg : 0;
+  const int flags = raised(a);
+  const long long total = runs(a, flags) ? (long long)tiles * a.hg : 0;
+  // with no request flagged by the gather the first sequence takes every tile
+  const bool choose = !a.half || (flags & kGathered);
+  auto skip = [&](int tile) { return choose && !takes(a, flags, request_of(a, tile), !a.half); };
   const bool in_f16 = a.half && a.fmt == MLA_CACHE_E4M3;   // latents and weights
   PlanHeader* hdr = a.hdr;
   if (blockIdx.x == 0 && tid == 0) hdr->pad[4] = 0;
@@ -560,6 +579,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
       bool ok = true;
       for (long long w = blockIdx.x; w < total && ok; w += gridDim.x) {
         const int h = a.h0 + (int)(w / tiles), tile = (int)(w % tiles);
+        if (choose && skip(tile)) continue;
         for (int kb = 0; kb < nkb; ++kb, ++c) {
           const int s = c % kExpStages;
           if (c >= kExpStages && !(ok = wait(&cs->empty[s], ((c / kExpStages) & 1) ^ 1, &cs->ctl, hdr))) break;
@@ -583,7 +603,8 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
     const uint32_t base = smem_u32(sm);
     int c = 0, it = 0;
     bool ok = true;
-    for (long long w = blockIdx.x; w < total && ok; w += gridDim.x, ++it) {
+    for (long long w = blockIdx.x; w < total && ok; w += gridDim.x) {
+      if (choose && skip((int)(w % tiles))) continue;
       const uint32_t acc = tmem + 256 * (it & 1);
       if (it >= 2 && !(ok = wwait(&cs->acc_empty[it & 1], ((it >> 1) & 1) ^ 1, &cs->ctl, hdr))) break;
       for (int kb = 0; kb < nkb; ++kb, ++c) {
@@ -606,6 +627,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
       }
       if (ok && elect_one()) mma_commit(&cs->acc_full[it & 1]);
       __syncwarp();
+      ++it;
     }
     __syncwarp();
   } else {
@@ -614,9 +636,10 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
     const int nb = a.nbk + a.nbv;
     const bool first = tid == 64;   // issues the bulk stores
     int it = 0, n = 0;
-    bool wide = false;
-    for (long long w = blockIdx.x; w < total; w += gridDim.x, ++it) {
+    for (long long w = blockIdx.x; w < total; w += gridDim.x) {
       const int h = (int)(w / tiles), tile = (int)(w % tiles);   // h within the pass
+      if (choose && skip(tile)) continue;
+      bool wide = false;
       const bool ok = wwait(&cs->acc_full[it & 1], (it >> 1) & 1, &cs->ctl, hdr);
       if (!all_of_128(1, ok)) break;
       tc_fence_after();
@@ -656,8 +679,9 @@ __global__ void __launch_bounds__(kExpThreads, 1) expand_kernel(const __grid_con
           bulk_commit();
         }
       }
+      if (a.half && wide) raise(a, kExpanded, request_of(a, tile));
+      ++it;
     }
-    if (a.half && __any_sync(0xffffffffu, wide) && lane == 0) atomicOr(&hdr->pad[3], 1);
     if (first) bulk_wait_all();
   }
   tc_fence_before();
@@ -736,17 +760,19 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >=
 // Block `at`: split fastest, then head, then query block (the longest first, so that the SMs
 // finish together), in groups of as many heads as keep their keys and values in half the L2
 // (16,384 tokens x 16 heads 978 us head by head, 895 so; 927 and 902 with 16 and 128 MB).
-__device__ __forceinline__ void set_block(const Args& a, int nitems, long long at, Block& k) {
+// A block of a request that the other sequence takes becomes one without query tokens.
+__device__ __forceinline__ void set_block(const Args& a, int nitems, long long at, int flags, Block& k) {
   const long long head = (long long)max(a.hdr->total_tiles, 1) * (a.nbk + a.nbv) * kBox, i = at / a.splits;
   const int group = (int)min((long long)a.hg, max(1ll, kGroupBytes / head));
   const int h0 = (int)(i / ((long long)group * nitems)) * group, heads = min(group, a.hg - h0);
   const long long in = i - (long long)h0 * nitems;
   const int split = (int)(at % a.splits), item = (int)(in / heads);
   const int2 it = a.items[item];
-  const Req q = a.reqs[it.x];
+  Req q = a.reqs[it.x];
+  if (flags && !takes(a, flags, it.x, true)) q.qlen = 0;
   const int r0 = it.y * 2 * kTile, nsub = q.qlen > r0 + kTile ? 2 : 1;
   int j0[2] = {0, 0}, j1[2] = {0, 0};
-  if (q.fits)
+  if (q.fits && q.qlen > 0)
     for (int s = 0; s < nsub; ++s)
       tile_range(a, q, r0 + s * kTile, min(r0 + (s + 1) * kTile, q.qlen), j0[s], j1[s]);
   const bool on0 = j1[0] > j0[0], on1 = j1[1] > j0[1];
@@ -785,7 +811,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
   griddep_launch();
   griddep_wait();
   fence_proxy_async_global();
-  if (!runs(a)) return;
+  const int flags = raised(a);
+  if (!runs(a, flags)) return;
   const int nitems = hdr->pad[2];
   const long long nblocks = (long long)a.splits * nitems * a.hg;
   if (warp == 1) {
@@ -847,7 +874,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         if (i >= kBlocks && !wait(&cs->blk_empty[i % kBlocks], ((i / kBlocks) & 1) ^ 1, &cs->ctl, hdr)) break;
         const long long at = i == 0 ? blockIdx.x : (long long)gridDim.x + atomicAdd(&hdr->pad[4], 1);
         Block& k = cs->blk[i % kBlocks];
-        if (at < nblocks) set_block(a, nitems, at, k);
+        if (at < nblocks) set_block(a, nitems, at, flags, k);
         else k.h = -1;
         mbar_arrive(&cs->blk_full[i % kBlocks]);
         if (at >= nblocks) break;

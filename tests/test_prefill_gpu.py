@@ -464,3 +464,44 @@ def test_widest_window(dev):
         out, lse = call(c, dev, debug=past[0] >= 0)
         c.lens = c.lens.astype(np.int64)
         compare(c, out, lse, "f16")
+
+
+@pytest.mark.parametrize("what", ["large", "small", "rope"])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_request_out_of_range_changes_no_other(dev, fmt, what):
+    # one request of a batch holds rows that f16 does not: the bits of the others are those of a batch
+    # without it, over key splits and passes of heads too, and its own values are right
+    import mla_decode_attention_06_gb300 as M
+    scale = {"large": 2.0 ** -17, "small": None, "rope": 2.0 ** -23}[what]
+    kw = dict(**NARROW, H=3, qlens=(140, 20, 300, 0, 5), past=(3, 250, 0, 40, 90), scale=scale, pad=2)
+    clean, c = Case(fmt, 26, **kw), Case(fmt, 26, **kw)
+    row = c.rows[1]
+    if what == "rope":
+        v = ref.bf16_values(np.ascontiguousarray(c.pool[row, -2 * c.R:]).view(np.uint16)) * 2.0 ** 20
+        c.pool[row, -2 * c.R:] = ref.bf16_bits(v).view(np.uint8)
+    else:
+        k = 14 if what == "large" else -22
+        if fmt == "bf16":
+            v = ref.bf16_values(np.ascontiguousarray(c.pool[row, :2 * c.L]).view(np.uint16)) * 2.0 ** k
+            c.pool[row, :2 * c.L] = ref.bf16_bits(v).view(np.uint8)
+        elif fmt == "e4m3":
+            c.scales[row] *= np.float32(2.0 ** k)
+        else:
+            at = c.pool[row, c.L // 2:c.L // 2 + c.L // 32].astype(np.int64) + k
+            c.pool[row, c.L // 2:c.L // 2 + c.L // 32] = at.astype(np.uint8)
+    others = np.r_[0:140, 160:465]
+    want_all, want_lse_all = c.expected()
+    for splits in (1, 3):
+        want, want_lse = check(clean, dev, num_splits=splits)
+        dims = M.MlaDims(num_heads=3, qk_nope=c.N, qk_rope=c.R, kv_lora_rank=c.L, v_head=c.V, page_size=c.ps, num_pages=c.num_pages)
+        opts = M.MlaOpts(mask=1, window=0, scale=float(c.scale), num_splits=splits, flags=0)
+        n = M.mla_prefill_workspace_size(dims, opts, c.fmt, 5, c.T + 2, int(c.lens.sum()))
+        one_head = (int(c.lens.sum()) // 128 + 5) * 2 * 16384
+        for heads in (3, 1):
+            ws = torch.empty(n - (3 - heads) * one_head, dtype=torch.uint8, device=dev)
+            out, lse = call(c, dev, num_splits=splits, workspace=ws)
+            assert torch.equal(out[others], want[others]) and torch.equal(lse[others], want_lse[others])
+            assert (out[c.T:] == 7).all() and (lse[c.T:] == 7).all()
+            g, w = out[140:160].float().cpu().numpy().astype(np.float64), want_all[140:160]
+            assert np.linalg.norm(g - w) <= TOL["bf16 e4m3" if fmt == "e4m3" else "bf16"] * np.linalg.norm(w)
+            assert np.abs(lse[140:160].cpu().numpy() - want_lse_all[140:160]).max() <= TOL_LSE["bf16 e4m3" if fmt == "e4m3" else "bf16"]
