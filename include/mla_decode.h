@@ -314,8 +314,8 @@ int mla_cache_append(const mla_dims_t* dims, int32_t cache_format, const void* k
  * a NaN or an infinity in its latent part makes NaN of the queries that see it and of no
  * other.  Keys, values and probabilities are f16 where the largest magnitude of each row of 64
  * columns (of 256 e4m3 weights) is zero or within [2^-15, 2^15]; where one is not, its request
- * (for weights the call) is worked in bf16, which takes a call up to 1.5 times as long.  A
- * request's result does not depend on the others of the call.
+ * (for weights the call) is worked in bf16, which takes a call up to 1.5 times as long.  The
+ * other requests of the call are not affected.
  * The fp8 call takes the cache and weights of mla_decode_paged_fp8, the fp4 call the cache
  * of mla_decode_paged_fp4 and bf16 weights. */
 int mla_prefill_workspace_size(const mla_dims_t* dims, const mla_opts_t* opts, int32_t cache_format, int32_t batch,

@@ -36,8 +36,8 @@
 // a row small beside its neighbours loses nothing that the second sequence would keep, and
 // heads or weights some thousand times smaller than usual stay in the first.  A second
 // sequence of the same kernels with bf16 throughout follows in the stream: it takes the flagged
-// requests, the first leaves them, so a request's result does not depend on what it is batched
-// with; without flags it returns at once.  Measured, all requests flagged by the gather, all by the
+// requests, the first leaves them, so that the other requests of the call keep their bits;
+// without flags it returns at once.  Measured, all requests flagged by the gather, all by the
 // expansion, the first one by the gather, none: two chunks behind 7,600 e2m1 keys 702, 928, 736 and
 // 619 us, seven short prompts 218, 275, 245 and 183, one prompt of 16,384 tokens x 16 heads 962, 986
 // and 894.  A flag is raised by one kernel and decides in later ones only: within a launch no two
