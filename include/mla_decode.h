@@ -287,6 +287,57 @@ int mla_cache_append(const mla_dims_t* dims, int32_t cache_format, const void* k
                      int32_t max_seq_len, const void* kv_norm_gamma, float epsilon, uint32_t flags, void* workspace,
                      size_t workspace_bytes, void* stream);
 
+/* Cache rows read back as bf16 values: the inverse addressing of mla_cache_append.  Request b
+ * gives its last n = input_row_offsets[b + 1] - input_row_offsets[b] tokens of cache_lens[b]
+ * (a prefix of a request: cache_lens[b] = the prefix's length); row t = input_row_offsets[b] + i
+ * of the result is the cache row at pos = cache_lens[b] - n + i,
+ *   rows_out[t] = [ bf16(c_kv) (L) ; k_rope (R) ],   c_kv = code * scale
+ * each value rounded once (exact but past bf16's range for BF16, E2M1 and power-of-two scales).
+ *   dims           kv_lora_rank, qk_rope, page_size and num_pages are used; L a multiple of
+ *                  32 up to 512, R of 8 up to 128
+ *   kv_pool        the cache, rows of the format; kv_scales float [num_pages, ps] for E4M3, else
+ *                  NULL; any fp32 scales
+ *   rows_out       bf16 [total_rows, L+R]
+ *   flags, workspace   as mla_branch_prologue
+ * kv_pool and rows_out are 16-byte aligned.  Rows t >= input_row_offsets[B] keep what they held.  A
+ * token whose position is below 0 or outside the block table, or whose page id is outside
+ * [0, num_pages), is skipped (its row keeps what it held) and recorded: MLA_ERR_DEVICE_CHECK in
+ * debug mode. */
+int mla_cache_read(const mla_dims_t* dims, int32_t cache_format, const uint32_t* input_row_offsets, int32_t batch,
+                   int32_t total_rows, const void* kv_pool, const float* kv_scales, const int32_t* block_table,
+                   int32_t block_table_stride, const uint32_t* cache_lens, void* rows_out, uint32_t flags,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* 8-bit codes of activations, and the row scale that goes with them (value = code * scale):
+ *   BF16   no codes
+ *   E4M3   OCP E4M3FN, scale = the least 2^e with max|y| <= 448 * 2^e (as MLA_CACHE_E4M3)
+ *   INT8   -127 .. 127, scale = max|y| / 127 rounded to fp32, at least 2^-126
+ * Codes are the nearest to y / scale, ties to even; the scale of a row of zeros is 1.  A row that
+ * holds a NaN or an infinity reads back as NaN throughout (E4M3: NaN codes; INT8: a NaN scale). */
+typedef enum {
+  MLA_CODES_BF16 = 0,
+  MLA_CODES_E4M3 = 1,
+  MLA_CODES_INT8 = 2
+} mla_code_format_t;
+
+/* Residual addition, RMSNorm and 8-bit codes of rows, in one pass: the input of a projection
+ * over codes (mla_linear_fp8, mla_linear_int8).
+ *   h = bf16( x + residual )                                  (h = x if residual is NULL)
+ *   y = bf16( h / sqrt(mean(h^2) + epsilon) * gamma )          (y = h if gamma is NULL)
+ * y is rounded once, from within a few double-precision units of its value; codes are those of y.
+ *   x              bf16 [rows, x_stride], the first `width` of each row are used; x_stride in
+ *                  elements, >= width, a multiple of 8
+ *   residual       bf16 [rows, width] or NULL; residual_out bf16 [rows, width] receives h, NULL
+ *                  exactly if residual is; residual_out == residual updates in place
+ *   gamma          bf16 [width] or NULL
+ *   y_out          bf16 [rows, width] or NULL; required for MLA_CODES_BF16
+ *   codes_out      e4m3 or int8 [rows, width], scales_out float [rows]; both NULL for MLA_CODES_BF16
+ * width is a multiple of 8 up to 32768; all tensors but scales_out are 16-byte aligned.  Outputs
+ * may not overlap each other or an input, but for the in-place residual. */
+int mla_rmsnorm_quant(int32_t code_format, int32_t rows, int32_t width, const void* x, int64_t x_stride,
+                      const void* residual, void* residual_out, const void* gamma, float epsilon, void* y_out,
+                      void* codes_out, float* scales_out, void* stream);
+
 /* Prefill: the decode's attention for many query tokens per request, in the expanded
  * form (generic_flare_mla_prefill_kv_cache_ragged page), over the paged latent cache that
  * mla_cache_append fills.  Per head, every visible cached row becomes a key
@@ -373,6 +424,38 @@ int mla_indexer_fp8(int32_t num_heads, int32_t head_dim, int32_t page_size, int3
                     int32_t block_table_stride, const uint32_t* cache_lens, int32_t mask, int32_t window,
                     int32_t top_k, int32_t* output_indices, double* output_scores, uint32_t flags,
                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* The writer of the indexer's inputs.  Token t of request b at pos = cache_lens[b] - qlen + i
+ * brings its index key k (D values) and, if q is given, its index queries (H heads of D):
+ *   k = bf16( (k - mean) / sqrt(var + epsilon) * k_norm_gamma + k_norm_beta )
+ *       (LayerNorm over D, var = mean((k - mean)^2); left out if k_norm_gamma is NULL)
+ *   the last rope_dim values of k and of every head of q turned by freqs_cis[pos] as in
+ *       mla_branch_prologue, rounded once to bf16 (left out if freqs_cis is NULL)
+ *   e4m3 codes of each row, scale = the least 2^e with max <= 448 * 2^e (1 for zeros; a row that
+ *       holds a NaN or an infinity gets NaN codes)
+ *   cache row at pos of request b = k's codes, k_scales[row] = its scale;
+ *   q_codes, q_scales[t, h] = scale * q_weight[t, h]        (q_weight NULL: the scale)
+ * so that mla_indexer_fp8(q_codes, q_scales, k_cache, k_scales) ranks keys by the weighted sum of
+ * the heads' products.
+ *   k_new          bf16 [T, k_new_stride], the first head_dim of each row are used; stride in
+ *                  elements, >= head_dim, a multiple of 8
+ *   q              bf16 [T, H, D] or NULL (num_heads is then ignored); q_codes e4m3 [T, H, D] and
+ *                  q_scales float [T, H] NULL exactly if q is; q_weight float [T, H] or NULL
+ *   k_cache        e4m3 [num_pages, ps, D]; k_scales float [num_pages, ps]
+ *   freqs_cis      bf16 [max_seq_len, rope_dim] or NULL (rope_dim and max_seq_len then ignored)
+ *   k_norm_gamma, k_norm_beta   bf16 [D], both or neither
+ *   flags, workspace   as mla_branch_prologue
+ * head_dim is a multiple of 8 up to 256, rope_dim a multiple of 8 up to head_dim; k_new, q, q_codes,
+ * k_cache, freqs_cis, k_norm_gamma and k_norm_beta are 16-byte aligned.  Padding tokens
+ * (t >= input_row_offsets[B]), tokens out of range (position outside the block table or
+ * [0, max_seq_len), page id outside [0, num_pages)) and tokens that share a row: as mla_cache_append. */
+int mla_indexer_append(int32_t num_heads, int32_t head_dim, int32_t rope_dim, int32_t page_size, int32_t num_pages,
+                       const void* k_new, int64_t k_new_stride, const uint32_t* input_row_offsets, int32_t batch,
+                       int32_t total_q, const void* q, const float* q_weight, void* q_codes, float* q_scales,
+                       void* k_cache, float* k_scales, const int32_t* block_table, int32_t block_table_stride,
+                       const uint32_t* cache_lens, const void* freqs_cis, int32_t max_seq_len, const void* k_norm_gamma,
+                       const void* k_norm_beta, float epsilon, uint32_t flags, void* workspace, size_t workspace_bytes,
+                       void* stream);
 
 /* Mean per-kernel device durations (milliseconds) over the calls on the current
  * device that set MLA_FLAG_KERNEL_TIMING since the previous read (at most the

@@ -13,6 +13,9 @@ Entry points (same names as the C ABI):
   mla_cache_append      new latent rows into a bf16, e4m3 or e2m1 cache (RMSNorm, RoPE, codes); RoPE on q
   mla_branch_prologue   RoPE on q and the new cache rows, RMSNorm of their latent part
   mla_prefill_paged     many query tokens a request, expanded form (also _fp8, _fp4)
+  mla_cache_read        cache rows of any format back as bf16 values
+  mla_rmsnorm_quant     residual addition, RMSNorm and 8-bit codes (e4m3, int8) of activations
+  mla_indexer_append    the indexer's keys (LayerNorm, RoPE, e4m3) into its paged cache, its queries as codes
   mla_indexer_fp8       top-k cache rows per query token by FP8 index scores (sparse input)
 """
 from __future__ import annotations
@@ -25,13 +28,15 @@ import torch
 
 from . import _lib
 from ._lib import (MLA_FLAG_DEBUG_CHECKS, MLA_FLAG_KERNEL_TIMING, MLA_FLAG_FOLD_PAIRS, MLA_FLAG_PER_TOKEN,
-                   MLA_CACHE_BF16, MLA_CACHE_E2M1, MLA_CACHE_E4M3, MLA_MASK_CAUSAL, MLA_MASK_NULL,
+                   MLA_CACHE_BF16, MLA_CACHE_E2M1, MLA_CACHE_E4M3, MLA_CODES_BF16, MLA_CODES_E4M3, MLA_CODES_INT8,
+                   MLA_MASK_CAUSAL, MLA_MASK_NULL,
                    MLA_MASK_SLIDING_WINDOW_CAUSAL, MlaDims, MlaError, MlaOpts, kernel_times)
 
 __all__ = ["mla_decode_paged", "mla_decode_paged_fp8", "mla_decode_paged_fp4", "mla_decode_sparse",
            "mla_branch_prologue", "mla_cache_append", "mla_cache_row_bytes", "mla_indexer_fp8",
            "mla_prefill_paged", "mla_prefill_paged_fp8", "mla_prefill_paged_fp4", "mla_prefill_workspace_size",
-           "MLA_CACHE_BF16", "MLA_CACHE_E4M3", "MLA_CACHE_E2M1",
+           "mla_cache_read", "mla_rmsnorm_quant", "mla_indexer_append",
+           "MLA_CACHE_BF16", "MLA_CACHE_E4M3", "MLA_CACHE_E2M1", "MLA_CODES_BF16", "MLA_CODES_E4M3", "MLA_CODES_INT8",
            "mla_decode_workspace_size", "MlaDims", "MlaOpts", "MlaError", "MLA_MASK_NULL",
            "MLA_MASK_CAUSAL", "MLA_MASK_SLIDING_WINDOW_CAUSAL", "library_path", "kernel_times"]
 
@@ -288,6 +293,138 @@ def mla_cache_append(kv_new, input_row_offsets, kv_pool, block_table, cache_lens
           MLA_FLAG_DEBUG_CHECKS if debug else 0, _ptr(workspace, "workspace", None, dev),
           workspace.numel() * workspace.element_size(), ctypes.c_void_p(s.cuda_stream))
     return kv_pool, q_out
+
+
+def _row_strided(t, name, shape):
+    """Pointer and row stride of a bf16 CUDA tensor whose rows may lie apart (a slice of a wider one)."""
+    if t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise TypeError(f"{name} must be a bf16 CUDA tensor")
+    if t.dim() != 2 or t.shape[1] != shape or (t.shape[0] > 0 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, {shape}] with unit stride along a row")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else -(-shape // 8) * 8
+
+
+def _sized(t, name, n):
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values")
+
+
+def mla_cache_read(input_row_offsets, kv_pool, block_table, cache_lens, *, kv_lora_rank: int, qk_rope: int,
+                   page_size: int, total_rows: Optional[int] = None, cache_format: int = MLA_CACHE_BF16, kv_scales=None,
+                   out=None, debug: bool = False, workspace=None, stream=None):
+    """Cache rows back as bf16 values: the last input_row_offsets[b+1] - input_row_offsets[b] of request b's
+    cache_lens[b] tokens.  total_rows (host) is input_row_offsets' last value; it may be left out where `out`
+    bf16 [total_rows, L+R] is given.  Returns out."""
+    dev = kv_pool.device
+    L, R = int(kv_lora_rank), int(qk_rope)
+    dims = MlaDims(num_heads=1, qk_nope=0, qk_rope=R, kv_lora_rank=L, v_head=1, page_size=page_size,
+                   num_pages=_pages(kv_pool, page_size, mla_cache_row_bytes(cache_format, L, R)))
+    _sized(kv_scales, "kv_scales", dims.num_pages * page_size)
+    B, offsets, table, table_stride, lens = _tables(input_row_offsets, block_table, cache_lens, dev)
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if out is None:
+        if total_rows is None:
+            raise ValueError("total_rows or out must be given")
+        out = _buffer((total_rows, L + R), torch.bfloat16, dev, stream, returned=True)
+    elif out.dim() != 2 or out.shape[1] != L + R or (total_rows is not None and out.shape[0] != total_rows):
+        raise ValueError("out must be [total_rows, L+R]")
+    if workspace is None:
+        workspace = _buffer(256, torch.uint8, dev, stream) if debug else _unread_status(dev, s)
+    _call("mla_cache_read", dev, ctypes.byref(dims), int(cache_format), offsets, B, out.shape[0],
+          _ptr(kv_pool, "kv_pool", None, dev), _ptr(kv_scales, "kv_scales", (torch.float32,), dev), table, table_stride,
+          lens, _ptr(out, "out", _BF16, dev), MLA_FLAG_DEBUG_CHECKS if debug else 0,
+          _ptr(workspace, "workspace", None, dev), workspace.numel() * workspace.element_size(),
+          ctypes.c_void_p(s.cuda_stream))
+    return out
+
+
+_CODES = {MLA_CODES_BF16: torch.bfloat16, MLA_CODES_E4M3: torch.float8_e4m3fn, MLA_CODES_INT8: torch.int8}
+
+
+def mla_rmsnorm_quant(x, gamma=None, *, epsilon: float = 1e-6, code_format: int = MLA_CODES_E4M3, residual=None,
+                      residual_out=None, y_out=None, codes_out=None, scales_out=None, stream=None):
+    """Rows x bf16 [T, D] (rows may be strided) plus residual bf16 [T, D], normalised by gamma bf16 [D] (as they
+    are without it), as e4m3 or int8 codes with one fp32 scale a row.  The sum goes to residual_out (in place if
+    it is None); y_out bf16 [T, D] receives the normalised rows.  Returns (codes [T, D], scales [T],
+    residual_out or None); for MLA_CODES_BF16 (y_out, None, residual_out or None)."""
+    dev = x.device
+    if code_format not in _CODES:
+        raise ValueError(f"unknown code format {code_format}")
+    if x.dim() != 2:
+        raise ValueError("x must be [T, D]")
+    T, D = x.shape
+    px, stride = _row_strided(x, "x", D)
+    if residual is not None:
+        residual_out = residual if residual_out is None else residual_out
+    elif residual_out is not None:
+        raise ValueError("residual_out without residual")
+    coded = code_format != MLA_CODES_BF16
+    if coded:
+        if codes_out is None:
+            codes_out = _buffer((T, D), _CODES[code_format], dev, stream, returned=True)
+        if scales_out is None:
+            scales_out = _buffer((T,), torch.float32, dev, stream, returned=True)
+    elif codes_out is not None or scales_out is not None:
+        raise ValueError("MLA_CODES_BF16 writes no codes")
+    elif y_out is None:
+        y_out = _buffer((T, D), torch.bfloat16, dev, stream, returned=True)
+    for t, name in ((residual, "residual"), (residual_out, "residual_out"), (y_out, "y_out"), (codes_out, "codes_out")):
+        if t is not None and tuple(t.shape) != (T, D):
+            raise ValueError(f"{name} must be [T, D]")
+    _sized(gamma, "gamma", D)
+    _sized(scales_out, "scales_out", T)
+    _call("mla_rmsnorm_quant", dev, code_format, T, D, px, stride, _ptr(residual, "residual", _BF16, dev),
+          _ptr(residual_out, "residual_out", _BF16, dev), _ptr(gamma, "gamma", _BF16, dev), float(epsilon),
+          _ptr(y_out, "y_out", _BF16, dev), _ptr(codes_out, "codes_out", (_CODES[code_format], torch.uint8), dev),
+          _ptr(scales_out, "scales_out", (torch.float32,), dev), _stream(stream, dev))
+    return (codes_out, scales_out, residual_out) if coded else (y_out, None, residual_out)
+
+
+def mla_indexer_append(k_new, input_row_offsets, k_cache, k_scales, block_table, cache_lens, *, page_size: int,
+                       freqs_cis=None, k_norm_gamma=None, k_norm_beta=None, epsilon: float = 1e-6, q=None,
+                       q_weight=None, q_codes=None, q_scales=None, debug: bool = False, workspace=None, stream=None):
+    """The inputs of mla_indexer_fp8: keys k_new bf16 [T, D] (rows may be strided) through LayerNorm
+    (k_norm_gamma, k_norm_beta bf16 [D]) and RoPE of their last R values (freqs_cis bf16 [max_seq_len, R]) into the
+    e4m3 cache k_cache (page-major rows of D) with k_scales f32 [rows]; queries q bf16 [T, H, D] turned and coded,
+    their scales times q_weight f32 [T, H].  Returns (q_codes e4m3 [T, H, D], q_scales f32 [T, H]) or (None, None)."""
+    dev = k_new.device
+    if k_new.dim() != 2:
+        raise ValueError("k_new must be [T, D]")
+    T, D = k_new.shape
+    pk, stride = _row_strided(k_new, "k_new", D)
+    f8 = (torch.uint8, torch.float8_e4m3fn)
+    R, max_len = (freqs_cis.shape[1], freqs_cis.shape[0]) if freqs_cis is not None else (0, 0)
+    num_pages = _pages(k_cache, page_size, D)
+    _sized(k_scales, "k_scales", num_pages * page_size)
+    _sized(k_norm_gamma, "k_norm_gamma", D)
+    _sized(k_norm_beta, "k_norm_beta", D)
+    H = 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D:
+            raise ValueError("q must be [T, H, D]")
+        H = q.shape[1]
+        if q_codes is None:
+            q_codes = _buffer((T, H, D), torch.float8_e4m3fn, dev, stream, returned=True)
+        if q_scales is None:
+            q_scales = _buffer((T, H), torch.float32, dev, stream, returned=True)
+        _sized(q_codes, "q_codes", T * H * D)
+        _sized(q_scales, "q_scales", T * H)
+        _sized(q_weight, "q_weight", T * H)
+    elif q_weight is not None or q_codes is not None or q_scales is not None:
+        raise ValueError("q_weight, q_codes or q_scales without q")
+    B, offsets, table, table_stride, lens = _tables(input_row_offsets, block_table, cache_lens, dev)
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if workspace is None:
+        workspace = _buffer(256, torch.uint8, dev, stream) if debug else _unread_status(dev, s)
+    f32 = (torch.float32,)
+    _call("mla_indexer_append", dev, H, D, R, page_size, num_pages, pk, stride, offsets, B, T, _ptr(q, "q", _BF16, dev),
+          _ptr(q_weight, "q_weight", f32, dev), _ptr(q_codes, "q_codes", f8, dev), _ptr(q_scales, "q_scales", f32, dev),
+          _ptr(k_cache, "k_cache", f8, dev), _ptr(k_scales, "k_scales", f32, dev), table, table_stride, lens,
+          _ptr(freqs_cis, "freqs_cis", _BF16, dev), max_len, _ptr(k_norm_gamma, "k_norm_gamma", _BF16, dev),
+          _ptr(k_norm_beta, "k_norm_beta", _BF16, dev), float(epsilon), MLA_FLAG_DEBUG_CHECKS if debug else 0,
+          _ptr(workspace, "workspace", None, dev), workspace.numel() * workspace.element_size(),
+          ctypes.c_void_p(s.cuda_stream))
+    return q_codes, q_scales
 
 
 def mla_decode_paged_fp4(q, input_row_offsets, kv_pool_fp4, block_table, cache_lens, w_uk, w_uv, *,

@@ -28,6 +28,9 @@ MLA_FLAG_PER_TOKEN = 8
 MLA_CACHE_BF16 = 0
 MLA_CACHE_E4M3 = 1
 MLA_CACHE_E2M1 = 2
+MLA_CODES_BF16 = 0
+MLA_CODES_E4M3 = 1
+MLA_CODES_INT8 = 2
 KERNEL_NAMES = ("absorb_w_uk", "decode_splitkv", "w_uv")
 
 EXPORTED = ("mla_decode_workspace_size", "mla_decode_paged", "mla_decode_paged_fp8",
@@ -35,6 +38,7 @@ EXPORTED = ("mla_decode_workspace_size", "mla_decode_paged", "mla_decode_paged_f
             "mla_cache_append", "mla_prefill_workspace_size", "mla_prefill_paged", "mla_prefill_paged_fp8",
             "mla_prefill_paged_fp4",
             "mla_indexer_workspace_size", "mla_indexer_fp8",
+            "mla_cache_read", "mla_rmsnorm_quant", "mla_indexer_append",
             "mla_debug_wait_selftest",
             "mla_status_string")
 
@@ -77,6 +81,14 @@ _SIGS = {
     "mla_prefill_paged_fp4": [_P(MlaDims), _P(MlaOpts), c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p,
                               c_int32, c_void_p, ctypes.c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                               c_size_t, c_void_p],
+    "mla_cache_read": [_P(MlaDims), c_int32, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int32,
+                       c_void_p, c_void_p, c_uint32, c_void_p, c_size_t, c_void_p],
+    "mla_rmsnorm_quant": [c_int32, c_int32, c_int32, c_void_p, ctypes.c_int64, c_void_p, c_void_p, c_void_p, c_float,
+                          c_void_p, c_void_p, c_void_p, c_void_p],
+    "mla_indexer_append": [c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, ctypes.c_int64, c_void_p, c_int32,
+                           c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32,
+                           c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_float, c_uint32, c_void_p, c_size_t,
+                           c_void_p],
     "mla_decode_sparse": [_P(MlaDims), _P(MlaOpts), c_void_p, c_void_p, c_int32, c_int32, c_void_p,
                           c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                           c_void_p, c_size_t, c_void_p],

@@ -492,6 +492,100 @@ int mla_cache_append(const mla_dims_t* dims, int32_t cache_format, const void* k
   return MLA_OK;
 }
 
+int mla_cache_read(const mla_dims_t* dims, int32_t cache_format, const uint32_t* input_row_offsets, int32_t batch,
+                   int32_t total_rows, const void* kv_pool, const float* kv_scales, const int32_t* block_table,
+                   int32_t block_table_stride, const uint32_t* cache_lens, void* rows_out, uint32_t flags,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dims || dims->qk_rope < 1 || dims->kv_lora_rank < 1 || dims->page_size < 1 || dims->num_pages < 1)
+    return MLA_ERR_INVALID_ARG;
+  if (cache_format < MLA_CACHE_BF16 || cache_format > MLA_CACHE_E2M1) return MLA_ERR_INVALID_ARG;
+  if (dims->kv_lora_rank % 32 != 0 || dims->kv_lora_rank > 512 || dims->qk_rope % 8 != 0 || dims->qk_rope > 128)
+    return MLA_ERR_UNSUPPORTED;
+  if ((int64_t)dims->num_pages * dims->page_size > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if (batch < 1 || total_rows < 0 || block_table_stride < 1 || (flags & ~MLA_FLAG_DEBUG_CHECKS))
+    return MLA_ERR_INVALID_ARG;
+  if ((!rows_out && total_rows > 0) || !input_row_offsets || !kv_pool || !block_table || !cache_lens || !workspace)
+    return MLA_ERR_INVALID_ARG;
+  if ((cache_format == MLA_CACHE_E4M3) != (kv_scales != nullptr)) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(kv_pool) || !aligned16(rows_out)) return MLA_ERR_INVALID_ARG;
+  if (workspace_bytes < sizeof(PlanHeader) || !aligned16(workspace)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  PlanHeader* hdr = static_cast<PlanHeader*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((flags & MLA_FLAG_DEBUG_CHECKS) && cudaMemsetAsync(hdr, 0, sizeof(PlanHeader), s) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  const cudaError_t e = launch_cache_read(*dims, cache_format, input_row_offsets, batch, total_rows, kv_pool, kv_scales,
+                                          block_table, block_table_stride, cache_lens, rows_out, hdr, s);
+  if (e != cudaSuccess) {
+    std::fprintf(stderr, "mla_cache_read: %s\n", cudaGetErrorString(e));
+    return MLA_ERR_CUDA;
+  }
+  if (flags & MLA_FLAG_DEBUG_CHECKS) return device_status(hdr, s);
+  return MLA_OK;
+}
+
+int mla_indexer_append(int32_t num_heads, int32_t head_dim, int32_t rope_dim, int32_t page_size, int32_t num_pages,
+                       const void* k_new, int64_t k_new_stride, const uint32_t* input_row_offsets, int32_t batch,
+                       int32_t total_q, const void* q, const float* q_weight, void* q_codes, float* q_scales,
+                       void* k_cache, float* k_scales, const int32_t* block_table, int32_t block_table_stride,
+                       const uint32_t* cache_lens, const void* freqs_cis, int32_t max_seq_len, const void* k_norm_gamma,
+                       const void* k_norm_beta, float epsilon, uint32_t flags, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  if ((q && num_heads < 1) || head_dim < 1 || page_size < 1 || num_pages < 1 || batch < 1 || total_q < 0 ||
+      block_table_stride < 1 || k_new_stride < head_dim || k_new_stride % 8 != 0 || (flags & ~MLA_FLAG_DEBUG_CHECKS))
+    return MLA_ERR_INVALID_ARG;
+  if (freqs_cis && (rope_dim < 1 || rope_dim > head_dim || max_seq_len < 1)) return MLA_ERR_INVALID_ARG;
+  if (head_dim % 8 != 0 || head_dim > 256 || (freqs_cis && rope_dim % 8 != 0)) return MLA_ERR_UNSUPPORTED;
+  if ((int64_t)num_pages * page_size > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if (indexer_append_blocks(num_heads, head_dim, total_q, q != nullptr) > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if ((!k_new && total_q > 0) || !input_row_offsets || !k_cache || !k_scales || !block_table || !cache_lens || !workspace)
+    return MLA_ERR_INVALID_ARG;
+  if ((q != nullptr) != (q_codes != nullptr) || (q != nullptr) != (q_scales != nullptr) || (q_weight && !q) ||
+      (k_norm_gamma != nullptr) != (k_norm_beta != nullptr))
+    return MLA_ERR_INVALID_ARG;
+  for (const void* p : {k_new, q, static_cast<const void*>(q_codes), static_cast<const void*>(k_cache), freqs_cis,
+                        k_norm_gamma, k_norm_beta})
+    if (!aligned16(p)) return MLA_ERR_INVALID_ARG;
+  if (!(epsilon >= 0.f)) return MLA_ERR_INVALID_ARG;
+  if (workspace_bytes < sizeof(PlanHeader) || !aligned16(workspace)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  PlanHeader* hdr = static_cast<PlanHeader*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((flags & MLA_FLAG_DEBUG_CHECKS) && cudaMemsetAsync(hdr, 0, sizeof(PlanHeader), s) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  const cudaError_t e = launch_indexer_append(num_heads, head_dim, rope_dim, page_size, num_pages, k_new, k_new_stride,
+                                              input_row_offsets, batch, total_q, q, q_weight, q_codes, q_scales, k_cache,
+                                              k_scales, block_table, block_table_stride, cache_lens, freqs_cis,
+                                              max_seq_len, k_norm_gamma, k_norm_beta, epsilon, hdr, s);
+  if (e != cudaSuccess) {
+    std::fprintf(stderr, "mla_indexer_append: %s\n", cudaGetErrorString(e));
+    return MLA_ERR_CUDA;
+  }
+  if (flags & MLA_FLAG_DEBUG_CHECKS) return device_status(hdr, s);
+  return MLA_OK;
+}
+
+int mla_rmsnorm_quant(int32_t code_format, int32_t rows, int32_t width, const void* x, int64_t x_stride,
+                      const void* residual, void* residual_out, const void* gamma, float epsilon, void* y_out,
+                      void* codes_out, float* scales_out, void* stream) {
+  if (code_format < MLA_CODES_BF16 || code_format > MLA_CODES_INT8 || rows < 0 || width < 1 || x_stride < width ||
+      x_stride % 8 != 0 || !(epsilon >= 0.f))
+    return MLA_ERR_INVALID_ARG;
+  if (width % 8 != 0 || width > kMaxRowWidth) return MLA_ERR_UNSUPPORTED;
+  const bool coded = code_format != MLA_CODES_BF16;
+  if ((residual != nullptr) != (residual_out != nullptr)) return MLA_ERR_INVALID_ARG;
+  if (rows > 0 && (!x || coded != (codes_out != nullptr) || coded != (scales_out != nullptr) || (!coded && !y_out)))
+    return MLA_ERR_INVALID_ARG;
+  for (const void* p : {x, residual, static_cast<const void*>(residual_out), gamma, static_cast<const void*>(y_out),
+                        static_cast<const void*>(codes_out)})
+    if (!aligned16(p)) return MLA_ERR_INVALID_ARG;
+  const cudaError_t e = launch_rmsnorm(code_format, rows, width, x, x_stride, residual, residual_out, gamma, epsilon,
+                                       y_out, codes_out, scales_out, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) {
+    std::fprintf(stderr, "mla_rmsnorm_quant: %s\n", cudaGetErrorString(e));
+    return MLA_ERR_CUDA;
+  }
+  return MLA_OK;
+}
+
 namespace {
 // K and V boxes of a pass: all heads if they fit this, else as many as do.
 constexpr size_t kPrefillPassBytes = size_t(4) << 30;

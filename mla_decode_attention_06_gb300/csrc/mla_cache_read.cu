@@ -1,0 +1,167 @@
+// mla_cache_read: rows of the paged latent cache as bf16 values, request after request: token t of
+// request b at pos = cache_len - n + i (the addressing of mla_cache_append) gives
+//
+//   out[t] = [ bf16(code * scale) (L) ; k_rope (R) ]
+//
+// e2m1 codes times powers of two are bf16 values; an e4m3 code times a row scale has up to 28
+// bits, so the product is rounded to odd (mla_rows.cuh) before it is rounded to bf16, once in all.
+//
+// Layout.  A warp takes `rows_per_warp` consecutive tokens.  Its lanes look their tokens up at
+// once, a lane a token (request by bisection, length, page), so the chain of dependent reads is
+// paid once a warp and not once a row; then the rows are copied, two at a time, 16 bytes of output
+// (8 values) a lane, all loads of the two out before the first is used.  Bound by HBM.
+#include <cuda_fp4.h>
+
+#include "mla_kernels.cuh"
+#include "mla_rows.cuh"
+
+namespace mla {
+namespace rd {
+
+using namespace rows;
+
+constexpr int kWarps = 4;
+constexpr int kTogether = 2;         // rows in flight in a warp
+constexpr int kMaxPieces = 3;        // 8-value pieces of a row a lane: L + R <= 768
+
+struct Args {
+  int L, R, ps, num_pages, B, T, bt_stride, per_warp;
+  long long row_bytes;
+  const uint8_t* pool;
+  const float* scales;
+  const uint32_t* offsets;
+  const uint32_t* cache_lens;
+  const int32_t* block_table;
+  __nv_bfloat16* out;
+  PlanHeader* hdr;
+};
+
+// One lane: the cache row of token t, -1 if there is none to read.
+__device__ __forceinline__ long long find(const Args& a, int t) {
+  if (t >= a.T || (uint32_t)t >= a.offsets[a.B]) return -1;
+  int lo = 0, n = a.B;   // the request is the last b with offsets[b] <= t
+  while (n > 1) {
+    const int half = n >> 1;
+    const bool up = a.offsets[lo + half] <= (uint32_t)t;
+    lo += up ? half : 0;
+    n = up ? n - half : half;
+  }
+  const uint32_t qb = a.offsets[lo], qe = a.offsets[lo + 1];
+  const long long pos = (long long)a.cache_lens[lo] - qe + t;
+  if (qb <= (uint32_t)t && (uint32_t)t < qe && pos >= 0 && pos < (long long)a.bt_stride * a.ps) {
+    const int page = a.block_table[(size_t)lo * a.bt_stride + pos / a.ps];
+    if (page >= 0 && page < a.num_pages) return (long long)page * a.ps + pos % a.ps;
+  }
+  atomicOr(&a.hdr->status, kDeviceCheckFailed);
+  return -1;
+}
+
+// x * s rounded to odd.
+__device__ __forceinline__ float mul_odd(float x, float s) {
+  const float down = __fmul_rd(x, s), up = __fmul_ru(x, s);
+  return __float_as_uint(down) & 1u ? down : up;
+}
+
+// What a lane holds of a row: 8 values of the latent part as they are stored, or of the rope part.
+template <int kFmt>
+struct Piece {
+  uint4 raw;
+  float scale;
+};
+
+template <int kFmt>
+__device__ __forceinline__ void load(const Args& a, long long row, int piece, Piece<kFmt>& p) {
+  const uint8_t* src = a.pool + row * a.row_bytes;
+  const int latent = a.L / 8;
+  if (kFmt == MLA_CACHE_BF16 || piece >= latent) {
+    p.raw = *reinterpret_cast<const uint4*>(src + (a.row_bytes - 2 * (a.L + a.R)) + 16 * piece);
+  } else if (kFmt == MLA_CACHE_E4M3) {
+    const uint2 v = *reinterpret_cast<const uint2*>(src + 8 * piece);
+    p.raw.x = v.x;
+    p.raw.y = v.y;
+    p.scale = a.scales[row];
+  } else {
+    p.raw.x = *reinterpret_cast<const uint32_t*>(src + 4 * piece);
+    const uint8_t e = src[a.L / 2 + piece / 4];   // 2^(e - 127), 255 = NaN
+    p.scale = __uint_as_float(e == 255 ? 0x7FC00000u : e == 0 ? 0x00400000u : (uint32_t)e << 23);
+  }
+}
+
+template <int kFmt>
+__device__ __forceinline__ uint4 values(const Args& a, int piece, const Piece<kFmt>& p) {
+  if (kFmt == MLA_CACHE_BF16 || piece >= a.L / 8) return p.raw;
+  uint32_t o[4] = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kFmt == MLA_CACHE_E4M3) {
+      const uint32_t two = ((i < 2 ? p.raw.x : p.raw.y) >> (16 * (i & 1))) & 0xFFFFu;
+      const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
+      o[i] = pack(mul_odd(v.x, p.scale), mul_odd(v.y, p.scale));
+    } else if constexpr (kFmt == MLA_CACHE_E2M1) {
+      const uint32_t two = (p.raw.x >> (8 * i)) & 0xFFu;
+      const float2 v = __half22float2(__half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)two, __NV_E2M1)));
+      o[i] = pack(v.x * p.scale, v.y * p.scale);
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int kFmt>
+__global__ void __launch_bounds__(32 * kWarps) read_kernel(const Args a) {
+  const int lane = threadIdx.x & 31;
+  const long long t0 = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * a.per_warp;
+  if (t0 >= a.T) return;
+  const long long mine = lane < a.per_warp ? find(a, (int)min(t0 + lane, (long long)a.T)) : -1;
+  const int pieces = (a.L + a.R) / 8;
+  for (int i = 0; i < a.per_warp; i += kTogether) {
+    Piece<kFmt> p[kTogether][kMaxPieces];
+    long long row[kTogether];
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j) {
+      row[j] = __shfl_sync(0xffffffffu, mine, (i + j) & 31);
+      if (i + j >= a.per_warp) row[j] = -1;
+#pragma unroll
+      for (int c = 0; c < kMaxPieces; ++c)
+        if (row[j] >= 0 && lane + 32 * c < pieces) load<kFmt>(a, row[j], lane + 32 * c, p[j][c]);
+    }
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j)
+#pragma unroll
+      for (int c = 0; c < kMaxPieces; ++c)
+        if (row[j] >= 0 && lane + 32 * c < pieces)
+          reinterpret_cast<uint4*>(a.out + (t0 + i + j) * (a.L + a.R))[lane + 32 * c] =
+              values<kFmt>(a, lane + 32 * c, p[j][c]);
+  }
+}
+
+}  // namespace rd
+
+cudaError_t launch_cache_read(const mla_dims_t& d, int fmt, const uint32_t* offsets, int B, int T, const void* pool,
+                              const float* scales, const int32_t* block_table, int bt_stride,
+                              const uint32_t* cache_lens, void* out, PlanHeader* hdr, cudaStream_t s) {
+  if (T == 0) return cudaSuccess;
+  rd::Args a{};
+  a.L = d.kv_lora_rank;
+  a.R = d.qk_rope;
+  a.ps = d.page_size;
+  a.num_pages = d.num_pages;
+  a.B = B;
+  a.T = T;
+  a.bt_stride = bt_stride;
+  a.row_bytes = cache_row_bytes(fmt, a.L, a.R);
+  a.pool = static_cast<const uint8_t*>(pool);
+  a.scales = scales;
+  a.offsets = offsets;
+  a.cache_lens = cache_lens;
+  a.block_table = block_table;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.hdr = hdr;
+  a.per_warp = 8;
+  const unsigned blocks = (unsigned)(((long long)T + rd::kWarps * a.per_warp - 1) / (rd::kWarps * a.per_warp));
+  if (fmt == MLA_CACHE_BF16) rd::read_kernel<MLA_CACHE_BF16><<<blocks, 32 * rd::kWarps, 0, s>>>(a);
+  else if (fmt == MLA_CACHE_E4M3) rd::read_kernel<MLA_CACHE_E4M3><<<blocks, 32 * rd::kWarps, 0, s>>>(a);
+  else rd::read_kernel<MLA_CACHE_E2M1><<<blocks, 32 * rd::kWarps, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace mla

@@ -1,0 +1,226 @@
+// mla_indexer_append: the writer of mla_indexer_fp8's inputs.  For token t of request b at
+// pos = cache_len - qlen + i, with the new index key k (D values) and the index queries q (H heads):
+//
+//   k = bf16( (k - mean) / sqrt(var + eps) * gamma + beta )      (with a norm; LayerNorm over D)
+//   k, q: the last R values turned by freqs_cis[pos], bf16        (with freqs_cis)
+//   e4m3: s = the least 2^e with amax <= 448 s, codes of the exact quotients, a scale a row and head
+//   cache row at pos: k's codes and s;  q_codes, q_scales = s * q_weight
+//
+// Arithmetic as in mla_append.cu: rotations rounded once, codes of exact quotients; the LayerNorm of
+// the one key a token is fp64 (its work is 1 / H of the queries').
+//
+// Layout.  D / 8 neighbouring lanes hold a row, 8 values (16 bytes) each, so that a row's largest
+// magnitude is a few shuffles away and a warp reads and writes whole rows; a block takes one token's
+// heads, four rows a lane group with all loads out before the token's place is looked up.  Keys
+// have blocks of their own.  Bound by HBM for prompts, by the chain of dependent reads for a step.
+#include "mla_kernels.cuh"
+#include "mla_rows.cuh"
+
+namespace mla {
+namespace ia {
+
+using namespace rows;
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;   // rows of queries a lane group
+
+struct Args {
+  int D, H, R, ps, num_pages, B, T, bt_stride;
+  int lanes;                       // of a row: 8, 16 or 32, the first D / 8 of them used
+  int key_blocks, q_blocks;        // blocks of keys; blocks per token of queries
+  long long max_seq_len, k_stride;
+  double eps;
+  const __nv_bfloat16* k_new;      // [T, >= D]
+  const __nv_bfloat16* q;          // [T, H, D]
+  const float* q_weight;           // [T, H] or NULL
+  uint8_t* q_codes;                // [T, H, D]
+  float* q_scales;                 // [T, H]
+  uint8_t* k_cache;                // [pages, ps, D]
+  float* k_scales;                 // [pages, ps]
+  const uint32_t* offsets;
+  const uint32_t* cache_lens;
+  const int32_t* block_table;
+  const __nv_bfloat16* freqs;      // [max_seq_len, R] or NULL
+  const __nv_bfloat16* gamma;      // [D] or NULL
+  const __nv_bfloat16* beta;
+  PlanHeader* hdr;
+};
+
+// Codes and scale of a row whose values x (8 a lane, bf16 pairs) lie on `lanes` neighbours.  Whole warp.
+__device__ __forceinline__ uint2 coded(const Args& a, uint4 x, float& scale) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) amax = max(amax, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+  for (int o = a.lanes / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const bool bad = amax >= 0x7F80u;   // a NaN or an infinity: every code a NaN
+  const int e = bad ? 0 : scale_exponent(amax, 8, -126, 127);
+  const float rs = pow2(-e);
+  scale = pow2(e);
+  uint32_t two[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    two[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo_f(w[i]) * rs, hi_f(w[i]) * rs), __NV_SATFINITE, __NV_E4M3);
+  if (bad) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  return make_uint2(two[0] | (two[1] << 16), two[2] | (two[3] << 16));
+}
+
+// The eight values at column `col` of a row, turned if they are of its last R.
+__device__ __forceinline__ uint4 turned(const Args& a, uint4 x, int col, long long pos) {
+  if (a.R == 0 || col < a.D - a.R || col >= a.D) return x;
+  const uint4 f = *reinterpret_cast<const uint4*>(a.freqs + pos * a.R + (col - (a.D - a.R)));
+  uint32_t lost = 0;
+  const uint4 y = turn(x, f, lost);
+  return lost ? turn_wide(x, f) : y;
+}
+
+// LayerNorm of a key, its values on `lanes` neighbours, in fp64; as bf16 pairs.  Whole warp.
+__device__ __forceinline__ uint4 layer_norm(const Args& a, uint4 x, int col, bool have) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  double v[8], sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = i & 1 ? hi_f(w[i / 2]) : lo_f(w[i / 2]);
+    sum += v[i];
+  }
+  for (int o = a.lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const double mean = sum / (double)a.D;
+  sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] -= mean;
+    sum += have ? v[i] * v[i] : 0.0;
+  }
+  for (int o = a.lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const double inv = rsqrt(sum / (double)a.D + a.eps);
+  uint4 gv = make_uint4(0, 0, 0, 0), bv = gv;
+  if (have) {
+    gv = *reinterpret_cast<const uint4*>(a.gamma + col);
+    bv = *reinterpret_cast<const uint4*>(a.beta + col);
+  }
+  const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w}, b[4] = {bv.x, bv.y, bv.z, bv.w};
+  uint32_t y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    y[i] = pack(double_odd(v[2 * i] * inv * (double)lo_f(g[i]) + (double)lo_f(b[i])),
+                double_odd(v[2 * i + 1] * inv * (double)hi_f(g[i]) + (double)hi_f(b[i])));
+  return have ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(0, 0, 0, 0);
+}
+
+// Whole warp: the keys of 32 / lanes tokens.
+__device__ __forceinline__ void new_keys(const Args& a, long long t0, int lane) {
+  const int groups = 32 / a.lanes, sub = lane % a.lanes, col = 8 * sub;
+  const long long t = t0 + lane / a.lanes;
+  const bool have = t < a.T && col < a.D;
+  uint4 x = make_uint4(0, 0, 0, 0);
+  if (have) x = *reinterpret_cast<const uint4*>(a.k_new + t * a.k_stride + col);
+  Place p{-1, 0};
+  for (int i = 0; i < groups; ++i) {
+    if (t0 + i >= a.T) break;
+    const Place q = locate(a, (int)(t0 + i), lane);
+    if (lane / a.lanes == i) p = q;
+  }
+  if (a.gamma) x = layer_norm(a, x, col, have);
+  if (have && p.pos >= 0) x = turned(a, x, col, p.pos);
+  float s;
+  const uint2 c = coded(a, x, s);
+  if (!have || p.pos < 0) return;
+  *reinterpret_cast<uint2*>(a.k_cache + p.row * a.D + col) = c;
+  if (sub == 0) a.k_scales[p.row] = s;
+}
+
+// Heads [part * rows, ...) of token t's queries, rows = kBatch times the block's lane groups.
+__device__ __forceinline__ void queries(const Args& a, int t, int part, int lane) {
+  const int per = kThreads / a.lanes, sub = (int)threadIdx.x % a.lanes, col = 8 * sub;
+  const int h0 = part * per * kBatch + (int)threadIdx.x / a.lanes;
+  const bool used = col < a.D;
+  const size_t base = (size_t)t * a.H;
+  uint4 v[kBatch];
+  float wt[kBatch];
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) {
+    const int h = h0 + j * per;
+    v[j] = make_uint4(0, 0, 0, 0);
+    wt[j] = 1.f;
+    if (h < a.H && used) {
+      v[j] = *reinterpret_cast<const uint4*>(a.q + (base + h) * a.D + col);
+      if (a.q_weight && sub == 0) wt[j] = a.q_weight[base + h];
+    }
+  }
+  const Place p = locate(a, t, lane);
+  if (p.pos < 0) return;
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) {
+    const int h = h0 + j * per;
+    float s;
+    const uint2 c = coded(a, turned(a, v[j], col, p.pos), s);
+    if (h < a.H && used) {
+      *reinterpret_cast<uint2*>(a.q_codes + (base + h) * a.D + col) = c;
+      if (sub == 0) a.q_scales[base + h] = __fmul_rn(s, wt[j]);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) indexer_append_kernel(const Args a) {
+  const int lane = threadIdx.x & 31, blk = (int)blockIdx.x;
+  if (blk < a.key_blocks) {
+    const long long t0 = ((long long)blk * (kThreads / 32) + (threadIdx.x >> 5)) * (32 / a.lanes);
+    if (t0 < a.T) new_keys(a, t0, lane);
+  } else {
+    const int i = blk - a.key_blocks;
+    queries(a, i / a.q_blocks, i % a.q_blocks, lane);
+  }
+}
+
+int lanes_of(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
+
+}  // namespace ia
+
+long long indexer_append_blocks(int H, int D, int T, bool queries) {
+  const int per = ia::kThreads / ia::lanes_of(D);
+  return ((long long)T + per - 1) / per +
+         (queries ? (long long)T * (((long long)H + per * ia::kBatch - 1) / (per * ia::kBatch)) : 0);
+}
+
+cudaError_t launch_indexer_append(int H, int D, int R, int ps, int num_pages, const void* k_new, long long k_stride,
+                                  const uint32_t* offsets, int B, int T, const void* q, const float* q_weight,
+                                  void* q_codes, float* q_scales, void* k_cache, float* k_scales,
+                                  const int32_t* block_table, int bt_stride, const uint32_t* cache_lens,
+                                  const void* freqs, int max_seq_len, const void* gamma, const void* beta, float eps,
+                                  PlanHeader* hdr, cudaStream_t s) {
+  if (T == 0) return cudaSuccess;
+  ia::Args a{};
+  a.D = D;
+  a.H = H;
+  a.R = freqs ? R : 0;
+  a.ps = ps;
+  a.num_pages = num_pages;
+  a.B = B;
+  a.T = T;
+  a.bt_stride = bt_stride;
+  a.lanes = ia::lanes_of(D);
+  a.max_seq_len = freqs ? max_seq_len : INT64_MAX;
+  a.k_stride = k_stride;
+  a.eps = (double)eps;
+  a.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_weight = q_weight;
+  a.q_codes = static_cast<uint8_t*>(q_codes);
+  a.q_scales = q_scales;
+  a.k_cache = static_cast<uint8_t*>(k_cache);
+  a.k_scales = k_scales;
+  a.offsets = offsets;
+  a.cache_lens = cache_lens;
+  a.block_table = block_table;
+  a.freqs = static_cast<const __nv_bfloat16*>(freqs);
+  a.gamma = static_cast<const __nv_bfloat16*>(gamma);
+  a.beta = static_cast<const __nv_bfloat16*>(beta);
+  a.hdr = hdr;
+  const long long blocks = indexer_append_blocks(H, D, T, q != nullptr);
+  a.key_blocks = (int)indexer_append_blocks(H, D, T, false);
+  a.q_blocks = (int)((blocks - a.key_blocks) / T);
+  ia::indexer_append_kernel<<<(unsigned)blocks, ia::kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace mla

@@ -80,6 +80,27 @@ cudaError_t launch_append(const mla_dims_t& d, int fmt, const void* kv_new, long
                           const uint32_t* cache_lens, const void* freqs, int max_seq_len, const void* gamma,
                           float eps, PlanHeader* hdr, cudaStream_t s);
 
+// Rows of up to kMaxRowWidth bf16 values: residual, RMSNorm, 8-bit codes (mla_code_format_t).
+constexpr int kMaxRowWidth = 32768;
+cudaError_t launch_rmsnorm(int fmt, int rows, int width, const void* x, long long x_stride, const void* residual,
+                           void* residual_out, const void* gamma, float eps, void* y_out, void* codes, float* scales,
+                           cudaStream_t s);
+
+// Rows of the paged latent cache as bf16 values.
+cudaError_t launch_cache_read(const mla_dims_t& d, int fmt, const uint32_t* offsets, int B, int T, const void* pool,
+                              const float* scales, const int32_t* block_table, int bt_stride,
+                              const uint32_t* cache_lens, void* out, PlanHeader* hdr, cudaStream_t s);
+
+// The indexer's inputs: keys into the paged e4m3 cache, queries as codes; q, freqs, gamma may be NULL.
+// Blocks of its grid, at most 2^31 - 1.
+long long indexer_append_blocks(int H, int D, int T, bool queries);
+cudaError_t launch_indexer_append(int H, int D, int R, int ps, int num_pages, const void* k_new, long long k_stride,
+                                  const uint32_t* offsets, int B, int T, const void* q, const float* q_weight,
+                                  void* q_codes, float* q_scales, void* k_cache, float* k_scales,
+                                  const int32_t* block_table, int bt_stride, const uint32_t* cache_lens,
+                                  const void* freqs, int max_seq_len, const void* gamma, const void* beta, float eps,
+                                  PlanHeader* hdr, cudaStream_t s);
+
 // The FP8 indexer: exact scores into the workspace, then per-token top_k selection.
 size_t indexer_workspace_bytes(int T, int max_keys);
 // Dynamic shared memory of the scores kernel for H heads of D dimensions.

@@ -1,0 +1,331 @@
+// mla_rmsnorm_quant: what stands between a layer's residual stream (or a latent, or the
+// attention's output) and a projection over 8-bit codes, in one pass over the row:
+//
+//   h = bf16( x + residual )                       (h = x without a residual)
+//   y = bf16( h / sqrt(mean(h^2) + eps) * gamma )  (y = h without gamma)
+//   e4m3: s = the least 2^e with amax|y| <= 448 s, codes y / s     (an exact quotient, rounded once)
+//   int8: s = fl32(amax|y| / 127), at least 2^-126, codes y / s    (nearest, ties to even)
+//
+// Arithmetic.  A code follows the last bit of y, so y is the correctly rounded value: the squares
+// of bf16 values are exact in fp32 and summed as unevaluated pairs (Knuth's TwoSum), 1 / sqrt is
+// taken once a row in fp64 and split into two floats, h * gamma is exact, and the one fma that is
+// left is rounded to odd before it is rounded to bf16 (mla_rows.cuh).  x + residual needs no such
+// care: a sum of two 8-bit significands rounded to 24 bits and then to 8 is rounded as if once
+// (24 >= 2 * 8 + 2).  An int8 quotient is formed with the reciprocal of s, off by at most
+// 127 * 2^-23, and decided in fp64 where that leaves its rounding open (one value in 4,096), where
+// the product of s and a half-integer is exact.
+//
+// Layout.  A row is read once and stays in registers: 8 values (16 bytes) a thread V times.  Rows of
+// up to 1,024 values take a warp, longer ones a block with three barriers a row (sum, 1 / sqrt,
+// largest code).  Bound by HBM for many rows, by those steps' latency for few.
+#include "mla_kernels.cuh"
+#include "mla_rows.cuh"
+
+namespace mla {
+namespace rq {
+
+using namespace rows;
+
+constexpr int kWarpRows = 8;          // rows of a block where a warp takes a row
+constexpr int kMaxThreads = 1024;
+
+struct Args {
+  int fmt, T, D;
+  long long x_stride;
+  double eps;
+  const __nv_bfloat16* x;          // [T, >= D]
+  const __nv_bfloat16* residual;   // [T, D] or NULL
+  __nv_bfloat16* residual_out;     // [T, D], may be residual
+  const __nv_bfloat16* gamma;      // [D] or NULL
+  __nv_bfloat16* y_out;            // [T, D] or NULL
+  uint8_t* codes;                  // [T, D] or NULL
+  float* scales;                   // [T]
+};
+
+constexpr uint32_t kLow = 0x2B800000u, kSpan = 0x5D800000u - kLow;   // fp32 magnitudes 2^-40 .. 2^60
+
+// h * inv * gamma of any one value, rounded to odd.
+static __device__ __noinline__ float normed_any(float h, float g, float ih, float il, double inv, bool inner) {
+  const float m = __fmul_rn(h, g);
+  if (inner && ((__float_as_uint(m) & 0x7FFFFFFFu) - kLow <= kSpan || h == 0.f || g == 0.f))
+    return fma_odd(m, ih, __fmul_rn(m, il));
+  return double_odd((double)h * inv * (double)g);
+}
+
+// h * inv * gamma of eight values (packed pairs), as packed bf16 pairs.  inv = ih + il, il >= 0, so
+// that a zero keeps its sign.  The fma's operands must be exact: products in fp32's inner range.
+__device__ __forceinline__ void normed(const uint32_t (&h)[4], const uint32_t (&g)[4], float ih, float il, double inv,
+                                       bool inner, uint32_t (&y)[4]) {
+  float m[8];
+  uint32_t worst = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[2 * i] = __fmul_rn(lo_f(h[i]), lo_f(g[i]));
+    m[2 * i + 1] = __fmul_rn(hi_f(h[i]), hi_f(g[i]));
+    worst = max(worst, max((__float_as_uint(m[2 * i]) & 0x7FFFFFFFu) - kLow,
+                           (__float_as_uint(m[2 * i + 1]) & 0x7FFFFFFFu) - kLow));
+  }
+  if (inner && worst <= kSpan) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      y[i] = pack(fma_odd(m[2 * i], ih, __fmul_rn(m[2 * i], il)),
+                  fma_odd(m[2 * i + 1], ih, __fmul_rn(m[2 * i + 1], il)));
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    y[i] = pack(normed_any(lo_f(h[i]), lo_f(g[i]), ih, il, inv, inner), normed_any(hi_f(h[i]), hi_f(g[i]), ih, il, inv, inner));
+}
+
+// The int8 code of y / s where the fp32 quotient k + r lies next to a half-integer.
+static __device__ __noinline__ int int8_decide(float y, float s, float k, float r) {
+  const float half = k + (r > 0.f ? 0.5f : -0.5f);
+  const double d = (double)y - (double)half * (double)s;   // sign of y / s - half: the product is exact
+  const int below = __float2int_rd(half);
+  return d > 0.0 ? below + 1 : d < 0.0 ? below : (below & 1) ? below + 1 : below;
+}
+
+// Eight values (packed bf16 pairs) as eight int8 codes.
+__device__ __forceinline__ uint2 int8_codes(const uint32_t (&y)[4], float s, float rs) {
+  constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: an integer added to it sits in the low bits
+  uint32_t b[8];
+  float worst = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float z = __fmul_rn(i & 1 ? hi_f(y[i / 2]) : lo_f(y[i / 2]), rs), u = __fadd_rn(z, kMagic);
+    b[i] = __float_as_uint(u);
+    worst = fmaxf(worst, fabsf(__fsub_rn(z, __fsub_rn(u, kMagic))));
+  }
+  if (worst > 0.5f - 0x1p-13f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = i & 1 ? hi_f(y[i / 2]) : lo_f(y[i / 2]);
+      const float z = __fmul_rn(v, rs), k = __fsub_rn(__fadd_rn(z, kMagic), kMagic), r = __fsub_rn(z, k);
+      if (fabsf(r) > 0.5f - 0x1p-13f) b[i] = (uint32_t)int8_decide(v, s, k, r);
+    }
+  }
+  uint2 w;
+  w.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+  w.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+  return w;
+}
+
+// Eight values as eight e4m3 codes of y * rs, rs a power of two.
+__device__ __forceinline__ uint2 e4m3_codes(const uint32_t (&y)[4], float rs) {
+  uint32_t two[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    two[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo_f(y[i]) * rs, hi_f(y[i]) * rs), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(two[0] | (two[1] << 16), two[2] | (two[3] << 16));
+}
+
+// V pieces of 8 values a thread; kWarp: a warp takes a row, else the block does.
+template <int V, bool kWarp>
+__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMaxThreads) rmsnorm_kernel(const Args a) {
+  __shared__ float part_hi[32], part_lo[32];
+  __shared__ double part_wide[32];
+  __shared__ uint32_t part_max[32];
+  __shared__ double inv_of_row;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warps = kWarp ? 1 : (int)blockDim.x >> 5;
+  const int first = kWarp ? lane : (int)threadIdx.x, step = kWarp ? 32 : (int)blockDim.x;
+  const long long t = kWarp ? (long long)blockIdx.x * kWarpRows + warp : (long long)blockIdx.x;
+  if (kWarp && t >= a.T) return;
+  const int n8 = a.D >> 3;
+
+  uint32_t h[V][4];
+  {
+    uint4 xv[V], rv[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = first + v * step;
+      xv[v] = rv[v] = make_uint4(0, 0, 0, 0);
+      if (p < n8) {
+        xv[v] = reinterpret_cast<const uint4*>(a.x + t * a.x_stride)[p];
+        if (a.residual) rv[v] = reinterpret_cast<const uint4*>(a.residual + t * a.D)[p];
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      h[v][0] = xv[v].x; h[v][1] = xv[v].y; h[v][2] = xv[v].z; h[v][3] = xv[v].w;
+      if (a.residual) {
+        const uint32_t r[4] = {rv[v].x, rv[v].y, rv[v].z, rv[v].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          h[v][i] = pack(__fadd_rn(lo_f(h[v][i]), lo_f(r[i])), __fadd_rn(hi_f(h[v][i]), hi_f(r[i])));
+        const int p = first + v * step;
+        if (p < n8)
+          reinterpret_cast<uint4*>(a.residual_out + t * a.D)[p] = make_uint4(h[v][0], h[v][1], h[v][2], h[v][3]);
+      }
+    }
+  }
+
+  if (a.gamma) {
+    // mean square: pairs of floats where the largest magnitude leaves the squares room, else fp64
+    uint32_t top = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max(top, max(h[v][i] & 0x7FFFu, (h[v][i] >> 16) & 0x7FFFu));
+    top = __reduce_max_sync(0xffffffffu, top);
+    const float top_f = __uint_as_float(top << 16);
+    bool wide = top != 0 && !(top_f >= 0x1p-40f && top_f <= 0x1p55f);
+    float hi = 0.f, lo = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float e;
+        two_sum(hi, __fmul_rn(lo_f(h[v][i]), lo_f(h[v][i])), hi, e);
+        lo = __fadd_rn(lo, e);
+        two_sum(hi, __fmul_rn(hi_f(h[v][i]), hi_f(h[v][i])), hi, e);
+        lo = __fadd_rn(lo, e);
+      }
+    auto reduce_pair = [&]() {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float h2 = __shfl_xor_sync(0xffffffffu, hi, o), l2 = __shfl_xor_sync(0xffffffffu, lo, o);
+        float e;
+        two_sum(hi, h2, hi, e);
+        lo = __fadd_rn(__fadd_rn(lo, l2), e);
+      }
+    };
+    auto reduce_wide = [&]() {
+      double s = 0.0;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s += (double)lo_f(h[v][i]) * (double)lo_f(h[v][i]);
+          s += (double)hi_f(h[v][i]) * (double)hi_f(h[v][i]);
+        }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      return s;
+    };
+    reduce_pair();
+    double inv;
+    if (kWarp) {
+      inv = rsqrt((wide ? reduce_wide() : (double)hi + (double)lo) / (double)a.D + a.eps);
+    } else {
+      if (lane == 0) {
+        part_hi[warp] = hi;
+        part_lo[warp] = lo;
+      }
+      wide = __syncthreads_or(wide);
+      if (wide) {   // the same for the whole block
+        const double s = reduce_wide();
+        if (lane == 0) part_wide[warp] = s;
+        __syncthreads();
+      }
+      if (warp == 0) {
+        double sum;
+        if (wide) {
+          sum = 0.0;
+          for (int w = 0; w < warps; ++w) sum += part_wide[w];
+        } else {
+          hi = lane < warps ? part_hi[lane] : 0.f;
+          lo = lane < warps ? part_lo[lane] : 0.f;
+          reduce_pair();
+          sum = (double)hi + (double)lo;
+        }
+        if (lane == 0) inv_of_row = rsqrt(sum / (double)a.D + a.eps);
+      }
+      __syncthreads();
+      inv = inv_of_row;
+    }
+    const float ih = __double2float_rd(inv), il = (float)(inv - (double)ih);
+    const bool inner = ih >= 0x1p-60f && ih <= 0x1p60f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = first + v * step;
+      if (p < n8) {
+        const uint4 gv = reinterpret_cast<const uint4*>(a.gamma)[p];
+        const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w};
+        normed(h[v], g, ih, il, inv, inner, h[v]);
+      }
+    }
+  }
+
+  if (a.y_out) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = first + v * step;
+      if (p < n8) reinterpret_cast<uint4*>(a.y_out + t * a.D)[p] = make_uint4(h[v][0], h[v][1], h[v][2], h[v][3]);
+    }
+  }
+  if (a.fmt == MLA_CODES_BF16) return;
+
+  uint32_t amax = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) amax = max(amax, max(h[v][i] & 0x7FFFu, (h[v][i] >> 16) & 0x7FFFu));
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  if (!kWarp) {
+    if (lane == 0) part_max[warp] = amax;
+    __syncthreads();
+    amax = __reduce_max_sync(0xffffffffu, lane < warps ? part_max[lane] : 0u);
+  }
+  const bool bad = amax >= 0x7F80u;   // a NaN or an infinity: every value of the row reads back as NaN
+  const bool int8 = a.fmt == MLA_CODES_INT8;
+  float s, rs;
+  if (int8) {
+    s = amax == 0 ? 1.f : fmaxf(__fdiv_rn(__uint_as_float(amax << 16), 127.f), 0x1p-126f);
+    rs = __frcp_rn(s);
+  } else {
+    const int e = bad ? 0 : scale_exponent(amax, 8, -126, 127);
+    s = pow2(e);
+    rs = pow2(-e);
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int p = first + v * step;
+    if (p >= n8) continue;
+    uint2 w;
+    if (bad) w = int8 ? make_uint2(0, 0) : make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    else w = int8 ? int8_codes(h[v], s, rs) : e4m3_codes(h[v], rs);
+    reinterpret_cast<uint2*>(a.codes + t * a.D)[p] = w;
+  }
+  if (first == 0) a.scales[t] = bad && int8 ? __uint_as_float(0x7FC00000u) : s;
+}
+
+template <int V, bool kWarp>
+void start(const Args& a, int threads, cudaStream_t s) {
+  const unsigned blocks = kWarp ? ((unsigned)a.T + kWarpRows - 1) / kWarpRows : (unsigned)a.T;
+  rmsnorm_kernel<V, kWarp><<<blocks, threads, 0, s>>>(a);
+}
+
+}  // namespace rq
+
+cudaError_t launch_rmsnorm(int fmt, int rows, int width, const void* x, long long x_stride, const void* residual,
+                           void* residual_out, const void* gamma, float eps, void* y_out, void* codes, float* scales,
+                           cudaStream_t s) {
+  if (rows == 0) return cudaSuccess;
+  rq::Args a{};
+  a.fmt = fmt;
+  a.T = rows;
+  a.D = width;
+  a.x_stride = x_stride;
+  a.eps = (double)eps;
+  a.x = static_cast<const __nv_bfloat16*>(x);
+  a.residual = static_cast<const __nv_bfloat16*>(residual);
+  a.residual_out = static_cast<__nv_bfloat16*>(residual_out);
+  a.gamma = static_cast<const __nv_bfloat16*>(gamma);
+  a.y_out = static_cast<__nv_bfloat16*>(y_out);
+  a.codes = static_cast<uint8_t*>(codes);
+  a.scales = scales;
+  const int n8 = width / 8;
+  if (n8 <= 32) rq::start<1, true>(a, 32 * rq::kWarpRows, s);
+  else if (n8 <= 64) rq::start<2, true>(a, 32 * rq::kWarpRows, s);
+  else if (n8 <= 128) rq::start<4, true>(a, 32 * rq::kWarpRows, s);
+  else {
+    auto threads = [&](int v) { return ((n8 + v - 1) / v + 31) / 32 * 32; };
+    if (n8 <= 512) rq::start<1, false>(a, threads(1), s);
+    else if (n8 <= 1024) rq::start<2, false>(a, threads(2), s);
+    else rq::start<4, false>(a, threads(4), s);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace mla

@@ -1,0 +1,118 @@
+// What the kernels that write and read cache rows and 8-bit codes share: exact and correctly
+// rounded arithmetic on bf16 values, the scales of codes, rotations, and where a token's row is.
+#pragma once
+
+#include "mla_common.cuh"
+
+namespace mla {
+namespace rows {
+
+__device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+// (a + b) as an exact pair (Knuth's TwoSum).
+__device__ __forceinline__ void two_sum(float a, float b, float& hi, float& lo) {
+  hi = __fadd_rn(a, b);
+  const float z = __fsub_rn(hi, a);
+  lo = __fadd_rn(__fsub_rn(a, __fsub_rn(hi, z)), __fsub_rn(b, z));
+}
+
+// a * b + c rounded to odd.
+__device__ __forceinline__ float fma_odd(float a, float b, float c) {
+  const float down = __fmaf_rd(a, b, c), up = __fmaf_ru(a, b, c);
+  return __float_as_uint(down) & 1u ? down : up;
+}
+
+// Two floats as a bf16 pair, the first in the low half; nearest, ties to even.
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// A double as a float rounded to odd (truncated, the last bit set if anything was dropped).
+__device__ __forceinline__ float double_odd(double x) {
+  const float f = __double2float_rz(x);
+  return isfinite(f) && (double)f != x ? __uint_as_float(__float_as_uint(f) | 1u) : f;
+}
+
+// The least e with amax <= 7 * 2^(e - 3 + over), from bits of a bf16 magnitude: its exponent
+// field counts from 2^-127, a subnormal's leading bit is found by counting.  0 for zero.
+__device__ __forceinline__ int scale_exponent(uint32_t mag, int over, int low, int high) {
+  if (mag == 0) return 0;
+  int k = (int)(mag >> 7) - 127;
+  uint32_t frac = mag & 0x7Fu;
+  if ((mag >> 7) == 0) {
+    const int s = __clz(frac) - 25;   // the leading one of 7 fraction bits of 2^-126
+    k = -127 - s;
+    frac = (frac << (s + 1)) & 0x7Fu;
+  }
+  const int e = k - over + (frac > 0x60u ? 1 : 0);   // 1.75 = 1 + 0x60 / 128
+  return min(max(e, low), high);
+}
+// 2^e as a float, e >= -149; -e of a clamped exponent is never below -127
+__device__ __forceinline__ float pow2(int e) {
+  return e >= -126 ? __uint_as_float((uint32_t)(e + 127) << 23) : __uint_as_float(1u << (e + 149));
+}
+
+// `turn` for products that fp32 does not hold.
+__device__ __forceinline__ uint32_t turn_wide(uint32_t x, uint32_t f) {
+  const double x0 = lo_f(x), x1 = hi_f(x), c = lo_f(f), s = hi_f(f);
+  return pack(double_odd(add_odd(x0 * c, -(x1 * s))), double_odd(add_odd(x0 * s, x1 * c)));
+}
+// The pair (x0, x1) of `x` turned by (cos, sin) of `f`, as a bf16 pair.  Products of bf16 values
+// are exact in fp32's normal range; `lost` becomes other than 0 where one is not.
+__device__ __forceinline__ uint32_t turn(uint32_t x, uint32_t f, uint32_t& lost) {
+  const float x0 = lo_f(x), x1 = hi_f(x), c = lo_f(f), s = hi_f(f);
+  const float p = __fmul_rn(x1, s), r = __fmul_rn(x1, c);
+  lost |= product_lost(p, x1, s) | product_lost(r, x1, c);
+  return pack(fma_odd(x0, c, -p), fma_odd(x0, s, r));
+}
+// 16 bytes of pairs.
+static __device__ __noinline__ uint4 turn_wide(uint4 x, uint4 f) {
+  return make_uint4(turn_wide(x.x, f.x), turn_wide(x.y, f.y), turn_wide(x.z, f.z), turn_wide(x.w, f.w));
+}
+__device__ __forceinline__ uint4 turn(uint4 x, uint4 f, uint32_t& lost) {
+  return make_uint4(turn(x.x, f.x, lost), turn(x.y, f.y, lost), turn(x.z, f.z, lost), turn(x.w, f.w, lost));
+}
+
+struct Place {
+  long long pos;   // -1: the token is left alone
+  long long row;   // physical cache row
+};
+
+// Whole warp: where token t of a call goes.  `A` holds the call's offsets, cache_lens, block_table,
+// bt_stride, ps, num_pages, B, max_seq_len and hdr.  The request is the last b with offsets[b] <= t,
+// found by 32 probes a round (two rounds up to 1024 requests).  Tokens at or past
+// offsets[B] belong to nobody and are skipped; a position or page out of range is
+// reported.
+template <class A>
+__device__ __forceinline__ Place locate(const A& a, int t, int lane) {
+  Place p{-1, 0};
+  int lo = 0, n = a.B;   // candidates [lo, lo + n)
+  const uint32_t end = a.offsets[a.B];
+  while (n > 1) {
+    const int step = (n + 31) >> 5;
+    const int probe = lane * step;
+    const bool below = probe < n && a.offsets[lo + probe] <= (uint32_t)t;
+    const int cnt = __popc(__ballot_sync(0xffffffffu, below));
+    const int skip = cnt > 0 ? (cnt - 1) * step : 0;
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  const uint32_t qb = a.offsets[lo], qe = a.offsets[lo + 1], len = a.cache_lens[lo];
+  if ((uint32_t)t >= end) return p;
+  const long long pos = (long long)len - qe + t;
+  bool ok = qb <= (uint32_t)t && (uint32_t)t < qe && pos >= 0 && pos < a.max_seq_len &&
+            pos < (long long)a.bt_stride * a.ps;
+  if (ok) {
+    const int page = a.block_table[(size_t)lo * a.bt_stride + pos / a.ps];
+    ok = page >= 0 && page < a.num_pages;
+    p.row = (long long)page * a.ps + pos % a.ps;
+  }
+  if (ok) p.pos = pos;
+  else if (lane == 0) atomicOr(&a.hdr->status, kDeviceCheckFailed);
+  return p;
+}
+
+}  // namespace rows
+}  // namespace mla
