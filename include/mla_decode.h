@@ -338,6 +338,27 @@ int mla_rmsnorm_quant(int32_t code_format, int32_t rows, int32_t width, const vo
                       const void* residual, void* residual_out, const void* gamma, float epsilon, void* y_out,
                       void* codes_out, float* scales_out, void* stream);
 
+/* Projections over 8-bit codes with a scale for each token and each output channel: a layer's
+ * projections around the attention (down to the latents, queries up, output), on what
+ * mla_rmsnorm_quant writes.
+ *   out[t, n] = bf16( (sum_k x[t, k] * w[n, k]) * x_scales[t] * w_scales[n] )
+ * in fp32 (sums of fp32 in the tensor core's order; products of codes are exact), rounded once to
+ * bf16.  A NaN code or scale makes NaN of the results that it enters.
+ *   x_codes        [tokens, k], x_scales float [tokens]
+ *   w_codes        [n, k], w_scales float [n]
+ *   out            bf16, row t at out + t * out_stride; out_stride in elements, >= n
+ *   flags, workspace   as mla_branch_prologue (a wait that runs out is recorded there)
+ * The codes are e4m3 (OCP E4M3FN) for _fp8 and int8 for _int8.  k is a multiple of 16, n and
+ * out_stride of 8, tokens at most 2^22; x_codes, w_codes, w_scales and out are 16-byte aligned.  The result of a token
+ * does not depend on the timing of the call; it may differ in rounding between calls of different
+ * numbers of tokens (K is split where there are few). */
+int mla_linear_fp8(int32_t tokens, int32_t n, int32_t k, const void* x_codes, const float* x_scales,
+                   const void* w_codes, const float* w_scales, void* out, int64_t out_stride, uint32_t flags,
+                   void* workspace, size_t workspace_bytes, void* stream);
+int mla_linear_int8(int32_t tokens, int32_t n, int32_t k, const void* x_codes, const float* x_scales,
+                    const void* w_codes, const float* w_scales, void* out, int64_t out_stride, uint32_t flags,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* Prefill: the decode's attention for many query tokens per request, in the expanded
  * form (generic_flare_mla_prefill_kv_cache_ragged page), over the paged latent cache that
  * mla_cache_append fills.  Per head, every visible cached row becomes a key

@@ -15,6 +15,7 @@ Entry points (same names as the C ABI):
   mla_prefill_paged     many query tokens a request, expanded form (also _fp8, _fp4)
   mla_cache_read        cache rows of any format back as bf16 values
   mla_rmsnorm_quant     residual addition, RMSNorm and 8-bit codes (e4m3, int8) of activations
+  mla_linear_fp8        projections over e4m3 codes with scales per token and channel (also _int8)
   mla_indexer_append    the indexer's keys (LayerNorm, RoPE, e4m3) into its paged cache, its queries as codes
   mla_indexer_fp8       top-k cache rows per query token by FP8 index scores (sparse input)
 """
@@ -35,7 +36,7 @@ from ._lib import (MLA_FLAG_DEBUG_CHECKS, MLA_FLAG_KERNEL_TIMING, MLA_FLAG_FOLD_
 __all__ = ["mla_decode_paged", "mla_decode_paged_fp8", "mla_decode_paged_fp4", "mla_decode_sparse",
            "mla_branch_prologue", "mla_cache_append", "mla_cache_row_bytes", "mla_indexer_fp8",
            "mla_prefill_paged", "mla_prefill_paged_fp8", "mla_prefill_paged_fp4", "mla_prefill_workspace_size",
-           "mla_cache_read", "mla_rmsnorm_quant", "mla_indexer_append",
+           "mla_cache_read", "mla_rmsnorm_quant", "mla_linear_fp8", "mla_linear_int8", "mla_indexer_append",
            "MLA_CACHE_BF16", "MLA_CACHE_E4M3", "MLA_CACHE_E2M1", "MLA_CODES_BF16", "MLA_CODES_E4M3", "MLA_CODES_INT8",
            "mla_decode_workspace_size", "MlaDims", "MlaOpts", "MlaError", "MLA_MASK_NULL",
            "MLA_MASK_CAUSAL", "MLA_MASK_SLIDING_WINDOW_CAUSAL", "library_path", "kernel_times"]
@@ -378,6 +379,44 @@ def mla_rmsnorm_quant(x, gamma=None, *, epsilon: float = 1e-6, code_format: int 
           _ptr(y_out, "y_out", _BF16, dev), _ptr(codes_out, "codes_out", (_CODES[code_format], torch.uint8), dev),
           _ptr(scales_out, "scales_out", (torch.float32,), dev), _stream(stream, dev))
     return (codes_out, scales_out, residual_out) if coded else (y_out, None, residual_out)
+
+
+def _linear(name, dtypes, x_codes, x_scales, w_codes, w_scales, out, debug, workspace, stream):
+    dev = x_codes.device
+    if x_codes.dim() != 2 or w_codes.dim() != 2 or x_codes.shape[1] != w_codes.shape[1]:
+        raise ValueError("x_codes must be [T, K] and w_codes [N, K]")
+    T, K = x_codes.shape
+    N = w_codes.shape[0]
+    _sized(x_scales, "x_scales", T)
+    _sized(w_scales, "w_scales", N)
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if out is None:
+        out = _buffer((T, N), torch.bfloat16, dev, stream, returned=True)
+    elif out.shape[0] != T:
+        raise ValueError(f"out must be [{T}, {N}]")
+    p_out, out_stride = _row_strided(out, "out", N)
+    if out.device != dev:
+        raise ValueError(f"out is on {out.device}, expected {dev}")
+    if workspace is None:
+        workspace = _buffer(256, torch.uint8, dev, stream) if debug else _unread_status(dev, s)
+    f32 = (torch.float32,)
+    _call(name, dev, T, N, K, _ptr(x_codes, "x_codes", dtypes, dev), _ptr(x_scales, "x_scales", f32, dev),
+          _ptr(w_codes, "w_codes", dtypes, dev), _ptr(w_scales, "w_scales", f32, dev), p_out, out_stride,
+          MLA_FLAG_DEBUG_CHECKS if debug else 0, _ptr(workspace, "workspace", None, dev),
+          workspace.numel() * workspace.element_size(), ctypes.c_void_p(s.cuda_stream))
+    return out
+
+
+def mla_linear_fp8(x_codes, x_scales, w_codes, w_scales, *, out=None, debug: bool = False, workspace=None, stream=None):
+    """Projection over e4m3 codes: x_codes [T, K], w_codes [N, K] (float8_e4m3fn or uint8), x_scales f32 [T],
+    w_scales f32 [N].  Returns out bf16 [T, N] (rows may be strided if given)."""
+    return _linear("mla_linear_fp8", (torch.float8_e4m3fn, torch.uint8), x_codes, x_scales, w_codes, w_scales, out, debug,
+                   workspace, stream)
+
+
+def mla_linear_int8(x_codes, x_scales, w_codes, w_scales, *, out=None, debug: bool = False, workspace=None, stream=None):
+    """mla_linear_fp8 over int8 codes."""
+    return _linear("mla_linear_int8", (torch.int8,), x_codes, x_scales, w_codes, w_scales, out, debug, workspace, stream)
 
 
 def mla_indexer_append(k_new, input_row_offsets, k_cache, k_scales, block_table, cache_lens, *, page_size: int,

@@ -38,7 +38,7 @@ EXPORTED = ("mla_decode_workspace_size", "mla_decode_paged", "mla_decode_paged_f
             "mla_cache_append", "mla_prefill_workspace_size", "mla_prefill_paged", "mla_prefill_paged_fp8",
             "mla_prefill_paged_fp4",
             "mla_indexer_workspace_size", "mla_indexer_fp8",
-            "mla_cache_read", "mla_rmsnorm_quant", "mla_indexer_append",
+            "mla_cache_read", "mla_rmsnorm_quant", "mla_linear_fp8", "mla_linear_int8", "mla_indexer_append",
             "mla_debug_wait_selftest",
             "mla_status_string")
 
@@ -55,6 +55,8 @@ class MlaOpts(ctypes.Structure):
 
 
 _P = ctypes.POINTER
+_LINEAR = [c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, ctypes.c_int64, c_uint32,
+           c_void_p, c_size_t, c_void_p]
 _SIGS = {
     "mla_decode_workspace_size": [_P(MlaDims), _P(MlaOpts), c_int32, c_int32, _P(c_size_t)],
     "mla_decode_paged": [_P(MlaDims), _P(MlaOpts), c_void_p, c_void_p, c_int32, c_int32, c_void_p,
@@ -85,6 +87,8 @@ _SIGS = {
                        c_void_p, c_void_p, c_uint32, c_void_p, c_size_t, c_void_p],
     "mla_rmsnorm_quant": [c_int32, c_int32, c_int32, c_void_p, ctypes.c_int64, c_void_p, c_void_p, c_void_p, c_float,
                           c_void_p, c_void_p, c_void_p, c_void_p],
+    "mla_linear_fp8": _LINEAR,
+    "mla_linear_int8": _LINEAR,
     "mla_indexer_append": [c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, ctypes.c_int64, c_void_p, c_int32,
                            c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32,
                            c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_float, c_uint32, c_void_p, c_size_t,

@@ -587,6 +587,44 @@ int mla_rmsnorm_quant(int32_t code_format, int32_t rows, int32_t width, const vo
 }
 
 namespace {
+int run_linear(const char* name, bool int8, int32_t tokens, int32_t n, int32_t k, const void* x, const float* x_scales,
+               const void* w, const float* w_scales, void* out, int64_t out_stride, uint32_t flags, void* workspace,
+               size_t workspace_bytes, void* stream) {
+  if (tokens < 0 || n < 1 || k < 1 || out_stride < n || (flags & ~MLA_FLAG_DEBUG_CHECKS)) return MLA_ERR_INVALID_ARG;
+  if (n % 8 != 0 || k % 16 != 0 || out_stride % 8 != 0 || tokens > kMaxLinearTokens) return MLA_ERR_UNSUPPORTED;
+  if ((tokens > 0 && (!x || !x_scales || !out)) || !w || !w_scales || !workspace) return MLA_ERR_INVALID_ARG;
+  for (const void* p : {x, w, static_cast<const void*>(w_scales), static_cast<const void*>(out)})
+    if (!aligned16(p)) return MLA_ERR_INVALID_ARG;
+  if (workspace_bytes < sizeof(PlanHeader) || !aligned16(workspace)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  PlanHeader* hdr = static_cast<PlanHeader*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((flags & MLA_FLAG_DEBUG_CHECKS) && cudaMemsetAsync(hdr, 0, sizeof(PlanHeader), s) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  const cudaError_t e = launch_linear(int8, tokens, n, k, x, x_scales, w, w_scales, out, out_stride, hdr, s);
+  if (e != cudaSuccess) {
+    std::fprintf(stderr, "%s: %s\n", name, cudaGetErrorString(e));
+    return MLA_ERR_CUDA;
+  }
+  if (flags & MLA_FLAG_DEBUG_CHECKS) return device_status(hdr, s);
+  return MLA_OK;
+}
+}  // namespace
+
+int mla_linear_fp8(int32_t tokens, int32_t n, int32_t k, const void* x_codes, const float* x_scales,
+                   const void* w_codes, const float* w_scales, void* out, int64_t out_stride, uint32_t flags,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  return run_linear("mla_linear_fp8", false, tokens, n, k, x_codes, x_scales, w_codes, w_scales, out, out_stride, flags,
+                    workspace, workspace_bytes, stream);
+}
+
+int mla_linear_int8(int32_t tokens, int32_t n, int32_t k, const void* x_codes, const float* x_scales,
+                    const void* w_codes, const float* w_scales, void* out, int64_t out_stride, uint32_t flags,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  return run_linear("mla_linear_int8", true, tokens, n, k, x_codes, x_scales, w_codes, w_scales, out, out_stride, flags,
+                    workspace, workspace_bytes, stream);
+}
+
+namespace {
 // K and V boxes of a pass: all heads if they fit this, else as many as do.
 constexpr size_t kPrefillPassBytes = size_t(4) << 30;
 

@@ -86,6 +86,11 @@ cudaError_t launch_rmsnorm(int fmt, int rows, int width, const void* x, long lon
                            void* residual_out, const void* gamma, float eps, void* y_out, void* codes, float* scales,
                            cudaStream_t s);
 
+// Projection over 8-bit codes (int8, else e4m3): K a multiple of 16, N of 8, out_stride of 8.
+constexpr int kMaxLinearTokens = 1 << 22;   // tiles of tokens are a grid's second dimension
+cudaError_t launch_linear(bool int8, int T, int N, int K, const void* x, const float* x_scale, const void* w,
+                          const float* w_scale, void* out, long long out_stride, PlanHeader* hdr, cudaStream_t s);
+
 // Rows of the paged latent cache as bf16 values.
 cudaError_t launch_cache_read(const mla_dims_t& d, int fmt, const uint32_t* offsets, int B, int T, const void* pool,
                               const float* scales, const int32_t* block_table, int bt_stride,
