@@ -12,6 +12,14 @@
 // call is bound by reading those once.  Where the tiles are fewer than the SMs, a cluster of CTAs
 // splits K: each leaves its fp32 partial in its shared memory and sums a share of the tokens over the
 // cluster, in rank order (the result does not depend on timing).
+//
+// Many tokens (pair kernel).  One pair of CTAs a pair of SMs, cta_group::2: 256 tokens (A) by 256
+// channels (B; int8 192), each CTA loading half of either operand, one tile after another.  Tiles go
+// group by group of token tiles, so that those in flight share operands in L2.  The accumulator is
+// double: while a tile's products run, four warps scale the last one, lay it out in shared memory
+// and store it by TMA, which also cuts off what lies past the last token or channel.  int8: four
+// warps widen the tokens' codes into tensor memory, four the weights' into shared memory (both
+// there would cost more of its bandwidth than the products leave).
 #include <algorithm>
 
 #include "mla_kernels.cuh"
@@ -36,7 +44,7 @@ constexpr int kMaxStages = 12;
 constexpr int kConvWarps = 8;          // int8: warps that widen codes
 
 struct Maps {
-  CUtensorMap w, x;
+  CUtensorMap w, x, out;
 };
 
 struct Args {
@@ -248,16 +256,289 @@ __global__ void __launch_bounds__(kInt8 ? 128 + 32 * kConvWarps : 128)
   }
 }
 
+// ------------------------------------------------------------------ many tokens
+
+template <bool kInt8>
+struct Pair {
+  static constexpr int kN = kInt8 ? 192 : 256;              // channels of a tile
+  static constexpr int kStepK = kInt8 ? 64 : 128;           // codes of a stage
+  static constexpr int kRows = 128 + kN / 2;                // rows of a stage in a CTA: its tokens, its channels
+  static constexpr int kStage = kRows * kStepK;
+  static constexpr int kStages = 6;
+  static constexpr int kStages2 = 4;                        // int8, widened: tokens 32 TMEM columns, channels a box
+  static constexpr int kStage2 = kN / 2 * 128;
+  static constexpr int kBoxOut = 128 * 128;                 // 128 tokens x 64 channels bf16
+  static constexpr int kRing2 = kStages * kStage;
+  static constexpr int kOut = kRing2 + (kInt8 ? kStages2 * kStage2 : 0);
+  static constexpr int kScales = kOut + 2 * kBoxOut;        // [kN] channel scales
+  static constexpr int kBars = kScales + kN * 4;
+  static constexpr int kSmem = 1024 + kBars + 8 * (2 * kStages + 2 * kStages2 + 4) + 16;
+  static_assert(kSmem <= 232448);
+  static constexpr int kThreads = kInt8 ? 512 : 256;
+};
+
+// Tile i of a call: tokens from m0, channels from n0.  Groups of 8 token tiles, channel tiles in turn
+// within a group, the group's token tiles one after the other.
+struct Tile {
+  int m0, n0;
+};
+__device__ __forceinline__ Tile tile_of(int i, int mtiles, int ntiles, int kn) {
+  const int group = i / (8 * ntiles), in = i - group * 8 * ntiles;
+  const int gm = min(8, mtiles - 8 * group);
+  return Tile{(8 * group + in % gm) * 256, in / gm * kn};
+}
+
+__device__ __forceinline__ bool wait_bar_cluster(uint64_t* bar, uint32_t parity, PlanHeader* hdr) {
+  if (mbar_wait<true>(bar, parity, kWaitLimitNs)) return true;
+  atomicOr(&hdr->status, kDeviceTimeout);
+  return false;
+}
+
+// Warp 0 copies, warp 1 (of the pair's first CTA) issues the products, warp 2 owns the tensor memory,
+// warps 4-7 are the epilogue; int8: warps 8-11 widen tokens (thread = row = TMEM lane), 12-15 channels.
+template <bool kInt8>
+__global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 1, 1)
+    pair_kernel(const __grid_constant__ Maps maps, const Args a) {
+  using P = Pair<kInt8>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + P::kBars);   // e4m3: the first CTA's, for both; int8: each its own
+  uint64_t* empty = full + P::kStages;
+  uint64_t* full2 = empty + P::kStages;      // int8: widened, in the first CTA
+  uint64_t* empty2 = full2 + P::kStages2;
+  uint64_t* acc_full = empty2 + P::kStages2;           // a tile's products are done
+  uint64_t* acc_empty = acc_full + 2;        // ... and read, in the first CTA
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_ctarank();
+  const int mtiles = (a.T + 255) / 256, ntiles = (a.N + P::kN - 1) / P::kN;
+  const int tiles = mtiles * ntiles, pairs = (int)gridDim.x / 2, first = (int)blockIdx.x / 2;
+  const int nkb = (a.K + P::kStepK - 1) / P::kStepK;
+
+  if (tid == 0) {
+    for (int s = 0; s < P::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kInt8 ? 8 : 1);
+    }
+    for (int s = 0; s < P::kStages2; ++s) {
+      mbar_init(&full2[s], 16);
+      mbar_init(&empty2[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&acc_full[s], 1);
+      mbar_init(&acc_empty[s], 8);
+    }
+    fence_mbar_init();
+    prefetch_tensormap(&maps.x);
+    prefetch_tensormap(&maps.w);
+    prefetch_tensormap(&maps.out);
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the other CTA's barriers are there
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t kColA = 2 * P::kN;   // int8: columns of the widened tokens
+
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      int i = 0;
+      for (int tile = first; tile < tiles && ok; tile += pairs) {
+        const Tile at = tile_of(tile, mtiles, ntiles, P::kN);
+        for (int kb = 0; kb < nkb; ++kb, ++i) {
+          const int s = i % P::kStages;
+          if (i >= P::kStages && !(ok = wait_bar(&empty[s], ((i / P::kStages) & 1) ^ 1, a.hdr))) break;
+          uint8_t* dst = sm + s * P::kStage;
+          if (kInt8) {
+            mbar_arrive_expect_tx(&full[s], P::kStage);
+            tma_load_2d(dst, &maps.x, &full[s], kb * P::kStepK, at.m0 + 128 * rank);
+            tma_load_2d(dst + 128 * P::kStepK, &maps.w, &full[s], kb * P::kStepK, at.n0 + P::kN / 2 * rank);
+          } else {
+            const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * P::kStage);
+            tma_load_2d_pair(dst, &maps.x, bar, kb * P::kStepK, at.m0 + 128 * rank);
+            tma_load_2d_pair(dst + 128 * P::kStepK, &maps.w, bar, kb * P::kStepK, at.n0 + P::kN / 2 * rank);
+          }
+        }
+      }
+      // no copy and no arrival outlives the pair, whatever became of those who wait for them
+      for (int j = max(0, i - P::kStages); j < i; ++j) {
+        if (kInt8 || rank == 0) wait_bar(&full[j % P::kStages], (j / P::kStages) & 1, a.hdr);
+        wait_bar(&empty[j % P::kStages], (j / P::kStages) & 1, a.hdr);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = idesc_f32(256, P::kN, 0);   // f16 and e4m3 are both type 0 of their kinds
+      bool ok = true;
+      int i = 0, n = 0;
+      for (int tile = first; tile < tiles && ok; tile += pairs, ++n) {
+        const int b = n & 1;
+        const uint32_t d = tmem + b * P::kN;
+        if (n >= 2 && !(ok = wait_bar_cluster(&acc_empty[b], ((n >> 1) & 1) ^ 1, a.hdr))) break;
+        tc_fence_after();
+        for (int kb = 0; kb < nkb; ++kb, ++i) {
+          if (kInt8) {
+            const int s = i % P::kStages2;
+            if (!(ok = wait_bar_cluster(&full2[s], (i / P::kStages2) & 1, a.hdr))) break;
+            tc_fence_after();
+            const uint64_t wd = smem_desc(smem_u32(sm + P::kRing2 + s * P::kStage2), 16, 1024, kLayoutSw128);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts_pair(d, tmem + kColA + 32 * s + 8 * kk, wd + 2 * kk, idesc, (kb | kk) != 0);
+            mma_commit_pair(&empty2[s]);
+          } else {
+            const int s = i % P::kStages;
+            if (!(ok = wait_bar_cluster(&full[s], (i / P::kStages) & 1, a.hdr))) break;
+            tc_fence_after();
+            const uint64_t xd = smem_desc(smem_u32(sm + s * P::kStage), 16, 1024, kLayoutSw128);
+            const uint64_t wd = smem_desc(smem_u32(sm + s * P::kStage + 128 * 128), 16, 1024, kLayoutSw128);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mma_ss_f8_pair(d, xd + 2 * kk, wd + 2 * kk, idesc, (kb | kk) != 0);
+            mma_commit_pair(&empty[s]);
+          }
+        }
+        mma_commit_pair(&acc_full[b]);
+      }
+    }
+  } else if (warp >= 4 && warp < 8) {
+    const int row = tid - 128;                       // token of the CTA's half = TMEM lane
+    uint8_t* box = sm + P::kOut;
+    float* ws = reinterpret_cast<float*>(sm + P::kScales);   // read between a chunk's two barriers only
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    int n = 0, chunk = 0;
+    for (int tile = first; tile < tiles; tile += pairs, ++n) {
+      const Tile at = tile_of(tile, mtiles, ntiles, P::kN);
+      const int b = n & 1, m0 = at.m0 + 128 * rank;
+      for (int c = row; c < P::kN; c += 128) ws[c] = at.n0 + c < a.N ? a.w_scale[at.n0 + c] : 0.f;
+      const float xs = m0 + row < a.T ? a.x_scale[m0 + row] : 0.f;
+      bool ok = wait_bar(&acc_full[b], (n >> 1) & 1, a.hdr);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c0 = 0; c0 < P::kN; c0 += 64, ++chunk) {
+        uint32_t r[2][32];
+        tmem_ld32(tmem + b * P::kN + c0 + lanes, r[0]);
+        tmem_ld32(tmem + b * P::kN + c0 + 32 + lanes, r[1]);
+        tmem_ld_wait();
+        if (c0 + 64 == P::kN) {   // the tile's accumulator is read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[b]), 0));
+        }
+        // the box written two chunks ago has left (its writer waits), the scales are there
+        uint8_t* dst = box + (chunk & 1) * P::kBoxOut;
+        if (row == 0) bulk_wait_read<1>();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            const int c = 8 * g + 2 * j;
+            const float4 w4 = *reinterpret_cast<const float4*>(ws + c0 + c);
+            const uint32_t* v = &r[c >> 5][c & 31];
+            const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(v[0]) * xs * w4.x, __uint_as_float(v[1]) * xs * w4.y);
+            const __nv_bfloat162 q = __floats2bfloat162_rn(__uint_as_float(v[2]) * xs * w4.z, __uint_as_float(v[3]) * xs * w4.w);
+            o[j] = *reinterpret_cast<const uint32_t*>(&p);
+            o[j + 1] = *reinterpret_cast<const uint32_t*>(&q);
+          }
+          *reinterpret_cast<uint4*>(dst + row * 128 + ((g ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        fence_proxy_async_smem();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (row == 0) {
+          if (m0 < a.T && at.n0 + c0 < a.N) tma_store_2d(&maps.out, dst, at.n0 + c0, m0);
+          bulk_commit();
+        }
+      }
+    }
+    if (row == 0) bulk_wait_all();
+  } else if (kInt8 && warp >= 8) {
+    const bool tokens = warp < 12;
+    const int row = tid & 127;
+    int i = 0;
+    bool ok = true;
+    for (int tile = first; tile < tiles && ok; tile += pairs)
+      for (int kb = 0; kb < nkb; ++kb, ++i) {
+        const int s = i % P::kStages, s2 = i % P::kStages2;
+        ok = wait_bar(&full[s], (i / P::kStages) & 1, a.hdr);
+        if (ok && i >= P::kStages2) ok = wait_bar(&empty2[s2], ((i / P::kStages2) & 1) ^ 1, a.hdr);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const uint8_t* raw = sm + s * P::kStage;
+        if (tokens) {
+          tc_fence_after();
+          uint32_t o[32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {   // 64-byte rows in the 64-byte swizzle
+            uint4 lo, hi;
+            widen(*reinterpret_cast<const uint4*>(raw + row * 64 + ((q ^ ((row >> 1) & 3)) << 4)), lo, hi);
+            o[8 * q] = lo.x; o[8 * q + 1] = lo.y; o[8 * q + 2] = lo.z; o[8 * q + 3] = lo.w;
+            o[8 * q + 4] = hi.x; o[8 * q + 5] = hi.y; o[8 * q + 6] = hi.z; o[8 * q + 7] = hi.w;
+          }
+          tmem_st32(tmem + kColA + 32 * s2 + ((uint32_t)(32 * (warp & 3)) << 16), o);
+          tmem_st_wait();
+          tc_fence_before();
+        } else {
+          uint8_t* dst = sm + P::kRing2 + s2 * P::kStage2;
+          for (int j = row; j < P::kN / 2 * 4; j += 128) {
+            const int r = j >> 2, q = j & 3;   // place q of row r holds the codes of piece p
+            const int p = q ^ ((r >> 1) & 3);
+            uint4 lo, hi;
+            widen(*reinterpret_cast<const uint4*>(raw + 128 * 64 + 16 * j), lo, hi);
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((2 * p) ^ (r & 7)) << 4)) = lo;
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((2 * p + 1) ^ (r & 7)) << 4)) = hi;
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&empty[s]);
+          mbar_arrive_cluster(mapa_shared(smem_u32(&full2[s2]), 0));
+        }
+      }
+    // the pair's last arrivals on this CTA's barriers
+    if (warp == 8 && lane == 0)
+      for (int j = max(0, i - P::kStages2); j < i; ++j) wait_bar(&empty2[j % P::kStages2], (j / P::kStages2) & 1, a.hdr);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // neither CTA leaves while the other's products use its memory
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
 // Rows of K codes as a tensor map with boxes of `rows` rows and `step` codes.
-bool encode_codes(CUtensorMap* m, const void* p, int K, int rows_total, int step, int rows) {
+bool encode_codes(CUtensorMap* m, const void* p, int K, int rows_total, int step, int rows, CUtensorMapSwizzle swizzle) {
   const wg::EncodeTiledFn fn = wg::encode_fn();
   cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows_total};
   cuuint64_t strides[1] = {(cuuint64_t)K};
   cuuint32_t box[2] = {(cuuint32_t)step, (cuuint32_t)rows};
   cuuint32_t es[2] = {1, 1};
   return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, step == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The output, boxes of 128 tokens by 64 channels.
+bool encode_out(CUtensorMap* m, void* p, int T, int N, long long stride) {
+  const wg::EncodeTiledFn fn = wg::encode_fn();
+  cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)T};
+  cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+  cuuint32_t box[2] = {64, 128};
+  cuuint32_t es[2] = {1, 1};
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool kInt8>
@@ -277,7 +558,9 @@ cudaError_t launch_split(Args a, const void* x, const void* w, int sms, cudaStre
     a.S2 = 0;
     a.S = std::min(kMaxStages, budget / (rows * kStepK));
   }
-  if (!encode_codes(&maps.w, w, a.K, a.N, kStepK, kRowsW) || !encode_codes(&maps.x, x, a.K, a.T, kStepK, a.TN))
+  const CUtensorMapSwizzle swizzle = kInt8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+  if (!encode_codes(&maps.w, w, a.K, a.N, kStepK, kRowsW, swizzle) ||
+      !encode_codes(&maps.x, x, a.K, a.T, kStepK, a.TN, swizzle))
     return cudaErrorInvalidValue;
   const size_t ring = std::max((size_t)a.S * rows * kStepK + (size_t)a.S2 * rows * 128, (size_t)a.TN * kRowsW * 4);
   const size_t smem = 1024 + ring + (4 * kMaxStages + 2) * 8;
@@ -298,6 +581,23 @@ cudaError_t launch_split(Args a, const void* x, const void* w, int sms, cudaStre
   return e;
 }
 
+template <bool kInt8>
+cudaError_t launch_pair(const Args& a, const void* x, const void* w, int sms, cudaStream_t s) {
+  using P = Pair<kInt8>;
+  Maps maps;
+  const CUtensorMapSwizzle swizzle = kInt8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  if (!encode_codes(&maps.x, x, a.K, a.T, P::kStepK, 128, swizzle) ||
+      !encode_codes(&maps.w, w, a.K, a.N, P::kStepK, P::kN / 2, swizzle) ||
+      !encode_out(&maps.out, a.out, a.T, a.N, a.out_stride))
+    return cudaErrorInvalidValue;
+  const long long tiles = (long long)((a.T + 255) / 256) * ((a.N + P::kN - 1) / P::kN);
+  const int pairs = (int)std::min<long long>(tiles, sms / 2);
+  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(pair_kernel<kInt8>), P::kSmem);
+  if (e != cudaSuccess) return e;
+  pair_kernel<kInt8><<<2 * pairs, P::kThreads, P::kSmem, s>>>(maps, a);
+  return cudaGetLastError();
+}
+
 }  // namespace lin
 
 cudaError_t launch_linear(bool int8, int T, int N, int K, const void* x, const float* x_scale, const void* w,
@@ -316,6 +616,7 @@ cudaError_t launch_linear(bool int8, int T, int N, int K, const void* x, const f
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
+  if (T > lin::kMaxTokens) return int8 ? lin::launch_pair<true>(a, x, w, sms, s) : lin::launch_pair<false>(a, x, w, sms, s);
   return int8 ? lin::launch_split<true>(a, x, w, sms, s) : lin::launch_split<false>(a, x, w, sms, s);
 }
 
