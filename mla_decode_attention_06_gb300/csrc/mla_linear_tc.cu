@@ -38,6 +38,7 @@ namespace lin {
 using namespace sm100;
 
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
+constexpr int kStepK = 128;            // codes of a stage along K
 constexpr int kRowsW = 128;            // output channels of a tile
 constexpr int kMaxTokens = 256;        // tokens of a tile (MMA N)
 constexpr int kMaxStages = 12;
@@ -59,12 +60,33 @@ struct Args {
   PlanHeader* hdr;
 };
 
+// Waits spin: a suspended waiter (try_wait) can wake a microsecond after the phase completes, longer
+// than a stage takes.  The clock is looked at once in 256 polls.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, PlanHeader* hdr) {
-  if (mbar_wait(bar, parity, kWaitLimitNs)) return true;
-  atomicOr(&hdr->status, kDeviceTimeout);
-  return false;
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 1; !mbar_test_wait(bar, parity); ++i) {
+    if ((i & 255u) != 0) continue;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
+      atomicOr(&hdr->status, kDeviceTimeout);
+      return false;
+    }
+  }
+  return true;
 }
-
+// Place in a ring of `n` stages, and the parity of the round.
+struct Ring {
+  int s = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++s == n) {
+      s = 0;
+      round ^= 1;
+    }
+  }
+};
 // Sixteen int8 codes as sixteen f16 values: a code with its sign bit flipped, in the low bits of
 // 1024, is 1024 + 128 + code.
 __device__ __forceinline__ void widen(uint4 raw, uint4& lo, uint4& hi) {
@@ -84,18 +106,17 @@ __device__ __forceinline__ void widen(uint4 raw, uint4& lo, uint4& hi) {
   hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// A thread's share of widening `rows` rows of 64 codes (64 bytes apart) into rows of 64 f16 values in
-// the 128-byte swizzle.  Four neighbours take a row: reads are contiguous, the writes of eight
-// neighbours meet each bank once.
-__device__ __forceinline__ void widen_rows(const uint8_t* raw, uint8_t* dst, int rows, int i0, int step) {
-  for (int i = i0; i < rows * 4; i += step) {
-    const int r = i >> 2, q = i & 3;
-    uint4 lo, hi;
-    widen(*reinterpret_cast<const uint4*>(raw + 16 * i), lo, hi);
-    uint8_t* d = dst + r * 128;
-    *reinterpret_cast<uint4*>(d + (((2 * q) ^ (r & 7)) << 4)) = lo;
-    *reinterpret_cast<uint4*>(d + (((2 * q + 1) ^ (r & 7)) << 4)) = hi;
-  }
+// Piece q (of four) of half `h` of row r: 16 of the row's 128 codes, which lie in the 128-byte swizzle.
+__device__ __forceinline__ uint4 codes_at(const uint8_t* raw, int r, int h, int q) {
+  return *reinterpret_cast<const uint4*>(raw + r * 128 + (((4 * h + q) ^ (r & 7)) << 4));
+}
+// ... widened into a row of 64 f16 values, in the same swizzle.  Neighbouring lanes take neighbouring
+// rows, so that the reads and the writes of eight meet each bank once.
+__device__ __forceinline__ void store_widened(uint4 codes, uint8_t* dst, int r, int q) {
+  uint4 lo, hi;
+  widen(codes, lo, hi);
+  *reinterpret_cast<uint4*>(dst + r * 128 + (((2 * q) ^ (r & 7)) << 4)) = lo;
+  *reinterpret_cast<uint4*>(dst + r * 128 + (((2 * q + 1) ^ (r & 7)) << 4)) = hi;
 }
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -111,13 +132,11 @@ __global__ void __launch_bounds__(kInt8 ? 128 + 32 * kConvWarps : 128)
     split_kernel(const __grid_constant__ Maps maps, const Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  constexpr int kStepK = kInt8 ? 64 : 128;     // codes of a stage along K
   const int TN = a.TN, S = a.S, S2 = a.S2;
-  const int stage = (kRowsW + TN) * kStepK;    // what the copies fill
-  const int stage2 = (kRowsW + TN) * 128;      // operands: rows of 128 bytes
+  const int stage = (kRowsW + TN) * 128;       // rows of 128 codes, or of 64 widened ones
   uint8_t* ring2 = kInt8 ? sm : nullptr;       // widened operands, then the codes
-  uint8_t* ring = kInt8 ? sm + S2 * stage2 : sm;
-  const int ring_bytes = max(S * stage + (kInt8 ? S2 * stage2 : 0), TN * kRowsW * 4);
+  uint8_t* ring = kInt8 ? sm + S2 * stage : sm;
+  const int ring_bytes = max((S + S2) * stage, TN * kRowsW * 4);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + ring_bytes);
   uint64_t* empty = full + kMaxStages;
   uint64_t* full2 = empty + kMaxStages;
@@ -156,52 +175,76 @@ __global__ void __launch_bounds__(kInt8 ? 128 + 32 * kConvWarps : 128)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // A whole warp walks each loop and elects the lane that issues (in a loop of one lane the operands of
+  // copies and products, which are warp-uniform, cost hundreds of cycles a stage).
   if (warp == 0) {
-    if (lane == 0) {
-      bool ok = true;
-      int i = 0;
-      for (; i < kn; ++i) {
-        const int s = i % S;
-        if (i >= S && !(ok = wait_bar(&empty[s], ((i / S) & 1) ^ 1, a.hdr))) break;
-        mbar_arrive_expect_tx(&full[s], stage);
-        tma_load_2d(ring + s * stage, &maps.w, &full[s], (kb0 + i) * kStepK, n0);
-        tma_load_2d(ring + s * stage + kRowsW * kStepK, &maps.x, &full[s], (kb0 + i) * kStepK, t0);
+    Ring at;
+    int i = 0;
+    for (; i < kn; ++i, at.next(S)) {
+      if (i >= S && !wait_bar(&empty[at.s], at.round ^ 1, a.hdr)) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&full[at.s], stage);
+        tma_load_2d(ring + at.s * stage, &maps.w, &full[at.s], (kb0 + i) * kStepK, n0);
+        tma_load_2d(ring + at.s * stage + kRowsW * 128, &maps.x, &full[at.s], (kb0 + i) * kStepK, t0);
       }
-      // no copy outlives the block, whatever became of those who read them
-      for (int j = max(0, i - S); j < i; ++j) wait_bar(&full[j % S], (j / S) & 1, a.hdr);
+      __syncwarp();
     }
+    // no copy outlives the block, whatever became of those who read them
+    for (int j = max(0, i - S); j < i; ++j) wait_bar(&full[j % S], (j / S) & 1, a.hdr);
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_f32(128, TN, 0);   // f16 and e4m3 are both type 0 of their kinds
-      for (int i = 0; i < kn; ++i) {
-        const int s = kInt8 ? i % S2 : i % S;
-        if (!wait_bar(kInt8 ? &full2[s] : &full[s], (kInt8 ? i / S2 : i / S) & 1, a.hdr)) break;
-        tc_fence_after();
-        const uint8_t* w = kInt8 ? ring2 + s * stage2 : ring + s * stage;
-        const uint64_t wd = smem_desc(smem_u32(w), 16, 1024, kLayoutSw128);
-        const uint64_t xd = smem_desc(smem_u32(w + kRowsW * 128), 16, 1024, kLayoutSw128);
+    const uint32_t idesc = idesc_f32(128, TN, 0);   // f16 and e4m3 are both type 0 of their kinds
+    const int steps = kInt8 ? 2 * kn : kn;          // int8: half a stage of codes at a time
+    const int stages = kInt8 ? S2 : S;
+    uint64_t* landed = kInt8 ? full2 : full;
+    uint64_t* read = kInt8 ? empty2 : empty;
+    const uint64_t d0 = smem_desc(smem_u32(kInt8 ? ring2 : ring), 16, 1024, kLayoutSw128);
+    Ring at;
+    for (int i = 0; i < steps; ++i, at.next(stages)) {
+      if (!wait_bar(&landed[at.s], at.round, a.hdr)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t wd = d0 + (uint64_t)(at.s * (stage >> 4)), xd = wd + (kRowsW * 128 >> 4);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {   // 32 bytes of K at a time
           if (kInt8) mma_ss(tmem, wd + 2 * kk, xd + 2 * kk, idesc, (i | kk) != 0);
           else mma_ss_f8(tmem, wd + 2 * kk, xd + 2 * kk, idesc, (i | kk) != 0);
         }
-        mma_commit(kInt8 ? &empty2[s] : &empty[s]);
+        mma_commit(&read[at.s]);
       }
-      mma_commit(done);
+      __syncwarp();
     }
+    if (elect_one()) mma_commit(done);
+    __syncwarp();
   } else if (kInt8 && warp >= 4) {
-    for (int i = 0; i < kn; ++i) {
-      const int s = i % S, s2 = i % S2;
-      bool ok = wait_bar(&full[s], (i / S) & 1, a.hdr);
-      if (ok && i >= S2) ok = wait_bar(&empty2[s2], ((i / S2) & 1) ^ 1, a.hdr);
+    constexpr int kAhead = 3;   // rows of a lane whose codes are loaded together
+    const int rows = kRowsW + TN;
+    Ring from, to;
+    for (int i = 0; i < 2 * kn; ++i, to.next(S2)) {
+      bool ok = (i & 1) || wait_bar(&full[from.s], from.round, a.hdr);
+      if (ok && i >= S2) ok = wait_bar(&empty2[to.s], to.round ^ 1, a.hdr);
       if (!__all_sync(0xffffffffu, ok)) break;
-      widen_rows(ring + s * stage, ring2 + s2 * stage2, kRowsW + TN, tid - 128, 32 * kConvWarps);
+      const uint8_t* raw = ring + from.s * stage;
+      uint8_t* dst = ring2 + to.s * stage;
+      // a warp a piece column: pairs of warps share one, rows in turn
+      const int q = (warp - 4) >> 1;
+#pragma unroll 1
+      for (int r0 = 32 * (warp & 1) + lane; r0 < rows; r0 += 64 * kAhead) {
+        uint4 v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (r0 + 64 * j < rows) v[j] = codes_at(raw, r0 + 64 * j, i & 1, q);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (r0 + 64 * j < rows) store_widened(v[j], dst, r0 + 64 * j, q);
+      }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&empty[s]);
-        mbar_arrive(&full2[s2]);
+      if (elect_one()) {
+        if (i & 1) mbar_arrive(&empty[from.s]);
+        mbar_arrive(&full2[to.s]);
       }
+      __syncwarp();
+      if (i & 1) from.next(S);
     }
   }
   __syncwarp();
@@ -230,21 +273,36 @@ __global__ void __launch_bounds__(kInt8 ? 128 + 32 * kConvWarps : 128)
     const float4 ws = *reinterpret_cast<const float4*>(a.w_scale + n0 + 4 * lane);
     const int tokens = min(TN, a.T - t0);
     const int lo = tokens * (int)rank / a.C, hi = tokens * ((int)rank + 1) / a.C;
-    for (int t = lo + warp; t < hi; t += warps) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      const uint32_t at = smem_u32(part + t * kRowsW + 4 * lane);
-      for (int c = 0; c < a.C; ++c) {
-        const float4 u = ld_cluster_f4(a.C > 1 ? mapa_shared(at, c) : at);
-        v.x += u.x;
-        v.y += u.y;
-        v.z += u.z;
-        v.w += u.w;
+    for (int t1 = lo + warp; t1 < hi; t1 += 4 * warps) {   // four tokens at a time
+      float xs[4];
+      float4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = t1 + j * warps;
+        xs[j] = t < hi ? a.x_scale[t0 + t] : 0.f;
+        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      const float xs = a.x_scale[t0 + t];
-      const __nv_bfloat162 p = __floats2bfloat162_rn(v.x * xs * ws.x, v.y * xs * ws.y);
-      const __nv_bfloat162 q = __floats2bfloat162_rn(v.z * xs * ws.z, v.w * xs * ws.w);
-      *reinterpret_cast<uint2*>(a.out + (t0 + t) * a.out_stride + n0 + 4 * lane) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+      for (int c = 0; c < a.C; ++c) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t = min(t1 + j * warps, hi - 1);
+          const uint32_t at = smem_u32(part + t * kRowsW + 4 * lane);
+          const float4 u = ld_cluster_f4(a.C > 1 ? mapa_shared(at, c) : at);
+          v[j].x += u.x;
+          v[j].y += u.y;
+          v[j].z += u.z;
+          v[j].w += u.w;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = t1 + j * warps;
+        const __nv_bfloat162 p = __floats2bfloat162_rn(v[j].x * xs[j] * ws.x, v[j].y * xs[j] * ws.y);
+        const __nv_bfloat162 q = __floats2bfloat162_rn(v[j].z * xs[j] * ws.z, v[j].w * xs[j] * ws.w);
+        if (t < hi)
+          *reinterpret_cast<uint2*>(a.out + (t0 + t) * a.out_stride + n0 + 4 * lane) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+      }
     }
   }
   __syncwarp();
@@ -261,10 +319,9 @@ __global__ void __launch_bounds__(kInt8 ? 128 + 32 * kConvWarps : 128)
 template <bool kInt8>
 struct Pair {
   static constexpr int kN = kInt8 ? 192 : 256;              // channels of a tile
-  static constexpr int kStepK = kInt8 ? 64 : 128;           // codes of a stage
   static constexpr int kRows = 128 + kN / 2;                // rows of a stage in a CTA: its tokens, its channels
-  static constexpr int kStage = kRows * kStepK;
-  static constexpr int kStages = 6;
+  static constexpr int kStage = kRows * 128;
+  static constexpr int kStages = kInt8 ? 4 : 6;
   static constexpr int kStages2 = 4;                        // int8, widened: tokens 32 TMEM columns, channels a box
   static constexpr int kStage2 = kN / 2 * 128;
   static constexpr int kBoxOut = 128 * 128;                 // 128 tokens x 64 channels bf16
@@ -288,12 +345,6 @@ __device__ __forceinline__ Tile tile_of(int i, int mtiles, int ntiles, int kn) {
   return Tile{(8 * group + in % gm) * 256, in / gm * kn};
 }
 
-__device__ __forceinline__ bool wait_bar_cluster(uint64_t* bar, uint32_t parity, PlanHeader* hdr) {
-  if (mbar_wait<true>(bar, parity, kWaitLimitNs)) return true;
-  atomicOr(&hdr->status, kDeviceTimeout);
-  return false;
-}
-
 // Warp 0 copies, warp 1 (of the pair's first CTA) issues the products, warp 2 owns the tensor memory,
 // warps 4-7 are the epilogue; int8: warps 8-11 widen tokens (thread = row = TMEM lane), 12-15 channels.
 template <bool kInt8>
@@ -314,7 +365,7 @@ __global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 
   const int rank = (int)cluster_ctarank();
   const int mtiles = (a.T + 255) / 256, ntiles = (a.N + P::kN - 1) / P::kN;
   const int tiles = mtiles * ntiles, pairs = (int)gridDim.x / 2, first = (int)blockIdx.x / 2;
-  const int nkb = (a.K + P::kStepK - 1) / P::kStepK;
+  const int nkb = (a.K + kStepK - 1) / kStepK;
 
   if (tid == 0) {
     for (int s = 0; s < P::kStages; ++s) {
@@ -346,66 +397,65 @@ __global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 
   constexpr uint32_t kColA = 2 * P::kN;   // int8: columns of the widened tokens
 
   if (warp == 0) {
-    if (lane == 0) {
-      bool ok = true;
-      int i = 0;
-      for (int tile = first; tile < tiles && ok; tile += pairs) {
-        const Tile at = tile_of(tile, mtiles, ntiles, P::kN);
-        for (int kb = 0; kb < nkb; ++kb, ++i) {
-          const int s = i % P::kStages;
-          if (i >= P::kStages && !(ok = wait_bar(&empty[s], ((i / P::kStages) & 1) ^ 1, a.hdr))) break;
-          uint8_t* dst = sm + s * P::kStage;
+    bool ok = true;
+    Ring pos;
+    int i = 0;
+    for (int tile = first; tile < tiles && ok; tile += pairs) {
+      const Tile at = tile_of(tile, mtiles, ntiles, P::kN);
+      for (int kb = 0; kb < nkb; ++kb, ++i, pos.next(P::kStages)) {
+        if (i >= P::kStages && !(ok = wait_bar(&empty[pos.s], pos.round ^ 1, a.hdr))) break;
+        if (elect_one()) {
+          uint8_t* dst = sm + pos.s * P::kStage;
           if (kInt8) {
-            mbar_arrive_expect_tx(&full[s], P::kStage);
-            tma_load_2d(dst, &maps.x, &full[s], kb * P::kStepK, at.m0 + 128 * rank);
-            tma_load_2d(dst + 128 * P::kStepK, &maps.w, &full[s], kb * P::kStepK, at.n0 + P::kN / 2 * rank);
+            mbar_arrive_expect_tx(&full[pos.s], P::kStage);
+            tma_load_2d(dst, &maps.x, &full[pos.s], kb * kStepK, at.m0 + 128 * rank);
+            tma_load_2d(dst + 128 * 128, &maps.w, &full[pos.s], kb * kStepK, at.n0 + P::kN / 2 * rank);
           } else {
-            const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * P::kStage);
-            tma_load_2d_pair(dst, &maps.x, bar, kb * P::kStepK, at.m0 + 128 * rank);
-            tma_load_2d_pair(dst + 128 * P::kStepK, &maps.w, bar, kb * P::kStepK, at.n0 + P::kN / 2 * rank);
+            const uint32_t bar = mapa_shared(smem_u32(&full[pos.s]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[pos.s], 2 * P::kStage);
+            tma_load_2d_pair(dst, &maps.x, bar, kb * kStepK, at.m0 + 128 * rank);
+            tma_load_2d_pair(dst + 128 * 128, &maps.w, bar, kb * kStepK, at.n0 + P::kN / 2 * rank);
           }
         }
-      }
-      // no copy and no arrival outlives the pair, whatever became of those who wait for them
-      for (int j = max(0, i - P::kStages); j < i; ++j) {
-        if (kInt8 || rank == 0) wait_bar(&full[j % P::kStages], (j / P::kStages) & 1, a.hdr);
-        wait_bar(&empty[j % P::kStages], (j / P::kStages) & 1, a.hdr);
+        __syncwarp();
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      const uint32_t idesc = idesc_f32(256, P::kN, 0);   // f16 and e4m3 are both type 0 of their kinds
-      bool ok = true;
-      int i = 0, n = 0;
-      for (int tile = first; tile < tiles && ok; tile += pairs, ++n) {
-        const int b = n & 1;
-        const uint32_t d = tmem + b * P::kN;
-        if (n >= 2 && !(ok = wait_bar_cluster(&acc_empty[b], ((n >> 1) & 1) ^ 1, a.hdr))) break;
+    // no copy and no arrival outlives the pair, whatever became of those who wait for them
+    for (int j = max(0, i - P::kStages); j < i; ++j) {
+      if (kInt8 || rank == 0) wait_bar(&full[j % P::kStages], (j / P::kStages) & 1, a.hdr);
+      wait_bar(&empty[j % P::kStages], (j / P::kStages) & 1, a.hdr);
+    }
+  } else if (warp == 1 && rank == 0) {
+    const uint32_t idesc = idesc_f32(256, P::kN, 0);   // f16 and e4m3 are both type 0 of their kinds
+    const uint64_t d0 = smem_desc(smem_u32(sm + (kInt8 ? P::kRing2 : 0)), 16, 1024, kLayoutSw128);
+    bool ok = true;
+    Ring pos, acc;
+    int n = 0;
+    for (int tile = first; tile < tiles && ok; tile += pairs, ++n, acc.next(2)) {
+      const uint32_t d = tmem + acc.s * P::kN;
+      if (n >= 2 && !(ok = wait_bar(&acc_empty[acc.s], acc.round ^ 1, a.hdr))) break;
+      tc_fence_after();
+      for (int kb = 0; kb < (kInt8 ? 2 * nkb : nkb); ++kb, pos.next(kInt8 ? P::kStages2 : P::kStages)) {
+        if (!(ok = wait_bar(kInt8 ? &full2[pos.s] : &full[pos.s], pos.round, a.hdr))) break;
         tc_fence_after();
-        for (int kb = 0; kb < nkb; ++kb, ++i) {
+        if (elect_one()) {
           if (kInt8) {
-            const int s = i % P::kStages2;
-            if (!(ok = wait_bar_cluster(&full2[s], (i / P::kStages2) & 1, a.hdr))) break;
-            tc_fence_after();
-            const uint64_t wd = smem_desc(smem_u32(sm + P::kRing2 + s * P::kStage2), 16, 1024, kLayoutSw128);
+            const uint64_t wd = d0 + (uint64_t)(pos.s * (P::kStage2 >> 4));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_ts_pair(d, tmem + kColA + 32 * s + 8 * kk, wd + 2 * kk, idesc, (kb | kk) != 0);
-            mma_commit_pair(&empty2[s]);
+              mma_ts_pair(d, tmem + kColA + 32 * pos.s + 8 * kk, wd + 2 * kk, idesc, (kb | kk) != 0);
+            mma_commit_pair(&empty2[pos.s]);
           } else {
-            const int s = i % P::kStages;
-            if (!(ok = wait_bar_cluster(&full[s], (i / P::kStages) & 1, a.hdr))) break;
-            tc_fence_after();
-            const uint64_t xd = smem_desc(smem_u32(sm + s * P::kStage), 16, 1024, kLayoutSw128);
-            const uint64_t wd = smem_desc(smem_u32(sm + s * P::kStage + 128 * 128), 16, 1024, kLayoutSw128);
+            const uint64_t xd = d0 + (uint64_t)(pos.s * (P::kStage >> 4)), wd = xd + (128 * 128 >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) mma_ss_f8_pair(d, xd + 2 * kk, wd + 2 * kk, idesc, (kb | kk) != 0);
-            mma_commit_pair(&empty[s]);
+            mma_commit_pair(&empty[pos.s]);
           }
         }
-        mma_commit_pair(&acc_full[b]);
+        __syncwarp();
       }
+      if (elect_one()) mma_commit_pair(&acc_full[acc.s]);
+      __syncwarp();
     }
   } else if (warp >= 4 && warp < 8) {
     const int row = tid - 128;                       // token of the CTA's half = TMEM lane
@@ -430,7 +480,7 @@ __global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 
         if (c0 + 64 == P::kN) {   // the tile's accumulator is read
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[b]), 0));
+          if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&acc_empty[b]), 0));
         }
         // the box written two chunks ago has left (its writer waits), the scales are there
         uint8_t* dst = box + (chunk & 1) * P::kBoxOut;
@@ -465,43 +515,47 @@ __global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 
     const int row = tid & 127;
     int i = 0;
     bool ok = true;
+    Ring from, to;
     for (int tile = first; tile < tiles && ok; tile += pairs)
-      for (int kb = 0; kb < nkb; ++kb, ++i) {
-        const int s = i % P::kStages, s2 = i % P::kStages2;
-        ok = wait_bar(&full[s], (i / P::kStages) & 1, a.hdr);
-        if (ok && i >= P::kStages2) ok = wait_bar(&empty2[s2], ((i / P::kStages2) & 1) ^ 1, a.hdr);
+      for (int kb = 0; kb < 2 * nkb; ++kb, ++i, to.next(P::kStages2)) {   // half a stage of codes at a time
+        const int h = kb & 1;
+        ok = h || wait_bar(&full[from.s], from.round, a.hdr);
+        if (ok && i >= P::kStages2) ok = wait_bar(&empty2[to.s], to.round ^ 1, a.hdr);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        const uint8_t* raw = sm + s * P::kStage;
+        const uint8_t* raw = sm + from.s * P::kStage;
         if (tokens) {
           tc_fence_after();
+          uint4 v[4];
           uint32_t o[32];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {   // 64-byte rows in the 64-byte swizzle
+          for (int q = 0; q < 4; ++q) v[q] = codes_at(raw, row, h, q);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
             uint4 lo, hi;
-            widen(*reinterpret_cast<const uint4*>(raw + row * 64 + ((q ^ ((row >> 1) & 3)) << 4)), lo, hi);
+            widen(v[q], lo, hi);
             o[8 * q] = lo.x; o[8 * q + 1] = lo.y; o[8 * q + 2] = lo.z; o[8 * q + 3] = lo.w;
             o[8 * q + 4] = hi.x; o[8 * q + 5] = hi.y; o[8 * q + 6] = hi.z; o[8 * q + 7] = hi.w;
           }
-          tmem_st32(tmem + kColA + 32 * s2 + ((uint32_t)(32 * (warp & 3)) << 16), o);
+          tmem_st32(tmem + kColA + 32 * to.s + ((uint32_t)(32 * (warp & 3)) << 16), o);
           tmem_st_wait();
           tc_fence_before();
         } else {
-          uint8_t* dst = sm + P::kRing2 + s2 * P::kStage2;
-          for (int j = row; j < P::kN / 2 * 4; j += 128) {
-            const int r = j >> 2, q = j & 3;   // place q of row r holds the codes of piece p
-            const int p = q ^ ((r >> 1) & 3);
-            uint4 lo, hi;
-            widen(*reinterpret_cast<const uint4*>(raw + 128 * 64 + 16 * j), lo, hi);
-            *reinterpret_cast<uint4*>(dst + r * 128 + (((2 * p) ^ (r & 7)) << 4)) = lo;
-            *reinterpret_cast<uint4*>(dst + r * 128 + (((2 * p + 1) ^ (r & 7)) << 4)) = hi;
-          }
+          // warp 12 + q takes piece q of the CTA's channels
+          uint4 v[P::kN / 64];
+#pragma unroll
+          for (int j = 0; j < P::kN / 64; ++j) v[j] = codes_at(raw + 128 * 128, 32 * j + lane, h, warp & 3);
+#pragma unroll
+          for (int j = 0; j < P::kN / 64; ++j)
+            store_widened(v[j], sm + P::kRing2 + to.s * P::kStage2, 32 * j + lane, warp & 3);
           fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&empty[s]);
-          mbar_arrive_cluster(mapa_shared(smem_u32(&full2[s2]), 0));
+        if (elect_one()) {
+          if (h) mbar_arrive(&empty[from.s]);
+          mbar_arrive_remote(mapa_shared(smem_u32(&full2[to.s]), 0));
         }
+        __syncwarp();
+        if (h) from.next(P::kStages);
       }
     // the pair's last arrivals on this CTA's barriers
     if (warp == 8 && lane == 0)
@@ -517,15 +571,16 @@ __global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 
   }
 }
 
-// Rows of K codes as a tensor map with boxes of `rows` rows and `step` codes.
-bool encode_codes(CUtensorMap* m, const void* p, int K, int rows_total, int step, int rows, CUtensorMapSwizzle swizzle) {
+// Rows of K codes as a tensor map, boxes of `rows` rows of 128 codes.  (Boxes of 64 codes took three
+// times as long a byte.)
+bool encode_codes(CUtensorMap* m, const void* p, int K, int rows_total, int rows) {
   const wg::EncodeTiledFn fn = wg::encode_fn();
   cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows_total};
   cuuint64_t strides[1] = {(cuuint64_t)K};
-  cuuint32_t box[2] = {(cuuint32_t)step, (cuuint32_t)rows};
+  cuuint32_t box[2] = {kStepK, (cuuint32_t)rows};
   cuuint32_t es[2] = {1, 1};
   return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -543,26 +598,20 @@ bool encode_out(CUtensorMap* m, void* p, int T, int N, long long stride) {
 
 template <bool kInt8>
 cudaError_t launch_split(Args a, const void* x, const void* w, int sms, cudaStream_t s) {
-  constexpr int kStepK = kInt8 ? 64 : 128;
   Maps maps;
   a.TN = a.T >= kMaxTokens ? kMaxTokens : (a.T + 15) / 16 * 16;
   const int tiles = (a.N + kRowsW - 1) / kRowsW, ttiles = (a.T + a.TN - 1) / a.TN;
   const int nkb = (a.K + kStepK - 1) / kStepK;
   a.C = 1;
   while (a.C < 8 && (long long)tiles * ttiles * a.C * 2 <= sms && nkb >= 8 * a.C) a.C *= 2;
-  const int rows = kRowsW + a.TN, budget = 200 * 1024;
-  if (kInt8) {
-    a.S2 = std::min(4, budget * 2 / 3 / (rows * 128));
-    a.S = std::min(kMaxStages, (budget - a.S2 * rows * 128) / (rows * kStepK));
-  } else {
-    a.S2 = 0;
-    a.S = std::min(kMaxStages, budget / (rows * kStepK));
-  }
-  const CUtensorMapSwizzle swizzle = kInt8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
-  if (!encode_codes(&maps.w, w, a.K, a.N, kStepK, kRowsW, swizzle) ||
-      !encode_codes(&maps.x, x, a.K, a.T, kStepK, a.TN, swizzle))
+  // two blocks share an SM where there are more than SMs
+  const int stage = (kRowsW + a.TN) * 128, budget = (long long)tiles * ttiles * a.C > sms ? 100 * 1024 : 200 * 1024;
+  const int fit = std::max(2, budget / stage);
+  a.S2 = kInt8 ? std::max(1, std::min(4, fit / 2)) : 0;
+  a.S = std::min({kMaxStages, fit - a.S2, nkb});
+  if (!encode_codes(&maps.w, w, a.K, a.N, kRowsW) || !encode_codes(&maps.x, x, a.K, a.T, a.TN))
     return cudaErrorInvalidValue;
-  const size_t ring = std::max((size_t)a.S * rows * kStepK + (size_t)a.S2 * rows * 128, (size_t)a.TN * kRowsW * 4);
+  const size_t ring = std::max((size_t)(a.S + a.S2) * stage, (size_t)a.TN * kRowsW * 4);
   const size_t smem = 1024 + ring + (4 * kMaxStages + 2) * 8;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles * a.C, ttiles);
@@ -585,9 +634,7 @@ template <bool kInt8>
 cudaError_t launch_pair(const Args& a, const void* x, const void* w, int sms, cudaStream_t s) {
   using P = Pair<kInt8>;
   Maps maps;
-  const CUtensorMapSwizzle swizzle = kInt8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-  if (!encode_codes(&maps.x, x, a.K, a.T, P::kStepK, 128, swizzle) ||
-      !encode_codes(&maps.w, w, a.K, a.N, P::kStepK, P::kN / 2, swizzle) ||
+  if (!encode_codes(&maps.x, x, a.K, a.T, 128) || !encode_codes(&maps.w, w, a.K, a.N, P::kN / 2) ||
       !encode_out(&maps.out, a.out, a.T, a.N, a.out_stride))
     return cudaErrorInvalidValue;
   const long long tiles = (long long)((a.T + 255) / 256) * ((a.N + P::kN - 1) / P::kN);
