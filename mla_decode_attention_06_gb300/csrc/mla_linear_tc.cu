@@ -42,7 +42,7 @@ constexpr int kStepK = 128;            // codes of a stage along K
 constexpr int kRowsW = 128;            // output channels of a tile
 constexpr int kMaxTokens = 256;        // tokens of a tile (MMA N)
 constexpr int kMaxStages = 12;
-constexpr int kConvWarps = 8;          // int8: warps that widen codes
+constexpr int kConvWarps = 16;         // int8: warps that widen codes, eight for either half of a stage
 
 struct Maps {
   CUtensorMap w, x, out;
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kInt8 ? 128 + 32 * kConvWarps : 128)
     }
     if (kInt8)
       for (int s = 0; s < S2; ++s) {
-        mbar_init(&full2[s], kConvWarps);
+        mbar_init(&full2[s], kConvWarps / 2);
         mbar_init(&empty2[s], 1);
       }
     mbar_init(done, 1);
@@ -218,21 +218,23 @@ __global__ void __launch_bounds__(kInt8 ? 128 + 32 * kConvWarps : 128)
   } else if (kInt8 && warp >= 4) {
     constexpr int kAhead = 3;   // rows of a lane whose codes are loaded together
     const int rows = kRowsW + TN;
+    const int h = (warp - 4) >> 3;   // its half of every stage
     Ring from, to;
-    for (int i = 0; i < 2 * kn; ++i, to.next(S2)) {
-      bool ok = (i & 1) || wait_bar(&full[from.s], from.round, a.hdr);
+    if (h) to.next(S2);
+    for (int i = h; i < 2 * kn; i += 2, from.next(S)) {
+      bool ok = wait_bar(&full[from.s], from.round, a.hdr);
       if (ok && i >= S2) ok = wait_bar(&empty2[to.s], to.round ^ 1, a.hdr);
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint8_t* raw = ring + from.s * stage;
       uint8_t* dst = ring2 + to.s * stage;
       // a warp a piece column: pairs of warps share one, rows in turn
-      const int q = (warp - 4) >> 1;
+      const int q = (warp >> 1) & 3;
 #pragma unroll 1
       for (int r0 = 32 * (warp & 1) + lane; r0 < rows; r0 += 64 * kAhead) {
         uint4 v[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
-          if (r0 + 64 * j < rows) v[j] = codes_at(raw, r0 + 64 * j, i & 1, q);
+          if (r0 + 64 * j < rows) v[j] = codes_at(raw, r0 + 64 * j, h, q);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
           if (r0 + 64 * j < rows) store_widened(v[j], dst, r0 + 64 * j, q);
@@ -240,11 +242,12 @@ __global__ void __launch_bounds__(kInt8 ? 128 + 32 * kConvWarps : 128)
       fence_proxy_async_smem();
       __syncwarp();
       if (elect_one()) {
-        if (i & 1) mbar_arrive(&empty[from.s]);
+        mbar_arrive(&empty[from.s]);
         mbar_arrive(&full2[to.s]);
       }
       __syncwarp();
-      if (i & 1) from.next(S);
+      to.next(S2);
+      to.next(S2);
     }
   }
   __syncwarp();
@@ -331,7 +334,7 @@ struct Pair {
   static constexpr int kBars = kScales + kN * 4;
   static constexpr int kSmem = 1024 + kBars + 8 * (2 * kStages + 2 * kStages2 + 4) + 16;
   static_assert(kSmem <= 232448);
-  static constexpr int kThreads = kInt8 ? 512 : 256;
+  static constexpr int kThreads = kInt8 ? 768 : 256;
 };
 
 // Tile i of a call: tokens from m0, channels from n0.  Groups of 8 token tiles, channel tiles in turn
@@ -346,7 +349,8 @@ __device__ __forceinline__ Tile tile_of(int i, int mtiles, int ntiles, int kn) {
 }
 
 // Warp 0 copies, warp 1 (of the pair's first CTA) issues the products, warp 2 owns the tensor memory,
-// warps 4-7 are the epilogue; int8: warps 8-11 widen tokens (thread = row = TMEM lane), 12-15 channels.
+// warps 4-7 are the epilogue; int8: warps 8-11 widen the first half of a stage's tokens (thread = row =
+// TMEM lane), 12-15 of its channels, 16-23 the second half's.
 template <bool kInt8>
 __global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 1, 1)
     pair_kernel(const __grid_constant__ Maps maps, const Args a) {
@@ -370,7 +374,7 @@ __global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 
   if (tid == 0) {
     for (int s = 0; s < P::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kInt8 ? 8 : 1);
+      mbar_init(&empty[s], kInt8 ? 16 : 1);
     }
     for (int s = 0; s < P::kStages2; ++s) {
       mbar_init(&full2[s], 16);
@@ -473,33 +477,39 @@ __global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 
       tc_fence_after();
 #pragma unroll 1
       for (int c0 = 0; c0 < P::kN; c0 += 64, ++chunk) {
-        uint32_t r[2][32];
-        tmem_ld32(tmem + b * P::kN + c0 + lanes, r[0]);
-        tmem_ld32(tmem + b * P::kN + c0 + 32 + lanes, r[1]);
-        tmem_ld_wait();
-        if (c0 + 64 == P::kN) {   // the tile's accumulator is read
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&acc_empty[b]), 0));
-        }
-        // the box written two chunks ago has left (its writer waits), the scales are there
         uint8_t* dst = box + (chunk & 1) * P::kBoxOut;
-        if (row == 0) bulk_wait_read<1>();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          uint32_t o[4];
-#pragma unroll
-          for (int j = 0; j < 4; j += 2) {
-            const int c = 8 * g + 2 * j;
-            const float4 w4 = *reinterpret_cast<const float4*>(ws + c0 + c);
-            const uint32_t* v = &r[c >> 5][c & 31];
-            const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(v[0]) * xs * w4.x, __uint_as_float(v[1]) * xs * w4.y);
-            const __nv_bfloat162 q = __floats2bfloat162_rn(__uint_as_float(v[2]) * xs * w4.z, __uint_as_float(v[3]) * xs * w4.w);
-            o[j] = *reinterpret_cast<const uint32_t*>(&p);
-            o[j + 1] = *reinterpret_cast<const uint32_t*>(&q);
+        for (int half = 0; half < 2; ++half) {
+          uint32_t r[32];
+          tmem_ld32(tmem + b * P::kN + c0 + 32 * half + lanes, r);
+          if (half == 0) {
+            // the box written two chunks ago has left (its writer waits), the scales are there
+            if (row == 0) bulk_wait_read<1>();
+            asm volatile("bar.sync 1, 128;" ::: "memory");
           }
-          *reinterpret_cast<uint4*>(dst + row * 128 + ((g ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          tmem_ld_wait();
+          if (half == 1 && c0 + 64 == P::kN) {   // the tile's accumulator is read
+            tc_fence_before();
+            __syncwarp();
+            if (elect_one()) mbar_arrive_remote(mapa_shared(smem_u32(&acc_empty[b]), 0));
+          }
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              const int c = 8 * g + 2 * j;
+              const float4 w4 = *reinterpret_cast<const float4*>(ws + c0 + 32 * half + c);
+              const __nv_bfloat162 p =
+                  __floats2bfloat162_rn(__uint_as_float(r[c]) * xs * w4.x, __uint_as_float(r[c + 1]) * xs * w4.y);
+              const __nv_bfloat162 q =
+                  __floats2bfloat162_rn(__uint_as_float(r[c + 2]) * xs * w4.z, __uint_as_float(r[c + 3]) * xs * w4.w);
+              o[j] = *reinterpret_cast<const uint32_t*>(&p);
+              o[j + 1] = *reinterpret_cast<const uint32_t*>(&q);
+            }
+            *reinterpret_cast<uint4*>(dst + row * 128 + (((4 * half + g) ^ (row & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
         }
         fence_proxy_async_smem();
         asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -511,15 +521,15 @@ __global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 
     }
     if (row == 0) bulk_wait_all();
   } else if (kInt8 && warp >= 8) {
-    const bool tokens = warp < 12;
-    const int row = tid & 127;
-    int i = 0;
+    const bool tokens = (warp & 4) == 0;
+    const int row = tid & 127, h = (warp - 8) >> 3;   // its half of every stage
+    int i = h;
     bool ok = true;
     Ring from, to;
+    if (h) to.next(P::kStages2);
     for (int tile = first; tile < tiles && ok; tile += pairs)
-      for (int kb = 0; kb < 2 * nkb; ++kb, ++i, to.next(P::kStages2)) {   // half a stage of codes at a time
-        const int h = kb & 1;
-        ok = h || wait_bar(&full[from.s], from.round, a.hdr);
+      for (int kb = 0; kb < nkb; ++kb, i += 2) {
+        ok = wait_bar(&full[from.s], from.round, a.hdr);
         if (ok && i >= P::kStages2) ok = wait_bar(&empty2[to.s], to.round ^ 1, a.hdr);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         const uint8_t* raw = sm + from.s * P::kStage;
@@ -540,7 +550,7 @@ __global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 
           tmem_st_wait();
           tc_fence_before();
         } else {
-          // warp 12 + q takes piece q of the CTA's channels
+          // each of four warps takes a piece of the CTA's channels
           uint4 v[P::kN / 64];
 #pragma unroll
           for (int j = 0; j < P::kN / 64; ++j) v[j] = codes_at(raw + 128 * 128, 32 * j + lane, h, warp & 3);
@@ -551,15 +561,17 @@ __global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 
         }
         __syncwarp();
         if (elect_one()) {
-          if (h) mbar_arrive(&empty[from.s]);
+          mbar_arrive(&empty[from.s]);
           mbar_arrive_remote(mapa_shared(smem_u32(&full2[to.s]), 0));
         }
         __syncwarp();
-        if (h) from.next(P::kStages);
+        from.next(P::kStages);
+        to.next(P::kStages2);
+        to.next(P::kStages2);
       }
     // the pair's last arrivals on this CTA's barriers
-    if (warp == 8 && lane == 0)
-      for (int j = max(0, i - P::kStages2); j < i; ++j) wait_bar(&empty2[j % P::kStages2], (j / P::kStages2) & 1, a.hdr);
+    if (warp == 16)   // half 1: i is one past the last
+      for (int j = max(0, i - 1 - P::kStages2); j < i - 1; ++j) wait_bar(&empty2[j % P::kStages2], (j / P::kStages2) & 1, a.hdr);
   }
   __syncwarp();
   tc_fence_before();
