@@ -42,7 +42,7 @@ constexpr int kStepK = 128;            // codes of a stage along K
 constexpr int kRowsW = 128;            // output channels of a tile
 constexpr int kMaxTokens = 256;        // tokens of a tile (MMA N)
 constexpr int kMaxStages = 12;
-constexpr int kConvWarps = 16;         // int8: warps that widen codes, eight for either half of a stage
+constexpr int kConvWarps = 8;          // split kernel, int8: warps that widen codes, four for either half of a stage
 
 struct Maps {
   CUtensorMap w, x, out;
@@ -51,7 +51,7 @@ struct Maps {
 struct Args {
   int T, N, K;
   int TN;                 // tokens of a tile
-  int S, S2;              // stages of the ring the copies fill; int8: of the ring of widened operands
+  int S, S2;              // stages of the ring the copies fill; int8: of the ring of widened operands (even)
   int C;                  // CTAs that split K
   long long out_stride;
   const float* x_scale;
@@ -216,9 +216,9 @@ __global__ void __launch_bounds__(kInt8 ? 128 + 32 * kConvWarps : 128)
     if (elect_one()) mma_commit(done);
     __syncwarp();
   } else if (kInt8 && warp >= 4) {
-    constexpr int kAhead = 3;   // rows of a lane whose codes are loaded together
+    constexpr int kAhead = 4;   // rows of a lane whose codes are loaded together
     const int rows = kRowsW + TN;
-    const int h = (warp - 4) >> 3;   // its half of every stage
+    const int h = (warp - 4) >> 2, q = warp & 3;   // its half of every stage, its piece of every row
     Ring from, to;
     if (h) to.next(S2);
     for (int i = h; i < 2 * kn; i += 2, from.next(S)) {
@@ -227,17 +227,15 @@ __global__ void __launch_bounds__(kInt8 ? 128 + 32 * kConvWarps : 128)
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint8_t* raw = ring + from.s * stage;
       uint8_t* dst = ring2 + to.s * stage;
-      // a warp a piece column: pairs of warps share one, rows in turn
-      const int q = (warp >> 1) & 3;
 #pragma unroll 1
-      for (int r0 = 32 * (warp & 1) + lane; r0 < rows; r0 += 64 * kAhead) {
+      for (int r0 = lane; r0 < rows; r0 += 32 * kAhead) {
         uint4 v[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
-          if (r0 + 64 * j < rows) v[j] = codes_at(raw, r0 + 64 * j, h, q);
+          if (r0 + 32 * j < rows) v[j] = codes_at(raw, r0 + 32 * j, h, q);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
-          if (r0 + 64 * j < rows) store_widened(v[j], dst, r0 + 64 * j, q);
+          if (r0 + 32 * j < rows) store_widened(v[j], dst, r0 + 32 * j, q);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -616,10 +614,11 @@ cudaError_t launch_split(Args a, const void* x, const void* w, int sms, cudaStre
   const int nkb = (a.K + kStepK - 1) / kStepK;
   a.C = 1;
   while (a.C < 8 && (long long)tiles * ttiles * a.C * 2 <= sms && nkb >= 8 * a.C) a.C *= 2;
-  // two blocks share an SM where there are more than SMs
-  const int stage = (kRowsW + a.TN) * 128, budget = (long long)tiles * ttiles * a.C > sms ? 100 * 1024 : 200 * 1024;
-  const int fit = std::max(2, budget / stage);
-  a.S2 = kInt8 ? std::max(1, std::min(4, fit / 2)) : 0;
+  // Two blocks share an SM where there are more than SMs, and where clusters are large: of eight blocks that
+  // fill an SM each the device holds 16 (17 tiles of one token took two waves, 19 us).
+  const int stage = (kRowsW + a.TN) * 128, budget = (long long)tiles * ttiles * a.C > sms || a.C > 2 ? 108 * 1024 : 200 * 1024;
+  const int fit = std::max(kInt8 ? 4 : 2, budget / stage);
+  a.S2 = kInt8 ? (fit >= 8 ? 4 : 2) : 0;   // even: the warps of either half wait for places of their own
   a.S = std::min({kMaxStages, fit - a.S2, nkb});
   if (!encode_codes(&maps.w, w, a.K, a.N, kRowsW) || !encode_codes(&maps.x, x, a.K, a.T, a.TN))
     return cudaErrorInvalidValue;
