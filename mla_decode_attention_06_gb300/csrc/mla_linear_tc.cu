@@ -40,7 +40,7 @@ using namespace sm100;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr int kStepK = 128;            // codes of a stage along K
 constexpr int kRowsW = 128;            // output channels of a tile
-constexpr int kMaxTokens = 256;        // tokens of a tile (MMA N)
+constexpr int kMaxTokens = 128;        // tokens of a split tile (MMA N)
 constexpr int kMaxStages = 12;
 constexpr int kConvWarps = 8;          // split kernel, int8: warps that widen codes, four for either half of a stage
 
@@ -125,10 +125,13 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
+template <bool kInt8>
+constexpr int kSplitThreads = kInt8 ? 128 + 32 * kConvWarps : 256;
+
 // Threads: warp 0 copies, warp 1 issues the products and owns the tensor memory, warps 4 on widen
 // (int8); all of them take part in the epilogue.
 template <bool kInt8>
-__global__ void __launch_bounds__(kInt8 ? 128 + 32 * kConvWarps : 128)
+__global__ void __launch_bounds__(kSplitThreads<kInt8>, 2)
     split_kernel(const __grid_constant__ Maps maps, const Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -274,35 +277,31 @@ __global__ void __launch_bounds__(kInt8 ? 128 + 32 * kConvWarps : 128)
     const float4 ws = *reinterpret_cast<const float4*>(a.w_scale + n0 + 4 * lane);
     const int tokens = min(TN, a.T - t0);
     const int lo = tokens * (int)rank / a.C, hi = tokens * ((int)rank + 1) / a.C;
-    for (int t1 = lo + warp; t1 < hi; t1 += 4 * warps) {   // four tokens at a time
-      float xs[4];
-      float4 v[4];
+    // eight partials at a time, of 8 / C tokens (C a power of two up to 8), all loads out before the first sum
+    const int cmask = a.C - 1, cshift = 31 - __clz(a.C);
+    for (int t1 = lo + warp; t1 < hi; t1 += (8 >> cshift) * warps) {
+      float4 u[8], v = make_float4(0.f, 0.f, 0.f, 0.f);
+      float xs[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = t1 + j * warps;
-        xs[j] = t < hi ? a.x_scale[t0 + t] : 0.f;
-        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      for (int c = 0; c < a.C; ++c) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = min(t1 + j * warps, hi - 1);
-          const uint32_t at = smem_u32(part + t * kRowsW + 4 * lane);
-          const float4 u = ld_cluster_f4(a.C > 1 ? mapa_shared(at, c) : at);
-          v[j].x += u.x;
-          v[j].y += u.y;
-          v[j].z += u.z;
-          v[j].w += u.w;
-        }
+      for (int j = 0; j < 8; ++j) {
+        const int t = min(t1 + (j >> cshift) * warps, hi - 1);
+        const uint32_t at = smem_u32(part + t * kRowsW + 4 * lane);
+        u[j] = ld_cluster_f4(a.C > 1 ? mapa_shared(at, j & cmask) : at);
+        xs[j] = a.x_scale[t0 + t];
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = t1 + j * warps;
-        const __nv_bfloat162 p = __floats2bfloat162_rn(v[j].x * xs[j] * ws.x, v[j].y * xs[j] * ws.y);
-        const __nv_bfloat162 q = __floats2bfloat162_rn(v[j].z * xs[j] * ws.z, v[j].w * xs[j] * ws.w);
-        if (t < hi)
-          *reinterpret_cast<uint2*>(a.out + (t0 + t) * a.out_stride + n0 + 4 * lane) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+      for (int j = 0; j < 8; ++j) {
+        const bool first = (j & cmask) == 0;
+        v.x = (first ? 0.f : v.x) + u[j].x;
+        v.y = (first ? 0.f : v.y) + u[j].y;
+        v.z = (first ? 0.f : v.z) + u[j].z;
+        v.w = (first ? 0.f : v.w) + u[j].w;
+        const int t = t1 + (j >> cshift) * warps;
+        if ((j & cmask) != cmask || t >= hi) continue;
+        const __nv_bfloat162 p = __floats2bfloat162_rn(v.x * xs[j] * ws.x, v.y * xs[j] * ws.y);
+        const __nv_bfloat162 q = __floats2bfloat162_rn(v.z * xs[j] * ws.z, v.w * xs[j] * ws.w);
+        *reinterpret_cast<uint2*>(a.out + (t0 + t) * a.out_stride + n0 + 4 * lane) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
       }
     }
   }
@@ -317,21 +316,24 @@ __global__ void __launch_bounds__(kInt8 ? 128 + 32 * kConvWarps : 128)
 
 // ------------------------------------------------------------------ many tokens
 
-template <bool kInt8>
+// kW: channels of a tile.  int8 tiles of 256 leave no room for a second accumulator beside the widened tokens.
+template <bool kInt8, int kW>
 struct Pair {
-  static constexpr int kN = kInt8 ? 192 : 256;              // channels of a tile
+  static constexpr int kN = kW;
   static constexpr int kRows = 128 + kN / 2;                // rows of a stage in a CTA: its tokens, its channels
   static constexpr int kStage = kRows * 128;
-  static constexpr int kStages = kInt8 ? 4 : 6;
+  static constexpr int kStages = kInt8 ? (kN == 256 ? 3 : 4) : (kN == 128 ? 8 : 6);
   static constexpr int kStages2 = 4;                        // int8, widened: tokens 32 TMEM columns, channels a box
   static constexpr int kStage2 = kN / 2 * 128;
+  static constexpr int kAccs = kInt8 && kN == 256 ? 1 : 2;  // accumulators
+  static constexpr int kColA = 384;                         // int8: TMEM columns of the widened tokens
   static constexpr int kBoxOut = 128 * 128;                 // 128 tokens x 64 channels bf16
   static constexpr int kRing2 = kStages * kStage;
   static constexpr int kOut = kRing2 + (kInt8 ? kStages2 * kStage2 : 0);
   static constexpr int kScales = kOut + 2 * kBoxOut;        // [kN] channel scales
   static constexpr int kBars = kScales + kN * 4;
   static constexpr int kSmem = 1024 + kBars + 8 * (2 * kStages + 2 * kStages2 + 4) + 16;
-  static_assert(kSmem <= 232448);
+  static_assert(kSmem <= 232448 && (!kInt8 || kAccs * kN <= kColA));
   static constexpr int kThreads = kInt8 ? 768 : 256;
 };
 
@@ -349,10 +351,10 @@ __device__ __forceinline__ Tile tile_of(int i, int mtiles, int ntiles, int kn) {
 // Warp 0 copies, warp 1 (of the pair's first CTA) issues the products, warp 2 owns the tensor memory,
 // warps 4-7 are the epilogue; int8: warps 8-11 widen the first half of a stage's tokens (thread = row =
 // TMEM lane), 12-15 of its channels, 16-23 the second half's.
-template <bool kInt8>
-__global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 1, 1)
+template <bool kInt8, int kW>
+__global__ void __launch_bounds__(Pair<kInt8, kW>::kThreads, 1) __cluster_dims__(2, 1, 1)
     pair_kernel(const __grid_constant__ Maps maps, const Args a) {
-  using P = Pair<kInt8>;
+  using P = Pair<kInt8, kW>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + P::kBars);   // e4m3: the first CTA's, for both; int8: each its own
@@ -396,7 +398,6 @@ __global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 
   cluster_sync();   // the other CTA's barriers are there
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  constexpr uint32_t kColA = 2 * P::kN;   // int8: columns of the widened tokens
 
   if (warp == 0) {
     bool ok = true;
@@ -433,9 +434,9 @@ __global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 
     bool ok = true;
     Ring pos, acc;
     int n = 0;
-    for (int tile = first; tile < tiles && ok; tile += pairs, ++n, acc.next(2)) {
+    for (int tile = first; tile < tiles && ok; tile += pairs, ++n, acc.next(P::kAccs)) {
       const uint32_t d = tmem + acc.s * P::kN;
-      if (n >= 2 && !(ok = wait_bar(&acc_empty[acc.s], acc.round ^ 1, a.hdr))) break;
+      if (n >= P::kAccs && !(ok = wait_bar(&acc_empty[acc.s], acc.round ^ 1, a.hdr))) break;
       tc_fence_after();
       for (int kb = 0; kb < (kInt8 ? 2 * nkb : nkb); ++kb, pos.next(kInt8 ? P::kStages2 : P::kStages)) {
         if (!(ok = wait_bar(kInt8 ? &full2[pos.s] : &full[pos.s], pos.round, a.hdr))) break;
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 
             const uint64_t wd = d0 + (uint64_t)(pos.s * (P::kStage2 >> 4));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_ts_pair(d, tmem + kColA + 32 * pos.s + 8 * kk, wd + 2 * kk, idesc, (kb | kk) != 0);
+              mma_ts_pair(d, tmem + P::kColA + 32 * pos.s + 8 * kk, wd + 2 * kk, idesc, (kb | kk) != 0);
             mma_commit_pair(&empty2[pos.s]);
           } else {
             const uint64_t xd = d0 + (uint64_t)(pos.s * (P::kStage >> 4)), wd = xd + (128 * 128 >> 4);
@@ -464,13 +465,14 @@ __global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 
     uint8_t* box = sm + P::kOut;
     float* ws = reinterpret_cast<float*>(sm + P::kScales);   // read between a chunk's two barriers only
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    int n = 0, chunk = 0;
-    for (int tile = first; tile < tiles; tile += pairs, ++n) {
+    int chunk = 0;
+    Ring acc;
+    for (int tile = first; tile < tiles; tile += pairs, acc.next(P::kAccs)) {
       const Tile at = tile_of(tile, mtiles, ntiles, P::kN);
-      const int b = n & 1, m0 = at.m0 + 128 * rank;
+      const int b = acc.s, m0 = at.m0 + 128 * rank;
       for (int c = row; c < P::kN; c += 128) ws[c] = at.n0 + c < a.N ? a.w_scale[at.n0 + c] : 0.f;
       const float xs = m0 + row < a.T ? a.x_scale[m0 + row] : 0.f;
-      bool ok = wait_bar(&acc_full[b], (n >> 1) & 1, a.hdr);
+      bool ok = wait_bar(&acc_full[b], acc.round, a.hdr);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
 #pragma unroll 1
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(Pair<kInt8>::kThreads, 1) __cluster_dims__(2, 
             o[8 * q] = lo.x; o[8 * q + 1] = lo.y; o[8 * q + 2] = lo.z; o[8 * q + 3] = lo.w;
             o[8 * q + 4] = hi.x; o[8 * q + 5] = hi.y; o[8 * q + 6] = hi.z; o[8 * q + 7] = hi.w;
           }
-          tmem_st32(tmem + kColA + 32 * to.s + ((uint32_t)(32 * (warp & 3)) << 16), o);
+          tmem_st32(tmem + P::kColA + 32 * to.s + ((uint32_t)(32 * (warp & 3)) << 16), o);
           tmem_st_wait();
           tc_fence_before();
         } else {
@@ -618,7 +620,7 @@ cudaError_t launch_split(Args a, const void* x, const void* w, int sms, cudaStre
   // fill an SM each the device holds 16 (17 tiles of one token took two waves, 19 us).
   const int stage = (kRowsW + a.TN) * 128, budget = (long long)tiles * ttiles * a.C > sms || a.C > 2 ? 108 * 1024 : 200 * 1024;
   const int fit = std::max(kInt8 ? 4 : 2, budget / stage);
-  a.S2 = kInt8 ? (fit >= 8 ? 4 : 2) : 0;   // even: the warps of either half wait for places of their own
+  a.S2 = kInt8 ? (fit >= 6 ? 4 : 2) : 0;   // even: the warps of either half wait for places of their own
   a.S = std::min({kMaxStages, fit - a.S2, nkb});
   if (!encode_codes(&maps.w, w, a.K, a.N, kRowsW) || !encode_codes(&maps.x, x, a.K, a.T, a.TN))
     return cudaErrorInvalidValue;
@@ -626,7 +628,7 @@ cudaError_t launch_split(Args a, const void* x, const void* w, int sms, cudaStre
   const size_t smem = 1024 + ring + (4 * kMaxStages + 2) * 8;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles * a.C, ttiles);
-  cfg.blockDim = dim3(kInt8 ? 128 + 32 * kConvWarps : 128);
+  cfg.blockDim = dim3(kSplitThreads<kInt8>);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -641,19 +643,52 @@ cudaError_t launch_split(Args a, const void* x, const void* w, int sms, cudaStre
   return e;
 }
 
-template <bool kInt8>
+template <bool kInt8, int kW>
 cudaError_t launch_pair(const Args& a, const void* x, const void* w, int sms, cudaStream_t s) {
-  using P = Pair<kInt8>;
+  using P = Pair<kInt8, kW>;
   Maps maps;
   if (!encode_codes(&maps.x, x, a.K, a.T, 128) || !encode_codes(&maps.w, w, a.K, a.N, P::kN / 2) ||
       !encode_out(&maps.out, a.out, a.T, a.N, a.out_stride))
     return cudaErrorInvalidValue;
   const long long tiles = (long long)((a.T + 255) / 256) * ((a.N + P::kN - 1) / P::kN);
   const int pairs = (int)std::min<long long>(tiles, sms / 2);
-  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(pair_kernel<kInt8>), P::kSmem);
+  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(pair_kernel<kInt8, kW>), P::kSmem);
   if (e != cudaSuccess) return e;
-  pair_kernel<kInt8><<<2 * pairs, P::kThreads, P::kSmem, s>>>(maps, a);
+  pair_kernel<kInt8, kW><<<2 * pairs, P::kThreads, P::kSmem, s>>>(maps, a);
   return cudaGetLastError();
+}
+
+// The width of the pair kernel's tiles: the one that takes least time by its number of rounds of tiles over the
+// pairs of SMs, the wider of two equals.  A round of e4m3 tiles takes as long as its width and a
+// quarter more of the widest (333 tokens, 8,192 x 16,384, a round of 256, 192, 128: 44, 33, 25.5 us;
+// 4,096 tokens, 24,576 x 1,536: 4.5, 3.8, 2.8 us); one of int8 tiles is held up by the widening of
+// its tokens' codes where it is narrow (84, 70, 68 us; 9.7, 6.9, 6.4 us).
+template <bool kInt8>
+int pair_width(int T, int N, int sms) {
+  int best = 0;
+  long long least = 0;
+  for (int w : {256, 192, 128}) {
+    const long long tiles = (long long)((T + 255) / 256) * ((N + w - 1) / w);
+    const long long cost = (tiles + sms / 2 - 1) / (sms / 2) * (kInt8 ? std::max(w, 184) : w + 64);
+    if (best == 0 || cost < least) {
+      best = w;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+template <bool kInt8>
+cudaError_t launch(const Args& a, const void* x, const void* w, int sms, cudaStream_t s) {
+  // Above 128 tokens a pair's 256 rows cost less than they waste (192 tokens, 8,192 x 16,384: 70 us against 83
+  // for int8, 33 against 34 for e4m3; 256: 70 against 91, 34 against 40); above 64 where the split kernel's
+  // tiles are more than the SMs (128 tokens, 24,576 x 1,536: 20.5 against 34.5, 13.2 against 14.1).
+  if (a.T <= 64 || (a.T <= 128 && (a.N + kRowsW - 1) / kRowsW <= sms)) return launch_split<kInt8>(a, x, w, sms, s);
+  switch (pair_width<kInt8>(a.T, a.N, sms)) {
+    case 256: return launch_pair<kInt8, 256>(a, x, w, sms, s);
+    case 192: return launch_pair<kInt8, 192>(a, x, w, sms, s);
+    default: return launch_pair<kInt8, 128>(a, x, w, sms, s);
+  }
 }
 
 }  // namespace lin
@@ -674,8 +709,7 @@ cudaError_t launch_linear(bool int8, int T, int N, int K, const void* x, const f
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  if (T > lin::kMaxTokens) return int8 ? lin::launch_pair<true>(a, x, w, sms, s) : lin::launch_pair<false>(a, x, w, sms, s);
-  return int8 ? lin::launch_split<true>(a, x, w, sms, s) : lin::launch_split<false>(a, x, w, sms, s);
+  return int8 ? lin::launch<true>(a, x, w, sms, s) : lin::launch<false>(a, x, w, sms, s);
 }
 
 }  // namespace mla
