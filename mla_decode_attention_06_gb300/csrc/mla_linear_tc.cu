@@ -13,6 +13,10 @@
 // splits K: each leaves its fp32 partial in its shared memory and sums a share of the tokens over the
 // cluster, in rank order (the result does not depend on timing).
 //
+// Up to eight int8 tokens (dot kernel).  Widening costs the split kernel more than the weights' way from memory
+// does, so here warps take the dot products of codes on the integer units (four a lane and
+// instruction, exact), straight from registers; K is split over a block's warps where rows are few.
+//
 // Many tokens (pair kernel).  One pair of CTAs a pair of SMs, cta_group::2: 256 tokens (A) by 256
 // channels (B; int8 192), each CTA loading half of either operand, one tile after another.  Tiles go
 // group by group of token tiles, so that those in flight share operands in L2.  The accumulator is
@@ -312,6 +316,70 @@ __global__ void __launch_bounds__(kSplitThreads<kInt8>, 2)
     tc_fence_after();
     tmem_dealloc(tmem, tcols);
   }
+}
+
+// ------------------------------------------------------------------ up to eight int8 tokens
+
+constexpr int kDotWarps = 8;
+constexpr int kDotMaxK = 1 << 16;    // 2^16 products of up to 2^14 each stay within 32 bits
+
+// TT: tokens, R: rows of weights (channels) of a warp.  `along` of a block's warps (a power of two) share the
+// rows and split K.
+template <int TT, int R>
+__global__ void __launch_bounds__(32 * kDotWarps) dot_kernel(const int8_t* __restrict__ x, const int8_t* __restrict__ w,
+                                                             const Args a, int along) {
+  constexpr int kAhead = R * TT >= 16 ? 1 : 8 / (R + TT) > 1 ? 8 / (R + TT) : 2;   // steps whose loads are out together
+  __shared__ int part[kDotWarps][R * TT];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n0 = ((int)blockIdx.x * (kDotWarps / along) + warp / along) * R;
+  const int pieces = a.K / 16, step = 32 * along;
+  const uint4* xp[TT];
+  const uint4* wp[R];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) xp[t] = reinterpret_cast<const uint4*>(x + (size_t)min(t, a.T - 1) * a.K);
+#pragma unroll
+  for (int r = 0; r < R; ++r) wp[r] = reinterpret_cast<const uint4*>(w + (size_t)min(n0 + r, a.N - 1) * a.K);
+  int acc[R * TT] = {};
+#pragma unroll 1
+  for (int c = (warp & (along - 1)) * 32 + lane; c < pieces; c += kAhead * step) {
+    uint4 wv[kAhead][R], xv[kAhead][TT];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const bool in = c + u * step < pieces;
+#pragma unroll
+      for (int r = 0; r < R; ++r) wv[u][r] = in ? __ldcs(wp[r] + c + u * step) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) xv[u][t] = in ? __ldg(xp[t] + c + u * step) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          int s = acc[r * TT + t];
+          s = __dp4a((int)wv[u][r].x, (int)xv[u][t].x, s);
+          s = __dp4a((int)wv[u][r].y, (int)xv[u][t].y, s);
+          s = __dp4a((int)wv[u][r].z, (int)xv[u][t].z, s);
+          acc[r * TT + t] = __dp4a((int)wv[u][r].w, (int)xv[u][t].w, s);
+        }
+  }
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < R * TT; ++i) {
+    const int s = __reduce_add_sync(0xffffffffu, acc[i]);
+    if (lane == i) mine = s;
+  }
+  if (along > 1) {
+    if (lane < R * TT) part[warp][lane] = mine;
+    __syncthreads();
+    if (warp & (along - 1)) return;
+    if (lane < R * TT)
+      for (int i = 1; i < along; ++i) mine += part[warp + i][lane];
+  }
+  const int n = n0 + lane / TT, t = lane % TT;
+  if (lane < R * TT && n < a.N && t < a.T)
+    a.out[t * a.out_stride + n] = __float2bfloat16_rn((float)mine * a.x_scale[t] * a.w_scale[n]);
 }
 
 // ------------------------------------------------------------------ many tokens
@@ -643,6 +711,17 @@ cudaError_t launch_split(Args a, const void* x, const void* w, int sms, cudaStre
   return e;
 }
 
+template <int TT, int R>
+cudaError_t launch_dot(const Args& a, const void* x, const void* w, int sms, cudaStream_t s) {
+  const long long groups = (a.N + R - 1) / R;
+  int along = 1;   // some 24 warps an SM, each with two steps along K and more
+  while (along < kDotWarps && groups * along < 24ll * sms && a.K >= 2048 * along) along *= 2;
+  const int per = kDotWarps / along;
+  dot_kernel<TT, R><<<(unsigned)((groups + per - 1) / per), 32 * kDotWarps, 0, s>>>(
+      static_cast<const int8_t*>(x), static_cast<const int8_t*>(w), a, along);
+  return cudaGetLastError();
+}
+
 template <bool kInt8, int kW>
 cudaError_t launch_pair(const Args& a, const void* x, const void* w, int sms, cudaStream_t s) {
   using P = Pair<kInt8, kW>;
@@ -680,6 +759,11 @@ int pair_width(int T, int N, int sms) {
 
 template <bool kInt8>
 cudaError_t launch(const Args& a, const void* x, const void* w, int sms, cudaStream_t s) {
+  if (kInt8 && a.T <= 8 && a.K <= kDotMaxK) {
+    if (a.T == 1) return launch_dot<1, 2>(a, x, w, sms, s);
+    if (a.T == 2) return launch_dot<2, 2>(a, x, w, sms, s);
+    return a.T <= 4 ? launch_dot<4, 4>(a, x, w, sms, s) : launch_dot<8, 4>(a, x, w, sms, s);
+  }
   // Above 128 tokens a pair's 256 rows cost less than they waste (192 tokens, 8,192 x 16,384: 70 us against 83
   // for int8, 33 against 34 for e4m3; 256: 70 against 91, 34 against 40); above 64 where the split kernel's
   // tiles are more than the SMs (128 tokens, 24,576 x 1,536: 20.5 against 34.5, 13.2 against 14.1).

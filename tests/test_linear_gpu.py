@@ -60,7 +60,7 @@ def check(out, x, xs, w, ws):
         assert (err.norm() / ref.norm()).item() <= 2.3e-3
 
 
-SHAPES = [(1, 8, 16), (1, 128, 128), (1, 2112, 8192), (2, 136, 144), (3, 64, 48), (15, 576, 1024), (16, 120, 4096),
+SHAPES = [(1, 8, 16), (1, 4104, 528), (2, 8, 65536), (4, 136, 65552), (5, 64, 2064), (6, 24576, 96), (8, 2112, 8192), (1, 128, 128), (1, 2112, 8192), (2, 136, 144), (3, 64, 48), (15, 576, 1024), (16, 120, 4096),
           (17, 2048, 208), (33, 1000, 1536), (64, 4096, 1536), (100, 576, 7168), (129, 264, 512), (255, 128, 64),
           (256, 1024, 1040), (257, 520, 272), (333, 1096, 4096), (512, 512, 512), (700, 24, 16), (1025, 768, 1536),
           (2000, 2304, 576), (64, 24576, 1536),
