@@ -6,14 +6,20 @@
 //   e4m3: s = the least 2^e with amax|y| <= 448 s, codes y / s     (an exact quotient, rounded once)
 //   int8: s = fl32(amax|y| / 127), at least 2^-126, codes y / s    (nearest, ties to even)
 //
-// Arithmetic.  A code follows the last bit of y, so y is the correctly rounded value: the squares
-// of bf16 values are exact in fp32 and summed as unevaluated pairs (Knuth's TwoSum), 1 / sqrt is
-// taken once a row in fp64 and split into two floats, h * gamma is exact, and the one fma that is
-// left is rounded to odd before it is rounded to bf16 (mla_rows.cuh).  x + residual needs no such
-// care: a sum of two 8-bit significands rounded to 24 bits and then to 8 is rounded as if once
-// (24 >= 2 * 8 + 2).  An int8 quotient is formed with the reciprocal of s, off by at most
-// 127 * 2^-23, and decided in fp64 where that leaves its rounding open (one value in 4,096), where
-// the product of s and a half-integer is exact.
+// Arithmetic.  A code follows the last bit of y, so y is the correctly rounded value.
+//   Sum of squares: s' = fma(h, h, s) loses fma(h, h, s - s') exactly as long as s is not below h^2, so each
+//   thread starts at a power of two B above its largest square and adds up the losses; the threads' pairs
+//   (s - B, losses) are joined by Knuth's TwoSum.  Four operations a value, and two values an
+//   instruction.
+//   1 / sqrt, once a row, in fp64, as ih + il, il >= 0 (a zero keeps its sign).
+//   y: m = h * gamma is exact in fp32, and so is the sum of fma(m, ih, m * il) but for its one rounding.
+//   Truncated and its last bit set it rounds to bf16 as the exact value does (no number with that bit
+//   lies on a bf16 boundary); where il = 0 the sum may be exact and the row is done one value at a time
+//   (fma_odd), as are values at the ends of fp32's range.
+//   x + residual needs no such care: a sum of two 8-bit significands rounded to 24 bits and then to 8
+//   is rounded as if once (24 >= 2 * 8 + 2).  An int8 quotient is formed with the reciprocal of s, off by
+//   at most 127 * 2^-23, and decided in fp64 where that leaves its rounding open (one value in
+//   4,096): the product of s and a half-integer is exact there.
 //
 // Layout.  A row is read once and stays in registers: 8 values (16 bytes) a thread V times.  Rows of
 // up to 1,024 values take a warp, longer ones a block with three barriers a row (sum, 1 / sqrt,
@@ -27,7 +33,6 @@ namespace rq {
 using namespace rows;
 
 constexpr int kWarpRows = 8;          // rows of a block where a warp takes a row
-constexpr int kMaxThreads = 1024;
 
 struct Args {
   int fmt, T, D;
@@ -44,37 +49,12 @@ struct Args {
 
 constexpr uint32_t kLow = 0x2B800000u, kSpan = 0x5D800000u - kLow;   // fp32 magnitudes 2^-40 .. 2^60
 
-// h * inv * gamma of any one value, rounded to odd.
+// h * inv * gamma of any one value, rounded to odd.  inner: ih within [2^-60, 2^60].
 static __device__ __noinline__ float normed_any(float h, float g, float ih, float il, double inv, bool inner) {
   const float m = __fmul_rn(h, g);
   if (inner && ((__float_as_uint(m) & 0x7FFFFFFFu) - kLow <= kSpan || h == 0.f || g == 0.f))
     return fma_odd(m, ih, __fmul_rn(m, il));
   return double_odd((double)h * inv * (double)g);
-}
-
-// h * inv * gamma of eight values (packed pairs), as packed bf16 pairs.  inv = ih + il, il >= 0, so
-// that a zero keeps its sign.  The fma's operands must be exact: products in fp32's inner range.
-__device__ __forceinline__ void normed(const uint32_t (&h)[4], const uint32_t (&g)[4], float ih, float il, double inv,
-                                       bool inner, uint32_t (&y)[4]) {
-  float m[8];
-  uint32_t worst = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    m[2 * i] = __fmul_rn(lo_f(h[i]), lo_f(g[i]));
-    m[2 * i + 1] = __fmul_rn(hi_f(h[i]), hi_f(g[i]));
-    worst = max(worst, max((__float_as_uint(m[2 * i]) & 0x7FFFFFFFu) - kLow,
-                           (__float_as_uint(m[2 * i + 1]) & 0x7FFFFFFFu) - kLow));
-  }
-  if (inner && worst <= kSpan) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      y[i] = pack(fma_odd(m[2 * i], ih, __fmul_rn(m[2 * i], il)),
-                  fma_odd(m[2 * i + 1], ih, __fmul_rn(m[2 * i + 1], il)));
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    y[i] = pack(normed_any(lo_f(h[i]), lo_f(g[i]), ih, il, inv, inner), normed_any(hi_f(h[i]), hi_f(g[i]), ih, il, inv, inner));
 }
 
 // The int8 code of y / s where the fp32 quotient k + r lies next to a half-integer.
@@ -88,22 +68,27 @@ static __device__ __noinline__ int int8_decide(float y, float s, float k, float 
 // Eight values (packed bf16 pairs) as eight int8 codes.
 __device__ __forceinline__ uint2 int8_codes(const uint32_t (&y)[4], float s, float rs) {
   constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: an integer added to it sits in the low bits
-  uint32_t b[8];
-  float worst = 0.f;
+  const float2x magic = both(kMagic, kMagic), rs2 = both(rs, rs);
+  float k[8], worst = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float z = __fmul_rn(i & 1 ? hi_f(y[i / 2]) : lo_f(y[i / 2]), rs), u = __fadd_rn(z, kMagic);
-    b[i] = __float_as_uint(u);
-    worst = fmaxf(worst, fabsf(__fsub_rn(z, __fsub_rn(u, kMagic))));
+  for (int i = 0; i < 4; ++i) {
+    const float2x z = mul2(widen2(y[i]), rs2), u = add2(z, magic);
+    float r0, r1;
+    apart(u, k[2 * i], k[2 * i + 1]);
+    apart(sub2(z, sub2(u, magic)), r0, r1);
+    worst = fmaxf(worst, fmaxf(fabsf(r0), fabsf(r1)));
   }
   if (worst > 0.5f - 0x1p-13f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float v = i & 1 ? hi_f(y[i / 2]) : lo_f(y[i / 2]);
-      const float z = __fmul_rn(v, rs), k = __fsub_rn(__fadd_rn(z, kMagic), kMagic), r = __fsub_rn(z, k);
-      if (fabsf(r) > 0.5f - 0x1p-13f) b[i] = (uint32_t)int8_decide(v, s, k, r);
+      const float n = __fsub_rn(k[i], kMagic), r = __fsub_rn(__fmul_rn(v, rs), n);
+      if (fabsf(r) > 0.5f - 0x1p-13f) k[i] = __uint_as_float((uint32_t)int8_decide(v, s, n, r));
     }
   }
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(k[i]);
   uint2 w;
   w.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
   w.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
@@ -114,14 +99,21 @@ __device__ __forceinline__ uint2 int8_codes(const uint32_t (&y)[4], float s, flo
 __device__ __forceinline__ uint2 e4m3_codes(const uint32_t (&y)[4], float rs) {
   uint32_t two[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    two[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo_f(y[i]) * rs, hi_f(y[i]) * rs), __NV_SATFINITE, __NV_E4M3);
+  for (int i = 0; i < 4; ++i) {
+    float2 v;
+    apart(mul2(widen2(y[i]), both(rs, rs)), v.x, v.y);
+    two[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+  }
   return make_uint2(two[0] | (two[1] << 16), two[2] | (two[3] << 16));
 }
 
+// Largest 16-bit half (0 .. 0xFFFF) of a word of two.
+__device__ __forceinline__ uint32_t halves_max(uint32_t v) { return max(v & 0xFFFFu, v >> 16); }
+__device__ __forceinline__ uint32_t halves_min(uint32_t v) { return min(v & 0xFFFFu, v >> 16); }
+
 // V pieces of 8 values a thread; kWarp: a warp takes a row, else the block does.
-template <int V, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMaxThreads) rmsnorm_kernel(const Args a) {
+template <int V, bool kWarp, int kThreads>
+__global__ void __launch_bounds__(kThreads) rmsnorm_kernel(const Args a) {
   __shared__ float part_hi[32], part_lo[32];
   __shared__ double part_wide[32];
   __shared__ uint32_t part_max[32];
@@ -151,8 +143,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMaxThreads) rmsnorm_
       if (a.residual) {
         const uint32_t r[4] = {rv[v].x, rv[v].y, rv[v].z, rv[v].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          h[v][i] = pack(__fadd_rn(lo_f(h[v][i]), lo_f(r[i])), __fadd_rn(hi_f(h[v][i]), hi_f(r[i])));
+        for (int i = 0; i < 4; ++i) h[v][i] = pack2(add2(widen2(h[v][i]), widen2(r[i])));
         const int p = first + v * step;
         if (p < n8)
           reinterpret_cast<uint4*>(a.residual_out + t * a.D)[p] = make_uint4(h[v][0], h[v][1], h[v][2], h[v][3]);
@@ -161,26 +152,34 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMaxThreads) rmsnorm_
   }
 
   if (a.gamma) {
-    // mean square: pairs of floats where the largest magnitude leaves the squares room, else fp64
-    uint32_t top = 0;
+    uint32_t top2 = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = max(top, max(h[v][i] & 0x7FFFu, (h[v][i] >> 16) & 0x7FFFu));
-    top = __reduce_max_sync(0xffffffffu, top);
-    const float top_f = __uint_as_float(top << 16);
-    bool wide = top != 0 && !(top_f >= 0x1p-40f && top_f <= 0x1p55f);
-    float hi = 0.f, lo = 0.f;
+      for (int i = 0; i < 4; ++i) top2 = __vmaxu2(top2, h[v][i] & 0x7FFF7FFFu);
+    const uint32_t top = halves_max(top2);
+    // fp64 where the squares of this thread's largest values would leave fp32's inner range
+    bool wide = top != 0 && !(top >= (0x2B800000u >> 16) && top <= (0x5B000000u >> 16));   // 2^-40 .. 2^55
+    const float bias = __uint_as_float(top == 0 ? 0u : (2 * (top >> 7) - 125) << 23);   // the square of twice its power of two
+    float hi, lo;
+    {
+      float2x s = both(bias, bias), e = both(0.f, 0.f);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float e;
-        two_sum(hi, __fmul_rn(lo_f(h[v][i]), lo_f(h[v][i])), hi, e);
-        lo = __fadd_rn(lo, e);
-        two_sum(hi, __fmul_rn(hi_f(h[v][i]), hi_f(h[v][i])), hi, e);
-        lo = __fadd_rn(lo, e);
-      }
+        for (int i = 0; i < 4; ++i) {
+          const float2x x2 = widen2(h[v][i]), n = fma2(x2, x2, s);
+          e = add2(e, fma2(x2, x2, sub2(s, n)));
+          s = n;
+        }
+      float s0, s1, e0, e1, f0, f1, f2;
+      apart(s, s0, s1);
+      apart(e, e0, e1);
+      two_sum(s0, -bias, s0, f0);
+      two_sum(s1, -bias, s1, f1);
+      two_sum(s0, s1, hi, f2);
+      lo = __fadd_rn(__fadd_rn(e0, e1), __fadd_rn(__fadd_rn(f0, f1), f2));
+    }
     auto reduce_pair = [&]() {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
@@ -206,6 +205,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMaxThreads) rmsnorm_
     reduce_pair();
     double inv;
     if (kWarp) {
+      wide = __any_sync(0xffffffffu, wide);
       inv = rsqrt((wide ? reduce_wide() : (double)hi + (double)lo) / (double)a.D + a.eps);
     } else {
       if (lane == 0) {
@@ -236,13 +236,37 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMaxThreads) rmsnorm_
     }
     const float ih = __double2float_rd(inv), il = (float)(inv - (double)ih);
     const bool inner = ih >= 0x1p-60f && ih <= 0x1p60f;
+    // The quick way gives every y right whose magnitude is zero or within [2^-90, 2^90): with ih <= 2^15 a
+    // product h * gamma that fp32 does not hold exactly belongs to a smaller y, and one that it takes
+    // for zero to a y that is zero.
+    const bool quick = il != 0.f && ih >= 0x1p-30f && ih <= 0x1p15f;
+    constexpr uint32_t kLeast = 0x12800000u >> 16, kMost = 0x6C800000u >> 16;   // 2^-90, 2^90
+    const float2x ih2 = both(ih, ih), il2 = both(il, il);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int p = first + v * step;
       if (p < n8) {
         const uint4 gv = reinterpret_cast<const uint4*>(a.gamma)[p];
         const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w};
-        normed(h[v], g, ih, il, inv, inner, h[v]);
+        uint32_t y[4], least = 0xFFFFFFFFu, most = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2x m = mul2(widen2(h[v][i]), widen2(g[i]));
+          float r0, r1;
+          apart(fma2_rz(m, ih2, mul2(m, il2)), r0, r1);
+          y[i] = pack(__uint_as_float(__float_as_uint(r0) | 1u), __uint_as_float(__float_as_uint(r1) | 1u));
+          const uint32_t mag = y[i] & 0x7FFF7FFFu;
+          most = __vmaxu2(most, mag);
+          least = __vminu2(least, (mag + 0x7FFF7FFFu) ^ 0x80008000u);   // magnitude - 1, zero the largest
+        }
+        if (!(quick && halves_min(least) >= kLeast && halves_max(most) < kMost)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            y[i] = pack(normed_any(lo_f(h[v][i]), lo_f(g[i]), ih, il, inv, inner),
+                        normed_any(hi_f(h[v][i]), hi_f(g[i]), ih, il, inv, inner));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[v][i] = y[i];
       }
     }
   }
@@ -260,7 +284,8 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMaxThreads) rmsnorm_
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) amax = max(amax, max(h[v][i] & 0x7FFFu, (h[v][i] >> 16) & 0x7FFFu));
+    for (int i = 0; i < 4; ++i) amax = __vmaxu2(amax, h[v][i] & 0x7FFF7FFFu);
+  amax = halves_max(amax);
   amax = __reduce_max_sync(0xffffffffu, amax);
   if (!kWarp) {
     if (lane == 0) part_max[warp] = amax;
@@ -290,10 +315,10 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMaxThreads) rmsnorm_
   if (first == 0) a.scales[t] = bad && int8 ? __uint_as_float(0x7FC00000u) : s;
 }
 
-template <int V, bool kWarp>
+template <int V, bool kWarp, int kThreads>
 void start(const Args& a, int threads, cudaStream_t s) {
   const unsigned blocks = kWarp ? ((unsigned)a.T + kWarpRows - 1) / kWarpRows : (unsigned)a.T;
-  rmsnorm_kernel<V, kWarp><<<blocks, threads, 0, s>>>(a);
+  rmsnorm_kernel<V, kWarp, kThreads><<<blocks, threads, 0, s>>>(a);
 }
 
 }  // namespace rq
@@ -316,14 +341,16 @@ cudaError_t launch_rmsnorm(int fmt, int rows, int width, const void* x, long lon
   a.codes = static_cast<uint8_t*>(codes);
   a.scales = scales;
   const int n8 = width / 8;
-  if (n8 <= 32) rq::start<1, true>(a, 32 * rq::kWarpRows, s);
-  else if (n8 <= 64) rq::start<2, true>(a, 32 * rq::kWarpRows, s);
-  else if (n8 <= 128) rq::start<4, true>(a, 32 * rq::kWarpRows, s);
+  constexpr int kWarpThreads = 32 * rq::kWarpRows;
+  if (n8 <= 32) rq::start<1, true, kWarpThreads>(a, kWarpThreads, s);
+  else if (n8 <= 64) rq::start<2, true, kWarpThreads>(a, kWarpThreads, s);
+  else if (n8 <= 128) rq::start<4, true, kWarpThreads>(a, kWarpThreads, s);
   else {
     auto threads = [&](int v) { return ((n8 + v - 1) / v + 31) / 32 * 32; };
-    if (n8 <= 512) rq::start<1, false>(a, threads(1), s);
-    else if (n8 <= 1024) rq::start<2, false>(a, threads(2), s);
-    else rq::start<4, false>(a, threads(4), s);
+    if (n8 <= 256) rq::start<1, false, 256>(a, threads(1), s);
+    else if (n8 <= 512) rq::start<2, false, 256>(a, threads(2), s);
+    else if (n8 <= 1024) rq::start<4, false, 256>(a, threads(4), s);
+    else rq::start<4, false, 1024>(a, threads(4), s);
   }
   return cudaGetLastError();
 }

@@ -35,6 +35,47 @@ __device__ __forceinline__ float double_odd(double x) {
   return isfinite(f) && (double)f != x ? __uint_as_float(__float_as_uint(f) | 1u) : f;
 }
 
+// Two floats worked on at once (one instruction for both).
+typedef unsigned long long float2x;
+__device__ __forceinline__ float2x both(float lo, float hi) {
+  float2x r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void apart(float2x v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ float2x add2(float2x a, float2x b) {
+  float2x r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float2x sub2(float2x a, float2x b) {
+  float2x r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float2x mul2(float2x a, float2x b) {
+  float2x r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float2x fma2(float2x a, float2x b, float2x c) {
+  float2x r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float2x fma2_rz(float2x a, float2x b, float2x c) {
+  float2x r;
+  asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// A bf16 pair as two floats, and back (nearest, ties to even).
+__device__ __forceinline__ float2x widen2(uint32_t v) { return both(lo_f(v), hi_f(v)); }
+__device__ __forceinline__ uint32_t pack2(float2x v) {
+  float lo, hi;
+  apart(v, lo, hi);
+  return pack(lo, hi);
+}
+
 // The least e with amax <= 7 * 2^(e - 3 + over), from bits of a bf16 magnitude: its exponent
 // field counts from 2^-127, a subnormal's leading bit is found by counting.  0 for zero.
 __device__ __forceinline__ int scale_exponent(uint32_t mag, int over, int low, int high) {
