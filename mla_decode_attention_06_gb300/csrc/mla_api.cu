@@ -545,7 +545,7 @@ int mla_indexer_append(int32_t num_heads, int32_t head_dim, int32_t rope_dim, in
   for (const void* p : {k_new, q, static_cast<const void*>(q_codes), static_cast<const void*>(k_cache), freqs_cis,
                         k_norm_gamma, k_norm_beta})
     if (!aligned16(p)) return MLA_ERR_INVALID_ARG;
-  if (!(epsilon >= 0.f)) return MLA_ERR_INVALID_ARG;
+  if (!(epsilon >= 0.f && epsilon - epsilon == 0.f)) return MLA_ERR_INVALID_ARG;
   if (workspace_bytes < sizeof(PlanHeader) || !aligned16(workspace)) return MLA_ERR_WORKSPACE_TOO_SMALL;
   PlanHeader* hdr = static_cast<PlanHeader*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -567,7 +567,7 @@ int mla_rmsnorm_quant(int32_t code_format, int32_t rows, int32_t width, const vo
                       const void* residual, void* residual_out, const void* gamma, float epsilon, void* y_out,
                       void* codes_out, float* scales_out, void* stream) {
   if (code_format < MLA_CODES_BF16 || code_format > MLA_CODES_INT8 || rows < 0 || width < 1 || x_stride < width ||
-      x_stride % 8 != 0 || !(epsilon >= 0.f))
+      x_stride % 8 != 0 || !(epsilon >= 0.f && epsilon - epsilon == 0.f))
     return MLA_ERR_INVALID_ARG;
   if (width % 8 != 0 || width > kMaxRowWidth) return MLA_ERR_UNSUPPORTED;
   const bool coded = code_format != MLA_CODES_BF16;

@@ -156,7 +156,8 @@ cudaError_t launch_cache_read(const mla_dims_t& d, int fmt, const uint32_t* offs
   a.block_table = block_table;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.hdr = hdr;
-  a.per_warp = 8;
+  // rows of a warp: eight where that leaves every SM some 16 warps, else fewer
+  a.per_warp = T >= 8 * 16 * 152 ? 8 : T >= 4 * 16 * 152 ? 4 : 2;
   const unsigned blocks = (unsigned)(((long long)T + rd::kWarps * a.per_warp - 1) / (rd::kWarps * a.per_warp));
   if (fmt == MLA_CACHE_BF16) rd::read_kernel<MLA_CACHE_BF16><<<blocks, 32 * rd::kWarps, 0, s>>>(a);
   else if (fmt == MLA_CACHE_E4M3) rd::read_kernel<MLA_CACHE_E4M3><<<blocks, 32 * rd::kWarps, 0, s>>>(a);

@@ -6,8 +6,10 @@
 //   e4m3: s = the least 2^e with amax <= 448 s, codes of the exact quotients, a scale a row and head
 //   cache row at pos: k's codes and s;  q_codes, q_scales = s * q_weight
 //
-// Arithmetic as in mla_append.cu: rotations rounded once, codes of exact quotients; the LayerNorm of
-// the one key a token is fp64 (its work is 1 / H of the queries').
+// Arithmetic as in mla_append.cu: rotations rounded once, codes of exact quotients.  The LayerNorm works
+// on unevaluated pairs of floats (mean, deviations, their squares' sum, 1 / sqrt, the result), to some
+// 2^-44, and rounds the pair that comes out once; rows at the ends of fp32's range and epsilons below
+// 2^-60 take fp64, which for all keys was the longest part of the call (97 us of 8,483 tokens).
 //
 // Layout.  D / 8 neighbouring lanes hold a row, 8 values (16 bytes) each, so that a row's largest
 // magnitude is a few shuffles away and a warp reads and writes whole rows; a block takes one token's
@@ -30,6 +32,7 @@ struct Args {
   int key_blocks, q_blocks;        // blocks of keys; blocks per token of queries
   long long max_seq_len, k_stride;
   double eps;
+  float inv_h, inv_l;              // 1 / D as a pair
   const __nv_bfloat16* k_new;      // [T, >= D]
   const __nv_bfloat16* q;          // [T, H, D]
   const float* q_weight;           // [T, H] or NULL
@@ -74,8 +77,8 @@ __device__ __forceinline__ uint4 turned(const Args& a, uint4 x, int col, long lo
   return lost ? turn_wide(x, f) : y;
 }
 
-// LayerNorm of a key, its values on `lanes` neighbours, in fp64; as bf16 pairs.  Whole warp.
-__device__ __forceinline__ uint4 layer_norm(const Args& a, uint4 x, int col, bool have) {
+// LayerNorm of a key, its values on `lanes` neighbours, in fp64.  Whole warp.
+__device__ __noinline__ uint4 layer_norm_wide(const Args& a, uint4 x, uint4 gv, uint4 bv, bool have) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   double v[8], sum = 0.0;
 #pragma unroll
@@ -93,33 +96,107 @@ __device__ __forceinline__ uint4 layer_norm(const Args& a, uint4 x, int col, boo
   }
   for (int o = a.lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const double inv = rsqrt(sum / (double)a.D + a.eps);
-  uint4 gv = make_uint4(0, 0, 0, 0), bv = gv;
-  if (have) {
-    gv = *reinterpret_cast<const uint4*>(a.gamma + col);
-    bv = *reinterpret_cast<const uint4*>(a.beta + col);
-  }
   const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w}, b[4] = {bv.x, bv.y, bv.z, bv.w};
   uint32_t y[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     y[i] = pack(double_odd(v[2 * i] * inv * (double)lo_f(g[i]) + (double)lo_f(b[i])),
                 double_odd(v[2 * i + 1] * inv * (double)hi_f(g[i]) + (double)hi_f(b[i])));
+  return make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+// hi + lo rounded to odd: of the floats on either side of the sum the one whose last bit is set.
+__device__ __forceinline__ float pair_odd(float hi, float lo) {
+  float s, e;
+  two_sum(hi, lo, s, e);
+  const uint32_t u = __float_as_uint(s);
+  if (e == 0.f || (u & 1u)) return s;
+  return __uint_as_float((e > 0.f) == (s > 0.f) ? u + 1 : u - 1);
+}
+
+// The sum of a pair over a group of `lanes` neighbours, in all of them.
+__device__ __forceinline__ void group_sum(int lanes, float& hi, float& lo) {
+  for (int o = lanes / 2; o > 0; o >>= 1) {
+    const float h2 = __shfl_xor_sync(0xffffffffu, hi, o), l2 = __shfl_xor_sync(0xffffffffu, lo, o);
+    float e;
+    two_sum(hi, h2, hi, e);
+    lo = __fadd_rn(__fadd_rn(lo, l2), e);
+  }
+}
+
+// LayerNorm of a key, its values on `lanes` neighbours; as bf16 pairs, zeros in lanes without values.  Whole warp.
+__device__ __forceinline__ uint4 layer_norm(const Args& a, uint4 x, int col, bool have) {
+  uint4 gv = make_uint4(0, 0, 0, 0), bv = gv;
+  if (have) {
+    gv = *reinterpret_cast<const uint4*>(a.gamma + col);
+    bv = *reinterpret_cast<const uint4*>(a.beta + col);
+  }
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w}, g[4] = {gv.x, gv.y, gv.z, gv.w}, b[4] = {bv.x, bv.y, bv.z, bv.w};
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+  // lanes whose largest value is below 2^-40 are fine beside larger ones; rows that are all that small are not
+  uint32_t row_top = top;
+  for (int o = a.lanes / 2; o > 0; o >>= 1) row_top = max(row_top, __shfl_xor_sync(0xffffffffu, row_top, o));
+  const bool wide = a.eps < 0x1p-60 || a.eps > 0x1p60 ||
+                    (row_top != 0 && !(row_top >= (0x2B800000u >> 16) && row_top <= (0x53800000u >> 16)));
+  uint32_t y[4];
+  if (__any_sync(0xffffffffu, wide)) {
+    const uint4 r = layer_norm_wide(a, x, gv, bv, have);
+    return have ? r : make_uint4(0, 0, 0, 0);
+  }
+  float v[8], hi = 0.f, lo = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float e;
+    v[i] = i & 1 ? hi_f(w[i / 2]) : lo_f(w[i / 2]);
+    two_sum(hi, v[i], hi, e);
+    lo = __fadd_rn(lo, e);
+  }
+  group_sum(a.lanes, hi, lo);
+  float mh, ml;
+  mean_plus(hi, lo, a.inv_h, a.inv_l, 0.f, mh, ml);
+  float dl[8];
+  hi = lo = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float e;
+    two_sum(v[i], -mh, v[i], e);
+    two_sum(v[i], __fsub_rn(e, ml), v[i], dl[i]);
+    const float p = __fmul_rn(v[i], v[i]);
+    const float pe = __fadd_rn(__fmaf_rn(v[i], v[i], -p), __fmul_rn(__fadd_rn(v[i], v[i]), dl[i]));
+    two_sum(hi, have ? p : 0.f, hi, e);
+    lo = __fadd_rn(lo, __fadd_rn(e, have ? pe : 0.f));
+  }
+  group_sum(a.lanes, hi, lo);
+  float vh, vl, ih, il;
+  mean_plus(hi, lo, a.inv_h, a.inv_l, (float)a.eps, vh, vl);
+  rsqrt_pair(vh, vl, ih, il);
+  float o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float gm = i & 1 ? hi_f(g[i / 2]) : lo_f(g[i / 2]), bt = i & 1 ? hi_f(b[i / 2]) : lo_f(b[i / 2]);
+    const float p = __fmul_rn(v[i], ih);
+    const float pe = __fadd_rn(__fmaf_rn(v[i], ih, -p), __fmaf_rn(v[i], il, __fmul_rn(dl[i], ih)));
+    const float q = __fmul_rn(p, gm), qe = __fmaf_rn(pe, gm, __fmaf_rn(p, gm, -q));
+    float s, e;
+    two_sum(q, bt, s, e);
+    o[i] = pair_odd(s, __fadd_rn(e, qe));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = pack(o[2 * i], o[2 * i + 1]);
   return have ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(0, 0, 0, 0);
 }
 
 // Whole warp: the keys of 32 / lanes tokens.
 __device__ __forceinline__ void new_keys(const Args& a, long long t0, int lane) {
-  const int groups = 32 / a.lanes, sub = lane % a.lanes, col = 8 * sub;
+  const int sub = lane & (a.lanes - 1), col = 8 * sub;
   const long long t = t0 + lane / a.lanes;
   const bool have = t < a.T && col < a.D;
   uint4 x = make_uint4(0, 0, 0, 0);
   if (have) x = *reinterpret_cast<const uint4*>(a.k_new + t * a.k_stride + col);
-  Place p{-1, 0};
-  for (int i = 0; i < groups; ++i) {
-    if (t0 + i >= a.T) break;
-    const Place q = locate(a, (int)(t0 + i), lane);
-    if (lane / a.lanes == i) p = q;
-  }
+  Place p = locate_groups(a, (int)min(t, a.T - 1ll), a.lanes, sub);
+  if (t >= a.T) p.pos = -1;
   if (a.gamma) x = layer_norm(a, x, col, have);
   if (have && p.pos >= 0) x = turned(a, x, col, p.pos);
   float s;
@@ -202,6 +279,8 @@ cudaError_t launch_indexer_append(int H, int D, int R, int ps, int num_pages, co
   a.max_seq_len = freqs ? max_seq_len : INT64_MAX;
   a.k_stride = k_stride;
   a.eps = (double)eps;
+  a.inv_h = (float)(1.0 / D);
+  a.inv_l = (float)(1.0 / D - (double)a.inv_h);
   a.k_new = static_cast<const __nv_bfloat16*>(k_new);
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_weight = q_weight;

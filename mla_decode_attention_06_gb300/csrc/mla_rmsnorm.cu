@@ -11,18 +11,18 @@
 //   thread starts at a power of two B above its largest square and adds up the losses; the threads' pairs
 //   (s - B, losses) are joined by Knuth's TwoSum.  Four operations a value, and two values an
 //   instruction.
-//   1 / sqrt, once a row, in fp64, as ih + il, il >= 0 (a zero keeps its sign).
+//   1 / sqrt, once a row, as a pair of floats ih + il, il >= 0 (a zero keeps its sign).
 //   y: m = h * gamma is exact in fp32, and so is the sum of fma(m, ih, m * il) but for its one rounding.
 //   Truncated and its last bit set it rounds to bf16 as the exact value does (no number with that bit
 //   lies on a bf16 boundary); where il = 0 the sum may be exact and the row is done one value at a time
 //   (fma_odd), as are values at the ends of fp32's range.
 //   x + residual needs no such care: a sum of two 8-bit significands rounded to 24 bits and then to 8
 //   is rounded as if once (24 >= 2 * 8 + 2).  An int8 quotient is formed with the reciprocal of s, off by
-//   at most 127 * 2^-23, and decided in fp64 where that leaves its rounding open (one value in
-//   4,096): the product of s and a half-integer is exact there.
+//   at most 127 * 2^-23; where that leaves its rounding open (values that are the largest over a power of two
+//   among them, three in a thousand) the sign of y less s times the half-integer decides, one exact fma.
 //
 // Layout.  A row is read once and stays in registers: 8 values (16 bytes) a thread V times.  Rows of
-// up to 1,024 values take a warp, longer ones a block with three barriers a row (sum, 1 / sqrt,
+// up to 2,048 values take a warp, longer ones a block with three barriers a row (sum, 1 / sqrt,
 // largest code).  Bound by HBM for many rows, by those steps' latency for few.
 #include "mla_kernels.cuh"
 #include "mla_rows.cuh"
@@ -38,6 +38,7 @@ struct Args {
   int fmt, T, D;
   long long x_stride;
   double eps;
+  float inv_h, inv_l;              // 1 / D as a pair
   const __nv_bfloat16* x;          // [T, >= D]
   const __nv_bfloat16* residual;   // [T, D] or NULL
   __nv_bfloat16* residual_out;     // [T, D], may be residual
@@ -49,46 +50,63 @@ struct Args {
 
 constexpr uint32_t kLow = 0x2B800000u, kSpan = 0x5D800000u - kLow;   // fp32 magnitudes 2^-40 .. 2^60
 
-// h * inv * gamma of any one value, rounded to odd.  inner: ih within [2^-60, 2^60].
-static __device__ __noinline__ float normed_any(float h, float g, float ih, float il, double inv, bool inner) {
-  const float m = __fmul_rn(h, g);
-  if (inner && ((__float_as_uint(m) & 0x7FFFFFFFu) - kLow <= kSpan || h == 0.f || g == 0.f))
-    return fma_odd(m, ih, __fmul_rn(m, il));
-  return double_odd((double)h * inv * (double)g);
+// h * inv * gamma of eight values of any magnitude, each rounded to odd and then to bf16.
+static __device__ __noinline__ uint4 normed_any(uint4 h, uint4 g, float ih, float il, double inv) {
+  uint32_t x[4] = {h.x, h.y, h.z, h.w}, y[4] = {g.x, g.y, g.z, g.w};
+  const bool inner = ih >= 0x1p-60f && ih <= 0x1p60f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float r[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float v = j ? hi_f(x[i]) : lo_f(x[i]), gm = j ? hi_f(y[i]) : lo_f(y[i]), m = __fmul_rn(v, gm);
+      r[j] = inner && ((__float_as_uint(m) & 0x7FFFFFFFu) - kLow <= kSpan || v == 0.f || gm == 0.f)
+                 ? fma_odd(m, ih, __fmul_rn(m, il))
+                 : double_odd((double)v * inv * (double)gm);
+    }
+    x[i] = pack(r[0], r[1]);
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// The int8 code of y / s where the fp32 quotient k + r lies next to a half-integer.
-static __device__ __noinline__ int int8_decide(float y, float s, float k, float r) {
-  const float half = k + (r > 0.f ? 0.5f : -0.5f);
-  const double d = (double)y - (double)half * (double)s;   // sign of y / s - half: the product is exact
-  const int below = __float2int_rd(half);
-  return d > 0.0 ? below + 1 : d < 0.0 ? below : (below & 1) ? below + 1 : below;
+// Eight values as int8 codes, exactly: where the fp32 quotient lies next to a half-integer, by the sign of
+// y less that half-integer times s, which one fma gives (32 bits of product; a scale so small that the
+// difference could underflow is brought up with y).
+static __device__ __noinline__ uint2 int8_exact(uint4 yv, float s, float rs) {
+  const uint32_t y[4] = {yv.x, yv.y, yv.z, yv.w};
+  const float up = s < 0x1p-60f ? 0x1p60f : 1.f, su = __fmul_rn(s, up);
+  uint32_t b[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = i & 1 ? hi_f(y[i / 2]) : lo_f(y[i / 2]);
+    const float z = __fmul_rn(v, rs), k = rintf(z), r = __fsub_rn(z, k);
+    float code = k;
+    if (fabsf(r) > 0.5f - 0x1p-15f) {
+      const float half = k + (r > 0.f ? 0.5f : -0.5f), d = __fmaf_rn(-half, su, __fmul_rn(v, up));
+      code = d > 0.f ? ceilf(half) : d < 0.f ? floorf(half) : rintf(half);
+    }
+    b[i / 4] |= ((uint32_t)(int)code & 0xFFu) << (8 * (i & 3));
+  }
+  return make_uint2(b[0], b[1]);
 }
 
 // Eight values (packed bf16 pairs) as eight int8 codes.
 __device__ __forceinline__ uint2 int8_codes(const uint32_t (&y)[4], float s, float rs) {
   constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: an integer added to it sits in the low bits
   const float2x magic = both(kMagic, kMagic), rs2 = both(rs, rs);
-  float k[8], worst = 0.f;
+  uint32_t b[8];
+  float worst = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2x z = mul2(widen2(y[i]), rs2), u = add2(z, magic);
     float r0, r1;
-    apart(u, k[2 * i], k[2 * i + 1]);
+    apart(u, r0, r1);
+    b[2 * i] = __float_as_uint(r0);
+    b[2 * i + 1] = __float_as_uint(r1);
     apart(sub2(z, sub2(u, magic)), r0, r1);
     worst = fmaxf(worst, fmaxf(fabsf(r0), fabsf(r1)));
   }
-  if (worst > 0.5f - 0x1p-13f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float v = i & 1 ? hi_f(y[i / 2]) : lo_f(y[i / 2]);
-      const float n = __fsub_rn(k[i], kMagic), r = __fsub_rn(__fmul_rn(v, rs), n);
-      if (fabsf(r) > 0.5f - 0x1p-13f) k[i] = __uint_as_float((uint32_t)int8_decide(v, s, n, r));
-    }
-  }
-  uint32_t b[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(k[i]);
+  if (worst > 0.5f - 0x1p-15f) return int8_exact(make_uint4(y[0], y[1], y[2], y[3]), s, rs);
   uint2 w;
   w.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
   w.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
@@ -112,12 +130,14 @@ __device__ __forceinline__ uint32_t halves_max(uint32_t v) { return max(v & 0xFF
 __device__ __forceinline__ uint32_t halves_min(uint32_t v) { return min(v & 0xFFFFu, v >> 16); }
 
 // V pieces of 8 values a thread; kWarp: a warp takes a row, else the block does.
+// Blocks of 256 threads: four an SM at 64 registers (8,192 x 8,192 e4m3 84 us; three at 72 93).
 template <int V, bool kWarp, int kThreads>
-__global__ void __launch_bounds__(kThreads) rmsnorm_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, kThreads == 256 && !kWarp ? 4 : 1) rmsnorm_kernel(const Args a) {
   __shared__ float part_hi[32], part_lo[32];
   __shared__ double part_wide[32];
   __shared__ uint32_t part_max[32];
-  __shared__ double inv_of_row;
+  __shared__ double inv_wide[kWarp ? kWarpRows : 1];
+  __shared__ float2 inv_pair;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int warps = kWarp ? 1 : (int)blockDim.x >> 5;
   const int first = kWarp ? lane : (int)threadIdx.x, step = kWarp ? 32 : (int)blockDim.x;
@@ -159,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_kernel(const Args a) {
       for (int i = 0; i < 4; ++i) top2 = __vmaxu2(top2, h[v][i] & 0x7FFF7FFFu);
     const uint32_t top = halves_max(top2);
     // fp64 where the squares of this thread's largest values would leave fp32's inner range
-    bool wide = top != 0 && !(top >= (0x2B800000u >> 16) && top <= (0x5B000000u >> 16));   // 2^-40 .. 2^55
+    bool wide = a.eps > 0x1p60 || (top != 0 && !(top >= (0x2B800000u >> 16) && top <= (0x53800000u >> 16)));   // 2^-40 .. 2^40
     const float bias = __uint_as_float(top == 0 ? 0u : (2 * (top >> 7) - 125) << 23);   // the square of twice its power of two
     float hi, lo;
     {
@@ -203,10 +223,21 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_kernel(const Args a) {
       return s;
     };
     reduce_pair();
-    double inv;
+    float ih, il;
+    auto root = [&]() {   // of the reduced pair
+      float vh, vl;
+      mean_plus(hi, lo, a.inv_h, a.inv_l, (float)a.eps, vh, vl);
+      rsqrt_pair(vh, vl, ih, il);
+    };
     if (kWarp) {
       wide = __any_sync(0xffffffffu, wide);
-      inv = rsqrt((wide ? reduce_wide() : (double)hi + (double)lo) / (double)a.D + a.eps);
+      if (wide) {
+        const double inv = rsqrt(reduce_wide() / (double)a.D + a.eps);
+        if (lane == 0) inv_wide[warp] = inv;
+        __syncwarp();
+      } else {
+        root();
+      }
     } else {
       if (lane == 0) {
         part_hi[warp] = hi;
@@ -219,23 +250,27 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_kernel(const Args a) {
         __syncthreads();
       }
       if (warp == 0) {
-        double sum;
         if (wide) {
-          sum = 0.0;
+          double sum = 0.0;
           for (int w = 0; w < warps; ++w) sum += part_wide[w];
+          if (lane == 0) inv_wide[0] = rsqrt(sum / (double)a.D + a.eps);
         } else {
           hi = lane < warps ? part_hi[lane] : 0.f;
           lo = lane < warps ? part_lo[lane] : 0.f;
           reduce_pair();
-          sum = (double)hi + (double)lo;
+          root();
+          if (lane == 0) inv_pair = make_float2(ih, il);
         }
-        if (lane == 0) inv_of_row = rsqrt(sum / (double)a.D + a.eps);
       }
       __syncthreads();
-      inv = inv_of_row;
+      ih = inv_pair.x;
+      il = inv_pair.y;
     }
-    const float ih = __double2float_rd(inv), il = (float)(inv - (double)ih);
-    const bool inner = ih >= 0x1p-60f && ih <= 0x1p60f;
+    if (wide) {
+      const double inv = inv_wide[kWarp ? warp : 0];
+      ih = __double2float_rd(inv);
+      il = (float)(inv - (double)ih);
+    }
     // The quick way gives every y right whose magnitude is zero or within [2^-90, 2^90): with ih <= 2^15 a
     // product h * gamma that fp32 does not hold exactly belongs to a smaller y, and one that it takes
     // for zero to a y that is zero.
@@ -260,10 +295,12 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_kernel(const Args a) {
           least = __vminu2(least, (mag + 0x7FFF7FFFu) ^ 0x80008000u);   // magnitude - 1, zero the largest
         }
         if (!(quick && halves_min(least) >= kLeast && halves_max(most) < kMost)) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            y[i] = pack(normed_any(lo_f(h[v][i]), lo_f(g[i]), ih, il, inv, inner),
-                        normed_any(hi_f(h[v][i]), hi_f(g[i]), ih, il, inv, inner));
+          const double inv = wide ? inv_wide[kWarp ? warp : 0] : (double)ih + (double)il;
+          const uint4 r = normed_any(make_uint4(h[v][0], h[v][1], h[v][2], h[v][3]), gv, ih, il, inv);
+          y[0] = r.x;
+          y[1] = r.y;
+          y[2] = r.z;
+          y[3] = r.w;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[v][i] = y[i];
@@ -333,6 +370,8 @@ cudaError_t launch_rmsnorm(int fmt, int rows, int width, const void* x, long lon
   a.D = width;
   a.x_stride = x_stride;
   a.eps = (double)eps;
+  a.inv_h = (float)(1.0 / width);
+  a.inv_l = (float)(1.0 / width - (double)a.inv_h);
   a.x = static_cast<const __nv_bfloat16*>(x);
   a.residual = static_cast<const __nv_bfloat16*>(residual);
   a.residual_out = static_cast<__nv_bfloat16*>(residual_out);
@@ -345,10 +384,11 @@ cudaError_t launch_rmsnorm(int fmt, int rows, int width, const void* x, long lon
   if (n8 <= 32) rq::start<1, true, kWarpThreads>(a, kWarpThreads, s);
   else if (n8 <= 64) rq::start<2, true, kWarpThreads>(a, kWarpThreads, s);
   else if (n8 <= 128) rq::start<4, true, kWarpThreads>(a, kWarpThreads, s);
+  else if (n8 <= 192) rq::start<6, true, kWarpThreads>(a, kWarpThreads, s);
+  else if (n8 <= 256) rq::start<8, true, kWarpThreads>(a, kWarpThreads, s);
   else {
     auto threads = [&](int v) { return ((n8 + v - 1) / v + 31) / 32 * 32; };
-    if (n8 <= 256) rq::start<1, false, 256>(a, threads(1), s);
-    else if (n8 <= 512) rq::start<2, false, 256>(a, threads(2), s);
+    if (n8 <= 512) rq::start<2, false, 256>(a, threads(2), s);
     else if (n8 <= 1024) rq::start<4, false, 256>(a, threads(4), s);
     else rq::start<4, false, 1024>(a, threads(4), s);
   }

@@ -35,6 +35,35 @@ __device__ __forceinline__ float double_odd(double x) {
   return isfinite(f) && (double)f != x ? __uint_as_float(__float_as_uint(f) | 1u) : f;
 }
 
+// 1 / sqrt(v) as ih + il, il >= 0, to some 2^-44 of its value (infinity and 0 for v = 0): v = vh + vl, vh the
+// sum rounded, 2^-100 <= vh <= 2^100 or 0.  One Newton step of third order on the fp32 root, its residual
+// 1 - v r^2 formed from exact products.  (In fp64 it takes some 30 operations, at a 64th of fp32's rate
+// the longest part of a short row's work.)
+__device__ __forceinline__ void rsqrt_pair(float vh, float vl, float& ih, float& il) {
+  const float r = rsqrtf(vh);
+  const float ph = __fmul_rn(r, r), pl = __fmaf_rn(r, r, -ph);
+  const float qh = __fmul_rn(vh, ph), ql = __fmaf_rn(vh, ph, -qh);
+  const float e = __fsub_rn(__fsub_rn(__fsub_rn(1.f, qh), ql), __fmaf_rn(vh, pl, __fmul_rn(vl, ph)));
+  const float c = __fmul_rn(r, __fmul_rn(e, __fmaf_rn(e, 0.375f, 0.5f)));
+  two_sum(r, c, ih, il);
+  if (il < 0.f) {
+    const float below = __uint_as_float(__float_as_uint(ih) - 1u);
+    il = __fadd_rn(__fsub_rn(ih, below), il);
+    ih = below;
+  }
+  if (vh == 0.f) {
+    ih = __uint_as_float(0x7F800000u);
+    il = 0.f;
+  }
+}
+// hi + lo (an unevaluated sum) times 1 / n = nh + nl, plus eps, as vh + vl.
+__device__ __forceinline__ void mean_plus(float hi, float lo, float nh, float nl, float eps, float& vh, float& vl) {
+  const float p = __fmul_rn(hi, nh), pe = __fadd_rn(__fmaf_rn(hi, nh, -p), __fmaf_rn(hi, nl, __fmul_rn(lo, nh)));
+  float s, se;
+  two_sum(p, eps, s, se);
+  two_sum(s, __fadd_rn(se, pe), vh, vl);
+}
+
 // Two floats worked on at once (one instruction for both).
 typedef unsigned long long float2x;
 __device__ __forceinline__ float2x both(float lo, float hi) {
@@ -121,7 +150,42 @@ struct Place {
   long long row;   // physical cache row
 };
 
-// Whole warp: where token t of a call goes.  `A` holds the call's offsets, cache_lens, block_table,
+// Whole warp: where the tokens t of a call go, a token a group of `lanes` neighbours (a power of two up to
+// 32; t is the group's, `sub` the lane's place in it).  `A` holds the call's offsets, cache_lens,
+// block_table, bt_stride, ps, num_pages, B, max_seq_len and hdr.  The request is the last b with
+// offsets[b] <= t, found by `lanes` probes a round (at 32, two rounds up to 1024 requests).  Tokens at or
+// past offsets[B] belong to nobody and are skipped; a position or page out of range is reported.
+template <class A>
+__device__ __forceinline__ Place locate_groups(const A& a, int t, int lanes, int sub) {
+  Place p{-1, 0};
+  int lo = 0, n = a.B;   // candidates [lo, lo + n)
+  const uint32_t end = a.offsets[a.B];
+  const int first = (int)(threadIdx.x & 31) - sub, shift = 31 - __clz(lanes);
+  const uint32_t mask = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1) << first;
+  while (__any_sync(0xffffffffu, n > 1)) {
+    const int step = (n + lanes - 1) >> shift;
+    const int probe = sub * step;
+    const bool below = probe < n && a.offsets[lo + probe] <= (uint32_t)t;
+    const int cnt = __popc(__ballot_sync(0xffffffffu, below) & mask);
+    const int skip = cnt > 0 ? (cnt - 1) * step : 0;
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  const uint32_t qb = a.offsets[lo], qe = a.offsets[lo + 1], len = a.cache_lens[lo];
+  if ((uint32_t)t >= end) return p;
+  const long long pos = (long long)len - qe + t;
+  bool ok = qb <= (uint32_t)t && (uint32_t)t < qe && pos >= 0 && pos < a.max_seq_len &&
+            pos < (long long)a.bt_stride * a.ps;
+  if (ok) {
+    const int page = a.block_table[(size_t)lo * a.bt_stride + pos / a.ps];
+    ok = page >= 0 && page < a.num_pages;
+    p.row = (long long)page * a.ps + pos % a.ps;
+  }
+  if (ok) p.pos = pos;
+  else if (sub == 0) atomicOr(&a.hdr->status, kDeviceCheckFailed);
+  return p;
+}
+// One token for the whole warp: where token t goes.  `A` holds the call's offsets, cache_lens, block_table,
 // bt_stride, ps, num_pages, B, max_seq_len and hdr.  The request is the last b with offsets[b] <= t,
 // found by 32 probes a round (two rounds up to 1024 requests).  Tokens at or past
 // offsets[B] belong to nobody and are skipped; a position or page out of range is
