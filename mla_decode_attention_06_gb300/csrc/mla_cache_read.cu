@@ -8,8 +8,8 @@
 //
 // Layout.  A warp takes `rows_per_warp` consecutive tokens.  Its lanes look their tokens up at
 // once, a lane a token (request by bisection, length, page), so the chain of dependent reads is
-// paid once a warp and not once a row; then the rows are copied, two at a time, 16 bytes of output
-// (8 values) a lane, all loads of the two out before the first is used.  Bound by HBM.
+// paid once a warp and not once a row; then the rows are copied, one or two at a time, 16 bytes of output
+// (8 values) a lane, all loads out before the first is used.  Bound by HBM.
 #include <cuda_fp4.h>
 
 #include "mla_kernels.cuh"
@@ -21,7 +21,6 @@ namespace rd {
 using namespace rows;
 
 constexpr int kWarps = 4;
-constexpr int kTogether = 2;         // rows in flight in a warp
 constexpr int kMaxPieces = 3;        // 8-value pieces of a row a lane: L + R <= 768
 
 struct Args {
@@ -113,6 +112,7 @@ __global__ void __launch_bounds__(32 * kWarps) read_kernel(const Args a) {
   if (t0 >= a.T) return;
   const long long mine = lane < a.per_warp ? find(a, (int)min(t0 + lane, (long long)a.T)) : -1;
   const int pieces = (a.L + a.R) / 8;
+  constexpr int kTogether = kFmt == MLA_CACHE_E2M1 ? 1 : 2;   // rows whose loads are out together (e2m1: two 76 us, one 70)
   for (int i = 0; i < a.per_warp; i += kTogether) {
     Piece<kFmt> p[kTogether][kMaxPieces];
     long long row[kTogether];

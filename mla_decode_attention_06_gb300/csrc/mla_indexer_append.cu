@@ -11,10 +11,11 @@
 // 2^-44, and rounds the pair that comes out once; rows at the ends of fp32's range and epsilons below
 // 2^-60 take fp64, which for all keys was the longest part of the call (97 us of 8,483 tokens).
 //
-// Layout.  D / 8 neighbouring lanes hold a row, 8 values (16 bytes) each, so that a row's largest
-// magnitude is a few shuffles away and a warp reads and writes whole rows; a block takes one token's
-// heads, four rows a lane group with all loads out before the token's place is looked up.  Keys
-// have blocks of their own.  Bound by HBM for prompts, by the chain of dependent reads for a step.
+// Layout.  Neighbouring lanes hold a row, so that its largest magnitude is a few shuffles away and a warp
+// reads and writes whole rows.  A query row takes D / 16 lanes of two 8-value pieces half a row apart, so
+// that with R = D / 2 all lanes turn one piece of their two together; a block takes one token's
+// heads, two rows a lane group with all loads out before the token's place is looked up.  Keys (a piece a
+// lane) have blocks of their own.  Bound by HBM for prompts, by the chain of dependent reads for a step.
 #include "mla_kernels.cuh"
 #include "mla_rows.cuh"
 
@@ -24,12 +25,14 @@ namespace ia {
 using namespace rows;
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;   // rows of queries a lane group
+constexpr int kBatch = 2;   // rows of queries a lane group
 
 struct Args {
   int D, H, R, ps, num_pages, B, T, bt_stride;
-  int lanes;                       // of a row: 8, 16 or 32, the first D / 8 of them used
-  int key_blocks, q_blocks;        // blocks of keys; blocks per token of queries
+  int lanes;                       // of a key: 8, 16 or 32, the first D / 8 of them used
+  int q_lanes;                     // of a query row, two pieces each
+  int key_blocks, q_blocks;        // blocks of keys; blocks of queries for the same tokens
+  int tokens;                      // tokens of a block of queries, a power of two
   long long max_seq_len, k_stride;
   double eps;
   float inv_h, inv_l;              // 1 / D as a pair
@@ -49,29 +52,40 @@ struct Args {
   PlanHeader* hdr;
 };
 
-// Codes and scale of a row whose values x (8 a lane, bf16 pairs) lie on `lanes` neighbours.  Whole warp.
-__device__ __forceinline__ uint2 coded(const Args& a, uint4 x, float& scale) {
+// The larger magnitudes of two words of bf16 pairs, half by half.
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return __vmaxu2(a, b & 0x7FFF7FFFu); }
+__device__ __forceinline__ uint32_t largest(uint32_t top, uint4 x) {
+  return larger(larger(larger(larger(top, x.x), x.y), x.z), x.w);
+}
+// The scale of a row whose lanes' largest magnitudes (a word of two halves) lie on `lanes` neighbours: its
+// exponent, or a value above 127 where the row holds a NaN or an infinity.  Whole warp.
+__device__ __forceinline__ int row_exponent(uint32_t top, int lanes) {
+  uint32_t amax = max(top & 0xFFFFu, top >> 16);
+  for (int o = lanes / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  return amax >= 0x7F80u ? 255 : scale_exponent(amax, 8, -126, 127);
+}
+__device__ __forceinline__ float scale_of(int e) { return e == 255 ? 1.f : pow2(e); }
+// Eight values as e4m3 codes under that exponent.
+__device__ __forceinline__ uint2 coded(uint4 x, int e) {
+  if (e == 255) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);   // every code a NaN
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t amax = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) amax = max(amax, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-  for (int o = a.lanes / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const bool bad = amax >= 0x7F80u;   // a NaN or an infinity: every code a NaN
-  const int e = bad ? 0 : scale_exponent(amax, 8, -126, 127);
   const float rs = pow2(-e);
-  scale = pow2(e);
   uint32_t two[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    two[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo_f(w[i]) * rs, hi_f(w[i]) * rs), __NV_SATFINITE, __NV_E4M3);
-  if (bad) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  for (int i = 0; i < 4; ++i) {
+    float2 v;
+    apart(mul2(widen2(w[i]), both(rs, rs)), v.x, v.y);
+    two[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+  }
   return make_uint2(two[0] | (two[1] << 16), two[2] | (two[3] << 16));
 }
 
-// The eight values at column `col` of a row, turned if they are of its last R.
-__device__ __forceinline__ uint4 turned(const Args& a, uint4 x, int col, long long pos) {
-  if (a.R == 0 || col < a.D - a.R || col >= a.D) return x;
-  const uint4 f = *reinterpret_cast<const uint4*>(a.freqs + pos * a.R + (col - (a.D - a.R)));
+// Whether column `col` lies in the part of a row that is turned, and its rotations.
+__device__ __forceinline__ bool in_rope(const Args& a, int col) { return a.R > 0 && col >= a.D - a.R && col < a.D; }
+__device__ __forceinline__ uint4 rotations(const Args& a, int col, long long pos) {
+  return *reinterpret_cast<const uint4*>(a.freqs + pos * a.R + (col - (a.D - a.R)));
+}
+__device__ __forceinline__ uint4 turned(uint4 x, uint4 f) {
   uint32_t lost = 0;
   const uint4 y = turn(x, f, lost);
   return lost ? turn_wide(x, f) : y;
@@ -198,43 +212,63 @@ __device__ __forceinline__ void new_keys(const Args& a, long long t0, int lane) 
   Place p = locate_groups(a, (int)min(t, a.T - 1ll), a.lanes, sub);
   if (t >= a.T) p.pos = -1;
   if (a.gamma) x = layer_norm(a, x, col, have);
-  if (have && p.pos >= 0) x = turned(a, x, col, p.pos);
-  float s;
-  const uint2 c = coded(a, x, s);
+  if (have && p.pos >= 0 && in_rope(a, col)) x = turned(x, rotations(a, col, p.pos));
+  const int e = row_exponent(largest(0u, x), a.lanes);
   if (!have || p.pos < 0) return;
-  *reinterpret_cast<uint2*>(a.k_cache + p.row * a.D + col) = c;
-  if (sub == 0) a.k_scales[p.row] = s;
+  *reinterpret_cast<uint2*>(a.k_cache + p.row * a.D + col) = coded(x, e);
+  if (sub == 0) a.k_scales[p.row] = scale_of(e);
 }
 
-// Heads [part * rows, ...) of token t's queries, rows = kBatch times the block's lane groups.
-__device__ __forceinline__ void queries(const Args& a, int t, int part, int lane) {
-  const int per = kThreads / a.lanes, sub = (int)threadIdx.x % a.lanes, col = 8 * sub;
-  const int h0 = part * per * kBatch + (int)threadIdx.x / a.lanes;
-  const bool used = col < a.D;
-  const size_t base = (size_t)t * a.H;
-  uint4 v[kBatch];
+// Heads [part * rows, ...) of the queries of tokens [t0, t0 + a.tokens), rows = kBatch times the block's lane
+// groups.  The tokens' places are looked up side by side, a group of lanes a token, so that the chain of
+// dependent reads is paid once.
+__device__ __forceinline__ void queries(const Args& a, int t0, int part, int lane) {
+  const int per = kThreads / a.q_lanes, sub = (int)threadIdx.x & (a.q_lanes - 1);
+  const int h0 = part * per * kBatch + (int)threadIdx.x / a.q_lanes;
+  const int col[2] = {8 * sub, 8 * (sub + a.q_lanes)};
+  const int look = 32 / a.tokens, tokens = min(a.tokens, a.T - t0);
+  uint4 v[kBatch][2];
   float wt[kBatch];
+  auto load = [&](int t) {
+    const size_t base = (size_t)t * a.H;
 #pragma unroll
-  for (int j = 0; j < kBatch; ++j) {
-    const int h = h0 + j * per;
-    v[j] = make_uint4(0, 0, 0, 0);
-    wt[j] = 1.f;
-    if (h < a.H && used) {
-      v[j] = *reinterpret_cast<const uint4*>(a.q + (base + h) * a.D + col);
-      if (a.q_weight && sub == 0) wt[j] = a.q_weight[base + h];
-    }
-  }
-  const Place p = locate(a, t, lane);
-  if (p.pos < 0) return;
+    for (int j = 0; j < kBatch; ++j) {
+      const int h = h0 + j * per;
+      wt[j] = h < a.H && a.q_weight && sub == 0 ? a.q_weight[base + h] : 1.f;
 #pragma unroll
-  for (int j = 0; j < kBatch; ++j) {
-    const int h = h0 + j * per;
-    float s;
-    const uint2 c = coded(a, turned(a, v[j], col, p.pos), s);
-    if (h < a.H && used) {
-      *reinterpret_cast<uint2*>(a.q_codes + (base + h) * a.D + col) = c;
-      if (sub == 0) a.q_scales[base + h] = __fmul_rn(s, wt[j]);
+      for (int k = 0; k < 2; ++k) {
+        v[j][k] = make_uint4(0, 0, 0, 0);
+        if (h < a.H && col[k] < a.D) v[j][k] = *reinterpret_cast<const uint4*>(a.q + (base + h) * a.D + col[k]);
+      }
     }
+  };
+  load(t0);   // on its way while the places are looked up
+  long long mine = locate_groups(a, min(t0 + lane / look, a.T - 1), look, lane & (look - 1)).pos;
+#pragma unroll 1
+  for (int i = 0; i < tokens; ++i) {
+    if (i > 0) load(t0 + i);
+    const long long pos = __shfl_sync(0xffffffffu, mine, i * look);
+    if (pos < 0) continue;
+    const size_t base = (size_t)(t0 + i) * a.H;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (!in_rope(a, col[k])) continue;
+      const uint4 f = rotations(a, col[k], pos);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) v[j][k] = turned(v[j][k], f);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int h = h0 + j * per;
+      const int e = row_exponent(largest(largest(0u, v[j][0]), v[j][1]), a.q_lanes);
+      if (h >= a.H) continue;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (col[k] < a.D) *reinterpret_cast<uint2*>(a.q_codes + (base + h) * a.D + col[k]) = coded(v[j][k], e);
+      if (sub == 0) a.q_scales[base + h] = __fmul_rn(scale_of(e), wt[j]);
+    }
+    __syncwarp();
   }
 }
 
@@ -245,18 +279,31 @@ __global__ void __launch_bounds__(kThreads) indexer_append_kernel(const Args a) 
     if (t0 < a.T) new_keys(a, t0, lane);
   } else {
     const int i = blk - a.key_blocks;
-    queries(a, i / a.q_blocks, i % a.q_blocks, lane);
+    queries(a, i / a.q_blocks * a.tokens, i % a.q_blocks, lane);
   }
 }
 
 int lanes_of(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
+int q_lanes_of(int D) {
+  int n = 1;
+  while (16 * n < D) n *= 2;
+  return n;
+}
 
 }  // namespace ia
 
+// Four tokens a block of queries where that leaves every SM eight blocks, else one.
+static int tokens_of(long long T, long long parts) { return T * parts >= 4ll * 8 * 152 ? 4 : 1; }
+
+static long long query_parts(int H, int D) {
+  const int heads = ia::kThreads / ia::q_lanes_of(D) * ia::kBatch;
+  return ((long long)H + heads - 1) / heads;
+}
+
 long long indexer_append_blocks(int H, int D, int T, bool queries) {
-  const int per = ia::kThreads / ia::lanes_of(D);
-  return ((long long)T + per - 1) / per +
-         (queries ? (long long)T * (((long long)H + per * ia::kBatch - 1) / (per * ia::kBatch)) : 0);
+  const int keys = ia::kThreads / ia::lanes_of(D);
+  const long long parts = queries ? query_parts(H, D) : 0, n = tokens_of(T, parts);
+  return ((long long)T + keys - 1) / keys + (T + n - 1) / n * parts;
 }
 
 cudaError_t launch_indexer_append(int H, int D, int R, int ps, int num_pages, const void* k_new, long long k_stride,
@@ -276,6 +323,7 @@ cudaError_t launch_indexer_append(int H, int D, int R, int ps, int num_pages, co
   a.T = T;
   a.bt_stride = bt_stride;
   a.lanes = ia::lanes_of(D);
+  a.q_lanes = ia::q_lanes_of(D);
   a.max_seq_len = freqs ? max_seq_len : INT64_MAX;
   a.k_stride = k_stride;
   a.eps = (double)eps;
@@ -297,7 +345,8 @@ cudaError_t launch_indexer_append(int H, int D, int R, int ps, int num_pages, co
   a.hdr = hdr;
   const long long blocks = indexer_append_blocks(H, D, T, q != nullptr);
   a.key_blocks = (int)indexer_append_blocks(H, D, T, false);
-  a.q_blocks = (int)((blocks - a.key_blocks) / T);
+  a.q_blocks = q ? (int)query_parts(H, D) : 0;
+  a.tokens = tokens_of(T, a.q_blocks);
   ia::indexer_append_kernel<<<(unsigned)blocks, ia::kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
