@@ -3,8 +3,7 @@
 //
 //   out[t] = [ bf16(code * scale) (L) ; k_rope (R) ]
 //
-// e2m1 codes times powers of two are bf16 values; an e4m3 code times a row scale has up to 28
-// bits, so the product is rounded to odd (mla_rows.cuh) before it is rounded to bf16, once in all.
+// each value rounded once.
 //
 // Layout.  A warp takes `rows_per_warp` consecutive tokens.  Its lanes look their tokens up at
 // once, a lane a token (request by bisection, length, page), so the chain of dependent reads is
@@ -61,6 +60,52 @@ __device__ __forceinline__ float mul_odd(float x, float s) {
   return __float_as_uint(down) & 1u ? down : up;
 }
 
+// Eight e4m3 codes times a row scale, each rounded once.  A truncated product with its last bit set rounds
+// to bf16 as the exact one does unless that is a tie (or fp32's range ends).  A code has four
+// significant bits, so where the scale's last four bits are zero the product is exact and is left alone;
+// where they are not it is no tie, whose scale would end in fifteen zeros.
+__device__ __forceinline__ uint4 e4m3_values(uint2 codes, float s) {
+  uint32_t o[4];
+  const bool inner = s >= 0x1p-100f || !(s == s);
+  const uint32_t sticky = (__float_as_uint(s) & 15u) != 0 ? 1u : 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t two = ((i < 2 ? codes.x : codes.y) >> (16 * (i & 1))) & 0xFFFFu;
+    const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
+    float lo, hi;
+    if (inner) {
+      apart(mul2_rz(both(v.x, v.y), both(s, s)), lo, hi);
+      lo = __uint_as_float(__float_as_uint(lo) | sticky);
+      hi = __uint_as_float(__float_as_uint(hi) | sticky);
+    } else {
+      lo = mul_odd(v.x, s);
+      hi = mul_odd(v.y, s);
+    }
+    o[i] = pack(lo, hi);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Eight e2m1 codes times a power of two, by bytes: a code's magnitude picks the two bytes of its bf16 value, its
+// sign the upper one's top bit; the product of bf16 pairs is exact (or bf16's range ends).
+__device__ __forceinline__ uint4 e2m1_values(uint32_t codes, __nv_bfloat162 s) {
+  constexpr uint32_t kHi0 = 0x3F3F3F00u, kHi1 = 0x40404040u, kLo0 = 0xC0800000u, kLo1 = 0xC0804000u;   // 0 .5 1 1.5 2 3 4 6
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {   // four codes: a selector takes four nibbles
+    const uint32_t mag = (codes >> (16 * i)) & 0x7777u, sign = (codes >> (16 * i + 3)) & 0x1111u;
+    const uint32_t hi = __byte_perm(kHi0, kHi1, mag) | __byte_perm(0x00008000u, 0u, sign);
+    const uint32_t lo = __byte_perm(kLo0, kLo1, mag);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t v = __byte_perm(lo, hi, j ? 0x7362 : 0x5140);
+      const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), s);
+      o[2 * i + j] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // What a lane holds of a row: 8 values of the latent part as they are stored, or of the rope part.
 template <int kFmt>
 struct Piece {
@@ -89,20 +134,8 @@ __device__ __forceinline__ void load(const Args& a, long long row, int piece, Pi
 template <int kFmt>
 __device__ __forceinline__ uint4 values(const Args& a, int piece, const Piece<kFmt>& p) {
   if (kFmt == MLA_CACHE_BF16 || piece >= a.L / 8) return p.raw;
-  uint32_t o[4] = {};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (kFmt == MLA_CACHE_E4M3) {
-      const uint32_t two = ((i < 2 ? p.raw.x : p.raw.y) >> (16 * (i & 1))) & 0xFFFFu;
-      const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
-      o[i] = pack(mul_odd(v.x, p.scale), mul_odd(v.y, p.scale));
-    } else if constexpr (kFmt == MLA_CACHE_E2M1) {
-      const uint32_t two = (p.raw.x >> (8 * i)) & 0xFFu;
-      const float2 v = __half22float2(__half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)two, __NV_E2M1)));
-      o[i] = pack(v.x * p.scale, v.y * p.scale);
-    }
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+  if constexpr (kFmt == MLA_CACHE_E4M3) return e4m3_values(make_uint2(p.raw.x, p.raw.y), p.scale);
+  else return e2m1_values(p.raw.x, __float2bfloat162_rn(p.scale));
 }
 
 template <int kFmt>

@@ -25,7 +25,7 @@ namespace ia {
 using namespace rows;
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 2;   // rows of queries a lane group
+constexpr int kBatch = 2;   // rows of queries a lane group (two: `queries` names them)
 
 struct Args {
   int D, H, R, ps, num_pages, B, T, bt_stride;
@@ -254,8 +254,18 @@ __device__ __forceinline__ void queries(const Args& a, int t0, int part, int lan
     for (int k = 0; k < 2; ++k) {
       if (!in_rope(a, col[k])) continue;
       const uint4 f = rotations(a, col[k], pos);
+      uint32_t lost = 0;
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) v[j][k] = turned(v[j][k], f);
+      for (int j = 0; j < kBatch; ++j) v[j][k] = turn(v[j][k], f, lost);
+      if (lost) {   // once for all: the rows are read again
+#pragma unroll 1
+        for (int j = 0; j < kBatch; ++j) {
+          const int h = min(h0 + j * per, a.H - 1);
+          const uint4 x = turn_wide(*reinterpret_cast<const uint4*>(a.q + (base + h) * a.D + col[k]), f);
+          if (j == 0) v[0][k] = x;
+          else v[1][k] = x;
+        }
+      }
     }
     __syncwarp();
 #pragma unroll

@@ -50,8 +50,10 @@ struct Args {
 
 constexpr uint32_t kLow = 0x2B800000u, kSpan = 0x5D800000u - kLow;   // fp32 magnitudes 2^-40 .. 2^60
 
-// h * inv * gamma of eight values of any magnitude, each rounded to odd and then to bf16.
-static __device__ __noinline__ uint4 normed_any(uint4 h, uint4 g, float ih, float il, double inv) {
+// h * inv * gamma of eight values of any magnitude, each rounded to odd and then to bf16; inv = ih + il, or what
+// `wide` points to.
+static __device__ __noinline__ uint4 normed_any(uint4 h, uint4 g, float ih, float il, const double* wide) {
+  const double inv = wide ? *wide : (double)ih + (double)il;
   uint32_t x[4] = {h.x, h.y, h.z, h.w}, y[4] = {g.x, g.y, g.z, g.w};
   const bool inner = ih >= 0x1p-60f && ih <= 0x1p60f;
 #pragma unroll
@@ -295,8 +297,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 && !kWarp ? 4 : 1) r
           least = __vminu2(least, (mag + 0x7FFF7FFFu) ^ 0x80008000u);   // magnitude - 1, zero the largest
         }
         if (!(quick && halves_min(least) >= kLeast && halves_max(most) < kMost)) {
-          const double inv = wide ? inv_wide[kWarp ? warp : 0] : (double)ih + (double)il;
-          const uint4 r = normed_any(make_uint4(h[v][0], h[v][1], h[v][2], h[v][3]), gv, ih, il, inv);
+          const uint4 r = normed_any(make_uint4(h[v][0], h[v][1], h[v][2], h[v][3]), gv, ih, il,
+                                     wide ? &inv_wide[kWarp ? warp : 0] : nullptr);
           y[0] = r.x;
           y[1] = r.y;
           y[2] = r.z;

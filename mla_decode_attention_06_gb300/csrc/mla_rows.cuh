@@ -97,6 +97,11 @@ __device__ __forceinline__ float2x fma2_rz(float2x a, float2x b, float2x c) {
   asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ float2x mul2_rz(float2x a, float2x b) {
+  float2x r;
+  asm("mul.rz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // A bf16 pair as two floats, and back (nearest, ties to even).
 __device__ __forceinline__ float2x widen2(uint32_t v) { return both(lo_f(v), hi_f(v)); }
 __device__ __forceinline__ uint32_t pack2(float2x v) {
