@@ -7,10 +7,9 @@
 //
 // Layout.  A warp takes `rows_per_warp` consecutive tokens.  Its lanes look their tokens up at
 // once, a lane a token (request by bisection, length, page), so the chain of dependent reads is
-// paid once a warp and not once a row; then the rows are copied, one or two at a time, 16 bytes of output
-// (8 values) a lane, all loads out before the first is used.  Bound by HBM.
-#include <cuda_fp4.h>
-
+// paid once a warp and not once a row; then the rows are copied, 16 bytes of output (8 values) a lane.
+// bf16 and e4m3 rows are loaded two at a time by the lanes that write them; e2m1 rows, of which a lane's 8
+// values are 4 bytes and a scale, whole, 16 bytes a lane, four at a time, through shared memory.  Bound by HBM.
 #include "mla_kernels.cuh"
 #include "mla_rows.cuh"
 
@@ -119,23 +118,60 @@ __device__ __forceinline__ void load(const Args& a, long long row, int piece, Pi
   const int latent = a.L / 8;
   if (kFmt == MLA_CACHE_BF16 || piece >= latent) {
     p.raw = *reinterpret_cast<const uint4*>(src + (a.row_bytes - 2 * (a.L + a.R)) + 16 * piece);
-  } else if (kFmt == MLA_CACHE_E4M3) {
+  } else {
     const uint2 v = *reinterpret_cast<const uint2*>(src + 8 * piece);
     p.raw.x = v.x;
     p.raw.y = v.y;
     p.scale = a.scales[row];
-  } else {
-    p.raw.x = *reinterpret_cast<const uint32_t*>(src + 4 * piece);
-    const uint8_t e = src[a.L / 2 + piece / 4];   // 2^(e - 127), 255 = NaN
-    p.scale = __uint_as_float(e == 255 ? 0x7FC00000u : e == 0 ? 0x00400000u : (uint32_t)e << 23);
   }
 }
 
 template <int kFmt>
 __device__ __forceinline__ uint4 values(const Args& a, int piece, const Piece<kFmt>& p) {
   if (kFmt == MLA_CACHE_BF16 || piece >= a.L / 8) return p.raw;
-  if constexpr (kFmt == MLA_CACHE_E4M3) return e4m3_values(make_uint2(p.raw.x, p.raw.y), p.scale);
-  else return e2m1_values(p.raw.x, __float2bfloat162_rn(p.scale));
+  return e4m3_values(make_uint2(p.raw.x, p.raw.y), p.scale);
+}
+
+// The rows of a warp's tokens from t0 on; `mine`: lane i's is token t0 + i's cache row.
+__device__ __forceinline__ void copy_e2m1(const Args& a, long long t0, long long mine, int lane) {
+  constexpr int kRows = 4, kRowBytes = 544;   // rows are at most 528 bytes (L = 512, R = 128)
+  __shared__ __align__(16) uint8_t rows[kWarps][kRows][kRowBytes];
+  uint8_t(*row)[kRowBytes] = rows[threadIdx.x >> 5];
+  const int whole = (int)(a.row_bytes / 16), latent = a.L / 8, pieces = (a.L + a.R) / 8;
+#pragma unroll 1
+  for (int i = 0; i < a.per_warp; i += kRows) {
+    uint4 v[kRows][2];
+    long long at[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      at[j] = __shfl_sync(0xffffffffu, mine, (i + j) & 31);
+      if (i + j >= a.per_warp) at[j] = -1;
+      const uint4* src = reinterpret_cast<const uint4*>(a.pool + at[j] * a.row_bytes);
+      if (at[j] >= 0 && lane < whole) v[j][0] = src[lane];
+      if (at[j] >= 0 && lane + 32 < whole) v[j][1] = src[lane + 32];
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      if (at[j] >= 0 && lane < whole) reinterpret_cast<uint4*>(row[j])[lane] = v[j][0];
+      if (at[j] >= 0 && lane + 32 < whole) reinterpret_cast<uint4*>(row[j])[lane + 32] = v[j][1];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      if (at[j] < 0) continue;
+      uint4* out = reinterpret_cast<uint4*>(a.out + (t0 + i + j) * (a.L + a.R));
+      for (int c = lane; c < pieces; c += 32) {
+        if (c >= latent) {
+          out[c] = *reinterpret_cast<const uint4*>(row[j] + a.row_bytes - 2 * (a.L + a.R) + 16 * c);
+        } else {
+          const uint32_t e = row[j][a.L / 2 + c / 4];   // 2^(e - 127) as a bf16 value, 255 = NaN
+          const uint32_t s = e == 255 ? 0x7FC0u : e == 0 ? 0x0040u : e << 7, s2 = s | s << 16;
+          out[c] = e2m1_values(*reinterpret_cast<const uint32_t*>(row[j] + 4 * c), *reinterpret_cast<const __nv_bfloat162*>(&s2));
+        }
+      }
+    }
+    __syncwarp();
+  }
 }
 
 template <int kFmt>
@@ -145,7 +181,11 @@ __global__ void __launch_bounds__(32 * kWarps) read_kernel(const Args a) {
   if (t0 >= a.T) return;
   const long long mine = lane < a.per_warp ? find(a, (int)min(t0 + lane, (long long)a.T)) : -1;
   const int pieces = (a.L + a.R) / 8;
-  constexpr int kTogether = kFmt == MLA_CACHE_E2M1 ? 1 : 2;   // rows whose loads are out together (e2m1: two 76 us, one 70)
+  if constexpr (kFmt == MLA_CACHE_E2M1) {
+    copy_e2m1(a, t0, mine, lane);
+    return;
+  }
+  constexpr int kTogether = 2;   // rows whose loads are out together
   for (int i = 0; i < a.per_warp; i += kTogether) {
     Piece<kFmt> p[kTogether][kMaxPieces];
     long long row[kTogether];
@@ -190,7 +230,7 @@ cudaError_t launch_cache_read(const mla_dims_t& d, int fmt, const uint32_t* offs
   a.out = static_cast<__nv_bfloat16*>(out);
   a.hdr = hdr;
   // rows of a warp: eight where that leaves every SM some 16 warps, else fewer
-  a.per_warp = T >= 8 * 16 * 152 ? 8 : T >= 4 * 16 * 152 ? 4 : 2;
+  a.per_warp = T >= 8 * 16 * 152 ? 8 : T >= 4 * 16 * 152 ? 4 : 2;   // at most 32, a lane a row
   const unsigned blocks = (unsigned)(((long long)T + rd::kWarps * a.per_warp - 1) / (rd::kWarps * a.per_warp));
   if (fmt == MLA_CACHE_BF16) rd::read_kernel<MLA_CACHE_BF16><<<blocks, 32 * rd::kWarps, 0, s>>>(a);
   else if (fmt == MLA_CACHE_E4M3) rd::read_kernel<MLA_CACHE_E4M3><<<blocks, 32 * rd::kWarps, 0, s>>>(a);
