@@ -311,7 +311,7 @@ int mla_cache_read(const mla_dims_t* dims, int32_t cache_format, const uint32_t*
 /* 8-bit codes of activations, and the row scale that goes with them (value = code * scale):
  *   BF16   no codes
  *   E4M3   OCP E4M3FN, scale = the least 2^e with max|y| <= 448 * 2^e (as MLA_CACHE_E4M3)
- *   INT8   -127 .. 127, scale = max|y| / 127 rounded to fp32, at least 2^-126
+ *   INT8   -127 .. 127, scale = max|y| times the fp32 number next to 1 / 127, rounded to fp32, at least 2^-126
  * Codes are the nearest to y / scale, ties to even; the scale of a row of zeros is 1.  A row that
  * holds a NaN or an infinity reads back as NaN throughout (E4M3: NaN codes; INT8: a NaN scale). */
 typedef enum {

@@ -191,6 +191,7 @@ def mla_decode_paged_fp8(q, input_row_offsets, kv_pool_fp8, kv_scales, block_tab
 
 _I32 = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32,)
 _BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
 
 
 _status = {}
@@ -208,9 +209,32 @@ def _unread_status(device, stream):
     return t
 
 
+def _handle(stream, device):
+    """The cudaStream_t that a call runs on, without a Stream object for the current one (3 us of a call)."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _status_word(workspace, debug, device, stream, handle):
+    """Pointer and size of a call's status word: the caller's workspace, one of its own where it is read."""
+    if workspace is None:
+        if debug:
+            workspace = _buffer(256, torch.uint8, device, stream)
+        else:
+            workspace = _status.get((device.index, handle))
+            if workspace is not None:
+                return workspace.data_ptr(), 256, workspace
+            workspace = _unread_status(device, torch.cuda.current_stream(device) if stream is None else stream)
+    return _ptr(workspace, "workspace", None, device), workspace.numel() * workspace.element_size(), workspace
+
+
+_fns = {}
+
+
 def _call(name, device, *args):
     """One library call with `device` current (the library launches on the current device)."""
-    fn = getattr(_lib.load(), name)
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(_lib.load(), name)
     if device.index is None or torch.cuda.current_device() == device.index:
         rc = fn(*args)
     else:
@@ -322,20 +346,17 @@ def mla_cache_read(input_row_offsets, kv_pool, block_table, cache_lens, *, kv_lo
                    num_pages=_pages(kv_pool, page_size, mla_cache_row_bytes(cache_format, L, R)))
     _sized(kv_scales, "kv_scales", dims.num_pages * page_size)
     B, offsets, table, table_stride, lens = _tables(input_row_offsets, block_table, cache_lens, dev)
-    s = torch.cuda.current_stream(dev) if stream is None else stream
+    handle = _handle(stream, dev)
     if out is None:
         if total_rows is None:
             raise ValueError("total_rows or out must be given")
         out = _buffer((total_rows, L + R), torch.bfloat16, dev, stream, returned=True)
     elif out.dim() != 2 or out.shape[1] != L + R or (total_rows is not None and out.shape[0] != total_rows):
         raise ValueError("out must be [total_rows, L+R]")
-    if workspace is None:
-        workspace = _buffer(256, torch.uint8, dev, stream) if debug else _unread_status(dev, s)
+    status, status_bytes, workspace = _status_word(workspace, debug, dev, stream, handle)
     _call("mla_cache_read", dev, ctypes.byref(dims), int(cache_format), offsets, B, out.shape[0],
-          _ptr(kv_pool, "kv_pool", None, dev), _ptr(kv_scales, "kv_scales", (torch.float32,), dev), table, table_stride,
-          lens, _ptr(out, "out", _BF16, dev), MLA_FLAG_DEBUG_CHECKS if debug else 0,
-          _ptr(workspace, "workspace", None, dev), workspace.numel() * workspace.element_size(),
-          ctypes.c_void_p(s.cuda_stream))
+          _ptr(kv_pool, "kv_pool", None, dev), _ptr(kv_scales, "kv_scales", _F32, dev), table, table_stride,
+          lens, _ptr(out, "out", _BF16, dev), MLA_FLAG_DEBUG_CHECKS if debug else 0, status, status_bytes, handle)
     return out
 
 
@@ -377,7 +398,7 @@ def mla_rmsnorm_quant(x, gamma=None, *, epsilon: float = 1e-6, code_format: int 
     _call("mla_rmsnorm_quant", dev, code_format, T, D, px, stride, _ptr(residual, "residual", _BF16, dev),
           _ptr(residual_out, "residual_out", _BF16, dev), _ptr(gamma, "gamma", _BF16, dev), float(epsilon),
           _ptr(y_out, "y_out", _BF16, dev), _ptr(codes_out, "codes_out", (_CODES[code_format], torch.uint8), dev),
-          _ptr(scales_out, "scales_out", (torch.float32,), dev), _stream(stream, dev))
+          _ptr(scales_out, "scales_out", _F32, dev), _handle(stream, dev))
     return (codes_out, scales_out, residual_out) if coded else (y_out, None, residual_out)
 
 
@@ -389,7 +410,7 @@ def _linear(name, dtypes, x_codes, x_scales, w_codes, w_scales, out, debug, work
     N = w_codes.shape[0]
     _sized(x_scales, "x_scales", T)
     _sized(w_scales, "w_scales", N)
-    s = torch.cuda.current_stream(dev) if stream is None else stream
+    handle = _handle(stream, dev)
     if out is None:
         out = _buffer((T, N), torch.bfloat16, dev, stream, returned=True)
     elif out.shape[0] != T:
@@ -397,13 +418,10 @@ def _linear(name, dtypes, x_codes, x_scales, w_codes, w_scales, out, debug, work
     p_out, out_stride = _row_strided(out, "out", N)
     if out.device != dev:
         raise ValueError(f"out is on {out.device}, expected {dev}")
-    if workspace is None:
-        workspace = _buffer(256, torch.uint8, dev, stream) if debug else _unread_status(dev, s)
-    f32 = (torch.float32,)
-    _call(name, dev, T, N, K, _ptr(x_codes, "x_codes", dtypes, dev), _ptr(x_scales, "x_scales", f32, dev),
-          _ptr(w_codes, "w_codes", dtypes, dev), _ptr(w_scales, "w_scales", f32, dev), p_out, out_stride,
-          MLA_FLAG_DEBUG_CHECKS if debug else 0, _ptr(workspace, "workspace", None, dev),
-          workspace.numel() * workspace.element_size(), ctypes.c_void_p(s.cuda_stream))
+    status, status_bytes, workspace = _status_word(workspace, debug, dev, stream, handle)
+    _call(name, dev, T, N, K, _ptr(x_codes, "x_codes", dtypes, dev), _ptr(x_scales, "x_scales", _F32, dev),
+          _ptr(w_codes, "w_codes", dtypes, dev), _ptr(w_scales, "w_scales", _F32, dev), p_out, out_stride,
+          MLA_FLAG_DEBUG_CHECKS if debug else 0, status, status_bytes, handle)
     return out
 
 
@@ -452,17 +470,14 @@ def mla_indexer_append(k_new, input_row_offsets, k_cache, k_scales, block_table,
     elif q_weight is not None or q_codes is not None or q_scales is not None:
         raise ValueError("q_weight, q_codes or q_scales without q")
     B, offsets, table, table_stride, lens = _tables(input_row_offsets, block_table, cache_lens, dev)
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    if workspace is None:
-        workspace = _buffer(256, torch.uint8, dev, stream) if debug else _unread_status(dev, s)
-    f32 = (torch.float32,)
+    handle = _handle(stream, dev)
+    status, status_bytes, workspace = _status_word(workspace, debug, dev, stream, handle)
     _call("mla_indexer_append", dev, H, D, R, page_size, num_pages, pk, stride, offsets, B, T, _ptr(q, "q", _BF16, dev),
-          _ptr(q_weight, "q_weight", f32, dev), _ptr(q_codes, "q_codes", f8, dev), _ptr(q_scales, "q_scales", f32, dev),
-          _ptr(k_cache, "k_cache", f8, dev), _ptr(k_scales, "k_scales", f32, dev), table, table_stride, lens,
+          _ptr(q_weight, "q_weight", _F32, dev), _ptr(q_codes, "q_codes", f8, dev), _ptr(q_scales, "q_scales", _F32, dev),
+          _ptr(k_cache, "k_cache", f8, dev), _ptr(k_scales, "k_scales", _F32, dev), table, table_stride, lens,
           _ptr(freqs_cis, "freqs_cis", _BF16, dev), max_len, _ptr(k_norm_gamma, "k_norm_gamma", _BF16, dev),
           _ptr(k_norm_beta, "k_norm_beta", _BF16, dev), float(epsilon), MLA_FLAG_DEBUG_CHECKS if debug else 0,
-          _ptr(workspace, "workspace", None, dev), workspace.numel() * workspace.element_size(),
-          ctypes.c_void_p(s.cuda_stream))
+          status, status_bytes, handle)
     return q_codes, q_scales
 
 

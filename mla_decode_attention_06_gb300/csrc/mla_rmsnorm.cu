@@ -4,7 +4,7 @@
 //   h = bf16( x + residual )                       (h = x without a residual)
 //   y = bf16( h / sqrt(mean(h^2) + eps) * gamma )  (y = h without gamma)
 //   e4m3: s = the least 2^e with amax|y| <= 448 s, codes y / s     (an exact quotient, rounded once)
-//   int8: s = fl32(amax|y| / 127), at least 2^-126, codes y / s    (nearest, ties to even)
+//   int8: s = fl32(amax|y| * fl32(1 / 127)), at least 2^-126, codes y / s    (nearest, ties to even)
 //
 // Arithmetic.  A code follows the last bit of y, so y is the correctly rounded value.
 //   Sum of squares: s' = fma(h, h, s) loses fma(h, h, s - s') exactly as long as s is not below h^2, so each
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 && !kWarp ? 4 : 1) r
   const bool int8 = a.fmt == MLA_CODES_INT8;
   float s, rs;
   if (int8) {
-    s = amax == 0 ? 1.f : fmaxf(__fdiv_rn(__uint_as_float(amax << 16), 127.f), 0x1p-126f);
+    s = amax == 0 ? 1.f : fmaxf(__fmul_rn(__uint_as_float(amax << 16), 1.f / 127.f), 0x1p-126f);
     rs = __frcp_rn(s);
   } else {
     const int e = bad ? 0 : scale_exponent(amax, 8, -126, 127);

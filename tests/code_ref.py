@@ -25,7 +25,7 @@ def encode(y_bits, fmt):
         codes = nearest_e4m3(np.ldexp(y, -e[:, None]))
         codes[bad] = 0x7F
         return codes, np.ldexp(1.0, e).astype(np.float32)
-    scale = np.where(amax > 0, np.maximum(amax.astype(np.float32) / np.float32(127), np.float32(2.0 ** -126)),
+    scale = np.where(amax > 0, np.maximum(amax.astype(np.float32) * (np.float32(1) / np.float32(127)), np.float32(2.0 ** -126)),
                      np.float32(1)).astype(np.float32)
     codes = np.rint(y / scale[:, None].astype(np.float64)).astype(np.int8).view(np.uint8)
     scale[bad] = np.nan
