@@ -13,8 +13,8 @@
 //
 // Layout.  Neighbouring lanes hold a row, so that its largest magnitude is a few shuffles away and a warp
 // reads and writes whole rows.  A query row takes D / 16 lanes of two 8-value pieces half a row apart, so
-// that with R = D / 2 all lanes turn one piece of their two together; a block takes one token's
-// heads, two rows a lane group with all loads out before the token's place is looked up.  Keys (a piece a
+// that with R = D / 2 all lanes turn one piece of their two together; a block takes the heads of one or
+// several tokens, two rows a lane group with all loads out before the tokens' places are looked up.  Keys (a piece a
 // lane) have blocks of their own.  Bound by HBM for prompts, by the chain of dependent reads for a step.
 #include "mla_kernels.cuh"
 #include "mla_rows.cuh"
@@ -25,14 +25,15 @@ namespace ia {
 using namespace rows;
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 2;   // rows of queries a lane group (two: `queries` names them)
+constexpr int kBatch = 2;   // rows of queries a lane group
+constexpr int kMaxTokens = 32;   // of a block of queries: eight lanes look one up
 
 struct Args {
   int D, H, R, ps, num_pages, B, T, bt_stride;
   int lanes;                       // of a key: 8, 16 or 32, the first D / 8 of them used
   int q_lanes;                     // of a query row, two pieces each
   int key_blocks, q_blocks;        // blocks of keys; blocks of queries for the same tokens
-  int tokens;                      // tokens of a block of queries, a power of two
+  int together, steps, slots;      // tokens of a block of queries at a time, how many times; head slots of a token
   long long max_seq_len, k_stride;
   double eps;
   float inv_h, inv_l;              // 1 / D as a pair
@@ -219,64 +220,83 @@ __device__ __forceinline__ void new_keys(const Args& a, long long t0, int lane) 
   if (sub == 0) a.k_scales[p.row] = scale_of(e);
 }
 
-// Heads [part * rows, ...) of the queries of tokens [t0, t0 + a.tokens), rows = kBatch times the block's lane
-// groups.  The tokens' places are looked up side by side, a group of lanes a token, so that the chain of
-// dependent reads is paid once.
+// The queries of tokens [t0, t0 + a.together * a.steps), `together` at a time: where the heads of one leave lane
+// groups free, a block takes several tokens' side by side (slots of a.slots heads, a power of two); else it takes
+// heads [part * rows, ...) of one, rows = kBatch times its lane groups.  The tokens' places are
+// looked up at once, eight lanes a token, so that the chain of dependent reads is paid once.
+// kSide: a.together > 1.
+template <bool kSide>
 __device__ __forceinline__ void queries(const Args& a, int t0, int part, int lane) {
-  const int per = kThreads / a.q_lanes, sub = (int)threadIdx.x & (a.q_lanes - 1);
-  const int h0 = part * per * kBatch + (int)threadIdx.x / a.q_lanes;
+  __shared__ long long places[kMaxTokens];
+  const int per = kThreads / a.q_lanes, sub = (int)threadIdx.x & (a.q_lanes - 1), group = (int)threadIdx.x / a.q_lanes;
   const int col[2] = {8 * sub, 8 * (sub + a.q_lanes)};
-  const int look = 32 / a.tokens, tokens = min(a.tokens, a.T - t0);
   uint4 v[kBatch][2];
   float wt[kBatch];
-  auto load = [&](int t) {
-    const size_t base = (size_t)t * a.H;
+  int tok[kBatch], head[kBatch];   // token of the step, head (H: none)
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) {
+    const int slot = group + j * per;
+    tok[j] = kSide ? slot / a.slots : 0;
+    head[j] = kSide ? slot & (a.slots - 1) : part * per * kBatch + slot;
+    if (kSide && tok[j] >= a.together) head[j] = a.H;
+  }
+  auto token = [&](int step, int j) { return kSide ? t0 + step * a.together + tok[j] : t0 + step; };
+  auto row_of = [&](int step, int j) { return (size_t)token(step, j) * a.H + head[j]; };
+  auto have = [&](int step, int j) { return head[j] < a.H && token(step, j) < a.T; };
+  auto place = [&](int step, int j) { return places[kSide ? step * a.together + (head[j] < a.H ? tok[j] : 0) : step]; };
+  auto load = [&](int step) {
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int h = h0 + j * per;
-      wt[j] = h < a.H && a.q_weight && sub == 0 ? a.q_weight[base + h] : 1.f;
+      const bool ok = have(step, j);
+      wt[j] = ok && a.q_weight && sub == 0 ? a.q_weight[row_of(step, j)] : 1.f;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         v[j][k] = make_uint4(0, 0, 0, 0);
-        if (h < a.H && col[k] < a.D) v[j][k] = *reinterpret_cast<const uint4*>(a.q + (base + h) * a.D + col[k]);
+        if (ok && col[k] < a.D) v[j][k] = *reinterpret_cast<const uint4*>(a.q + row_of(step, j) * a.D + col[k]);
       }
     }
   };
-  load(t0);   // on its way while the places are looked up
-  long long mine = locate_groups(a, min(t0 + lane / look, a.T - 1), look, lane & (look - 1)).pos;
+  load(0);   // on its way while the places are looked up
+  const int n = a.together * a.steps;
+  if (n == 1) {
+    if ((int)threadIdx.x < 32) places[0] = locate(a, t0, lane).pos;
+  } else if ((int)(threadIdx.x & ~31u) / 8 < n) {   // whole warps, four tokens each
+    const int i = (int)threadIdx.x / 8;
+    const long long pos = locate_groups(a, min(t0 + i, a.T - 1), 8, lane & 7).pos;
+    places[i] = t0 + i < a.T ? pos : -1;
+  }
+  __syncthreads();
 #pragma unroll 1
-  for (int i = 0; i < tokens; ++i) {
-    if (i > 0) load(t0 + i);
-    const long long pos = __shfl_sync(0xffffffffu, mine, i * look);
-    if (pos < 0) continue;
-    const size_t base = (size_t)(t0 + i) * a.H;
+  for (int step = 0; step < a.steps; ++step) {
+    if (step > 0) load(step);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (!in_rope(a, col[k])) continue;
-      const uint4 f = rotations(a, col[k], pos);
       uint32_t lost = 0;
+      uint4 f = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) v[j][k] = turn(v[j][k], f, lost);
+      for (int j = 0; j < kBatch; ++j) {
+        if ((kSide || j == 0) && place(step, j) >= 0) f = rotations(a, col[k], place(step, j));
+        v[j][k] = turn(v[j][k], f, lost);   // of a token without a place it is not used
+      }
       if (lost) {   // once for all: the rows are read again
-#pragma unroll 1
+#pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-          const int h = min(h0 + j * per, a.H - 1);
-          const uint4 x = turn_wide(*reinterpret_cast<const uint4*>(a.q + (base + h) * a.D + col[k]), f);
-          if (j == 0) v[0][k] = x;
-          else v[1][k] = x;
+          if (have(step, j) && place(step, j) >= 0)
+            v[j][k] = turn_wide(*reinterpret_cast<const uint4*>(a.q + row_of(step, j) * a.D + col[k]),
+                                rotations(a, col[k], place(step, j)));
         }
       }
     }
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int h = h0 + j * per;
       const int e = row_exponent(largest(largest(0u, v[j][0]), v[j][1]), a.q_lanes);
-      if (h >= a.H) continue;
+      if (!have(step, j) || place(step, j) < 0) continue;
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (col[k] < a.D) *reinterpret_cast<uint2*>(a.q_codes + (base + h) * a.D + col[k]) = coded(v[j][k], e);
-      if (sub == 0) a.q_scales[base + h] = __fmul_rn(scale_of(e), wt[j]);
+        if (col[k] < a.D) *reinterpret_cast<uint2*>(a.q_codes + row_of(step, j) * a.D + col[k]) = coded(v[j][k], e);
+      if (sub == 0) a.q_scales[row_of(step, j)] = __fmul_rn(scale_of(e), wt[j]);
     }
     __syncwarp();
   }
@@ -289,7 +309,9 @@ __global__ void __launch_bounds__(kThreads) indexer_append_kernel(const Args a) 
     if (t0 < a.T) new_keys(a, t0, lane);
   } else {
     const int i = blk - a.key_blocks;
-    queries(a, i / a.q_blocks * a.tokens, i % a.q_blocks, lane);
+    const int t0 = i / a.q_blocks * a.together * a.steps;
+    if (a.together > 1) queries<true>(a, t0, 0, lane);
+    else queries<false>(a, t0, i % a.q_blocks, lane);
   }
 }
 
@@ -302,18 +324,33 @@ int q_lanes_of(int D) {
 
 }  // namespace ia
 
-// Four tokens a block of queries where that leaves every SM eight blocks, else one.
-static int tokens_of(long long T, long long parts) { return T * parts >= 4ll * 8 * 152 ? 4 : 1; }
-
-static long long query_parts(int H, int D) {
-  const int heads = ia::kThreads / ia::q_lanes_of(D) * ia::kBatch;
-  return ((long long)H + heads - 1) / heads;
+struct QueryCut {
+  int together, steps, slots;
+  long long parts;   // blocks for the same tokens
+};
+// Tokens side by side where a block has room for the heads of two and more, as many as fit; else one
+// after the other, four where that leaves every SM eight blocks.
+static QueryCut query_cut(int H, int D, long long T) {
+  const int rows = ia::kThreads / ia::q_lanes_of(D) * ia::kBatch;
+  QueryCut c{1, 1, 1, 1};
+  while (c.slots < H && c.slots < rows) c.slots *= 2;
+  c.together = H <= c.slots ? rows / c.slots : 1;
+  if (c.together > ia::kMaxTokens) c.together = ia::kMaxTokens;
+  if (c.together == 1) {
+    c.parts = ((long long)H + rows - 1) / rows;
+    c.steps = T * c.parts >= 4ll * 8 * 152 ? 4 : 1;
+  }
+  return c;
 }
 
 long long indexer_append_blocks(int H, int D, int T, bool queries) {
   const int keys = ia::kThreads / ia::lanes_of(D);
-  const long long parts = queries ? query_parts(H, D) : 0, n = tokens_of(T, parts);
-  return ((long long)T + keys - 1) / keys + (T + n - 1) / n * parts;
+  long long n = ((long long)T + keys - 1) / keys;
+  if (queries) {
+    const QueryCut c = query_cut(H, D, T);
+    n += ((long long)T + c.together * c.steps - 1) / (c.together * c.steps) * c.parts;
+  }
+  return n;
 }
 
 cudaError_t launch_indexer_append(int H, int D, int R, int ps, int num_pages, const void* k_new, long long k_stride,
@@ -355,8 +392,11 @@ cudaError_t launch_indexer_append(int H, int D, int R, int ps, int num_pages, co
   a.hdr = hdr;
   const long long blocks = indexer_append_blocks(H, D, T, q != nullptr);
   a.key_blocks = (int)indexer_append_blocks(H, D, T, false);
-  a.q_blocks = q ? (int)query_parts(H, D) : 0;
-  a.tokens = tokens_of(T, a.q_blocks);
+  const QueryCut c = query_cut(H, D, T);
+  a.q_blocks = (int)c.parts;
+  a.together = c.together;
+  a.steps = c.steps;
+  a.slots = c.slots;
   ia::indexer_append_kernel<<<(unsigned)blocks, ia::kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }

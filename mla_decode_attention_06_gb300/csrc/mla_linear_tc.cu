@@ -20,8 +20,8 @@
 // Many tokens (pair kernel).  One pair of CTAs a pair of SMs, cta_group::2: 256 tokens (A) by 256
 // channels (B; int8 192), each CTA loading half of either operand, one tile after another.  Tiles go
 // group by group of token tiles, so that those in flight share operands in L2.  The accumulator is
-// double: while a tile's products run, four warps scale the last one, lay it out in shared memory
-// and store it by TMA, which also cuts off what lies past the last token or channel.  int8: four
+// double: while a tile's products run, other warps scale the last one, lay it out in shared memory and
+// store it by TMA, which also cuts off what lies past the last token or channel.  int8: four
 // warps widen the tokens' codes into tensor memory, four the weights' into shared memory (both
 // there would cost more of its bandwidth than the products leave).
 #include <algorithm>
@@ -64,13 +64,15 @@ struct Args {
   PlanHeader* hdr;
 };
 
-// Waits spin: a suspended waiter (try_wait) can wake a microsecond after the phase completes, longer
-// than a stage takes.  The clock is looked at once in 256 polls.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, PlanHeader* hdr) {
+// The issuing warps spin on a phase (a suspended waiter wakes later, between products); all others are
+// suspended by the hardware for a while, or two dozen spinning warps would take the issue slots of those
+// that work.  The clock is looked at now and then.
+template <bool kSpin>
+__device__ __forceinline__ bool wait_any(uint64_t* bar, uint32_t parity, PlanHeader* hdr) {
   uint64_t t0 = 0;
 #pragma unroll 1
-  for (uint32_t i = 1; !mbar_test_wait(bar, parity); ++i) {
-    if ((i & 255u) != 0) continue;
+  for (uint32_t i = 1; !(kSpin ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)); ++i) {
+    if ((i & (kSpin ? 255u : 15u)) != 0) continue;
     const uint64_t now = globaltimer_ns();
     if (t0 == 0) t0 = now;
     if (now - t0 > kWaitLimitNs) {
@@ -80,6 +82,13 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, PlanHea
   }
   return true;
 }
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, PlanHeader* hdr) {
+  return wait_any<false>(bar, parity, hdr);
+}
+__device__ __forceinline__ bool spin_bar(uint64_t* bar, uint32_t parity, PlanHeader* hdr) {
+  return wait_any<true>(bar, parity, hdr);
+}
+
 // Place in a ring of `n` stages, and the parity of the round.
 struct Ring {
   int s = 0;
@@ -91,6 +100,7 @@ struct Ring {
     }
   }
 };
+
 // Sixteen int8 codes as sixteen f16 values: a code with its sign bit flipped, in the low bits of
 // 1024, is 1024 + 128 + code.
 __device__ __forceinline__ void widen(uint4 raw, uint4& lo, uint4& hi) {
@@ -207,7 +217,7 @@ __global__ void __launch_bounds__(kSplitThreads<kInt8>, 2)
     const uint64_t d0 = smem_desc(smem_u32(kInt8 ? ring2 : ring), 16, 1024, kLayoutSw128);
     Ring at;
     for (int i = 0; i < steps; ++i, at.next(stages)) {
-      if (!wait_bar(&landed[at.s], at.round, a.hdr)) break;
+      if (!spin_bar(&landed[at.s], at.round, a.hdr)) break;
       tc_fence_after();
       if (elect_one()) {
         const uint64_t wd = d0 + (uint64_t)(at.s * (stage >> 4)), xd = wd + (kRowsW * 128 >> 4);
@@ -395,6 +405,8 @@ struct Pair {
   static constexpr int kStage2 = kN / 2 * 128;
   static constexpr int kAccs = kInt8 && kN == 256 ? 1 : 2;  // accumulators
   static constexpr int kColA = 384;                         // int8: TMEM columns of the widened tokens
+  static constexpr int kGroups = kInt8 ? 1 : 2;             // of four warps that read and store a tile
+  static constexpr int kBoxes = kInt8 ? 2 : 1;              // boxes of a group
   static constexpr int kBoxOut = 128 * 128;                 // 128 tokens x 64 channels bf16
   static constexpr int kRing2 = kStages * kStage;
   static constexpr int kOut = kRing2 + (kInt8 ? kStages2 * kStage2 : 0);
@@ -402,7 +414,7 @@ struct Pair {
   static constexpr int kBars = kScales + kN * 4;
   static constexpr int kSmem = 1024 + kBars + 8 * (2 * kStages + 2 * kStages2 + 4) + 16;
   static_assert(kSmem <= 232448 && (!kInt8 || kAccs * kN <= kColA));
-  static constexpr int kThreads = kInt8 ? 768 : 256;
+  static constexpr int kThreads = kInt8 ? 768 : 384;
 };
 
 // Tile i of a call: tokens from m0, channels from n0.  Groups of 8 token tiles, channel tiles in turn
@@ -417,7 +429,7 @@ __device__ __forceinline__ Tile tile_of(int i, int mtiles, int ntiles, int kn) {
 }
 
 // Warp 0 copies, warp 1 (of the pair's first CTA) issues the products, warp 2 owns the tensor memory,
-// warps 4-7 are the epilogue; int8: warps 8-11 widen the first half of a stage's tokens (thread = row =
+// warps 4-7 (e4m3: 4-11) are the epilogue; int8: warps 8-11 widen the first half of a stage's tokens (thread = row =
 // TMEM lane), 12-15 of its channels, 16-23 the second half's.
 template <bool kInt8, int kW>
 __global__ void __launch_bounds__(Pair<kInt8, kW>::kThreads, 1) __cluster_dims__(2, 1, 1)
@@ -450,7 +462,7 @@ __global__ void __launch_bounds__(Pair<kInt8, kW>::kThreads, 1) __cluster_dims__
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&acc_full[s], 1);
-      mbar_init(&acc_empty[s], 8);
+      mbar_init(&acc_empty[s], 8 * P::kGroups);
     }
     fence_mbar_init();
     prefetch_tensormap(&maps.x);
@@ -507,7 +519,7 @@ __global__ void __launch_bounds__(Pair<kInt8, kW>::kThreads, 1) __cluster_dims__
       if (n >= P::kAccs && !(ok = wait_bar(&acc_empty[acc.s], acc.round ^ 1, a.hdr))) break;
       tc_fence_after();
       for (int kb = 0; kb < (kInt8 ? 2 * nkb : nkb); ++kb, pos.next(kInt8 ? P::kStages2 : P::kStages)) {
-        if (!(ok = wait_bar(kInt8 ? &full2[pos.s] : &full[pos.s], pos.round, a.hdr))) break;
+        if (!(ok = spin_bar(kInt8 ? &full2[pos.s] : &full[pos.s], pos.round, a.hdr))) break;
         tc_fence_after();
         if (elect_one()) {
           if (kInt8) {
@@ -528,38 +540,40 @@ __global__ void __launch_bounds__(Pair<kInt8, kW>::kThreads, 1) __cluster_dims__
       if (elect_one()) mma_commit_pair(&acc_full[acc.s]);
       __syncwarp();
     }
-  } else if (warp >= 4 && warp < 8) {
-    const int row = tid - 128;                       // token of the CTA's half = TMEM lane
-    uint8_t* box = sm + P::kOut;
-    float* ws = reinterpret_cast<float*>(sm + P::kScales);   // read between a chunk's two barriers only
+  } else if (warp >= 4 && warp < 4 + 4 * P::kGroups) {
+    // Groups of four warps share the accumulator's chunks of 64 channels.
+    const int row = tid & 127, g4 = (warp - 4) >> 2;   // token of the CTA's half = TMEM lane; group
+    uint8_t* box = sm + P::kOut + g4 * P::kBoxes * P::kBoxOut;
+    float* ws = reinterpret_cast<float*>(sm + P::kScales);   // a group's own channels, read between its barriers
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + g4) : "memory"); };
     int chunk = 0;
     Ring acc;
     for (int tile = first; tile < tiles; tile += pairs, acc.next(P::kAccs)) {
       const Tile at = tile_of(tile, mtiles, ntiles, P::kN);
-      const int b = acc.s, m0 = at.m0 + 128 * rank;
-      for (int c = row; c < P::kN; c += 128) ws[c] = at.n0 + c < a.N ? a.w_scale[at.n0 + c] : 0.f;
+      const int m0 = at.m0 + 128 * rank;
+      for (int c = 64 * g4 + (row & 63) + 64 * P::kGroups * (row >> 6); c < P::kN; c += 128 * P::kGroups)
+        ws[c] = at.n0 + c < a.N ? a.w_scale[at.n0 + c] : 0.f;
       const float xs = m0 + row < a.T ? a.x_scale[m0 + row] : 0.f;
-      bool ok = wait_bar(&acc_full[b], acc.round, a.hdr);
+      const bool ok = wait_bar(&acc_full[acc.s], acc.round, a.hdr);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int c0 = 0; c0 < P::kN; c0 += 64, ++chunk) {
-        uint8_t* dst = box + (chunk & 1) * P::kBoxOut;
+      for (int c0 = 64 * g4; c0 < P::kN; c0 += 64 * P::kGroups, ++chunk) {
+        uint8_t* dst = box + (chunk & (P::kBoxes - 1)) * P::kBoxOut;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t r[32];
-          tmem_ld32(tmem + b * P::kN + c0 + 32 * half + lanes, r);
+          tmem_ld32(tmem + acc.s * P::kN + c0 + 32 * half + lanes, r);
           if (half == 0) {
-            // the box written two chunks ago has left (its writer waits), the scales are there
-            if (row == 0) bulk_wait_read<1>();
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (row == 0) bulk_wait_read<P::kBoxes - 1>();   // what the box held has left
+            group_sync();                                      // ... and the scales are there
           }
           tmem_ld_wait();
-          if (half == 1 && c0 + 64 == P::kN) {   // the tile's accumulator is read
+          if (half == 1 && c0 + 64 * P::kGroups >= P::kN) {   // this warp has read its part of the accumulator
             tc_fence_before();
             __syncwarp();
-            if (elect_one()) mbar_arrive_remote(mapa_shared(smem_u32(&acc_empty[b]), 0));
+            if (elect_one()) mbar_arrive_remote(mapa_shared(smem_u32(&acc_empty[acc.s]), 0));
           }
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
@@ -580,7 +594,7 @@ __global__ void __launch_bounds__(Pair<kInt8, kW>::kThreads, 1) __cluster_dims__
           }
         }
         fence_proxy_async_smem();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        group_sync();
         if (row == 0) {
           if (m0 < a.T && at.n0 + c0 < a.N) tma_store_2d(&maps.out, dst, at.n0 + c0, m0);
           bulk_commit();
@@ -676,14 +690,25 @@ bool encode_out(CUtensorMap* m, void* p, int T, int N, long long stride) {
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// How the split kernel cuts a call, and what that takes, in ns: as above, a stage of e4m3 200 ns and half a
+// one a token of the tile, of int8 580 and 2.2, 1.7 us a round of blocks and 3.5.
+template <bool kInt8>
+long long split_ns(Args* a, int sms) {
+  const int ttiles = (a->T + kMaxTokens - 1) / kMaxTokens;   // as even as they come, in 16s
+  a->TN = ((a->T + ttiles - 1) / ttiles + 15) / 16 * 16;
+  const long long tiles = (long long)((a->N + kRowsW - 1) / kRowsW) * ((a->T + a->TN - 1) / a->TN);
+  const int nkb = (a->K + kStepK - 1) / kStepK;
+  a->C = 1;
+  while (a->C < 8 && tiles * a->C * 2 <= sms && nkb >= 8 * a->C) a->C *= 2;
+  const int stage = kInt8 ? 580 + a->TN * 22 / 10 : 200 + a->TN / 2;
+  return 3500 + (tiles * a->C + sms - 1) / sms * (1700 + (nkb + a->C - 1ll) / a->C * stage);
+}
+
 template <bool kInt8>
 cudaError_t launch_split(Args a, const void* x, const void* w, int sms, cudaStream_t s) {
   Maps maps;
-  a.TN = a.T >= kMaxTokens ? kMaxTokens : (a.T + 15) / 16 * 16;
   const int tiles = (a.N + kRowsW - 1) / kRowsW, ttiles = (a.T + a.TN - 1) / a.TN;
   const int nkb = (a.K + kStepK - 1) / kStepK;
-  a.C = 1;
-  while (a.C < 8 && (long long)tiles * ttiles * a.C * 2 <= sms && nkb >= 8 * a.C) a.C *= 2;
   // Two blocks share an SM where there are more than SMs, and where clusters are large: of eight blocks that
   // fill an SM each the device holds 16 (17 tiles of one token took two waves, 19 us).
   const int stage = (kRowsW + a.TN) * 128, budget = (long long)tiles * ttiles * a.C > sms || a.C > 2 ? 108 * 1024 : 200 * 1024;
@@ -737,24 +762,22 @@ cudaError_t launch_pair(const Args& a, const void* x, const void* w, int sms, cu
   return cudaGetLastError();
 }
 
-// The width of the pair kernel's tiles: the one that takes least time by its number of rounds of tiles over the
-// pairs of SMs, the wider of two equals.  A round of e4m3 tiles takes as long as its width and a
-// quarter more of the widest (333 tokens, 8,192 x 16,384, a round of 256, 192, 128: 44, 33, 25.5 us;
-// 4,096 tokens, 24,576 x 1,536: 4.5, 3.8, 2.8 us); one of int8 tiles is held up by the widening of
-// its tokens' codes where it is narrow (84, 70, 68 us; 9.7, 6.9, 6.4 us).
+// What a call takes by the pair kernel, in ns, and the width of its tiles: rounds of tiles over the pairs of SMs
+// by stages of K by a stage's time (measured at 16,384 of K: tiles of 256, 192, 128 channels 340, 260, 200 ns,
+// int8 660, 550, 530 - there the widening of the tokens' codes holds up narrow tiles), and 8 us.
 template <bool kInt8>
-int pair_width(int T, int N, int sms) {
-  int best = 0;
+long long pair_ns(const Args& a, int sms, int* width) {
   long long least = 0;
   for (int w : {256, 192, 128}) {
-    const long long tiles = (long long)((T + 255) / 256) * ((N + w - 1) / w);
-    const long long cost = (tiles + sms / 2 - 1) / (sms / 2) * (kInt8 ? std::max(w, 184) : w + 64);
-    if (best == 0 || cost < least) {
-      best = w;
-      least = cost;
+    const long long tiles = (long long)((a.T + 255) / 256) * ((a.N + w - 1) / w), nkb = (a.K + kStepK - 1) / kStepK;
+    const int stage = kInt8 ? (w == 256 ? 660 : w == 192 ? 550 : 530) : (w == 256 ? 340 : w == 192 ? 260 : 200);
+    const long long ns = 8000 + (tiles + sms / 2 - 1) / (sms / 2) * (nkb * stage + 400);
+    if (least == 0 || ns < least) {
+      *width = w;
+      least = ns;
     }
   }
-  return best;
+  return least;
 }
 
 template <bool kInt8>
@@ -764,11 +787,14 @@ cudaError_t launch(const Args& a, const void* x, const void* w, int sms, cudaStr
     if (a.T == 2) return launch_dot<2, 2>(a, x, w, sms, s);
     return a.T <= 4 ? launch_dot<4, 4>(a, x, w, sms, s) : launch_dot<8, 4>(a, x, w, sms, s);
   }
-  // Above 128 tokens a pair's 256 rows cost less than they waste (192 tokens, 8,192 x 16,384: 70 us against 83
-  // for int8, 33 against 34 for e4m3; 256: 70 against 91, 34 against 40); above 64 where the split kernel's
-  // tiles are more than the SMs (128 tokens, 24,576 x 1,536: 20.5 against 34.5, 13.2 against 14.1).
-  if (a.T <= 64 || (a.T <= 128 && (a.N + kRowsW - 1) / kRowsW <= sms)) return launch_split<kInt8>(a, x, w, sms, s);
-  switch (pair_width<kInt8>(a.T, a.N, sms)) {
+  // The estimates follow what was measured within a fifth where the two kernels are close: 128 tokens, 8,192 x
+  // 16,384, pair 70 us and split 61 (int8), 33 and 30; 24,576 x 1,536, 20.5 and 34.5, 13.2 and 14.1;
+  // 192 tokens, 8,192 x 16,384, 70 and 83, 33 and 34.
+  int width = 0;
+  const long long pair = pair_ns<kInt8>(a, sms, &width);
+  Args b = a;
+  if (split_ns<kInt8>(&b, sms) <= pair) return launch_split<kInt8>(b, x, w, sms, s);
+  switch (width) {
     case 256: return launch_pair<kInt8, 256>(a, x, w, sms, s);
     case 192: return launch_pair<kInt8, 192>(a, x, w, sms, s);
     default: return launch_pair<kInt8, 128>(a, x, w, sms, s);

@@ -102,6 +102,13 @@ def test_heads(dev, H):
     check(Case(H=H, D=64, R=0, qlens=(3, 30), past=(70, 0)), dev)
 
 
+@pytest.mark.parametrize("H,D,R,tokens", [(64, 128, 64, 4870), (65, 128, 64, 2440), (4, 64, 64, 1003), (1, 128, 32, 100),
+                                          (17, 96, 0, 333), (3, 8, 8, 70), (128, 64, 32, 50), (1, 16, 16, 1000)])
+def test_tokens_of_a_block(dev, H, D, R, tokens):
+    """One token after the other, and several side by side, in blocks that the last tokens leave part empty."""
+    check(Case(D=D, R=R, H=H, qlens=(tokens - 37, 0, 30, 7), past=(0, 5, 11, 3), pad=3, ps=16), dev)
+
+
 @pytest.mark.parametrize("B,ps", [(1, 1), (2, 8), (33, 24), (1100, 64)])
 def test_many_requests_and_pages(dev, B, ps):
     r = np.random.default_rng(B)
