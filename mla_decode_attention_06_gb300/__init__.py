@@ -211,6 +211,8 @@ def _unread_status(device, stream):
 
 def _handle(stream, device):
     """The cudaStream_t that a call runs on, without a Stream object for the current one (3 us of a call)."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be CUDA tensors, not on {device}")
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 

@@ -132,3 +132,22 @@ def test_refusals_streams_and_graph(dev):
     for x in (a, b):
         assert same(x.view(torch.int16).cpu().numpy().view(np.uint16), c.expected())
     assert M.mla_cache_read(t(np.zeros(2, np.int32)), *args[1:], **kw, total_rows=0).shape == (0, 576)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_offsets_past_32_bits(dev, fmt):
+    """The last pages of a pool of more than 2^32 bytes."""
+    import mla_decode_attention_06_gb300 as M
+    c = Case(FORMATS[fmt], 512, 64, ps=64, qlens=(100, 30), past=(0, 40))
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)  # noqa: E731
+    base = (1 << 32) // (64 * c.pool.shape[1]) + 5
+    pool = torch.empty((base + c.num_pages) * 64, c.pool.shape[1], dtype=torch.uint8, device=dev)
+    pool[base * 64:] = t(c.pool)
+    scales = None
+    if c.scales is not None:
+        scales = torch.empty(len(pool), device=dev)
+        scales[base * 64:] = t(c.scales)
+    table = np.where(c.table >= 0, c.table + base, -1).astype(np.int32)
+    got = M.mla_cache_read(t(c.offsets), pool, t(table), t(c.lens), kv_lora_rank=512, qk_rope=64, page_size=64,
+                           total_rows=c.T, cache_format=FORMATS[fmt], kv_scales=scales, debug=True)
+    assert same(got.view(torch.int16).cpu().numpy().view(np.uint16), c.expected())

@@ -192,3 +192,21 @@ def test_streams_and_graph(dev):
     for got in ((*pools[0], *a), (*pools[1], *b)):
         for x, y in zip(got, want):
             assert np.array_equal(x.view(torch.uint8).cpu().numpy(), np.ascontiguousarray(y).view(np.uint8))
+
+
+def test_offsets_past_32_bits(dev):
+    """The last pages of an index cache of more than 2^32 bytes."""
+    import mla_decode_attention_06_gb300 as M
+    c = Case(qlens=(100, 30), past=(0, 40), ps=64, H=2)
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)  # noqa: E731
+    base = (1 << 32) // (64 * 128) + 5
+    pool = torch.empty((base + c.num_pages) * 64, 128, dtype=torch.uint8, device=dev)
+    scales = torch.empty(len(pool), device=dev)
+    pool[base * 64:], scales[base * 64:] = t(c.pool), t(c.scales)
+    table = np.where(c.table >= 0, c.table + base, -1).astype(np.int32)
+    M.mla_indexer_append(bf16(c.k, dev), t(c.offsets), pool, scales, t(table), t(c.lens), page_size=64,
+                         freqs_cis=bf16(c.freqs, dev), k_norm_gamma=bf16(c.gamma, dev), k_norm_beta=bf16(c.beta, dev),
+                         epsilon=EPS, debug=True)
+    want = c.expected()
+    assert np.array_equal(pool[base * 64:].cpu().numpy(), want[0])
+    assert np.array_equal(scales[base * 64:].cpu().numpy(), want[1])

@@ -164,3 +164,49 @@ def test_no_tokens(dev):
     w, ws = codes("int8", 2, 64, 32, dev)
     x = torch.empty(0, 32, dtype=torch.int8, device=dev)
     assert call("int8", x, torch.empty(0, device=dev), w, ws).shape == (0, 64)
+
+
+@pytest.mark.parametrize("kind,T", [("int8", 1), ("int8", 9), ("int8", 300), ("fp8", 2), ("fp8", 300)])
+def test_offsets_past_32_bits(dev, kind, T):
+    """Weights of more than 2^32 codes, outputs far behind each other: the last channels and tokens."""
+    N, K = 262144 + 264, 16384
+    w = torch.zeros(N, K, dtype=torch.int8 if kind == "int8" else torch.float8_e4m3fn, device=dev)
+    ws = torch.ones(N, device=dev)
+    tail, tail_s = codes(kind, 5, 200, K, dev)
+    w.view(torch.uint8)[-200:] = tail.view(torch.uint8)
+    ws[-200:] = tail_s
+    x, xs = codes(kind, 6, T, K, dev)
+    out = call(kind, x, xs, w, ws, debug=True)
+    check(out[:, -200:], x, xs, tail, tail_s)
+    assert (out[:, :-200] == 0).all()
+
+
+def test_wide_output_strides(dev):
+    """Rows of the output more than 2^31 elements after the first."""
+    x, xs = codes("fp8", 6, 140, 64, dev)
+    w, ws = codes("fp8", 7, 64, 64, dev)
+    stride = 1 << 24
+    buf = torch.empty(139 * stride + 64, dtype=torch.bfloat16, device=dev)
+    out = buf.as_strided((140, 64), (stride, 1))
+    call("fp8", x, xs, w, ws, out=out, debug=True)
+    check(out, x, xs, w, ws)
+    big, bs = codes("fp8", 8, 300, 64, dev)
+    buf = torch.empty(299 * (1 << 23) + 64, dtype=torch.bfloat16, device=dev)
+    out = buf.as_strided((300, 64), (1 << 23, 1))
+    call("fp8", big, bs, w, ws, out=out, debug=True)
+    check(out, big, bs, w, ws)
+
+
+def test_refuses_outputs_off_the_boundary(dev):
+    import mla_decode_attention_06_gb300 as M
+    x, xs = codes("int8", 1, 20, 64, dev)
+    w, ws = codes("int8", 2, 64, 64, dev)
+    wide = torch.empty(20, 128, dtype=torch.bfloat16, device=dev)
+    with pytest.raises(M.MlaError):
+        call("int8", x, xs, w, ws, out=wide[:, 4:68])
+    with pytest.raises(M.MlaError):
+        call("int8", x, xs, w, ws, out=wide[:1, :64].expand(20, 64))
+    with pytest.raises(ValueError):
+        call("int8", x, xs, w, ws, out=wide[:19, :64])
+    with pytest.raises(ValueError):
+        call("int8", x, xs, w.T.contiguous()[:, :20], ws, out=None)

@@ -179,3 +179,17 @@ def test_empty_and_streams_and_graph(dev):
             graph.replay()
         assert np.array_equal(got[0].cpu().numpy().view(np.uint8), want[0])
         assert np.array_equal(got[1].cpu().numpy(), want[1])
+
+
+def test_offsets_past_32_bits(dev):
+    """Rows that lie, and outputs that end, more than 2^31 elements after the first."""
+    import mla_decode_attention_06_gb300 as M
+    for T, D, stride in ((300, 264, 1 << 23), (66000, 32768, 32768)):
+        x = torch.empty((T - 1) * stride + D, dtype=torch.bfloat16, device=dev).as_strided((T, D), (stride, 1))
+        last = rows(3, 2, D)
+        x.zero_()
+        x[-2:] = bf16(last, dev)
+        codes, s, _ = M.mla_rmsnorm_quant(x, code_format=M.MLA_CODES_INT8)
+        want = cr.encode(last, cr.INT8)
+        assert np.array_equal(codes[-2:].cpu().numpy().view(np.uint8), want[0])
+        assert np.array_equal(s[-2:].cpu().numpy(), want[1]) and (s[:-2] == 1).all() and not codes[:-2].any()
