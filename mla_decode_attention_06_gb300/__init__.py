@@ -190,6 +190,9 @@ def mla_decode_paged_fp8(q, input_row_offsets, kv_pool_fp8, kv_scales, block_tab
 
 
 _I32 = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32,)
+_INT32 = (torch.int32,)
+_INT8 = (torch.int8,)
+_F8 = (torch.float8_e4m3fn, torch.uint8)
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
 
@@ -229,6 +232,22 @@ def _status_word(workspace, debug, device, stream, handle):
     return _ptr(workspace, "workspace", None, device), workspace.numel() * workspace.element_size(), workspace
 
 
+def _at(t, name, dtypes, index):
+    """_ptr of a tensor that is right, by its cheapest attributes; what is not goes to _ptr, which says why."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype in dtypes and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t, name, dtypes, torch.device("cuda", index))
+
+
+def _bytes_at(t, name, index):
+    """_at of a tensor of any type."""
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t, name, None, torch.device("cuda", index))
+
+
 _fns = {}
 
 
@@ -237,7 +256,7 @@ def _call(name, device, *args):
     fn = _fns.get(name)
     if fn is None:
         fn = _fns[name] = getattr(_lib.load(), name)
-    if device.index is None or torch.cuda.current_device() == device.index:
+    if device.index is None or torch._C._cuda_getDevice() == device.index:
         rc = fn(*args)
     else:
         with torch.cuda.device(device):
@@ -250,9 +269,11 @@ def _tables(input_row_offsets, block_table, cache_lens, dev):
     B = input_row_offsets.numel() - 1
     if B < 1 or block_table.dim() != 2 or block_table.shape[0] < B or cache_lens.numel() < B:
         raise ValueError("input_row_offsets, block_table and cache_lens disagree on the number of requests")
-    return (B, _ptr(input_row_offsets, "input_row_offsets", _I32, dev),
-            _ptr(block_table, "block_table", (torch.int32,), dev), block_table.shape[1],
-            _ptr(cache_lens, "cache_lens", _I32, dev))
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be CUDA tensors, not on {dev}")
+    i = dev.index
+    return (B, _at(input_row_offsets, "input_row_offsets", _I32, i), _at(block_table, "block_table", _INT32, i),
+            block_table.shape[1], _at(cache_lens, "cache_lens", _I32, i))
 
 
 def mla_cache_row_bytes(cache_format: int, kv_lora_rank: int, qk_rope: int) -> int:
@@ -326,9 +347,13 @@ def _row_strided(t, name, shape):
     """Pointer and row stride of a bf16 CUDA tensor whose rows may lie apart (a slice of a wider one)."""
     if t.dtype != torch.bfloat16 or not t.is_cuda:
         raise TypeError(f"{name} must be a bf16 CUDA tensor")
-    if t.dim() != 2 or t.shape[1] != shape or (t.shape[0] > 0 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [rows, {shape}] with unit stride along a row")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else -(-shape // 8) * 8
+    if t.dim() != 2 or t.shape[1] != shape:
+        raise ValueError(f"{name} must be [rows, {shape}]")
+    n = t.shape[0]
+    by_row, along = t.stride()
+    if n > 0 and along != 1:
+        raise ValueError(f"{name} must have unit stride along a row")
+    return t.data_ptr(), by_row if n > 1 else -(-shape // 8) * 8
 
 
 def _sized(t, name, n):
@@ -356,12 +381,15 @@ def mla_cache_read(input_row_offsets, kv_pool, block_table, cache_lens, *, kv_lo
     elif out.dim() != 2 or out.shape[1] != L + R or (total_rows is not None and out.shape[0] != total_rows):
         raise ValueError("out must be [total_rows, L+R]")
     status, status_bytes, workspace = _status_word(workspace, debug, dev, stream, handle)
+    i = dev.index
     _call("mla_cache_read", dev, ctypes.byref(dims), int(cache_format), offsets, B, out.shape[0],
-          _ptr(kv_pool, "kv_pool", None, dev), _ptr(kv_scales, "kv_scales", _F32, dev), table, table_stride,
-          lens, _ptr(out, "out", _BF16, dev), MLA_FLAG_DEBUG_CHECKS if debug else 0, status, status_bytes, handle)
+          _bytes_at(kv_pool, "kv_pool", i), _at(kv_scales, "kv_scales", _F32, i), table, table_stride, lens,
+          _at(out, "out", _BF16, i), MLA_FLAG_DEBUG_CHECKS if debug else 0, status, status_bytes, handle)
     return out
 
 
+_CODES_OUT = {MLA_CODES_BF16: (), MLA_CODES_E4M3: (torch.float8_e4m3fn, torch.uint8),
+              MLA_CODES_INT8: (torch.int8, torch.uint8)}
 _CODES = {MLA_CODES_BF16: torch.bfloat16, MLA_CODES_E4M3: torch.float8_e4m3fn, MLA_CODES_INT8: torch.int8}
 
 
@@ -393,36 +421,39 @@ def mla_rmsnorm_quant(x, gamma=None, *, epsilon: float = 1e-6, code_format: int 
     elif y_out is None:
         y_out = _buffer((T, D), torch.bfloat16, dev, stream, returned=True)
     for t, name in ((residual, "residual"), (residual_out, "residual_out"), (y_out, "y_out"), (codes_out, "codes_out")):
-        if t is not None and tuple(t.shape) != (T, D):
+        if t is not None and t.shape != x.shape:
             raise ValueError(f"{name} must be [T, D]")
     _sized(gamma, "gamma", D)
     _sized(scales_out, "scales_out", T)
-    _call("mla_rmsnorm_quant", dev, code_format, T, D, px, stride, _ptr(residual, "residual", _BF16, dev),
-          _ptr(residual_out, "residual_out", _BF16, dev), _ptr(gamma, "gamma", _BF16, dev), float(epsilon),
-          _ptr(y_out, "y_out", _BF16, dev), _ptr(codes_out, "codes_out", (_CODES[code_format], torch.uint8), dev),
-          _ptr(scales_out, "scales_out", _F32, dev), _handle(stream, dev))
+    handle, i = _handle(stream, dev), dev.index
+    _call("mla_rmsnorm_quant", dev, code_format, T, D, px, stride, _at(residual, "residual", _BF16, i),
+          _at(residual_out, "residual_out", _BF16, i), _at(gamma, "gamma", _BF16, i), epsilon, _at(y_out, "y_out", _BF16, i),
+          _at(codes_out, "codes_out", _CODES_OUT[code_format], i), _at(scales_out, "scales_out", _F32, i), handle)
     return (codes_out, scales_out, residual_out) if coded else (y_out, None, residual_out)
 
 
 def _linear(name, dtypes, x_codes, x_scales, w_codes, w_scales, out, debug, workspace, stream):
     dev = x_codes.device
-    if x_codes.dim() != 2 or w_codes.dim() != 2 or x_codes.shape[1] != w_codes.shape[1]:
+    x_shape, w_shape = x_codes.shape, w_codes.shape
+    if len(x_shape) != 2 or len(w_shape) != 2 or x_shape[1] != w_shape[1]:
         raise ValueError("x_codes must be [T, K] and w_codes [N, K]")
-    T, K = x_codes.shape
-    N = w_codes.shape[0]
+    T, K = x_shape
+    N = w_shape[0]
     _sized(x_scales, "x_scales", T)
     _sized(w_scales, "w_scales", N)
-    handle = _handle(stream, dev)
+    handle, i = _handle(stream, dev), dev.index
     if out is None:
         out = _buffer((T, N), torch.bfloat16, dev, stream, returned=True)
-    elif out.shape[0] != T:
-        raise ValueError(f"out must be [{T}, {N}]")
-    p_out, out_stride = _row_strided(out, "out", N)
-    if out.device != dev:
-        raise ValueError(f"out is on {out.device}, expected {dev}")
+        p_out, out_stride = out.data_ptr(), N
+    else:
+        if out.shape[0] != T:
+            raise ValueError(f"out must be [{T}, {N}]")
+        p_out, out_stride = _row_strided(out, "out", N)
+        if out.get_device() != i:
+            raise ValueError(f"out is on {out.device}, expected {dev}")
     status, status_bytes, workspace = _status_word(workspace, debug, dev, stream, handle)
-    _call(name, dev, T, N, K, _ptr(x_codes, "x_codes", dtypes, dev), _ptr(x_scales, "x_scales", _F32, dev),
-          _ptr(w_codes, "w_codes", dtypes, dev), _ptr(w_scales, "w_scales", _F32, dev), p_out, out_stride,
+    _call(name, dev, T, N, K, _at(x_codes, "x_codes", dtypes, i), _at(x_scales, "x_scales", _F32, i),
+          _at(w_codes, "w_codes", dtypes, i), _at(w_scales, "w_scales", _F32, i), p_out, out_stride,
           MLA_FLAG_DEBUG_CHECKS if debug else 0, status, status_bytes, handle)
     return out
 
@@ -430,13 +461,13 @@ def _linear(name, dtypes, x_codes, x_scales, w_codes, w_scales, out, debug, work
 def mla_linear_fp8(x_codes, x_scales, w_codes, w_scales, *, out=None, debug: bool = False, workspace=None, stream=None):
     """Projection over e4m3 codes: x_codes [T, K], w_codes [N, K] (float8_e4m3fn or uint8), x_scales f32 [T],
     w_scales f32 [N].  Returns out bf16 [T, N] (rows may be strided if given)."""
-    return _linear("mla_linear_fp8", (torch.float8_e4m3fn, torch.uint8), x_codes, x_scales, w_codes, w_scales, out, debug,
+    return _linear("mla_linear_fp8", _F8, x_codes, x_scales, w_codes, w_scales, out, debug,
                    workspace, stream)
 
 
 def mla_linear_int8(x_codes, x_scales, w_codes, w_scales, *, out=None, debug: bool = False, workspace=None, stream=None):
     """mla_linear_fp8 over int8 codes."""
-    return _linear("mla_linear_int8", (torch.int8,), x_codes, x_scales, w_codes, w_scales, out, debug, workspace, stream)
+    return _linear("mla_linear_int8", _INT8, x_codes, x_scales, w_codes, w_scales, out, debug, workspace, stream)
 
 
 def mla_indexer_append(k_new, input_row_offsets, k_cache, k_scales, block_table, cache_lens, *, page_size: int,
@@ -451,7 +482,6 @@ def mla_indexer_append(k_new, input_row_offsets, k_cache, k_scales, block_table,
         raise ValueError("k_new must be [T, D]")
     T, D = k_new.shape
     pk, stride = _row_strided(k_new, "k_new", D)
-    f8 = (torch.uint8, torch.float8_e4m3fn)
     R, max_len = (freqs_cis.shape[1], freqs_cis.shape[0]) if freqs_cis is not None else (0, 0)
     num_pages = _pages(k_cache, page_size, D)
     _sized(k_scales, "k_scales", num_pages * page_size)
@@ -474,12 +504,13 @@ def mla_indexer_append(k_new, input_row_offsets, k_cache, k_scales, block_table,
     B, offsets, table, table_stride, lens = _tables(input_row_offsets, block_table, cache_lens, dev)
     handle = _handle(stream, dev)
     status, status_bytes, workspace = _status_word(workspace, debug, dev, stream, handle)
-    _call("mla_indexer_append", dev, H, D, R, page_size, num_pages, pk, stride, offsets, B, T, _ptr(q, "q", _BF16, dev),
-          _ptr(q_weight, "q_weight", _F32, dev), _ptr(q_codes, "q_codes", f8, dev), _ptr(q_scales, "q_scales", _F32, dev),
-          _ptr(k_cache, "k_cache", f8, dev), _ptr(k_scales, "k_scales", _F32, dev), table, table_stride, lens,
-          _ptr(freqs_cis, "freqs_cis", _BF16, dev), max_len, _ptr(k_norm_gamma, "k_norm_gamma", _BF16, dev),
-          _ptr(k_norm_beta, "k_norm_beta", _BF16, dev), float(epsilon), MLA_FLAG_DEBUG_CHECKS if debug else 0,
-          status, status_bytes, handle)
+    i = dev.index
+    _call("mla_indexer_append", dev, H, D, R, page_size, num_pages, pk, stride, offsets, B, T, _at(q, "q", _BF16, i),
+          _at(q_weight, "q_weight", _F32, i), _at(q_codes, "q_codes", _F8, i), _at(q_scales, "q_scales", _F32, i),
+          _at(k_cache, "k_cache", _F8, i), _at(k_scales, "k_scales", _F32, i), table, table_stride, lens,
+          _at(freqs_cis, "freqs_cis", _BF16, i), max_len, _at(k_norm_gamma, "k_norm_gamma", _BF16, i),
+          _at(k_norm_beta, "k_norm_beta", _BF16, i), epsilon, MLA_FLAG_DEBUG_CHECKS if debug else 0, status, status_bytes,
+          handle)
     return q_codes, q_scales
 
 
