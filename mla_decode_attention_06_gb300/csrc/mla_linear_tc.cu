@@ -4,26 +4,31 @@
 //
 // on tcgen05, fp32 accumulators in tensor memory.  e4m3 codes are the operands of kind::f8f6f4 as
 // they lie in memory.  The GB300 has no fast integer tensor path (its int8 rate is a tenth of its
-// f16 rate), so int8 codes are widened to f16 in shared memory: every int8 value is an f16 value, every
-// product of two is exact in the fp32 accumulator.
+// f16 rate), so int8 codes are widened to f16 on the SM: every int8 value is an f16 value, every
+// product of two is exact in the fp32 accumulator.  Three kernels, chosen by estimated time:
 //
 // Few tokens (split kernel).  The weights are the A operand (128 output channels a tile), the
-// tokens the B operand (up to 256), so that one token costs no more than a tile's weights, and the
+// tokens the B operand (16 to 128), so that one token costs no more than a tile's weights, and the
 // call is bound by reading those once.  Where the tiles are fewer than the SMs, a cluster of CTAs
 // splits K: each leaves its fp32 partial in its shared memory and sums a share of the tokens over the
-// cluster, in rank order (the result does not depend on timing).
+// cluster, in rank order (the result does not depend on timing).  Times of a call among others, inputs out
+// of L2: 64 x 24,576 x 1,536 e4m3 10.9 us (6.0 at the copy rate; launch, first bytes and end of a
+// block take 5), 1 x 2,112 x 8,192 e4m3 8.0 us, 16 tokens of int8 14.3 us (widening).
 //
-// Up to eight int8 tokens (dot kernel).  Widening costs the split kernel more than the weights' way from memory
-// does, so here warps take the dot products of codes on the integer units (four a lane and
-// instruction, exact), straight from registers; K is split over a block's warps where rows are few.
+// Up to eight int8 tokens (dot kernel).  Widening costs the split kernel more than the weights' way from
+// memory does, so here warps take the dot products of codes on the integer units (four products a
+// lane and instruction, exact), straight from registers; K is split over a block's warps where rows are
+// few.  1 x 2,112 x 8,192 5.0 us (2.5 at the copy rate), 1 x 8,192 x 16,384 25 us (20).
 //
-// Many tokens (pair kernel).  One pair of CTAs a pair of SMs, cta_group::2: 256 tokens (A) by 256
-// channels (B; int8 192), each CTA loading half of either operand, one tile after another.  Tiles go
-// group by group of token tiles, so that those in flight share operands in L2.  The accumulator is
-// double: while a tile's products run, other warps scale the last one, lay it out in shared memory and
-// store it by TMA, which also cuts off what lies past the last token or channel.  int8: four
-// warps widen the tokens' codes into tensor memory, four the weights' into shared memory (both
-// there would cost more of its bandwidth than the products leave).
+// Many tokens (pair kernel).  A pair of CTAs a pair of SMs, cta_group::2: 256 tokens (A) by 256, 192 or 128
+// channels (B), each CTA loading half of either operand, one tile after another.  Tiles go group by
+// group of token tiles, so that those in flight share operands in L2.  The accumulator is double: while
+// a tile's products run, other warps scale the last one, lay it out in shared memory and store it by TMA,
+// which also cuts off what lies past the last token or channel.  int8: for either half of a stage four
+// warps widen the tokens' codes into tensor memory, four the weights' into shared memory (both there would
+// cost more of its bandwidth than the products leave).  8,192 x 8,192 x 16,384 e4m3: 600 us, 670 under the
+// power cap, 95 % of twice the measured bf16 rate of either; the tensor pipe is active 98 % of the time.
+// 4,096 x 24,576 x 1,536: e4m3 95 us (80), int8 188 us (161).
 #include <algorithm>
 
 #include "mla_kernels.cuh"
@@ -547,6 +552,15 @@ __global__ void __launch_bounds__(Pair<kInt8, kW>::kThreads, 1) __cluster_dims__
     float* ws = reinterpret_cast<float*>(sm + P::kScales);   // a group's own channels, read between its barriers
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + g4) : "memory"); };
+    auto group_and = [&](bool ok) {
+      uint32_t r;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+          : "=r"(r)
+          : "r"((uint32_t)ok), "r"(1 + g4)
+          : "memory");
+      return r != 0;
+    };
     int chunk = 0;
     Ring acc;
     for (int tile = first; tile < tiles; tile += pairs, acc.next(P::kAccs)) {
@@ -555,8 +569,8 @@ __global__ void __launch_bounds__(Pair<kInt8, kW>::kThreads, 1) __cluster_dims__
       for (int c = 64 * g4 + (row & 63) + 64 * P::kGroups * (row >> 6); c < P::kN; c += 128 * P::kGroups)
         ws[c] = at.n0 + c < a.N ? a.w_scale[at.n0 + c] : 0.f;
       const float xs = m0 + row < a.T ? a.x_scale[m0 + row] : 0.f;
-      const bool ok = wait_bar(&acc_full[acc.s], acc.round, a.hdr);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      // the group goes on or gives up together: its barriers count all of its warps
+      if (!group_and(wait_bar(&acc_full[acc.s], acc.round, a.hdr))) break;
       tc_fence_after();
 #pragma unroll 1
       for (int c0 = 64 * g4; c0 < P::kN; c0 += 64 * P::kGroups, ++chunk) {
@@ -764,14 +778,15 @@ cudaError_t launch_pair(const Args& a, const void* x, const void* w, int sms, cu
 
 // What a call takes by the pair kernel, in ns, and the width of its tiles: rounds of tiles over the pairs of SMs
 // by stages of K by a stage's time (measured at 16,384 of K: tiles of 256, 192, 128 channels 340, 260, 200 ns,
-// int8 660, 550, 530 - there the widening of the tokens' codes holds up narrow tiles), and 8 us.
+// int8 660, 550, 530 - there the widening of the tokens' codes holds up narrow tiles, and the end of
+// a tile of 256, without a second accumulator, is not overlapped), and 8 us.
 template <bool kInt8>
 long long pair_ns(const Args& a, int sms, int* width) {
   long long least = 0;
   for (int w : {256, 192, 128}) {
     const long long tiles = (long long)((a.T + 255) / 256) * ((a.N + w - 1) / w), nkb = (a.K + kStepK - 1) / kStepK;
     const int stage = kInt8 ? (w == 256 ? 660 : w == 192 ? 550 : 530) : (w == 256 ? 340 : w == 192 ? 260 : 200);
-    const long long ns = 8000 + (tiles + sms / 2 - 1) / (sms / 2) * (nkb * stage + 400);
+    const long long ns = 8000 + (tiles + sms / 2 - 1) / (sms / 2) * (nkb * stage + (kInt8 && w == 256 ? 1800 : 400));
     if (least == 0 || ns < least) {
       *width = w;
       least = ns;
