@@ -324,7 +324,7 @@ typedef enum {
  * over codes (mla_linear_fp8, mla_linear_int8).
  *   h = bf16( x + residual )                                  (h = x if residual is NULL)
  *   y = bf16( h / sqrt(mean(h^2) + epsilon) * gamma )          (y = h if gamma is NULL)
- * y is rounded once, from within a few double-precision units of its value; codes are those of y.
+ * y is rounded once, from within 2^-40 of its value; codes are those of y.
  *   x              bf16 [rows, x_stride], the first `width` of each row are used; x_stride in
  *                  elements, >= width, a multiple of 8
  *   residual       bf16 [rows, width] or NULL; residual_out bf16 [rows, width] receives h, NULL
@@ -342,16 +342,16 @@ int mla_rmsnorm_quant(int32_t code_format, int32_t rows, int32_t width, const vo
  * projections around the attention (down to the latents, queries up, output), on what
  * mla_rmsnorm_quant writes.
  *   out[t, n] = bf16( (sum_k x[t, k] * w[n, k]) * x_scales[t] * w_scales[n] )
- * in fp32 (sums of fp32 in the tensor core's order; products of codes are exact), rounded once to
- * bf16.  A NaN code or scale makes NaN of the results that it enters.
+ * in fp32 (products of codes are exact, their sum is fp32 in the tensor core's order, or exact for
+ * up to eight int8 tokens), rounded once to bf16.  A NaN code or scale makes NaN of the results that it enters.
  *   x_codes        [tokens, k], x_scales float [tokens]
  *   w_codes        [n, k], w_scales float [n]
  *   out            bf16, row t at out + t * out_stride; out_stride in elements, >= n
  *   flags, workspace   as mla_branch_prologue (a wait that runs out is recorded there)
  * The codes are e4m3 (OCP E4M3FN) for _fp8 and int8 for _int8.  k is a multiple of 16, n and
- * out_stride of 8, tokens at most 2^22, n at most 2^24; x_codes, w_codes, w_scales and out are 16-byte aligned.  The result of a token
- * does not depend on the timing of the call; it may differ in rounding between calls of different
- * numbers of tokens (K is split where there are few). */
+ * out_stride of 8, tokens at most 2^22, n at most 2^24; x_codes, w_codes, w_scales and out are
+ * 16-byte aligned.  The result of a token does not depend on the timing of the call; it may differ in
+ * rounding between calls of different numbers of tokens (K is split where there are few). */
 int mla_linear_fp8(int32_t tokens, int32_t n, int32_t k, const void* x_codes, const float* x_scales,
                    const void* w_codes, const float* w_scales, void* out, int64_t out_stride, uint32_t flags,
                    void* workspace, size_t workspace_bytes, void* stream);
@@ -449,7 +449,8 @@ int mla_indexer_fp8(int32_t num_heads, int32_t head_dim, int32_t page_size, int3
 /* The writer of the indexer's inputs.  Token t of request b at pos = cache_lens[b] - qlen + i
  * brings its index key k (D values) and, if q is given, its index queries (H heads of D):
  *   k = bf16( (k - mean) / sqrt(var + epsilon) * k_norm_gamma + k_norm_beta )
- *       (LayerNorm over D, var = mean((k - mean)^2); left out if k_norm_gamma is NULL)
+ *       (LayerNorm over D, var = mean((k - mean)^2), rounded once from within 2^-40 of the larger
+ *       of the two terms; left out if k_norm_gamma is NULL)
  *   the last rope_dim values of k and of every head of q turned by freqs_cis[pos] as in
  *       mla_branch_prologue, rounded once to bf16 (left out if freqs_cis is NULL)
  *   e4m3 codes of each row, scale = the least 2^e with max <= 448 * 2^e (1 for zeros; a row that

@@ -10,6 +10,8 @@
 // paid once a warp and not once a row; then the rows are copied, 16 bytes of output (8 values) a lane.
 // bf16 and e4m3 rows are loaded two at a time by the lanes that write them; e2m1 rows, of which a lane's 8
 // values are 4 bytes and a scale, whole, 16 bytes a lane, four at a time, through shared memory.  Bound by HBM.
+// 199,000 e4m3 rows 61.5 us (5.8 TB/s, 85 % of the copy rate), 278,000 bf16 rows 71.5 us (94 %), as many e2m1
+// rows 54 us (83 %; loaded 4 bytes a lane 70); 4,000 e2m1 rows 3.8 us.
 #include "mla_kernels.cuh"
 #include "mla_rows.cuh"
 
@@ -229,7 +231,7 @@ cudaError_t launch_cache_read(const mla_dims_t& d, int fmt, const uint32_t* offs
   a.block_table = block_table;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.hdr = hdr;
-  // rows of a warp: eight where that leaves every SM some 16 warps, else fewer
+  // rows of a warp: eight where that leaves every SM some 16 warps, else fewer (4,000 e2m1 rows: two 3.8 us, eight 6.9)
   a.per_warp = T >= 8 * 16 * 152 ? 8 : T >= 4 * 16 * 152 ? 4 : 2;   // at most 32, a lane a row
   const unsigned blocks = (unsigned)(((long long)T + rd::kWarps * a.per_warp - 1) / (rd::kWarps * a.per_warp));
   if (fmt == MLA_CACHE_BF16) rd::read_kernel<MLA_CACHE_BF16><<<blocks, 32 * rd::kWarps, 0, s>>>(a);

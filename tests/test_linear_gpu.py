@@ -210,3 +210,14 @@ def test_refuses_outputs_off_the_boundary(dev):
         call("int8", x, xs, w, ws, out=wide[:19, :64])
     with pytest.raises(ValueError):
         call("int8", x, xs, w.T.contiguous()[:, :20], ws, out=None)
+
+
+def test_callers_workspace_and_raw_codes(dev):
+    """A status word of the caller's, which a clean call leaves clean, and e4m3 codes as bytes."""
+    x, xs = codes("fp8", 1, 20, 64, dev)
+    w, ws = codes("fp8", 2, 64, 64, dev)
+    word = torch.full((256,), 0x5A, dtype=torch.uint8, device=dev)
+    a = call("fp8", x.view(torch.uint8), xs, w.view(torch.uint8), ws, workspace=word)
+    assert (word == 0x5A).all()
+    b = call("fp8", x, xs, w, ws, workspace=word, debug=True)
+    assert (word == 0).all() and torch.equal(a, b)
