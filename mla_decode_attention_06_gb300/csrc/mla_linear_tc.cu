@@ -13,12 +13,13 @@
 // splits K: each leaves its fp32 partial in its shared memory and sums a share of the tokens over the
 // cluster, in rank order (the result does not depend on timing).  Times of a call among others, inputs out
 // of L2: 64 x 24,576 x 1,536 e4m3 10.9 us (6.0 at the copy rate; launch, first bytes and end of a
-// block take 5), 1 x 2,112 x 8,192 e4m3 8.0 us, 16 tokens of int8 14.3 us (widening).
+// block take 5), 16 x 2,112 x 8,192 e4m3 8.1 us, int8 14.3 us (widening).
 //
-// Up to eight int8 tokens (dot kernel).  Widening costs the split kernel more than the weights' way from
-// memory does, so here warps take the dot products of codes on the integer units (four products a
-// lane and instruction, exact), straight from registers; K is split over a block's warps where rows are
-// few.  1 x 2,112 x 8,192 5.0 us (2.5 at the copy rate), 1 x 8,192 x 16,384 25 us (20).
+// One token, and up to eight of int8 (dot kernel).  Widening costs the split kernel more than the weights' way
+// from memory does, and tensor memory, clusters and copies take time to begin and end, so here warps take
+// the dot products straight from registers, of int8 on the integer units (four products a lane and
+// instruction, exact), of e4m3 in fp32; K is split over a block's warps where rows are few.  1 x 2,112 x
+// 8,192 int8 4.7, e4m3 5.8 us (2.5 at the copy rate), 1 x 8,192 x 16,384 25 us (20).
 //
 // Many tokens (pair kernel).  A pair of CTAs a pair of SMs, cta_group::2: 256 tokens (A) by 256, 192 or 128
 // channels (B), each CTA loading half of either operand, one tile after another.  Tiles go group by
@@ -30,6 +31,7 @@
 // power cap, 95 % of twice the measured bf16 rate of either; the tensor pipe is active 98 % of the time.
 // 4,096 x 24,576 x 1,536: e4m3 95 us (80), int8 188 us (161).
 #include <algorithm>
+#include <type_traits>
 
 #include "mla_kernels.cuh"
 #include "sm100_ptx.cuh"
@@ -333,18 +335,54 @@ __global__ void __launch_bounds__(kSplitThreads<kInt8>, 2)
   }
 }
 
-// ------------------------------------------------------------------ up to eight int8 tokens
+// ------------------------------------------------------------------ one to eight tokens
 
 constexpr int kDotWarps = 8;
-constexpr int kDotMaxK = 1 << 16;    // 2^16 products of up to 2^14 each stay within 32 bits
+constexpr int kDotMaxK = 1 << 16;    // int8: 2^16 products of up to 2^14 each stay within 32 bits
+
+// Sixteen products of codes added to s: int8 exactly, four an instruction; e4m3 in fp32, each product exact.
+__device__ __forceinline__ void dot16(uint4 w, uint4 x, int& s) {
+  s = __dp4a((int)w.x, (int)x.x, s);
+  s = __dp4a((int)w.y, (int)x.y, s);
+  s = __dp4a((int)w.z, (int)x.z, s);
+  s = __dp4a((int)w.w, (int)x.w, s);
+}
+struct E4m3x16 {
+  float2 v[8];
+};
+__device__ __forceinline__ E4m3x16 e4m3x16(uint4 c) {
+  const uint32_t u[4] = {c.x, c.y, c.z, c.w};
+  E4m3x16 r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    r.v[i] = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u[i / 2] >> (16 * (i & 1))), __NV_E4M3)));
+  return r;
+}
+// The sums of the codes' even and odd places, side by side.
+__device__ __forceinline__ void dot16(const E4m3x16& w, const E4m3x16& x, float2& s) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    s.x = fmaf(w.v[i].x, x.v[i].x, s.x);
+    s.y = fmaf(w.v[i].y, x.v[i].y, s.y);
+  }
+}
+__device__ __forceinline__ int warp_sum(int s) { return __reduce_add_sync(0xffffffffu, s); }
+__device__ __forceinline__ float warp_sum(float2 v) {
+  float s = v.x + v.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
 
 // TT: tokens, R: rows of weights (channels) of a warp.  `along` of a block's warps (a power of two) share the
 // rows and split K.
-template <int TT, int R>
-__global__ void __launch_bounds__(32 * kDotWarps) dot_kernel(const int8_t* __restrict__ x, const int8_t* __restrict__ w,
+template <bool kInt8, int TT, int R>
+__global__ void __launch_bounds__(32 * kDotWarps) dot_kernel(const uint8_t* __restrict__ x, const uint8_t* __restrict__ w,
                                                              const Args a, int along) {
+  using Sum = std::conditional_t<kInt8, int, float>;
+  using Acc = std::conditional_t<kInt8, int, float2>;
   constexpr int kAhead = R * TT >= 16 ? 1 : 8 / (R + TT) > 1 ? 8 / (R + TT) : 2;   // steps whose loads are out together
-  __shared__ int part[kDotWarps][R * TT];
+  __shared__ Sum part[kDotWarps][R * TT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n0 = ((int)blockIdx.x * (kDotWarps / along) + warp / along) * R;
   const int pieces = a.K / 16, step = 32 * along;
@@ -354,7 +392,7 @@ __global__ void __launch_bounds__(32 * kDotWarps) dot_kernel(const int8_t* __res
   for (int t = 0; t < TT; ++t) xp[t] = reinterpret_cast<const uint4*>(x + (size_t)min(t, a.T - 1) * a.K);
 #pragma unroll
   for (int r = 0; r < R; ++r) wp[r] = reinterpret_cast<const uint4*>(w + (size_t)min(n0 + r, a.N - 1) * a.K);
-  int acc[R * TT] = {};
+  Acc acc[R * TT] = {};
 #pragma unroll 1
   for (int c = (warp & (along - 1)) * 32 + lane; c < pieces; c += kAhead * step) {
     uint4 wv[kAhead][R], xv[kAhead][TT];
@@ -367,22 +405,26 @@ __global__ void __launch_bounds__(32 * kDotWarps) dot_kernel(const int8_t* __res
       for (int t = 0; t < TT; ++t) xv[u][t] = in ? __ldg(xp[t] + c + u * step) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
+    for (int u = 0; u < kAhead; ++u) {
+      if constexpr (kInt8) {
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int t = 0; t < TT; ++t) dot16(wv[u][r], xv[u][t], acc[r * TT + t]);
+      } else {
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-          int s = acc[r * TT + t];
-          s = __dp4a((int)wv[u][r].x, (int)xv[u][t].x, s);
-          s = __dp4a((int)wv[u][r].y, (int)xv[u][t].y, s);
-          s = __dp4a((int)wv[u][r].z, (int)xv[u][t].z, s);
-          acc[r * TT + t] = __dp4a((int)wv[u][r].w, (int)xv[u][t].w, s);
+          const E4m3x16 xf = e4m3x16(xv[u][t]);
+#pragma unroll
+          for (int r = 0; r < R; ++r) dot16(e4m3x16(wv[u][r]), xf, acc[r * TT + t]);
         }
+      }
+    }
   }
-  int mine = 0;
+  Sum mine = 0;
 #pragma unroll
   for (int i = 0; i < R * TT; ++i) {
-    const int s = __reduce_add_sync(0xffffffffu, acc[i]);
+    const Sum s = warp_sum(acc[i]);
     if (lane == i) mine = s;
   }
   if (along > 1) {
@@ -750,14 +792,14 @@ cudaError_t launch_split(Args a, const void* x, const void* w, int sms, cudaStre
   return e;
 }
 
-template <int TT, int R>
+template <bool kInt8, int TT, int R>
 cudaError_t launch_dot(const Args& a, const void* x, const void* w, int sms, cudaStream_t s) {
   const long long groups = (a.N + R - 1) / R;
   int along = 1;   // some 24 warps an SM, each with two steps along K and more
   while (along < kDotWarps && groups * along < 24ll * sms && a.K >= 2048 * along) along *= 2;
   const int per = kDotWarps / along;
-  dot_kernel<TT, R><<<(unsigned)((groups + per - 1) / per), 32 * kDotWarps, 0, s>>>(
-      static_cast<const int8_t*>(x), static_cast<const int8_t*>(w), a, along);
+  dot_kernel<kInt8, TT, R><<<(unsigned)((groups + per - 1) / per), 32 * kDotWarps, 0, s>>>(
+      static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(w), a, along);
   return cudaGetLastError();
 }
 
@@ -797,10 +839,15 @@ long long pair_ns(const Args& a, int sms, int* width) {
 
 template <bool kInt8>
 cudaError_t launch(const Args& a, const void* x, const void* w, int sms, cudaStream_t s) {
-  if (kInt8 && a.T <= 8 && a.K <= kDotMaxK) {
-    if (a.T == 1) return launch_dot<1, 2>(a, x, w, sms, s);
-    if (a.T == 2) return launch_dot<2, 2>(a, x, w, sms, s);
-    return a.T <= 4 ? launch_dot<4, 4>(a, x, w, sms, s) : launch_dot<8, 4>(a, x, w, sms, s);
+  // 2,112 x 8,192 and 24,576 x 1,536, dot kernel against split kernel: one token int8 4.7 and 8.2 us against 14 and
+  // 18, e4m3 5.8 and 11 against 7.5 and 10.4 (576 x 2,048: 2.9 against 5.1); eight of int8 8.6 and 12 against 14 and
+  // 20; two of e4m3 7.6 and 15 against 7.9 and 10.5.
+  if (a.T == 1 && a.K <= kDotMaxK) return launch_dot<kInt8, 1, 4>(a, x, w, sms, s);
+  if constexpr (kInt8) {
+    if (a.T <= 8 && a.K <= kDotMaxK) {
+      if (a.T == 2) return launch_dot<true, 2, 2>(a, x, w, sms, s);
+      return a.T <= 4 ? launch_dot<true, 4, 4>(a, x, w, sms, s) : launch_dot<true, 8, 4>(a, x, w, sms, s);
+    }
   }
   // The estimates follow what was measured within a fifth where the two kernels are close: 128 tokens, 8,192 x
   // 16,384, pair 70 us and split 61 (int8), 33 and 30; 24,576 x 1,536, 20.5 and 34.5, 13.2 and 14.1;

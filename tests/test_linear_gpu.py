@@ -3,8 +3,11 @@
 Tolerance.  Products of codes are exact in fp32.  An instruction adds the products of 16 (int8, widened
 to f16) or 32 (e4m3) values of K to a running sum; its result is at worst a step of 2^-22 of the
 largest magnitude it meets, at most A = sum |x w|, off (fp32's 2^-23 with a bit for truncated
-alignment), so the sum is within K / 16 * 2^-22 * A.  The two products with the scales are rounded in
-fp32 (2^-23 in all) and the result to bf16, half a step, 2^-8."""
+alignment), so the sum is within K / 16 * 2^-22 * A.  One token of e4m3 codes is summed in plain fp32: a
+lane's two sums take at most 8 products for each 512 of K, then one addition, five joins of lanes and up to
+seven of warps, each within 2^-24 * A: (K / 64 + 8 + 13) * 2^-24 * A, less than the above and 2^-19 * A.
+(Up to eight tokens of int8 codes are exact.)  The two products with the scales are rounded in fp32
+(2^-23 in all) and the result to bf16, half a step, 2^-8."""
 import numpy as np
 import pytest
 import torch
@@ -44,7 +47,7 @@ def call(kind, *args, **kw):
 def check(out, x, xs, w, ws):
     x, w, xs, ws = x.double(), w.double(), xs.double()[:, None], ws.double()
     ref = (x @ w.T) * xs * ws
-    room = (x.abs() @ w.abs().T) * xs * ws * (-(-x.shape[1] // 16) * 2.0 ** -22)
+    room = (x.abs() @ w.abs().T) * xs * ws * (-(-x.shape[1] // 16) * 2.0 ** -22 + 2.0 ** -19)
     err = (out.double() - ref).abs()
     assert torch.isfinite(out).all()
     over = err - (ref.abs() * (2.0 ** -8 + 2.0 ** -22) + room)
@@ -105,7 +108,7 @@ def test_int8_ends(dev, T):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("T,N,K", [(5, 264, 512), (64, 576, 4096), (300, 520, 272)])
+@pytest.mark.parametrize("T,N,K", [(1, 264, 512), (5, 264, 512), (64, 576, 4096), (300, 520, 272)])
 def test_nan_stays_in_its_row_or_channel(dev, kind, T, N, K):
     x, xs = codes(kind, 1, T, K, dev)
     w, ws = codes(kind, 2, N, K, dev)
@@ -166,7 +169,7 @@ def test_no_tokens(dev):
     assert call("int8", x, torch.empty(0, device=dev), w, ws).shape == (0, 64)
 
 
-@pytest.mark.parametrize("kind,T", [("int8", 1), ("int8", 9), ("int8", 300), ("fp8", 2), ("fp8", 300)])
+@pytest.mark.parametrize("kind,T", [("int8", 1), ("int8", 9), ("int8", 300), ("fp8", 1), ("fp8", 2), ("fp8", 300)])
 def test_offsets_past_32_bits(dev, kind, T):
     """Weights of more than 2^32 codes, outputs far behind each other: the last channels and tokens."""
     N, K = 262144 + 264, 16384
