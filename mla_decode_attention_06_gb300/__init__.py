@@ -22,6 +22,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional
 
@@ -212,11 +213,15 @@ def _unread_status(device, stream):
     return t
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
 def _handle(stream, device):
     """The cudaStream_t that a call runs on, without a Stream object for the current one (3 us of a call)."""
-    if device.type != "cuda":
+    if device.index is None:
         raise ValueError(f"tensors must be CUDA tensors, not on {device}")
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    return _raw_stream(device.index) if stream is None else stream.cuda_stream
 
 
 def _status_word(workspace, debug, device, stream, handle):
@@ -256,7 +261,7 @@ def _call(name, device, *args):
     fn = _fns.get(name)
     if fn is None:
         fn = _fns[name] = getattr(_lib.load(), name)
-    if device.index is None or torch._C._cuda_getDevice() == device.index:
+    if device.index is None or _current_device() == device.index:
         rc = fn(*args)
     else:
         with torch.cuda.device(device):
@@ -269,9 +274,9 @@ def _tables(input_row_offsets, block_table, cache_lens, dev):
     B = input_row_offsets.numel() - 1
     if B < 1 or block_table.dim() != 2 or block_table.shape[0] < B or cache_lens.numel() < B:
         raise ValueError("input_row_offsets, block_table and cache_lens disagree on the number of requests")
-    if dev.type != "cuda":
-        raise ValueError(f"tensors must be CUDA tensors, not on {dev}")
     i = dev.index
+    if i is None:
+        raise ValueError(f"tensors must be CUDA tensors, not on {dev}")
     return (B, _at(input_row_offsets, "input_row_offsets", _I32, i), _at(block_table, "block_table", _INT32, i),
             block_table.shape[1], _at(cache_lens, "cache_lens", _I32, i))
 
@@ -343,22 +348,34 @@ def mla_cache_append(kv_new, input_row_offsets, kv_pool, block_table, cache_lens
     return kv_pool, q_out
 
 
-def _row_strided(t, name, shape):
+def _row_strided(t, name, width, index):
     """Pointer and row stride of a bf16 CUDA tensor whose rows may lie apart (a slice of a wider one)."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda:
-        raise TypeError(f"{name} must be a bf16 CUDA tensor")
-    if t.dim() != 2 or t.shape[1] != shape:
-        raise ValueError(f"{name} must be [rows, {shape}]")
-    n = t.shape[0]
+    if t.dtype != torch.bfloat16 or t.get_device() != index:
+        raise TypeError(f"{name} must be a bf16 tensor on cuda:{index}")
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width:
+        raise ValueError(f"{name} must be [rows, {width}]")
     by_row, along = t.stride()
-    if n > 0 and along != 1:
+    if along != 1 and shape[0] > 0:
         raise ValueError(f"{name} must have unit stride along a row")
-    return t.data_ptr(), by_row if n > 1 else -(-shape // 8) * 8
+    return t.data_ptr(), by_row if shape[0] > 1 else -(-width // 8) * 8
+
+
+def _out(t, name, dtypes, shape, index):
+    """Pointer of a given output of that shape."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    return _at(t, name, dtypes, index)
 
 
 def _sized(t, name, n):
     if t is not None and t.numel() != n:
         raise ValueError(f"{name} must hold {n} values")
+
+
+@functools.lru_cache(maxsize=64)
+def _cache_dims(L, R, page_size, num_pages):
+    return MlaDims(num_heads=1, qk_nope=0, qk_rope=R, kv_lora_rank=L, v_head=1, page_size=page_size, num_pages=num_pages)
 
 
 def mla_cache_read(input_row_offsets, kv_pool, block_table, cache_lens, *, kv_lora_rank: int, qk_rope: int,
@@ -367,30 +384,28 @@ def mla_cache_read(input_row_offsets, kv_pool, block_table, cache_lens, *, kv_lo
     """Cache rows back as bf16 values: the last input_row_offsets[b+1] - input_row_offsets[b] of request b's
     cache_lens[b] tokens.  total_rows (host) is input_row_offsets' last value; it may be left out where `out`
     bf16 [total_rows, L+R] is given.  Returns out."""
-    dev = kv_pool.device
-    L, R = int(kv_lora_rank), int(qk_rope)
-    dims = MlaDims(num_heads=1, qk_nope=0, qk_rope=R, kv_lora_rank=L, v_head=1, page_size=page_size,
-                   num_pages=_pages(kv_pool, page_size, mla_cache_row_bytes(cache_format, L, R)))
-    _sized(kv_scales, "kv_scales", dims.num_pages * page_size)
+    dev, L, R, page_size = kv_pool.device, int(kv_lora_rank), int(qk_rope), int(page_size)
+    i, handle = dev.index, _handle(stream, dev)
+    num_pages = _pages(kv_pool, page_size, mla_cache_row_bytes(cache_format, L, R))
+    _sized(kv_scales, "kv_scales", num_pages * page_size)
     B, offsets, table, table_stride, lens = _tables(input_row_offsets, block_table, cache_lens, dev)
-    handle = _handle(stream, dev)
     if out is None:
         if total_rows is None:
             raise ValueError("total_rows or out must be given")
         out = _buffer((total_rows, L + R), torch.bfloat16, dev, stream, returned=True)
-    elif out.dim() != 2 or out.shape[1] != L + R or (total_rows is not None and out.shape[0] != total_rows):
-        raise ValueError("out must be [total_rows, L+R]")
+        p_out = out.data_ptr()
+    else:
+        total_rows = out.shape[0] if total_rows is None else total_rows
+        p_out = _out(out, "out", _BF16, (total_rows, L + R), i)
     status, status_bytes, workspace = _status_word(workspace, debug, dev, stream, handle)
-    i = dev.index
-    _call("mla_cache_read", dev, ctypes.byref(dims), int(cache_format), offsets, B, out.shape[0],
-          _bytes_at(kv_pool, "kv_pool", i), _at(kv_scales, "kv_scales", _F32, i), table, table_stride, lens,
-          _at(out, "out", _BF16, i), MLA_FLAG_DEBUG_CHECKS if debug else 0, status, status_bytes, handle)
+    _call("mla_cache_read", dev, ctypes.byref(_cache_dims(L, R, page_size, num_pages)), int(cache_format), offsets, B,
+          total_rows, _bytes_at(kv_pool, "kv_pool", i), _at(kv_scales, "kv_scales", _F32, i), table, table_stride, lens,
+          p_out, MLA_FLAG_DEBUG_CHECKS if debug else 0, status, status_bytes, handle)
     return out
 
 
-_CODES_OUT = {MLA_CODES_BF16: (), MLA_CODES_E4M3: (torch.float8_e4m3fn, torch.uint8),
-              MLA_CODES_INT8: (torch.int8, torch.uint8)}
-_CODES = {MLA_CODES_BF16: torch.bfloat16, MLA_CODES_E4M3: torch.float8_e4m3fn, MLA_CODES_INT8: torch.int8}
+_CODES = {MLA_CODES_BF16: (), MLA_CODES_E4M3: (torch.float8_e4m3fn, torch.uint8),
+          MLA_CODES_INT8: (torch.int8, torch.uint8)}
 
 
 def mla_rmsnorm_quant(x, gamma=None, *, epsilon: float = 1e-6, code_format: int = MLA_CODES_E4M3, residual=None,
@@ -399,58 +414,65 @@ def mla_rmsnorm_quant(x, gamma=None, *, epsilon: float = 1e-6, code_format: int 
     are without it), as e4m3 or int8 codes with one fp32 scale a row.  The sum goes to residual_out (in place if
     it is None); y_out bf16 [T, D] receives the normalised rows.  Returns (codes [T, D], scales [T],
     residual_out or None); for MLA_CODES_BF16 (y_out, None, residual_out or None)."""
-    dev = x.device
+    dev, shape = x.device, tuple(x.shape)
+    i, handle = dev.index, _handle(stream, dev)
+    if len(shape) != 2:
+        raise ValueError("x must be [T, D]")
     if code_format not in _CODES:
         raise ValueError(f"unknown code format {code_format}")
-    if x.dim() != 2:
-        raise ValueError("x must be [T, D]")
-    T, D = x.shape
-    px, stride = _row_strided(x, "x", D)
+    T, D = shape
+    px, stride = _row_strided(x, "x", D, i)
+    p_res = p_res_out = p_gamma = p_y = p_codes = p_scales = None
     if residual is not None:
         residual_out = residual if residual_out is None else residual_out
+        p_res = _out(residual, "residual", _BF16, shape, i)
+        p_res_out = p_res if residual_out is residual else _out(residual_out, "residual_out", _BF16, shape, i)
     elif residual_out is not None:
         raise ValueError("residual_out without residual")
+    if gamma is not None:
+        _sized(gamma, "gamma", D)
+        p_gamma = _at(gamma, "gamma", _BF16, i)
     coded = code_format != MLA_CODES_BF16
-    if coded:
+    if not coded:
+        if codes_out is not None or scales_out is not None:
+            raise ValueError("MLA_CODES_BF16 writes no codes")
+        if y_out is None:
+            y_out = _buffer(shape, torch.bfloat16, dev, stream, returned=True)
+    else:
         if codes_out is None:
-            codes_out = _buffer((T, D), _CODES[code_format], dev, stream, returned=True)
+            codes_out = _buffer(shape, _CODES[code_format][0], dev, stream, returned=True)
+            p_codes = codes_out.data_ptr()
+        else:
+            p_codes = _out(codes_out, "codes_out", _CODES[code_format], shape, i)
         if scales_out is None:
-            scales_out = _buffer((T,), torch.float32, dev, stream, returned=True)
-    elif codes_out is not None or scales_out is not None:
-        raise ValueError("MLA_CODES_BF16 writes no codes")
-    elif y_out is None:
-        y_out = _buffer((T, D), torch.bfloat16, dev, stream, returned=True)
-    for t, name in ((residual, "residual"), (residual_out, "residual_out"), (y_out, "y_out"), (codes_out, "codes_out")):
-        if t is not None and t.shape != x.shape:
-            raise ValueError(f"{name} must be [T, D]")
-    _sized(gamma, "gamma", D)
-    _sized(scales_out, "scales_out", T)
-    handle, i = _handle(stream, dev), dev.index
-    _call("mla_rmsnorm_quant", dev, code_format, T, D, px, stride, _at(residual, "residual", _BF16, i),
-          _at(residual_out, "residual_out", _BF16, i), _at(gamma, "gamma", _BF16, i), epsilon, _at(y_out, "y_out", _BF16, i),
-          _at(codes_out, "codes_out", _CODES_OUT[code_format], i), _at(scales_out, "scales_out", _F32, i), handle)
+            scales_out = _buffer(T, torch.float32, dev, stream, returned=True)
+            p_scales = scales_out.data_ptr()
+        else:
+            _sized(scales_out, "scales_out", T)
+            p_scales = _at(scales_out, "scales_out", _F32, i)
+    if y_out is not None:
+        p_y = _out(y_out, "y_out", _BF16, shape, i)
+    _call("mla_rmsnorm_quant", dev, code_format, T, D, px, stride, p_res, p_res_out, p_gamma, epsilon, p_y, p_codes,
+          p_scales, handle)
     return (codes_out, scales_out, residual_out) if coded else (y_out, None, residual_out)
 
 
 def _linear(name, dtypes, x_codes, x_scales, w_codes, w_scales, out, debug, workspace, stream):
-    dev = x_codes.device
-    x_shape, w_shape = x_codes.shape, w_codes.shape
+    dev, x_shape, w_shape = x_codes.device, x_codes.shape, w_codes.shape
+    i, handle = dev.index, _handle(stream, dev)
     if len(x_shape) != 2 or len(w_shape) != 2 or x_shape[1] != w_shape[1]:
         raise ValueError("x_codes must be [T, K] and w_codes [N, K]")
     T, K = x_shape
     N = w_shape[0]
     _sized(x_scales, "x_scales", T)
     _sized(w_scales, "w_scales", N)
-    handle, i = _handle(stream, dev), dev.index
     if out is None:
         out = _buffer((T, N), torch.bfloat16, dev, stream, returned=True)
         p_out, out_stride = out.data_ptr(), N
     else:
         if out.shape[0] != T:
             raise ValueError(f"out must be [{T}, {N}]")
-        p_out, out_stride = _row_strided(out, "out", N)
-        if out.get_device() != i:
-            raise ValueError(f"out is on {out.device}, expected {dev}")
+        p_out, out_stride = _row_strided(out, "out", N, i)
     status, status_bytes, workspace = _status_word(workspace, debug, dev, stream, handle)
     _call(name, dev, T, N, K, _at(x_codes, "x_codes", dtypes, i), _at(x_scales, "x_scales", _F32, i),
           _at(w_codes, "w_codes", dtypes, i), _at(w_scales, "w_scales", _F32, i), p_out, out_stride,
@@ -461,8 +483,7 @@ def _linear(name, dtypes, x_codes, x_scales, w_codes, w_scales, out, debug, work
 def mla_linear_fp8(x_codes, x_scales, w_codes, w_scales, *, out=None, debug: bool = False, workspace=None, stream=None):
     """Projection over e4m3 codes: x_codes [T, K], w_codes [N, K] (float8_e4m3fn or uint8), x_scales f32 [T],
     w_scales f32 [N].  Returns out bf16 [T, N] (rows may be strided if given)."""
-    return _linear("mla_linear_fp8", _F8, x_codes, x_scales, w_codes, w_scales, out, debug,
-                   workspace, stream)
+    return _linear("mla_linear_fp8", _F8, x_codes, x_scales, w_codes, w_scales, out, debug, workspace, stream)
 
 
 def mla_linear_int8(x_codes, x_scales, w_codes, w_scales, *, out=None, debug: bool = False, workspace=None, stream=None):
@@ -477,11 +498,12 @@ def mla_indexer_append(k_new, input_row_offsets, k_cache, k_scales, block_table,
     (k_norm_gamma, k_norm_beta bf16 [D]) and RoPE of their last R values (freqs_cis bf16 [max_seq_len, R]) into the
     e4m3 cache k_cache (page-major rows of D) with k_scales f32 [rows]; queries q bf16 [T, H, D] turned and coded,
     their scales times q_weight f32 [T, H].  Returns (q_codes e4m3 [T, H, D], q_scales f32 [T, H]) or (None, None)."""
-    dev = k_new.device
-    if k_new.dim() != 2:
+    dev, shape = k_new.device, k_new.shape
+    i, handle = dev.index, _handle(stream, dev)
+    if len(shape) != 2:
         raise ValueError("k_new must be [T, D]")
-    T, D = k_new.shape
-    pk, stride = _row_strided(k_new, "k_new", D)
+    T, D = shape
+    pk, stride = _row_strided(k_new, "k_new", D, i)
     R, max_len = (freqs_cis.shape[1], freqs_cis.shape[0]) if freqs_cis is not None else (0, 0)
     num_pages = _pages(k_cache, page_size, D)
     _sized(k_scales, "k_scales", num_pages * page_size)
@@ -489,7 +511,7 @@ def mla_indexer_append(k_new, input_row_offsets, k_cache, k_scales, block_table,
     _sized(k_norm_beta, "k_norm_beta", D)
     H = 0
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D:
+        if len(q.shape) != 3 or q.shape[0] != T or q.shape[2] != D:
             raise ValueError("q must be [T, H, D]")
         H = q.shape[1]
         if q_codes is None:
@@ -502,9 +524,7 @@ def mla_indexer_append(k_new, input_row_offsets, k_cache, k_scales, block_table,
     elif q_weight is not None or q_codes is not None or q_scales is not None:
         raise ValueError("q_weight, q_codes or q_scales without q")
     B, offsets, table, table_stride, lens = _tables(input_row_offsets, block_table, cache_lens, dev)
-    handle = _handle(stream, dev)
     status, status_bytes, workspace = _status_word(workspace, debug, dev, stream, handle)
-    i = dev.index
     _call("mla_indexer_append", dev, H, D, R, page_size, num_pages, pk, stride, offsets, B, T, _at(q, "q", _BF16, i),
           _at(q_weight, "q_weight", _F32, i), _at(q_codes, "q_codes", _F8, i), _at(q_scales, "q_scales", _F32, i),
           _at(k_cache, "k_cache", _F8, i), _at(k_scales, "k_scales", _F32, i), table, table_stride, lens,
