@@ -343,7 +343,7 @@ int mla_rmsnorm_quant(int32_t code_format, int32_t rows, int32_t width, const vo
  * mla_rmsnorm_quant writes.
  *   out[t, n] = bf16( (sum_k x[t, k] * w[n, k]) * x_scales[t] * w_scales[n] )
  * in fp32 (products of codes are exact, their sum is fp32 in the tensor core's order, or exact for
- * up to eight int8 tokens), rounded once to bf16.  A NaN code or scale makes NaN of the results that it enters.
+ * up to eight int8 tokens of k up to 65536), rounded once to bf16.  A NaN code or scale makes NaN of the results that it enters.
  *   x_codes        [tokens, k], x_scales float [tokens]
  *   w_codes        [n, k], w_scales float [n]
  *   out            bf16, row t at out + t * out_stride; out_stride in elements, >= n

@@ -5,21 +5,28 @@
 // on tcgen05, fp32 accumulators in tensor memory.  e4m3 codes are the operands of kind::f8f6f4 as
 // they lie in memory.  The GB300 has no fast integer tensor path (its int8 rate is a tenth of its
 // f16 rate), so int8 codes are widened to f16 on the SM: every int8 value is an f16 value, every
-// product of two is exact in the fp32 accumulator.  Three kernels, chosen by estimated time:
+// product of two is exact in the fp32 accumulator.  Four kernels, chosen by estimated time:
 //
 // Few tokens (split kernel).  The weights are the A operand (128 output channels a tile), the
 // tokens the B operand (16 to 128), so that one token costs no more than a tile's weights, and the
-// call is bound by reading those once.  Where the tiles are fewer than the SMs, a cluster of CTAs
+// call is bound by reading those once.  int8: the weights are widened into tensor memory, the tokens into
+// shared memory (both there cost a sixth more).  Where the tiles are fewer than the SMs, a cluster of CTAs
 // splits K: each leaves its fp32 partial in its shared memory and sums a share of the tokens over the
 // cluster, in rank order (the result does not depend on timing).  Times of a call among others, inputs out
-// of L2: 64 x 24,576 x 1,536 e4m3 10.9 us (6.0 at the copy rate; launch, first bytes and end of a
-// block take 5), 16 x 2,112 x 8,192 e4m3 8.1 us, int8 14.3 us (widening).
+// of L2: 64 x 24,576 x 1,536 e4m3 10.8 us (6.0 at the copy rate; launch, first bytes and end of a
+// block take 5), int8 16.6 (a stage waits for its widening: 400 ns of two blocks side by side, e4m3 200), 16 x
+// 2,112 x 8,192 e4m3 8.4 us.
 //
-// One token, and up to eight of int8 (dot kernel).  Widening costs the split kernel more than the weights' way
-// from memory does, and tensor memory, clusters and copies take time to begin and end, so here warps take
-// the dot products straight from registers, of int8 on the integer units (four products a lane and
-// instruction, exact), of e4m3 in fp32; K is split over a block's warps where rows are few.  1 x 2,112 x
-// 8,192 int8 4.7, e4m3 5.8 us (2.5 at the copy rate), 1 x 8,192 x 16,384 25 us (20).
+// Up to 32 tokens of int8 (mma kernel).  Widening costs the split kernel more than the weights' way from memory
+// does, and tensor memory, clusters and copies take time to begin and end, so here warps take the codes from memory
+// into registers and multiply there, with the warp-wide instruction: nothing is handed on but the sums at the end.
+// Up to eight tokens the codes themselves, summed in integers (exact); more than that would wait for that
+// slow path (32 x 8,192 x 16,384 75 us, widened 52), so they are widened in registers.  8 and 16 x 2,112 x 8,192
+// 7.2 and 8.0 us (split kernel 12.6, 12.7), 8 and 16 x 24,576 x 1,536 10.3 and 12.3 (15.9, 16.2).
+//
+// One token, and two of int8 (dot kernel).  Dot products straight from registers, of int8 on the integer units
+// (four products a lane and instruction, exact), of e4m3 in fp32; K is split over a block's warps where rows
+// are few.  1 x 2,112 x 8,192 int8 4.7, e4m3 5.8 us (2.5 at the copy rate), 1 x 8,192 x 16,384 25 us (20).
 //
 // Many tokens (pair kernel).  A pair of CTAs a pair of SMs, cta_group::2: 256 tokens (A) by 256, 192 or 128
 // channels (B), each CTA loading half of either operand, one tile after another.  Tiles go group by
@@ -53,7 +60,10 @@ constexpr int kStepK = 128;            // codes of a stage along K
 constexpr int kRowsW = 128;            // output channels of a tile
 constexpr int kMaxTokens = 128;        // tokens of a split tile (MMA N)
 constexpr int kMaxStages = 12;
+constexpr int kHalfSm = 108 * 1024;    // shared memory for the stages of a block that shares an SM
 constexpr int kConvWarps = 8;          // split kernel, int8: warps that widen codes, four for either half of a stage
+constexpr int kPlaces = 4;             // ... of widened operands (even: the warps of either half wait for places of their own)
+constexpr int kColW = kMaxTokens;      // ... the weights' in tensor memory, 32 columns each, behind the accumulator
 
 struct Maps {
   CUtensorMap w, x, out;
@@ -62,7 +72,7 @@ struct Maps {
 struct Args {
   int T, N, K;
   int TN;                 // tokens of a tile
-  int S, S2;              // stages of the ring the copies fill; int8: of the ring of widened operands (even)
+  int S;                  // stages of the ring the copies fill
   int C;                  // CTAs that split K
   long long out_stride;
   const float* x_scale;
@@ -156,11 +166,11 @@ __global__ void __launch_bounds__(kSplitThreads<kInt8>, 2)
     split_kernel(const __grid_constant__ Maps maps, const Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  const int TN = a.TN, S = a.S, S2 = a.S2;
-  const int stage = (kRowsW + TN) * 128;       // rows of 128 codes, or of 64 widened ones
-  uint8_t* ring2 = kInt8 ? sm : nullptr;       // widened operands, then the codes
-  uint8_t* ring = kInt8 ? sm + S2 * stage : sm;
-  const int ring_bytes = max((S + S2) * stage, TN * kRowsW * 4);
+  const int TN = a.TN, S = a.S;
+  const int stage = (kRowsW + TN) * 128, stage2 = TN * 128;   // rows of 128 codes; of 64 widened ones
+  uint8_t* ring2 = sm;                                          // int8: widened tokens, then the codes
+  uint8_t* ring = kInt8 ? sm + kPlaces * stage2 : sm;
+  const int ring_bytes = max(S * stage + (kInt8 ? kPlaces * stage2 : 0), TN * kRowsW * 4);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + ring_bytes);
   uint64_t* empty = full + kMaxStages;
   uint64_t* full2 = empty + kMaxStages;
@@ -173,7 +183,7 @@ __global__ void __launch_bounds__(kSplitThreads<kInt8>, 2)
   const int n0 = ((int)blockIdx.x / a.C) * kRowsW, t0 = (int)blockIdx.y * TN;
   const int nkb = (a.K + kStepK - 1) / kStepK;
   const int kb0 = (int)((long long)nkb * rank / a.C), kn = (int)((long long)nkb * (rank + 1) / a.C) - kb0;
-  const uint32_t tcols = TN <= 32 ? 32 : TN <= 64 ? 64 : TN <= 128 ? 128 : 256;
+  const uint32_t tcols = kInt8 ? kColW + 32 * kPlaces : TN <= 32 ? 32 : TN <= 64 ? 64 : 128;
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
@@ -181,7 +191,7 @@ __global__ void __launch_bounds__(kSplitThreads<kInt8>, 2)
       mbar_init(&empty[s], kInt8 ? kConvWarps : 1);
     }
     if (kInt8)
-      for (int s = 0; s < S2; ++s) {
+      for (int s = 0; s < kPlaces; ++s) {
         mbar_init(&full2[s], kConvWarps / 2);
         mbar_init(&empty2[s], 1);
       }
@@ -218,7 +228,7 @@ __global__ void __launch_bounds__(kSplitThreads<kInt8>, 2)
   } else if (warp == 1) {
     const uint32_t idesc = idesc_f32(128, TN, 0);   // f16 and e4m3 are both type 0 of their kinds
     const int steps = kInt8 ? 2 * kn : kn;          // int8: half a stage of codes at a time
-    const int stages = kInt8 ? S2 : S;
+    const int stages = kInt8 ? kPlaces : S;
     uint64_t* landed = kInt8 ? full2 : full;
     uint64_t* read = kInt8 ? empty2 : empty;
     const uint64_t d0 = smem_desc(smem_u32(kInt8 ? ring2 : ring), 16, 1024, kLayoutSw128);
@@ -227,10 +237,10 @@ __global__ void __launch_bounds__(kSplitThreads<kInt8>, 2)
       if (!spin_bar(&landed[at.s], at.round, a.hdr)) break;
       tc_fence_after();
       if (elect_one()) {
-        const uint64_t wd = d0 + (uint64_t)(at.s * (stage >> 4)), xd = wd + (kRowsW * 128 >> 4);
+        const uint64_t wd = d0 + (uint64_t)(at.s * ((kInt8 ? stage2 : stage) >> 4)), xd = kInt8 ? wd : wd + (kRowsW * 128 >> 4);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {   // 32 bytes of K at a time
-          if (kInt8) mma_ss(tmem, wd + 2 * kk, xd + 2 * kk, idesc, (i | kk) != 0);
+          if (kInt8) mma_ts(tmem, tmem + kColW + 32 * at.s + 8 * kk, xd + 2 * kk, idesc, (i | kk) != 0);
           else mma_ss_f8(tmem, wd + 2 * kk, xd + 2 * kk, idesc, (i | kk) != 0);
         }
         mma_commit(&read[at.s]);
@@ -240,36 +250,45 @@ __global__ void __launch_bounds__(kSplitThreads<kInt8>, 2)
     if (elect_one()) mma_commit(done);
     __syncwarp();
   } else if (kInt8 && warp >= 4) {
-    constexpr int kAhead = 4;   // rows of a lane whose codes are loaded together
-    const int rows = kRowsW + TN;
-    const int h = (warp - 4) >> 2, q = warp & 3;   // its half of every stage, its piece of every row
+    // its half of every stage; its row of the weights (= TMEM lane), its piece of every token
+    const int h = (warp - 4) >> 2, q = warp & 3, row = 32 * q + lane;
     Ring from, to;
-    if (h) to.next(S2);
+    if (h) to.next(kPlaces);
     for (int i = h; i < 2 * kn; i += 2, from.next(S)) {
       bool ok = wait_bar(&full[from.s], from.round, a.hdr);
-      if (ok && i >= S2) ok = wait_bar(&empty2[to.s], to.round ^ 1, a.hdr);
+      if (ok && i >= kPlaces) ok = wait_bar(&empty2[to.s], to.round ^ 1, a.hdr);
       if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
       const uint8_t* raw = ring + from.s * stage;
-      uint8_t* dst = ring2 + to.s * stage;
-#pragma unroll 1
-      for (int r0 = lane; r0 < rows; r0 += 32 * kAhead) {
-        uint4 v[kAhead];
+      uint4 v[4], x[4];
+      uint32_t o[32];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-          if (r0 + 32 * j < rows) v[j] = codes_at(raw, r0 + 32 * j, h, q);
+      for (int j = 0; j < 4; ++j) v[j] = codes_at(raw, row, h, j);
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-          if (r0 + 32 * j < rows) store_widened(v[j], dst, r0 + 32 * j, q);
+      for (int j = 0; j < 4; ++j)
+        if (32 * j + lane < TN) x[j] = codes_at(raw + kRowsW * 128, 32 * j + lane, h, q);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint4 lo, hi;
+        widen(v[j], lo, hi);
+        o[8 * j] = lo.x; o[8 * j + 1] = lo.y; o[8 * j + 2] = lo.z; o[8 * j + 3] = lo.w;
+        o[8 * j + 4] = hi.x; o[8 * j + 5] = hi.y; o[8 * j + 6] = hi.z; o[8 * j + 7] = hi.w;
       }
+      tmem_st32(tmem + kColW + 32 * to.s + ((uint32_t)(32 * q) << 16), o);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (32 * j + lane < TN) store_widened(x[j], ring2 + to.s * stage2, 32 * j + lane, q);
       fence_proxy_async_smem();
+      tmem_st_wait();
+      tc_fence_before();
       __syncwarp();
       if (elect_one()) {
         mbar_arrive(&empty[from.s]);
         mbar_arrive(&full2[to.s]);
       }
       __syncwarp();
-      to.next(S2);
-      to.next(S2);
+      to.next(kPlaces);
+      to.next(kPlaces);
     }
   }
   __syncwarp();
@@ -335,7 +354,7 @@ __global__ void __launch_bounds__(kSplitThreads<kInt8>, 2)
   }
 }
 
-// ------------------------------------------------------------------ one to eight tokens
+// ------------------------------------------------------------------ one token, or two
 
 constexpr int kDotWarps = 8;
 constexpr int kDotMaxK = 1 << 16;    // int8: 2^16 products of up to 2^14 each stay within 32 bits
@@ -437,6 +456,111 @@ __global__ void __launch_bounds__(32 * kDotWarps) dot_kernel(const uint8_t* __re
   const int n = n0 + lane / TT, t = lane % TT;
   if (lane < R * TT && n < a.N && t < a.T)
     a.out[t * a.out_stride + n] = __float2bfloat16_rn((float)mine * a.x_scale[t] * a.w_scale[n]);
+}
+
+// ------------------------------------------------------------------ a few tokens of int8
+
+constexpr int kMmaWarps = 16;   // at most, of a block
+
+__device__ __forceinline__ void mma_warp(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_warp(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// A lane's 16 codes of a row as operand registers: the codes, or their f16 values.
+template <bool kExact>
+struct Operand {
+  uint32_t v[kExact ? 4 : 8];
+  __device__ __forceinline__ explicit Operand(uint4 c) {
+    uint4 lo = c, hi;
+    if constexpr (!kExact) {
+      widen(c, lo, hi);
+      v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+    }
+    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+  }
+};
+
+// NT * 8 tokens a block, 16 channels a warp, U steps of 64 codes along K whose loads are out together.  `along` of
+// a block's warps (a power of two) share the channels and split K.  The lanes of a row take 16 neighbouring
+// codes each: which of them an instruction takes for its place along K is free, as long as it is the same ones
+// of the weights and of the tokens.
+template <bool kExact, int NT, int U>
+__global__ void __launch_bounds__(32 * kMmaWarps) mma_kernel(const uint8_t* __restrict__ x, const uint8_t* __restrict__ w,
+                                                             const Args a, int along) {
+  using Sum = std::conditional_t<kExact, int, float>;
+  constexpr int kPitch = 20;   // 16 channels; the lanes' stores meet each bank once
+  extern __shared__ uint8_t smem_raw[];
+  Sum* part = reinterpret_cast<Sum*>(smem_raw);   // [warp][token][kPitch]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int per = ((int)blockDim.x >> 5) / along;
+  const int n0 = ((int)blockIdx.x * per + warp / along) * 16;
+  const uint8_t* wp[2];
+  const uint8_t* xp[NT];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) wp[r] = w + (size_t)min(n0 + 8 * r + g, a.N - 1) * a.K + 16 * c;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) xp[t] = x + (size_t)min(8 * t + g, a.T - 1) * a.K + 16 * c;
+  Sum acc[NT][4] = {};
+#pragma unroll 1
+  for (int k = (warp & (along - 1)) * 64 * U; k < a.K; k += 64 * U * along) {
+    uint4 wv[U][2], xv[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool in = k + 64 * u + 16 * c < a.K;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        wv[u][r] = in ? __ldcs(reinterpret_cast<const uint4*>(wp[r] + k + 64 * u)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        xv[u][t] = in ? __ldg(reinterpret_cast<const uint4*>(xp[t] + k + 64 * u)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const Operand<kExact> w0(wv[u][0]), w1(wv[u][1]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const Operand<kExact> xo(xv[u][t]);
+#pragma unroll
+        for (int j = 0; j < (kExact ? 4 : 8); j += 2)
+          mma_warp(acc[t], w0.v[j], w1.v[j], w0.v[j + 1], w1.v[j + 1], xo.v[j], xo.v[j + 1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      part[(warp * NT * 8 + 8 * t + 2 * c + (i & 1)) * kPitch + 8 * (i >> 1) + g] = acc[t][i];
+  __syncthreads();
+  // eight channels of a token a thread, the warps' sums in their order
+  for (int i = threadIdx.x; i < per * NT * 16; i += blockDim.x) {
+    const int half = i & 1, group = (i >> 1) % per, t = (i >> 1) / per;
+    const int n = ((int)blockIdx.x * per + group) * 16 + 8 * half;
+    if (t >= a.T || n >= a.N) continue;
+    Sum s[8] = {};
+    for (int j = 0; j < along; ++j) {
+      const Sum* p = part + ((group * along + j) * NT * 8 + t) * kPitch + 8 * half;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s[q] += p[q];
+    }
+    const float xs = a.x_scale[t];
+    uint32_t o[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float2 ws = *reinterpret_cast<const float2*>(a.w_scale + n + 2 * q);
+      const __nv_bfloat162 v = __floats2bfloat162_rn((float)s[2 * q] * xs * ws.x, (float)s[2 * q + 1] * xs * ws.y);
+      o[q] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    *reinterpret_cast<uint4*>(a.out + t * a.out_stride + n) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
 }
 
 // ------------------------------------------------------------------ many tokens
@@ -746,35 +870,46 @@ bool encode_out(CUtensorMap* m, void* p, int T, int N, long long stride) {
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How the split kernel cuts a call, and what that takes, in ns: as above, a stage of e4m3 200 ns and half a
-// one a token of the tile, of int8 580 and 2.2, 1.7 us a round of blocks and 3.5.
+// How the split kernel cuts a call, and what that takes, in ns: 3.5 us, and for each block of an SM 1.7 and its
+// stages (e4m3 200 ns and half a one a token of the tile, int8 540 and 1.5; of two int8 blocks side by side 1.3 us,
+// 400 ns and one a token).
 template <bool kInt8>
 long long split_ns(Args* a, int sms) {
   const int ttiles = (a->T + kMaxTokens - 1) / kMaxTokens;   // as even as they come, in 16s
   a->TN = ((a->T + ttiles - 1) / ttiles + 15) / 16 * 16;
   const long long tiles = (long long)((a->N + kRowsW - 1) / kRowsW) * ((a->T + a->TN - 1) / a->TN);
   const int nkb = (a->K + kStepK - 1) / kStepK;
+  const int stage = (kRowsW + a->TN) * 128, places = kInt8 ? kPlaces * a->TN * 128 : 0;
+  const bool pairable = places + 2 * stage <= kHalfSm;   // two blocks fit an SM
+  // K is split while there are SMs for the blocks and two stages left for each (16 x 576 x 2,048, eight blocks and
+  // two: int8 5.7 us and 6.9, e4m3 4.8 and 5.4).  int8 blocks wait for their own widening, so two an SM are taken
+  // where either keeps 16 stages: 16 x 8,192 x 16,384 32.8 us against 40.5, but 64 x 7,168 x 2,048 (4 stages) 12.6
+  // against 11.5.  Of clusters whose blocks fill an SM each the device holds 16 of eight and some 36 of four.
+  const auto fits = [&](int C) {
+    if (tiles * C > sms) return kInt8 && pairable && tiles * C <= 2 * sms && nkb >= 16 * C;
+    return nkb >= 2 * C && (pairable || C < 4 || tiles * C <= 128);
+  };
   a->C = 1;
-  while (a->C < 8 && tiles * a->C * 2 <= sms && nkb >= 8 * a->C) a->C *= 2;
-  const int stage = kInt8 ? 580 + a->TN * 22 / 10 : 200 + a->TN / 2;
-  return 3500 + (tiles * a->C + sms - 1) / sms * (1700 + (nkb + a->C - 1ll) / a->C * stage);
+  while (a->C < 8 && fits(2 * a->C)) a->C *= 2;
+  const long long blocks = tiles * a->C, stages = (nkb + a->C - 1) / a->C;
+  // blocks an SM (clusters of eight do not fill all SMs: 136 blocks of 17 share some)
+  const long long rounds = a->C == 8 && blocks > 128 ? 2 : (blocks + sms - 1) / sms;
+  const bool two = pairable && (rounds > 1 || a->C > 2);
+  a->S = std::min({kMaxStages, ((two ? kHalfSm : 200 * 1024) - places) / stage, nkb});
+  if (!kInt8) return 3500 + rounds * (1700 + stages * (200 + a->TN / 2));
+  return 3500 + rounds * (two && rounds > 1 ? 1300 + stages * (400 + a->TN) : 1700 + stages * (540 + a->TN * 3 / 2));
 }
 
 template <bool kInt8>
-cudaError_t launch_split(Args a, const void* x, const void* w, int sms, cudaStream_t s) {
+cudaError_t launch_split(const Args& a, const void* x, const void* w, cudaStream_t s) {
   Maps maps;
   const int tiles = (a.N + kRowsW - 1) / kRowsW, ttiles = (a.T + a.TN - 1) / a.TN;
-  const int nkb = (a.K + kStepK - 1) / kStepK;
-  // Two blocks share an SM where there are more than SMs, and where clusters are large: of eight blocks that
-  // fill an SM each the device holds 16 (17 tiles of one token took two waves, 19 us).
-  const int stage = (kRowsW + a.TN) * 128, budget = (long long)tiles * ttiles * a.C > sms || a.C > 2 ? 108 * 1024 : 200 * 1024;
-  const int fit = std::max(kInt8 ? 4 : 2, budget / stage);
-  a.S2 = kInt8 ? (fit >= 6 ? 4 : 2) : 0;   // even: the warps of either half wait for places of their own
-  a.S = std::min({kMaxStages, fit - a.S2, nkb});
+  const int stage = (kRowsW + a.TN) * 128, places = kInt8 ? kPlaces * a.TN * 128 : 0;
   if (!encode_codes(&maps.w, w, a.K, a.N, kRowsW) || !encode_codes(&maps.x, x, a.K, a.T, a.TN))
     return cudaErrorInvalidValue;
-  const size_t ring = std::max((size_t)(a.S + a.S2) * stage, (size_t)a.TN * kRowsW * 4);
-  const size_t smem = 1024 + ring + (4 * kMaxStages + 2) * 8;
+  const size_t ring = std::max((size_t)a.S * stage + places, (size_t)a.TN * kRowsW * 4);
+  // int8: more than a third of an SM's, whose tensor memory holds the columns of two blocks
+  const size_t smem = std::max<size_t>(1024 + ring + (4 * kMaxStages + 2) * 8, kInt8 ? 78 * 1024 : 0);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles * a.C, ttiles);
   cfg.blockDim = dim3(kSplitThreads<kInt8>);
@@ -799,6 +934,21 @@ cudaError_t launch_dot(const Args& a, const void* x, const void* w, int sms, cud
   while (along < kDotWarps && groups * along < 24ll * sms && a.K >= 2048 * along) along *= 2;
   const int per = kDotWarps / along;
   dot_kernel<kInt8, TT, R><<<(unsigned)((groups + per - 1) / per), 32 * kDotWarps, 0, s>>>(
+      static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(w), a, along);
+  return cudaGetLastError();
+}
+
+// What the mma kernel takes, in ns: 3.5 us, and for a million codes of weights 230, for more than 16 tokens 380.
+long long mma_ns(const Args& a) { return 3500 + (long long)a.N * a.K / 1000 * (a.T <= 16 ? 230 : 380) / 1000; }
+
+template <bool kExact, int NT>
+cudaError_t launch_mma(const Args& a, const void* x, const void* w, int sms, cudaStream_t s) {
+  constexpr int kU = NT <= 2 ? 4 : 2;   // 24,576 x 1,536: 8 tokens 10.3 us with 4 and 11.2 with 2, 32 26.9 and 17.8
+  const long long groups = (a.N + 15) / 16;
+  int along = 1;   // some 16 warps an SM (24: 8 x 24,576 x 1,536 13.3 us), each with work for its loads
+  while (along < kMmaWarps && groups * along < 16ll * sms && a.K >= 64 * kU * along) along *= 2;
+  const int warps = std::max(8, along), per = warps / along;
+  mma_kernel<kExact, NT, kU><<<(unsigned)((groups + per - 1) / per), 32 * warps, warps * NT * 8 * 20 * 4, s>>>(
       static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(w), a, along);
   return cudaGetLastError();
 }
@@ -839,23 +989,25 @@ long long pair_ns(const Args& a, int sms, int* width) {
 
 template <bool kInt8>
 cudaError_t launch(const Args& a, const void* x, const void* w, int sms, cudaStream_t s) {
-  // 2,112 x 8,192 and 24,576 x 1,536, dot kernel against split kernel: one token int8 4.7 and 8.2 us against 14 and
-  // 18, e4m3 5.8 and 11 against 7.5 and 10.4 (576 x 2,048: 2.9 against 5.1); eight of int8 8.6 and 12 against 14 and
-  // 20; two of e4m3 7.6 and 15 against 7.9 and 10.5.
+  // dot kernel against split kernel: one token, 2,112 x 8,192 and 24,576 x 1,536, int8 4.7 and 8.2 us against 12 and 15,
+  // e4m3 5.8 and 11 against 7.5 and 10.4 (576 x 2,048: 2.9 against 5.1); two of e4m3 7.6 and 15 against 7.9 and 10.5.
   if (a.T == 1 && a.K <= kDotMaxK) return launch_dot<kInt8, 1, 4>(a, x, w, sms, s);
   if constexpr (kInt8) {
-    if (a.T <= 8 && a.K <= kDotMaxK) {
-      if (a.T == 2) return launch_dot<true, 2, 2>(a, x, w, sms, s);
-      return a.T <= 4 ? launch_dot<true, 4, 4>(a, x, w, sms, s) : launch_dot<true, 8, 4>(a, x, w, sms, s);
-    }
+    // mma kernel, eight tokens: 7.3 and 10.3 us (dot products 8.5 and 12, split kernel 12.6 and 15.9)
+    if (a.T == 2 && a.K <= kDotMaxK) return launch_dot<true, 2, 2>(a, x, w, sms, s);
+    if (a.T <= 8 && a.K <= kDotMaxK) return launch_mma<true, 1>(a, x, w, sms, s);
   }
-  // The estimates follow what was measured within a fifth where the two kernels are close: 128 tokens, 8,192 x
-  // 16,384, pair 70 us and split 61 (int8), 33 and 30; 24,576 x 1,536, 20.5 and 34.5, 13.2 and 14.1;
-  // 192 tokens, 8,192 x 16,384, 70 and 83, 33 and 34.
+  // The estimates follow what was measured within a fifth where two kernels are close: 128 tokens, 8,192 x 16,384,
+  // pair 68 us and split 50 (int8), 33 and 30; 64 of 24,576 x 1,536 19.3 and 16.6; 192 of 8,192 x 16,384 68 and 66,
+  // 33 and 34; 32 of 2,112 x 8,192 mma 11 and split 13, of 8,192 x 8,192 28 and 20 (int8).
   int width = 0;
   const long long pair = pair_ns<kInt8>(a, sms, &width);
   Args b = a;
-  if (split_ns<kInt8>(&b, sms) <= pair) return launch_split<kInt8>(b, x, w, sms, s);
+  const long long split = split_ns<kInt8>(&b, sms);
+  if constexpr (kInt8)
+    if (a.T <= 32 && mma_ns(a) < std::min(split, pair))
+      return a.T <= 16 ? launch_mma<false, 2>(a, x, w, sms, s) : launch_mma<false, 4>(a, x, w, sms, s);
+  if (split <= pair) return launch_split<kInt8>(b, x, w, s);
   switch (width) {
     case 256: return launch_pair<kInt8, 256>(a, x, w, sms, s);
     case 192: return launch_pair<kInt8, 192>(a, x, w, sms, s);

@@ -67,7 +67,10 @@ SHAPES = [(1, 8, 16), (1, 4104, 528), (2, 8, 65536), (4, 136, 65552), (5, 64, 20
           (17, 2048, 208), (33, 1000, 1536), (64, 4096, 1536), (100, 576, 7168), (129, 264, 512), (255, 128, 64),
           (256, 1024, 1040), (257, 520, 272), (333, 1096, 4096), (512, 512, 512), (700, 24, 16), (1025, 768, 1536),
           (2000, 2304, 576), (64, 24576, 1536),
-          (4096, 8192, 208), (2560, 10000, 1040)]
+          (4096, 8192, 208), (2560, 10000, 1040),
+          (3, 24, 65536), (7, 1000, 272), (8, 8, 16), (9, 8, 48), (9, 136, 65552), (12, 4104, 1040), (16, 24, 16),
+          (24, 136, 2064), (31, 2112, 528), (32, 7168, 2048), (32, 8, 16), (20, 8192, 16384), (48, 2112, 8192),
+          (100, 4096, 4096), (128, 2112, 8192), (112, 2184, 8208)]
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -79,7 +82,9 @@ def test_shapes(dev, kind, T, N, K):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("K,N,T", [(256, 64, 256), (272, 136, 272), (1024, 256, 1024), (48, 8, 48)])
+@pytest.mark.parametrize("K,N,T", [(256, 64, 256), (272, 136, 272), (1024, 256, 1024), (48, 8, 48),
+                                   (272, 136, 2), (272, 264, 7), (1040, 520, 16), (1040, 1040, 32), (656, 656, 20),
+                                   (2064, 136, 8)])
 def test_each_code_lands_in_its_place(dev, kind, K, N, T):
     """One-hot tokens pick single weights: the result is the weight, exactly (every code is a bf16 value)."""
     w, _ = codes(kind, 3, N, K, dev)
@@ -95,7 +100,7 @@ def test_each_code_lands_in_its_place(dev, kind, K, N, T):
         assert torch.equal(out.double(), x.double()[:, :N])
 
 
-@pytest.mark.parametrize("T", [1, 40, 300])
+@pytest.mark.parametrize("T", [1, 2, 5, 12, 20, 40, 300])
 def test_int8_ends(dev, T):
     """The largest sums: 127 * 127 and (-128) * (-128) along all of K, exact in fp32 where K is a power of two."""
     for v in (127, -128):
@@ -108,7 +113,7 @@ def test_int8_ends(dev, T):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("T,N,K", [(1, 264, 512), (5, 264, 512), (64, 576, 4096), (300, 520, 272)])
+@pytest.mark.parametrize("T,N,K", [(1, 264, 512), (5, 264, 512), (16, 264, 512), (30, 264, 528), (64, 576, 4096), (300, 520, 272)])
 def test_nan_stays_in_its_row_or_channel(dev, kind, T, N, K):
     x, xs = codes(kind, 1, T, K, dev)
     w, ws = codes(kind, 2, N, K, dev)
@@ -133,7 +138,7 @@ def test_nan_stays_in_its_row_or_channel(dev, kind, T, N, K):
 
 @pytest.mark.parametrize("kind", KINDS)
 def test_strided_output_leaves_what_lies_between(dev, kind):
-    for T in (9, 290):
+    for T in (2, 6, 9, 25, 290):
         x, xs = codes(kind, 1, T, 512, dev)
         w, ws = codes(kind, 2, 136, 512, dev)
         wide = torch.full((T, 136 + 24), 7.0, dtype=torch.bfloat16, device=dev)
@@ -145,7 +150,7 @@ def test_strided_output_leaves_what_lies_between(dev, kind):
 @pytest.mark.parametrize("kind", KINDS)
 def test_same_bits_again_and_together(dev, kind):
     """Two streams at once, repeated and captured calls give the same bits."""
-    cases = [codes(kind, 10 + i, T, 1536, dev) for i, T in enumerate((1, 64, 400))]
+    cases = [codes(kind, 10 + i, T, 1536, dev) for i, T in enumerate((1, 2, 7, 13, 30, 64, 400))]
     w, ws = codes(kind, 2, 2112, 1536, dev)
     first = [call(kind, x, xs, w, ws) for x, xs in cases]
     torch.cuda.synchronize()
@@ -169,7 +174,7 @@ def test_no_tokens(dev):
     assert call("int8", x, torch.empty(0, device=dev), w, ws).shape == (0, 64)
 
 
-@pytest.mark.parametrize("kind,T", [("int8", 1), ("int8", 9), ("int8", 300), ("fp8", 1), ("fp8", 2), ("fp8", 300)])
+@pytest.mark.parametrize("kind,T", [("int8", 1), ("int8", 2), ("int8", 5), ("int8", 9), ("int8", 300), ("fp8", 1), ("fp8", 2), ("fp8", 300)])
 def test_offsets_past_32_bits(dev, kind, T):
     """Weights of more than 2^32 codes, outputs far behind each other: the last channels and tokens."""
     N, K = 262144 + 264, 16384
@@ -193,6 +198,12 @@ def test_wide_output_strides(dev):
     out = buf.as_strided((140, 64), (stride, 1))
     call("fp8", x, xs, w, ws, out=out, debug=True)
     check(out, x, xs, w, ws)
+    for T in (7, 14, 30):
+        few, fs = codes("int8", 6, T, 64, dev)
+        w8, w8s = codes("int8", 7, 64, 64, dev)
+        out = buf.as_strided((T, 64), (stride * 4, 1))
+        call("int8", few, fs, w8, w8s, out=out, debug=True)
+        check(out, few, fs, w8, w8s)
     big, bs = codes("fp8", 8, 300, 64, dev)
     buf = torch.empty(299 * (1 << 23) + 64, dtype=torch.bfloat16, device=dev)
     out = buf.as_strided((300, 64), (1 << 23, 1))
