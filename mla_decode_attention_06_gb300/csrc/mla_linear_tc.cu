@@ -26,7 +26,8 @@
 //
 // One token, and two of int8 (dot kernel).  Dot products straight from registers, of int8 on the integer units
 // (four products a lane and instruction, exact), of e4m3 in fp32; K is split over a block's warps where rows
-// are few.  1 x 2,112 x 8,192 int8 4.7, e4m3 5.8 us (2.5 at the copy rate), 1 x 8,192 x 16,384 25 us (20).
+// are few.  1 x 2,112 x 8,192 int8 4.5, e4m3 6.0 us (2.5 at the copy rate), 1 x 8,192 x 16,384
+// 23 and 25.5 us (20).
 //
 // Many tokens (pair kernel).  A pair of CTAs a pair of SMs, cta_group::2: 256 tokens (A) by 256, 192 or 128
 // channels (B), each CTA loading half of either operand, one tile after another.  Tiles go group by
