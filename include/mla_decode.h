@@ -467,10 +467,11 @@ int mla_indexer_fp8(int32_t num_heads, int32_t head_dim, int32_t page_size, int3
  *   freqs_cis      bf16 [max_seq_len, rope_dim] or NULL (rope_dim and max_seq_len then ignored)
  *   k_norm_gamma, k_norm_beta   bf16 [D], both or neither
  *   flags, workspace   as mla_branch_prologue
- * head_dim is a multiple of 8 up to 256, rope_dim a multiple of 8 up to head_dim; k_new, q, q_codes,
- * k_cache, freqs_cis, k_norm_gamma and k_norm_beta are 16-byte aligned.  Padding tokens
- * (t >= input_row_offsets[B]), tokens out of range (position outside the block table or
- * [0, max_seq_len), page id outside [0, num_pages)) and tokens that share a row: as mla_cache_append. */
+ * head_dim is a multiple of 8 up to 256, rope_dim a multiple of 8 up to head_dim, total_q with
+ * queries at most 2^31 - 65; k_new, q, q_codes, k_cache, freqs_cis, k_norm_gamma and k_norm_beta are
+ * 16-byte aligned.  Padding tokens (t >= input_row_offsets[B]), tokens out of range (position
+ * outside the block table or [0, max_seq_len), page id outside [0, num_pages)) and tokens that
+ * share a row: as mla_cache_append. */
 int mla_indexer_append(int32_t num_heads, int32_t head_dim, int32_t rope_dim, int32_t page_size, int32_t num_pages,
                        const void* k_new, int64_t k_new_stride, const uint32_t* input_row_offsets, int32_t batch,
                        int32_t total_q, const void* q, const float* q_weight, void* q_codes, float* q_scales,

@@ -536,6 +536,7 @@ int mla_indexer_append(int32_t num_heads, int32_t head_dim, int32_t rope_dim, in
   if (freqs_cis && (rope_dim < 1 || rope_dim > head_dim || max_seq_len < 1)) return MLA_ERR_INVALID_ARG;
   if (head_dim % 8 != 0 || head_dim > 256 || (freqs_cis && rope_dim % 8 != 0)) return MLA_ERR_UNSUPPORTED;
   if ((int64_t)num_pages * page_size > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if (q && total_q > INT32_MAX - 64) return MLA_ERR_UNSUPPORTED;   // blocks of queries count 32 tokens ahead in 32 bits
   if (indexer_append_blocks(num_heads, head_dim, total_q, q != nullptr) > INT32_MAX) return MLA_ERR_UNSUPPORTED;
   if ((!k_new && total_q > 0) || !input_row_offsets || !k_cache || !k_scales || !block_table || !cache_lens || !workspace)
     return MLA_ERR_INVALID_ARG;

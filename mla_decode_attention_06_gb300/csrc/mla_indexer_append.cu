@@ -15,7 +15,7 @@
 // reads and writes whole rows.  A query row takes D / 16 lanes of two 8-value pieces half a row apart, so
 // that with R = D / 2 all lanes turn one piece of their two together; a block takes the heads of one or
 // several tokens, two rows a lane group with all loads out before the tokens' places are looked up.  Keys (a piece a
-// lane) have blocks of their own.  8,483 prompt tokens of 64 heads: 62 us, 3.5 TB/s, half the copy rate, bound by
+// lane) have blocks of their own.  8,483 prompt tokens of 64 heads: 58 us, 3.75 TB/s, 55 % of the copy rate, bound by
 // the integer pipe (unpacking, rounding to odd, codes) and waits beside it; a step of 64 tokens: 4.5 us, bound by
 // the chain of dependent reads.
 #include "mla_kernels.cuh"
@@ -72,12 +72,11 @@ __device__ __forceinline__ float scale_of(int e) { return e == 255 ? 1.f : pow2(
 __device__ __forceinline__ uint2 coded(uint4 x, int e) {
   if (e == 255) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);   // every code a NaN
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  const float rs = pow2(-e);
+  const uint32_t rs = __float_as_uint(pow2(-e)) >> 16;   // a bf16 value: -e is -127 at least
   uint32_t two[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float2 v;
-    apart(mul2(widen2(w[i]), both(rs, rs)), v.x, v.y);
+    const float2 v = make_float2(bf_mul(w[i], rs), bf_mul(w[i] >> 16, rs));
     two[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
   }
   return make_uint2(two[0] | (two[1] << 16), two[2] | (two[3] << 16));
@@ -234,28 +233,26 @@ __device__ __forceinline__ void queries(const Args& a, int t0, int part, int lan
   const int col[2] = {8 * sub, 8 * (sub + a.q_lanes)};
   uint4 v[kBatch][2];
   float wt[kBatch];
-  int tok[kBatch], head[kBatch];   // token of the step, head (H: none)
+  int tok[kBatch];       // token of the step
+  bool use[kBatch];      // there is a head for it
+  size_t row[kBatch];    // of the queries; advanced from step to step
 #pragma unroll
   for (int j = 0; j < kBatch; ++j) {
     const int slot = group + j * per;
     tok[j] = kSide ? slot / a.slots : 0;
-    head[j] = kSide ? slot & (a.slots - 1) : part * per * kBatch + slot;
-    if (kSide && tok[j] >= a.together) head[j] = a.H;
+    const int head = kSide ? slot & (a.slots - 1) : part * per * kBatch + slot;
+    use[j] = head < a.H && (!kSide || tok[j] < a.together);
+    if (!use[j]) tok[j] = 0;
+    row[j] = (size_t)(t0 + tok[j]) * a.H + head;
   }
-  auto token = [&](int step, int j) { return kSide ? t0 + step * a.together + tok[j] : t0 + step; };
-  auto row_of = [&](int step, int j) { return (size_t)token(step, j) * a.H + head[j]; };
-  auto have = [&](int step, int j) { return head[j] < a.H && token(step, j) < a.T; };
-  auto place = [&](int step, int j) { return places[kSide ? step * a.together + (head[j] < a.H ? tok[j] : 0) : step]; };
-  auto load = [&](int step) {
+  auto load = [&](int first) {
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const bool ok = have(step, j);
-      wt[j] = ok && a.q_weight && sub == 0 ? a.q_weight[row_of(step, j)] : 1.f;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        v[j][k] = make_uint4(0, 0, 0, 0);
-        if (ok && col[k] < a.D) v[j][k] = *reinterpret_cast<const uint4*>(a.q + row_of(step, j) * a.D + col[k]);
-      }
+      const bool ok = use[j] && t0 + first + tok[j] < a.T;
+      wt[j] = ok && a.q_weight && sub == 0 ? a.q_weight[row[j]] : 1.f;
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + row[j] * a.D) + sub;
+      v[j][0] = ok ? src[0] : make_uint4(0, 0, 0, 0);
+      v[j][1] = ok && col[1] < a.D ? src[a.q_lanes] : make_uint4(0, 0, 0, 0);
     }
   };
   load(0);   // on its way while the places are looked up
@@ -269,8 +266,8 @@ __device__ __forceinline__ void queries(const Args& a, int t0, int part, int lan
   }
   __syncthreads();
 #pragma unroll 1
-  for (int step = 0; step < a.steps; ++step) {
-    if (step > 0) load(step);
+  for (int first = 0; first < n; first += a.together) {   // the step's first token, from t0
+    if (first > 0) load(first);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (!in_rope(a, col[k])) continue;
@@ -278,15 +275,16 @@ __device__ __forceinline__ void queries(const Args& a, int t0, int part, int lan
       uint4 f = make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        if ((kSide || j == 0) && place(step, j) >= 0) f = rotations(a, col[k], place(step, j));
+        const long long pos = places[first + tok[j]];
+        if ((kSide || j == 0) && pos >= 0) f = rotations(a, col[k], pos);
         v[j][k] = turn(v[j][k], f, lost);   // of a token without a place it is not used
       }
       if (lost) {   // once for all: the rows are read again
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-          if (have(step, j) && place(step, j) >= 0)
-            v[j][k] = turn_wide(*reinterpret_cast<const uint4*>(a.q + row_of(step, j) * a.D + col[k]),
-                                rotations(a, col[k], place(step, j)));
+          const long long pos = places[first + tok[j]];
+          if (use[j] && pos >= 0)
+            v[j][k] = turn_wide(*reinterpret_cast<const uint4*>(a.q + row[j] * a.D + col[k]), rotations(a, col[k], pos));
         }
       }
     }
@@ -294,11 +292,13 @@ __device__ __forceinline__ void queries(const Args& a, int t0, int part, int lan
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int e = row_exponent(largest(largest(0u, v[j][0]), v[j][1]), a.q_lanes);
-      if (!have(step, j) || place(step, j) < 0) continue;
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (col[k] < a.D) *reinterpret_cast<uint2*>(a.q_codes + row_of(step, j) * a.D + col[k]) = coded(v[j][k], e);
-      if (sub == 0) a.q_scales[row_of(step, j)] = __fmul_rn(scale_of(e), wt[j]);
+      if (use[j] && places[first + tok[j]] >= 0) {   // no place past the last token
+        uint2* dst = reinterpret_cast<uint2*>(a.q_codes + row[j] * a.D) + sub;
+        dst[0] = coded(v[j][0], e);
+        if (col[1] < a.D) dst[a.q_lanes] = coded(v[j][1], e);
+        if (sub == 0) a.q_scales[row[j]] = __fmul_rn(scale_of(e), wt[j]);
+      }
+      row[j] += (size_t)a.together * a.H;
     }
     __syncwarp();
   }
@@ -332,7 +332,7 @@ struct QueryCut {
 };
 // Tokens side by side where a block has room for the heads of two and more, as many as fit (5,500 tokens of 4
 // heads 7 us, a block each 35); else one after the other, four where that leaves every SM eight blocks
-// (8,483 tokens of 64 heads 62 us, one a block 76).
+// (8,483 tokens of 64 heads 58 us, two a block 63, eight 72).
 static QueryCut query_cut(int H, int D, long long T) {
   const int rows = ia::kThreads / ia::q_lanes_of(D) * ia::kBatch;
   QueryCut c{1, 1, 1, 1};

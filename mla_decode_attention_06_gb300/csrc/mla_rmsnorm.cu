@@ -9,23 +9,23 @@
 // Arithmetic.  A code follows the last bit of y, so y is the correctly rounded value.
 //   Sum of squares: s' = fma(h, h, s) loses fma(h, h, s - s') exactly as long as s is not below h^2, so each
 //   thread starts at a power of two B above its largest square and adds up the losses; the threads' pairs
-//   (s - B, losses) are joined by Knuth's TwoSum.  Four operations a value, and two values an
-//   instruction.
+//   (s - B, losses) are joined by Knuth's TwoSum.  Four operations a value, none of which
+//   unpacks it (bf_fma).
 //   1 / sqrt, once a row, as a pair of floats ih + il, il >= 0 (a zero keeps its sign).
 //   y: m = h * gamma is exact in fp32, and so is the sum of fma(m, ih, m * il) but for its one rounding.
 //   Truncated and its last bit set it rounds to bf16 as the exact value does (no number with that bit
 //   lies on a bf16 boundary); where il = 0 the sum may be exact and the row is done one value at a time
 //   (fma_odd), as are values at the ends of fp32's range.
 //   x + residual needs no such care: a sum of two 8-bit significands rounded to 24 bits and then to 8
-//   is rounded as if once (24 >= 2 * 8 + 2).  An int8 quotient is formed with the reciprocal of s, off by
-//   at most 127 * 2^-23; where that leaves its rounding open (values that are the largest over a power of two
-//   among them, three in a thousand) the sign of y less s times the half-integer decides, one exact fma.
+//   is rounded as if once (24 >= 2 * 8 + 2).  An int8 quotient is formed with reciprocals of s a
+//   little too large and too small; where that leaves its rounding open (values that are the largest over a power of
+//   two among them, three in a thousand) the sign of y less s times the half-integer decides, one exact fma.
 //
 // Layout.  A row is read once and stays in registers: 8 values (16 bytes) a thread V times.  Rows of
 // up to 2,048 values take a warp, longer ones a block with three barriers a row (sum, 1 / sqrt,
-// largest code).  Bound by HBM for many long rows (8,192 x 8,192 with residual: e4m3 79 us, 5.98 TB/s, 88 % of
-// the copy rate, the integer pipe 59 % busy; int8 94; bf16 81, 97 %; codes alone 4,096 x 16,384 35 us,
-// 85 %), by the steps' latency for short rows (8,192 x 1,536 14 us) and for few (3 to 5 us).
+// largest code).  Bound by HBM for many long rows (8,192 x 8,192 with residual: e4m3 71.4 us, 6.58 TB/s, 97 % of
+// the copy rate; int8 82.4; bf16 81, 97 %; codes alone 4,096 x 16,384 34 us, 86 %), by the steps' latency for short
+// rows (8,192 x 1,536 11.4 us) and for few (3 to 5 us).
 #include "mla_kernels.cuh"
 #include "mla_rows.cuh"
 
@@ -73,57 +73,58 @@ static __device__ __noinline__ uint4 normed_any(uint4 h, uint4 g, float ih, floa
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// Eight values as int8 codes, exactly: where the fp32 quotient lies next to a half-integer, by the sign of
-// y less that half-integer times s, which one fma gives (32 bits of product; a scale so small that the
-// difference could underflow is brought up with y).
-static __device__ __noinline__ uint2 int8_exact(uint4 yv, float s, float rs) {
+constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: an integer added to it sits in the low bits
+
+// Eight values as int8 codes, exactly, from reciprocals of s that are too large and too small: where the two
+// disagree the quotient lies next to the half-integer between, and the sign of y less that times s, which one fma
+// gives, decides (32 bits of product; a scale so small that the difference could underflow is brought up with y).
+static __device__ __noinline__ uint2 int8_exact(uint4 yv, float s, float above, float below) {
   const uint32_t y[4] = {yv.x, yv.y, yv.z, yv.w};
-  const float up = s < 0x1p-60f ? 0x1p60f : 1.f, su = __fmul_rn(s, up);
   uint32_t b[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float v = i & 1 ? hi_f(y[i / 2]) : lo_f(y[i / 2]);
-    const float z = __fmul_rn(v, rs), k = rintf(z), r = __fsub_rn(z, k);
-    float code = k;
-    if (fabsf(r) > 0.5f - 0x1p-15f) {
-      const float half = k + (r > 0.f ? 0.5f : -0.5f), d = __fmaf_rn(-half, su, __fmul_rn(v, up));
-      code = d > 0.f ? ceilf(half) : d < 0.f ? floorf(half) : rintf(half);
+    const float p = __fmaf_rn(v, above, kMagic), q = __fmaf_rn(v, below, kMagic);
+    uint32_t code = __float_as_uint(p);
+    if (p != q) {
+      const float up = s < 0x1p-60f ? 0x1p60f : 1.f, half = 0.5f * ((p - kMagic) + (q - kMagic));
+      const float d = __fmaf_rn(-half, __fmul_rn(s, up), __fmul_rn(v, up));
+      const uint32_t more = __float_as_uint(fmaxf(p, q)), less = __float_as_uint(fminf(p, q));
+      code = d > 0.f ? more : d < 0.f ? less : more & 1u ? less : more;
     }
-    b[i / 4] |= ((uint32_t)(int)code & 0xFFu) << (8 * (i & 3));
+    b[i / 4] |= (code & 0xFFu) << (8 * (i & 3));
   }
   return make_uint2(b[0], b[1]);
 }
 
 // Eight values (packed bf16 pairs) as eight int8 codes.
 __device__ __forceinline__ uint2 int8_codes(const uint32_t (&y)[4], float s, float rs) {
-  constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: an integer added to it sits in the low bits
-  const float2x magic = both(kMagic, kMagic), rs2 = both(rs, rs);
-  uint32_t b[8];
-  float worst = 0.f;
+  const float above = __fmul_rn(rs, 1.f + 0x1p-22f), below = __fmul_rn(rs, 1.f - 0x1p-22f);
+  const float2x magic = both(kMagic, kMagic), above2 = both(above, above), below2 = both(below, below);
+  uint32_t b[8], differ = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2x z = mul2(widen2(y[i]), rs2), u = add2(z, magic);
-    float r0, r1;
-    apart(u, r0, r1);
+    const float2x v = widen2(y[i]);
+    float r0, r1, q0, q1;
+    apart(fma2(v, above2, magic), r0, r1);
+    apart(fma2(v, below2, magic), q0, q1);
     b[2 * i] = __float_as_uint(r0);
     b[2 * i + 1] = __float_as_uint(r1);
-    apart(sub2(z, sub2(u, magic)), r0, r1);
-    worst = fmaxf(worst, fmaxf(fabsf(r0), fabsf(r1)));
+    differ |= (b[2 * i] ^ __float_as_uint(q0)) | (b[2 * i + 1] ^ __float_as_uint(q1));
   }
-  if (worst > 0.5f - 0x1p-15f) return int8_exact(make_uint4(y[0], y[1], y[2], y[3]), s, rs);
+  if (differ) return int8_exact(make_uint4(y[0], y[1], y[2], y[3]), s, above, below);
   uint2 w;
   w.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
   w.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
   return w;
 }
 
-// Eight values as eight e4m3 codes of y * rs, rs a power of two.
-__device__ __forceinline__ uint2 e4m3_codes(const uint32_t (&y)[4], float rs) {
+// Eight values as eight e4m3 codes of y * rs, rs the bits of a power of two as a bf16 value.
+__device__ __forceinline__ uint2 e4m3_codes(const uint32_t (&y)[4], uint32_t rs) {
   uint32_t two[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float2 v;
-    apart(mul2(widen2(y[i]), both(rs, rs)), v.x, v.y);
+    const float2 v = make_float2(bf_mul(y[i], rs), bf_mul(y[i] >> 16, rs));
     two[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
   }
   return make_uint2(two[0] | (two[1] << 16), two[2] | (two[3] << 16));
@@ -134,10 +135,10 @@ __device__ __forceinline__ uint32_t halves_max(uint32_t v) { return max(v & 0xFF
 __device__ __forceinline__ uint32_t halves_min(uint32_t v) { return min(v & 0xFFFFu, v >> 16); }
 
 // V pieces of 8 values a thread; kWarp: a warp takes a row, else the block does.
-// Blocks of 256 threads: four an SM at 64 registers where a block takes a row (8,192 x 8,192 e4m3 84 us; three
-// at 72 93), three at 80 where its warps do (8,192 x 1,536 13.9 us; two at 106 15.4).
+// Blocks of 256 threads: five an SM at 51 registers where a block takes a row (8,192 x 8,192 e4m3 71.4 us; four
+// 73.7, six 72.5), four at 64 where its warps do (8,192 x 1,536 11.4 us; three 12.3, five 12.3).
 template <int V, bool kWarp, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 ? (kWarp ? 3 : 4) : 1) rmsnorm_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? (kWarp ? 4 : 5) : 1) rmsnorm_kernel(const Args a) {
   __shared__ float part_hi[32], part_lo[32];
   __shared__ double part_wide[32];
   __shared__ uint32_t part_max[32];
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? (kWarp ? 3 : 4) : 
       if (a.residual) {
         const uint32_t r[4] = {rv[v].x, rv[v].y, rv[v].z, rv[v].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[v][i] = pack2(add2(widen2(h[v][i]), widen2(r[i])));
+        for (int i = 0; i < 4; ++i) h[v][i] = pack2(bf_fma2(h[v][i], 0x3F803F80u, widen2(r[i])));
         const int p = first + v * step;
         if (p < n8)
           reinterpret_cast<uint4*>(a.residual_out + t * a.D)[p] = make_uint4(h[v][0], h[v][1], h[v][2], h[v][3]);
@@ -176,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? (kWarp ? 3 : 4) : 
     }
   }
 
+  uint32_t amax = 0;   // of the results, halves side by side
   if (a.gamma) {
     uint32_t top2 = 0;
 #pragma unroll
@@ -193,8 +195,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? (kWarp ? 3 : 4) : 
       for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2x x2 = widen2(h[v][i]), n = fma2(x2, x2, s);
-          e = add2(e, fma2(x2, x2, sub2(s, n)));
+          const float2x n = bf_fma2(h[v][i], h[v][i], s);
+          e = add2(e, bf_fma2(h[v][i], h[v][i], sub2(s, n)));
           s = n;
         }
       float s0, s1, e0, e1, f0, f1, f2;
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? (kWarp ? 3 : 4) : 
         uint32_t y[4], least = 0xFFFFFFFFu, most = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2x m = mul2(widen2(h[v][i]), widen2(g[i]));
+          const float2x m = bf_mul2(h[v][i], g[i]);
           float r0, r1;
           apart(fma2_rz(m, ih2, mul2(m, il2)), r0, r1);
           y[i] = pack(__uint_as_float(__float_as_uint(r0) | 1u), __uint_as_float(__float_as_uint(r1) | 1u));
@@ -306,7 +308,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? (kWarp ? 3 : 4) : 
           y[1] = r.y;
           y[2] = r.z;
           y[3] = r.w;
+          most = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) most = __vmaxu2(most, y[i] & 0x7FFF7FFFu);
         }
+        amax = __vmaxu2(amax, most);
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[v][i] = y[i];
       }
@@ -322,11 +328,12 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? (kWarp ? 3 : 4) : 
   }
   if (a.fmt == MLA_CODES_BF16) return;
 
-  uint32_t amax = 0;
+  if (!a.gamma) {
 #pragma unroll
-  for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) amax = __vmaxu2(amax, h[v][i] & 0x7FFF7FFFu);
+      for (int i = 0; i < 4; ++i) amax = __vmaxu2(amax, h[v][i] & 0x7FFF7FFFu);
+  }
   amax = halves_max(amax);
   amax = __reduce_max_sync(0xffffffffu, amax);
   if (!kWarp) {
@@ -351,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? (kWarp ? 3 : 4) : 
     if (p >= n8) continue;
     uint2 w;
     if (bad) w = int8 ? make_uint2(0, 0) : make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    else w = int8 ? int8_codes(h[v], s, rs) : e4m3_codes(h[v], rs);
+    else w = int8 ? int8_codes(h[v], s, rs) : e4m3_codes(h[v], __float_as_uint(rs) >> 16);
     reinterpret_cast<uint2*>(a.codes + t * a.D)[p] = w;
   }
   if (first == 0) a.scales[t] = bad && int8 ? __uint_as_float(0x7FC00000u) : s;

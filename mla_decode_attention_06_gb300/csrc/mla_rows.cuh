@@ -23,6 +23,30 @@ __device__ __forceinline__ float fma_odd(float a, float b, float c) {
   return __float_as_uint(down) & 1u ? down : up;
 }
 
+// a * b + c in fp32 of bf16 values a and b (the low 16 bits of each), rounded once to nearest, down or up: the
+// instruction takes the halves of a word as they are, which saves their unpacking.  A product alone adds -0, so that a
+// zero keeps its sign.
+__device__ __forceinline__ float bf_fma(uint32_t a, uint32_t b, float c) {
+  float d;
+  asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"((uint16_t)a), "h"((uint16_t)b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float bf_fma_rd(uint32_t a, uint32_t b, float c) {
+  float d;
+  asm("fma.rm.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"((uint16_t)a), "h"((uint16_t)b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float bf_fma_ru(uint32_t a, uint32_t b, float c) {
+  float d;
+  asm("fma.rp.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"((uint16_t)a), "h"((uint16_t)b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float bf_mul(uint32_t a, uint32_t b) { return bf_fma(a, b, -0.f); }
+__device__ __forceinline__ float bf_fma_odd(uint32_t a, uint32_t b, float c) {   // rounded to odd
+  const float down = bf_fma_rd(a, b, c), up = bf_fma_ru(a, b, c);
+  return __float_as_uint(down) & 1u ? down : up;
+}
+
 // Two floats as a bf16 pair, the first in the low half; nearest, ties to even.
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -102,6 +126,13 @@ __device__ __forceinline__ float2x mul2_rz(float2x a, float2x b) {
   asm("mul.rz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// Products of bf16 pairs, and with a sum.
+__device__ __forceinline__ float2x bf_mul2(uint32_t a, uint32_t b) { return both(bf_mul(a, b), bf_mul(a >> 16, b >> 16)); }
+__device__ __forceinline__ float2x bf_fma2(uint32_t a, uint32_t b, float2x c) {
+  float lo, hi;
+  apart(c, lo, hi);
+  return both(bf_fma(a, b, lo), bf_fma(a >> 16, b >> 16, hi));
+}
 // A bf16 pair as two floats, and back (nearest, ties to even).
 __device__ __forceinline__ float2x widen2(uint32_t v) { return both(lo_f(v), hi_f(v)); }
 __device__ __forceinline__ uint32_t pack2(float2x v) {
@@ -135,12 +166,13 @@ __device__ __forceinline__ uint32_t turn_wide(uint32_t x, uint32_t f) {
   return pack(double_odd(add_odd(x0 * c, -(x1 * s))), double_odd(add_odd(x0 * s, x1 * c)));
 }
 // The pair (x0, x1) of `x` turned by (cos, sin) of `f`, as a bf16 pair.  Products of bf16 values
-// are exact in fp32's normal range; `lost` becomes other than 0 where one is not.
+// are exact in fp32's normal range; `lost` becomes other than 0 where one is not (what it lost, rounded up, is
+// +0 only if that is nothing).
 __device__ __forceinline__ uint32_t turn(uint32_t x, uint32_t f, uint32_t& lost) {
-  const float x0 = lo_f(x), x1 = hi_f(x), c = lo_f(f), s = hi_f(f);
-  const float p = __fmul_rn(x1, s), r = __fmul_rn(x1, c);
-  lost |= product_lost(p, x1, s) | product_lost(r, x1, c);
-  return pack(fma_odd(x0, c, -p), fma_odd(x0, s, r));
+  const uint32_t x1 = x >> 16, s = f >> 16;
+  const float p = bf_mul(x1, s), r = bf_mul(x1, f);
+  lost |= __float_as_uint(bf_fma_ru(x1, s, -p)) | __float_as_uint(bf_fma_ru(x1, f, -r));
+  return pack(bf_fma_odd(x, f, -p), bf_fma_odd(x, s, r));
 }
 // 16 bytes of pairs.
 static __device__ __noinline__ uint4 turn_wide(uint4 x, uint4 f) {

@@ -92,7 +92,7 @@ def test_indexer_append_refusals(lib):
                dict(cache=FAKE + 8), dict(freqs=FAKE + 8), dict(gamma=FAKE + 8), dict(beta=FAKE + 8)):
         assert call(**kw) == INVALID, kw
     for kw in (dict(D=132, stride=136, R=64), dict(D=264, stride=264), dict(R=60), dict(ps=1 << 20, pages=1 << 12),
-               dict(T=1 << 30, H=1 << 20)):
+               dict(T=1 << 30, H=1 << 20), dict(T=(1 << 31) - 40, H=1)):
         assert call(**kw) == UNSUPPORTED, kw
     assert call(ws_bytes=0) == TOO_SMALL and call(ws=FAKE + 8) == TOO_SMALL
     # without queries the head count is not looked at, without rotations the rope width
