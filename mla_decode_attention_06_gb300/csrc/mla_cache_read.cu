@@ -5,13 +5,11 @@
 //
 // each value rounded once.
 //
-// Layout.  A warp takes `rows_per_warp` consecutive tokens.  Its lanes look their tokens up at
-// once, a lane a token (request by bisection, length, page), so the chain of dependent reads is
-// paid once a warp and not once a row; then the rows are copied, 16 bytes of output (8 values) a lane.
-// bf16 and e4m3 rows are loaded two at a time by the lanes that write them; e2m1 rows, of which a lane's 8
-// values are 4 bytes and a scale, whole, 16 bytes a lane, four at a time, through shared memory.  Bound by HBM.
-// 199,000 e4m3 rows 61.5 us (5.8 TB/s, 85 % of the copy rate), 278,000 bf16 rows 71.5 us (94 %), as many e2m1
-// rows 54 us (83 %; loaded 4 bytes a lane 70); 4,000 e2m1 rows 3.8 us.
+// Layout.  A warp takes `per_warp` consecutive tokens.  Its lanes look their tokens up at once, a lane a
+// token (request by bisection, length, page), so the chain of dependent reads is paid once a warp and not
+// once a row; then the rows are copied, four at a time, all their loads out before the first store, 16 bytes a
+// lane each.  Bound by HBM.  199,000 e4m3 rows 58.5 us (6.1 TB/s, 90 % of the copy rate), 278,000 bf16 rows
+// 70.4 us (95 %), as many e2m1 rows 54 us (83 %; loaded 4 bytes a lane 70); 4,000 e2m1 rows 3.8 us.
 #include "mla_kernels.cuh"
 #include "mla_rows.cuh"
 
@@ -21,7 +19,6 @@ namespace rd {
 using namespace rows;
 
 constexpr int kWarps = 4;
-constexpr int kMaxPieces = 3;        // 8-value pieces of a row a lane: L + R <= 768
 
 struct Args {
   int L, R, ps, num_pages, B, T, bt_stride, per_warp;
@@ -107,36 +104,79 @@ __device__ __forceinline__ uint4 e2m1_values(uint32_t codes, __nv_bfloat162 s) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// What a lane holds of a row: 8 values of the latent part as they are stored, or of the rope part.
-template <int kFmt>
-struct Piece {
-  uint4 raw;
-  float scale;
-};
+// Rows of a warp whose loads are out together (199,000 e4m3 rows two 59.9 us, four 58.7; 278,000 bf16 rows 71.2
+// and 70.4).  The functions below copy the rows of a warp's tokens from t0 on; `mine`: lane i's is token t0 + i's
+// cache row.
+constexpr int kRows = 4;
 
-template <int kFmt>
-__device__ __forceinline__ void load(const Args& a, long long row, int piece, Piece<kFmt>& p) {
-  const uint8_t* src = a.pool + row * a.row_bytes;
-  const int latent = a.L / 8;
-  if (kFmt == MLA_CACHE_BF16 || piece >= latent) {
-    p.raw = *reinterpret_cast<const uint4*>(src + (a.row_bytes - 2 * (a.L + a.R)) + 16 * piece);
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(src + 8 * piece);
-    p.raw.x = v.x;
-    p.raw.y = v.y;
-    p.scale = a.scales[row];
+// Of kRows rows from the i-th on, whose `at` each is; -1: none.
+__device__ __forceinline__ void rows_at(const Args& a, long long mine, int i, long long (&at)[kRows]) {
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    at[j] = __shfl_sync(0xffffffffu, mine, (i + j) & 31);
+    if (i + j >= a.per_warp) at[j] = -1;
   }
 }
 
-template <int kFmt>
-__device__ __forceinline__ uint4 values(const Args& a, int piece, const Piece<kFmt>& p) {
-  if (kFmt == MLA_CACHE_BF16 || piece >= a.L / 8) return p.raw;
-  return e4m3_values(make_uint2(p.raw.x, p.raw.y), p.scale);
+__device__ __forceinline__ void copy_bf16(const Args& a, long long t0, long long mine, int lane) {
+  constexpr int kPieces = 3;   // 16 bytes of a row a lane: L + R <= 640
+  const int pieces = (a.L + a.R) / 8;
+#pragma unroll 1
+  for (int i = 0; i < a.per_warp; i += kRows) {
+    uint4 v[kRows][kPieces];
+    long long at[kRows];
+    rows_at(a, mine, i, at);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c)
+        if (at[j] >= 0 && lane + 32 * c < pieces)
+          v[j][c] = reinterpret_cast<const uint4*>(a.pool + at[j] * a.row_bytes)[lane + 32 * c];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c)
+        if (at[j] >= 0 && lane + 32 * c < pieces)
+          reinterpret_cast<uint4*>(a.out + (t0 + i + j) * (a.L + a.R))[lane + 32 * c] = v[j][c];
+  }
 }
 
-// The rows of a warp's tokens from t0 on; `mine`: lane i's is token t0 + i's cache row.
+// 16 codes of the latent part and 8 rope values a lane (8 codes, so that neighbouring lanes store neighbouring 16
+// bytes, took 61.3 us).
+__device__ __forceinline__ void copy_e4m3(const Args& a, long long t0, long long mine, int lane) {
+  const bool latent = lane < a.L / 16, rope = lane < a.R / 8;
+#pragma unroll 1
+  for (int i = 0; i < a.per_warp; i += kRows) {
+    uint4 v[kRows], r[kRows];
+    float s[kRows];
+    long long at[kRows];
+    rows_at(a, mine, i, at);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const uint8_t* src = a.pool + at[j] * a.row_bytes + 16 * lane;
+      if (at[j] >= 0 && latent) {
+        v[j] = *reinterpret_cast<const uint4*>(src);
+        s[j] = a.scales[at[j]];
+      }
+      if (at[j] >= 0 && rope) r[j] = *reinterpret_cast<const uint4*>(src + a.L);
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      if (at[j] < 0) continue;
+      __nv_bfloat16* out = a.out + (t0 + i + j) * (a.L + a.R);
+      if (latent) {
+        const uint4 lo = e4m3_values(make_uint2(v[j].x, v[j].y), s[j]), hi = e4m3_values(make_uint2(v[j].z, v[j].w), s[j]);
+        reinterpret_cast<uint4*>(out)[2 * lane] = lo;   // one right after the other, or half sectors go to L2 (69 us)
+        reinterpret_cast<uint4*>(out)[2 * lane + 1] = hi;
+      }
+      if (rope) reinterpret_cast<uint4*>(out + a.L)[lane] = r[j];
+    }
+  }
+}
+
+// Rows through shared memory: a lane's 8 values are 4 bytes and a scale, loaded 16 bytes a lane.
 __device__ __forceinline__ void copy_e2m1(const Args& a, long long t0, long long mine, int lane) {
-  constexpr int kRows = 4, kRowBytes = 544;   // rows are at most 528 bytes (L = 512, R = 128)
+  constexpr int kRowBytes = 544;   // rows are at most 528 bytes (L = 512, R = 128)
   __shared__ __align__(16) uint8_t rows[kWarps][kRows][kRowBytes];
   uint8_t(*row)[kRowBytes] = rows[threadIdx.x >> 5];
   const int whole = (int)(a.row_bytes / 16), latent = a.L / 8, pieces = (a.L + a.R) / 8;
@@ -144,10 +184,9 @@ __device__ __forceinline__ void copy_e2m1(const Args& a, long long t0, long long
   for (int i = 0; i < a.per_warp; i += kRows) {
     uint4 v[kRows][2];
     long long at[kRows];
+    rows_at(a, mine, i, at);
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      at[j] = __shfl_sync(0xffffffffu, mine, (i + j) & 31);
-      if (i + j >= a.per_warp) at[j] = -1;
       const uint4* src = reinterpret_cast<const uint4*>(a.pool + at[j] * a.row_bytes);
       if (at[j] >= 0 && lane < whole) v[j][0] = src[lane];
       if (at[j] >= 0 && lane + 32 < whole) v[j][1] = src[lane + 32];
@@ -182,31 +221,9 @@ __global__ void __launch_bounds__(32 * kWarps) read_kernel(const Args a) {
   const long long t0 = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * a.per_warp;
   if (t0 >= a.T) return;
   const long long mine = lane < a.per_warp ? find(a, (int)min(t0 + lane, (long long)a.T)) : -1;
-  const int pieces = (a.L + a.R) / 8;
-  if constexpr (kFmt == MLA_CACHE_E2M1) {
-    copy_e2m1(a, t0, mine, lane);
-    return;
-  }
-  constexpr int kTogether = 2;   // rows whose loads are out together
-  for (int i = 0; i < a.per_warp; i += kTogether) {
-    Piece<kFmt> p[kTogether][kMaxPieces];
-    long long row[kTogether];
-#pragma unroll
-    for (int j = 0; j < kTogether; ++j) {
-      row[j] = __shfl_sync(0xffffffffu, mine, (i + j) & 31);
-      if (i + j >= a.per_warp) row[j] = -1;
-#pragma unroll
-      for (int c = 0; c < kMaxPieces; ++c)
-        if (row[j] >= 0 && lane + 32 * c < pieces) load<kFmt>(a, row[j], lane + 32 * c, p[j][c]);
-    }
-#pragma unroll
-    for (int j = 0; j < kTogether; ++j)
-#pragma unroll
-      for (int c = 0; c < kMaxPieces; ++c)
-        if (row[j] >= 0 && lane + 32 * c < pieces)
-          reinterpret_cast<uint4*>(a.out + (t0 + i + j) * (a.L + a.R))[lane + 32 * c] =
-              values<kFmt>(a, lane + 32 * c, p[j][c]);
-  }
+  if constexpr (kFmt == MLA_CACHE_BF16) copy_bf16(a, t0, mine, lane);
+  else if constexpr (kFmt == MLA_CACHE_E4M3) copy_e4m3(a, t0, mine, lane);
+  else copy_e2m1(a, t0, mine, lane);
 }
 
 }  // namespace rd
