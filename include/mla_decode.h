@@ -349,7 +349,7 @@ int mla_rmsnorm_quant(int32_t code_format, int32_t rows, int32_t width, const vo
  *   out            bf16, row t at out + t * out_stride; out_stride in elements, >= n
  *   flags, workspace   as mla_branch_prologue (a wait that runs out is recorded there)
  * The codes are e4m3 (OCP E4M3FN) for _fp8 and int8 for _int8.  k is a multiple of 16, n and
- * out_stride of 8, tokens at most 2^22, n at most 2^24; x_codes, w_codes, w_scales and out are
+ * out_stride of 8, tokens at most 2^22, n and k at most 2^24; x_codes, w_codes, w_scales and out are
  * 16-byte aligned.  The result of a token does not depend on the timing of the call; it may differ in
  * rounding between calls of different numbers of tokens (K is split where there are few). */
 int mla_linear_fp8(int32_t tokens, int32_t n, int32_t k, const void* x_codes, const float* x_scales,

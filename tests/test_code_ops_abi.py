@@ -47,7 +47,8 @@ def test_linear_refusals(lib, name):
                dict(ws=None), dict(out=None), dict(wsp=None), dict(x=FAKE + 8), dict(w=FAKE + 8), dict(ws=FAKE + 4),
                dict(out=FAKE + 8)):
         assert call(**kw) == INVALID, kw
-    for kw in (dict(n=60), dict(k=72), dict(stride=68), dict(T=(1 << 22) + 1), dict(n=(1 << 24) + 8, stride=1 << 25)):
+    for kw in (dict(n=60), dict(k=72), dict(stride=68), dict(T=(1 << 22) + 1), dict(n=(1 << 24) + 8, stride=1 << 25),
+               dict(k=(1 << 24) + 16), dict(k=(1 << 31) - 16)):
         assert call(**kw) == UNSUPPORTED, kw
     for kw in (dict(wsp_bytes=255), dict(wsp=FAKE + 8)):
         assert call(**kw) == TOO_SMALL, kw
