@@ -40,6 +40,7 @@ struct Args {
   int fmt, T, D;
   long long x_stride;
   double eps;
+  bool eps_wide;                   // past what rsqrt_pair takes, alone under the root of a row of zeros
   float inv_h, inv_l;              // 1 / D as a pair
   const __nv_bfloat16* x;          // [T, >= D]
   const __nv_bfloat16* residual;   // [T, D] or NULL
@@ -185,8 +186,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? (kWarp ? 4 : 5) : 
 #pragma unroll
       for (int i = 0; i < 4; ++i) top2 = __vmaxu2(top2, h[v][i] & 0x7FFF7FFFu);
     const uint32_t top = halves_max(top2);
-    // fp64 where the squares of this thread's largest values would leave fp32's inner range
-    bool wide = a.eps > 0x1p60 || (top != 0 && !(top >= (0x2B800000u >> 16) && top <= (0x53800000u >> 16)));   // 2^-40 .. 2^40
+    // fp64 where the squares of this thread's largest values, or epsilon, would leave fp32's inner range
+    bool wide = a.eps_wide || (top != 0 && !(top >= (0x2B800000u >> 16) && top <= (0x53800000u >> 16)));   // 2^-40 .. 2^40
     const float bias = __uint_as_float(top == 0 ? 0u : (2 * (top >> 7) - 125) << 23);   // the square of twice its power of two
     float hi, lo;
     {
@@ -382,6 +383,7 @@ cudaError_t launch_rmsnorm(int fmt, int rows, int width, const void* x, long lon
   a.D = width;
   a.x_stride = x_stride;
   a.eps = (double)eps;
+  a.eps_wide = eps > 0x1p60f || (eps != 0.f && eps < 0x1p-100f);
   a.inv_h = (float)(1.0 / width);
   a.inv_l = (float)(1.0 / width - (double)a.inv_h);
   a.x = static_cast<const __nv_bfloat16*>(x);
