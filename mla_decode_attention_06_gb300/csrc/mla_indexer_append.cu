@@ -172,6 +172,9 @@ __device__ __forceinline__ uint4 layer_norm(const Args& a, uint4 x, int col, boo
   group_sum(a.lanes, hi, lo);
   float mh, ml;
   mean_plus(hi, lo, a.inv_h, a.inv_l, 0.f, mh, ml);
+  // what mh leaves of the sum is an fp32 number: divided, not multiplied by 1 / D, a mean that is one of the keys comes
+  // out exactly (equal keys of 184 had a deviation of some 2^-49 of theirs, which a beta of zero shows)
+  ml = __fdiv_rn(__fadd_rn(__fmaf_rn(-(float)a.D, mh, hi), lo), (float)a.D);
   float dl[8];
   hi = lo = 0.f;
 #pragma unroll
