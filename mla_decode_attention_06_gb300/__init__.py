@@ -213,15 +213,12 @@ def _unread_status(device, stream):
     return t
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
-
-
 def _handle(stream, device):
     """The cudaStream_t that a call runs on, without a Stream object for the current one (3 us of a call)."""
     if device.index is None:
         raise ValueError(f"tensors must be CUDA tensors, not on {device}")
-    return _raw_stream(device.index) if stream is None else stream.cuda_stream
+    # looked up here, not at import: a torch without CUDA has neither name, and the host functions need none
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _status_word(workspace, debug, device, stream, handle):
@@ -261,7 +258,7 @@ def _call(name, device, *args):
     fn = _fns.get(name)
     if fn is None:
         fn = _fns[name] = getattr(_lib.load(), name)
-    if device.index is None or _current_device() == device.index:
+    if device.index is None or torch._C._cuda_getDevice() == device.index:
         rc = fn(*args)
     else:
         with torch.cuda.device(device):
