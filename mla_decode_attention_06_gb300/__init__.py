@@ -192,7 +192,7 @@ def mla_decode_paged_fp8(q, input_row_offsets, kv_pool_fp8, kv_scales, block_tab
 
 _I32 = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32,)
 _INT32 = (torch.int32,)
-_INT8 = (torch.int8,)
+_INT8 = (torch.int8, torch.uint8)
 _F8 = (torch.float8_e4m3fn, torch.uint8)
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
@@ -484,7 +484,7 @@ def mla_linear_fp8(x_codes, x_scales, w_codes, w_scales, *, out=None, debug: boo
 
 
 def mla_linear_int8(x_codes, x_scales, w_codes, w_scales, *, out=None, debug: bool = False, workspace=None, stream=None):
-    """mla_linear_fp8 over int8 codes."""
+    """mla_linear_fp8 over int8 codes (int8, or uint8 that holds them)."""
     return _linear("mla_linear_int8", _INT8, x_codes, x_scales, w_codes, w_scales, out, debug, workspace, stream)
 
 
