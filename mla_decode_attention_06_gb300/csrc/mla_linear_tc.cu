@@ -85,11 +85,15 @@ struct Args {
 // The issuing warps spin on a phase (a suspended waiter wakes later, between products); all others are
 // suspended by the hardware for a while, or two dozen spinning warps would take the issue slots of those
 // that work.  The clock is looked at now and then.
-template <bool kSpin>
+template <bool kSpin, bool kCluster>
 __device__ __forceinline__ bool wait_any(uint64_t* bar, uint32_t parity, PlanHeader* hdr) {
+  auto there = [&]() {
+    if (kCluster) return kSpin ? mbar_test_wait_cluster(bar, parity) : mbar_try_wait_cluster(bar, parity);
+    return kSpin ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+  };
   uint64_t t0 = 0;
 #pragma unroll 1
-  for (uint32_t i = 1; !(kSpin ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)); ++i) {
+  for (uint32_t i = 1; !there(); ++i) {
     if ((i & (kSpin ? 255u : 15u)) != 0) continue;
     const uint64_t now = globaltimer_ns();
     if (t0 == 0) t0 = now;
@@ -101,10 +105,17 @@ __device__ __forceinline__ bool wait_any(uint64_t* bar, uint32_t parity, PlanHea
   return true;
 }
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, PlanHeader* hdr) {
-  return wait_any<false>(bar, parity, hdr);
+  return wait_any<false, false>(bar, parity, hdr);
 }
 __device__ __forceinline__ bool spin_bar(uint64_t* bar, uint32_t parity, PlanHeader* hdr) {
-  return wait_any<true>(bar, parity, hdr);
+  return wait_any<true, false>(bar, parity, hdr);
+}
+// The same for barriers on which the other CTA of a pair arrives: what it did before is there (acquire at cluster scope).
+__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, PlanHeader* hdr) {
+  return wait_any<false, true>(bar, parity, hdr);
+}
+__device__ __forceinline__ bool spin_pair(uint64_t* bar, uint32_t parity, PlanHeader* hdr) {
+  return wait_any<true, true>(bar, parity, hdr);
 }
 
 // Place in a ring of `n` stages, and the parity of the round.
@@ -600,9 +611,9 @@ __device__ __forceinline__ Tile tile_of(int i, int mtiles, int ntiles, int kn) {
   return Tile{(8 * group + in % gm) * 256, in / gm * kn};
 }
 
-// Warp 0 copies, warp 1 (of the pair's first CTA) issues the products, warp 2 owns the tensor memory,
-// warps 4-7 (e4m3: 4-11) are the epilogue; int8: warps 8-11 widen the first half of a stage's tokens (thread = row =
-// TMEM lane), 12-15 of its channels, 16-23 the second half's.
+// Warp 0 copies, warp 1 of the pair's first CTA issues the products, warp 2 owns the tensor memory, warps 4-7 (e4m3:
+// 4-11) are the epilogue; int8: warps 8-11 widen the first half of a stage's tokens (thread = row = TMEM lane), 12-15
+// of its channels, 16-23 the second half's, and warp 1 of the second CTA says that they are there.
 template <bool kInt8, int kW>
 __global__ void __launch_bounds__(Pair<kInt8, kW>::kThreads, 1) __cluster_dims__(2, 1, 1)
     pair_kernel(const __grid_constant__ Maps maps, const Args a) {
@@ -611,7 +622,7 @@ __global__ void __launch_bounds__(Pair<kInt8, kW>::kThreads, 1) __cluster_dims__
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + P::kBars);   // e4m3: the first CTA's, for both; int8: each its own
   uint64_t* empty = full + P::kStages;
-  uint64_t* full2 = empty + P::kStages;      // int8: widened, in the first CTA
+  uint64_t* full2 = empty + P::kStages;      // int8: widened in this CTA; the first's: in both
   uint64_t* empty2 = full2 + P::kStages2;
   uint64_t* acc_full = empty2 + P::kStages2;           // a tile's products are done
   uint64_t* acc_empty = acc_full + 2;        // ... and read, in the first CTA
@@ -629,7 +640,7 @@ __global__ void __launch_bounds__(Pair<kInt8, kW>::kThreads, 1) __cluster_dims__
       mbar_init(&empty[s], kInt8 ? 16 : 1);
     }
     for (int s = 0; s < P::kStages2; ++s) {
-      mbar_init(&full2[s], 16);
+      mbar_init(&full2[s], rank == 0 ? 9 : 8);   // its CTA's warps, and in the first what the second hands over
       mbar_init(&empty2[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -688,10 +699,10 @@ __global__ void __launch_bounds__(Pair<kInt8, kW>::kThreads, 1) __cluster_dims__
     int n = 0;
     for (int tile = first; tile < tiles && ok; tile += pairs, ++n, acc.next(P::kAccs)) {
       const uint32_t d = tmem + acc.s * P::kN;
-      if (n >= P::kAccs && !(ok = wait_bar(&acc_empty[acc.s], acc.round ^ 1, a.hdr))) break;
+      if (n >= P::kAccs && !(ok = wait_pair(&acc_empty[acc.s], acc.round ^ 1, a.hdr))) break;
       tc_fence_after();
       for (int kb = 0; kb < (kInt8 ? 2 * nkb : nkb); ++kb, pos.next(kInt8 ? P::kStages2 : P::kStages)) {
-        if (!(ok = spin_bar(kInt8 ? &full2[pos.s] : &full[pos.s], pos.round, a.hdr))) break;
+        if (!(ok = spin_pair(kInt8 ? &full2[pos.s] : &full[pos.s], pos.round, a.hdr))) break;
         tc_fence_after();
         if (elect_one()) {
           if (kInt8) {
@@ -712,6 +723,20 @@ __global__ void __launch_bounds__(Pair<kInt8, kW>::kThreads, 1) __cluster_dims__
       if (elect_one()) mma_commit_pair(&acc_full[acc.s]);
       __syncwarp();
     }
+  } else if (kInt8 && warp == 1) {
+    // What the second CTA's warps widened: they arrive here, and this warp hands it on to the first CTA.  The release to the
+    // cluster takes a warp that widens a twelfth of its time (4,096 x 24,576 x 1,536 196 us against 185); here
+    // nothing waits for it.
+    Ring pos;
+    bool ok = true;
+    for (int tile = first; tile < tiles && ok; tile += pairs)
+      for (int kb = 0; kb < 2 * nkb; ++kb, pos.next(P::kStages2)) {
+        if (!(ok = wait_bar(&full2[pos.s], pos.round, a.hdr))) break;
+        tc_fence_after();
+        tc_fence_before();
+        if (elect_one()) mbar_arrive_remote(mapa_shared(smem_u32(&full2[pos.s]), 0));
+        __syncwarp();
+      }
   } else if (warp >= 4 && warp < 4 + 4 * P::kGroups) {
     // Groups of four warps share the accumulator's chunks of 64 channels.
     const int row = tid & 127, g4 = (warp - 4) >> 2;   // token of the CTA's half = TMEM lane; group
@@ -825,7 +850,7 @@ __global__ void __launch_bounds__(Pair<kInt8, kW>::kThreads, 1) __cluster_dims__
         __syncwarp();
         if (elect_one()) {
           mbar_arrive(&empty[from.s]);
-          mbar_arrive_remote(mapa_shared(smem_u32(&full2[to.s]), 0));
+          mbar_arrive(&full2[to.s]);
         }
         __syncwarp();
         from.next(P::kStages);

@@ -86,11 +86,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// The same with the default scope (release at CTA scope).  Cluster-scope release waits for every store of the
-// thread, a microsecond; what a tensor-core product of the cluster reads has been handed over before this
-// by a proxy fence (shared memory) or tcgen05.wait (tensor memory).
+// The same, but the release orders accesses to this CTA's shared memory alone: a release of everything waits
+// for the thread's stores to global memory too, a microsecond.  What a product of the cluster reads has been handed to the
+// asynchronous proxy before this (shared memory) or ordered by a tcgen05 fence (tensor memory).
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+      : "memory");
 }
 
 // The same without ordering: for signals whose data is tracked by barriers of its own.
