@@ -342,14 +342,15 @@ int mla_rmsnorm_quant(int32_t code_format, int32_t rows, int32_t width, const vo
  * projections around the attention (down to the latents, queries up, output), on what
  * mla_rmsnorm_quant writes.
  *   out[t, n] = bf16( (sum_k x[t, k] * w[n, k]) * x_scales[t] * w_scales[n] )
- * in fp32 (products of codes are exact, their sum is fp32 in the tensor core's order, or exact for
- * up to eight int8 tokens of k up to 65536), rounded once to bf16.  A NaN code or scale makes NaN of the results that it enters.
+ * in fp32 (products of codes are exact; their sum is exact for up to eight int8 tokens of k up to
+ * 65536, else fp32 in the tensor core's order, within k / 16 * 2^-22 of sum_k |x w|: 2^-9 at the
+ * largest k), rounded once to bf16.  A NaN code or scale makes NaN of the results that it enters.
  *   x_codes        [tokens, k], x_scales float [tokens]
  *   w_codes        [n, k], w_scales float [n]
  *   out            bf16, row t at out + t * out_stride; out_stride in elements, >= n
  *   flags, workspace   as mla_branch_prologue (a wait that runs out is recorded there)
  * The codes are e4m3 (OCP E4M3FN) for _fp8 and int8 for _int8.  k is a multiple of 16, n and
- * out_stride of 8, tokens at most 2^22, n and k at most 2^24; x_codes, w_codes, w_scales and out are
+ * out_stride of 8, tokens at most 2^22, n 2^24, k 2^17; x_codes, w_codes, w_scales and out are
  * 16-byte aligned.  The result of a token does not depend on the timing of the call; it may differ in
  * rounding between calls of different numbers of tokens (K is split where there are few). */
 int mla_linear_fp8(int32_t tokens, int32_t n, int32_t k, const void* x_codes, const float* x_scales,

@@ -593,7 +593,7 @@ int run_linear(const char* name, bool int8, int32_t tokens, int32_t n, int32_t k
                size_t workspace_bytes, void* stream) {
   if (tokens < 0 || n < 1 || k < 1 || out_stride < n || (flags & ~MLA_FLAG_DEBUG_CHECKS)) return MLA_ERR_INVALID_ARG;
   if (n % 8 != 0 || k % 16 != 0 || out_stride % 8 != 0) return MLA_ERR_UNSUPPORTED;
-  if (tokens > kMaxLinearTokens || n > kMaxLinearWeights || k > kMaxLinearWeights) return MLA_ERR_UNSUPPORTED;
+  if (tokens > kMaxLinearTokens || n > kMaxLinearRows || k > kMaxLinearK) return MLA_ERR_UNSUPPORTED;
   if ((tokens > 0 && (!x || !x_scales || !out)) || !w || !w_scales || !workspace) return MLA_ERR_INVALID_ARG;
   for (const void* p : {x, w, static_cast<const void*>(w_scales), static_cast<const void*>(out)})
     if (!aligned16(p)) return MLA_ERR_INVALID_ARG;

@@ -87,7 +87,8 @@ cudaError_t launch_rmsnorm(int fmt, int rows, int width, const void* x, long lon
                            cudaStream_t s);
 
 // Projection over 8-bit codes (int8, else e4m3): K a multiple of 16, N of 8, out_stride of 8.
-constexpr int kMaxLinearTokens = 1 << 22, kMaxLinearWeights = 1 << 24;   // tiles and steps along K are counted in 32 bits
+constexpr int kMaxLinearTokens = 1 << 22, kMaxLinearRows = 1 << 24;   // tiles are counted in 32 bits
+constexpr int kMaxLinearK = 1 << 17;   // one fp32 sum: within K / 16 * 2^-22 of the sum of magnitudes, 2^-9 here
 cudaError_t launch_linear(bool int8, int T, int N, int K, const void* x, const float* x_scale, const void* w,
                           const float* w_scale, void* out, long long out_stride, PlanHeader* hdr, cudaStream_t s);
 

@@ -50,3 +50,27 @@ def test_same_bits_with_many_tiles_a_pair(dev, kind, T, N, K):  # noqa: F811
     for _ in range(40):
         call(kind, x, xs, w, ws, out=out.fill_(7.0))
         assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("T", [1, 2, 8, 9, 20, 100, 300])
+def test_longest_sums(dev, kind, T):  # noqa: F811
+    """The largest K, codes of one sign: each step of an fp32 sum may lose in the same direction.  The bound
+    (K / 16 * 2^-22 of the sum of magnitudes) is then 2^-9, half of what rounding to bf16 may take."""
+    K = 1 << 17
+    x, xs = codes(kind, 5, T, K, dev)
+    w, ws = codes(kind, 6, 72, K, dev)
+    if kind == "int8":
+        x, w = x.clamp(min=-127).abs(), w.clamp(min=-127).abs()
+    else:
+        x, w = (t.view(torch.uint8).bitwise_and(0x7F).view(torch.float8_e4m3fn) for t in (x, w))
+    check(call(kind, x, xs, w, ws, debug=True), x, xs, w, ws)
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+def test_longer_sums_are_refused(dev, kind):  # noqa: F811
+    import mla_decode_attention_06_gb300 as M
+    x, xs = codes(kind, 5, 3, (1 << 17) + 16, dev)
+    with pytest.raises(M.MlaError) as e:
+        call(kind, x, xs, x[:1].expand(8, -1).contiguous(), xs[:1].expand(8).contiguous())
+    assert e.value.code == 2
