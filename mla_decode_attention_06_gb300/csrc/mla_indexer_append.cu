@@ -72,14 +72,7 @@ __device__ __forceinline__ float scale_of(int e) { return e == 255 ? 1.f : pow2(
 __device__ __forceinline__ uint2 coded(uint4 x, int e) {
   if (e == 255) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);   // every code a NaN
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  const uint32_t rs = __float_as_uint(pow2(-e)) >> 16;   // a bf16 value: -e is -127 at least
-  uint32_t two[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = make_float2(bf_mul(w[i], rs), bf_mul(w[i] >> 16, rs));
-    two[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-  }
-  return make_uint2(two[0] | (two[1] << 16), two[2] | (two[3] << 16));
+  return e4m3_codes(w, __float_as_uint(pow2(-e)) >> 16);   // a bf16 value: -e is -127 at least
 }
 
 // Whether column `col` lies in the part of a row that is turned, and its rotations.

@@ -120,17 +120,6 @@ __device__ __forceinline__ uint2 int8_codes(const uint32_t (&y)[4], float s, flo
   return w;
 }
 
-// Eight values as eight e4m3 codes of y * rs, rs the bits of a power of two as a bf16 value.
-__device__ __forceinline__ uint2 e4m3_codes(const uint32_t (&y)[4], uint32_t rs) {
-  uint32_t two[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = make_float2(bf_mul(y[i], rs), bf_mul(y[i] >> 16, rs));
-    two[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-  }
-  return make_uint2(two[0] | (two[1] << 16), two[2] | (two[3] << 16));
-}
-
 // Largest 16-bit half (0 .. 0xFFFF) of a word of two.
 __device__ __forceinline__ uint32_t halves_max(uint32_t v) { return max(v & 0xFFFFu, v >> 16); }
 __device__ __forceinline__ uint32_t halves_min(uint32_t v) { return min(v & 0xFFFFu, v >> 16); }

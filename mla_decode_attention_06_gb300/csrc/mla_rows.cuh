@@ -160,6 +160,17 @@ __device__ __forceinline__ float pow2(int e) {
   return e >= -126 ? __uint_as_float((uint32_t)(e + 127) << 23) : __uint_as_float(1u << (e + 149));
 }
 
+// Eight values (packed bf16 pairs) as eight e4m3 codes of y * rs, rs the bits of a power of two as a bf16 value.
+__device__ __forceinline__ uint2 e4m3_codes(const uint32_t (&y)[4], uint32_t rs) {
+  uint32_t two[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = make_float2(bf_mul(y[i], rs), bf_mul(y[i] >> 16, rs));
+    two[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(two[0] | (two[1] << 16), two[2] | (two[3] << 16));
+}
+
 // `turn` for products that fp32 does not hold.
 __device__ __forceinline__ uint32_t turn_wide(uint32_t x, uint32_t f) {
   const double x0 = lo_f(x), x1 = hi_f(x), c = lo_f(f), s = hi_f(f);
@@ -222,38 +233,10 @@ __device__ __forceinline__ Place locate_groups(const A& a, int t, int lanes, int
   else if (sub == 0) atomicOr(&a.hdr->status, kDeviceCheckFailed);
   return p;
 }
-// One token for the whole warp: where token t goes.  `A` holds the call's offsets, cache_lens, block_table,
-// bt_stride, ps, num_pages, B, max_seq_len and hdr.  The request is the last b with offsets[b] <= t,
-// found by 32 probes a round (two rounds up to 1024 requests).  Tokens at or past
-// offsets[B] belong to nobody and are skipped; a position or page out of range is
-// reported.
+// One token for the whole warp.
 template <class A>
 __device__ __forceinline__ Place locate(const A& a, int t, int lane) {
-  Place p{-1, 0};
-  int lo = 0, n = a.B;   // candidates [lo, lo + n)
-  const uint32_t end = a.offsets[a.B];
-  while (n > 1) {
-    const int step = (n + 31) >> 5;
-    const int probe = lane * step;
-    const bool below = probe < n && a.offsets[lo + probe] <= (uint32_t)t;
-    const int cnt = __popc(__ballot_sync(0xffffffffu, below));
-    const int skip = cnt > 0 ? (cnt - 1) * step : 0;
-    lo += skip;
-    n = min(step, n - skip);
-  }
-  const uint32_t qb = a.offsets[lo], qe = a.offsets[lo + 1], len = a.cache_lens[lo];
-  if ((uint32_t)t >= end) return p;
-  const long long pos = (long long)len - qe + t;
-  bool ok = qb <= (uint32_t)t && (uint32_t)t < qe && pos >= 0 && pos < a.max_seq_len &&
-            pos < (long long)a.bt_stride * a.ps;
-  if (ok) {
-    const int page = a.block_table[(size_t)lo * a.bt_stride + pos / a.ps];
-    ok = page >= 0 && page < a.num_pages;
-    p.row = (long long)page * a.ps + pos % a.ps;
-  }
-  if (ok) p.pos = pos;
-  else if (lane == 0) atomicOr(&a.hdr->status, kDeviceCheckFailed);
-  return p;
+  return locate_groups(a, t, 32, lane);
 }
 
 }  // namespace rows
