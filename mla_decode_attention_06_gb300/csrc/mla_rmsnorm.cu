@@ -122,7 +122,6 @@ __device__ __forceinline__ uint2 int8_codes(const uint32_t (&y)[4], float s, flo
 
 // Largest 16-bit half (0 .. 0xFFFF) of a word of two.
 __device__ __forceinline__ uint32_t halves_max(uint32_t v) { return max(v & 0xFFFFu, v >> 16); }
-__device__ __forceinline__ uint32_t halves_min(uint32_t v) { return min(v & 0xFFFFu, v >> 16); }
 
 // V pieces of 8 values a thread; kWarp: a warp takes a row, else the block does.
 // Blocks of 256 threads: five an SM at 51 registers where a block takes a row (8,192 x 8,192 e4m3 71.4 us; four
@@ -268,11 +267,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? (kWarp ? 4 : 5) : 
       ih = __double2float_rd(inv);
       il = (float)(inv - (double)ih);
     }
-    // The quick way gives every y right whose magnitude is zero or within [2^-90, 2^90): with ih <= 2^15 a
-    // product h * gamma that fp32 does not hold exactly belongs to a smaller y, and one that it takes
-    // for zero to a y that is zero.
+    // The quick way gives every y right whose magnitude, before it is rounded to bf16, is zero or within [2^-90, 2^90):
+    // with ih <= 2^15 a product h * gamma that fp32 does not hold exactly belongs to a smaller y, and one that it takes
+    // for zero to a y that is zero.  (A smaller y may round to zero here and not be it.)
     const bool quick = il != 0.f && ih >= 0x1p-30f && ih <= 0x1p15f;
-    constexpr uint32_t kLeast = 0x12800000u >> 16, kMost = 0x6C800000u >> 16;   // 2^-90, 2^90
+    constexpr uint32_t kLeast = 2u * 0x12800000u - 1, kMost = 0x6C800000u >> 16;   // 2^-90, 2^90
     const float2x ih2 = both(ih, ih), il2 = both(il, il);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -287,11 +286,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? (kWarp ? 4 : 5) : 
           float r0, r1;
           apart(fma2_rz(m, ih2, mul2(m, il2)), r0, r1);
           y[i] = pack(__uint_as_float(__float_as_uint(r0) | 1u), __uint_as_float(__float_as_uint(r1) | 1u));
-          const uint32_t mag = y[i] & 0x7FFF7FFFu;
-          most = __vmaxu2(most, mag);
-          least = __vminu2(least, (mag + 0x7FFF7FFFu) ^ 0x80008000u);   // magnitude - 1, zero the largest
+          most = __vmaxu2(most, y[i] & 0x7FFF7FFFu);
+          least = min(least, min(2 * __float_as_uint(r0) - 1, 2 * __float_as_uint(r1) - 1));   // no sign; zero the largest
         }
-        if (!(quick && halves_min(least) >= kLeast && halves_max(most) < kMost)) {
+        if (!(quick && least >= kLeast && halves_max(most) < kMost)) {
           const uint4 r = normed_any(make_uint4(h[v][0], h[v][1], h[v][2], h[v][3]), gv, ih, il,
                                      wide ? &inv_wide[kWarp ? warp : 0] : nullptr);
           y[0] = r.x;
