@@ -15,8 +15,8 @@
 // reads and writes whole rows.  A query row takes D / 16 lanes of two 8-value pieces half a row apart, so
 // that with R = D / 2 all lanes turn one piece of their two together; a block takes the heads of one or
 // several tokens, two rows a lane group with all loads out before the tokens' places are looked up.  Keys (a piece a
-// lane) have blocks of their own.  8,483 prompt tokens of 64 heads: 58 us, 3.75 TB/s, 55 % of the copy rate, bound by
-// the integer pipe (unpacking, rounding to odd, codes) and waits beside it; a step of 64 tokens: 4.5 us, bound by
+// lane) have blocks of their own.  8,483 prompt tokens of 64 heads: 58 us, 3.75 TB/s, 55 % of the copy rate, held up
+// by loads that a step waits for at its top (the integer pipe is active 51 %); a step of 64 tokens: 4.5 us, bound by
 // the chain of dependent reads.
 #include "mla_kernels.cuh"
 #include "mla_rows.cuh"
