@@ -451,8 +451,8 @@ int mla_indexer_fp8(int32_t num_heads, int32_t head_dim, int32_t page_size, int3
  * brings its index key k (D values) and, if q is given, its index queries (H heads of D):
  *   k = bf16( (k - mean) / sqrt(var + epsilon) * k_norm_gamma + k_norm_beta )
  *       (LayerNorm over D, var = mean((k - mean)^2), rounded once from within 2^-38 of the larger
- *       of beta and what gamma makes of the row's largest deviation, so that equal keys give beta;
- *       left out if k_norm_gamma is NULL)
+ *       of beta and what gamma makes of the row's largest deviation, so that equal keys give beta,
+ *       and 2^-147; left out if k_norm_gamma is NULL)
  *   the last rope_dim values of k and of every head of q turned by freqs_cis[pos] as in
  *       mla_branch_prologue, rounded once to bf16 (left out if freqs_cis is NULL)
  *   e4m3 codes of each row, scale = the least 2^e with max <= 448 * 2^e (1 for zeros; a row that

@@ -74,3 +74,13 @@ def test_longer_sums_are_refused(dev, kind):  # noqa: F811
     with pytest.raises(M.MlaError) as e:
         call(kind, x, xs, x[:1].expand(8, -1).contiguous(), xs[:1].expand(8).contiguous())
     assert e.value.code == 2
+
+
+@pytest.mark.parametrize("T", range(1, 9))
+@pytest.mark.parametrize("N,K", [(2112, 8192), (136, 272), (1000, 65536)])
+def test_few_int8_tokens_are_exact(dev, T, N, K):  # noqa: F811
+    """Up to eight tokens of K up to 65,536: the whole number, rounded to fp32 and times either scale in fp32, to bf16."""
+    x, xs = codes("int8", T, T, K, dev)
+    w, ws = codes("int8", T + 9, N, K, dev)
+    want = ((x.double() @ w.double().T).float() * xs[:, None] * ws).to(torch.bfloat16)
+    assert torch.equal(call("int8", x, xs, w, ws, debug=True), want)
